@@ -1,0 +1,67 @@
+/*
+ * mxfp4moe.h -- C ABI of the 4-bit side of the routed-expert library and of the
+ * routed layer for a few tokens: MXFP4 quantization and grouped products, and a
+ * whole routed SwiGLU layer (top-k, gate, up, SwiGLU, down, weighted sum) for 1 to
+ * 64 tokens over MXFP8 or MXFP4 expert weights.  Same library, status codes,
+ * conventions and scale layouts as mxfp8moe.h (device pointers owned by the caller,
+ * nothing allocated, nothing synchronized, work enqueued on `stream`, argument
+ * errors returned before any launch).
+ *
+ * MXFP4 (OCP Microscaling v1.0): E2M1 elements (0, 0.5, 1, 1.5, 2, 3, 4, 6 and
+ * their negatives), one E8M0 scale per 32 elements.  e = floor(log2(amax)) - 2
+ * clamped at -127, scale byte s = e + 127, element x * 2^-e rounded to nearest
+ * even and saturated to +-6.  An all-zero block gets s = 0.  A block holding Inf or
+ * NaN gets s = 0xFF (NaN) and every code 7 with the element's sign.
+ * Codes are packed two to a byte along the row: element 2i in the low half of byte
+ * i, element 2i + 1 in the high half.
+ */
+#ifndef MXFP4MOE_H
+#define MXFP4MOE_H
+
+#include "mxfp8moe.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* ----------------------------------------------------------------------------
+ * mxfp4_quantize_2d -- x[M, K] bf16 -> q [M, K/2], scales along K.
+ *   s: compact [M, K/32], or blocked with row groups from `offs` (offs NULL: one
+ *   group of M rows), sized by mxfp8_scale_bytes(M, K, G, layout); the blocked
+ *   layout's padding bytes are written as 0.  With offs only the rows inside a
+ *   group are written (all of them, for offsets that end at M).
+ *   K % 32 == 0, M >= 0; x, q, s 16-byte aligned.
+ * mxfp4_swiglu_quantize -- the same for h = silu(h1) * h3 of two bf16 matrices
+ *   [M, K], silu(x) = x / (1 + e^-x), computed and quantized in fp32 (h is not
+ *   rounded to bf16 on the way).
+ * mxfp4_quantize_3d_experts -- w[G, N, K] bf16 -> q [G, N, K/2]; scales per expert,
+ *   compact [N, K/32] or blocked (ceil(N/128)*128*ceil(K/128)*4 bytes each).
+ * mxfp4_dequantize -- the values codes and scales stand for, in bf16 (exact):
+ *   out [batch, M, K] from q [batch, M, K/2]; scales compact, or blocked per matrix
+ *   (batch > 1 or offs NULL) or blocked with row groups (batch == 1).
+ * ------------------------------------------------------------------------- */
+mxfp8_status_t mxfp4_quantize_2d(const void* x_bf16, int64_t M, int64_t K, int scale_layout, const int32_t* offs,
+                                 int32_t G, void* q, void* s, mxfp8_stream_t stream);
+mxfp8_status_t mxfp4_swiglu_quantize(const void* h1_bf16, const void* h3_bf16, int64_t M, int64_t K, int scale_layout,
+                                     const int32_t* offs, int32_t G, void* q, void* s, mxfp8_stream_t stream);
+mxfp8_status_t mxfp4_quantize_3d_experts(const void* w_bf16, int32_t G, int64_t N, int64_t K, int scale_layout,
+                                         void* q, void* s, mxfp8_stream_t stream);
+mxfp8_status_t mxfp4_dequantize(const void* q, const void* s, int32_t batch, int64_t M, int64_t K, int scale_layout,
+                                const int32_t* offs, int32_t G, void* out_bf16, mxfp8_stream_t stream);
+
+/* ----------------------------------------------------------------------------
+ * mxfp4_grouped_mm_fwd -- out[m, n] = sum_k A[m,k] W[g][n,k] for the rows m of
+ *   group g, fp32 accumulation, bf16 out rounded to nearest even.
+ *   a_q [M, K/2], a_s blocked row groups (offs); w_q [G, N, K/2], w_s blocked per
+ *   expert; out [M, N].  K % 32 == 0, N % 32 == 0, 1 <= G <= MXFP8_MAX_GROUPS,
+ *   every pointer 16-byte aligned, group sizes of any length, M may be 0.  Rows
+ *   past the last group's end are not written.
+ * ------------------------------------------------------------------------- */
+mxfp8_status_t mxfp4_grouped_mm_fwd(const void* a_q, const void* a_s, const void* w_q, const void* w_s,
+                                    const int32_t* offs, int32_t G, int64_t M, int64_t N, int64_t K, void* out_bf16,
+                                    int32_t* dev_status, mxfp8_stream_t stream);
+
+#ifdef __cplusplus
+}
+#endif
+#endif /* MXFP4MOE_H */

@@ -1,4 +1,4 @@
-"""ctypes loader for libmxfp8moe.so (the sm_103a C ABI in include/mxfp8moe.h).
+"""ctypes loader for libmxfp8moe.so (the sm_103a C ABI in include/mxfp8moe.h and include/mxfp4moe.h).
 
 There is no fallback: if the library is missing or the device is not sm_103,
 every call raises.
@@ -69,6 +69,16 @@ def load():
     L.mxfp8_status_string.restype = ctypes.c_char_p
     L.mxfp8_debug_wait_timeout.argtypes = [P, ctypes.c_uint64, P]
     L.mxfp8_debug_wait_timeout.restype = S
+    for name, args in {
+        "mxfp4_quantize_2d": [P, I64, I64, INT, P, I32, P, P, P],
+        "mxfp4_swiglu_quantize": [P, P, I64, I64, INT, P, I32, P, P, P],
+        "mxfp4_quantize_3d_experts": [P, I32, I64, I64, INT, P, P, P],
+        "mxfp4_dequantize": [P, P, I32, I64, I64, INT, P, I32, P, P],
+        "mxfp4_grouped_mm_fwd": [P, P, P, P, P, I32, I64, I64, I64, P, P, P],
+    }.items():
+        f = getattr(L, name)
+        f.argtypes = args
+        f.restype = S
     _lib = L
     return L
 

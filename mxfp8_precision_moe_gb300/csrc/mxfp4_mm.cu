@@ -1,0 +1,450 @@
+// mxfp4_mm.cu -- block-scaled MXFP4 grouped GEMM for sm_103a on the 5th-generation tensor cores.
+//
+//   out[m, n] = sum_k A[m,k] W[g][n,k]  for the rows m of group g, bf16,
+// A [M, K] and W [G, N, K] as packed E2M1 codes with one E8M0 scale per 32 along K in the blocked layout.
+//
+// A cluster of two CTAs (cta_group::2) owns a 256 x 256 output tile.  A stage is 128 bytes = 256 elements of
+// K: each CTA stages its own 128 rows of A and 128 rows of B, and both halves' scale tiles (two 128 x 4 tiles
+// per 128 rows); the even CTA issues four M=256 x N=256 x K=64 tcgen05.mma.kind::mxf4 per stage, each with
+// two scale bytes a row (scale_vec::2X: bytes 0-1 or 2-3 of the 32-bit scale word).
+//   warp 0       TMA producer (both CTAs; every copy completes on the even CTA's stage barrier)
+//   warp 1       MMA issuer (even CTA)
+//   warps 2-9    epilogue: tensor memory -> bf16 -> shared memory -> 32-byte row pieces
+//   warp 10      scale copies, shared -> tensor memory (even CTA, both CTAs' tiles)
+// Rows past a group's end are read (they are the next group's) and masked at the store; a K that is not a
+// multiple of 256 multiplies only the 64-wide steps that hold any of it (a row's tail past K is TMA's zero
+// fill and the scale layout's zero padding).  Every wait is bounded.
+
+#include "host_common.h"
+#include "mx4.cuh"
+
+namespace mx {
+
+constexpr int kF4EpiWarps = 8;
+constexpr int kF4SfWarp = 2 + kF4EpiWarps;
+constexpr int kF4Threads = 96 + 32 * kF4EpiWarps;
+constexpr int kF4Band = 16;  // 256-row tiles per raster band (tiles of a band share B tiles in L2)
+
+struct CfgF4 {
+    static constexpr int kStages = 5;
+    static constexpr int kABytes = 128 * 128;
+    static constexpr int kBBytes = 128 * 128;
+    static constexpr int kSfaBytes = 2 * 512;      // two scale tiles: 256 elements of K
+    static constexpr int kSfbBytes = 2 * 2 * 512;  // both 128-row halves of B
+    static constexpr int kTx = 2 * (kABytes + kBBytes + kSfaBytes + kSfbBytes);
+    static constexpr int kSfCols = 8 + 16;
+    static constexpr int kSfCol0 = 256;
+    static constexpr int kTmemCols = 512;
+    static_assert(kSfCol0 + kStages * kSfCols <= kTmemCols, "tensor memory overflow");
+    static constexpr int kOffB = kStages * kABytes;
+    static constexpr int kOffSfa = kOffB + kStages * kBBytes;
+    static constexpr int kOffSfb = kOffSfa + kStages * kSfaBytes;
+    static constexpr int kOffStage = kOffSfb + kStages * kSfbBytes;
+    static constexpr int kOffBar = kOffStage + kF4EpiWarps * 1024;
+    static constexpr int kSmem = kOffBar + (3 * kStages + 4) * 8 + 16 + 1024;
+};
+static_assert(CfgF4::kSmem + 3 * MXFP8_MAX_GROUPS * 4 + 32 <= 227 * 1024, "shared memory");
+
+struct F4Params {
+    const int32_t* offs;
+    int32_t G;
+    int64_t M, N, K;
+    __nv_bfloat16* out;
+    int32_t* dev_status;
+    uint64_t timeout_ns;
+};
+
+// Instruction descriptor of kind::mxf4: E2M1 x E2M1, K-major, E8M0 scales, dense, K = 64.
+__host__ __device__ constexpr uint32_t idesc_mxf4(uint32_t M, uint32_t N, uint32_t a_sf, uint32_t b_sf) {
+    return ((b_sf & 3u) << 4) | (1u << 7) | (1u << 10) | ((N >> 3) << 17) | (1u << 23) | ((M >> 7) << 27) |
+           ((a_sf & 3u) << 29);
+}
+
+__device__ __forceinline__ void tc_mma_pair_mxf4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                                 uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa_tmem), "r"(sfb_tmem)
+        : "memory");
+}
+
+struct F4Tile {
+    int64_t a_row, b_row;
+    int64_t sfa_chunk, sfb_chunk[2];  // scale tile (512 bytes) of K element 0
+    __nv_bfloat16* out;               // first element of this CTA's 128 rows
+    int valid_rows, valid_cols;
+};
+
+// Tile t seen from CTA `half` of the pair.  pt_s: 128-row padded tiles before each group (scale bands);
+// tt_s: 256-row tiles before it.
+__device__ __forceinline__ F4Tile f4_tile(const F4Params& p, int64_t t, int half, const int32_t* ends_s,
+                                          const int32_t* pt_s, const int32_t* tt_s) {
+    const int64_t nt = (p.N + 255) / 256, ct = (p.K + 127) / 128, nchunk = (p.N + 127) / 128;
+    int lo = 0, hi = p.G;
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if ((int64_t)tt_s[mid] * nt <= t) lo = mid + 1;
+        else hi = mid;
+    }
+    const int g = lo - 1;
+    const int64_t start = g ? ends_s[g - 1] : 0, size = ends_s[g] - start, mt = (size + 255) / 256;
+    const int64_t l = t - (int64_t)tt_s[g] * nt;
+    const int64_t band = l / (kF4Band * nt), bm = min64(kF4Band, mt - band * kF4Band);
+    const int64_t idx = l - band * kF4Band * nt, n = idx / bm, m = band * kF4Band + (idx - n * bm);
+    const int64_t rows0 = m * 256 + half * 128;
+    F4Tile ti;
+    ti.a_row = start + rows0;
+    ti.b_row = (int64_t)g * p.N + n * 256 + half * 128;
+    // clamped: rows past the group, columns past N are masked
+    ti.sfa_chunk = (pt_s[g] + min64(2 * m + half, (size + 127) / 128 - 1)) * ct;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) ti.sfb_chunk[j] = ((int64_t)g * nchunk + min64(2 * n + j, nchunk - 1)) * ct;
+    ti.out = p.out + ti.a_row * p.N + n * 256;
+    ti.valid_rows = (int)max64(0, min64(128, size - rows0));
+    ti.valid_cols = (int)min64(256, p.N - n * 256);
+    return ti;
+}
+
+__global__ void __launch_bounds__(kF4Threads, 1)
+    mxfp4_grouped_mm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
+                            const __grid_constant__ CUtensorMap tmap_sfa,
+                            const __grid_constant__ CUtensorMap tmap_sfb, const F4Params p) {
+    using C = CfgF4;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    __shared__ int32_t ends_s[kMaxGroups];
+    __shared__ int32_t pt_s[kMaxGroups];
+    __shared__ int32_t tt_s[kMaxGroups];
+    __shared__ int32_t ttotal_s;
+    __shared__ uint32_t tmem_base_s;
+    __shared__ int abort_s;
+
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
+    uint64_t* empty = full + C::kStages;
+    uint64_t* sfull = empty + C::kStages;
+    uint64_t* tfull = sfull + C::kStages;
+    uint64_t* tempty = tfull + 1;
+    uint64_t* drain = tempty + 1;
+    uint64_t* sfdrain = drain + 1;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int half = (int)(cluster_ctarank() & 1u);
+    const bool leader = half == 0;
+
+    if (warp == 0) {
+        // clamped monotone ends, and the exclusive sums of each group's 128-row and 256-row tiles
+        const int G = p.G, per = (G + 31) / 32, g0 = lane * per, g1 = min(G, g0 + per);
+        const int32_t Mc = (int32_t)p.M;
+        int32_t mx = 0;
+        for (int g = g0; g < g1; ++g) mx = max(mx, min(max(p.offs[g], 0), Mc));
+        int32_t incl = mx;
+        for (int d = 1; d < 32; d <<= 1) {
+            const int32_t o = __shfl_up_sync(0xffffffffu, incl, d);
+            if (lane >= d) incl = max(incl, o);
+        }
+        int32_t run = __shfl_up_sync(0xffffffffu, incl, 1);
+        if (lane == 0) run = 0;
+        int32_t prev = run, psum = 0, tsum = 0;
+        for (int g = g0; g < g1; ++g) {
+            const int32_t e = max(prev, min(max(p.offs[g], 0), Mc));
+            ends_s[g] = e;
+            psum += (e - prev + 127) / 128;
+            tsum += (e - prev + 255) / 256;
+            prev = e;
+        }
+        int32_t pi = psum, tincl = tsum;
+        for (int d = 1; d < 32; d <<= 1) {
+            const int32_t o = __shfl_up_sync(0xffffffffu, pi, d), q = __shfl_up_sync(0xffffffffu, tincl, d);
+            if (lane >= d) {
+                pi += o;
+                tincl += q;
+            }
+        }
+        int32_t pe = pi - psum, te = tincl - tsum;
+        prev = run;
+        for (int g = g0; g < g1; ++g) {
+            const int32_t e = ends_s[g];
+            pt_s[g] = pe;
+            tt_s[g] = te;
+            pe += (e - prev + 127) / 128;
+            te += (e - prev + 255) / 256;
+            prev = e;
+        }
+        if (lane == 31) ttotal_s = tincl;
+        if (lane == 0) {
+            abort_s = 0;
+            prefetch_tmap(&tmap_a);
+            prefetch_tmap(&tmap_b);
+            prefetch_tmap(&tmap_sfa);
+            prefetch_tmap(&tmap_sfb);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            for (int s = 0; s < C::kStages; ++s) {
+                mbar_init(&full[s], 1);
+                mbar_init(&empty[s], 1);
+                mbar_init(&sfull[s], 1);
+            }
+            mbar_init(tfull, 1);
+            mbar_init(tempty, 2 * kF4EpiWarps);  // every epilogue warp of both CTAs
+            mbar_init(drain, 1);
+            mbar_init(sfdrain, 1);
+            fence_barrier_init();
+        }
+        __syncwarp();
+        tmem_alloc_pair(&tmem_base_s, C::kTmemCols);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // the peer may signal this CTA's barriers from here on
+    tc_fence_after();
+
+    const uint32_t tmem = tmem_base_s;
+    volatile int* abort_flag = &abort_s;
+    const int64_t ntiles = (int64_t)ttotal_s * ((p.N + 255) / 256);
+    const int64_t cid = blockIdx.x >> 1, ncl = gridDim.x >> 1;
+    const int k_tiles = (int)((p.K + 255) / 256);
+
+    if (warp == 0 && lane == 0) {
+        // ------------------------------------------------ TMA producer (both CTAs)
+        int stage = 0;
+        uint32_t phase = 0, issued = 0, last_phase = 0;
+        bool ok = true;
+        for (int64_t t = cid; t < ntiles && ok; t += ncl) {
+            const F4Tile ti = f4_tile(p, t, half, ends_s, pt_s, tt_s);
+            for (int kt = 0; kt < k_tiles; ++kt) {
+                if (!mbar_wait_bounded<true>(&empty[stage], phase ^ 1u, p.timeout_ns, abort_flag, p.dev_status)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t fb = cluster_addr(&full[stage], 0);
+                if (leader) mbar_arrive_expect_tx(&full[stage], C::kTx);
+                tma_load_2d_pair(smem + stage * C::kABytes, &tmap_a, kt * 128, (int32_t)ti.a_row, fb);
+                tma_load_2d_pair(smem + C::kOffB + stage * C::kBBytes, &tmap_b, kt * 128, (int32_t)ti.b_row, fb);
+                // two scale tiles a copy (an odd count's last copy reads one tile further, which nothing uses)
+                tma_load_2d_pair(smem + C::kOffSfa + stage * C::kSfaBytes, &tmap_sfa, 0,
+                                 (int32_t)(2 * (ti.sfa_chunk + 2 * kt)), fb);
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    tma_load_2d_pair(smem + C::kOffSfb + stage * C::kSfbBytes + 1024 * j, &tmap_sfb, 0,
+                                     (int32_t)(2 * (ti.sfb_chunk[j] + 2 * kt)), fb);
+                issued |= 1u << stage;
+                last_phase = (last_phase & ~(1u << stage)) | (phase << stage);
+                if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
+            }
+        }
+        if (!ok && leader) {  // given up: let the copies in flight land before the pair exits
+            volatile int no_abort = 0;
+            for (int s = 0; s < C::kStages; ++s)
+                if (issued & (1u << s))
+                    mbar_wait_bounded<true>(&full[s], (last_phase >> s) & 1u, p.timeout_ns, &no_abort, nullptr);
+        }
+    } else if (warp == 1 && lane == 0 && leader) {
+        // ------------------------------------------------ MMA issuer (even CTA)
+        int stage = 0;
+        uint32_t phase = 0, acc_phase = 0;
+        bool ok = true;
+        constexpr uint32_t idesc0 = idesc_mxf4(256, 256, 0, 0);
+        for (int64_t t = cid; t < ntiles && ok; t += ncl) {
+            if (!mbar_wait_bounded<true>(tempty, acc_phase ^ 1u, p.timeout_ns, abort_flag, p.dev_status)) break;
+            tc_fence_after();
+            for (int kt = 0; kt < k_tiles; ++kt) {
+                const int cur = stage;
+                if (!mbar_wait_bounded<true>(&full[cur], phase, p.timeout_ns, abort_flag, p.dev_status) ||
+                    !mbar_wait_bounded<true>(&sfull[cur], phase, p.timeout_ns, abort_flag, p.dev_status)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
+                const uint32_t sf = tmem + C::kSfCol0 + cur * C::kSfCols;
+                const uint32_t a_s = smem_u32(smem + cur * C::kABytes);
+                const uint32_t b_s = smem_u32(smem + C::kOffB + cur * C::kBBytes);
+                const int steps = (int)min64(4, (p.K - (int64_t)kt * 256 + 63) / 64);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    if (k >= steps) break;
+                    const uint64_t ad = smem_desc(a_s + 32 * k, 16, 1024, 2);
+                    const uint64_t bd = smem_desc(b_s + 32 * k, 16, 1024, 2);
+                    const uint32_t id = (uint32_t)(k & 1) * 2;  // scale bytes 0-1 or 2-3 of the word
+                    tc_mma_pair_mxf4(tmem, ad, bd, idesc0 | (id << 4) | (id << 29), sf + 4 * (k >> 1),
+                                     sf + 8 + 8 * (k >> 1), (kt | k) != 0);
+                }
+                tc_commit_pair(&empty[cur], 0x3);
+            }
+            if (!ok) break;
+            tc_commit_pair(tfull, 0x3);
+            acc_phase ^= 1u;
+        }
+        // all tensor-core work of the pair is done before the columns are freed
+        tc_commit_pair(drain, 0x1);
+        volatile int no_abort = 0;
+        mbar_wait_bounded<true>(drain, 0, p.timeout_ns, &no_abort, p.dev_status);
+    } else if (warp == kF4SfWarp) {
+        // ------------------------------------------------ scale copies (even CTA)
+        if (lane == 0 && leader) {
+            int stage = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int64_t t = cid; t < ntiles && ok; t += ncl) {
+                for (int kt = 0; kt < k_tiles; ++kt) {
+                    if (!mbar_wait_bounded<true>(&full[stage], phase, p.timeout_ns, abort_flag, p.dev_status)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t sf = tmem + C::kSfCol0 + stage * C::kSfCols;
+                    const uint32_t sa = smem_u32(smem + C::kOffSfa + stage * C::kSfaBytes);
+                    const uint32_t sb = smem_u32(smem + C::kOffSfb + stage * C::kSfbBytes);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        tc_cp_pair_32x128b_warpx4(sf + 4 * h, smem_desc(sa + 512 * h, 0, 128, 0));
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+                            tc_cp_pair_32x128b_warpx4(sf + 8 + 8 * h + 4 * j,
+                                                      smem_desc(sb + 1024 * j + 512 * h, 0, 128, 0));
+                    }
+                    tc_commit_pair(&sfull[stage], 0x1);
+                    if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
+                }
+            }
+            tc_commit_pair(sfdrain, 0x1);
+            volatile int no_abort = 0;
+            mbar_wait_bounded<true>(sfdrain, 0, p.timeout_ns, &no_abort, p.dev_status);
+        }
+    } else if (warp >= 2) {
+        // ------------------------------------------------ epilogue (both CTAs: own 128 rows)
+        // Warp w drains lane quarter w % 4 and column half (w - 2) / 4.
+        const int quarter = warp & 3;
+        const int c_base = ((warp - 2) >> 2) * 128;
+        uint8_t* stg = smem + C::kOffStage + (warp - 2) * 1024;  // 32 rows x 32 bytes
+        const uint32_t tempty_leader = cluster_addr(tempty, 0);
+        uint32_t acc_phase = 0;
+        for (int64_t t = cid; t < ntiles; t += ncl) {
+            const F4Tile ti = f4_tile(p, t, half, ends_s, pt_s, tt_s);
+            __nv_bfloat16* wout = ti.out + (int64_t)(quarter * 32) * p.N + c_base;
+            const int vrows = ti.valid_rows - quarter * 32;
+            const int vcols = ti.valid_cols - c_base;
+            if (!mbar_wait_bounded<true>(tfull, acc_phase, p.timeout_ns, abort_flag, p.dev_status)) break;
+            acc_phase ^= 1u;
+            tc_fence_after();
+            uint32_t packed[64];
+            const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + c_base;
+#pragma unroll
+            for (int c = 0; c < 128; c += 64) {
+                uint32_t v0[32], v1[32];
+                tmem_ld_32x32b_x32(taddr + c, v0);
+                tmem_ld_32x32b_x32(taddr + c + 32, v1);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    packed[c / 2 + i] = pack_bf16x2(__uint_as_float(v0[2 * i]), __uint_as_float(v0[2 * i + 1]));
+                    packed[c / 2 + 16 + i] = pack_bf16x2(__uint_as_float(v1[2 * i]), __uint_as_float(v1[2 * i + 1]));
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster_relaxed(tempty_leader);
+            // 16 columns a pass: lane = row parks two 16-byte pieces (order flipped every 4 rows: no bank
+            // conflicts), then two lanes a row store whole 32-byte pieces of 16 rows per instruction
+#pragma unroll
+            for (int ch = 0; ch < 8; ++ch) {
+                if (ch * 16 >= vcols) break;
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    st_shared_v4(stg + lane * 32 + ((j ^ ((lane >> 2) & 1)) * 16),
+                                 make_uint4(packed[ch * 8 + 4 * j], packed[ch * 8 + 4 * j + 1],
+                                            packed[ch * 8 + 4 * j + 2], packed[ch * 8 + 4 * j + 3]));
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int rl = (lane >> 1) + 16 * i, piece = lane & 1;
+                    const uint4 val = ld_shared_v4(stg + rl * 32 + ((piece ^ ((rl >> 2) & 1)) * 16));
+                    if (rl < vrows && ch * 16 + piece * 8 < vcols)
+                        *reinterpret_cast<uint4*>(wout + (int64_t)rl * p.N + ch * 16 + piece * 8) = val;
+                }
+                __syncwarp();
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // neither CTA frees tensor memory or exits while the pair still works
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, C::kTmemCols);
+    }
+}
+
+// ---------------------------------------------------------------- host side
+// uint8 [rows][cols], boxes of box_rows x box_cols bytes.
+static bool f4_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int box_rows, int box_cols,
+                   bool swizzle) {
+    host::EncodeTiledFn fn = host::encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)cols};
+    cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace mx
+
+using namespace mx;
+
+extern "C" mxfp8_status_t mxfp4_grouped_mm_fwd(const void* a_q, const void* a_s, const void* w_q, const void* w_s,
+                                               const int32_t* offs, int32_t G, int64_t M, int64_t N, int64_t K,
+                                               void* out_bf16, int32_t* dev_status, mxfp8_stream_t stream) {
+    if (!offs || !w_q || !w_s) return MXFP8_ERR_NULL;
+    if (G < 1 || G > MXFP8_MAX_GROUPS || M < 0 || N <= 0 || K <= 0 || M > INT32_MAX || K > INT32_MAX ||
+        (int64_t)G * N > INT32_MAX)
+        return MXFP8_ERR_SHAPE;
+    if (K % 32 || N % 32) return MXFP8_ERR_ALIGN;
+    if (M == 0) return MXFP8_OK;  // empty tensors may have no address
+    if (!a_q || !a_s || !out_bf16) return MXFP8_ERR_NULL;
+    const void* ptrs[] = {a_q, a_s, w_q, w_s, out_bf16};
+    for (const void* q : ptrs)
+        if (!host::aligned16(q)) return MXFP8_ERR_ALIGN;
+    const int64_t ct = (K + 127) / 128;
+    const int64_t sfa_rows = ((M + 127) / 128 + G) * ct * 2, sfb_rows = (int64_t)G * ((N + 127) / 128) * ct * 2;
+    if (sfa_rows > INT32_MAX - 4 || sfb_rows > INT32_MAX - 4) return MXFP8_ERR_SHAPE;  // TMA coordinates
+    if (mxfp8_status_t a = host::check_arch(); a != MXFP8_OK) return a;
+    CUtensorMap ma, mb, msa, msb;
+    if (!f4_map(&ma, a_q, M, K / 2, 128, 128, true) || !f4_map(&mb, w_q, (int64_t)G * N, K / 2, 128, 128, true) ||
+        !f4_map(&msa, a_s, sfa_rows, 256, 4, 256, false) || !f4_map(&msb, w_s, sfb_rows, 256, 4, 256, false))
+        return MXFP8_ERR_DRIVER;
+    F4Params p{};
+    p.offs = offs;
+    p.G = G;
+    p.M = M;
+    p.N = N;
+    p.K = K;
+    p.out = static_cast<__nv_bfloat16*>(out_bf16);
+    p.dev_status = dev_status;
+    p.timeout_ns = 2000000000ull;
+    static std::atomic<int> attr_set[host::kMaxDevices];
+    if (!host::ensure_smem(reinterpret_cast<const void*>(mxfp4_grouped_mm_kernel), CfgF4::kSmem, attr_set))
+        return MXFP8_ERR_LAUNCH;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.blockDim = dim3(kF4Threads);
+    cfg.dynamicSmemBytes = CfgF4::kSmem;
+    cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const int64_t bound = ((M + 255) / 256 + G) * ((N + 255) / 256);
+    cfg.gridDim = dim3(2 * (unsigned)max64(1, min64(bound, host::num_sms() / 2)));
+    if (cudaLaunchKernelEx(&cfg, mxfp4_grouped_mm_kernel, ma, mb, msa, msb, p) != cudaSuccess) return MXFP8_ERR_LAUNCH;
+    return host::last_launch_status();
+}
