@@ -61,6 +61,37 @@ mxfp8_status_t mxfp4_grouped_mm_fwd(const void* a_q, const void* a_s, const void
                                     const int32_t* offs, int32_t G, int64_t M, int64_t N, int64_t K, void* out_bf16,
                                     int32_t* dev_status, mxfp8_stream_t stream);
 
+/* ----------------------------------------------------------------------------
+ * mx_moe_tokens -- a routed SwiGLU layer for T = 1 .. 64 tokens in one launch:
+ *   S_t  = the top_k largest of router_logits[t] (NaN ranks above everything, ties go to
+ *          the lowest expert, -inf is never selected);
+ *   w_te = MX_SCORE_SOFTMAX: softmax over S_t; MX_SCORE_SOFTMAX_ALL: softmax over all
+ *          experts; MX_SCORE_SIGMOID: 1 / (1 + e^-logit);
+ *   h_te = silu(xq_t Wg_e^T) * (xq_t Wu_e^T) in fp32;
+ *   y_t  = bf16( sum over e in S_t of w_te MX(h_te) Wd_e^T ), fp32 sums, one rounding.
+ * xq = MX(x_t) and MX(h) are quantized along D and H to the weights' format: bits = 8
+ * (E4M3, codes [E, H, D] / [E, D, H]) or 4 (E2M1, two codes to a byte).  Weight scales
+ * blocked per expert, as mxfp8_quantize_3d_experts / mxfp4_quantize_3d_experts write
+ * them.  x [T, D] bf16, router_logits [T, E] fp32, y [T, D] bf16.  A token whose logits
+ * are all -inf gets y = 0.  Only the experts that some token selected are read.
+ *   D % 32 == 0, H % 32 == 0, E <= 256, top_k <= min(E, 16); pointers 16-byte aligned
+ *   (the logits 4).  T == 0 does nothing.
+ *   workspace: mx_moe_tokens_workspace(max_tokens, ...) bytes for T <= max_tokens, the
+ *   first 256 zero before the first call; it is the launch's own until the launch has
+ *   finished (one per stream).  Every launch leaves it ready for the next.
+ *   The launch is cooperative (its CTAs wait for one another, each wait bounded:
+ *   MXFP8_ERR_TIMEOUT in dev_status); it can be captured into a graph.
+ * mx_moe_tokens_workspace returns 0 for arguments mx_moe_tokens would refuse.
+ * ------------------------------------------------------------------------- */
+enum { MX_SCORE_SOFTMAX = 0, MX_SCORE_SOFTMAX_ALL = 1, MX_SCORE_SIGMOID = 2 };
+
+size_t mx_moe_tokens_workspace(int32_t max_tokens, int32_t E, int64_t D, int64_t H, int32_t top_k, int32_t bits);
+mxfp8_status_t mx_moe_tokens(const void* x_bf16, const float* router_logits, int32_t T, int32_t E, int64_t D,
+                             int64_t H, int32_t top_k, int32_t score, int32_t bits, const void* gate_q,
+                             const void* gate_s, const void* up_q, const void* up_s, const void* down_q,
+                             const void* down_s, void* workspace, size_t workspace_bytes, void* y_bf16,
+                             int32_t* dev_status, mxfp8_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

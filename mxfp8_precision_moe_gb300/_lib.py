@@ -75,10 +75,13 @@ def load():
         "mxfp4_quantize_3d_experts": [P, I32, I64, I64, INT, P, P, P],
         "mxfp4_dequantize": [P, P, I32, I64, I64, INT, P, I32, P, P],
         "mxfp4_grouped_mm_fwd": [P, P, P, P, P, I32, I64, I64, I64, P, P, P],
+        "mx_moe_tokens": [P, P, I32, I32, I64, I64, I32, I32, I32, P, P, P, P, P, P, P, ctypes.c_size_t, P, P, P],
     }.items():
         f = getattr(L, name)
         f.argtypes = args
         f.restype = S
+    L.mx_moe_tokens_workspace.argtypes = [I32, I32, I64, I64, I32, I32]
+    L.mx_moe_tokens_workspace.restype = ctypes.c_size_t
     _lib = L
     return L
 

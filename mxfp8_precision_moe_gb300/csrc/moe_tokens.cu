@@ -1,0 +1,771 @@
+// moe_tokens.cu -- a whole routed SwiGLU layer for 1 .. 64 tokens in one kernel, expert weights in MXFP8 or
+// MXFP4 (activations quantized to the same format), for sm_103a.
+//
+//   S_t = the k largest of token t's router logits;  w_te = softmax over S_t (or over all, or sigmoid)
+//   h_te = silu(xq_t Wg_e^T) * (xq_t Wu_e^T),   y_t = bf16( sum_{e in S_t} w_te MX(h_te) Wd_e^T )
+//
+// With few tokens the layer is one pass over the weights of the experts that any token selected, so every
+// choice serves that stream.  One cooperative launch, one CTA per SM, weights through TMA into a ring of
+// stages that never drains: the same ring runs through both halves of the layer, and the down weights are
+// on their way while the last gate/up tiles finish.  Weights are the tensor cores' 128-row operand,
+// tokens the narrow one (N = 32 or 64 columns): every token is multiplied with every selected expert, which
+// costs no bandwidth and no gather, and a routing mask decides which columns are used -- so a NaN in an
+// expert's weights reaches only the tokens routed to it.
+//
+// A unit of work is one 128-byte step along the contraction of two 128-row weight tiles (32 KB):
+//   first half   tile = 128 rows of one expert's gate and up matrices; steps along D
+//   second half  tile = 256 rows of D; steps along every selected expert's H in turn
+// Each half's units, in order, are cut into equal runs, one per CTA, so the load is even however few experts
+// or tiles there are.  A run that ends inside a tile leaves fp32 partial sums in the workspace; the CTA
+// that arrives last at a tile adds them in the order of their runs (the result does not depend on arrival).
+//
+//   warp 0      weight producer (TMA tiles and their scale tiles); waits for nothing but free stages
+//   warp 1      token producer (quantized x or h and their scales); waits at the two grid-wide points:
+//               x is quantized, h is complete
+//   warp 2      tensor-core issuer: scale copies into tensor memory, then the block-scaled MMAs
+//   warps 4-11  quantize this CTA's share of x; then the epilogues
+// Every wait is bounded by time (MXFP8_ERR_TIMEOUT and an orderly exit).
+
+#include "host_common.h"
+#include "mx4.cuh"
+
+namespace mx {
+
+constexpr int kMtMaxTokens = 64;
+constexpr int kMtMaxExperts = 256;
+constexpr int kMtMaxTopK = 16;
+constexpr int kMtThreads = 384;
+constexpr int kMtEpiWarp0 = 4;
+constexpr int kMtEpiThreads = 256;
+constexpr int kMtStages = 5;
+constexpr int kMtHeader = 256;  // workspace bytes before the tile counters
+
+template <int BITS, int N>
+struct MtCfg {
+    static constexpr int kKE = BITS == 8 ? 128 : 256;   // contraction elements of a step (128 bytes)
+    static constexpr int kSfTiles = kKE / 128;          // 512-byte scale tiles of a step
+    static constexpr int kOffSfA = 2 * 128 * 128;       // within a stage: two weight tiles, ...
+    static constexpr int kOffB = kOffSfA + 2 * kSfTiles * 512;
+    static constexpr int kOffSfB = kOffB + N * 128;
+    static constexpr int kStage = (kOffSfB + kSfTiles * 512 + 1023) / 1024 * 1024;
+    static constexpr int kSfCols = 3 * 4 * kSfTiles;    // tensor-memory columns of a stage's scales
+    static constexpr int kSfCol0 = 4 * N;               // after two buffers of two accumulators
+    static constexpr int kSmem = kMtStages * kStage + 1024;
+    static_assert(kOffB % 1024 == 0, "swizzled tiles start on 1024-byte boundaries");
+    static_assert(kSfCol0 + kMtStages * kSfCols <= 512, "tensor memory overflow");
+};
+static_assert(MtCfg<4, 64>::kSmem + 10 * 1024 <= 227 * 1024, "shared memory");
+
+struct MtParams {
+    const uint8_t* x;        // bf16 [T][D]
+    const float* logits;     // [T][E]
+    const uint8_t* s_gate;   // blocked scales, per expert
+    const uint8_t* s_up;
+    const uint8_t* s_down;
+    uint8_t* xq;             // workspace: codes [T][D], scales [ct(D)][512]
+    uint8_t* xs;
+    uint8_t* hq;             // codes [active][T][H], scales [active][ct(H)][512]
+    uint8_t* hs;
+    float* part;             // [CTA][2][2][T][128] partial sums
+    uint32_t* header;        // grid barrier arrivals, exits
+    uint32_t* counters;      // arrivals per tile: first half, then second half
+    __nv_bfloat16* y;        // [T][D]
+    int32_t* dev_status;
+    uint64_t timeout_ns;
+    int64_t D, H;
+    int T, E, top_k, score;
+    int ncounters;
+};
+
+__device__ __forceinline__ void tc_mma_mxf4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                            uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa_tmem), "r"(sfb_tmem)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[16]) { tmem_ld_32x32b_x16(taddr, r); }
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[32]) { tmem_ld_32x32b_x32(taddr, r); }
+
+__device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
+
+__device__ __forceinline__ void epi_sync() {
+    __syncwarp();
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+}
+// Whether every epilogue thread says yes (and a barrier for them).
+__device__ __forceinline__ bool epi_all(bool yes) {
+    uint32_t r;
+    __syncwarp();
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, 1, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)yes)
+        : "memory");
+    return r != 0;
+}
+
+__device__ __forceinline__ uint32_t ld_acquire(const uint32_t* p) {
+    uint32_t v;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+
+// One half's units cut into n equal runs (n <= units, so none is empty).
+struct MtSplit {
+    uint32_t units, n;
+    __device__ __forceinline__ uint32_t start(uint32_t c) const { return (uint32_t)((uint64_t)c * units / n); }
+    __device__ __forceinline__ uint32_t owner(uint32_t u) const {  // the run that holds unit u
+        return (uint32_t)((((uint64_t)u + 1) * n - 1) / units);
+    }
+};
+// A run holds at least this many units: below it, exchanging partial sums costs more than the steps saved.
+constexpr uint32_t kMtMinUnits = 4;
+
+__device__ __forceinline__ MtSplit mt_split(uint32_t units) {
+    const uint32_t most = (units + kMtMinUnits - 1) / kMtMinUnits;
+    return MtSplit{units, units == 0 ? 1u : min(gridDim.x, most)};
+}
+
+template <int BITS, int N>
+__global__ void __launch_bounds__(kMtThreads, 1)
+    moe_tokens_kernel(const __grid_constant__ CUtensorMap map_gate, const __grid_constant__ CUtensorMap map_up,
+                      const __grid_constant__ CUtensorMap map_down, const __grid_constant__ CUtensorMap map_x,
+                      const __grid_constant__ CUtensorMap map_h, const MtParams p) {
+    using C = MtCfg<BITS, N>;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t full[kMtStages], empty[kMtStages], tfull[2], tempty[2], drain;
+    __shared__ uint64_t mask_s[kMtMaxExperts];                 // tokens of each active expert
+    __shared__ uint16_t list_s[kMtMaxExperts];                 // active experts, ascending
+    __shared__ uint32_t active_s[kMtMaxExperts / 32];
+    __shared__ uint16_t sel_e[kMtMaxTokens * kMtMaxTopK];      // a token's experts, best first (0xFFFF: none)
+    __shared__ float sel_w[kMtMaxTokens * kMtMaxTopK];         // their logits, then their weights
+    __shared__ float w_s[2][kMtMaxTokens];
+    __shared__ int nactive_s;
+    __shared__ uint32_t tmem_base_s, last_s;
+    __shared__ int abort_s;
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int T = p.T, E = p.E;
+    volatile int* abort_flag = &abort_s;
+
+    // ---------------------------------------------------------------- routing (every CTA, the same)
+    uint32_t* keys = reinterpret_cast<uint32_t*>(smem);  // [T][E], before the first stage is filled
+    for (int i = tid; i < T * E; i += kMtThreads) {
+        const uint32_t b = __float_as_uint(p.logits[i]);
+        // unsigned keys that order as the logits do: NaN above everything, -0 equal to +0
+        uint32_t k = (b & 0x80000000u) ? ~b : b | 0x80000000u;
+        if ((b & 0x7FFFFFFFu) > 0x7F800000u) k = 0xFFFFFFFFu;
+        if (b == 0x80000000u) k = 0x80000000u;
+        keys[i] = k;
+    }
+    for (int i = tid; i < T * p.top_k; i += kMtThreads) sel_e[i] = 0xFFFFu;
+    if (tid < kMtMaxExperts / 32) active_s[tid] = 0;
+    if (tid < kMtMaxExperts) mask_s[tid] = 0;
+    if (warp == 2) {
+        if (lane == 0) {
+            for (int s = 0; s < kMtStages; ++s) {
+                mbar_init(&full[s], 2);  // the weight and the token producer
+                mbar_init(&empty[s], 1);
+            }
+            for (int b = 0; b < 2; ++b) {
+                mbar_init(&tfull[b], 1);
+                mbar_init(&tempty[b], kMtEpiThreads / 32);
+            }
+            mbar_init(&drain, 1);
+            abort_s = 0;
+            fence_barrier_init();
+            prefetch_tmap(&map_gate);
+            prefetch_tmap(&map_up);
+            prefetch_tmap(&map_down);
+            prefetch_tmap(&map_x);
+            prefetch_tmap(&map_h);
+        }
+        __syncwarp();
+        tmem_alloc(&tmem_base_s, 512);
+        tmem_relinquish();
+    }
+    __syncthreads();
+    for (int i = tid; i < T * E; i += kMtThreads) {
+        const int t = i / E, e = i - t * E;
+        const uint32_t k = keys[i];
+        const uint32_t* row = keys + t * E;
+        int rank = 0;  // logits before this one: larger, or equal at a lower index
+        for (int o = 0; o < E; ++o) rank += (row[o] > k) || (row[o] == k && o < e);
+        if (rank < p.top_k && k != 0x007FFFFFu) {  // -inf is never selected
+            sel_e[t * p.top_k + rank] = (uint16_t)e;
+            sel_w[t * p.top_k + rank] = p.logits[i];
+            atomicOr(&active_s[e >> 5], 1u << (e & 31));
+        }
+    }
+    __syncthreads();
+    if (tid < T) {
+        const uint16_t* se = sel_e + tid * p.top_k;
+        float* sw = sel_w + tid * p.top_k;
+        if (p.score == MX_SCORE_SIGMOID) {
+            for (int j = 0; j < p.top_k && se[j] != 0xFFFFu; ++j) sw[j] = 1.0f / (1.0f + expf(-sw[j]));
+        } else {
+            const float m = se[0] != 0xFFFFu ? sw[0] : 0.0f;  // the largest logit
+            float sum = 0.0f;
+            if (p.score == MX_SCORE_SOFTMAX) {
+                for (int j = 0; j < p.top_k && se[j] != 0xFFFFu; ++j) sum += expf(sw[j] - m);
+            } else {
+                for (int e = 0; e < E; ++e) sum += expf(p.logits[tid * E + e] - m);
+            }
+            for (int j = 0; j < p.top_k && se[j] != 0xFFFFu; ++j) sw[j] = expf(sw[j] - m) / sum;
+        }
+    }
+    if (warp == 3) {  // the active experts in ascending order
+        const uint32_t w = lane < kMtMaxExperts / 32 ? active_s[lane] : 0u;
+        int incl = __popc(w);
+        const int own = incl;
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, incl, d);
+            if (lane >= d) incl += o;
+        }
+        int at = incl - own;
+        for (uint32_t m = w; m; m &= m - 1) list_s[at++] = (uint16_t)(lane * 32 + __ffs(m) - 1);
+        if (lane == 31) nactive_s = incl;
+    }
+    __syncthreads();
+    const int A = nactive_s;
+    for (int i = tid; i < T * p.top_k; i += kMtThreads) {
+        const int e = sel_e[i];
+        if (e == 0xFFFF) continue;
+        const uint32_t below = active_s[e >> 5] & ((1u << (e & 31)) - 1u);
+        int a = __popc(below);
+        for (int w = 0; w < (e >> 5); ++w) a += __popc(active_s[w]);
+        atomicOr(reinterpret_cast<unsigned long long*>(&mask_s[a]), 1ull << (i / p.top_k));
+    }
+    fence_proxy_async();  // the keys' shared memory is TMA's from here on
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_base_s;
+
+    const int64_t D = p.D, H = p.H;
+    const uint32_t ct_d = (uint32_t)((D + 127) / 128), ct_h = (uint32_t)((H + 127) / 128);
+    const uint32_t K1 = (uint32_t)((D + C::kKE - 1) / C::kKE), K2 = (uint32_t)((H + C::kKE - 1) / C::kKE);
+    const uint32_t TH = ct_h, TD = (uint32_t)((D + 255) / 256);
+    const MtSplit sp1 = mt_split((uint32_t)A * TH * K1), sp2 = mt_split(TD * (uint32_t)A * K2);
+    const uint32_t cta = blockIdx.x;
+    const uint32_t u1_0 = cta < sp1.n ? sp1.start(cta) : 0, u1_1 = cta < sp1.n ? sp1.start(cta + 1) : 0;
+    const uint32_t u2_0 = cta < sp2.n ? sp2.start(cta) : 0, u2_1 = cta < sp2.n ? sp2.start(cta + 1) : 0;
+    const uint32_t AK2 = (uint32_t)A * K2;
+
+    if (A == 0) {
+        for (int64_t i = (int64_t)cta * kMtThreads + tid; i < T * D; i += (int64_t)gridDim.x * kMtThreads)
+            p.y[i] = __float2bfloat16(0.0f);
+    } else if (warp == 0) {
+        if (lane == 0) {
+            // -------------------------------------------- weight producer
+            int stage = 0;
+            uint32_t phase = 0;
+            auto load = [&](bool first, const CUtensorMap* m0, const CUtensorMap* m1, int32_t row0, int32_t row1,
+                            const uint8_t* s0, const uint8_t* s1, uint32_t k, uint32_t ct) -> bool {
+                if (!mbar_wait_bounded<true>(&empty[stage], phase ^ 1u, p.timeout_ns, abort_flag, p.dev_status))
+                    return false;
+                uint8_t* st = smem + stage * C::kStage;
+                const uint32_t sfb = min((uint32_t)C::kSfTiles, ct - k * C::kSfTiles) * 512;
+                const bool two = first || row1 >= 0;
+                mbar_arrive_expect_tx(&full[stage], (two ? 2u : 1u) * (16384u + sfb));
+                tma_load_2d(st, m0, (int32_t)(k * 128), row0, &full[stage]);
+                bulk_load(st + C::kOffSfA, s0 + (int64_t)k * C::kSfTiles * 512, sfb, &full[stage]);
+                if (two) {
+                    tma_load_2d(st + 16384, m1, (int32_t)(k * 128), row1, &full[stage]);
+                    bulk_load(st + C::kOffSfA + C::kSfTiles * 512, s1 + (int64_t)k * C::kSfTiles * 512, sfb,
+                              &full[stage]);
+                }
+                if (++stage == kMtStages) { stage = 0; phase ^= 1u; }
+                return true;
+            };
+            bool ok = true;
+            for (uint32_t u = u1_0; u < u1_1 && ok;) {
+                const uint32_t tile = u / K1, a = tile / TH, j = tile - a * TH, e = list_s[a];
+                const uint32_t end = min(u1_1, (tile + 1) * K1);
+                const int64_t so = (int64_t)e * ct_h * ct_d * 512 + (int64_t)j * ct_d * 512;
+                const int32_t row = (int32_t)((int64_t)e * H + j * 128);
+                for (; u < end && ok; ++u)
+                    ok = load(true, &map_gate, &map_up, row, row, p.s_gate + so, p.s_up + so, u - tile * K1, ct_d);
+            }
+            for (uint32_t u = u2_0; u < u2_1 && ok;) {
+                const uint32_t tile = u / AK2, r = u - tile * AK2, a = r / K2, e = list_s[a];
+                const uint32_t base = tile * AK2 + a * K2, end = min(u2_1, base + K2);
+                const int64_t so = ((int64_t)e * ct_d + 2 * tile) * ct_h * 512;
+                const int32_t row = (int32_t)((int64_t)e * D + tile * 256);
+                const bool two = 2 * tile + 1 < ct_d;
+                for (; u < end && ok; ++u)
+                    ok = load(false, &map_down, &map_down, row, two ? row + 128 : -1, p.s_down + so,
+                              p.s_down + so + (int64_t)ct_h * 512, u - base, ct_h);
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            // -------------------------------------------- token producer
+            int stage = 0;
+            uint32_t phase = 0;
+            auto grid_wait = [&](uint32_t target) -> bool {
+                const uint64_t t0 = globaltimer_ns();
+                while (ld_acquire(p.header) < target) {
+                    if (*abort_flag) return false;
+                    if (globaltimer_ns() - t0 > p.timeout_ns) {
+                        *abort_flag = 1;
+                        report(p.dev_status, MXFP8_ERR_TIMEOUT);
+                        return false;
+                    }
+                }
+                fence_proxy_async();  // what the other CTAs wrote, before TMA reads it
+                return true;
+            };
+            auto load = [&](const CUtensorMap* m, int32_t z, const uint8_t* s, uint32_t k, uint32_t ct) -> bool {
+                if (!mbar_wait_bounded<true>(&empty[stage], phase ^ 1u, p.timeout_ns, abort_flag, p.dev_status))
+                    return false;
+                uint8_t* st = smem + stage * C::kStage;
+                const uint32_t sfb = min((uint32_t)C::kSfTiles, ct - k * C::kSfTiles) * 512;
+                mbar_arrive_expect_tx(&full[stage], N * 128u + sfb);
+                tma_load_3d(st + C::kOffB, m, (int32_t)(k * 128), 0, z, &full[stage]);
+                bulk_load(st + C::kOffSfB, s + (int64_t)k * C::kSfTiles * 512, sfb, &full[stage]);
+                if (++stage == kMtStages) { stage = 0; phase ^= 1u; }
+                return true;
+            };
+            bool ok = grid_wait(gridDim.x);
+            for (uint32_t u = u1_0; u < u1_1 && ok; ++u) ok = load(&map_x, 0, p.xs, u % K1, ct_d);
+            if (ok && u2_0 < u2_1) ok = grid_wait(2 * gridDim.x);
+            for (uint32_t u = u2_0; u < u2_1 && ok; ++u) {
+                const uint32_t r = u % AK2, a = r / K2;
+                ok = load(&map_h, (int32_t)a, p.hs + (int64_t)a * ct_h * 512, r - a * K2, ct_h);
+            }
+        }
+    } else if (warp == 2) {
+        if (lane == 0) {
+            // -------------------------------------------- tensor-core issuer
+            int stage = 0, buf = 0;
+            uint32_t phase = 0, buf_phase = 0;
+            // steps k0 .. k1-1 of a contraction of K elements into the next accumulator pair
+            auto contract = [&](uint32_t k0, uint32_t k1, int64_t K) -> bool {
+                if (!mbar_wait_bounded<true>(&tempty[buf], buf_phase ^ 1u, p.timeout_ns, abort_flag, p.dev_status))
+                    return false;
+                tc_fence_after();
+                const uint32_t d0 = tmem + buf * 2 * N;
+                for (uint32_t k = k0; k < k1; ++k) {
+                    if (!mbar_wait_bounded<true>(&full[stage], phase, p.timeout_ns, abort_flag, p.dev_status))
+                        return false;
+                    tc_fence_after();
+                    const uint32_t st = smem_u32(smem + stage * C::kStage);
+                    const uint32_t sf = tmem + C::kSfCol0 + stage * C::kSfCols;
+#pragma unroll
+                    for (int i = 0; i < 2 * C::kSfTiles; ++i)
+                        tc_cp_32x128b_warpx4(sf + 4 * i, smem_desc(st + C::kOffSfA + 512 * i, 0, 128, 0));
+#pragma unroll
+                    for (int i = 0; i < C::kSfTiles; ++i)
+                        tc_cp_32x128b_warpx4(sf + 4 * (2 * C::kSfTiles + i),
+                                             smem_desc(st + C::kOffSfB + 512 * i, 0, 128, 0));
+                    const int steps = (int)min64(4, (K - (int64_t)k * C::kKE + C::kKE / 4 - 1) / (C::kKE / 4));
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) {
+                        if (s >= steps) break;
+                        const uint64_t bd = smem_desc(st + C::kOffB + 32 * s, 16, 1024, 2);
+#pragma unroll
+                        for (int w = 0; w < 2; ++w) {
+                            const uint64_t ad = smem_desc(st + w * 16384 + 32 * s, 16, 1024, 2);
+                            const uint32_t acc = (k != k0 || s != 0) ? 1u : 0u;
+                            if constexpr (BITS == 8) {
+                                tc_mma_mxf8(d0 + w * N, ad, bd, idesc_mxf8(128, N, s, s), sf + 4 * w, sf + 8, acc);
+                            } else {
+                                constexpr uint32_t id0 = (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) |
+                                                         (1u << 23) | (1u << 27);  // E2M1 x E2M1, E8M0, M = 128
+                                const uint32_t id = (uint32_t)(s & 1) * 2;
+                                tc_mma_mxf4(d0 + w * N, ad, bd, id0 | (id << 4) | (id << 29),
+                                            sf + 8 * w + 4 * (s >> 1), sf + 16 + 4 * (s >> 1), acc);
+                            }
+                        }
+                    }
+                    tc_commit(&empty[stage]);
+                    if (++stage == kMtStages) { stage = 0; phase ^= 1u; }
+                }
+                tc_commit(&tfull[buf]);
+                if (++buf == 2) { buf = 0; buf_phase ^= 1u; }
+                return true;
+            };
+            bool ok = true;
+            for (uint32_t u = u1_0; u < u1_1 && ok;) {
+                const uint32_t tile = u / K1, end = min(u1_1, (tile + 1) * K1);
+                ok = contract(u - tile * K1, end - tile * K1, D);
+                u = end;
+            }
+            for (uint32_t u = u2_0; u < u2_1 && ok;) {
+                const uint32_t base = u / K2 * K2, end = min(u2_1, base + K2);  // AK2 is a multiple of K2
+                ok = contract(u - base, end - base, H);
+                u = end;
+            }
+            tc_commit(&drain);
+            volatile int no_abort = 0;
+            mbar_wait_bounded<true>(&drain, 0, p.timeout_ns, &no_abort, p.dev_status);
+        }
+    } else if (warp >= kMtEpiWarp0) {
+        const int et = tid - kMtEpiWarp0 * 32;
+        // ------------------------------------------------ zero the tile counters, quantize a share of x
+        for (int i = cta * kMtEpiThreads + et; i < p.ncounters; i += gridDim.x * kMtEpiThreads) p.counters[i] = 0;
+        {
+            const int64_t per_row = D / 8, items = T * per_row;  // 8 elements each; 4 neighbours make a block
+            for (int64_t i0 = (int64_t)cta * kMtEpiThreads + et - lane; i0 < items;
+                 i0 += (int64_t)gridDim.x * kMtEpiThreads) {
+                const int64_t i = i0 + lane;
+                const bool in = i < items;
+                const int64_t t = in ? i / per_row : 0, c = in ? (i - t * per_row) * 8 : 0;
+                uint4 u = make_uint4(0, 0, 0, 0);
+                if (in) u = *reinterpret_cast<const uint4*>(p.x + i * 16);
+                float v[8] = {bf16lo(u.x), bf16hi(u.x), bf16lo(u.y), bf16hi(u.y),
+                              bf16lo(u.z), bf16hi(u.z), bf16lo(u.w), bf16hi(u.w)};
+                uint32_t m = 0;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+                m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+                m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+                if (!in) continue;
+                const uint32_t s = e8m0_of<BITS == 8 ? 8 : 2>(m);
+                const float f = s == 0xFFu ? __uint_as_float(0x7FC00000u) : __uint_as_float((254u - s) << 23);
+                if constexpr (BITS == 8) {
+                    uint2 q;
+                    q.x = cvt_e4m3x2(v[0] * f, v[1] * f) | (cvt_e4m3x2(v[2] * f, v[3] * f) << 16);
+                    q.y = cvt_e4m3x2(v[4] * f, v[5] * f) | (cvt_e4m3x2(v[6] * f, v[7] * f) << 16);
+                    *reinterpret_cast<uint2*>(p.xq + i * 8) = q;
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[j] *= f;  // a NaN scale makes the block NaN whatever its codes
+                    *reinterpret_cast<uint32_t*>(p.xq + i * 4) = cvt_e2m1x8(v);
+                }
+                if ((lane & 3) == 0) {
+                    const int64_t kb = c / 32;
+                    uint8_t* w = p.xs + (kb >> 2) * 512 + (t & 31) * 16 + (t >> 5) * 4;
+                    w[kb & 3] = (uint8_t)s;
+                    if (c + 32 >= D)  // the rest of the last tile's word is padding
+                        for (int64_t z = (kb & 3) + 1; z < 4; ++z) w[z] = 0;
+                }
+            }
+        }
+        fence_proxy_async();
+        __threadfence();
+        epi_sync();
+        if (et == 0) atomicAdd(p.header, 1u);
+
+        const int quarter = warp & 3, cg = (warp - kMtEpiWarp0) >> 2;
+        const int r = quarter * 32 + lane;  // row of a weight tile = tensor-memory lane
+        const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16);
+        int buf = 0;
+        uint32_t buf_phase = 0;
+        bool ok = true;
+        const uint32_t slot_words = 2u * (uint32_t)T * 128u;  // one partial tile pair
+        auto my_slot = [&](uint32_t c, uint32_t first_tile, uint32_t tile) -> float* {
+            return p.part + (int64_t)(2 * c + (tile != first_tile)) * slot_words;
+        };
+        // every epilogue thread has written its partial sums: true for the CTA that completes the tile
+        auto arrive_last = [&](uint32_t* counter, uint32_t of) -> bool {
+            __threadfence();
+            epi_sync();
+            if (et == 0) {
+                last_s = atomicAdd(counter, 1u) + 1u == of;
+                __threadfence();
+            }
+            epi_sync();
+            return last_s != 0;
+        };
+
+        // ------------------------------------------------ first half: gate, up, SwiGLU, quantize h
+        constexpr int NC = N / 2;  // token columns of this warp
+        for (uint32_t u = u1_0; u < u1_1 && ok;) {
+            const uint32_t tile = u / K1, a = tile / TH, j = tile - a * TH;
+            const uint32_t end = min(u1_1, (tile + 1) * K1);
+            const bool whole = u == tile * K1 && end == (tile + 1) * K1;
+            u = end;
+            ok = epi_all(mbar_wait_bounded<true>(&tfull[buf], buf_phase, p.timeout_ns, abort_flag, p.dev_status));
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t mask = mask_s[a];
+            const int c0 = cg * NC;
+            const bool any = ((mask >> c0) & ((1ull << NC) - 1ull)) != 0;
+            uint32_t g[NC], h[NC];
+            if (any) {
+                tmem_ld_cols(lane_base + buf * 2 * N + c0, g);
+                tmem_ld_cols(lane_base + buf * 2 * N + N + c0, h);
+                tmem_ld_wait();
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&tempty[buf]);
+            if (++buf == 2) { buf = 0; buf_phase ^= 1u; }
+            if (!whole) {
+                float* w = my_slot(cta, u1_0 / K1, tile);
+#pragma unroll
+                for (int c = 0; c < NC; ++c)
+                    if ((mask >> (c0 + c)) & 1u) {
+                        __stcg(w + (c0 + c) * 128 + r, __uint_as_float(g[c]));
+                        __stcg(w + (T + c0 + c) * 128 + r, __uint_as_float(h[c]));
+                    }
+                const uint32_t lo = sp1.owner(tile * K1), hi = sp1.owner((tile + 1) * K1 - 1);
+                if (!arrive_last(p.counters + tile, hi - lo + 1)) continue;
+#pragma unroll
+                for (int c = 0; c < NC; ++c) g[c] = h[c] = 0u;
+                for (uint32_t o = lo; o <= hi; ++o) {
+                    const float* q = my_slot(o, sp1.start(o) / K1, tile);
+#pragma unroll
+                    for (int c = 0; c < NC; ++c)
+                        if ((mask >> (c0 + c)) & 1u) {
+                            g[c] = __float_as_uint(__uint_as_float(g[c]) + __ldcg(q + (c0 + c) * 128 + r));
+                            h[c] = __float_as_uint(__uint_as_float(h[c]) + __ldcg(q + (T + c0 + c) * 128 + r));
+                        }
+                }
+            }
+            const int64_t row = (int64_t)j * 128 + r;
+            const bool in = row < H;
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                const int t = c0 + c;
+                if (!((mask >> t) & 1u)) continue;
+                const float x1 = __uint_as_float(g[c]);
+                const float v = in ? x1 / (1.0f + expf(-x1)) * __uint_as_float(h[c]) : 0.0f;
+                // the warp's 32 rows are one block of token t
+                const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(v) & 0x7FFFFFFFu);
+                const uint32_t s = e8m0_of<BITS == 8 ? 8 : 2>(m);
+                const float f = s == 0xFFu ? __uint_as_float(0x7FC00000u) : __uint_as_float((254u - s) << 23);
+                const int64_t at = (int64_t)a * T + t;
+                if constexpr (BITS == 8) {
+                    if (in) p.hq[at * H + row] = (uint8_t)cvt_e4m3x2(v * f, 0.0f);
+                } else {
+                    const float q8[8] = {v * f, __shfl_down_sync(0xffffffffu, v * f, 1), 0, 0, 0, 0, 0, 0};
+                    if (in && (lane & 1) == 0) p.hq[at * (H / 2) + row / 2] = (uint8_t)cvt_e2m1x8(q8);
+                }
+                if (lane == 0)
+                    p.hs[((int64_t)a * ct_h + j) * 512 + (t & 31) * 16 + (t >> 5) * 4 + quarter] =
+                        (uint8_t)(in ? s : 0u);
+            }
+        }
+        fence_proxy_async();
+        __threadfence();
+        epi_sync();
+        if (et == 0) atomicAdd(p.header, 1u);
+
+        // ------------------------------------------------ second half: down, weighted sum over experts
+        float total[N];  // warps 4-7: rows 0-127 of the tile, warps 8-11: rows 128-255
+        for (uint32_t u = u2_0; u < u2_1 && ok;) {
+            const uint32_t tile = u / AK2, t_end = min(u2_1, (tile + 1) * AK2);
+            const bool whole = u == tile * AK2 && t_end == (tile + 1) * AK2;
+#pragma unroll
+            for (int c = 0; c < N; ++c) total[c] = 0.0f;
+            while (u < t_end) {
+                const uint32_t a = (u - tile * AK2) / K2;
+                u = min(t_end, tile * AK2 + (a + 1) * K2);
+                if (et < T) {  // token et's weight for this expert
+                    const int e = list_s[a];
+                    float w = 0.0f;
+                    for (int j = 0; j < p.top_k; ++j)
+                        if (sel_e[et * p.top_k + j] == e) w = sel_w[et * p.top_k + j];
+                    w_s[buf][et] = w;
+                }
+                ok = epi_all(mbar_wait_bounded<true>(&tfull[buf], buf_phase, p.timeout_ns, abort_flag, p.dev_status));
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t mask = mask_s[a];
+#pragma unroll
+                for (int c = 0; c < N; c += 32) {
+                    if (((mask >> c) & 0xFFFFFFFFull) == 0) continue;
+                    uint32_t v[32];
+                    tmem_ld_32x32b_x32(lane_base + buf * 2 * N + cg * N + c, v);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if ((mask >> (c + i)) & 1u) total[c + i] += w_s[buf][c + i] * __uint_as_float(v[i]);
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&tempty[buf]);
+                if (++buf == 2) { buf = 0; buf_phase ^= 1u; }
+            }
+            if (!ok) break;
+            if (!whole) {
+                float* w = my_slot(cta, u2_0 / AK2, tile) + cg * T * 128;
+#pragma unroll
+                for (int c = 0; c < N; ++c)
+                    if (c < T) __stcg(w + c * 128 + r, total[c]);
+                const uint32_t lo = sp2.owner(tile * AK2), hi = sp2.owner((tile + 1) * AK2 - 1);
+                if (!arrive_last(p.counters + A * TH + tile, hi - lo + 1)) continue;
+#pragma unroll
+                for (int c = 0; c < N; ++c) total[c] = 0.0f;
+                for (uint32_t o = lo; o <= hi; ++o) {
+                    const float* q = my_slot(o, sp2.start(o) / AK2, tile) + cg * T * 128;
+#pragma unroll
+                    for (int c = 0; c < N; ++c)
+                        if (c < T) total[c] += __ldcg(q + c * 128 + r);
+                }
+            }
+            const int64_t d = (int64_t)tile * 256 + cg * 128 + r;
+            if (d < D)
+#pragma unroll
+                for (int c = 0; c < N; ++c)
+                    if (c < T) p.y[c * D + d] = __float2bfloat16(total[c]);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (abort_s && tid == 0) {  // given up: let the copies in flight land before the CTA's memory goes
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 1000000ull) __nanosleep(1000);
+    }
+    __syncthreads();
+    if (warp == 2) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+    if (tid == 0) {
+        // the last CTA to leave puts the grid barrier back to zero for the next launch
+        __threadfence();
+        if (atomicAdd(p.header + 1, 1u) + 1u == gridDim.x) {
+            p.header[0] = 0u;
+            p.header[1] = 0u;
+            __threadfence();
+        }
+    }
+}
+
+// ---------------------------------------------------------------- host side
+static int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
+
+struct MtLayout {
+    int64_t counters, ncounters, xq, xs, hq, hs, part, total;
+};
+
+static MtLayout mt_layout(int64_t T, int64_t E, int64_t D, int64_t H, int64_t k, int bits) {
+    const int64_t A = std::min(E, T * k), ct_d = (D + 127) / 128, ct_h = (H + 127) / 128;
+    MtLayout l;
+    l.counters = kMtHeader;
+    l.ncounters = A * ct_h + (D + 255) / 256;
+    l.xq = l.counters + up256(l.ncounters * 4);
+    l.xs = l.xq + up256(T * D * bits / 8);
+    l.hq = l.xs + up256(ct_d * 512);
+    l.hs = l.hq + up256(A * T * H * bits / 8);
+    l.part = l.hs + up256(A * ct_h * 512);
+    l.total = l.part + (int64_t)host::num_sms() * 2 * 2 * T * 128 * 4;
+    return l;
+}
+
+static bool mt_map(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int64_t planes, int box_rows) {
+    host::EncodeTiledFn fn = host::encode_fn();
+    if (!fn) return false;
+    const int rank = planes > 0 ? 3 : 2;
+    cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)planes};
+    cuuint64_t strides[2] = {(cuuint64_t)cols, (cuuint64_t)(cols * rows)};
+    cuuint32_t box[3] = {128, (cuuint32_t)box_rows, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<void*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int BITS, int N>
+static mxfp8_status_t mt_launch(const CUtensorMap (&m)[5], const MtParams& p, cudaStream_t st) {
+    using C = MtCfg<BITS, N>;
+    static std::atomic<int> attr_set[host::kMaxDevices];
+    if (!host::ensure_smem(reinterpret_cast<const void*>(moe_tokens_kernel<BITS, N>), C::kSmem, attr_set))
+        return MXFP8_ERR_LAUNCH;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeCooperative;  // every CTA is resident: they wait for one another
+    attr[0].val.cooperative = 1;
+    cfg.gridDim = dim3((unsigned)host::num_sms());
+    cfg.blockDim = dim3(kMtThreads);
+    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, moe_tokens_kernel<BITS, N>, m[0], m[1], m[2], m[3], m[4], p) != cudaSuccess) {
+        cudaGetLastError();
+        return MXFP8_ERR_LAUNCH;
+    }
+    return host::last_launch_status();
+}
+
+static mxfp8_status_t mt_shape(int64_t T, int64_t E, int64_t D, int64_t H, int32_t k, int32_t bits) {
+    if (T < 0 || T > kMtMaxTokens || E < 1 || E > kMtMaxExperts || D <= 0 || H <= 0 || k < 1 || k > kMtMaxTopK || k > E ||
+        E * D > INT32_MAX || E * H > INT32_MAX)
+        return MXFP8_ERR_SHAPE;
+    if (bits != 4 && bits != 8) return MXFP8_ERR_LAYOUT;
+    // units of work are counted in 32 bits
+    if (E * ((H + 127) / 128) * ((D + 127) / 128) > INT32_MAX) return MXFP8_ERR_SHAPE;
+    return (D % 32 || H % 32) ? MXFP8_ERR_ALIGN : MXFP8_OK;
+}
+
+}  // namespace mx
+
+using namespace mx;
+
+extern "C" size_t mx_moe_tokens_workspace(int32_t max_tokens, int32_t E, int64_t D, int64_t H, int32_t top_k,
+                                          int32_t bits) {
+    if (max_tokens < 1 || mt_shape(max_tokens, E, D, H, top_k, bits) != MXFP8_OK) return 0;
+    return (size_t)mt_layout(max_tokens, E, D, H, top_k, bits).total;
+}
+
+extern "C" mxfp8_status_t mx_moe_tokens(const void* x_bf16, const float* router_logits, int32_t T, int32_t E, int64_t D,
+                                        int64_t H, int32_t top_k, int32_t score, int32_t bits, const void* gate_q,
+                                        const void* gate_s, const void* up_q, const void* up_s, const void* down_q,
+                                        const void* down_s, void* workspace, size_t workspace_bytes, void* y_bf16,
+                                        int32_t* dev_status, mxfp8_stream_t stream) {
+    if (mxfp8_status_t s = mt_shape(T, E, D, H, top_k, bits); s != MXFP8_OK) return s;
+    if (score < MX_SCORE_SOFTMAX || score > MX_SCORE_SIGMOID) return MXFP8_ERR_LAYOUT;
+    if (T == 0) return MXFP8_OK;
+    const void* ptrs[] = {x_bf16, gate_q, gate_s, up_q, up_s, down_q, down_s, workspace, y_bf16};
+    if (!router_logits) return MXFP8_ERR_NULL;
+    for (const void* q : ptrs)
+        if (!q) return MXFP8_ERR_NULL;
+    for (const void* q : ptrs)
+        if (!host::aligned16(q)) return MXFP8_ERR_ALIGN;
+    if (reinterpret_cast<uintptr_t>(router_logits) & 3u) return MXFP8_ERR_ALIGN;
+    if (mxfp8_status_t a = host::check_arch(); a != MXFP8_OK) return a;
+    const MtLayout l = mt_layout(T, E, D, H, top_k, bits);
+    if (workspace_bytes < (size_t)l.total) return MXFP8_ERR_SHAPE;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    const int N = T <= 32 ? 32 : 64;
+    const int64_t Db = D * bits / 8, Hb = H * bits / 8;
+    CUtensorMap m[5];
+    if (!mt_map(&m[0], gate_q, Db, (int64_t)E * H, 0, 128) || !mt_map(&m[1], up_q, Db, (int64_t)E * H, 0, 128) ||
+        !mt_map(&m[2], down_q, Hb, (int64_t)E * D, 0, 128) || !mt_map(&m[3], ws + l.xq, Db, T, 1, N) ||
+        !mt_map(&m[4], ws + l.hq, Hb, T, std::min<int64_t>(E, (int64_t)T * top_k), N))
+        return MXFP8_ERR_DRIVER;
+    MtParams p{};
+    p.x = static_cast<const uint8_t*>(x_bf16);
+    p.logits = router_logits;
+    p.s_gate = static_cast<const uint8_t*>(gate_s);
+    p.s_up = static_cast<const uint8_t*>(up_s);
+    p.s_down = static_cast<const uint8_t*>(down_s);
+    p.xq = ws + l.xq;
+    p.xs = ws + l.xs;
+    p.hq = ws + l.hq;
+    p.hs = ws + l.hs;
+    p.part = reinterpret_cast<float*>(ws + l.part);
+    p.header = reinterpret_cast<uint32_t*>(ws);
+    p.counters = reinterpret_cast<uint32_t*>(ws + l.counters);
+    p.y = static_cast<__nv_bfloat16*>(y_bf16);
+    p.dev_status = dev_status;
+    p.timeout_ns = 2000000000ull;
+    p.D = D;
+    p.H = H;
+    p.T = T;
+    p.E = E;
+    p.top_k = top_k;
+    p.score = score;
+    p.ncounters = (int)l.ncounters;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (bits == 8) return N == 32 ? mt_launch<8, 32>(m, p, st) : mt_launch<8, 64>(m, p, st);
+    return N == 32 ? mt_launch<4, 32>(m, p, st) : mt_launch<4, 64>(m, p, st);
+}

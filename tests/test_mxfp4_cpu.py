@@ -87,6 +87,30 @@ def test_refusals_of_the_binding(call, match):
         call()
 
 
+@pytest.mark.parametrize("make,match", [
+    (lambda: mx.MxMoeTokens(u8(2, 64, 128), u8(2, 512), u8(2, 128, 64), 1), "gate"),
+    (lambda: mx.MxMoeTokens((u8(2, 64, 128), u8(2, 512)), (u8(2, 64, 128), u8(2, 512)), (u8(2, 100, 64), u8(2, 512)),
+                            1), "gate codes"),
+    (lambda: mx.MxMoeTokens((u8(2, 64, 128), u8(2, 512)), (u8(2, 32, 128), u8(2, 512)), (u8(2, 128, 64), u8(2, 512)),
+                            1), "up codes"),
+    (lambda: mx.MxMoeTokens((u8(2, 64, 128), u8(2, 512)), (u8(2, 64, 128), u8(2, 512)), (u8(2, 128, 32), u8(2, 512)),
+                            1), "down codes"),
+    (lambda: mx.MxMoeTokens((u8(2, 64, 128), u8(2, 512)), (u8(2, 64, 128), u8(2, 512)), (u8(2, 128, 64), u8(2, 512)),
+                            3), "top_k"),
+    (lambda: mx.MxMoeTokens((u8(2, 64, 128), u8(2, 511)), (u8(2, 64, 128), u8(2, 512)), (u8(2, 128, 64), u8(2, 512)),
+                            1), "gate scales"),
+    (lambda: mx.MxMoeTokens((u8(2, 64, 48), u8(2, 512)), (u8(2, 64, 48), u8(2, 512)), (u8(2, 48, 64), u8(2, 512)),
+                            1), "multiples of 32"),
+    (lambda: mx.MxMoeTokens((u8(300, 32, 32), u8(300, 512)), (u8(300, 32, 32), u8(300, 512)),
+                            (u8(300, 32, 32), u8(300, 512)), 1), "experts"),
+    (lambda: mx.MxMoeTokens((u8(2, 64, 128), u8(2, 512)), (u8(2, 64, 128), u8(2, 512)), (u8(2, 128, 64), u8(2, 512)),
+                            1), "CUDA"),
+])
+def test_refusals_of_the_few_token_layer(make, match):
+    with pytest.raises(ValueError, match=match):
+        make()
+
+
 def test_refusals_of_the_c_abi():
     L = mx.load()
     P = ctypes.c_void_p
@@ -117,3 +141,15 @@ def test_refusals_of_the_c_abi():
     assert mm(a, a, a, a, a, 2, 64, 64, 48, a, None, None) == 3
     assert mm(a, a, odd, a, a, 2, 64, 64, 64, a, None, None) == 3
     assert mm(a, a, a, a, a, 2, 1 << 32, 64, 64, a, None, None) == 2
+    mt = L.mx_moe_tokens
+    ok = dict(x=a, l=a, T=4, E=8, D=64, H=64, k=2, score=0, bits=8, g=a, gs=a, u=a, us=a, d=a, ds=a, ws=a, n=1 << 40,
+              y=a, st=None, stream=None)
+    call = lambda **kw: mt(*{**ok, **kw}.values())
+    assert call(T=65) == 2 and call(T=-1) == 2 and call(E=0) == 2 and call(E=257) == 2 and call(k=0) == 2
+    assert call(k=9) == 2 and call(E=32, k=17) == 2 and call(D=0) == 2 and call(D=48) == 3 and call(H=40) == 3
+    assert call(bits=6) == 4 and call(score=3) == 4 and call(x=None) == 1 and call(l=None) == 1 and call(ws=None) == 1
+    assert call(y=odd) == 3 and call(gs=odd) == 3 and call(l=P((1 << 20) + 2)) == 3 and call(D=1 << 40) == 2
+    assert call(T=0, x=None) == 0
+    size = L.mx_moe_tokens_workspace
+    assert size(65, 8, 64, 64, 2, 8) == 0 and size(4, 8, 64, 64, 9, 8) == 0 and size(4, 8, 60, 64, 2, 8) == 0
+    assert size(4, 8, 64, 64, 2, 8) > 0 and size(64, 8, 64, 64, 2, 8) > size(4, 8, 64, 64, 2, 8)
