@@ -1,15 +1,22 @@
 // mxfp4_quantize.cu -- MXFP4 quantization (plain, of expert weights, and of silu(h1) * h3) and its inverse.
 //
 // Per block of 32 elements along the row: e = floor(log2 amax) - 2, clamped at -127; codes
-// RNE_E2M1(x 2^-e), saturated at 6; scale byte e + 127.  Bounded by HBM: 2 (4 for SwiGLU) bytes read and
-// 17/32 written per element, about ten arithmetic instructions each (SwiGLU: thirty).
+// RNE_E2M1(x 2^-e), saturated at 6; scale byte e + 127.  2 (4 for SwiGLU) bytes read and 17/32 written per
+// element, the inverse the other way round.
 //
 // A CTA of 8 warps owns 128 rows x 256 columns of a padded row tile (groups start on fresh 128-row tiles in
-// the blocked scale layout, so a CTA's rows are one band of it and it also writes the band's padding); each
-// warp 32 rows x 128 columns, two rows per load instruction, 16 lanes x 16 bytes a row.  A block of 32 spans
-// 4 lanes (2 shuffles for its amax); the four scale bytes of a row's 128 columns meet in one 32-bit word
-// (2 shuffles) and lane l stores the word of row l, so a warp writes its quarter of the 512-byte scale tile
-// with one instruction.
+// the blocked scale layout, so a CTA's rows are one band of it and it also writes the band's padding), each
+// warp 32 rows x 128 columns.
+//   plain     a thread takes a whole block (four 16-byte loads, one 16-byte store of codes): no shuffles but
+//             two that join a row's four scale bytes into one word.  Against four lanes a block this halves
+//             the instructions per element: [16, 8192, 5120] takes 260 us instead of 303, 6.5 TB/s, which
+//             is HBM's copy rate.  Five CTAs an SM; six spill, four leave loads too few.
+//   SwiGLU    two threads a block, to fit six CTAs an SM.  expf and the correctly rounded division make 25 of
+//             about 32 instructions an element, so it is bound by issue slots, not HBM: 171 us for 16384 x 8192,
+//             3.6 TB/s (a block a thread 174-197 us, four lanes a block 169-190).  A cheaper exponential or
+//             division would move values across E2M1's wide rounding borders; it is not taken.
+//   inverse   four lanes a block: 16-byte stores of 8 values, whole 32-byte sectors by neighbouring lanes.
+//             274 us for [16, 8192, 5120], 6.2 TB/s (write-heavy traffic).
 
 #include "host_common.h"
 #include "mx4.cuh"
@@ -18,7 +25,6 @@ namespace mx {
 
 constexpr int kQ4Threads = 256;
 constexpr int kQ4Cols = 256;   // columns of a CTA's tile
-constexpr int kQ4Batch = 8;    // row pairs whose loads are in flight together
 
 struct Q4Params {
     const uint8_t* x;      // bf16 [batch][R][C] (h1 for SwiGLU); dequantize: codes [batch][R][C/2]
@@ -81,79 +87,163 @@ __device__ __forceinline__ void unpack8(const uint4& u, float (&v)[8]) {
     }
 }
 
+// Largest magnitude of each half of two bf16 pairs, NaN winning (the sign bits left are not used).
+__device__ __forceinline__ uint32_t amax_pair(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+// A bf16 pair times the bf16 power of two f, exact in fp32 (a -0 addend keeps the sign of a zero).
+__device__ __forceinline__ float2 scale_pair(uint32_t w, uint32_t f) {
+    float2 r;
+    asm("{\n\t.reg .b16 a0, a1, b0, b1;\n\tmov.b32 {a0, a1}, %2;\n\tmov.b32 {b0, b1}, %3;\n\t"
+        "fma.rn.f32.bf16 %0, a0, b0, 0f80000000;\n\tfma.rn.f32.bf16 %1, a1, b0, 0f80000000;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "r"(w), "r"(f));
+    return r;
+}
+
+// A block of 32 bf16 (16 pairs) -> its scale byte, codes in c.
+__device__ __forceinline__ uint32_t q4_block_bf16(const uint32_t (&w)[16], uint32_t (&c)[4]) {
+    uint32_t m = w[0];
+#pragma unroll
+    for (int i = 1; i < 16; ++i) m = amax_pair(m, w[i]);
+    const uint32_t s = e8m0_of<2>(max(m & 0x7FFFu, (m >> 16) & 0x7FFFu) << 16);
+    const uint32_t f = (254u - s) << 7;  // 2^(127 - s) as a bf16: s <= 252 for a finite amax
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 r = scale_pair(w[4 * i + j], f);
+            v[2 * j] = r.x;
+            v[2 * j + 1] = r.y;
+        }
+        c[i] = cvt_e2m1x8(v);
+    }
+    if (s == 0xFFu) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float v[8] = {bf16lo(w[4 * i]), bf16hi(w[4 * i]), bf16lo(w[4 * i + 1]), bf16hi(w[4 * i + 1]),
+                                bf16lo(w[4 * i + 2]), bf16hi(w[4 * i + 2]), bf16lo(w[4 * i + 3]), bf16hi(w[4 * i + 3])};
+            c[i] = nonfinite_e2m1x8(v);
+        }
+    }
+    return s;
+}
+
+// fp32 pairs, two lanes of one instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 z, x, y;\n\t"
+        "mov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
+// EPT elements of a block (the other 32 / EPT - 1 shares are the neighbouring lanes') of silu(w) * g in fp32 -> the
+// block's scale byte, this share's codes in c.
+template <int EPT>
+__device__ __forceinline__ uint32_t q4_share_swiglu(const uint32_t (&w)[EPT / 2], const uint32_t (&g)[EPT / 2],
+                                                    uint32_t (&c)[EPT / 8]) {
+    float v[EPT];
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < EPT / 2; ++i) {
+        const float a = bf16lo(w[i]), b = bf16hi(w[i]);
+        const float2 h = mul2(make_float2(a / (1.0f + expf(-a)), b / (1.0f + expf(-b))),
+                              make_float2(bf16lo(g[i]), bf16hi(g[i])));
+        v[2 * i] = h.x;
+        v[2 * i + 1] = h.y;
+        m = max(m, max(__float_as_uint(h.x) & 0x7FFFFFFFu, __float_as_uint(h.y) & 0x7FFFFFFFu));
+    }
+#pragma unroll
+    for (int d = 1; d < 32 / EPT; d <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
+    const uint32_t s = e8m0_of<2>(m);
+    const float f = __uint_as_float((254u - s) << 23);
+#pragma unroll
+    for (int i = 0; i < EPT / 8; ++i) {
+        float z[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 h = mul2(make_float2(v[8 * i + 2 * j], v[8 * i + 2 * j + 1]), make_float2(f, f));
+            z[2 * j] = h.x;
+            z[2 * j + 1] = h.y;
+        }
+        c[i] = cvt_e2m1x8(z);
+    }
+    if (s == 0xFFu) {
+#pragma unroll
+        for (int i = 0; i < EPT / 8; ++i) {
+            float z[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) z[j] = v[8 * i + j];
+            c[i] = nonfinite_e2m1x8(z);
+        }
+    }
+    return s;
+}
+
+// KIND's elements of a thread: a whole block of a plain quantization needs no shuffles, while SwiGLU's
+// arithmetic wants more warps than its registers would leave with one.
 template <int KIND>
-__global__ void __launch_bounds__(kQ4Threads) mxfp4_quantize_kernel(const Q4Params p) {
+__global__ void __launch_bounds__(kQ4Threads, KIND == kQ4Swiglu ? 6 : 5) mxfp4_quantize_kernel(const Q4Params p) {
+    constexpr int EPT = KIND == kQ4Swiglu ? 16 : 32;
+    constexpr int kLanes = 128 / EPT;        // lanes along a row's 128 columns
+    constexpr int kRows = 32 / kLanes;       // rows a warp takes at a time
     const Q4Rows t = q4_rows(p);
     if (t.rows == 0) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int quarter = warp & 3, half = lane >> 4;
+    const int quarter = warp & 3;
     const int64_t C = p.C, ct = (C + 127) / 128;
-    const int64_t base = t.b * p.R + t.row0;  // first row among all matrices'
-    const int rq = quarter * 32;              // the warp's first row in the tile
+    const int r0 = quarter * 32 + lane / kLanes;
     uint8_t* sb = p.s + t.b * p.s_bstride;
     for (int cc = 0; cc < p.cols_per_cta; ++cc) {
         const int64_t k128 = (blockIdx.y * (int64_t)p.cols_per_cta + cc) * (kQ4Cols / 128) + (warp >> 2);
         if (k128 >= ct) break;
-        const int64_t c = k128 * 128 + (lane & 15) * 8;  // C % 32 == 0: a lane's 8 columns are all in or all out
+        const int64_t c = k128 * 128 + (lane % kLanes) * EPT;
         const bool cin = c < C;
-        uint32_t word = 0;  // scale bytes of row rq + lane
+        int64_t at = (t.b * p.R + t.row0 + r0) * C + c;  // the thread's first element
+#pragma unroll 1
+        for (int i = 0; i < 32; i += kRows, at += kRows * C) {
+            const int r = r0 + i;
+            const bool in = cin && r < t.rows;
+            uint32_t w[EPT / 2], g[KIND == kQ4Swiglu ? EPT / 2 : 1], codes[EPT / 8], s;
 #pragma unroll
-        for (int b0 = 0; b0 < 16; b0 += kQ4Batch) {
-            uint4 u[kQ4Batch], u2[KIND == kQ4Swiglu ? kQ4Batch : 1];
-#pragma unroll
-            for (int i = 0; i < kQ4Batch; ++i) {
-                const int r = rq + 2 * (b0 + i) + half;
-                u[i] = make_uint4(0, 0, 0, 0);
-                if (KIND == kQ4Swiglu) u2[i] = u[i];
-                if (cin && r < t.rows) {
-                    u[i] = ld_stream(p.x + ((base + r) * C + c) * 2);
-                    if (KIND == kQ4Swiglu) u2[i] = ld_stream(p.x2 + ((base + r) * C + c) * 2);
+            for (int j = 0; j < EPT / 8; ++j) {
+                uint4 u = make_uint4(0, 0, 0, 0);
+                if (in) u = *reinterpret_cast<const uint4*>(p.x + at * 2 + 16 * j);
+                w[4 * j] = u.x; w[4 * j + 1] = u.y; w[4 * j + 2] = u.z; w[4 * j + 3] = u.w;
+                if constexpr (KIND == kQ4Swiglu) {
+                    if (in) u = *reinterpret_cast<const uint4*>(p.x2 + at * 2 + 16 * j);
+                    g[4 * j] = u.x; g[4 * j + 1] = u.y; g[4 * j + 2] = u.z; g[4 * j + 3] = u.w;
                 }
             }
+            if constexpr (KIND == kQ4Swiglu) s = q4_share_swiglu<EPT>(w, g, codes);
+            else s = q4_block_bf16(w, codes);
+            if (in) {
+                uint8_t* q = p.q + at / 2;
+                if constexpr (EPT == 32) *reinterpret_cast<uint4*>(q) = make_uint4(codes[0], codes[1], codes[2], codes[3]);
+                else if constexpr (EPT == 16) *reinterpret_cast<uint2*>(q) = make_uint2(codes[0], codes[1]);
+                else *reinterpret_cast<uint32_t*>(q) = codes[0];
+            }
+            if (p.blocked) {
+                // rows outside the group and columns past C were read as zeros: their scales are 0
+                uint32_t word = s << (8 * ((lane % kLanes) / (32 / EPT)));
 #pragma unroll
-            for (int i = 0; i < kQ4Batch; ++i) {
-                const int r = rq + 2 * (b0 + i) + half;
-                float v[8];
-                unpack8(u[i], v);
-                if constexpr (KIND == kQ4Swiglu) {
-                    float g[8];
-                    unpack8(u2[i], g);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) v[j] = v[j] / (1.0f + expf(-v[j])) * g[j];
-                }
-                uint32_t m = 0;  // magnitude bits order like the magnitudes, NaN above Inf above all else
-#pragma unroll
-                for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
-                m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-                m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-                const uint32_t s = e8m0_of<2>(m);
-                uint32_t codes;
-                if (s == 0xFFu) {
-                    codes = nonfinite_e2m1x8(v);
-                } else {
-                    const float f = __uint_as_float((254u - s) << 23);  // 2^(127 - s): s <= 252 here
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) v[j] *= f;
-                    codes = cvt_e2m1x8(v);
-                }
-                if (cin && r < t.rows) *reinterpret_cast<uint32_t*>(p.q + ((base + r) * C + c) / 2) = codes;
-                if (p.blocked) {
-                    uint32_t w = s << (8 * ((lane >> 2) & 3));
-                    w |= __shfl_xor_sync(0xffffffffu, w, 4);
-                    w |= __shfl_xor_sync(0xffffffffu, w, 8);
-                    w = __shfl_sync(0xffffffffu, w, (lane & 1) * 16);
-                    if ((lane >> 1) == b0 + i) word = w;  // rows outside the group and columns past C: 0
-                } else if (cin && r < t.rows && (lane & 3) == 0) {
-                    sb[(t.row0 + r) * (C / 32) + c / 32] = (uint8_t)s;
-                }
+                for (int d = 32 / EPT; d < kLanes; d <<= 1) word |= __shfl_xor_sync(0xffffffffu, word, d);
+                if (lane % kLanes == 0)
+                    *reinterpret_cast<uint32_t*>(sb + (t.band * ct + k128) * 512 + (r & 31) * 16 + quarter * 4) = word;
+            } else if (in && c % 32 == 0) {
+                sb[(t.row0 + r) * (C / 32) + c / 32] = (uint8_t)s;
             }
         }
-        if (p.blocked)
-            *reinterpret_cast<uint32_t*>(sb + (t.band * ct + k128) * 512 + lane * 16 + quarter * 4) = word;
     }
 }
 
-__global__ void __launch_bounds__(kQ4Threads) mxfp4_dequantize_kernel(const Q4Params p) {
+__global__ void __launch_bounds__(kQ4Threads, 6) mxfp4_dequantize_kernel(const Q4Params p) {
     const Q4Rows t = q4_rows(p);
     if (t.rows == 0) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -170,28 +260,31 @@ __global__ void __launch_bounds__(kQ4Threads) mxfp4_dequantize_kernel(const Q4Pa
         uint32_t word = 0;
         if (p.blocked)
             word = *reinterpret_cast<const uint32_t*>(sb + (t.band * ct + k128) * 512 + lane * 16 + quarter * 4);
-        uint32_t codes[16];
+#pragma unroll 1
+        for (int b0 = 0; b0 < 16; b0 += 8) {
+            uint32_t codes[8];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int r = rq + 2 * i + half;
-            codes[i] = 0;
-            if (cin && r < t.rows) codes[i] = *reinterpret_cast<const uint32_t*>(p.x + ((base + r) * C + c) / 2);
-        }
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int r = rq + 2 * i + half;
-            const uint32_t w = __shfl_sync(0xffffffffu, word, 2 * i + half);
-            uint32_t s = (w >> (8 * ((lane >> 2) & 3))) & 0xFFu;
-            if (!cin || r >= t.rows) continue;
-            if (!p.blocked) s = sb[(t.row0 + r) * (C / 32) + c / 32];
-            const float f = e8m0_value(s);
-            uint32_t o[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 v = e2m1x2_value((codes[i] >> (8 * j)) & 0xFFu);
-                o[j] = pack_bf16x2(v.x * f, v.y * f);
+            for (int i = 0; i < 8; ++i) {
+                const int r = rq + 2 * (b0 + i) + half;
+                codes[i] = 0;
+                if (cin && r < t.rows) codes[i] = *reinterpret_cast<const uint32_t*>(p.x + ((base + r) * C + c) / 2);
             }
-            *reinterpret_cast<uint4*>(p.q + ((base + r) * C + c) * 2) = make_uint4(o[0], o[1], o[2], o[3]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int r = rq + 2 * (b0 + i) + half;
+                const uint32_t w = __shfl_sync(0xffffffffu, word, 2 * (b0 + i) + half);
+                uint32_t s = (w >> (8 * ((lane >> 2) & 3))) & 0xFFu;
+                if (!cin || r >= t.rows) continue;
+                if (!p.blocked) s = sb[(t.row0 + r) * (C / 32) + c / 32];
+                const float f = e8m0_value(s);
+                uint32_t o[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 v = e2m1x2_value((codes[i] >> (8 * j)) & 0xFFu);
+                    o[j] = pack_bf16x2(v.x * f, v.y * f);
+                }
+                *reinterpret_cast<uint4*>(p.q + ((base + r) * C + c) * 2) = make_uint4(o[0], o[1], o[2], o[3]);
+            }
         }
     }
 }
