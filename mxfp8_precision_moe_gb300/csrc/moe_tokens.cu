@@ -37,8 +37,9 @@ constexpr int kMtMaxTopK = 16;
 constexpr int kMtThreads = 384;
 constexpr int kMtEpiWarp0 = 4;
 constexpr int kMtEpiThreads = 256;
-constexpr int kMtStages = 5;
+constexpr int kMtRouteThreads = 128;
 constexpr int kMtHeader = 256;  // workspace bytes before the tile counters
+constexpr int kMtStatic = 10 * 1024;  // static shared memory at most
 
 template <int BITS, int N>
 struct MtCfg {
@@ -50,11 +51,16 @@ struct MtCfg {
     static constexpr int kStage = (kOffSfB + kSfTiles * 512 + 1023) / 1024 * 1024;
     static constexpr int kSfCols = 3 * 4 * kSfTiles;    // tensor-memory columns of a stage's scales
     static constexpr int kSfCol0 = 4 * N;               // after two buffers of two accumulators
-    static constexpr int kSmem = kMtStages * kStage + 1024;
+    static constexpr int kStages = (227 * 1024 - kMtStatic - 1024) / kStage;
+    static constexpr int kSmem = kStages * kStage + 1024;
+    static_assert(kStages >= 5, "too few stages to cover HBM's latency");
     static_assert(kOffB % 1024 == 0, "swizzled tiles start on 1024-byte boundaries");
-    static_assert(kSfCol0 + kMtStages * kSfCols <= 512, "tensor memory overflow");
+    static_assert(kSfCol0 + kStages * kSfCols <= 512, "tensor memory overflow");
 };
-static_assert(MtCfg<4, 64>::kSmem + 10 * 1024 <= 227 * 1024, "shared memory");
+
+// Words of the workspace's header: CTAs that have arrived at each grid-wide point.  One word each: a CTA does not
+// wait at a point that it has no use for, so arrivals at different points mix.
+enum MtPoint : int { kMtXDone = 0, kMtHDone = 1, kMtSumsDone = 2, kMtExits = 3 };
 
 struct MtParams {
     const uint8_t* x;        // bf16 [T][D]
@@ -67,7 +73,7 @@ struct MtParams {
     uint8_t* hq;             // codes [active][T][H], scales [active][ct(H)][512]
     uint8_t* hs;
     float* part;             // [CTA][2][2][T][128] partial sums
-    uint32_t* header;        // grid barrier arrivals, exits
+    uint32_t* header;        // arrivals at the grid-wide points (MtPoint)
     uint32_t* counters;      // arrivals per tile: first half, then second half
     __nv_bfloat16* y;        // [T][D]
     int32_t* dev_status;
@@ -77,14 +83,42 @@ struct MtParams {
     int ncounters;
 };
 
-__device__ __forceinline__ void tc_mma_mxf4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                            uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate) {
+// One lane of a converged warp.
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r;
+}
+// Tensor-core operations of the lane whose `one` is set.
+__device__ __forceinline__ void cp_scales(uint32_t one, uint32_t taddr, uint64_t sdesc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(
-            d_tmem),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa_tmem), "r"(sfb_tmem)
+        "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %0, 0;\n\t"
+        "@q tcgen05.cp.cta_group::1.32x128b.warpx4 [%1], %2;\n\t}" ::"r"(one),
+        "r"(taddr), "l"(sdesc)
+        : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t one, uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %0, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%1];\n\t}" ::"r"(one),
+        "r"(smem_u32(bar))
+        : "memory");
+}
+__device__ __forceinline__ void mma_mxf8(uint32_t one, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
+                                         uint32_t sfb, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.u32 q, %7, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(
+            d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb), "r"(one)
+        : "memory");
+}
+__device__ __forceinline__ void mma_mxf4(uint32_t one, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
+                                         uint32_t sfb, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.u32 q, %7, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb), "r"(one)
         : "memory");
 }
 
@@ -95,6 +129,12 @@ __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
           "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(taddr));
+}
+// One column: a value per lane.
+__device__ __forceinline__ uint32_t tmem_ld_col(uint32_t taddr) {
+    uint32_t r;
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr));
+    return r;
 }
 __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[16]) { tmem_ld_32x32b_x16(taddr, r); }
 __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[32]) { tmem_ld_32x32b_x32(taddr, r); }
@@ -117,26 +157,60 @@ __device__ __forceinline__ bool epi_all(bool yes) {
     return r != 0;
 }
 
+// Shared-memory descriptors by halves: the low word is address / 16 (14 bits) with the leading offset above it
+// (unused by 128-byte swizzled tiles; 1), the high word is constant for tiles (stride 1024 bytes between 8-row
+// groups, version 1, 128-byte swizzle) and for 32 x 16-byte scale tiles (stride 128, no swizzle).
+constexpr uint32_t kDescLbo = 1u << 16;
+constexpr uint32_t kDescTile = (1024u >> 4) | (1u << 14) | (2u << 29);
+constexpr uint32_t kDescScale = (128u >> 4) | (1u << 14);
+__device__ __forceinline__ uint64_t desc_of(uint32_t lo, uint32_t hi) { return ((uint64_t)hi << 32) | lo; }
+
+// The epilogue warps wait here for the routing tables; the other four warps only arrive.
+__device__ __forceinline__ void routed_arrive() { asm volatile("bar.arrive 3, 384;" ::: "memory"); }
+__device__ __forceinline__ void routed_wait() { asm volatile("bar.sync 3, 384;" ::: "memory"); }
+__device__ __forceinline__ void route_sync() { asm volatile("bar.sync 2, 128;" ::: "memory"); }
+
+// v = *p where `yes`, past L1; a predicate and not a branch, so that many are in flight.
+__device__ __forceinline__ void ld_if(float& v, const float* p, bool yes) {
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %2, 0;\n\t@q ld.global.cg.f32 %0, [%1];\n\t}"
+                 : "+f"(v)
+                 : "l"(p), "r"((uint32_t)yes));
+}
+
+__device__ __forceinline__ void ld_if(float4& v, const float* p, bool yes) {
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %5, 0;\n\t@q ld.global.cg.v4.f32 {%0, %1, %2, %3}, [%4];\n\t}"
+                 : "+f"(v.x), "+f"(v.y), "+f"(v.z), "+f"(v.w)
+                 : "l"(p), "r"((uint32_t)yes));
+}
+
 __device__ __forceinline__ uint32_t ld_acquire(const uint32_t* p) {
     uint32_t v;
     asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
     return v;
 }
 
+constexpr uint32_t kMtWholeSteps = 12;
+
 // One half's units cut into n equal runs (n <= units, so none is empty).
 struct MtSplit {
     uint32_t units, n;
-    __device__ __forceinline__ uint32_t start(uint32_t c) const { return (uint32_t)((uint64_t)c * units / n); }
-    __device__ __forceinline__ uint32_t owner(uint32_t u) const {  // the run that holds unit u
-        return (uint32_t)((((uint64_t)u + 1) * n - 1) / units);
+    __device__ __forceinline__ static uint32_t div(uint64_t a, uint32_t b) {
+        return a >> 32 ? (uint32_t)(a / b) : (uint32_t)a / b;  // 64-bit division is several times as long
     }
+    __device__ __forceinline__ uint32_t start(uint32_t c) const { return div((uint64_t)c * units, n); }
+    __device__ __forceinline__ uint32_t owner(uint32_t u) const {  // the run that holds unit u
+        return div(((uint64_t)u + 1) * n - 1, units);
+    }
+    // whether run `c`, which holds some of the tile that begins at unit `begin`, also holds an earlier tile
+    __device__ __forceinline__ bool earlier(uint32_t c, uint32_t begin) const { return start(c) < begin; }
 };
-// A run holds at least this many units: below it, exchanging partial sums costs more than the steps saved.
-constexpr uint32_t kMtMinUnits = 4;
-
-__device__ __forceinline__ MtSplit mt_split(uint32_t units) {
-    const uint32_t most = (units + kMtMinUnits - 1) / kMtMinUnits;
-    return MtSplit{units, units == 0 ? 1u : min(gridDim.x, most)};
+// Tiles of few steps are not cut (the exchange of partial sums costs about as much as a dozen steps) where
+// they fit one to a CTA; other runs hold at least four units.
+__device__ __forceinline__ MtSplit mt_split(uint32_t units, uint32_t per_tile) {
+    if (units == 0) return MtSplit{0u, 1u};
+    const uint32_t tiles = units / per_tile;
+    if (tiles <= gridDim.x && per_tile <= kMtWholeSteps) return MtSplit{units, tiles};
+    return MtSplit{units, min(gridDim.x, (units + 3) / 4)};
 }
 
 template <int BITS, int N>
@@ -146,8 +220,8 @@ __global__ void __launch_bounds__(kMtThreads, 1)
                       const __grid_constant__ CUtensorMap map_h, const MtParams p) {
     using C = MtCfg<BITS, N>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t full[kMtStages], empty[kMtStages], tfull[2], tempty[2], drain;
-    __shared__ uint64_t mask_s[kMtMaxExperts];                 // tokens of each active expert
+    __shared__ __align__(8) uint64_t full[C::kStages], empty[C::kStages], tfull[2], tempty[2], drain;
+    __shared__ uint32_t mask_s[kMtMaxExperts][2];              // tokens of each active expert, a bit each
     __shared__ uint16_t list_s[kMtMaxExperts];                 // active experts, ascending
     __shared__ uint32_t active_s[kMtMaxExperts / 32];
     __shared__ uint16_t sel_e[kMtMaxTokens * kMtMaxTopK];      // a token's experts, best first (0xFFFF: none)
@@ -157,113 +231,184 @@ __global__ void __launch_bounds__(kMtThreads, 1)
     __shared__ uint32_t tmem_base_s, last_s;
     __shared__ int abort_s;
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int T = p.T, E = p.E;
     volatile int* abort_flag = &abort_s;
 
-    // ---------------------------------------------------------------- routing (every CTA, the same)
-    uint32_t* keys = reinterpret_cast<uint32_t*>(smem);  // [T][E], before the first stage is filled
-    for (int i = tid; i < T * E; i += kMtThreads) {
-        const uint32_t b = __float_as_uint(p.logits[i]);
-        // unsigned keys that order as the logits do: NaN above everything, -0 equal to +0
-        uint32_t k = (b & 0x80000000u) ? ~b : b | 0x80000000u;
-        if ((b & 0x7FFFFFFFu) > 0x7F800000u) k = 0xFFFFFFFFu;
-        if (b == 0x80000000u) k = 0x80000000u;
-        keys[i] = k;
-    }
-    for (int i = tid; i < T * p.top_k; i += kMtThreads) sel_e[i] = 0xFFFFu;
-    if (tid < kMtMaxExperts / 32) active_s[tid] = 0;
-    if (tid < kMtMaxExperts) mask_s[tid] = 0;
-    if (warp == 2) {
-        if (lane == 0) {
-            for (int s = 0; s < kMtStages; ++s) {
-                mbar_init(&full[s], 2);  // the weight and the token producer
-                mbar_init(&empty[s], 1);
-            }
-            for (int b = 0; b < 2; ++b) {
-                mbar_init(&tfull[b], 1);
-                mbar_init(&tempty[b], kMtEpiThreads / 32);
-            }
-            mbar_init(&drain, 1);
-            abort_s = 0;
-            fence_barrier_init();
-            prefetch_tmap(&map_gate);
-            prefetch_tmap(&map_up);
-            prefetch_tmap(&map_down);
-            prefetch_tmap(&map_x);
-            prefetch_tmap(&map_h);
-        }
-        __syncwarp();
-        tmem_alloc(&tmem_base_s, 512);
-        tmem_relinquish();
-    }
-    __syncthreads();
-    for (int i = tid; i < T * E; i += kMtThreads) {
-        const int t = i / E, e = i - t * E;
-        const uint32_t k = keys[i];
-        const uint32_t* row = keys + t * E;
-        int rank = 0;  // logits before this one: larger, or equal at a lower index
-        for (int o = 0; o < E; ++o) rank += (row[o] > k) || (row[o] == k && o < e);
-        if (rank < p.top_k && k != 0x007FFFFFu) {  // -inf is never selected
-            sel_e[t * p.top_k + rank] = (uint16_t)e;
-            sel_w[t * p.top_k + rank] = p.logits[i];
-            atomicOr(&active_s[e >> 5], 1u << (e & 31));
-        }
-    }
-    __syncthreads();
-    if (tid < T) {
-        const uint16_t* se = sel_e + tid * p.top_k;
-        float* sw = sel_w + tid * p.top_k;
-        if (p.score == MX_SCORE_SIGMOID) {
-            for (int j = 0; j < p.top_k && se[j] != 0xFFFFu; ++j) sw[j] = 1.0f / (1.0f + expf(-sw[j]));
-        } else {
-            const float m = se[0] != 0xFFFFu ? sw[0] : 0.0f;  // the largest logit
-            float sum = 0.0f;
-            if (p.score == MX_SCORE_SOFTMAX) {
-                for (int j = 0; j < p.top_k && se[j] != 0xFFFFu; ++j) sum += expf(sw[j] - m);
+    const int64_t D = p.D, H = p.H;
+    const uint32_t cta = blockIdx.x;
+    const int et = tid - kMtEpiWarp0 * 32;
+
+    if (warp >= kMtEpiWarp0) {
+        // ------------------------------------------------ quantize a share of x, zero the tile counters
+        // (before any weight is asked for: x's loads would wait behind megabytes of them)
+        const int64_t per_row = D / 8, items = T * per_row;  // 8 elements each; 4 neighbours make a block
+        for (int64_t i0 = (int64_t)cta * kMtEpiThreads + et - lane; i0 < items;
+             i0 += (int64_t)gridDim.x * kMtEpiThreads) {
+            const int64_t i = i0 + lane;
+            const bool in = i < items;
+            const int64_t t = in ? i / per_row : 0, c = in ? (i - t * per_row) * 8 : 0;
+            uint4 u = make_uint4(0, 0, 0, 0);
+            if (in) u = *reinterpret_cast<const uint4*>(p.x + i * 16);
+            float v[8] = {bf16lo(u.x), bf16hi(u.x), bf16lo(u.y), bf16hi(u.y),
+                          bf16lo(u.z), bf16hi(u.z), bf16lo(u.w), bf16hi(u.w)};
+            uint32_t m = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+            m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+            m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+            if (!in) continue;
+            const uint32_t s = e8m0_of<BITS == 8 ? 8 : 2>(m);
+            const float f = s == 0xFFu ? __uint_as_float(0x7FC00000u) : __uint_as_float((254u - s) << 23);
+            if constexpr (BITS == 8) {
+                uint2 q;
+                q.x = cvt_e4m3x2(v[0] * f, v[1] * f) | (cvt_e4m3x2(v[2] * f, v[3] * f) << 16);
+                q.y = cvt_e4m3x2(v[4] * f, v[5] * f) | (cvt_e4m3x2(v[6] * f, v[7] * f) << 16);
+                *reinterpret_cast<uint2*>(p.xq + i * 8) = q;
             } else {
-                for (int e = 0; e < E; ++e) sum += expf(p.logits[tid * E + e] - m);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] *= f;  // a NaN scale makes the block NaN whatever its codes
+                *reinterpret_cast<uint32_t*>(p.xq + i * 4) = cvt_e2m1x8(v);
             }
-            for (int j = 0; j < p.top_k && se[j] != 0xFFFFu; ++j) sw[j] = expf(sw[j] - m) / sum;
+            if ((lane & 3) == 0) {
+                const int64_t kb = c / 32;
+                uint8_t* w = p.xs + (kb >> 2) * 512 + (t & 31) * 16 + (t >> 5) * 4;
+                w[kb & 3] = (uint8_t)s;
+                if (c + 32 >= D)  // the rest of the last tile's word is padding
+                    for (int64_t z = (kb & 3) + 1; z < 4; ++z) w[z] = 0;
+            }
         }
-    }
-    if (warp == 3) {  // the active experts in ascending order
-        const uint32_t w = lane < kMtMaxExperts / 32 ? active_s[lane] : 0u;
-        int incl = __popc(w);
-        const int own = incl;
-        for (int d = 1; d < 32; d <<= 1) {
-            const int o = __shfl_up_sync(0xffffffffu, incl, d);
-            if (lane >= d) incl += o;
+        for (int i = cta * kMtEpiThreads + et; i < p.ncounters; i += gridDim.x * kMtEpiThreads) p.counters[i] = 0;
+        fence_proxy_async();
+        epi_sync();
+        if (et == 0) {
+            __threadfence();
+            atomicAdd(p.header + kMtXDone, 1u);
         }
-        int at = incl - own;
-        for (uint32_t m = w; m; m &= m - 1) list_s[at++] = (uint16_t)(lane * 32 + __ffs(m) - 1);
-        if (lane == 31) nactive_s = incl;
+        routed_wait();
+    } else {
+        // ------------------------------------------------ routing (every CTA, the same), barriers
+        uint32_t* keys = reinterpret_cast<uint32_t*>(smem);  // [T][E], before the first stage is filled
+        for (int i0 = tid; i0 < T * E; i0 += 8 * kMtRouteThreads) {
+            uint32_t b[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int i = i0 + j * kMtRouteThreads;
+                b[j] = i < T * E ? __float_as_uint(p.logits[i]) : 0u;
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int i = i0 + j * kMtRouteThreads;
+                // unsigned keys that order as the logits do: NaN above everything, -0 equal to +0
+                uint32_t k = (b[j] & 0x80000000u) ? ~b[j] : b[j] | 0x80000000u;
+                if ((b[j] & 0x7FFFFFFFu) > 0x7F800000u) k = 0xFFFFFFFFu;
+                if (b[j] == 0x80000000u) k = 0x80000000u;
+                if (i < T * E) keys[i] = k;
+            }
+        }
+        for (int i = tid; i < T * p.top_k; i += kMtRouteThreads) sel_e[i] = 0xFFFFu;
+        if (tid < kMtMaxExperts / 32) active_s[tid] = 0;
+        for (int i = tid; i < 2 * kMtMaxExperts; i += kMtRouteThreads) mask_s[i >> 1][i & 1] = 0;
+        if (warp == 2) {
+            if (lane == 0) {
+                for (int s = 0; s < C::kStages; ++s) {
+                    mbar_init(&full[s], 2);  // the weight and the token producer
+                    mbar_init(&empty[s], 1);
+                }
+                for (int b = 0; b < 2; ++b) {
+                    mbar_init(&tfull[b], 1);
+                    mbar_init(&tempty[b], kMtEpiThreads / 32);
+                }
+                mbar_init(&drain, 1);
+                abort_s = 0;
+                fence_barrier_init();
+                prefetch_tmap(&map_gate);
+                prefetch_tmap(&map_up);
+                prefetch_tmap(&map_down);
+                prefetch_tmap(&map_x);
+                prefetch_tmap(&map_h);
+            }
+            __syncwarp();
+            tmem_alloc(&tmem_base_s, 512);
+            tmem_relinquish();
+        }
+        route_sync();
+        for (int i = tid; i < T * E; i += kMtRouteThreads) {
+            const int t = i / E, e = i - t * E;
+            const uint32_t k = keys[i];
+            const uint32_t* row = keys + t * E;
+            int rank = 0;  // logits before this one: larger, or equal at a lower index
+#pragma unroll 8
+            for (int o = 0; o < E; ++o) rank += (row[o] > k) || (row[o] == k && o < e);
+            if (rank < p.top_k && k != 0x007FFFFFu) {  // -inf is never selected
+                sel_e[t * p.top_k + rank] = (uint16_t)e;
+                sel_w[t * p.top_k + rank] = __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k);  // the logit again
+                atomicOr(&active_s[e >> 5], 1u << (e & 31));
+            }
+        }
+        route_sync();
+        if (tid < T) {
+            const uint16_t* se = sel_e + tid * p.top_k;
+            float* sw = sel_w + tid * p.top_k;
+            if (p.score == MX_SCORE_SIGMOID) {
+                for (int j = 0; j < p.top_k && se[j] != 0xFFFFu; ++j) sw[j] = 1.0f / (1.0f + expf(-sw[j]));
+            } else {
+                const float m = se[0] != 0xFFFFu ? sw[0] : 0.0f;  // the largest logit
+                float sum = 0.0f;
+                if (p.score == MX_SCORE_SOFTMAX) {
+                    for (int j = 0; j < p.top_k && se[j] != 0xFFFFu; ++j) sum += expf(sw[j] - m);
+                } else {
+                    for (int e = 0; e < E; ++e) sum += expf(p.logits[tid * E + e] - m);
+                }
+                for (int j = 0; j < p.top_k && se[j] != 0xFFFFu; ++j) sw[j] = expf(sw[j] - m) / sum;
+            }
+        }
+        for (int i = tid; i < T * p.top_k; i += kMtRouteThreads) {
+            const int e = sel_e[i];
+            if (e == 0xFFFF) continue;
+            int a = __popc(active_s[e >> 5] & ((1u << (e & 31)) - 1u));  // the expert's place among the active
+            for (int w = 0; w < (e >> 5); ++w) a += __popc(active_s[w]);
+            const int t = i / p.top_k;
+            list_s[a] = (uint16_t)e;
+            atomicOr(&mask_s[a][t >> 5], 1u << (t & 31));
+        }
+        if (tid == 0) {
+            int n = 0;
+            for (int w = 0; w < kMtMaxExperts / 32; ++w) n += __popc(active_s[w]);
+            nactive_s = n;
+        }
+        fence_proxy_async();  // the keys' shared memory is TMA's from here on
+        tc_fence_before();
+        route_sync();
+        routed_arrive();
     }
-    __syncthreads();
-    const int A = nactive_s;
-    for (int i = tid; i < T * p.top_k; i += kMtThreads) {
-        const int e = sel_e[i];
-        if (e == 0xFFFF) continue;
-        const uint32_t below = active_s[e >> 5] & ((1u << (e & 31)) - 1u);
-        int a = __popc(below);
-        for (int w = 0; w < (e >> 5); ++w) a += __popc(active_s[w]);
-        atomicOr(reinterpret_cast<unsigned long long*>(&mask_s[a]), 1ull << (i / p.top_k));
-    }
-    fence_proxy_async();  // the keys' shared memory is TMA's from here on
-    tc_fence_before();
-    __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_base_s;
+    const int A = __shfl_sync(0xffffffffu, nactive_s, 0);
+    auto mask_of = [&](uint32_t a) -> uint64_t { return mask_s[a][0] | ((uint64_t)mask_s[a][1] << 32); };
 
-    const int64_t D = p.D, H = p.H;
     const uint32_t ct_d = (uint32_t)((D + 127) / 128), ct_h = (uint32_t)((H + 127) / 128);
     const uint32_t K1 = (uint32_t)((D + C::kKE - 1) / C::kKE), K2 = (uint32_t)((H + C::kKE - 1) / C::kKE);
     const uint32_t TH = ct_h, TD = (uint32_t)((D + 255) / 256);
-    const MtSplit sp1 = mt_split((uint32_t)A * TH * K1), sp2 = mt_split(TD * (uint32_t)A * K2);
-    const uint32_t cta = blockIdx.x;
+    const uint32_t AK2 = (uint32_t)A * K2;
+    const MtSplit sp1 = mt_split((uint32_t)A * TH * K1, K1), sp2 = mt_split(TD * AK2, AK2);
     const uint32_t u1_0 = cta < sp1.n ? sp1.start(cta) : 0, u1_1 = cta < sp1.n ? sp1.start(cta + 1) : 0;
     const uint32_t u2_0 = cta < sp2.n ? sp2.start(cta) : 0, u2_1 = cta < sp2.n ? sp2.start(cta + 1) : 0;
-    const uint32_t AK2 = (uint32_t)A * K2;
+
+    // every CTA's arrivals at a grid-wide point, from one thread
+    auto grid_wait = [&](int point) -> bool {
+        const uint64_t t0 = globaltimer_ns();
+        while (ld_acquire(p.header + point) < gridDim.x) {
+            if (*abort_flag) return false;
+            if (globaltimer_ns() - t0 > p.timeout_ns) {
+                *abort_flag = 1;
+                report(p.dev_status, MXFP8_ERR_TIMEOUT);
+                return false;
+            }
+        }
+        fence_proxy_async();  // what the other CTAs wrote, before TMA reads it
+        return true;
+    };
 
     if (A == 0) {
         for (int64_t i = (int64_t)cta * kMtThreads + tid; i < T * D; i += (int64_t)gridDim.x * kMtThreads)
@@ -271,44 +416,102 @@ __global__ void __launch_bounds__(kMtThreads, 1)
     } else if (warp == 0) {
         if (lane == 0) {
             // -------------------------------------------- weight producer
-            int stage = 0;
-            uint32_t phase = 0;
-            auto load = [&](bool first, const CUtensorMap* m0, const CUtensorMap* m1, int32_t row0, int32_t row1,
-                            const uint8_t* s0, const uint8_t* s1, uint32_t k, uint32_t ct) -> bool {
-                if (!mbar_wait_bounded<true>(&empty[stage], phase ^ 1u, p.timeout_ns, abort_flag, p.dev_status))
-                    return false;
-                uint8_t* st = smem + stage * C::kStage;
-                const uint32_t sfb = min((uint32_t)C::kSfTiles, ct - k * C::kSfTiles) * 512;
-                const bool two = first || row1 >= 0;
-                mbar_arrive_expect_tx(&full[stage], (two ? 2u : 1u) * (16384u + sfb));
-                tma_load_2d(st, m0, (int32_t)(k * 128), row0, &full[stage]);
-                bulk_load(st + C::kOffSfA, s0 + (int64_t)k * C::kSfTiles * 512, sfb, &full[stage]);
-                if (two) {
-                    tma_load_2d(st + 16384, m1, (int32_t)(k * 128), row1, &full[stage]);
-                    bulk_load(st + C::kOffSfA + C::kSfTiles * 512, s1 + (int64_t)k * C::kSfTiles * 512, sfb,
-                              &full[stage]);
-                }
-                if (++stage == kMtStages) { stage = 0; phase ^= 1u; }
-                return true;
+            // A place in this CTA's two runs, one after the other.  Stepping costs a few additions: the
+            // divisions (hundreds of cycles each on one thread) are paid once a run.
+            struct Place {
+                const CUtensorMap *m0, *m1;
+                const uint8_t *s0, *s1;
+                int32_t row0, row1;       // row1 < 0: no second tile
+                uint32_t k, K, left;      // step, steps of this tile and expert, units left in this half
+                uint32_t a, j;            // active expert, tile
+                uint32_t ct;
+                bool first;
             };
-            bool ok = true;
-            for (uint32_t u = u1_0; u < u1_1 && ok;) {
-                const uint32_t tile = u / K1, a = tile / TH, j = tile - a * TH, e = list_s[a];
-                const uint32_t end = min(u1_1, (tile + 1) * K1);
-                const int64_t so = (int64_t)e * ct_h * ct_d * 512 + (int64_t)j * ct_d * 512;
-                const int32_t row = (int32_t)((int64_t)e * H + j * 128);
-                for (; u < end && ok; ++u)
-                    ok = load(true, &map_gate, &map_up, row, row, p.s_gate + so, p.s_up + so, u - tile * K1, ct_d);
-            }
-            for (uint32_t u = u2_0; u < u2_1 && ok;) {
-                const uint32_t tile = u / AK2, r = u - tile * AK2, a = r / K2, e = list_s[a];
-                const uint32_t base = tile * AK2 + a * K2, end = min(u2_1, base + K2);
-                const int64_t so = ((int64_t)e * ct_d + 2 * tile) * ct_h * 512;
-                const int32_t row = (int32_t)((int64_t)e * D + tile * 256);
-                const bool two = 2 * tile + 1 < ct_d;
-                for (; u < end && ok; ++u)
-                    ok = load(false, &map_down, &map_down, row, two ? row + 128 : -1, p.s_down + so,
-                              p.s_down + so + (int64_t)ct_h * 512, u - base, ct_h);
+            auto settle = [&](Place& q) {  // rows, scales of (a, j) from step k on
+                const uint32_t e = list_s[q.a];
+                if (q.first) {
+                    const int64_t so = (((int64_t)e * ct_h + q.j) * ct_d + q.k * C::kSfTiles) * 512;
+                    q.row0 = q.row1 = (int32_t)((int64_t)e * H + q.j * 128);
+                    q.s0 = p.s_gate + so;
+                    q.s1 = p.s_up + so;
+                } else {
+                    q.row0 = (int32_t)((int64_t)e * D + q.j * 256);
+                    q.row1 = 2 * q.j + 1 < ct_d ? q.row0 + 128 : -1;
+                    q.s0 = p.s_down + (((int64_t)e * ct_d + 2 * q.j) * ct_h + q.k * C::kSfTiles) * 512;
+                    q.s1 = q.s0 + (int64_t)ct_h * 512;
+                }
+            };
+            auto second = [&](Place& q) {
+                const uint32_t r = u2_0 % AK2;
+                q.first = false;
+                q.m0 = q.m1 = &map_down;
+                q.j = u2_0 / AK2;
+                q.a = r / K2;
+                q.k = r - q.a * K2;
+                q.K = K2;
+                q.ct = ct_h;
+                q.left = u2_1 - u2_0;
+            };
+            auto begin = [&]() -> Place {
+                Place q;
+                if (u1_0 < u1_1) {
+                    const uint32_t tile = u1_0 / K1;
+                    q.first = true;
+                    q.m0 = &map_gate;
+                    q.m1 = &map_up;
+                    q.a = tile / TH;
+                    q.j = tile - q.a * TH;
+                    q.k = u1_0 - tile * K1;
+                    q.K = K1;
+                    q.ct = ct_d;
+                    q.left = u1_1 - u1_0;
+                } else {
+                    second(q);
+                }
+                settle(q);
+                return q;
+            };
+            auto step = [&](Place& q) {
+                --q.left;
+                if (++q.k < q.K && q.left != 0) {
+                    q.s0 += C::kSfTiles * 512;
+                    q.s1 += C::kSfTiles * 512;
+                    return;
+                }
+                if (q.left == 0) {
+                    if (!q.first || u2_0 == u2_1) return;  // the end
+                    second(q);
+                } else {
+                    q.k = 0;
+                    if (q.first) {
+                        if (++q.j == TH) { q.j = 0; ++q.a; }
+                    } else {
+                        if (++q.a == (uint32_t)A) { q.a = 0; ++q.j; }
+                    }
+                }
+                settle(q);
+            };
+            auto sf_bytes = [&](const Place& q) { return min((uint32_t)C::kSfTiles, q.ct - q.k * C::kSfTiles) * 512u; };
+            const uint32_t total = (u1_1 - u1_0) + (u2_1 - u2_0);
+            if (total != 0) {
+                int stage = 0;
+                uint32_t phase = 0;
+                Place q = begin();
+                for (uint32_t i = 0; i < total; ++i) {
+                    if (!mbar_wait_bounded<true>(&empty[stage], phase ^ 1u, p.timeout_ns, abort_flag, p.dev_status)) break;
+                    uint8_t* st = smem + stage * C::kStage;
+                    const uint32_t n = sf_bytes(q);
+                    const int32_t x = (int32_t)(q.k * 128);
+                    mbar_arrive_expect_tx(&full[stage], (q.row1 >= 0 ? 2u : 1u) * (16384u + n));
+                    tma_load_2d(st, q.m0, x, q.row0, &full[stage]);
+                    bulk_load(st + C::kOffSfA, q.s0, n, &full[stage]);
+                    if (q.row1 >= 0) {
+                        tma_load_2d(st + 16384, q.m1, x, q.row1, &full[stage]);
+                        bulk_load(st + C::kOffSfA + C::kSfTiles * 512, q.s1, n, &full[stage]);
+                    }
+                    step(q);
+                    if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
+                }
             }
         }
     } else if (warp == 1) {
@@ -316,19 +519,7 @@ __global__ void __launch_bounds__(kMtThreads, 1)
             // -------------------------------------------- token producer
             int stage = 0;
             uint32_t phase = 0;
-            auto grid_wait = [&](uint32_t target) -> bool {
-                const uint64_t t0 = globaltimer_ns();
-                while (ld_acquire(p.header) < target) {
-                    if (*abort_flag) return false;
-                    if (globaltimer_ns() - t0 > p.timeout_ns) {
-                        *abort_flag = 1;
-                        report(p.dev_status, MXFP8_ERR_TIMEOUT);
-                        return false;
-                    }
-                }
-                fence_proxy_async();  // what the other CTAs wrote, before TMA reads it
-                return true;
-            };
+            // step k of the contraction: tile (k, plane z) of the map, scale tiles at s
             auto load = [&](const CUtensorMap* m, int32_t z, const uint8_t* s, uint32_t k, uint32_t ct) -> bool {
                 if (!mbar_wait_bounded<true>(&empty[stage], phase ^ 1u, p.timeout_ns, abort_flag, p.dev_status))
                     return false;
@@ -336,66 +527,100 @@ __global__ void __launch_bounds__(kMtThreads, 1)
                 const uint32_t sfb = min((uint32_t)C::kSfTiles, ct - k * C::kSfTiles) * 512;
                 mbar_arrive_expect_tx(&full[stage], N * 128u + sfb);
                 tma_load_3d(st + C::kOffB, m, (int32_t)(k * 128), 0, z, &full[stage]);
-                bulk_load(st + C::kOffSfB, s + (int64_t)k * C::kSfTiles * 512, sfb, &full[stage]);
-                if (++stage == kMtStages) { stage = 0; phase ^= 1u; }
+                bulk_load(st + C::kOffSfB, s, sfb, &full[stage]);
+                if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
                 return true;
             };
-            bool ok = grid_wait(gridDim.x);
-            for (uint32_t u = u1_0; u < u1_1 && ok; ++u) ok = load(&map_x, 0, p.xs, u % K1, ct_d);
-            if (ok && u2_0 < u2_1) ok = grid_wait(2 * gridDim.x);
+            bool ok = grid_wait(kMtXDone);
+            uint32_t k = u1_0 % K1;
+            const uint8_t* s = p.xs + k * C::kSfTiles * 512;
+            for (uint32_t u = u1_0; u < u1_1 && ok; ++u) {
+                ok = load(&map_x, 0, s, k, ct_d);
+                s += C::kSfTiles * 512;
+                if (++k == K1) {
+                    k = 0;
+                    s = p.xs;
+                }
+            }
+            if (ok && u2_0 < u2_1) ok = grid_wait(kMtHDone);
+            uint32_t a = u2_0 % AK2 / K2;
+            k = u2_0 % K2;  // AK2 is a multiple of K2
+            s = p.hs + ((int64_t)a * ct_h + k * C::kSfTiles) * 512;
             for (uint32_t u = u2_0; u < u2_1 && ok; ++u) {
-                const uint32_t r = u % AK2, a = r / K2;
-                ok = load(&map_h, (int32_t)a, p.hs + (int64_t)a * ct_h * 512, r - a * K2, ct_h);
+                ok = load(&map_h, (int32_t)a, s, k, ct_h);
+                s += C::kSfTiles * 512;
+                if (++k == K2) {
+                    k = 0;
+                    if (++a == (uint32_t)A) a = 0;
+                    s = p.hs + (int64_t)a * ct_h * 512;
+                }
             }
         }
     } else if (warp == 2) {
-        if (lane == 0) {
+        {
             // -------------------------------------------- tensor-core issuer
+            // The whole warp walks the loop and one elected lane issues, so that descriptors and addresses stay in
+            // uniform registers, where these instructions take them from.
+            const uint32_t one = elect_one();
+            const uint32_t ring = __shfl_sync(0xffffffffu, smem_u32(smem), 0);
+            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+            auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+                return __all_sync(0xffffffffu,
+                                  mbar_wait_bounded<true>(bar, parity, p.timeout_ns, abort_flag, p.dev_status));
+            };
             int stage = 0, buf = 0;
             uint32_t phase = 0, buf_phase = 0;
             // steps k0 .. k1-1 of a contraction of K elements into the next accumulator pair
             auto contract = [&](uint32_t k0, uint32_t k1, int64_t K) -> bool {
-                if (!mbar_wait_bounded<true>(&tempty[buf], buf_phase ^ 1u, p.timeout_ns, abort_flag, p.dev_status))
+                if (!wait(&tempty[buf], buf_phase ^ 1u))
                     return false;
                 tc_fence_after();
-                const uint32_t d0 = tmem + buf * 2 * N;
+                const uint32_t d0 = tm + buf * 2 * N;
                 for (uint32_t k = k0; k < k1; ++k) {
-                    if (!mbar_wait_bounded<true>(&full[stage], phase, p.timeout_ns, abort_flag, p.dev_status))
+                    if (!wait(&full[stage], phase))
                         return false;
                     tc_fence_after();
-                    const uint32_t st = smem_u32(smem + stage * C::kStage);
-                    const uint32_t sf = tmem + C::kSfCol0 + stage * C::kSfCols;
+                    // descriptors of a stage differ from its first only in their address field
+                    const uint32_t at = (ring + stage * C::kStage) >> 4;
+                    const uint32_t sf = tm + C::kSfCol0 + stage * C::kSfCols;
 #pragma unroll
-                    for (int i = 0; i < 2 * C::kSfTiles; ++i)
-                        tc_cp_32x128b_warpx4(sf + 4 * i, smem_desc(st + C::kOffSfA + 512 * i, 0, 128, 0));
-#pragma unroll
-                    for (int i = 0; i < C::kSfTiles; ++i)
-                        tc_cp_32x128b_warpx4(sf + 4 * (2 * C::kSfTiles + i),
-                                             smem_desc(st + C::kOffSfB + 512 * i, 0, 128, 0));
-                    const int steps = (int)min64(4, (K - (int64_t)k * C::kKE + C::kKE / 4 - 1) / (C::kKE / 4));
-#pragma unroll
-                    for (int s = 0; s < 4; ++s) {
-                        if (s >= steps) break;
-                        const uint64_t bd = smem_desc(st + C::kOffB + 32 * s, 16, 1024, 2);
+                    for (int i = 0; i < 3 * C::kSfTiles; ++i) {
+                        const int off = i < 2 * C::kSfTiles ? C::kOffSfA + 512 * i
+                                                            : C::kOffSfB + 512 * (i - 2 * C::kSfTiles);
+                        cp_scales(one, sf + 4 * i, desc_of(at + off / 16, kDescScale));
+                    }
+                    auto mma = [&](int s, uint32_t acc) {
+                        const uint64_t bd = desc_of((at + (C::kOffB + 32 * s) / 16) | kDescLbo, kDescTile);
 #pragma unroll
                         for (int w = 0; w < 2; ++w) {
-                            const uint64_t ad = smem_desc(st + w * 16384 + 32 * s, 16, 1024, 2);
-                            const uint32_t acc = (k != k0 || s != 0) ? 1u : 0u;
+                            const uint64_t ad = desc_of((at + (w * 16384 + 32 * s) / 16) | kDescLbo, kDescTile);
                             if constexpr (BITS == 8) {
-                                tc_mma_mxf8(d0 + w * N, ad, bd, idesc_mxf8(128, N, s, s), sf + 4 * w, sf + 8, acc);
+                                mma_mxf8(one, d0 + w * N, ad, bd, idesc_mxf8(128, N, s, s), sf + 4 * w, sf + 8, acc);
                             } else {
                                 constexpr uint32_t id0 = (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) |
                                                          (1u << 23) | (1u << 27);  // E2M1 x E2M1, E8M0, M = 128
                                 const uint32_t id = (uint32_t)(s & 1) * 2;
-                                tc_mma_mxf4(d0 + w * N, ad, bd, id0 | (id << 4) | (id << 29),
+                                mma_mxf4(one, d0 + w * N, ad, bd, id0 | (id << 4) | (id << 29),
                                             sf + 8 * w + 4 * (s >> 1), sf + 16 + 4 * (s >> 1), acc);
                             }
                         }
+                    };
+                    if ((int64_t)(k + 1) * C::kKE <= K) {
+                        mma(0, k != k0);
+                        mma(1, 1u);
+                        mma(2, 1u);
+                        mma(3, 1u);
+                    } else {  // the contraction's last elements
+                        const int steps = (int)((K - (int64_t)k * C::kKE + C::kKE / 4 - 1) / (C::kKE / 4));
+                        mma(0, k != k0);
+                        if (steps > 1) mma(1, 1u);
+                        if (steps > 2) mma(2, 1u);
+                        if (steps > 3) mma(3, 1u);
                     }
-                    tc_commit(&empty[stage]);
-                    if (++stage == kMtStages) { stage = 0; phase ^= 1u; }
+                    commit(one, &empty[stage]);
+                    if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
                 }
-                tc_commit(&tfull[buf]);
+                commit(one, &tfull[buf]);
                 if (++buf == 2) { buf = 0; buf_phase ^= 1u; }
                 return true;
             };
@@ -410,57 +635,11 @@ __global__ void __launch_bounds__(kMtThreads, 1)
                 ok = contract(u - base, end - base, H);
                 u = end;
             }
-            tc_commit(&drain);
+            commit(one, &drain);
             volatile int no_abort = 0;
             mbar_wait_bounded<true>(&drain, 0, p.timeout_ns, &no_abort, p.dev_status);
         }
     } else if (warp >= kMtEpiWarp0) {
-        const int et = tid - kMtEpiWarp0 * 32;
-        // ------------------------------------------------ zero the tile counters, quantize a share of x
-        for (int i = cta * kMtEpiThreads + et; i < p.ncounters; i += gridDim.x * kMtEpiThreads) p.counters[i] = 0;
-        {
-            const int64_t per_row = D / 8, items = T * per_row;  // 8 elements each; 4 neighbours make a block
-            for (int64_t i0 = (int64_t)cta * kMtEpiThreads + et - lane; i0 < items;
-                 i0 += (int64_t)gridDim.x * kMtEpiThreads) {
-                const int64_t i = i0 + lane;
-                const bool in = i < items;
-                const int64_t t = in ? i / per_row : 0, c = in ? (i - t * per_row) * 8 : 0;
-                uint4 u = make_uint4(0, 0, 0, 0);
-                if (in) u = *reinterpret_cast<const uint4*>(p.x + i * 16);
-                float v[8] = {bf16lo(u.x), bf16hi(u.x), bf16lo(u.y), bf16hi(u.y),
-                              bf16lo(u.z), bf16hi(u.z), bf16lo(u.w), bf16hi(u.w)};
-                uint32_t m = 0;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
-                m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-                m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-                if (!in) continue;
-                const uint32_t s = e8m0_of<BITS == 8 ? 8 : 2>(m);
-                const float f = s == 0xFFu ? __uint_as_float(0x7FC00000u) : __uint_as_float((254u - s) << 23);
-                if constexpr (BITS == 8) {
-                    uint2 q;
-                    q.x = cvt_e4m3x2(v[0] * f, v[1] * f) | (cvt_e4m3x2(v[2] * f, v[3] * f) << 16);
-                    q.y = cvt_e4m3x2(v[4] * f, v[5] * f) | (cvt_e4m3x2(v[6] * f, v[7] * f) << 16);
-                    *reinterpret_cast<uint2*>(p.xq + i * 8) = q;
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) v[j] *= f;  // a NaN scale makes the block NaN whatever its codes
-                    *reinterpret_cast<uint32_t*>(p.xq + i * 4) = cvt_e2m1x8(v);
-                }
-                if ((lane & 3) == 0) {
-                    const int64_t kb = c / 32;
-                    uint8_t* w = p.xs + (kb >> 2) * 512 + (t & 31) * 16 + (t >> 5) * 4;
-                    w[kb & 3] = (uint8_t)s;
-                    if (c + 32 >= D)  // the rest of the last tile's word is padding
-                        for (int64_t z = (kb & 3) + 1; z < 4; ++z) w[z] = 0;
-                }
-            }
-        }
-        fence_proxy_async();
-        __threadfence();
-        epi_sync();
-        if (et == 0) atomicAdd(p.header, 1u);
-
         const int quarter = warp & 3, cg = (warp - kMtEpiWarp0) >> 2;
         const int r = quarter * 32 + lane;  // row of a weight tile = tensor-memory lane
         const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16);
@@ -468,14 +647,15 @@ __global__ void __launch_bounds__(kMtThreads, 1)
         uint32_t buf_phase = 0;
         bool ok = true;
         const uint32_t slot_words = 2u * (uint32_t)T * 128u;  // one partial tile pair
-        auto my_slot = [&](uint32_t c, uint32_t first_tile, uint32_t tile) -> float* {
-            return p.part + (int64_t)(2 * c + (tile != first_tile)) * slot_words;
+        // A run leaves partial sums of at most two tiles: the one it begins in and the one it ends in.
+        auto slot = [&](uint32_t c, bool second) -> float* {
+            return p.part + (int64_t)(2 * c + (second ? 1 : 0)) * slot_words;
         };
         // every epilogue thread has written its partial sums: true for the CTA that completes the tile
         auto arrive_last = [&](uint32_t* counter, uint32_t of) -> bool {
-            __threadfence();
             epi_sync();
             if (et == 0) {
+                __threadfence();  // the CTA's writes, ordered before this by the barrier
                 last_s = atomicAdd(counter, 1u) + 1u == of;
                 __threadfence();
             }
@@ -484,7 +664,10 @@ __global__ void __launch_bounds__(kMtThreads, 1)
         };
 
         // ------------------------------------------------ first half: gate, up, SwiGLU, quantize h
-        constexpr int NC = N / 2;  // token columns of this warp
+        // Token columns are taken kCols at a time from those the expert's mask names, the odd batches by warps
+        // 8-11: tensor memory and the partial sums are both addressed by column, so nothing is done for the others
+        // and the code stays a short loop (unrolled over all columns it did not fit the instruction cache).
+        constexpr int kCols = 4;
         for (uint32_t u = u1_0; u < u1_1 && ok;) {
             const uint32_t tile = u / K1, a = tile / TH, j = tile - a * TH;
             const uint32_t end = min(u1_1, (tile + 1) * K1);
@@ -493,79 +676,142 @@ __global__ void __launch_bounds__(kMtThreads, 1)
             ok = epi_all(mbar_wait_bounded<true>(&tfull[buf], buf_phase, p.timeout_ns, abort_flag, p.dev_status));
             if (!ok) break;
             tc_fence_after();
-            const uint64_t mask = mask_s[a];
-            const int c0 = cg * NC;
-            const bool any = ((mask >> c0) & ((1ull << NC) - 1ull)) != 0;
-            uint32_t g[NC], h[NC];
-            if (any) {
-                tmem_ld_cols(lane_base + buf * 2 * N + c0, g);
-                tmem_ld_cols(lane_base + buf * 2 * N + N + c0, h);
+            const uint64_t mask = mask_of(a);
+            const uint32_t acc = lane_base + buf * 2 * N;
+            // the next batch of columns: their indexes (the last repeated), and how many
+            auto batch = [&](uint64_t& left, int (&col)[kCols]) -> int {
+                int n = 0;
+#pragma unroll
+                for (int i = 0; i < kCols; ++i) {
+                    if (left) {
+                        col[i] = __ffsll(left) - 1;
+                        left &= left - 1;
+                        n = i + 1;
+                    } else {
+                        col[i] = i ? col[i - 1] : 0;
+                    }
+                }
+                return n;
+            };
+            auto from_tmem = [&](const int (&col)[kCols], float (&g)[kCols], float (&h)[kCols]) {
+                uint32_t x[kCols], y[kCols];
+#pragma unroll
+                for (int i = 0; i < kCols; ++i) {
+                    x[i] = tmem_ld_col(acc + col[i]);
+                    y[i] = tmem_ld_col(acc + N + col[i]);
+                }
                 tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < kCols; ++i) {
+                    asm volatile("" : "+r"(x[i]), "+r"(y[i]));  // not before the wait
+                    g[i] = __uint_as_float(x[i]);
+                    h[i] = __uint_as_float(y[i]);
+                }
+            };
+            // SwiGLU and quantization of n columns; the warp's 32 rows are one block of a token's h
+            const int64_t row = (int64_t)j * 128 + r;
+            const bool in = row < H;
+            auto finish = [&](const int (&col)[kCols], int n, const float (&g)[kCols], const float (&h)[kCols]) {
+                float v[kCols];
+                uint32_t m[kCols];
+#pragma unroll
+                for (int i = 0; i < kCols; ++i) {
+                    v[i] = in ? g[i] / (1.0f + expf(-g[i])) * h[i] : 0.0f;
+                    m[i] = __reduce_max_sync(0xffffffffu, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+                }
+#pragma unroll
+                for (int i = 0; i < kCols; ++i) {
+                    const uint32_t s = e8m0_of<BITS == 8 ? 8 : 2>(m[i]);
+                    const float f = s == 0xFFu ? __uint_as_float(0x7FC00000u) : __uint_as_float((254u - s) << 23);
+                    const int64_t at = (int64_t)a * T + col[i];
+                    if constexpr (BITS == 8) {
+                        if (in && i < n) p.hq[at * H + row] = (uint8_t)cvt_e4m3x2(v[i] * f, 0.0f);
+                    } else {
+                        const float q8[8] = {v[i] * f, __shfl_down_sync(0xffffffffu, v[i] * f, 1), 0, 0, 0, 0, 0, 0};
+                        if (in && i < n && (lane & 1) == 0) p.hq[at * (H / 2) + row / 2] = (uint8_t)cvt_e2m1x8(q8);
+                    }
+                    if (lane == 0 && i < n)
+                        p.hs[((int64_t)a * ct_h + j) * 512 + (col[i] & 31) * 16 + (col[i] >> 5) * 4 + quarter] =
+                            (uint8_t)(in ? s : 0u);
+                }
+            };
+            float* own = slot(cta, u1_0 < tile * K1);
+            uint64_t left = mask;
+            for (int turn = 0; left; ++turn) {
+                int col[kCols];
+                const int n = batch(left, col);
+                if ((turn & 1) != cg) continue;
+                float g[kCols], h[kCols];
+                from_tmem(col, g, h);
+                if (whole) {
+                    finish(col, n, g, h);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < kCols; ++i)
+                        if (i < n) {
+                            __stcg(own + col[i] * 128 + r, g[i]);
+                            __stcg(own + (T + col[i]) * 128 + r, h[i]);
+                        }
+                }
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&tempty[buf]);
             if (++buf == 2) { buf = 0; buf_phase ^= 1u; }
-            if (!whole) {
-                float* w = my_slot(cta, u1_0 / K1, tile);
+            if (whole) continue;
+            const uint32_t lo = sp1.owner(tile * K1), hi = sp1.owner((tile + 1) * K1 - 1);
+            const bool lo_second = sp1.earlier(lo, tile * K1);  // the others begin in this tile
+            if (!arrive_last(p.counters + tile, hi - lo + 1)) continue;
+            left = mask;
+            for (int turn = 0; left; ++turn) {
+                int col[kCols];
+                const int n = batch(left, col);
+                if ((turn & 1) != cg) continue;
+                float g[kCols], h[kCols];
 #pragma unroll
-                for (int c = 0; c < NC; ++c)
-                    if ((mask >> (c0 + c)) & 1u) {
-                        __stcg(w + (c0 + c) * 128 + r, __uint_as_float(g[c]));
-                        __stcg(w + (T + c0 + c) * 128 + r, __uint_as_float(h[c]));
+                for (int i = 0; i < kCols; ++i) g[i] = h[i] = 0.0f;
+                constexpr int kRuns = 4;  // runs whose sums are in flight together
+                for (uint32_t o = lo; o <= hi; o += kRuns) {
+                    float v[kRuns][kCols], w[kRuns][kCols];
+#pragma unroll
+                    for (int x = 0; x < kRuns; ++x) {
+                        const bool have = o + x <= hi;
+                        const float* q = slot(o + x, o + x == lo && lo_second);
+#pragma unroll
+                        for (int i = 0; i < kCols; ++i) {
+                            v[x][i] = w[x][i] = 0.0f;
+                            ld_if(v[x][i], q + col[i] * 128 + r, have && i < n);
+                            ld_if(w[x][i], q + (T + col[i]) * 128 + r, have && i < n);
+                        }
                     }
-                const uint32_t lo = sp1.owner(tile * K1), hi = sp1.owner((tile + 1) * K1 - 1);
-                if (!arrive_last(p.counters + tile, hi - lo + 1)) continue;
 #pragma unroll
-                for (int c = 0; c < NC; ++c) g[c] = h[c] = 0u;
-                for (uint32_t o = lo; o <= hi; ++o) {
-                    const float* q = my_slot(o, sp1.start(o) / K1, tile);
+                    for (int x = 0; x < kRuns; ++x)
 #pragma unroll
-                    for (int c = 0; c < NC; ++c)
-                        if ((mask >> (c0 + c)) & 1u) {
-                            g[c] = __float_as_uint(__uint_as_float(g[c]) + __ldcg(q + (c0 + c) * 128 + r));
-                            h[c] = __float_as_uint(__uint_as_float(h[c]) + __ldcg(q + (T + c0 + c) * 128 + r));
+                        for (int i = 0; i < kCols; ++i) {
+                            g[i] += v[x][i];
+                            h[i] += w[x][i];
                         }
                 }
-            }
-            const int64_t row = (int64_t)j * 128 + r;
-            const bool in = row < H;
-#pragma unroll
-            for (int c = 0; c < NC; ++c) {
-                const int t = c0 + c;
-                if (!((mask >> t) & 1u)) continue;
-                const float x1 = __uint_as_float(g[c]);
-                const float v = in ? x1 / (1.0f + expf(-x1)) * __uint_as_float(h[c]) : 0.0f;
-                // the warp's 32 rows are one block of token t
-                const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(v) & 0x7FFFFFFFu);
-                const uint32_t s = e8m0_of<BITS == 8 ? 8 : 2>(m);
-                const float f = s == 0xFFu ? __uint_as_float(0x7FC00000u) : __uint_as_float((254u - s) << 23);
-                const int64_t at = (int64_t)a * T + t;
-                if constexpr (BITS == 8) {
-                    if (in) p.hq[at * H + row] = (uint8_t)cvt_e4m3x2(v * f, 0.0f);
-                } else {
-                    const float q8[8] = {v * f, __shfl_down_sync(0xffffffffu, v * f, 1), 0, 0, 0, 0, 0, 0};
-                    if (in && (lane & 1) == 0) p.hq[at * (H / 2) + row / 2] = (uint8_t)cvt_e2m1x8(q8);
-                }
-                if (lane == 0)
-                    p.hs[((int64_t)a * ct_h + j) * 512 + (t & 31) * 16 + (t >> 5) * 4 + quarter] =
-                        (uint8_t)(in ? s : 0u);
+                finish(col, n, g, h);
             }
         }
         fence_proxy_async();
-        __threadfence();
         epi_sync();
-        if (et == 0) atomicAdd(p.header, 1u);
+        if (et == 0) {
+            __threadfence();
+            atomicAdd(p.header + kMtHDone, 1u);
+        }
 
         // ------------------------------------------------ second half: down, weighted sum over experts
+        constexpr int kLd = N < 32 ? N : 32;
         float total[N];  // warps 4-7: rows 0-127 of the tile, warps 8-11: rows 128-255
         for (uint32_t u = u2_0; u < u2_1 && ok;) {
             const uint32_t tile = u / AK2, t_end = min(u2_1, (tile + 1) * AK2);
             const bool whole = u == tile * AK2 && t_end == (tile + 1) * AK2;
 #pragma unroll
             for (int c = 0; c < N; ++c) total[c] = 0.0f;
-            while (u < t_end) {
-                const uint32_t a = (u - tile * AK2) / K2;
+            uint32_t a = (u - tile * AK2) / K2;
+            for (; u < t_end; ++a) {
                 u = min(t_end, tile * AK2 + (a + 1) * K2);
                 if (et < T) {  // token et's weight for this expert
                     const int e = list_s[a];
@@ -577,15 +823,15 @@ __global__ void __launch_bounds__(kMtThreads, 1)
                 ok = epi_all(mbar_wait_bounded<true>(&tfull[buf], buf_phase, p.timeout_ns, abort_flag, p.dev_status));
                 if (!ok) break;
                 tc_fence_after();
-                const uint64_t mask = mask_s[a];
+                const uint64_t mask = mask_of(a);
 #pragma unroll
-                for (int c = 0; c < N; c += 32) {
-                    if (((mask >> c) & 0xFFFFFFFFull) == 0) continue;
-                    uint32_t v[32];
-                    tmem_ld_32x32b_x32(lane_base + buf * 2 * N + cg * N + c, v);
+                for (int c = 0; c < N; c += kLd) {
+                    if (((mask >> c) & ((1ull << kLd) - 1ull)) == 0) continue;
+                    uint32_t v[kLd];
+                    tmem_ld_cols(lane_base + buf * 2 * N + cg * N + c, v);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
+                    for (int i = 0; i < kLd; ++i)
                         if ((mask >> (c + i)) & 1u) total[c + i] += w_s[buf][c + i] * __uint_as_float(v[i]);
                 }
                 tc_fence_before();
@@ -595,26 +841,69 @@ __global__ void __launch_bounds__(kMtThreads, 1)
             }
             if (!ok) break;
             if (!whole) {
-                float* w = my_slot(cta, u2_0 / AK2, tile) + cg * T * 128;
+                float* w = slot(cta, u2_0 < tile * AK2) + cg * T * 128;
 #pragma unroll
                 for (int c = 0; c < N; ++c)
                     if (c < T) __stcg(w + c * 128 + r, total[c]);
-                const uint32_t lo = sp2.owner(tile * AK2), hi = sp2.owner((tile + 1) * AK2 - 1);
-                if (!arrive_last(p.counters + A * TH + tile, hi - lo + 1)) continue;
-#pragma unroll
-                for (int c = 0; c < N; ++c) total[c] = 0.0f;
-                for (uint32_t o = lo; o <= hi; ++o) {
-                    const float* q = my_slot(o, sp2.start(o) / AK2, tile) + cg * T * 128;
-#pragma unroll
-                    for (int c = 0; c < N; ++c)
-                        if (c < T) total[c] += __ldcg(q + c * 128 + r);
-                }
+                continue;
             }
             const int64_t d = (int64_t)tile * 256 + cg * 128 + r;
             if (d < D)
 #pragma unroll
                 for (int c = 0; c < N; ++c)
                     if (c < T) p.y[c * D + d] = __float2bfloat16(total[c]);
+        }
+        // ------------------------------------------------ add up the tiles that several runs share
+        // All CTAs take part, four columns of one token a thread; a tile's sums are added in its runs' order.
+        if (sp2.units % sp2.n != 0 || sp2.units / sp2.n % AK2 != 0) {
+            epi_sync();
+            if (et == 0) {
+                __threadfence();
+                atomicAdd(p.header + kMtSumsDone, 1u);
+                ok = ok && grid_wait(kMtSumsDone);
+            }
+            ok = epi_all(ok);
+            // A warp takes 128 columns (half a tile) of kTok tokens at a time: the runs of its tile are found once and
+            // its loads are whole lines, kTok * kRuns of them in flight.
+            constexpr int kTok = N == 16 ? 1 : N == 32 ? 2 : 4, kRuns = 12 / kTok;
+            const uint32_t halves = ct_d, groups = (T + kTok - 1) / kTok;
+            for (uint32_t i = (et >> 5) * gridDim.x + cta; ok && i < halves * groups;
+                 i += gridDim.x * (kMtEpiThreads / 32)) {
+                const uint32_t gr = i / halves, hf = i - gr * halves, tile = hf >> 1;
+                const uint32_t lo = sp2.owner(tile * AK2), hi = sp2.owner((tile + 1) * AK2 - 1);
+                if (lo == hi) continue;  // one run had the whole tile
+                const bool lo_second = sp2.earlier(lo, tile * AK2);
+                const uint32_t d = hf * 128 + lane * 4, t0 = gr * kTok;
+                float4 sum[kTok];
+#pragma unroll
+                for (int t = 0; t < kTok; ++t) sum[t] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                for (uint32_t o = lo; o <= hi; o += kRuns) {
+                    float4 v[kRuns][kTok];
+#pragma unroll
+                    for (int x = 0; x < kRuns; ++x) {
+                        const float* q = slot(o + x, o + x == lo && lo_second) + ((int64_t)(hf & 1) * T + t0) * 128 + lane * 4;
+#pragma unroll
+                        for (int t = 0; t < kTok; ++t) {
+                            v[x][t] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                            ld_if(v[x][t], q + t * 128, o + x <= hi && t0 + t < (uint32_t)T);
+                        }
+                    }
+#pragma unroll
+                    for (int x = 0; x < kRuns; ++x)
+#pragma unroll
+                        for (int t = 0; t < kTok; ++t) {
+                            sum[t].x += v[x][t].x;
+                            sum[t].y += v[x][t].y;
+                            sum[t].z += v[x][t].z;
+                            sum[t].w += v[x][t].w;
+                        }
+                }
+#pragma unroll
+                for (int t = 0; t < kTok; ++t)
+                    if (d < D && t0 + t < (uint32_t)T)  // D is a multiple of 32
+                        *reinterpret_cast<uint2*>(p.y + (int64_t)(t0 + t) * D + d) =
+                            make_uint2(pack_bf16x2(sum[t].x, sum[t].y), pack_bf16x2(sum[t].z, sum[t].w));
+            }
         }
     }
     tc_fence_before();
@@ -629,11 +918,10 @@ __global__ void __launch_bounds__(kMtThreads, 1)
         tmem_dealloc(tmem, 512);
     }
     if (tid == 0) {
-        // the last CTA to leave puts the grid barrier back to zero for the next launch
+        // the last CTA to leave puts the arrivals back to zero for the next launch
         __threadfence();
-        if (atomicAdd(p.header + 1, 1u) + 1u == gridDim.x) {
-            p.header[0] = 0u;
-            p.header[1] = 0u;
+        if (atomicAdd(p.header + kMtExits, 1u) + 1u == gridDim.x) {
+            for (int i = 0; i <= kMtExits; ++i) p.header[i] = 0u;
             __threadfence();
         }
     }
@@ -735,7 +1023,7 @@ extern "C" mxfp8_status_t mx_moe_tokens(const void* x_bf16, const float* router_
     const MtLayout l = mt_layout(T, E, D, H, top_k, bits);
     if (workspace_bytes < (size_t)l.total) return MXFP8_ERR_SHAPE;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    const int N = T <= 32 ? 32 : 64;
+    const int N = T <= 16 ? 16 : T <= 32 ? 32 : 64;
     const int64_t Db = D * bits / 8, Hb = H * bits / 8;
     CUtensorMap m[5];
     if (!mt_map(&m[0], gate_q, Db, (int64_t)E * H, 0, 128) || !mt_map(&m[1], up_q, Db, (int64_t)E * H, 0, 128) ||
@@ -766,6 +1054,7 @@ extern "C" mxfp8_status_t mx_moe_tokens(const void* x_bf16, const float* router_
     p.score = score;
     p.ncounters = (int)l.ncounters;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (bits == 8) return N == 32 ? mt_launch<8, 32>(m, p, st) : mt_launch<8, 64>(m, p, st);
-    return N == 32 ? mt_launch<4, 32>(m, p, st) : mt_launch<4, 64>(m, p, st);
+    if (bits == 8)
+        return N == 16 ? mt_launch<8, 16>(m, p, st) : N == 32 ? mt_launch<8, 32>(m, p, st) : mt_launch<8, 64>(m, p, st);
+    return N == 16 ? mt_launch<4, 16>(m, p, st) : N == 32 ? mt_launch<4, 32>(m, p, st) : mt_launch<4, 64>(m, p, st);
 }
