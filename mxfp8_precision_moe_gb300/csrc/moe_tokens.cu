@@ -83,45 +83,6 @@ struct MtParams {
     int ncounters;
 };
 
-// One lane of a converged warp.
-__device__ __forceinline__ uint32_t elect_one() {
-    uint32_t r;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-    return r;
-}
-// Tensor-core operations of the lane whose `one` is set.
-__device__ __forceinline__ void cp_scales(uint32_t one, uint32_t taddr, uint64_t sdesc) {
-    asm volatile(
-        "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %0, 0;\n\t"
-        "@q tcgen05.cp.cta_group::1.32x128b.warpx4 [%1], %2;\n\t}" ::"r"(one),
-        "r"(taddr), "l"(sdesc)
-        : "memory");
-}
-__device__ __forceinline__ void commit(uint32_t one, uint64_t* bar) {
-    asm volatile(
-        "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %0, 0;\n\t"
-        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%1];\n\t}" ::"r"(one),
-        "r"(smem_u32(bar))
-        : "memory");
-}
-__device__ __forceinline__ void mma_mxf8(uint32_t one, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
-                                         uint32_t sfb, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.u32 q, %7, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(
-            d),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb), "r"(one)
-        : "memory");
-}
-__device__ __forceinline__ void mma_mxf4(uint32_t one, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
-                                         uint32_t sfb, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.u32 q, %7, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb), "r"(one)
-        : "memory");
-}
-
 __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
@@ -156,14 +117,6 @@ __device__ __forceinline__ bool epi_all(bool yes) {
         : "memory");
     return r != 0;
 }
-
-// Shared-memory descriptors by halves: the low word is address / 16 (14 bits) with the leading offset above it
-// (unused by 128-byte swizzled tiles; 1), the high word is constant for tiles (stride 1024 bytes between 8-row
-// groups, version 1, 128-byte swizzle) and for 32 x 16-byte scale tiles (stride 128, no swizzle).
-constexpr uint32_t kDescLbo = 1u << 16;
-constexpr uint32_t kDescTile = (1024u >> 4) | (1u << 14) | (2u << 29);
-constexpr uint32_t kDescScale = (128u >> 4) | (1u << 14);
-__device__ __forceinline__ uint64_t desc_of(uint32_t lo, uint32_t hi) { return ((uint64_t)hi << 32) | lo; }
 
 // The epilogue warps wait here for the routing tables; the other four warps only arrive.
 __device__ __forceinline__ void routed_arrive() { asm volatile("bar.arrive 3, 384;" ::: "memory"); }

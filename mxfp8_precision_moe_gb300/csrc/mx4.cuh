@@ -116,4 +116,103 @@ __device__ __forceinline__ RowTile locate_row_tile(const int32_t* offs, int G, i
     return r;
 }
 
+// Shared-memory descriptors by halves: the low word is address / 16 (14 bits) with the leading offset above it
+// (unused by 128-byte swizzled tiles; 1), the high word is constant for tiles (stride 1024 bytes between 8-row
+// groups, version 1, 128-byte swizzle) and for 32 x 16-byte scale tiles (stride 128, no swizzle).
+constexpr uint32_t kDescLbo = 1u << 16;
+constexpr uint32_t kDescTile = (1024u >> 4) | (1u << 14) | (2u << 29);
+constexpr uint32_t kDescScale = (128u >> 4) | (1u << 14);
+__device__ __forceinline__ uint64_t desc_of(uint32_t lo, uint32_t hi) { return ((uint64_t)hi << 32) | lo; }
+
+// One lane of a converged warp.
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r;
+}
+// Operations of the lane whose `one` is set, in a loop that the whole warp walks: their descriptors and addresses then
+// stay in uniform registers, where these instructions take them from.  Issued from a lane == 0 branch, each
+// tcgen05.mma took about 70 cycles and each tcgen05.cp 56, which is what bounds a kernel whose MMAs are short.
+__device__ __forceinline__ void cp_scales(uint32_t one, uint32_t taddr, uint64_t sdesc) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %0, 0;\n\t"
+        "@q tcgen05.cp.cta_group::1.32x128b.warpx4 [%1], %2;\n\t}" ::"r"(one),
+        "r"(taddr), "l"(sdesc)
+        : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t one, uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %0, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%1];\n\t}" ::"r"(one),
+        "r"(smem_u32(bar))
+        : "memory");
+}
+__device__ __forceinline__ void mma_mxf8(uint32_t one, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
+                                         uint32_t sfb, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.u32 q, %7, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(
+            d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb), "r"(one)
+        : "memory");
+}
+__device__ __forceinline__ void mma_mxf4(uint32_t one, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
+                                         uint32_t sfb, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.u32 q, %7, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb), "r"(one)
+        : "memory");
+}
+
+// The same for a CTA pair.
+__device__ __forceinline__ void cp_scales_pair(uint32_t one, uint32_t taddr, uint64_t sdesc) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %0, 0;\n\t"
+        "@q tcgen05.cp.cta_group::2.32x128b.warpx4 [%1], %2;\n\t}" ::"r"(one),
+        "r"(taddr), "l"(sdesc)
+        : "memory");
+}
+__device__ __forceinline__ void commit_pair(uint32_t one, uint64_t* bar, uint16_t cta_mask) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %0, 0;\n\t"
+        "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%1], %2;\n\t}" ::"r"(
+            one),
+        "r"(smem_u32(bar)), "h"(cta_mask)
+        : "memory");
+}
+__device__ __forceinline__ void mma_pair_mxf4(uint32_t one, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                              uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.u32 q, %7, 0;\n\t"
+        "@q tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb), "r"(one)
+        : "memory");
+}
+__device__ __forceinline__ void load_2d_pair(uint32_t one, uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y,
+                                             uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+        "@q cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+        "%3}], [%4];\n\t}" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "r"(one)
+        : "memory");
+}
+__device__ __forceinline__ void load_3d_pair(uint32_t one, uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y,
+                                             int32_t z, uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %6, 0;\n\t"
+        "@q cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, "
+        "%4}], [%5];\n\t}" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar), "r"(one)
+        : "memory");
+}
+__device__ __forceinline__ void expect_tx(uint32_t one, uint64_t* bar, uint32_t bytes) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %2, 0;\n\t"
+        "@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(smem_u32(bar)),
+        "r"(bytes), "r"(one)
+        : "memory");
+}
+
 }  // namespace mx

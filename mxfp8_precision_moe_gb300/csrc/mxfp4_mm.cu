@@ -14,6 +14,14 @@
 // Rows past a group's end are read (they are the next group's) and masked at the store; a K that is not a
 // multiple of 256 multiplies only the 64-wide steps that hold any of it (a row's tail past K is TMA's zero
 // fill and the scale layout's zero padding).  Every wait is bounded.
+//
+// At 4 bits a stage's four MMAs take about 0.25 us, so what the issuing threads do per stage decides.  8 experts,
+// 16384 tokens, N = 8192, K = 5120: 249 us (5.5 PFLOP/s) with one thread issuing from a lane == 0 branch,
+// 210 us with whole warps and an elected lane (mx4.cuh) and one copy for both of B's scale tiles, 204 us
+// (6.7 PFLOP/s) with six stages instead of five.  What is left: with a quarter of the MMAs the same kernel takes 166 us,
+// with half the operand loads 186, without its stores 195, so L2's feed (18 TB/s at 166 us) and the tensor cores
+// bound it together, and the single accumulator's drain adds the rest (a second one does not fit beside the
+// scales' columns).  Rastering bands of 8 or 32 tiles instead of 16: 218 and 223 us.
 
 #include "host_common.h"
 #include "mx4.cuh"
@@ -25,8 +33,11 @@ constexpr int kF4SfWarp = 2 + kF4EpiWarps;
 constexpr int kF4Threads = 96 + 32 * kF4EpiWarps;
 constexpr int kF4Band = 16;  // 256-row tiles per raster band (tiles of a band share B tiles in L2)
 
+// The group tables (three words a group) share the block's memory with the ring: six stages up to kMostGroups
+// groups, five beyond.
+template <int STAGES>
 struct CfgF4 {
-    static constexpr int kStages = 5;
+    static constexpr int kStages = STAGES;
     static constexpr int kABytes = 128 * 128;
     static constexpr int kBBytes = 128 * 128;
     static constexpr int kSfaBytes = 2 * 512;      // two scale tiles: 256 elements of K
@@ -41,9 +52,12 @@ struct CfgF4 {
     static constexpr int kOffSfb = kOffSfa + kStages * kSfaBytes;
     static constexpr int kOffStage = kOffSfb + kStages * kSfbBytes;
     static constexpr int kOffBar = kOffStage + kF4EpiWarps * 1024;
-    static constexpr int kSmem = kOffBar + (3 * kStages + 4) * 8 + 16 + 1024;
+    static constexpr int kOffTable = kOffBar + (3 * kStages + 4) * 8 + 16;
+    static constexpr int kMost = 226 * 1024;  // the static variables take the last KB
+    static constexpr int smem(int G) { return kOffTable + 12 * G + 1024; }
+    static constexpr int kMostGroups = (kMost - smem(0)) / 12;
 };
-static_assert(CfgF4::kSmem + 3 * MXFP8_MAX_GROUPS * 4 + 32 <= 227 * 1024, "shared memory");
+static_assert(CfgF4<6>::kMostGroups >= 256 && CfgF4<5>::kMostGroups >= MXFP8_MAX_GROUPS, "shared memory");
 
 struct F4Params {
     const int32_t* offs;
@@ -60,20 +74,9 @@ __host__ __device__ constexpr uint32_t idesc_mxf4(uint32_t M, uint32_t N, uint32
            ((a_sf & 3u) << 29);
 }
 
-__device__ __forceinline__ void tc_mma_pair_mxf4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                                 uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(
-            d_tmem),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa_tmem), "r"(sfb_tmem)
-        : "memory");
-}
-
 struct F4Tile {
     int64_t a_row, b_row;
-    int64_t sfa_chunk, sfb_chunk[2];  // scale tile (512 bytes) of K element 0
+    int64_t sfa_chunk, sfb_chunk;     // scale tile (512 bytes) of K element 0; 128-row chunk of B
     __nv_bfloat16* out;               // first element of this CTA's 128 rows
     int valid_rows, valid_cols;
 };
@@ -98,25 +101,22 @@ __device__ __forceinline__ F4Tile f4_tile(const F4Params& p, int64_t t, int half
     F4Tile ti;
     ti.a_row = start + rows0;
     ti.b_row = (int64_t)g * p.N + n * 256 + half * 128;
-    // clamped: rows past the group, columns past N are masked
+    // clamped: rows past the group are masked (so are columns past N, whose scales are the next expert's or 0)
     ti.sfa_chunk = (pt_s[g] + min64(2 * m + half, (size + 127) / 128 - 1)) * ct;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) ti.sfb_chunk[j] = ((int64_t)g * nchunk + min64(2 * n + j, nchunk - 1)) * ct;
+    ti.sfb_chunk = (int64_t)g * nchunk + 2 * n;
     ti.out = p.out + ti.a_row * p.N + n * 256;
     ti.valid_rows = (int)max64(0, min64(128, size - rows0));
     ti.valid_cols = (int)min64(256, p.N - n * 256);
     return ti;
 }
 
+template <int STAGES>
 __global__ void __launch_bounds__(kF4Threads, 1)
     mxfp4_grouped_mm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
                             const __grid_constant__ CUtensorMap tmap_sfa,
                             const __grid_constant__ CUtensorMap tmap_sfb, const F4Params p) {
-    using C = CfgF4;
+    using C = CfgF4<STAGES>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    __shared__ int32_t ends_s[kMaxGroups];
-    __shared__ int32_t pt_s[kMaxGroups];
-    __shared__ int32_t tt_s[kMaxGroups];
     __shared__ int32_t ttotal_s;
     __shared__ uint32_t tmem_base_s;
     __shared__ int abort_s;
@@ -129,8 +129,11 @@ __global__ void __launch_bounds__(kF4Threads, 1)
     uint64_t* tempty = tfull + 1;
     uint64_t* drain = tempty + 1;
     uint64_t* sfdrain = drain + 1;
+    int32_t* ends_s = reinterpret_cast<int32_t*>(smem + C::kOffTable);
+    int32_t* pt_s = ends_s + p.G;
+    int32_t* tt_s = pt_s + p.G;
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int half = (int)(cluster_ctarank() & 1u);
     const bool leader = half == 0;
 
@@ -203,35 +206,41 @@ __global__ void __launch_bounds__(kF4Threads, 1)
     cluster_sync();  // the peer may signal this CTA's barriers from here on
     tc_fence_after();
 
-    const uint32_t tmem = tmem_base_s;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_base_s, 0);
+    const uint32_t ring = __shfl_sync(0xffffffffu, smem_u32(smem), 0);
     volatile int* abort_flag = &abort_s;
-    const int64_t ntiles = (int64_t)ttotal_s * ((p.N + 255) / 256);
+    const int64_t ntiles = (int64_t)__shfl_sync(0xffffffffu, ttotal_s, 0) * ((p.N + 255) / 256);
     const int64_t cid = blockIdx.x >> 1, ncl = gridDim.x >> 1;
     const int k_tiles = (int)((p.K + 255) / 256);
+    // a wait by a whole warp that goes on, or gives up, together
+    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu, mbar_wait_bounded<true>(bar, parity, p.timeout_ns, abort_flag, p.dev_status));
+    };
 
-    if (warp == 0 && lane == 0) {
+    if (warp == 0) {
         // ------------------------------------------------ TMA producer (both CTAs)
+        const uint32_t one = elect_one();
         int stage = 0;
         uint32_t phase = 0, issued = 0, last_phase = 0;
         bool ok = true;
         for (int64_t t = cid; t < ntiles && ok; t += ncl) {
             const F4Tile ti = f4_tile(p, t, half, ends_s, pt_s, tt_s);
+            const int32_t a_row = __shfl_sync(0xffffffffu, (int32_t)ti.a_row, 0);
+            const int32_t b_row = __shfl_sync(0xffffffffu, (int32_t)ti.b_row, 0);
+            const int32_t sfa = __shfl_sync(0xffffffffu, (int32_t)(2 * ti.sfa_chunk), 0);
+            const int32_t sfb = __shfl_sync(0xffffffffu, (int32_t)ti.sfb_chunk, 0);
             for (int kt = 0; kt < k_tiles; ++kt) {
-                if (!mbar_wait_bounded<true>(&empty[stage], phase ^ 1u, p.timeout_ns, abort_flag, p.dev_status)) {
+                if (!wait(&empty[stage], phase ^ 1u)) {
                     ok = false;
                     break;
                 }
                 const uint32_t fb = cluster_addr(&full[stage], 0);
-                if (leader) mbar_arrive_expect_tx(&full[stage], C::kTx);
-                tma_load_2d_pair(smem + stage * C::kABytes, &tmap_a, kt * 128, (int32_t)ti.a_row, fb);
-                tma_load_2d_pair(smem + C::kOffB + stage * C::kBBytes, &tmap_b, kt * 128, (int32_t)ti.b_row, fb);
+                if (leader) expect_tx(one, &full[stage], C::kTx);
+                load_2d_pair(one, ring + stage * C::kABytes, &tmap_a, kt * 128, a_row, fb);
+                load_2d_pair(one, ring + C::kOffB + stage * C::kBBytes, &tmap_b, kt * 128, b_row, fb);
                 // two scale tiles a copy (an odd count's last copy reads one tile further, which nothing uses)
-                tma_load_2d_pair(smem + C::kOffSfa + stage * C::kSfaBytes, &tmap_sfa, 0,
-                                 (int32_t)(2 * (ti.sfa_chunk + 2 * kt)), fb);
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    tma_load_2d_pair(smem + C::kOffSfb + stage * C::kSfbBytes + 1024 * j, &tmap_sfb, 0,
-                                     (int32_t)(2 * (ti.sfb_chunk[j] + 2 * kt)), fb);
+                load_2d_pair(one, ring + C::kOffSfa + stage * C::kSfaBytes, &tmap_sfa, 0, sfa + 4 * kt, fb);
+                load_3d_pair(one, ring + C::kOffSfb + stage * C::kSfbBytes, &tmap_sfb, 0, 4 * kt, sfb, fb);
                 issued |= 1u << stage;
                 last_phase = (last_phase & ~(1u << stage)) | (phase << stage);
                 if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
@@ -243,76 +252,84 @@ __global__ void __launch_bounds__(kF4Threads, 1)
                 if (issued & (1u << s))
                     mbar_wait_bounded<true>(&full[s], (last_phase >> s) & 1u, p.timeout_ns, &no_abort, nullptr);
         }
-    } else if (warp == 1 && lane == 0 && leader) {
+    } else if (warp == 1) {
         // ------------------------------------------------ MMA issuer (even CTA)
-        int stage = 0;
-        uint32_t phase = 0, acc_phase = 0;
-        bool ok = true;
-        constexpr uint32_t idesc0 = idesc_mxf4(256, 256, 0, 0);
-        for (int64_t t = cid; t < ntiles && ok; t += ncl) {
-            if (!mbar_wait_bounded<true>(tempty, acc_phase ^ 1u, p.timeout_ns, abort_flag, p.dev_status)) break;
-            tc_fence_after();
-            for (int kt = 0; kt < k_tiles; ++kt) {
-                const int cur = stage;
-                if (!mbar_wait_bounded<true>(&full[cur], phase, p.timeout_ns, abort_flag, p.dev_status) ||
-                    !mbar_wait_bounded<true>(&sfull[cur], phase, p.timeout_ns, abort_flag, p.dev_status)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
-                const uint32_t sf = tmem + C::kSfCol0 + cur * C::kSfCols;
-                const uint32_t a_s = smem_u32(smem + cur * C::kABytes);
-                const uint32_t b_s = smem_u32(smem + C::kOffB + cur * C::kBBytes);
-                const int steps = (int)min64(4, (p.K - (int64_t)kt * 256 + 63) / 64);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    if (k >= steps) break;
-                    const uint64_t ad = smem_desc(a_s + 32 * k, 16, 1024, 2);
-                    const uint64_t bd = smem_desc(b_s + 32 * k, 16, 1024, 2);
-                    const uint32_t id = (uint32_t)(k & 1) * 2;  // scale bytes 0-1 or 2-3 of the word
-                    tc_mma_pair_mxf4(tmem, ad, bd, idesc0 | (id << 4) | (id << 29), sf + 4 * (k >> 1),
-                                     sf + 8 + 8 * (k >> 1), (kt | k) != 0);
-                }
-                tc_commit_pair(&empty[cur], 0x3);
-            }
-            if (!ok) break;
-            tc_commit_pair(tfull, 0x3);
-            acc_phase ^= 1u;
-        }
-        // all tensor-core work of the pair is done before the columns are freed
-        tc_commit_pair(drain, 0x1);
-        volatile int no_abort = 0;
-        mbar_wait_bounded<true>(drain, 0, p.timeout_ns, &no_abort, p.dev_status);
-    } else if (warp == kF4SfWarp) {
-        // ------------------------------------------------ scale copies (even CTA)
-        if (lane == 0 && leader) {
+        if (leader) {
+            const uint32_t one = elect_one();
             int stage = 0;
-            uint32_t phase = 0;
+            uint32_t phase = 0, acc_phase = 0;
             bool ok = true;
+            constexpr uint32_t idesc0 = idesc_mxf4(256, 256, 0, 0);
             for (int64_t t = cid; t < ntiles && ok; t += ncl) {
+                if (!wait(tempty, acc_phase ^ 1u)) break;
+                tc_fence_after();
                 for (int kt = 0; kt < k_tiles; ++kt) {
-                    if (!mbar_wait_bounded<true>(&full[stage], phase, p.timeout_ns, abort_flag, p.dev_status)) {
+                    if (!wait(&full[stage], phase) || !wait(&sfull[stage], phase)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
                     const uint32_t sf = tmem + C::kSfCol0 + stage * C::kSfCols;
-                    const uint32_t sa = smem_u32(smem + C::kOffSfa + stage * C::kSfaBytes);
-                    const uint32_t sb = smem_u32(smem + C::kOffSfb + stage * C::kSfbBytes);
+                    const uint32_t a_s = ((ring + stage * C::kABytes) >> 4) | kDescLbo;
+                    const uint32_t b_s = ((ring + C::kOffB + stage * C::kBBytes) >> 4) | kDescLbo;
+                    auto mma = [&](int k, uint32_t acc) {
+                        const uint32_t id = (uint32_t)(k & 1) * 2;  // scale bytes 0-1 or 2-3 of the word
+                        mma_pair_mxf4(one, tmem, desc_of(a_s + 2 * k, kDescTile), desc_of(b_s + 2 * k, kDescTile),
+                                      idesc0 | (id << 4) | (id << 29), sf + 4 * (k >> 1), sf + 8 + 8 * (k >> 1), acc);
+                    };
+                    if ((int64_t)(kt + 1) * 256 <= p.K) {
+                        mma(0, kt != 0);
+                        mma(1, 1u);
+                        mma(2, 1u);
+                        mma(3, 1u);
+                    } else {  // the contraction's last elements
+                        const int steps = (int)((p.K - (int64_t)kt * 256 + 63) / 64);
+                        mma(0, kt != 0);
+                        if (steps > 1) mma(1, 1u);
+                        if (steps > 2) mma(2, 1u);
+                        if (steps > 3) mma(3, 1u);
+                    }
+                    commit_pair(one, &empty[stage], 0x3);
+                    if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
+                }
+                if (!ok) break;
+                commit_pair(one, tfull, 0x3);
+                acc_phase ^= 1u;
+            }
+            // all tensor-core work of the pair is done before the columns are freed
+            commit_pair(one, drain, 0x1);
+            volatile int no_abort = 0;
+            mbar_wait_bounded<true>(drain, 0, p.timeout_ns, &no_abort, p.dev_status);
+        }
+    } else if (warp == kF4SfWarp) {
+        // ------------------------------------------------ scale copies (even CTA)
+        if (leader) {
+            const uint32_t one = elect_one();
+            int stage = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int64_t t = cid; t < ntiles && ok; t += ncl) {
+                for (int kt = 0; kt < k_tiles; ++kt) {
+                    if (!wait(&full[stage], phase)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t sf = tmem + C::kSfCol0 + stage * C::kSfCols;
+                    const uint32_t sa = (ring + C::kOffSfa + stage * C::kSfaBytes) >> 4;
+                    const uint32_t sb = (ring + C::kOffSfb + stage * C::kSfbBytes) >> 4;
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        tc_cp_pair_32x128b_warpx4(sf + 4 * h, smem_desc(sa + 512 * h, 0, 128, 0));
+                        cp_scales_pair(one, sf + 4 * h, desc_of(sa + 32 * h, kDescScale));
 #pragma unroll
                         for (int j = 0; j < 2; ++j)
-                            tc_cp_pair_32x128b_warpx4(sf + 8 + 8 * h + 4 * j,
-                                                      smem_desc(sb + 1024 * j + 512 * h, 0, 128, 0));
+                            cp_scales_pair(one, sf + 8 + 8 * h + 4 * j, desc_of(sb + 64 * j + 32 * h, kDescScale));
                     }
-                    tc_commit_pair(&sfull[stage], 0x1);
+                    commit_pair(one, &sfull[stage], 0x1);
                     if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
                 }
             }
-            tc_commit_pair(sfdrain, 0x1);
+            commit_pair(one, sfdrain, 0x1);
             volatile int no_abort = 0;
             mbar_wait_bounded<true>(sfdrain, 0, p.timeout_ns, &no_abort, p.dev_status);
         }
@@ -381,18 +398,44 @@ __global__ void __launch_bounds__(kF4Threads, 1)
 }
 
 // ---------------------------------------------------------------- host side
-// uint8 [rows][cols], boxes of box_rows x box_cols bytes.
+// uint8 [planes][rows][cols], boxes of box_planes x box_rows x box_cols bytes.
 static bool f4_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int box_rows, int box_cols,
-                   bool swizzle) {
+                   bool swizzle, int64_t planes = 1, int box_planes = 1) {
     host::EncodeTiledFn fn = host::encode_fn();
     if (!fn) return false;
-    cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-    cuuint64_t strides[1] = {(cuuint64_t)cols};
-    cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
-    cuuint32_t estr[2] = {1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+    cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)planes};
+    cuuint64_t strides[2] = {(cuuint64_t)cols, (cuuint64_t)(cols * rows)};
+    cuuint32_t box[3] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, (cuuint32_t)box_planes};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, box_planes > 1 ? 3 : 2, const_cast<void*>(base), dims, strides, box, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int STAGES>
+static mxfp8_status_t f4_launch(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& msa,
+                                const CUtensorMap& msb, const F4Params& p, int clusters, cudaStream_t st) {
+    using C = CfgF4<STAGES>;
+    static std::atomic<int> attr_set[host::kMaxDevices];
+    if (!host::ensure_smem(reinterpret_cast<const void*>(mxfp4_grouped_mm_kernel<STAGES>), C::kMost, attr_set))
+        return MXFP8_ERR_LAUNCH;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(2 * (unsigned)clusters);
+    cfg.blockDim = dim3(kF4Threads);
+    cfg.dynamicSmemBytes = C::smem(p.G);
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, mxfp4_grouped_mm_kernel<STAGES>, ma, mb, msa, msb, p) != cudaSuccess) {
+        cudaGetLastError();
+        return MXFP8_ERR_LAUNCH;
+    }
+    return host::last_launch_status();
 }
 
 }  // namespace mx
@@ -418,7 +461,7 @@ extern "C" mxfp8_status_t mxfp4_grouped_mm_fwd(const void* a_q, const void* a_s,
     if (mxfp8_status_t a = host::check_arch(); a != MXFP8_OK) return a;
     CUtensorMap ma, mb, msa, msb;
     if (!f4_map(&ma, a_q, M, K / 2, 128, 128, true) || !f4_map(&mb, w_q, (int64_t)G * N, K / 2, 128, 128, true) ||
-        !f4_map(&msa, a_s, sfa_rows, 256, 4, 256, false) || !f4_map(&msb, w_s, sfb_rows, 256, 4, 256, false))
+        !f4_map(&msa, a_s, sfa_rows, 256, 4, 256, false) || !f4_map(&msb, w_s, ct * 2, 256, 4, 256, false, (int64_t)G * ((N + 127) / 128), 2))
         return MXFP8_ERR_DRIVER;
     F4Params p{};
     p.offs = offs;
@@ -429,22 +472,9 @@ extern "C" mxfp8_status_t mxfp4_grouped_mm_fwd(const void* a_q, const void* a_s,
     p.out = static_cast<__nv_bfloat16*>(out_bf16);
     p.dev_status = dev_status;
     p.timeout_ns = 2000000000ull;
-    static std::atomic<int> attr_set[host::kMaxDevices];
-    if (!host::ensure_smem(reinterpret_cast<const void*>(mxfp4_grouped_mm_kernel), CfgF4::kSmem, attr_set))
-        return MXFP8_ERR_LAUNCH;
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.blockDim = dim3(kF4Threads);
-    cfg.dynamicSmemBytes = CfgF4::kSmem;
-    cfg.stream = reinterpret_cast<cudaStream_t>(stream);
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
     const int64_t bound = ((M + 255) / 256 + G) * ((N + 255) / 256);
-    cfg.gridDim = dim3(2 * (unsigned)max64(1, min64(bound, host::num_sms() / 2)));
-    if (cudaLaunchKernelEx(&cfg, mxfp4_grouped_mm_kernel, ma, mb, msa, msb, p) != cudaSuccess) return MXFP8_ERR_LAUNCH;
-    return host::last_launch_status();
+    const int clusters = (int)max64(1, min64(bound, host::num_sms() / 2));
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    return G <= CfgF4<6>::kMostGroups ? f4_launch<6>(ma, mb, msa, msb, p, clusters, st)
+                                      : f4_launch<5>(ma, mb, msa, msb, p, clusters, st);
 }
