@@ -11,11 +11,11 @@ quantized to the same format along each product's contraction, as on the path fo
 """
 from __future__ import annotations
 
-import ctypes
-
 import torch
 
 from . import _bytes_at_least, _cuda, _expert_blocked_bytes, _status_word, _tensor, check, load
+
+_raw_stream = torch._C._cuda_getCurrentRawStream  # the current stream's handle, without building an object
 
 SCORES = {"softmax": 0, "softmax_all": 1, "sigmoid": 2}
 MAX_TOKENS, MAX_EXPERTS, MAX_TOP_K = 64, 256, 16
@@ -119,10 +119,10 @@ class MxMoeTokens:
             out = torch.empty((T, self.D), dtype=torch.bfloat16, device=self.device)
         if T == 0:
             return out
-        stream = torch.cuda.current_stream(self.device).cuda_stream
+        stream = _raw_stream(self.device.index)
         ws = self._workspace(stream)
         E, D, H, k, score, bits, *weights = self._fixed
         check(self._call(x.data_ptr(), router_logits.data_ptr(), T, E, D, H, k, score, bits, *weights, ws.data_ptr(),
                          self._bytes, out.data_ptr(), None if dev_status is None else dev_status.data_ptr(),
-                         ctypes.c_void_p(stream)), "mx_moe_tokens")
+                         stream), "mx_moe_tokens")
         return out

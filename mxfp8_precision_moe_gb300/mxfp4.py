@@ -11,10 +11,12 @@ from __future__ import annotations
 
 import torch
 
-from . import (COL, ROW, SCALES_BLOCKED, SCALES_COMPACT, _bytes_at_least, _cuda, _expert_blocked_bytes, _offsets, _p,
-               _status_word, _stream, _tensor, _u8, check, load, mxfp8_check_offsets, mxfp8_grouped_mm_dgrad,
-               mxfp8_grouped_mm_wgrad, mxfp8_quantize_2d, mxfp8_quantize_3d_experts, mxfp8_scale_bytes, new_status,
-               read_status)
+from . import (COL, ROW, SCALES_BLOCKED, SCALES_COMPACT, _bytes_at_least, _cuda, _expert_blocked_bytes, _offsets,
+               _status_word, _tensor, check, load, mxfp8_check_offsets, new_status, read_status)
+
+# torch's handle of a device's current stream as an integer: a few tenths of a microsecond, where
+# torch.cuda.current_stream() builds an object in several
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _width(K: int, name: str):
@@ -22,12 +24,26 @@ def _width(K: int, name: str):
         raise ValueError(f"{name}: the last dimension must be a positive multiple of 32, got {K}")
 
 
-def _row_scales(M: int, K: int, G: int, layout: int, device):
+def _group_bytes(M: int, K: int, G: int) -> int:
+    """Blocked scale bytes of M rows in G groups (the bound of mxfp8_scale_bytes)."""
+    return ((M + 127) // 128 + G) * ((K + 127) // 128) * 512
+
+
+def _col_bytes(R: int, M: int, G: int) -> int:
+    """Blocked scale bytes of R token-wise quantized rows (the bound of mxfp8_scale_bytes_colgroups)."""
+    return ((R + 127) // 128) * ((M + 127) // 128 + G) * 512
+
+
+def _row_scales(x: torch.Tensor, M: int, K: int, G: int, layout: int):
     if layout == SCALES_COMPACT:
-        return _u8((M, K // 32), device)
+        return x.new_empty((M, K // 32), dtype=torch.uint8)
     if layout != SCALES_BLOCKED:
         raise ValueError("scale_layout: SCALES_COMPACT or SCALES_BLOCKED expected")
-    return _u8((mxfp8_scale_bytes(M, K, G, SCALES_BLOCKED),), device)
+    return x.new_empty(_group_bytes(M, K, G), dtype=torch.uint8)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
 
 
 def mxfp4_quantize_2d(x: torch.Tensor, scale_layout: int = SCALES_BLOCKED, offs: torch.Tensor | None = None):
@@ -41,8 +57,8 @@ def mxfp4_quantize_2d(x: torch.Tensor, scale_layout: int = SCALES_BLOCKED, offs:
         _offsets(offs)
     _cuda(x, offs)
     G = int(offs.numel()) if offs is not None else 1
-    q, s = _u8((M, K // 2), x.device), _row_scales(M, K, G, scale_layout, x.device)
-    check(load().mxfp4_quantize_2d(_p(x), M, K, scale_layout, _p(offs), G, _p(q), _p(s), _stream(x.device)),
+    q, s = x.new_empty((M, K // 2), dtype=torch.uint8), _row_scales(x, M, K, G, scale_layout)
+    check(load().mxfp4_quantize_2d(_ptr(x), M, K, scale_layout, _ptr(offs), G, _ptr(q), _ptr(s), _raw_stream(x.device.index)),
           "mxfp4_quantize_2d")
     return q, s
 
@@ -59,9 +75,9 @@ def mxfp4_swiglu_quantize(h1: torch.Tensor, h3: torch.Tensor, scale_layout: int 
         _offsets(offs)
     _cuda(h1, h3, offs)
     G = int(offs.numel()) if offs is not None else 1
-    q, s = _u8((M, K // 2), h1.device), _row_scales(M, K, G, scale_layout, h1.device)
-    check(load().mxfp4_swiglu_quantize(_p(h1), _p(h3), M, K, scale_layout, _p(offs), G, _p(q), _p(s),
-                                       _stream(h1.device)), "mxfp4_swiglu_quantize")
+    q, s = h1.new_empty((M, K // 2), dtype=torch.uint8), _row_scales(h1, M, K, G, scale_layout)
+    check(load().mxfp4_swiglu_quantize(_ptr(h1), _ptr(h3), M, K, scale_layout, _ptr(offs), G, _ptr(q), _ptr(s),
+                                       _raw_stream(h1.device.index)), "mxfp4_swiglu_quantize")
     return q, s
 
 
@@ -72,12 +88,12 @@ def mxfp4_quantize_3d_experts(w: torch.Tensor, scale_layout: int = SCALES_BLOCKE
     G, N, K = w.shape
     _width(K, "w")
     _cuda(w)
-    q = _u8((G, N, K // 2), w.device)
+    q = w.new_empty((G, N, K // 2), dtype=torch.uint8)
     if scale_layout == SCALES_COMPACT:
-        s = _u8((G, N, K // 32), w.device)
+        s = w.new_empty((G, N, K // 32), dtype=torch.uint8)
     else:
-        s = _u8((G, _expert_blocked_bytes(N, K)), w.device)
-    check(load().mxfp4_quantize_3d_experts(_p(w), G, N, K, scale_layout, _p(q), _p(s), _stream(w.device)),
+        s = w.new_empty((G, _expert_blocked_bytes(N, K)), dtype=torch.uint8)
+    check(load().mxfp4_quantize_3d_experts(_ptr(w), G, N, K, scale_layout, _ptr(q), _ptr(s), _raw_stream(w.device.index)),
           "mxfp4_quantize_3d_experts")
     return q, s
 
@@ -93,11 +109,11 @@ def mxfp4_dequantize_2d(q: torch.Tensor, s: torch.Tensor, scale_layout: int = SC
         _offsets(offs)
     G = int(offs.numel()) if offs is not None else 1
     need = M * (K // 32) if scale_layout == SCALES_COMPACT else \
-        (mxfp8_scale_bytes(M, K, G, SCALES_BLOCKED) if offs is not None else _expert_blocked_bytes(M, K))
+        (_group_bytes(M, K, G) if offs is not None else _expert_blocked_bytes(M, K))
     _bytes_at_least(s, "s", need)
     _cuda(q, s, offs)
     out = torch.empty((M, K), dtype=torch.bfloat16, device=q.device)
-    check(load().mxfp4_dequantize(_p(q), _p(s), 1, M, K, scale_layout, _p(offs), G, _p(out), _stream(q.device)),
+    check(load().mxfp4_dequantize(_ptr(q), _ptr(s), 1, M, K, scale_layout, _ptr(offs), G, _ptr(out), _raw_stream(q.device.index)),
           "mxfp4_dequantize")
     return out
 
@@ -111,7 +127,7 @@ def mxfp4_dequantize_3d_experts(q: torch.Tensor, s: torch.Tensor,
     _bytes_at_least(s, "s", G * (N * (K // 32) if scale_layout == SCALES_COMPACT else _expert_blocked_bytes(N, K)))
     _cuda(q, s)
     out = torch.empty((G, N, K), dtype=torch.bfloat16, device=q.device)
-    check(load().mxfp4_dequantize(_p(q), _p(s), G, N, K, scale_layout, None, 0, _p(out), _stream(q.device)),
+    check(load().mxfp4_dequantize(_ptr(q), _ptr(s), G, N, K, scale_layout, None, 0, _ptr(out), _raw_stream(q.device.index)),
           "mxfp4_dequantize")
     return out
 
@@ -126,7 +142,7 @@ def mxfp4_grouped_mm_fwd(a_q, a_s, w_q, w_s, offs, out=None, dev_status=None):
     _tensor(w_q, "w_q", torch.uint8, shape=(G, N, K // 2))
     _width(K, "a_q")
     _offsets(offs, G)
-    _bytes_at_least(a_s, "a_s", mxfp8_scale_bytes(M, K, G, SCALES_BLOCKED))
+    _bytes_at_least(a_s, "a_s", _group_bytes(M, K, G))
     _bytes_at_least(w_s, "w_s", G * _expert_blocked_bytes(N, K))
     if out is not None:
         _tensor(out, "out", torch.bfloat16, shape=(M, N))
@@ -134,52 +150,105 @@ def mxfp4_grouped_mm_fwd(a_q, a_s, w_q, w_s, offs, out=None, dev_status=None):
     _cuda(a_q, a_s, w_q, w_s, offs, out, dev_status)
     if out is None:
         out = torch.empty((M, N), dtype=torch.bfloat16, device=a_q.device)
-    check(load().mxfp4_grouped_mm_fwd(_p(a_q), _p(a_s), _p(w_q), _p(w_s), _p(offs), G, M, N, K, _p(out),
-                                      _p(dev_status), _stream(a_q.device)), "mxfp4_grouped_mm_fwd")
+    check(load().mxfp4_grouped_mm_fwd(_ptr(a_q), _ptr(a_s), _ptr(w_q), _ptr(w_s), _ptr(offs), G, M, N, K, _ptr(out),
+                                      _ptr(dev_status), _raw_stream(a_q.device.index)), "mxfp4_grouped_mm_fwd")
     return out
+
+
+def _on_one_device(*ts):
+    for t in ts:
+        if not t.is_cuda:
+            raise ValueError("mxfp4: every tensor must live on a CUDA device")
+        if t.device != ts[0].device:
+            raise ValueError(f"mxfp4: tensors on {ts[0].device} and {t.device}")
+
+
+def _carve(like: torch.Tensor, *sizes: int):
+    """One allocation for several buffers of a call: the tensor that owns it and their addresses, each on a
+    256-byte boundary.  (An allocation costs the host as much as a launch; a step at a small size has few of both.)"""
+    starts, total = [], 0
+    for n in sizes:
+        starts.append(total)
+        total += (n + 255) // 256 * 256
+    buf = like.new_empty(total, dtype=torch.uint8)
+    base = buf.data_ptr()
+    return (buf,) + tuple(base + at for at in starts)
 
 
 class _ToMxfp4ThenScaledGroupedMM(torch.autograd.Function):
     """Forward: A and W quantized to MXFP4 along K, one grouped product.  Backward: both gradients
     on the MXFP8 path, dA = dOut W and dW = dOut^T A with every operand in MXFP8 along its own
     contraction.  Gradients keep 8 bits because E2M1's single mantissa bit rounds away most of what
-    small gradients carry; the forward, which tolerates it best, takes the 4-bit rate."""
+    small gradients carry; the forward, which tolerates it best, takes the 4-bit rate.
+
+    Shapes, types and devices are checked in to_mxfp4_then_scaled_grouped_mm; the calls below go to the
+    library directly."""
 
     @staticmethod
     def forward(ctx, A, W, offs, w_mxfp4, check_offsets):
         need_dA, need_dW = ctx.needs_input_grad[:2]
+        L, stream = load(), _raw_stream(A.device.index)
+        (M, K), (G, N, _) = A.shape, W.shape
         st = None
         if check_offsets:
             st = new_status(A.device)
-            mxfp8_check_offsets(offs, A.shape[0], 32 if need_dW else 1, st)
+            mxfp8_check_offsets(offs, M, 32 if need_dW else 1, st)
+        status, off = _ptr(st), offs.data_ptr()
         A = A.contiguous()
-        aq, as_ = mxfp4_quantize_2d(A, SCALES_BLOCKED, offs)
-        wq, ws = w_mxfp4 if w_mxfp4 is not None else mxfp4_quantize_3d_experts(W.contiguous())
-        out = mxfp4_grouped_mm_fwd(aq, as_, wq, ws, offs, dev_status=st)
-        aTq = aTs = None
-        if need_dW and A.shape[0]:  # the token-wise MXFP8 copy for dW: half the bytes of A itself
-            _, _, aTq, aTs = mxfp8_quantize_2d(A, COL, SCALES_BLOCKED, offs, st)
+        out = A.new_empty((M, N))
+        aT = None
+        if M:
+            a_sizes = (M * (K // 2), _group_bytes(M, K, G))
+            if w_mxfp4 is None:
+                Wc = W.contiguous()
+                _hold, aq, as_, wq, ws = _carve(A, *a_sizes, G * N * (K // 2), G * _expert_blocked_bytes(N, K))
+                check(L.mxfp4_quantize_3d_experts(Wc.data_ptr(), G, N, K, SCALES_BLOCKED, wq, ws, stream),
+                      "mxfp4_quantize_3d_experts")
+            else:
+                _hold, aq, as_ = _carve(A, *a_sizes)
+                wq, ws = w_mxfp4[0].data_ptr(), w_mxfp4[1].data_ptr()
+            check(L.mxfp4_quantize_2d(A.data_ptr(), M, K, SCALES_BLOCKED, off, G, aq, as_, stream), "mxfp4_quantize_2d")
+            check(L.mxfp4_grouped_mm_fwd(aq, as_, wq, ws, off, G, M, N, K, out.data_ptr(), status, stream),
+                  "mxfp4_grouped_mm_fwd")
+            if need_dW:  # the token-wise MXFP8 copy for dW: half the bytes of A itself
+                aT, q, s = _carve(A, K * M, _col_bytes(K, M, G))
+                check(L.mxfp8_quantize_2d(A.data_ptr(), M, K, COL, SCALES_BLOCKED, off, G, None, None, q, s, status,
+                                          stream), "mxfp8_quantize_2d")
         if st is not None:
             read_status(st, "to_mxfp4_then_scaled_grouped_mm (group offsets)")
-        ctx.save_for_backward(aTq, aTs, W if need_dA else None, offs)
-        ctx.shape_W = W.shape
+        ctx.save_for_backward(aT, W if need_dA else None, offs)
+        ctx.sizes = (G, M, N, K)
         return out
 
     @staticmethod
     def backward(ctx, dOut):
-        aTq, aTs, W, offs = ctx.saved_tensors
+        aT, W, offs = ctx.saved_tensors
         need_dA, need_dW = ctx.needs_input_grad[:2]
+        G, M, N, K = ctx.sizes
+        dOut = dOut.contiguous().to(torch.bfloat16)
+        dA = dOut.new_empty((M, K)) if need_dA else None
+        if M == 0:
+            return dA, dOut.new_zeros((G, N, K)) if need_dW else None, None, None, None
+        dW = dOut.new_empty((G, N, K)) if need_dW else None
+        L, stream, off = load(), _raw_stream(dOut.device.index), offs.data_ptr()
+        row = (M * N, _group_bytes(M, N, G), G * K * N, G * _expert_blocked_bytes(K, N)) if need_dA else (0,) * 4
+        col = (N * M, _col_bytes(N, M, G)) if need_dW else (0, 0)
+        _hold, dq, ds, wq, ws, dTq, dTs = _carve(dOut, *row, *col)
         dirs = (ROW if need_dA else 0) | (COL if need_dW else 0)
-        dA = dW = None
-        if dOut.shape[0] == 0:
-            return (dOut.new_empty((0, ctx.shape_W[2])) if need_dA else None,
-                    dOut.new_zeros(ctx.shape_W) if need_dW else None, None, None, None)
-        dq, ds, dTq, dTs = mxfp8_quantize_2d(dOut.contiguous().to(torch.bfloat16), dirs, SCALES_BLOCKED, offs)
+        check(L.mxfp8_quantize_2d(dOut.data_ptr(), M, N, dirs, SCALES_BLOCKED, off, G, dq if need_dA else None,
+                                  ds if need_dA else None, dTq if need_dW else None, dTs if need_dW else None, None,
+                                  stream), "mxfp8_quantize_2d")
         if need_dA:
-            _, _, wTq, wTs = mxfp8_quantize_3d_experts(W.detach().contiguous(), COL)
-            dA = mxfp8_grouped_mm_dgrad(dq, ds, wTq, wTs, offs)
+            W = W.contiguous()
+            check(L.mxfp8_quantize_3d_experts(W.data_ptr(), G, N, K, COL, SCALES_BLOCKED, None, None, wq, ws, None,
+                                              stream), "mxfp8_quantize_3d_experts")
+            check(L.mxfp8_grouped_mm_dgrad(dq, ds, wq, ws, off, G, M, N, K, dA.data_ptr(), None, stream),
+                  "mxfp8_grouped_mm_dgrad")
         if need_dW:
-            dW = mxfp8_grouped_mm_wgrad(dTq, dTs, aTq, aTs, offs)
+            q = aT.data_ptr()
+            s = q + (K * M + 255) // 256 * 256  # as _carve laid them out in the forward
+            check(L.mxfp8_grouped_mm_wgrad(dTq, dTs, q, s, off, G, M, N, K, dW.data_ptr(), None, stream),
+                  "mxfp8_grouped_mm_wgrad")
         return dA, dW, None, None, None
 
 
@@ -199,7 +268,7 @@ def to_mxfp4_then_scaled_grouped_mm(A: torch.Tensor, W: torch.Tensor, offs: torc
         raise ValueError("offs must be int32")
     if A.dim() != 2 or W.dim() != 3 or A.shape[1] != W.shape[2]:
         raise ValueError("to_mxfp4_then_scaled_grouped_mm: A [M, K] and W [G, N, K] expected")
-    G, N, K = W.shape
+    M, (G, N, K) = A.shape[0], W.shape
     _width(K, "A")
     _width(N, "W^T")
     _offsets(offs, G)
@@ -208,4 +277,11 @@ def to_mxfp4_then_scaled_grouped_mm(A: torch.Tensor, W: torch.Tensor, offs: torc
             raise ValueError("w_mxfp4 must be (codes, scales)")
         _tensor(w_mxfp4[0], "w_mxfp4 codes", torch.uint8, shape=(G, N, K // 2))
         _bytes_at_least(w_mxfp4[1], "w_mxfp4 scales", G * _expert_blocked_bytes(N, K))
+    _on_one_device(A, W, offs, *(w_mxfp4 or ()))
+    if w_mxfp4 is not None and not (w_mxfp4[0].is_contiguous() and w_mxfp4[1].is_contiguous()):
+        raise ValueError("w_mxfp4: tensors must be contiguous")
+    if not offs.is_contiguous():
+        raise ValueError("offs: must be contiguous")
+    if M % 32 and W.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"A: a multiple of 32 rows is needed where W needs a gradient, got {M}")
     return _ToMxfp4ThenScaledGroupedMM.apply(A, W, offs, w_mxfp4, bool(check_offsets))
