@@ -38,6 +38,7 @@ struct Q4Params {
     int32_t G;
     int blocked;
     int cols_per_cta;      // column tiles a CTA walks
+    int row_steps;         // of a tile's row steps, how many a CTA takes (blockIdx.z: which)
 };
 
 enum Q4Kind : int { kQ4Plain = 0, kQ4Swiglu = 1, kQ4Dequant = 2 };
@@ -206,8 +207,10 @@ __global__ void __launch_bounds__(kQ4Threads, KIND == kQ4Swiglu ? 6 : 5) mxfp4_q
         const int64_t c = k128 * 128 + (lane % kLanes) * EPT;
         const bool cin = c < C;
         int64_t at = (t.b * p.R + t.row0 + r0) * C + c;  // the thread's first element
+        const int i0 = blockIdx.z * p.row_steps * kRows;
+        at += i0 * C;
 #pragma unroll 1
-        for (int i = 0; i < 32; i += kRows, at += kRows * C) {
+        for (int i = i0; i < i0 + p.row_steps * kRows; i += kRows, at += kRows * C) {
             const int r = r0 + i;
             const bool in = cin && r < t.rows;
             uint32_t w[EPT / 2], g[KIND == kQ4Swiglu ? EPT / 2 : 1], codes[EPT / 8], s;
@@ -261,7 +264,7 @@ __global__ void __launch_bounds__(kQ4Threads, 6) mxfp4_dequantize_kernel(const Q
         if (p.blocked)
             word = *reinterpret_cast<const uint32_t*>(sb + (t.band * ct + k128) * 512 + lane * 16 + quarter * 4);
 #pragma unroll 1
-        for (int b0 = 0; b0 < 16; b0 += 8) {
+        for (int b0 = blockIdx.z * p.row_steps * 8; b0 < (int)(blockIdx.z + 1) * p.row_steps * 8; b0 += 8) {
             uint32_t codes[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -312,7 +315,12 @@ static mxfp8_status_t q4_run(int kind, Q4Params& p, int32_t batch, int scale_lay
     p.cols_per_cta = (int)max64(1, min64(tc, gx * tc / want));
     const int64_t gy = (tc + p.cols_per_cta - 1) / p.cols_per_cta;
     if (gx > INT32_MAX || gy > 65535) return MXFP8_ERR_SHAPE;
-    const dim3 grid((unsigned)gx, (unsigned)gy);
+    // few tiles: their row steps (a load's latency each) go to CTAs of their own
+    const int steps = kind == kQ4Plain ? 4 : kind == kQ4Swiglu ? 8 : 2;
+    int split = 1;
+    while (split < steps && gx * gy * split * 2 <= 4 * (int64_t)host::num_sms()) split *= 2;
+    p.row_steps = steps / split;
+    const dim3 grid((unsigned)gx, (unsigned)gy, (unsigned)split);
     if (kind == kQ4Plain) mxfp4_quantize_kernel<kQ4Plain><<<grid, kQ4Threads, 0, st>>>(p);
     else if (kind == kQ4Swiglu) mxfp4_quantize_kernel<kQ4Swiglu><<<grid, kQ4Threads, 0, st>>>(p);
     else mxfp4_dequantize_kernel<<<grid, kQ4Threads, 0, st>>>(p);

@@ -12,7 +12,7 @@ from __future__ import annotations
 import torch
 
 from . import (COL, ROW, SCALES_BLOCKED, SCALES_COMPACT, _bytes_at_least, _cuda, _expert_blocked_bytes, _offsets,
-               _status_word, _tensor, check, load, mxfp8_check_offsets, new_status, read_status)
+               _status_word, _tensor, _u8, check, load, mxfp8_check_offsets, new_status, read_status)
 
 # torch's handle of a device's current stream as an integer: a few tenths of a microsecond, where
 # torch.cuda.current_stream() builds an object in several
@@ -36,10 +36,10 @@ def _col_bytes(R: int, M: int, G: int) -> int:
 
 def _row_scales(x: torch.Tensor, M: int, K: int, G: int, layout: int):
     if layout == SCALES_COMPACT:
-        return x.new_empty((M, K // 32), dtype=torch.uint8)
+        return _u8((M, K // 32), x.device)
     if layout != SCALES_BLOCKED:
         raise ValueError("scale_layout: SCALES_COMPACT or SCALES_BLOCKED expected")
-    return x.new_empty(_group_bytes(M, K, G), dtype=torch.uint8)
+    return _u8(_group_bytes(M, K, G), x.device)
 
 
 def _ptr(t):
@@ -57,7 +57,7 @@ def mxfp4_quantize_2d(x: torch.Tensor, scale_layout: int = SCALES_BLOCKED, offs:
         _offsets(offs)
     _cuda(x, offs)
     G = int(offs.numel()) if offs is not None else 1
-    q, s = x.new_empty((M, K // 2), dtype=torch.uint8), _row_scales(x, M, K, G, scale_layout)
+    q, s = _u8((M, K // 2), x.device), _row_scales(x, M, K, G, scale_layout)
     check(load().mxfp4_quantize_2d(_ptr(x), M, K, scale_layout, _ptr(offs), G, _ptr(q), _ptr(s), _raw_stream(x.device.index)),
           "mxfp4_quantize_2d")
     return q, s
@@ -75,7 +75,7 @@ def mxfp4_swiglu_quantize(h1: torch.Tensor, h3: torch.Tensor, scale_layout: int 
         _offsets(offs)
     _cuda(h1, h3, offs)
     G = int(offs.numel()) if offs is not None else 1
-    q, s = h1.new_empty((M, K // 2), dtype=torch.uint8), _row_scales(h1, M, K, G, scale_layout)
+    q, s = _u8((M, K // 2), h1.device), _row_scales(h1, M, K, G, scale_layout)
     check(load().mxfp4_swiglu_quantize(_ptr(h1), _ptr(h3), M, K, scale_layout, _ptr(offs), G, _ptr(q), _ptr(s),
                                        _raw_stream(h1.device.index)), "mxfp4_swiglu_quantize")
     return q, s
@@ -88,11 +88,11 @@ def mxfp4_quantize_3d_experts(w: torch.Tensor, scale_layout: int = SCALES_BLOCKE
     G, N, K = w.shape
     _width(K, "w")
     _cuda(w)
-    q = w.new_empty((G, N, K // 2), dtype=torch.uint8)
+    q = _u8((G, N, K // 2), w.device)
     if scale_layout == SCALES_COMPACT:
-        s = w.new_empty((G, N, K // 32), dtype=torch.uint8)
+        s = _u8((G, N, K // 32), w.device)
     else:
-        s = w.new_empty((G, _expert_blocked_bytes(N, K)), dtype=torch.uint8)
+        s = _u8((G, _expert_blocked_bytes(N, K)), w.device)
     check(load().mxfp4_quantize_3d_experts(_ptr(w), G, N, K, scale_layout, _ptr(q), _ptr(s), _raw_stream(w.device.index)),
           "mxfp4_quantize_3d_experts")
     return q, s
@@ -170,7 +170,7 @@ def _carve(like: torch.Tensor, *sizes: int):
     for n in sizes:
         starts.append(total)
         total += (n + 255) // 256 * 256
-    buf = like.new_empty(total, dtype=torch.uint8)
+    buf = _u8(total, like.device)
     base = buf.data_ptr()
     return (buf,) + tuple(base + at for at in starts)
 
@@ -195,7 +195,7 @@ class _ToMxfp4ThenScaledGroupedMM(torch.autograd.Function):
             mxfp8_check_offsets(offs, M, 32 if need_dW else 1, st)
         status, off = _ptr(st), offs.data_ptr()
         A = A.contiguous()
-        out = A.new_empty((M, N))
+        out = torch.empty((M, N), dtype=torch.bfloat16, device=A.device)
         aT = None
         if M:
             a_sizes = (M * (K // 2), _group_bytes(M, K, G))
@@ -226,10 +226,10 @@ class _ToMxfp4ThenScaledGroupedMM(torch.autograd.Function):
         need_dA, need_dW = ctx.needs_input_grad[:2]
         G, M, N, K = ctx.sizes
         dOut = dOut.contiguous().to(torch.bfloat16)
-        dA = dOut.new_empty((M, K)) if need_dA else None
+        dA = torch.empty((M, K), dtype=torch.bfloat16, device=dOut.device) if need_dA else None
         if M == 0:
             return dA, dOut.new_zeros((G, N, K)) if need_dW else None, None, None, None
-        dW = dOut.new_empty((G, N, K)) if need_dW else None
+        dW = torch.empty((G, N, K), dtype=torch.bfloat16, device=dOut.device) if need_dW else None
         L, stream, off = load(), _raw_stream(dOut.device.index), offs.data_ptr()
         row = (M * N, _group_bytes(M, N, G), G * K * N, G * _expert_blocked_bytes(K, N)) if need_dA else (0,) * 4
         col = (N * M, _col_bytes(N, M, G)) if need_dW else (0, 0)
