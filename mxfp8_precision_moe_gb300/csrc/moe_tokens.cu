@@ -26,19 +26,13 @@
 //   warps 4-11  quantize this CTA's share of x; then the epilogues
 // Every wait is bounded by time (MXFP8_ERR_TIMEOUT and an orderly exit).
 
-#include "host_common.h"
-#include "mx4.cuh"
+#include "moe_tokens.cuh"
 
 namespace mx {
 
-constexpr int kMtMaxTokens = 64;
-constexpr int kMtMaxExperts = 256;
-constexpr int kMtMaxTopK = 16;
 constexpr int kMtThreads = 384;
 constexpr int kMtEpiWarp0 = 4;
 constexpr int kMtEpiThreads = 256;
-constexpr int kMtRouteThreads = 128;
-constexpr int kMtHeader = 256;  // workspace bytes before the tile counters
 constexpr int kMtStatic = 10 * 1024;  // static shared memory at most
 
 template <int BITS, int N>
@@ -58,31 +52,6 @@ struct MtCfg {
     static_assert(kSfCol0 + kStages * kSfCols <= 512, "tensor memory overflow");
 };
 
-// Words of the workspace's header: CTAs that have arrived at each grid-wide point.  One word each: a CTA does not
-// wait at a point that it has no use for, so arrivals at different points mix.
-enum MtPoint : int { kMtXDone = 0, kMtHDone = 1, kMtSumsDone = 2, kMtExits = 3 };
-
-struct MtParams {
-    const uint8_t* x;        // bf16 [T][D]
-    const float* logits;     // [T][E]
-    const uint8_t* s_gate;   // blocked scales, per expert
-    const uint8_t* s_up;
-    const uint8_t* s_down;
-    uint8_t* xq;             // workspace: codes [T][D], scales [ct(D)][512]
-    uint8_t* xs;
-    uint8_t* hq;             // codes [active][T][H], scales [active][ct(H)][512]
-    uint8_t* hs;
-    float* part;             // [CTA][2][2][T][128] partial sums
-    uint32_t* header;        // arrivals at the grid-wide points (MtPoint)
-    uint32_t* counters;      // arrivals per tile: first half, then second half
-    __nv_bfloat16* y;        // [T][D]
-    int32_t* dev_status;
-    uint64_t timeout_ns;
-    int64_t D, H;
-    int T, E, top_k, score;
-    int ncounters;
-};
-
 __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
@@ -99,8 +68,6 @@ __device__ __forceinline__ uint32_t tmem_ld_col(uint32_t taddr) {
 }
 __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[16]) { tmem_ld_32x32b_x16(taddr, r); }
 __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[32]) { tmem_ld_32x32b_x32(taddr, r); }
-
-__device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
 
 __device__ __forceinline__ void epi_sync() {
     __syncwarp();
@@ -121,8 +88,6 @@ __device__ __forceinline__ bool epi_all(bool yes) {
 // The epilogue warps wait here for the routing tables; the other four warps only arrive.
 __device__ __forceinline__ void routed_arrive() { asm volatile("bar.arrive 3, 384;" ::: "memory"); }
 __device__ __forceinline__ void routed_wait() { asm volatile("bar.sync 3, 384;" ::: "memory"); }
-__device__ __forceinline__ void route_sync() { asm volatile("bar.sync 2, 128;" ::: "memory"); }
-
 // v = *p where `yes`, past L1; a predicate and not a branch, so that many are in flight.
 __device__ __forceinline__ void ld_if(float& v, const float* p, bool yes) {
     asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %2, 0;\n\t@q ld.global.cg.f32 %0, [%1];\n\t}"
@@ -134,12 +99,6 @@ __device__ __forceinline__ void ld_if(float4& v, const float* p, bool yes) {
     asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %5, 0;\n\t@q ld.global.cg.v4.f32 {%0, %1, %2, %3}, [%4];\n\t}"
                  : "+f"(v.x), "+f"(v.y), "+f"(v.z), "+f"(v.w)
                  : "l"(p), "r"((uint32_t)yes));
-}
-
-__device__ __forceinline__ uint32_t ld_acquire(const uint32_t* p) {
-    uint32_t v;
-    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
-    return v;
 }
 
 constexpr uint32_t kMtWholeSteps = 6;
@@ -175,18 +134,13 @@ __global__ void __launch_bounds__(kMtThreads, 1)
     using C = MtCfg<BITS, N>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t full[C::kStages], empty[C::kStages], tfull[2], tempty[2], drain;
-    __shared__ uint32_t mask_s[kMtMaxExperts][2];              // tokens of each active expert, a bit each
-    __shared__ uint16_t list_s[kMtMaxExperts];                 // active experts, ascending
-    __shared__ uint32_t active_s[kMtMaxExperts / 32];
-    __shared__ uint16_t sel_e[kMtMaxTokens * kMtMaxTopK];      // a token's experts, best first (0xFFFF: none)
-    __shared__ float sel_w[kMtMaxTokens * kMtMaxTopK];         // their logits, then their weights
+    __shared__ MtRoute route;
     __shared__ float w_s[2][kMtMaxTokens];
-    __shared__ int nactive_s;
     __shared__ uint32_t tmem_base_s, last_s;
     __shared__ int abort_s;
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-    const int T = p.T, E = p.E;
+    const int T = p.T;
     volatile int* abort_flag = &abort_s;
 
     const int64_t D = p.D, H = p.H;
@@ -242,95 +196,31 @@ __global__ void __launch_bounds__(kMtThreads, 1)
         routed_wait();
     } else {
         // ------------------------------------------------ routing (every CTA, the same), barriers
-        uint32_t* keys = reinterpret_cast<uint32_t*>(smem);  // [T][E], before the first stage is filled
-        for (int i0 = tid; i0 < T * E; i0 += 8 * kMtRouteThreads) {
-            uint32_t b[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int i = i0 + j * kMtRouteThreads;
-                b[j] = i < T * E ? __float_as_uint(p.logits[i]) : 0u;
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int i = i0 + j * kMtRouteThreads;
-                // unsigned keys that order as the logits do: NaN above everything, -0 equal to +0
-                uint32_t k = (b[j] & 0x80000000u) ? ~b[j] : b[j] | 0x80000000u;
-                if ((b[j] & 0x7FFFFFFFu) > 0x7F800000u) k = 0xFFFFFFFFu;
-                if (b[j] == 0x80000000u) k = 0x80000000u;
-                if (i < T * E) keys[i] = k;
-            }
-        }
-        for (int i = tid; i < T * p.top_k; i += kMtRouteThreads) sel_e[i] = 0xFFFFu;
-        if (tid < kMtMaxExperts / 32) active_s[tid] = 0;
-        for (int i = tid; i < 2 * kMtMaxExperts; i += kMtRouteThreads) mask_s[i >> 1][i & 1] = 0;
-        if (warp == 2) {
-            if (lane == 0) {
-                for (int s = 0; s < C::kStages; ++s) {
-                    mbar_init(&full[s], 2);  // the weight and the token producer
-                    mbar_init(&empty[s], 1);
+        mt_route(p, reinterpret_cast<uint32_t*>(smem), route, tid, [&] {  // the keys, before the first stage is filled
+            if (warp == 2) {
+                if (lane == 0) {
+                    for (int s = 0; s < C::kStages; ++s) {
+                        mbar_init(&full[s], 2);  // the weight and the token producer
+                        mbar_init(&empty[s], 1);
+                    }
+                    for (int b = 0; b < 2; ++b) {
+                        mbar_init(&tfull[b], 1);
+                        mbar_init(&tempty[b], kMtEpiThreads / 32);
+                    }
+                    mbar_init(&drain, 1);
+                    abort_s = 0;
+                    fence_barrier_init();
+                    prefetch_tmap(&map_gate);
+                    prefetch_tmap(&map_up);
+                    prefetch_tmap(&map_down);
+                    prefetch_tmap(&map_x);
+                    prefetch_tmap(&map_h);
                 }
-                for (int b = 0; b < 2; ++b) {
-                    mbar_init(&tfull[b], 1);
-                    mbar_init(&tempty[b], kMtEpiThreads / 32);
-                }
-                mbar_init(&drain, 1);
-                abort_s = 0;
-                fence_barrier_init();
-                prefetch_tmap(&map_gate);
-                prefetch_tmap(&map_up);
-                prefetch_tmap(&map_down);
-                prefetch_tmap(&map_x);
-                prefetch_tmap(&map_h);
+                __syncwarp();
+                tmem_alloc(&tmem_base_s, 512);
+                tmem_relinquish();
             }
-            __syncwarp();
-            tmem_alloc(&tmem_base_s, 512);
-            tmem_relinquish();
-        }
-        route_sync();
-        for (int i = tid; i < T * E; i += kMtRouteThreads) {
-            const int t = i / E, e = i - t * E;
-            const uint32_t k = keys[i];
-            const uint32_t* row = keys + t * E;
-            int rank = 0;  // logits before this one: larger, or equal at a lower index
-#pragma unroll 8
-            for (int o = 0; o < E; ++o) rank += (row[o] > k) || (row[o] == k && o < e);
-            if (rank < p.top_k && k != 0x007FFFFFu) {  // -inf is never selected
-                sel_e[t * p.top_k + rank] = (uint16_t)e;
-                sel_w[t * p.top_k + rank] = __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k);  // the logit again
-                atomicOr(&active_s[e >> 5], 1u << (e & 31));
-            }
-        }
-        route_sync();
-        if (tid < T) {
-            const uint16_t* se = sel_e + tid * p.top_k;
-            float* sw = sel_w + tid * p.top_k;
-            if (p.score == MX_SCORE_SIGMOID) {
-                for (int j = 0; j < p.top_k && se[j] != 0xFFFFu; ++j) sw[j] = 1.0f / (1.0f + expf(-sw[j]));
-            } else {
-                const float m = se[0] != 0xFFFFu ? sw[0] : 0.0f;  // the largest logit
-                float sum = 0.0f;
-                if (p.score == MX_SCORE_SOFTMAX) {
-                    for (int j = 0; j < p.top_k && se[j] != 0xFFFFu; ++j) sum += expf(sw[j] - m);
-                } else {
-                    for (int e = 0; e < E; ++e) sum += expf(p.logits[tid * E + e] - m);
-                }
-                for (int j = 0; j < p.top_k && se[j] != 0xFFFFu; ++j) sw[j] = expf(sw[j] - m) / sum;
-            }
-        }
-        for (int i = tid; i < T * p.top_k; i += kMtRouteThreads) {
-            const int e = sel_e[i];
-            if (e == 0xFFFF) continue;
-            int a = __popc(active_s[e >> 5] & ((1u << (e & 31)) - 1u));  // the expert's place among the active
-            for (int w = 0; w < (e >> 5); ++w) a += __popc(active_s[w]);
-            const int t = i / p.top_k;
-            list_s[a] = (uint16_t)e;
-            atomicOr(&mask_s[a][t >> 5], 1u << (t & 31));
-        }
-        if (tid == 0) {
-            int n = 0;
-            for (int w = 0; w < kMtMaxExperts / 32; ++w) n += __popc(active_s[w]);
-            nactive_s = n;
-        }
+        });
         fence_proxy_async();  // the keys' shared memory is TMA's from here on
         tc_fence_before();
         route_sync();
@@ -338,8 +228,8 @@ __global__ void __launch_bounds__(kMtThreads, 1)
     }
     tc_fence_after();
     const uint32_t tmem = tmem_base_s;
-    const int A = __shfl_sync(0xffffffffu, nactive_s, 0);
-    auto mask_of = [&](uint32_t a) -> uint64_t { return mask_s[a][0] | ((uint64_t)mask_s[a][1] << 32); };
+    const int A = __shfl_sync(0xffffffffu, route.active_n, 0);
+    auto mask_of = [&](uint32_t a) -> uint64_t { return route.mask[a][0] | ((uint64_t)route.mask[a][1] << 32); };
 
     const uint32_t ct_d = (uint32_t)((D + 127) / 128), ct_h = (uint32_t)((H + 127) / 128);
     const uint32_t K1 = (uint32_t)((D + C::kKE - 1) / C::kKE), K2 = (uint32_t)((H + C::kKE - 1) / C::kKE);
@@ -349,20 +239,7 @@ __global__ void __launch_bounds__(kMtThreads, 1)
     const uint32_t u1_0 = cta < sp1.n ? sp1.start(cta) : 0, u1_1 = cta < sp1.n ? sp1.start(cta + 1) : 0;
     const uint32_t u2_0 = cta < sp2.n ? sp2.start(cta) : 0, u2_1 = cta < sp2.n ? sp2.start(cta + 1) : 0;
 
-    // every CTA's arrivals at a grid-wide point, from one thread
-    auto grid_wait = [&](int point) -> bool {
-        const uint64_t t0 = globaltimer_ns();
-        while (ld_acquire(p.header + point) < gridDim.x) {
-            if (*abort_flag) return false;
-            if (globaltimer_ns() - t0 > p.timeout_ns) {
-                *abort_flag = 1;
-                report(p.dev_status, MXFP8_ERR_TIMEOUT);
-                return false;
-            }
-        }
-        fence_proxy_async();  // what the other CTAs wrote, before TMA reads it
-        return true;
-    };
+    auto grid_wait = [&](int point) -> bool { return mt_grid_wait(p, point, abort_flag); };
 
     if (A == 0) {
         for (int64_t i = (int64_t)cta * kMtThreads + tid; i < T * D; i += (int64_t)gridDim.x * kMtThreads)
@@ -382,7 +259,7 @@ __global__ void __launch_bounds__(kMtThreads, 1)
                 bool first;
             };
             auto settle = [&](Place& q) {  // rows, scales of (a, j) from step k on
-                const uint32_t e = list_s[q.a];
+                const uint32_t e = route.list[q.a];
                 if (q.first) {
                     const int64_t so = (((int64_t)e * ct_h + q.j) * ct_d + q.k * C::kSfTiles) * 512;
                     q.row0 = q.row1 = (int32_t)((int64_t)e * H + q.j * 128);
@@ -768,10 +645,10 @@ __global__ void __launch_bounds__(kMtThreads, 1)
             for (; u < t_end; ++a) {
                 u = min(t_end, tile * AK2 + (a + 1) * K2);
                 if (et < T) {  // token et's weight for this expert
-                    const int e = list_s[a];
+                    const int e = route.list[a];
                     float w = 0.0f;
                     for (int j = 0; j < p.top_k; ++j)
-                        if (sel_e[et * p.top_k + j] == e) w = sel_w[et * p.top_k + j];
+                        if (route.sel_e[et * p.top_k + j] == e) w = route.sel_w[et * p.top_k + j];
                     w_s[buf][et] = w;
                 }
                 ok = epi_all(mbar_wait_bounded<true>(&tfull[buf], buf_phase, p.timeout_ns, abort_flag, p.dev_status));
@@ -871,14 +748,7 @@ __global__ void __launch_bounds__(kMtThreads, 1)
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
-    if (tid == 0) {
-        // the last CTA to leave puts the arrivals back to zero for the next launch
-        __threadfence();
-        if (atomicAdd(p.header + kMtExits, 1u) + 1u == gridDim.x) {
-            for (int i = 0; i <= kMtExits; ++i) p.header[i] = 0u;
-            __threadfence();
-        }
-    }
+    if (tid == 0) mt_leave(p);
 }
 
 // ---------------------------------------------------------------- host side
@@ -979,14 +849,12 @@ extern "C" mxfp8_status_t mx_moe_tokens(const void* x_bf16, const float* router_
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     const int N = T <= 16 ? 16 : T <= 32 ? 32 : 64;
     const int64_t Db = D * bits / 8, Hb = H * bits / 8;
-    CUtensorMap m[5];
-    if (!mt_map(&m[0], gate_q, Db, (int64_t)E * H, 0, 128) || !mt_map(&m[1], up_q, Db, (int64_t)E * H, 0, 128) ||
-        !mt_map(&m[2], down_q, Hb, (int64_t)E * D, 0, 128) || !mt_map(&m[3], ws + l.xq, Db, T, 1, N) ||
-        !mt_map(&m[4], ws + l.hq, Hb, T, std::min<int64_t>(E, (int64_t)T * top_k), N))
-        return MXFP8_ERR_DRIVER;
     MtParams p{};
     p.x = static_cast<const uint8_t*>(x_bf16);
     p.logits = router_logits;
+    p.q_gate = static_cast<const uint8_t*>(gate_q);
+    p.q_up = static_cast<const uint8_t*>(up_q);
+    p.q_down = static_cast<const uint8_t*>(down_q);
     p.s_gate = static_cast<const uint8_t*>(gate_s);
     p.s_up = static_cast<const uint8_t*>(up_s);
     p.s_down = static_cast<const uint8_t*>(down_s);
@@ -1008,6 +876,12 @@ extern "C" mxfp8_status_t mx_moe_tokens(const void* x_bf16, const float* router_
     p.score = score;
     p.ncounters = (int)l.ncounters;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (mt_rows_takes(p, bits)) return mt_rows_launch(p, bits, st);
+    CUtensorMap m[5];
+    if (!mt_map(&m[0], gate_q, Db, (int64_t)E * H, 0, 128) || !mt_map(&m[1], up_q, Db, (int64_t)E * H, 0, 128) ||
+        !mt_map(&m[2], down_q, Hb, (int64_t)E * D, 0, 128) || !mt_map(&m[3], ws + l.xq, Db, T, 1, N) ||
+        !mt_map(&m[4], ws + l.hq, Hb, T, std::min<int64_t>(E, (int64_t)T * top_k), N))
+        return MXFP8_ERR_DRIVER;
     if (bits == 8)
         return N == 16 ? mt_launch<8, 16>(m, p, st) : N == 32 ? mt_launch<8, 32>(m, p, st) : mt_launch<8, 64>(m, p, st);
     return N == 16 ? mt_launch<4, 16>(m, p, st) : N == 32 ? mt_launch<4, 32>(m, p, st) : mt_launch<4, 64>(m, p, st);
