@@ -21,8 +21,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libmxfp8moe.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
-SOURCES = ["api.cu", "quantize.cu", "grouped_mm.cu", "mxfp4_quantize.cu", "mxfp4_mm.cu", "moe_tokens.cu",
-           "moe_token_rows.cu"]
+SOURCES = ["api.cu", "quantize.cu", "grouped_mm.cu", "mxfp4_quantize.cu", "mxfp4_mm.cu", "moe_tokens.cu"]
 
 
 def nvcc() -> str:

@@ -8,16 +8,17 @@
 // choice serves that stream.  One cooperative launch, one CTA per SM, weights through TMA into a ring of
 // stages that never drains: the same ring runs through both halves of the layer, and the down weights are
 // on their way while the last gate/up tiles finish.  Weights are the tensor cores' 128-row operand,
-// tokens the narrow one (N = 32 or 64 columns): every token is multiplied with every selected expert, which
-// costs no bandwidth and no gather, and a routing mask decides which columns are used -- so a NaN in an
+// tokens the narrow one (N = 16, 32 or 64 columns): every token is multiplied with every selected expert,
+// which costs no bandwidth and no gather, and a routing mask decides which columns are used -- so a NaN in an
 // expert's weights reaches only the tokens routed to it.
 //
-// A unit of work is one 128-byte step along the contraction of two 128-row weight tiles (32 KB):
-//   first half   tile = 128 rows of one expert's gate and up matrices; steps along D
-//   second half  tile = 256 rows of D; steps along every selected expert's H in turn
-// Each half's units, in order, are cut into equal runs, one per CTA, so the load is even however few experts
-// or tiles there are.  A run that ends inside a tile leaves fp32 partial sums in the workspace; the CTA
-// that arrives last at a tile adds them in the order of their runs (the result does not depend on arrival).
+// A unit of work is a stage of two weight tiles of 128 or 64 rows and 128 bytes of the contraction (32 or 16 KB):
+//   first half   tile = 128 or 64 rows of one expert's gate and up matrices; units of one step along D
+//   second half  tile = 128 or 64 rows of D; units of two steps, along every selected expert's H in turn
+// Each half is cut into runs, one a CTA, in the way that should take least time (mt_split): whole tiles of 128
+// or 64 rows, or equal runs of units that end anywhere.  A run that ends inside a tile leaves fp32 partial sums
+// in the workspace.  In the first half the CTA that arrives last at a tile adds them, in the second all CTAs do
+// after a grid-wide point; both in the order of the runs, so that the result does not depend on arrival.
 //
 //   warp 0      weight producer (TMA tiles and their scale tiles); waits for nothing but free stages
 //   warp 1      token producer (quantized x or h and their scales); waits at the two grid-wide points:
@@ -26,30 +27,180 @@
 //   warps 4-11  quantize this CTA's share of x; then the epilogues
 // Every wait is bounded by time (MXFP8_ERR_TIMEOUT and an orderly exit).
 
-#include "moe_tokens.cuh"
+#include "host_common.h"
+#include "mx4.cuh"
 
 namespace mx {
+
+constexpr int kMtMaxTokens = 64;
+constexpr int kMtMaxExperts = 256;
+constexpr int kMtMaxTopK = 16;
+constexpr int kMtRouteThreads = 128;
+constexpr int kMtHeader = 256;  // workspace bytes before the tile counters
+
+// Words of the workspace's header: CTAs that have arrived at each grid-wide point.  One word each: a CTA does not
+// wait at a point that it has no use for, so arrivals at different points mix.
+enum MtPoint : int { kMtXDone = 0, kMtHDone = 1, kMtSumsDone = 2, kMtExits = 3 };
+
+struct MtParams {
+    const uint8_t* x;        // bf16 [T][D]
+    const float* logits;     // [T][E]
+    const uint8_t* s_gate;   // blocked scales, per expert
+    const uint8_t* s_up;
+    const uint8_t* s_down;
+    uint8_t* xq;             // workspace: codes [T][D], scales [ct(D)][512]
+    uint8_t* xs;
+    uint8_t* hq;             // codes [active][T][H], scales [active][ct(H)][512]
+    uint8_t* hs;
+    float* part;             // [CTA][2][2][T][128] partial sums
+    uint32_t* header;        // arrivals at the grid-wide points (MtPoint)
+    uint32_t* counters;      // arrivals per shared tile of the first half
+    __nv_bfloat16* y;        // [T][D]
+    int32_t* dev_status;
+    uint64_t timeout_ns;
+    int64_t D, H;
+    int T, E, top_k, score;
+    int ncounters;
+};
+
+__device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
+
+__device__ __forceinline__ uint32_t ld_acquire(const uint32_t* p) {
+    uint32_t v;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+
+// The routing tables, in shared memory.
+struct MtRoute {
+    uint32_t mask[kMtMaxExperts][2];            // tokens of each active expert, a bit each
+    uint32_t active[kMtMaxExperts / 32];        // experts that some token selected
+    float sel_w[kMtMaxTokens * kMtMaxTopK];     // the selected experts' logits, then their weights
+    uint16_t sel_e[kMtMaxTokens * kMtMaxTopK];  // a token's experts [T][top_k], best first (0xFFFF: none)
+    uint16_t list[kMtMaxExperts];               // active experts, ascending
+    int active_n;
+};
+
+__device__ __forceinline__ void route_sync() { asm volatile("bar.sync 2, 128;" ::: "memory"); }
+
+// Top-k of every token and the list of active experts, by threads 0 .. 127 of a CTA (barrier 2); the caller
+// orders what they wrote before anyone reads it.  keys: [T][E] words of scratch memory.  setup() runs while the
+// logits are on their way.
+template <class Setup>
+__device__ __forceinline__ void mt_route(const MtParams& p, uint32_t* keys, MtRoute& r, int tid, Setup setup) {
+    const int T = p.T, E = p.E;
+    for (int i0 = tid; i0 < T * E; i0 += 8 * kMtRouteThreads) {
+        uint32_t b[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int i = i0 + j * kMtRouteThreads;
+            b[j] = i < T * E ? __float_as_uint(p.logits[i]) : 0u;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int i = i0 + j * kMtRouteThreads;
+            // unsigned keys that order as the logits do: NaN above everything, -0 equal to +0
+            uint32_t k = (b[j] & 0x80000000u) ? ~b[j] : b[j] | 0x80000000u;
+            if ((b[j] & 0x7FFFFFFFu) > 0x7F800000u) k = 0xFFFFFFFFu;
+            if (b[j] == 0x80000000u) k = 0x80000000u;
+            if (i < T * E) keys[i] = k;
+        }
+    }
+    for (int i = tid; i < T * p.top_k; i += kMtRouteThreads) r.sel_e[i] = 0xFFFFu;
+    if (tid < kMtMaxExperts / 32) r.active[tid] = 0;
+    for (int i = tid; i < 2 * kMtMaxExperts; i += kMtRouteThreads) r.mask[i >> 1][i & 1] = 0;
+    setup();
+    route_sync();
+    for (int i = tid; i < T * E; i += kMtRouteThreads) {
+        const int t = i / E, e = i - t * E;
+        const uint32_t k = keys[i];
+        const uint32_t* row = keys + t * E;
+        int rank = 0;  // logits before this one: larger, or equal at a lower index
+#pragma unroll 8
+        for (int o = 0; o < E; ++o) rank += (row[o] > k) || (row[o] == k && o < e);
+        if (rank < p.top_k && k != 0x007FFFFFu) {  // -inf is never selected
+            r.sel_e[t * p.top_k + rank] = (uint16_t)e;
+            r.sel_w[t * p.top_k + rank] = __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k);  // the logit again
+            atomicOr(&r.active[e >> 5], 1u << (e & 31));
+        }
+    }
+    route_sync();
+    if (tid < T) {
+        const uint16_t* se = r.sel_e + tid * p.top_k;
+        float* sw = r.sel_w + tid * p.top_k;
+        if (p.score == MX_SCORE_SIGMOID) {
+            for (int j = 0; j < p.top_k && se[j] != 0xFFFFu; ++j) sw[j] = 1.0f / (1.0f + expf(-sw[j]));
+        } else {
+            const float m = se[0] != 0xFFFFu ? sw[0] : 0.0f;  // the largest logit
+            float sum = 0.0f;
+            if (p.score == MX_SCORE_SOFTMAX) {
+                for (int j = 0; j < p.top_k && se[j] != 0xFFFFu; ++j) sum += expf(sw[j] - m);
+            } else {
+                for (int e = 0; e < E; ++e) sum += expf(p.logits[tid * E + e] - m);
+            }
+            for (int j = 0; j < p.top_k && se[j] != 0xFFFFu; ++j) sw[j] = expf(sw[j] - m) / sum;
+        }
+    }
+    for (int i = tid; i < T * p.top_k; i += kMtRouteThreads) {
+        const int e = r.sel_e[i];
+        if (e == 0xFFFF) continue;
+        int a = __popc(r.active[e >> 5] & ((1u << (e & 31)) - 1u));  // the expert's place among the active
+        for (int w = 0; w < (e >> 5); ++w) a += __popc(r.active[w]);
+        const int t = i / p.top_k;
+        r.list[a] = (uint16_t)e;
+        atomicOr(&r.mask[a][t >> 5], 1u << (t & 31));
+    }
+    if (tid == 0) {
+        int n = 0;
+        for (int w = 0; w < kMtMaxExperts / 32; ++w) n += __popc(r.active[w]);
+        r.active_n = n;
+    }
+}
+
+// Whether every CTA has arrived at a grid-wide point; for one thread.
+__device__ __forceinline__ bool mt_grid_wait(const MtParams& p, int point, volatile int* abort_flag) {
+    const uint64_t t0 = globaltimer_ns();
+    while (ld_acquire(p.header + point) < gridDim.x) {
+        if (*abort_flag) return false;
+        if (globaltimer_ns() - t0 > p.timeout_ns) {
+            *abort_flag = 1;
+            report(p.dev_status, MXFP8_ERR_TIMEOUT);
+            return false;
+        }
+    }
+    fence_proxy_async();  // what the other CTAs wrote, before TMA reads it
+    return true;
+}
+
+// The last CTA to leave puts the arrivals back to zero for the next launch; for one thread of a CTA.
+__device__ __forceinline__ void mt_leave(const MtParams& p) {
+    __threadfence();
+    if (atomicAdd(p.header + kMtExits, 1u) + 1u == gridDim.x) {
+        for (int i = 0; i <= kMtExits; ++i) p.header[i] = 0u;
+        __threadfence();
+    }
+}
 
 constexpr int kMtThreads = 384;
 constexpr int kMtEpiWarp0 = 4;
 constexpr int kMtEpiThreads = 256;
 constexpr int kMtStatic = 10 * 1024;  // static shared memory at most
 
+constexpr int kMtStages = 10;  // at most
+
 template <int BITS, int N>
 struct MtCfg {
     static constexpr int kKE = BITS == 8 ? 128 : 256;   // contraction elements of a step (128 bytes)
     static constexpr int kSfTiles = kKE / 128;          // 512-byte scale tiles of a step
-    static constexpr int kOffSfA = 2 * 128 * 128;       // within a stage: two weight tiles, ...
-    static constexpr int kOffB = kOffSfA + 2 * kSfTiles * 512;
-    static constexpr int kOffSfB = kOffB + N * 128;
-    static constexpr int kStage = (kOffSfB + kSfTiles * 512 + 1023) / 1024 * 1024;
-    static constexpr int kSfCols = 3 * 4 * kSfTiles;    // tensor-memory columns of a stage's scales
+    static constexpr int kSfCols = 16 * kSfTiles;       // tensor-memory columns of a stage's scales
     static constexpr int kSfCol0 = 4 * N;               // after two buffers of two accumulators
-    static constexpr int kStages = (227 * 1024 - kMtStatic - 1024) / kStage;
-    static constexpr int kSmem = kStages * kStage + 1024;
-    static_assert(kStages >= 5, "too few stages to cover HBM's latency");
-    static_assert(kOffB % 1024 == 0, "swizzled tiles start on 1024-byte boundaries");
-    static_assert(kSfCol0 + kStages * kSfCols <= 512, "tensor memory overflow");
+    static constexpr int kSmem = 227 * 1024 - kMtStatic;
+    static_assert(kSfCol0 + 4 * kSfCols <= 512, "tensor memory overflow");
+};
+
+// The tensor maps, by rows of a box: 128 and 64.
+struct MtMaps {
+    CUtensorMap gate[2], up[2], down[2], x, h;
 };
 
 __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
@@ -65,6 +216,11 @@ __device__ __forceinline__ uint32_t tmem_ld_col(uint32_t taddr) {
     uint32_t r;
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr));
     return r;
+}
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
 }
 __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[16]) { tmem_ld_32x32b_x16(taddr, r); }
 __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[32]) { tmem_ld_32x32b_x32(taddr, r); }
@@ -101,39 +257,57 @@ __device__ __forceinline__ void ld_if(float4& v, const float* p, bool yes) {
                  : "l"(p), "r"((uint32_t)yes));
 }
 
-constexpr uint32_t kMtWholeSteps = 6;
-
-// One half's units cut into n equal runs (n <= units, so none is empty).
+// How one half of the layer is cut into runs, one a CTA.  Work is counted in units (a stage of weights each), `per` of
+// them a tile; a run begins and ends at multiples of `grain` units: at tiles (grain == per), so that no CTA shares one,
+// or anywhere (grain == 1).
 struct MtSplit {
-    uint32_t units, n;
+    uint32_t grains, n, grain, per;
+    int rows;  // weight rows of a tile: 128, or 64 (half of the 128-row band its scales lie in)
     __device__ __forceinline__ static uint32_t div(uint64_t a, uint32_t b) {
         return a >> 32 ? (uint32_t)(a / b) : (uint32_t)a / b;  // 64-bit division is several times as long
     }
-    __device__ __forceinline__ uint32_t start(uint32_t c) const { return div((uint64_t)c * units, n); }
+    __device__ __forceinline__ uint32_t start(uint32_t c) const { return div((uint64_t)c * grains, n) * grain; }
     __device__ __forceinline__ uint32_t owner(uint32_t u) const {  // the run that holds unit u
-        return div(((uint64_t)u + 1) * n - 1, units);
+        return div(((uint64_t)u / grain + 1) * n - 1, grains);
     }
     // whether run `c`, which holds some of the tile that begins at unit `begin`, also holds an earlier tile
     __device__ __forceinline__ bool earlier(uint32_t c, uint32_t begin) const { return start(c) < begin; }
+    __device__ __forceinline__ bool shared() const { return grain != per; }
 };
-// Tiles of few steps are not cut (an exchange of partial sums costs about 3 us, a step 0.3 us) where they fit
-// one to a CTA; other runs hold at least two units.  On 5 tokens, 6 experts, D = 352, H = 160: 16.0 us; with a
-// limit of 12 steps and four units 18.0 us.
-__device__ __forceinline__ MtSplit mt_split(uint32_t units, uint32_t per_tile) {
-    if (units == 0) return MtSplit{0u, 1u};
-    const uint32_t tiles = units / per_tile;
-    if (tiles <= gridDim.x && per_tile <= kMtWholeSteps) return MtSplit{units, tiles};
-    return MtSplit{units, min(gridDim.x, (units + 1) / 2)};
+
+// The cut that should take least, by clocks.  A half's bytes take their time at HBM's rate; a run takes its own on its
+// SM, 800 clocks a unit of 64-row tiles and 900 of 128-row tiles (the products of a unit are issued in 350 to 500, the
+// rest is the wait for the next stage).  Sharing tiles evens the runs out but costs an exchange of partial sums, 7000
+// clocks under load (two trips through L2 and the gathering).  bands: 128-row bands; per: units of one of them.
+// Measured, best cut against shared tiles throughout and whole tiles throughout: one token over MXFP8 experts of
+// 8192 x 5120 35.3 us / 39.1 / 38.5, MXFP4 27.0 / 31.7 / 27.3; four tokens, top-4 of 16 MXFP8 experts of 2048 x 7168 92.8 /
+// 92.1 / 104.9; 64 tokens over the same in MXFP4 80.7 / 89.5 / 90.8; five tokens, six experts of 160 x 352 16.0 / 21.0 / 16.1.
+constexpr float kMtHbm = 3300.0f;  // bytes a clock
+constexpr float kMtExchange = 7000.0f;
+
+__device__ __forceinline__ MtSplit mt_split(uint32_t bands, uint32_t per) {
+    if (bands == 0 || per == 0) return MtSplit{1u, 1u, 1u, 1u, 128};
+    const uint32_t g = gridDim.x;
+    const float hbm = (float)per * 32768.0f / kMtHbm;  // a band's bytes at HBM's rate
+    // m rounds of a tile for every CTA, then one for the rest
+    auto rounds = [&](uint32_t tiles, float bytes, float own) -> float {
+        const uint32_t m = tiles / g, r = tiles - m * g;
+        return (float)m * fmaxf(own, (float)g * bytes) + (r ? fmaxf(own, (float)r * bytes) : 0.0f);
+    };
+    const float whole = rounds(bands, hbm, (float)per * 900.0f), half = rounds(2 * bands, 0.5f * hbm, (float)per * 800.0f);
+    const uint32_t units = bands * per, runs = min(g, (units + 1) / 2);
+    const float cut = fmaxf((float)bands * hbm, (float)((units + runs - 1) / runs) * 900.0f) + kMtExchange;
+    if (whole <= half && whole <= cut) return MtSplit{bands, min(g, bands), per, per, 128};
+    if (half <= cut) return MtSplit{2 * bands, min(g, 2 * bands), per, per, 64};
+    return MtSplit{units, runs, 1u, per, 128};
 }
 
 template <int BITS, int N>
 __global__ void __launch_bounds__(kMtThreads, 1)
-    moe_tokens_kernel(const __grid_constant__ CUtensorMap map_gate, const __grid_constant__ CUtensorMap map_up,
-                      const __grid_constant__ CUtensorMap map_down, const __grid_constant__ CUtensorMap map_x,
-                      const __grid_constant__ CUtensorMap map_h, const MtParams p) {
+    moe_tokens_kernel(const __grid_constant__ MtMaps maps, const MtParams p) {
     using C = MtCfg<BITS, N>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t full[C::kStages], empty[C::kStages], tfull[2], tempty[2], drain;
+    __shared__ __align__(8) uint64_t full[kMtStages], empty[kMtStages], tfull[2], tempty[2], drain;
     __shared__ MtRoute route;
     __shared__ float w_s[2][kMtMaxTokens];
     __shared__ uint32_t tmem_base_s, last_s;
@@ -199,7 +373,7 @@ __global__ void __launch_bounds__(kMtThreads, 1)
         mt_route(p, reinterpret_cast<uint32_t*>(smem), route, tid, [&] {  // the keys, before the first stage is filled
             if (warp == 2) {
                 if (lane == 0) {
-                    for (int s = 0; s < C::kStages; ++s) {
+                    for (int s = 0; s < kMtStages; ++s) {
                         mbar_init(&full[s], 2);  // the weight and the token producer
                         mbar_init(&empty[s], 1);
                     }
@@ -210,11 +384,13 @@ __global__ void __launch_bounds__(kMtThreads, 1)
                     mbar_init(&drain, 1);
                     abort_s = 0;
                     fence_barrier_init();
-                    prefetch_tmap(&map_gate);
-                    prefetch_tmap(&map_up);
-                    prefetch_tmap(&map_down);
-                    prefetch_tmap(&map_x);
-                    prefetch_tmap(&map_h);
+                    prefetch_tmap(&maps.x);
+                    prefetch_tmap(&maps.h);
+                    for (int i = 0; i < 2; ++i) {
+                        prefetch_tmap(&maps.gate[i]);
+                        prefetch_tmap(&maps.up[i]);
+                        prefetch_tmap(&maps.down[i]);
+                    }
                 }
                 __syncwarp();
                 tmem_alloc(&tmem_base_s, 512);
@@ -233,238 +409,277 @@ __global__ void __launch_bounds__(kMtThreads, 1)
 
     const uint32_t ct_d = (uint32_t)((D + 127) / 128), ct_h = (uint32_t)((H + 127) / 128);
     const uint32_t K1 = (uint32_t)((D + C::kKE - 1) / C::kKE), K2 = (uint32_t)((H + C::kKE - 1) / C::kKE);
-    const uint32_t TH = ct_h, TD = (uint32_t)((D + 255) / 256);
-    const uint32_t AK2 = (uint32_t)A * K2;
-    const MtSplit sp1 = mt_split((uint32_t)A * TH * K1, K1), sp2 = mt_split(TD * AK2, AK2);
-    const uint32_t u1_0 = cta < sp1.n ? sp1.start(cta) : 0, u1_1 = cta < sp1.n ? sp1.start(cta + 1) : 0;
-    const uint32_t u2_0 = cta < sp2.n ? sp2.start(cta) : 0, u2_1 = cta < sp2.n ? sp2.start(cta + 1) : 0;
+    // first half: tiles (active expert, band of H, part), units of one step; second: tiles (band of D, part), units of two
+    // steps of one active expert's H
+    const uint32_t K2u = (K2 + 1) / 2, AK2 = (uint32_t)A * K2u;
+    const MtSplit sp1 = mt_split((uint32_t)A * ct_h, K1), sp2 = mt_split(A ? ct_d : 0, AK2);
+    const uint32_t u1_0 = A && cta < sp1.n ? sp1.start(cta) : 0, u1_1 = A && cta < sp1.n ? sp1.start(cta + 1) : 0;
+    const uint32_t u2_0 = A && cta < sp2.n ? sp2.start(cta) : 0, u2_1 = A && cta < sp2.n ? sp2.start(cta + 1) : 0;
+    const uint32_t R1 = sp1.rows, R2 = sp2.rows, parts1 = 128 / R1, parts2 = 128 / R2;
+    // A stage: two weight tiles, their scale tiles, two token tiles (the first half uses one), theirs.  A 64-row tile is
+    // multiplied as its half of a 128-row one: the other half is whatever lies beside it in shared memory (half a
+    // tile of room is left at both ends) and its results are not looked at.
+    const uint32_t off_sfa = 2 * max(R1, R2) * 128, off_b = off_sfa + 2 * C::kSfTiles * 512;
+    const uint32_t off_sfb = off_b + 2 * N * 128, stage_bytes = off_sfb + 2 * C::kSfTiles * 512;
+    const uint32_t edge = min(R1, R2) < 128 ? 64 * 128 : 0;
+    const uint32_t stages = min(min((uint32_t)kMtStages, (uint32_t)(512 - C::kSfCol0) / C::kSfCols),
+                                (C::kSmem - 1024 - 2 * edge) / stage_bytes);
+    uint8_t* ring = smem + edge;
+
+    const uint32_t ring_at = __shfl_sync(0xffffffffu, smem_u32(ring), 0);
 
     auto grid_wait = [&](int point) -> bool { return mt_grid_wait(p, point, abort_flag); };
+    // a wait by a whole warp that goes on, or gives up, together
+    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu, mbar_wait_bounded<true>(bar, parity, p.timeout_ns, abort_flag, p.dev_status));
+    };
+    // A place in the ring.  Whether the next stage can be had is asked one stage ahead, while this one's instructions are
+    // issued: a wait costs 130 clocks even at a barrier that is complete, a third of what a stage's products take.
+    struct Place {
+        uint32_t stage = 0, phase = 0, ready = 0;
+    };
+    auto take = [&](Place& at, uint64_t* bars, uint32_t flip) -> bool {  // waits for stage at.stage, then looks at the next
+        if (!at.ready && !wait(&bars[at.stage], at.phase ^ flip)) return false;
+        const bool wraps = at.stage + 1 == stages;
+        at.ready = peek(&bars[wraps ? 0 : at.stage + 1], at.phase ^ flip ^ (wraps ? 1u : 0u));
+        return true;
+    };
+    auto pass = [&](Place& at) {
+        if (++at.stage == stages) {
+            at.stage = 0;
+            at.phase ^= 1u;
+        }
+    };
+    // Tiles of the first half in order: (active expert a, band j of its rows, part of the band).
+    struct Tile1 {
+        uint32_t tile, a, j, part;
+    };
+    auto tile1 = [&](uint32_t u) -> Tile1 {
+        const uint32_t tile = u / K1, band = tile / parts1, a = band / ct_h;
+        return Tile1{tile, a, band - a * ct_h, tile - band * parts1};
+    };
+    auto next1 = [&](Tile1& t) {
+        ++t.tile;
+        if (++t.part < parts1) return;
+        t.part = 0;
+        if (++t.j < ct_h) return;
+        t.j = 0;
+        ++t.a;
+    };
+    // The second half: runs of one tile's units that belong to one active expert a.
+    struct Tile2 {
+        uint32_t tile, a;
+    };
+    auto tile2 = [&](uint32_t u) -> Tile2 {
+        const uint32_t tile = u / AK2;
+        return Tile2{tile, (u - tile * AK2) / K2u};
+    };
+    auto next2 = [&](Tile2& t) {
+        if (++t.a < (uint32_t)A) return;
+        t.a = 0;
+        ++t.tile;
+    };
 
     if (A == 0) {
         for (int64_t i = (int64_t)cta * kMtThreads + tid; i < T * D; i += (int64_t)gridDim.x * kMtThreads)
             p.y[i] = __float2bfloat16(0.0f);
     } else if (warp == 0) {
-        if (lane == 0) {
-            // -------------------------------------------- weight producer
-            // A place in this CTA's two runs, one after the other.  Stepping costs a few additions: the
-            // divisions (hundreds of cycles each on one thread) are paid once a run.
-            struct Place {
-                const CUtensorMap *m0, *m1;
-                const uint8_t *s0, *s1;
-                int32_t row0, row1;       // row1 < 0: no second tile
-                uint32_t k, K, left;      // step, steps of this tile and expert, units left in this half
-                uint32_t a, j;            // active expert, tile
-                uint32_t ct;
-                bool first;
-            };
-            auto settle = [&](Place& q) {  // rows, scales of (a, j) from step k on
-                const uint32_t e = route.list[q.a];
-                if (q.first) {
-                    const int64_t so = (((int64_t)e * ct_h + q.j) * ct_d + q.k * C::kSfTiles) * 512;
-                    q.row0 = q.row1 = (int32_t)((int64_t)e * H + q.j * 128);
-                    q.s0 = p.s_gate + so;
-                    q.s1 = p.s_up + so;
-                } else {
-                    q.row0 = (int32_t)((int64_t)e * D + q.j * 256);
-                    q.row1 = 2 * q.j + 1 < ct_d ? q.row0 + 128 : -1;
-                    q.s0 = p.s_down + (((int64_t)e * ct_d + 2 * q.j) * ct_h + q.k * C::kSfTiles) * 512;
-                    q.s1 = q.s0 + (int64_t)ct_h * 512;
-                }
-            };
-            auto second = [&](Place& q) {
-                const uint32_t r = u2_0 % AK2;
-                q.first = false;
-                q.m0 = q.m1 = &map_down;
-                q.j = u2_0 / AK2;
-                q.a = r / K2;
-                q.k = r - q.a * K2;
-                q.K = K2;
-                q.ct = ct_h;
-                q.left = u2_1 - u2_0;
-            };
-            auto begin = [&]() -> Place {
-                Place q;
-                if (u1_0 < u1_1) {
-                    const uint32_t tile = u1_0 / K1;
-                    q.first = true;
-                    q.m0 = &map_gate;
-                    q.m1 = &map_up;
-                    q.a = tile / TH;
-                    q.j = tile - q.a * TH;
-                    q.k = u1_0 - tile * K1;
-                    q.K = K1;
-                    q.ct = ct_d;
-                    q.left = u1_1 - u1_0;
-                } else {
-                    second(q);
-                }
-                settle(q);
-                return q;
-            };
-            auto step = [&](Place& q) {
-                --q.left;
-                if (++q.k < q.K && q.left != 0) {
-                    q.s0 += C::kSfTiles * 512;
-                    q.s1 += C::kSfTiles * 512;
-                    return;
-                }
-                if (q.left == 0) {
-                    if (!q.first || u2_0 == u2_1) return;  // the end
-                    second(q);
-                } else {
-                    q.k = 0;
-                    if (q.first) {
-                        if (++q.j == TH) { q.j = 0; ++q.a; }
-                    } else {
-                        if (++q.a == (uint32_t)A) { q.a = 0; ++q.j; }
-                    }
-                }
-                settle(q);
-            };
-            auto sf_bytes = [&](const Place& q) { return min((uint32_t)C::kSfTiles, q.ct - q.k * C::kSfTiles) * 512u; };
-            const uint32_t total = (u1_1 - u1_0) + (u2_1 - u2_0);
-            if (total != 0) {
-                int stage = 0;
-                uint32_t phase = 0;
-                Place q = begin();
-                for (uint32_t i = 0; i < total; ++i) {
-                    if (!mbar_wait_bounded<true>(&empty[stage], phase ^ 1u, p.timeout_ns, abort_flag, p.dev_status)) break;
-                    uint8_t* st = smem + stage * C::kStage;
-                    const uint32_t n = sf_bytes(q);
-                    const int32_t x = (int32_t)(q.k * 128);
-                    mbar_arrive_expect_tx(&full[stage], (q.row1 >= 0 ? 2u : 1u) * (16384u + n));
-                    tma_load_2d(st, q.m0, x, q.row0, &full[stage]);
-                    bulk_load(st + C::kOffSfA, q.s0, n, &full[stage]);
-                    if (q.row1 >= 0) {
-                        tma_load_2d(st + 16384, q.m1, x, q.row1, &full[stage]);
-                        bulk_load(st + C::kOffSfA + C::kSfTiles * 512, q.s1, n, &full[stage]);
-                    }
-                    step(q);
-                    if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
-                }
+        // ------------------------------------------------ weight producer
+        // (Warps 0-2 walk their loops whole and an elected lane issues, so that addresses and descriptors stay in uniform
+        // registers, where these instructions take them from; divisions are paid once a tile.)
+        const uint32_t one = elect_one();
+        Place at;
+        bool ok = true;
+        auto claim = [&](uint32_t bytes) -> bool {
+            if (!take(at, empty, 1u)) return false;
+            expect_tx(one, &full[at.stage], bytes);
+            return true;
+        };
+        const CUtensorMap *mg = &maps.gate[parts1 - 1], *mu = &maps.up[parts1 - 1], *md = &maps.down[parts2 - 1];
+        Tile1 t1 = tile1(u1_0);
+        for (uint32_t u = u1_0; u < u1_1 && ok; next1(t1)) {
+            const uint32_t end = min(u1_1, (t1.tile + 1) * K1);
+            const uint32_t e = __shfl_sync(0xffffffffu, (uint32_t)route.list[t1.a], 0);
+            const int32_t row = (int32_t)((int64_t)e * H + t1.j * 128 + t1.part * R1);
+            uint32_t k = u - t1.tile * K1;
+            const int64_t so = (((int64_t)e * ct_h + t1.j) * ct_d + k * C::kSfTiles) * 512;
+            const uint8_t *sg = p.s_gate + so, *su = p.s_up + so;
+            for (; u < end; ++u, ++k, sg += C::kSfTiles * 512, su += C::kSfTiles * 512) {
+                const uint32_t n = min((uint32_t)C::kSfTiles, ct_d - k * C::kSfTiles) * 512;
+                if (!(ok = claim(2 * (R1 * 128 + n)))) break;
+                const uint32_t st = ring_at + at.stage * stage_bytes;
+                load_2d(one, st, mg, (int32_t)(k * 128), row, &full[at.stage]);
+                load_2d(one, st + R1 * 128, mu, (int32_t)(k * 128), row, &full[at.stage]);
+                load_bulk(one, st + off_sfa, sg, n, &full[at.stage]);
+                load_bulk(one, st + off_sfa + C::kSfTiles * 512, su, n, &full[at.stage]);
+                pass(at);
+            }
+        }
+        Tile2 t2 = tile2(u2_0);
+        for (uint32_t u = u2_0; u < u2_1 && ok; next2(t2)) {
+            const uint32_t base = t2.tile * AK2 + t2.a * K2u, end = min(u2_1, base + K2u);
+            const uint32_t band = t2.tile / parts2, part = t2.tile - band * parts2;
+            const uint32_t e = __shfl_sync(0xffffffffu, (uint32_t)route.list[t2.a], 0);
+            const int32_t row = (int32_t)((int64_t)e * D + band * 128 + part * R2);
+            uint32_t k = 2 * (u - base);
+            const uint8_t* sd = p.s_down + (((int64_t)e * ct_d + band) * ct_h + k * C::kSfTiles) * 512;
+            for (; u < end; ++u, k += 2, sd += 2 * C::kSfTiles * 512) {
+                const uint32_t n = min(2u * C::kSfTiles, ct_h - k * C::kSfTiles) * 512;
+                const bool two = k + 1 < K2;
+                if (!(ok = claim((two ? 2 : 1) * R2 * 128 + n))) break;
+                const uint32_t st = ring_at + at.stage * stage_bytes;
+                load_2d(one, st, md, (int32_t)(k * 128), row, &full[at.stage]);
+                if (two) load_2d(one, st + R2 * 128, md, (int32_t)(k * 128 + 128), row, &full[at.stage]);
+                load_bulk(one, st + off_sfa, sd, n, &full[at.stage]);
+                pass(at);
             }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            // -------------------------------------------- token producer
-            int stage = 0;
-            uint32_t phase = 0;
-            // step k of the contraction: tile (k, plane z) of the map, scale tiles at s
-            auto load = [&](const CUtensorMap* m, int32_t z, const uint8_t* s, uint32_t k, uint32_t ct) -> bool {
-                if (!mbar_wait_bounded<true>(&empty[stage], phase ^ 1u, p.timeout_ns, abort_flag, p.dev_status))
-                    return false;
-                uint8_t* st = smem + stage * C::kStage;
-                const uint32_t sfb = min((uint32_t)C::kSfTiles, ct - k * C::kSfTiles) * 512;
-                mbar_arrive_expect_tx(&full[stage], N * 128u + sfb);
-                tma_load_3d(st + C::kOffB, m, (int32_t)(k * 128), 0, z, &full[stage]);
-                bulk_load(st + C::kOffSfB, s, sfb, &full[stage]);
-                if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
-                return true;
-            };
-            bool ok = grid_wait(kMtXDone);
-            uint32_t k = u1_0 % K1;
-            const uint8_t* s = p.xs + k * C::kSfTiles * 512;
-            for (uint32_t u = u1_0; u < u1_1 && ok; ++u) {
-                ok = load(&map_x, 0, s, k, ct_d);
-                s += C::kSfTiles * 512;
-                if (++k == K1) {
-                    k = 0;
-                    s = p.xs;
-                }
+        // ------------------------------------------------ token producer
+        const uint32_t one = elect_one();
+        Place at;
+        // steps k .. k + n - 1 of the contraction: tiles of plane z of the map, scale tiles at s
+        auto load = [&](const CUtensorMap* m, int32_t z, const uint8_t* s, uint32_t k, uint32_t n, uint32_t ct) -> bool {
+            if (!take(at, empty, 1u)) return false;
+            const uint32_t st = ring_at + at.stage * stage_bytes;
+            const uint32_t sfb = min(n * C::kSfTiles, ct - k * C::kSfTiles) * 512;
+            expect_tx(one, &full[at.stage], n * N * 128u + sfb);
+            load_3d(one, st + off_b, m, (int32_t)(k * 128), 0, z, &full[at.stage]);
+            if (n == 2) load_3d(one, st + off_b + N * 128, m, (int32_t)(k * 128 + 128), 0, z, &full[at.stage]);
+            load_bulk(one, st + off_sfb, s, sfb, &full[at.stage]);
+            pass(at);
+            return true;
+        };
+        bool ok = __all_sync(0xffffffffu, grid_wait(kMtXDone));
+        uint32_t k = u1_0 % K1;
+        const uint8_t* s = p.xs + k * C::kSfTiles * 512;
+        for (uint32_t u = u1_0; u < u1_1 && ok; ++u) {
+            ok = load(&maps.x, 0, s, k, 1, ct_d);
+            s += C::kSfTiles * 512;
+            if (++k == K1) {
+                k = 0;
+                s = p.xs;
             }
-            if (ok && u2_0 < u2_1) ok = grid_wait(kMtHDone);
-            uint32_t a = u2_0 % AK2 / K2;
-            k = u2_0 % K2;  // AK2 is a multiple of K2
-            s = p.hs + ((int64_t)a * ct_h + k * C::kSfTiles) * 512;
-            for (uint32_t u = u2_0; u < u2_1 && ok; ++u) {
-                ok = load(&map_h, (int32_t)a, s, k, ct_h);
-                s += C::kSfTiles * 512;
-                if (++k == K2) {
-                    k = 0;
-                    if (++a == (uint32_t)A) a = 0;
-                    s = p.hs + (int64_t)a * ct_h * 512;
-                }
+        }
+        if (ok && u2_0 < u2_1) ok = __all_sync(0xffffffffu, grid_wait(kMtHDone));
+        uint32_t a = u2_0 < u2_1 ? u2_0 % AK2 / K2u : 0;
+        k = u2_0 < u2_1 ? 2 * (u2_0 % K2u) : 0;  // AK2 is a multiple of K2u
+        s = p.hs + ((int64_t)a * ct_h + k * C::kSfTiles) * 512;
+        for (uint32_t u = u2_0; u < u2_1 && ok; ++u) {
+            ok = load(&maps.h, (int32_t)a, s, k, k + 1 < K2 ? 2 : 1, ct_h);
+            s += 2 * C::kSfTiles * 512;
+            if ((k += 2) >= K2) {
+                k = 0;
+                if (++a == (uint32_t)A) a = 0;
+                s = p.hs + (int64_t)a * ct_h * 512;
             }
         }
     } else if (warp == 2) {
         {
             // -------------------------------------------- tensor-core issuer
-            // The whole warp walks the loop and one elected lane issues, so that descriptors and addresses stay in
-            // uniform registers, where these instructions take them from.
             const uint32_t one = elect_one();
-            const uint32_t ring = __shfl_sync(0xffffffffu, smem_u32(smem), 0);
             const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-            auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-                return __all_sync(0xffffffffu,
-                                  mbar_wait_bounded<true>(bar, parity, p.timeout_ns, abort_flag, p.dev_status));
-            };
-            int stage = 0, buf = 0;
-            uint32_t phase = 0, buf_phase = 0;
-            // steps k0 .. k1-1 of a contraction of K elements into the next accumulator pair
-            auto contract = [&](uint32_t k0, uint32_t k1, int64_t K) -> bool {
-                if (!wait(&tempty[buf], buf_phase ^ 1u))
-                    return false;
-                tc_fence_after();
-                const uint32_t d0 = tm + buf * 2 * N;
-                for (uint32_t k = k0; k < k1; ++k) {
-                    if (!wait(&full[stage], phase))
-                        return false;
-                    tc_fence_after();
-                    // descriptors of a stage differ from its first only in their address field
-                    const uint32_t at = (ring + stage * C::kStage) >> 4;
-                    const uint32_t sf = tm + C::kSfCol0 + stage * C::kSfCols;
-#pragma unroll
-                    for (int i = 0; i < 3 * C::kSfTiles; ++i) {
-                        const int off = i < 2 * C::kSfTiles ? C::kOffSfA + 512 * i
-                                                            : C::kOffSfB + 512 * (i - 2 * C::kSfTiles);
-                        cp_scales(one, sf + 4 * i, desc_of(at + off / 16, kDescScale));
-                    }
-                    auto mma = [&](int s, uint32_t acc) {
-                        const uint64_t bd = desc_of((at + (C::kOffB + 32 * s) / 16) | kDescLbo, kDescTile);
-#pragma unroll
-                        for (int w = 0; w < 2; ++w) {
-                            const uint64_t ad = desc_of((at + (w * 16384 + 32 * s) / 16) | kDescLbo, kDescTile);
-                            if constexpr (BITS == 8) {
-                                mma_mxf8(one, d0 + w * N, ad, bd, idesc_mxf8(128, N, s, s), sf + 4 * w, sf + 8, acc);
-                            } else {
-                                constexpr uint32_t id0 = (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) |
-                                                         (1u << 23) | (1u << 27);  // E2M1 x E2M1, E8M0, M = 128
-                                const uint32_t id = (uint32_t)(s & 1) * 2;
-                                mma_mxf4(one, d0 + w * N, ad, bd, id0 | (id << 4) | (id << 29),
-                                            sf + 8 * w + 4 * (s >> 1), sf + 16 + 4 * (s >> 1), acc);
-                            }
-                        }
-                    };
-                    if ((int64_t)(k + 1) * C::kKE <= K) {
-                        mma(0, k != k0);
-                        mma(1, 1u);
-                        mma(2, 1u);
-                        mma(3, 1u);
-                    } else {  // the contraction's last elements
-                        const int steps = (int)((K - (int64_t)k * C::kKE + C::kKE / 4 - 1) / (C::kKE / 4));
-                        mma(0, k != k0);
-                        if (steps > 1) mma(1, 1u);
-                        if (steps > 2) mma(2, 1u);
-                        if (steps > 3) mma(3, 1u);
-                    }
-                    commit(one, &empty[stage]);
-                    if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
+            Place at;
+            int buf = 0;
+            uint32_t buf_phase = 0;
+            // one product of K = 32 (E4M3) or 64 (E2M1): quarter s of the steps at a (weights) and b (tokens)
+            auto mma = [&](uint32_t d, uint32_t a, uint32_t b, uint32_t sfa, uint32_t sfb, int s, uint32_t acc) {
+                const uint64_t ad = desc_of((a + 2 * s) | kDescLbo, kDescTile), bd = desc_of((b + 2 * s) | kDescLbo, kDescTile);
+                if constexpr (BITS == 8) {
+                    mma_mxf8(one, d, ad, bd, idesc_mxf8(128, N, s, s), sfa, sfb, acc);
+                } else {
+                    constexpr uint32_t id0 = (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | (1u << 23) |
+                                             (1u << 27);  // E2M1 x E2M1, E8M0, M = 128
+                    const uint32_t id = (uint32_t)(s & 1) * 2;
+                    mma_mxf4(one, d, ad, bd, id0 | (id << 4) | (id << 29), sfa + 4 * (s >> 1), sfb + 4 * (s >> 1), acc);
                 }
-                commit(one, &tfull[buf]);
-                if (++buf == 2) { buf = 0; buf_phase ^= 1u; }
+            };
+            // quarters of step k that hold any of K elements
+            auto quarters = [&](uint32_t k, uint32_t K) -> uint32_t {
+                return min(4u, (K - k * C::kKE + C::kKE / 4 - 1) / (C::kKE / 4));
+            };
+            const uint32_t q_d = quarters(K1 - 1, (uint32_t)D), q_h = quarters(K2 - 1, (uint32_t)H);
+            auto open = [&]() -> bool {
+                if (!peek(&tempty[buf], buf_phase ^ 1u) && !wait(&tempty[buf], buf_phase ^ 1u)) return false;
+                tc_fence_after();
                 return true;
             };
+            // the quarters of a step, of which the first q hold anything
+            auto each = [](uint32_t q, auto&& quarter) {
+                quarter(0);
+                if (q == 4) {
+                    quarter(1);
+                    quarter(2);
+                    quarter(3);
+                } else {
+                    if (q > 1) quarter(1);
+                    if (q > 2) quarter(2);
+                }
+            };
+            auto close = [&] {
+                commit(one, &tfull[buf]);
+                if (++buf == 2) { buf = 0; buf_phase ^= 1u; }
+            };
+            auto release = [&] {
+                commit(one, &empty[at.stage]);
+                pass(at);
+            };
             bool ok = true;
-            for (uint32_t u = u1_0; u < u1_1 && ok;) {
-                const uint32_t tile = u / K1, end = min(u1_1, (tile + 1) * K1);
-                ok = contract(u - tile * K1, end - tile * K1, D);
-                u = end;
+            Tile1 t1 = tile1(u1_0);
+            for (uint32_t u = u1_0; u < u1_1 && ok; next1(t1)) {
+                const uint32_t end = min(u1_1, (t1.tile + 1) * K1), back = t1.part * R1 * 8;
+                if (!(ok = open())) break;
+                const uint32_t d0 = tm + buf * 2 * N;
+                for (uint32_t k = u - t1.tile * K1, acc = 0; u < end; ++u, ++k) {
+                    if (!(ok = take(at, full, 0u))) break;
+                    tc_fence_after();
+                    // descriptors of a stage differ from its first only in their address field (in units of 16 bytes)
+                    const uint32_t st = (ring_at + at.stage * stage_bytes) >> 4, sf = tm + C::kSfCol0 + at.stage * C::kSfCols;
+                    const uint32_t a = st - back, b = st + (off_b >> 4);
+#pragma unroll
+                    for (int i = 0; i < 2 * C::kSfTiles; ++i)
+                        cp_scales(one, sf + 4 * i, desc_of(st + (off_sfa >> 4) + 32 * i, kDescScale));
+#pragma unroll
+                    for (int i = 0; i < C::kSfTiles; ++i)
+                        cp_scales(one, sf + 8 * C::kSfTiles + 4 * i, desc_of(st + (off_sfb >> 4) + 32 * i, kDescScale));
+                    auto quarter = [&](int s) {
+                        mma(d0, a, b, sf, sf + 8 * C::kSfTiles, s, acc);
+                        mma(d0 + N, a + R1 * 8, b, sf + 4 * C::kSfTiles, sf + 8 * C::kSfTiles, s, acc);
+                        acc = 1;
+                    };
+                    each(k + 1 == K1 ? q_d : 4u, quarter);
+                    release();
+                }
+                if (ok) close();
             }
-            for (uint32_t u = u2_0; u < u2_1 && ok;) {
-                const uint32_t base = u / K2 * K2, end = min(u2_1, base + K2);  // AK2 is a multiple of K2
-                ok = contract(u - base, end - base, H);
-                u = end;
+            Tile2 t2 = tile2(u2_0);
+            for (uint32_t u = u2_0; u < u2_1 && ok; next2(t2)) {
+                const uint32_t base = t2.tile * AK2 + t2.a * K2u, end = min(u2_1, base + K2u);
+                const uint32_t back = (t2.tile & (parts2 - 1)) * R2 * 8;
+                if (!(ok = open())) break;
+                const uint32_t d0 = tm + buf * 2 * N;
+                for (uint32_t k = 2 * (u - base), acc = 0; u < end; ++u, k += 2) {
+                    if (!(ok = take(at, full, 0u))) break;
+                    tc_fence_after();
+                    const uint32_t st = (ring_at + at.stage * stage_bytes) >> 4, sf = tm + C::kSfCol0 + at.stage * C::kSfCols;
+                    const uint32_t a = st - back, b = st + (off_b >> 4);
+#pragma unroll
+                    for (int i = 0; i < 2 * C::kSfTiles; ++i) {
+                        cp_scales(one, sf + 4 * i, desc_of(st + (off_sfa >> 4) + 32 * i, kDescScale));
+                        cp_scales(one, sf + 8 * C::kSfTiles + 4 * i, desc_of(st + (off_sfb >> 4) + 32 * i, kDescScale));
+                    }
+                    auto half = [&](int w, uint32_t q) {
+                        each(q, [&](int s) {
+                            mma(d0, a + w * R2 * 8, b + w * N * 8, sf + 4 * C::kSfTiles * w, sf + (8 + 4 * w) * C::kSfTiles, s,
+                                acc);
+                            acc = 1;
+                        });
+                    };
+                    half(0, k + 1 == K2 ? q_h : 4u);
+                    if (k + 1 < K2) half(1, k + 2 == K2 ? q_h : 4u);
+                    release();
+                }
+                if (ok) close();
             }
             commit(one, &drain);
             volatile int no_abort = 0;
@@ -500,8 +715,8 @@ __global__ void __launch_bounds__(kMtThreads, 1)
         // and the code stays a short loop (unrolled over all columns it did not fit the instruction cache).
         constexpr int kCols = 4;
         for (uint32_t u = u1_0; u < u1_1 && ok;) {
-            const uint32_t tile = u / K1, a = tile / TH, j = tile - a * TH;
-            const uint32_t end = min(u1_1, (tile + 1) * K1);
+            const uint32_t tile = u / K1, band = tile / parts1, a = band / ct_h, j = band - a * ct_h;
+            const uint32_t end = min(u1_1, (tile + 1) * K1), r0 = (tile & (parts1 - 1)) * R1;
             const bool whole = u == tile * K1 && end == (tile + 1) * K1;
             u = end;
             ok = epi_all(mbar_wait_bounded<true>(&tfull[buf], buf_phase, p.timeout_ns, abort_flag, p.dev_status));
@@ -541,6 +756,7 @@ __global__ void __launch_bounds__(kMtThreads, 1)
             };
             // SwiGLU and quantization of n columns; the warp's 32 rows are one block of a token's h
             const int64_t row = (int64_t)j * 128 + r;
+            const bool mine = quarter * 32 >= r0 && quarter * 32 < r0 + R1;  // this warp's rows are in the tile
             const bool in = row < H;
             auto finish = [&](const int (&col)[kCols], int n, const float (&g)[kCols], const float (&h)[kCols]) {
                 float v[kCols];
@@ -567,7 +783,7 @@ __global__ void __launch_bounds__(kMtThreads, 1)
                 }
             };
             float* own = slot(cta, u1_0 < tile * K1);
-            uint64_t left = mask;
+            uint64_t left = mine ? mask : 0;
             for (int turn = 0; left; ++turn) {
                 int col[kCols];
                 const int n = batch(left, col);
@@ -634,16 +850,20 @@ __global__ void __launch_bounds__(kMtThreads, 1)
         }
 
         // ------------------------------------------------ second half: down, weighted sum over experts
-        constexpr int kLd = N < 32 ? N : 32;
-        float total[N];  // warps 4-7: rows 0-127 of the tile, warps 8-11: rows 128-255
+        // (an accumulator for each expert: a token's column is added in, with its weight, if it was routed there)
+        constexpr int NC = N / 2;  // token columns of this warp
+        const int c0 = cg * NC;
+        float total[NC];
         for (uint32_t u = u2_0; u < u2_1 && ok;) {
             const uint32_t tile = u / AK2, t_end = min(u2_1, (tile + 1) * AK2);
             const bool whole = u == tile * AK2 && t_end == (tile + 1) * AK2;
+            const uint32_t band = tile / parts2, r0 = (tile & (parts2 - 1)) * R2;
+            const bool mine = quarter * 32 >= r0 && quarter * 32 < r0 + R2;
 #pragma unroll
-            for (int c = 0; c < N; ++c) total[c] = 0.0f;
-            uint32_t a = (u - tile * AK2) / K2;
+            for (int c = 0; c < NC; ++c) total[c] = 0.0f;
+            uint32_t a = (u - tile * AK2) / K2u;
             for (; u < t_end; ++a) {
-                u = min(t_end, tile * AK2 + (a + 1) * K2);
+                u = min(t_end, tile * AK2 + (a + 1) * K2u);
                 if (et < T) {  // token et's weight for this expert
                     const int e = route.list[a];
                     float w = 0.0f;
@@ -654,16 +874,14 @@ __global__ void __launch_bounds__(kMtThreads, 1)
                 ok = epi_all(mbar_wait_bounded<true>(&tfull[buf], buf_phase, p.timeout_ns, abort_flag, p.dev_status));
                 if (!ok) break;
                 tc_fence_after();
-                const uint64_t mask = mask_of(a);
-#pragma unroll
-                for (int c = 0; c < N; c += kLd) {
-                    if (((mask >> c) & ((1ull << kLd) - 1ull)) == 0) continue;
-                    uint32_t v[kLd];
-                    tmem_ld_cols(lane_base + buf * 2 * N + cg * N + c, v);
+                const uint32_t mask = (uint32_t)(mask_of(a) >> c0);
+                if (mine && (mask & (uint32_t)((1ull << NC) - 1ull)) != 0) {
+                    uint32_t v[NC];
+                    tmem_ld_cols(lane_base + buf * 2 * N + c0, v);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int i = 0; i < kLd; ++i)
-                        if ((mask >> (c + i)) & 1u) total[c + i] += w_s[buf][c + i] * __uint_as_float(v[i]);
+                    for (int i = 0; i < NC; ++i)
+                        if ((mask >> i) & 1u) total[i] += w_s[buf][c0 + i] * __uint_as_float(v[i]);
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -671,22 +889,22 @@ __global__ void __launch_bounds__(kMtThreads, 1)
                 if (++buf == 2) { buf = 0; buf_phase ^= 1u; }
             }
             if (!ok) break;
-            if (!whole) {
-                float* w = slot(cta, u2_0 < tile * AK2) + cg * T * 128;
+            if (!whole) {  // (a shared tile has all 128 rows)
+                float* w = slot(cta, u2_0 < tile * AK2);
 #pragma unroll
-                for (int c = 0; c < N; ++c)
-                    if (c < T) __stcg(w + c * 128 + r, total[c]);
+                for (int c = 0; c < NC; ++c)
+                    if (c0 + c < T) __stcg(w + (c0 + c) * 128 + r, total[c]);
                 continue;
             }
-            const int64_t d = (int64_t)tile * 256 + cg * 128 + r;
-            if (d < D)
+            const int64_t d = (int64_t)band * 128 + r;
+            if (mine && d < D)
 #pragma unroll
-                for (int c = 0; c < N; ++c)
-                    if (c < T) p.y[c * D + d] = __float2bfloat16(total[c]);
+                for (int c = 0; c < NC; ++c)
+                    if (c0 + c < T) p.y[(c0 + c) * D + d] = __float2bfloat16(total[c]);
         }
         // ------------------------------------------------ add up the tiles that several runs share
         // All CTAs take part, four columns of one token a thread; a tile's sums are added in its runs' order.
-        if (sp2.units % sp2.n != 0 || sp2.units / sp2.n % AK2 != 0) {
+        if (sp2.shared()) {
             epi_sync();
             if (et == 0) {
                 __threadfence();
@@ -694,17 +912,17 @@ __global__ void __launch_bounds__(kMtThreads, 1)
                 ok = ok && grid_wait(kMtSumsDone);
             }
             ok = epi_all(ok);
-            // A warp takes 128 columns (half a tile) of kTok tokens at a time: the runs of its tile are found once and
+            // A warp takes a tile's 128 columns of kTok tokens at a time: the runs of its tile are found once and
             // its loads are whole lines, kTok * kRuns of them in flight.
             constexpr int kTok = N == 16 ? 1 : N == 32 ? 2 : 4, kRuns = 12 / kTok;
-            const uint32_t halves = ct_d, groups = (T + kTok - 1) / kTok;
-            for (uint32_t i = (et >> 5) * gridDim.x + cta; ok && i < halves * groups;
+            const uint32_t groups = (T + kTok - 1) / kTok;
+            for (uint32_t i = (et >> 5) * gridDim.x + cta; ok && i < ct_d * groups;
                  i += gridDim.x * (kMtEpiThreads / 32)) {
-                const uint32_t gr = i / halves, hf = i - gr * halves, tile = hf >> 1;
+                const uint32_t gr = i / ct_d, tile = i - gr * ct_d;
                 const uint32_t lo = sp2.owner(tile * AK2), hi = sp2.owner((tile + 1) * AK2 - 1);
                 if (lo == hi) continue;  // one run had the whole tile
                 const bool lo_second = sp2.earlier(lo, tile * AK2);
-                const uint32_t d = hf * 128 + lane * 4, t0 = gr * kTok;
+                const uint32_t d = tile * 128 + lane * 4, t0 = gr * kTok;
                 float4 sum[kTok];
 #pragma unroll
                 for (int t = 0; t < kTok; ++t) sum[t] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -712,7 +930,7 @@ __global__ void __launch_bounds__(kMtThreads, 1)
                     float4 v[kRuns][kTok];
 #pragma unroll
                     for (int x = 0; x < kRuns; ++x) {
-                        const float* q = slot(o + x, o + x == lo && lo_second) + ((int64_t)(hf & 1) * T + t0) * 128 + lane * 4;
+                        const float* q = slot(o + x, o + x == lo && lo_second) + (int64_t)t0 * 128 + lane * 4;
 #pragma unroll
                         for (int t = 0; t < kTok; ++t) {
                             v[x][t] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -762,7 +980,7 @@ static MtLayout mt_layout(int64_t T, int64_t E, int64_t D, int64_t H, int64_t k,
     const int64_t A = std::min(E, T * k), ct_d = (D + 127) / 128, ct_h = (H + 127) / 128;
     MtLayout l;
     l.counters = kMtHeader;
-    l.ncounters = A * ct_h + (D + 255) / 256;
+    l.ncounters = A * ct_h;
     l.xq = l.counters + up256(l.ncounters * 4);
     l.xs = l.xq + up256(T * D * bits / 8);
     l.hq = l.xs + up256(ct_d * 512);
@@ -786,7 +1004,7 @@ static bool mt_map(CUtensorMap* m, const void* base, int64_t cols, int64_t rows,
 }
 
 template <int BITS, int N>
-static mxfp8_status_t mt_launch(const CUtensorMap (&m)[5], const MtParams& p, cudaStream_t st) {
+static mxfp8_status_t mt_launch(const MtMaps& m, const MtParams& p, cudaStream_t st) {
     using C = MtCfg<BITS, N>;
     static std::atomic<int> attr_set[host::kMaxDevices];
     if (!host::ensure_smem(reinterpret_cast<const void*>(moe_tokens_kernel<BITS, N>), C::kSmem, attr_set))
@@ -801,7 +1019,7 @@ static mxfp8_status_t mt_launch(const CUtensorMap (&m)[5], const MtParams& p, cu
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, moe_tokens_kernel<BITS, N>, m[0], m[1], m[2], m[3], m[4], p) != cudaSuccess) {
+    if (cudaLaunchKernelEx(&cfg, moe_tokens_kernel<BITS, N>, m, p) != cudaSuccess) {
         cudaGetLastError();
         return MXFP8_ERR_LAUNCH;
     }
@@ -852,9 +1070,6 @@ extern "C" mxfp8_status_t mx_moe_tokens(const void* x_bf16, const float* router_
     MtParams p{};
     p.x = static_cast<const uint8_t*>(x_bf16);
     p.logits = router_logits;
-    p.q_gate = static_cast<const uint8_t*>(gate_q);
-    p.q_up = static_cast<const uint8_t*>(up_q);
-    p.q_down = static_cast<const uint8_t*>(down_q);
     p.s_gate = static_cast<const uint8_t*>(gate_s);
     p.s_up = static_cast<const uint8_t*>(up_s);
     p.s_down = static_cast<const uint8_t*>(down_s);
@@ -876,11 +1091,14 @@ extern "C" mxfp8_status_t mx_moe_tokens(const void* x_bf16, const float* router_
     p.score = score;
     p.ncounters = (int)l.ncounters;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (mt_rows_takes(p, bits)) return mt_rows_launch(p, bits, st);
-    CUtensorMap m[5];
-    if (!mt_map(&m[0], gate_q, Db, (int64_t)E * H, 0, 128) || !mt_map(&m[1], up_q, Db, (int64_t)E * H, 0, 128) ||
-        !mt_map(&m[2], down_q, Hb, (int64_t)E * D, 0, 128) || !mt_map(&m[3], ws + l.xq, Db, T, 1, N) ||
-        !mt_map(&m[4], ws + l.hq, Hb, T, std::min<int64_t>(E, (int64_t)T * top_k), N))
+    MtMaps m;
+    for (int i = 0; i < 2; ++i)
+        if (!mt_map(&m.gate[i], gate_q, Db, (int64_t)E * H, 0, 128 >> i) ||
+            !mt_map(&m.up[i], up_q, Db, (int64_t)E * H, 0, 128 >> i) ||
+            !mt_map(&m.down[i], down_q, Hb, (int64_t)E * D, 0, 128 >> i))
+            return MXFP8_ERR_DRIVER;
+    if (!mt_map(&m.x, ws + l.xq, Db, T, 1, N) ||
+        !mt_map(&m.h, ws + l.hq, Hb, T, std::min<int64_t>(E, (int64_t)T * top_k), N))
         return MXFP8_ERR_DRIVER;
     if (bits == 8)
         return N == 16 ? mt_launch<8, 16>(m, p, st) : N == 32 ? mt_launch<8, 32>(m, p, st) : mt_launch<8, 64>(m, p, st);

@@ -165,6 +165,51 @@ __device__ __forceinline__ void mma_mxf4(uint32_t one, uint32_t d, uint64_t a, u
         : "memory");
 }
 
+// Whether a phase of an mbarrier has completed, without waiting; the same answer for a whole warp.
+__device__ __forceinline__ uint32_t peek(uint64_t* bar, uint32_t parity) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tmbarrier.test_wait.parity.shared::cta.b64 q, [%1], %2;\n\t"
+        "vote.sync.all.pred q, q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return r;
+}
+
+__device__ __forceinline__ void expect_tx(uint32_t one, uint64_t* bar, uint32_t bytes) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %2, 0;\n\t"
+        "@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(smem_u32(bar)),
+        "r"(bytes), "r"(one)
+        : "memory");
+}
+__device__ __forceinline__ void load_2d(uint32_t one, uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y,
+                                        uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+        "@q cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n\t}" ::"r"(
+            dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar)), "r"(one)
+        : "memory");
+}
+__device__ __forceinline__ void load_3d(uint32_t one, uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, int32_t z,
+                                        uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %6, 0;\n\t"
+        "@q cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+        "[%5];\n\t}" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar)), "r"(one)
+        : "memory");
+}
+__device__ __forceinline__ void load_bulk(uint32_t one, uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %4, 0;\n\t"
+        "@q cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n\t}" ::"r"(dst),
+        "l"(src), "r"(bytes), "r"(smem_u32(bar)), "r"(one)
+        : "memory");
+}
+
 // The same for a CTA pair.
 __device__ __forceinline__ void cp_scales_pair(uint32_t one, uint32_t taddr, uint64_t sdesc) {
     asm volatile(
@@ -205,13 +250,6 @@ __device__ __forceinline__ void load_3d_pair(uint32_t one, uint32_t dst, const C
         "@q cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, "
         "%4}], [%5];\n\t}" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar), "r"(one)
-        : "memory");
-}
-__device__ __forceinline__ void expect_tx(uint32_t one, uint64_t* bar, uint32_t bytes) {
-    asm volatile(
-        "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %2, 0;\n\t"
-        "@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(smem_u32(bar)),
-        "r"(bytes), "r"(one)
         : "memory");
 }
 

@@ -71,23 +71,6 @@ __device__ __forceinline__ Q4Rows q4_rows(const Q4Params& p) {
     return r;
 }
 
-__device__ __forceinline__ uint4 ld_stream(const uint8_t* p) {
-    uint4 v;
-    asm("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-        : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-        : "l"(p));
-    return v;
-}
-
-__device__ __forceinline__ void unpack8(const uint4& u, float (&v)[8]) {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[2 * i] = bf16lo(w[i]);
-        v[2 * i + 1] = bf16hi(w[i]);
-    }
-}
-
 // Largest magnitude of each half of two bf16 pairs, NaN winning (the sign bits left are not used).
 __device__ __forceinline__ uint32_t amax_pair(uint32_t a, uint32_t b) {
     uint32_t d;

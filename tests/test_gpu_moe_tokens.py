@@ -88,6 +88,50 @@ def test_matches_the_definition(mx, T, E, D, H, k, bits):
 
 
 @pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("T,E,D,H,k", [
+    (1, 2, 256, 256, 1), (1, 8, 512, 1280, 2), (2, 3, 2304, 256, 1), (3, 4, 256, 2304, 3), (7, 5, 768, 512, 2),
+    (8, 16, 1024, 512, 4), (8, 3, 4096, 1024, 1), (8, 3, 4352, 512, 2), (9, 3, 512, 512, 2), (5, 130, 256, 256, 16),
+])
+def test_whole_chunks_of_few_tokens(mx, T, E, D, H, k, bits):
+    """Widths of whole 128-byte chunks, with few and many tiles and steps."""
+    lay = Layer(mx, E, D, H, k, bits, seed=T + D)
+    lay.check(*inputs(T, D, E, seed=T))
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+def test_edges_of_whole_chunks(mx, bits):
+    """Non-finite weights and tokens, unrouted tokens and repeats, all in one batch."""
+    lay = Layer(mx, 4, 512, 256, 1, bits, bad=2)
+    x, logits = inputs(6, 512, 4)
+    logits[:] = 0
+    for t, e in enumerate((0, 2, 1, 3, 2, 0)):
+        logits[t, e] = 5
+    logits[3] = -float("inf")
+    x[5, 511] = float("nan")
+    y = lay.op(x, logits)
+    assert torch.isnan(y).any(1).tolist() == [False, True, False, False, True, True]
+    assert torch.isnan(y[1]).all() and torch.isnan(y[5]).all() and not y[3].any()
+    want, tol = lay.want(x[[0, 2]], logits[[0, 2]])
+    assert (np.abs(f64(y[[0, 2]]) - want) <= tol).all()
+    for _ in range(10):
+        again = lay.op(x, logits)
+        assert torch.equal(again.isnan(), y.isnan()) and torch.equal(again.nan_to_num(), y.nan_to_num())
+    logits[:] = -float("inf")
+    assert not lay.op(x, logits).any()
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("T,E,D,H,k", [
+    (8, 8, 256, 2432, 2), (40, 8, 256, 2432, 2), (1, 2, 256, 2432, 1), (3, 2, 19456, 64, 1), (33, 2, 8192, 256, 1),
+    (2, 2, 8192, 288, 2), (20, 2, 256, 8192, 1), (1, 3, 352, 8192, 2),
+])
+def test_cuts(mx, T, E, D, H, k, bits):
+    """Both halves cut each way: into whole tiles of 128 and of 64 rows, and into runs that share tiles."""
+    lay = Layer(mx, E, D, H, k, bits, seed=H + T)
+    lay.check(*inputs(T, D, E, seed=T + 1))
+
+
+@pytest.mark.parametrize("bits", [8, 4])
 def test_wide_layer(mx, bits):
     """Many tiles and steps: runs that begin and end inside tiles, several experts a run."""
     lay = Layer(mx, 6, 2080, 1056, 2, bits, seed=9)
