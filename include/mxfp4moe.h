@@ -34,6 +34,10 @@ extern "C" {
  * mxfp4_swiglu_quantize -- the same for h = silu(h1) * h3 of two bf16 matrices
  *   [M, K], silu(x) = x / (1 + e^-x), computed and quantized in fp32 (h is not
  *   rounded to bf16 on the way).
+ * mxfp4_quantize_2d_mxfp8_cols -- both copies that a product with an MXFP4 forward and an
+ *   MXFP8 weight gradient needs, from one read of x: q, s as mxfp4_quantize_2d
+ *   writes them (blocked), and qT [K, M], sT as mxfp8_quantize_2d writes its
+ *   column-wise copy (blocked).  M % 32 == 0; group sizes multiples of 32.
  * mxfp4_quantize_3d_experts -- w[G, N, K] bf16 -> q [G, N, K/2]; scales per expert,
  *   compact [N, K/32] or blocked (ceil(N/128)*128*ceil(K/128)*4 bytes each).
  * mxfp4_dequantize -- the values codes and scales stand for, in bf16 (exact):
@@ -44,6 +48,9 @@ mxfp8_status_t mxfp4_quantize_2d(const void* x_bf16, int64_t M, int64_t K, int s
                                  int32_t G, void* q, void* s, mxfp8_stream_t stream);
 mxfp8_status_t mxfp4_swiglu_quantize(const void* h1_bf16, const void* h3_bf16, int64_t M, int64_t K, int scale_layout,
                                      const int32_t* offs, int32_t G, void* q, void* s, mxfp8_stream_t stream);
+mxfp8_status_t mxfp4_quantize_2d_mxfp8_cols(const void* x_bf16, int64_t M, int64_t K, const int32_t* offs, int32_t G,
+                                            void* q, void* s, void* qT, void* sT, int32_t* dev_status,
+                                            mxfp8_stream_t stream);
 mxfp8_status_t mxfp4_quantize_3d_experts(const void* w_bf16, int32_t G, int64_t N, int64_t K, int scale_layout,
                                          void* q, void* s, mxfp8_stream_t stream);
 mxfp8_status_t mxfp4_dequantize(const void* q, const void* s, int32_t batch, int64_t M, int64_t K, int scale_layout,

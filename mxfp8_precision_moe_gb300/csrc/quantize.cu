@@ -28,6 +28,7 @@
 
 #include "common.cuh"
 #include "host_common.h"
+#include "mx4.cuh"
 
 namespace mx {
 
@@ -62,8 +63,9 @@ struct QParams {
 
 // Kernel modes: plain MX quantization; the Hadamard variants (fp32 values), without and with
 // stochastic rounding; the fused SwiGLU backward (three inputs dh, h1, h3; two quantized outputs);
-// stochastic rounding alone (the plain kernel's bf16 data path with stochastic codes).
-enum QuantMode : int { kModePlain = 0, kModeExt = 1, kModeSwiBwd = 2, kModeSR = 3, kModeExtSR = 4 };
+// stochastic rounding alone (the plain kernel's bf16 data path with stochastic codes); MXFP4 codes for the
+// row-wise copy beside MXFP8 ones for the column-wise copy.
+enum QuantMode : int { kModePlain = 0, kModeExt = 1, kModeSwiBwd = 2, kModeSR = 3, kModeExtSR = 4, kModeRow4 = 5 };
 
 // Warp 0 builds, for G groups over R rows, the clamped monotone end rows and
 // the padded start rows P[g] = sum_{h<g} ceil(size_h/128)*128 (also the scale
@@ -253,6 +255,29 @@ __device__ __forceinline__ uint2 quant8_bf16(const uint32_t (&w)[4], uint32_t f2
 #pragma unroll
     for (int k = 0; k < 4; ++k) c[k] = cvt_e4m3x2(scale_bf16<0, HF>(w[k], f2), scale_bf16<1, HF>(w[k], f2));
     return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+}
+
+// The same for E2M1 elements, whose largest exponent is 2: s = max(E - 2, 0), 253 where E is 255.
+__device__ __forceinline__ uint32_t e8m0_pair_e2m1(uint32_t m) {
+    return vmax_u16x2((m >> 7) & 0x00FF00FFu, 0x00020002u) - 0x00020002u;
+}
+constexpr uint32_t kNonfiniteAddE2m1 = 0x00030003u;
+// Eight bf16 times the scale in half HF of f2 -> eight E2M1 codes; of a non-finite block: 7 with each sign.
+template <int HF>
+__device__ __forceinline__ uint32_t quant8_e2m1(const uint32_t (&w)[4], uint32_t f2) {
+    float v[8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        v[2 * k] = scale_bf16<0, HF>(w[k], f2);
+        v[2 * k + 1] = scale_bf16<1, HF>(w[k], f2);
+    }
+    return cvt_e2m1x8(v);
+}
+__device__ __forceinline__ uint32_t nonfinite8_e2m1(const uint32_t (&w)[4]) {
+    uint32_t r = 0x77777777u;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) r |= (((w[k] >> 12) & 8u) | ((w[k] >> 24) & 0x80u)) << (8 * k);
+    return r;
 }
 
 // Sign bits of eight bf16 moved to bit 7 of each byte; used to give the codes
@@ -456,7 +481,7 @@ __global__ void __launch_bounds__(kQThreadsOf<kMode>, 2)
         if constexpr (!kSwiBwd) {
             if (!mbar_wait_bounded(&full[stage], phase, kQTimeoutNs, abort_flag, p.dev_status)) break;
             src = tiles + stage * kStageBytes + (32 * wi + 8 * li) * 256 + (64 * wj + 8 * lj) * 2;
-            if constexpr (kMode == kModePlain || kMode == kModeSR) {
+            if constexpr (!kExt) {
 #pragma unroll
                 for (int rr = 0; rr < 8; ++rr) {
                     const uint4 u = *reinterpret_cast<const uint4*>(src + rr * 256);
@@ -592,13 +617,32 @@ __global__ void __launch_bounds__(kQThreadsOf<kMode>, 2)
                         uint32_t m = amax_bf16x2(__byte_perm(a, c, 0x5410), __byte_perm(a, c, 0x7632));
                         m = shfl_xor_amax(m, 1);
                         m = shfl_xor_amax(m, 2);
-                        s2[k] = e8m0_pair(m);
+                        s2[k] = kMode == kModeRow4 ? e8m0_pair_e2m1(m) : e8m0_pair(m);
                     }
                 }
                 uint32_t nf = 0;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) nf |= s2[k] + kNonfiniteAdd;
+                for (int k = 0; k < 4; ++k) nf |= s2[k] + (kMode == kModeRow4 ? kNonfiniteAddE2m1 : kNonfiniteAdd);
                 const bool any_nonfinite = __any_sync(0xffffffffu, (nf & kNonfiniteBits) != 0u);
+                if constexpr (kMode == kModeRow4) {
+                    uint8_t* q4 = q_row + (row0 + 8 * li) * (C / 2) + c8 / 2;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t f2 = inv_scale_pair_bf16(s2[k]);
+                        uint32_t q[2] = {quant8_e2m1<0>(v[2 * k], f2), quant8_e2m1<1>(v[2 * k + 1], f2)};
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int rr = 2 * k + h;
+                            if (any_nonfinite && pair_half(s2[k], h) == 253u) {
+                                q[h] = nonfinite8_e2m1(v[rr]);
+                                s2[k] |= h ? 0xFFu << 16 : 0xFFu;
+                            }
+                            if (cval && row0 + 8 * li + rr < R) *reinterpret_cast<uint32_t*>(q4 + rr * (C / 2)) = q[h];
+                        }
+                    }
+                    store_row_scales(s_row, __byte_perm(s2[0], s2[1], 0x6420), __byte_perm(s2[2], s2[3], 0x6420));
+                    return;
+                }
                 uint8_t* qb = q_row + b * R * C;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
@@ -1097,6 +1141,15 @@ static mxfp8_status_t launch_tiles_ext(unsigned dirs, const QParams& p, cudaStre
                                            : launch_had<kModeExt>(dirs, had, m, p, grid, st);
 }
 
+// MXFP4 along the rows and MXFP8 down the columns, from one read.
+static mxfp8_status_t launch_row4(const QParams& p, cudaStream_t st) {
+    if (p.ntiles == 0) return MXFP8_OK;
+    CUtensorMap m;
+    if (!make_x_map(&m, p, p.x)) return MXFP8_ERR_DRIVER;
+    const int64_t grid = std::min<int64_t>(p.ntiles, (int64_t)host::num_sms() * 2);
+    return launch_dirs<MXFP8_ROW | MXFP8_COL, kModeRow4>(m, p, grid, st);
+}
+
 // The fused SwiGLU backward: p.x = dh, p.x2 = h1, p.x3 = h3 (direct loads; the tensor map is unused).
 static mxfp8_status_t launch_swiglu_bwd(const QParams& p, cudaStream_t st) {
     if (p.ntiles == 0) return MXFP8_OK;
@@ -1235,4 +1288,29 @@ extern "C" mxfp8_status_t mxfp8_swiglu_bwd_quantize(const void* dh_bf16, const v
     p.x2 = static_cast<const uint16_t*>(h1_bf16);
     p.x3 = static_cast<const uint16_t*>(h3_bf16);
     return launch_swiglu_bwd(p, reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" mxfp8_status_t mxfp4_quantize_2d_mxfp8_cols(const void* x_bf16, int64_t M, int64_t K, const int32_t* offs,
+                                                       int32_t G, void* q, void* s, void* qT, void* sT,
+                                                       int32_t* dev_status, mxfp8_stream_t stream) {
+    if (M < 0 || K <= 0 || M > INT32_MAX || K > INT32_MAX || (offs && (G < 1 || G > MXFP8_MAX_GROUPS)))
+        return MXFP8_ERR_SHAPE;
+    if (K % 32 || M % 32) return MXFP8_ERR_ALIGN;
+    if (M == 0) return MXFP8_OK;  // an empty tensor may have no address
+    if (!x_bf16 || !q || !s || !qT || !sT) return MXFP8_ERR_NULL;
+    const void* ptrs[] = {x_bf16, q, s, qT, sT};
+    for (const void* v : ptrs)
+        if (!host::aligned16(v)) return MXFP8_ERR_ALIGN;
+    if (mxfp8_status_t a = host::check_arch(); a != MXFP8_OK) return a;
+    QParams p{};
+    p.x = static_cast<const uint16_t*>(x_bf16);
+    p.R = M; p.C = K; p.batch = 1;
+    p.q_row = static_cast<uint8_t*>(q); p.s_row = static_cast<uint8_t*>(s);
+    p.q_col = static_cast<uint8_t*>(qT); p.s_col = static_cast<uint8_t*>(sT);
+    p.blocked = 1;
+    p.offs = offs; p.G = offs ? G : 0;
+    p.dev_status = dev_status;
+    p.tiles_r = (M + 127) / 128; p.tiles_c = (K + 127) / 128; p.ntiles = p.tiles_r * p.tiles_c;
+    if (p.ntiles >= INT32_MAX) return MXFP8_ERR_SHAPE;
+    return launch_row4(p, reinterpret_cast<cudaStream_t>(stream));
 }

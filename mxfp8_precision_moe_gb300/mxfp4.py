@@ -11,7 +11,7 @@ from __future__ import annotations
 
 import torch
 
-from . import (COL, ROW, SCALES_BLOCKED, SCALES_COMPACT, _bytes_at_least, _cuda, _expert_blocked_bytes, _offsets,
+from . import (COL, MAX_GROUPS, ROW, SCALES_BLOCKED, SCALES_COMPACT, _bytes_at_least, _cuda, _expert_blocked_bytes, _offsets,
                _status_word, _tensor, _u8, check, load, mxfp8_check_offsets, new_status, read_status)
 
 # torch's handle of a device's current stream as an integer: a few tenths of a microsecond, where
@@ -34,50 +34,94 @@ def _col_bytes(R: int, M: int, G: int) -> int:
     return ((R + 127) // 128) * ((M + 127) // 128 + G) * 512
 
 
-def _row_scales(x: torch.Tensor, M: int, K: int, G: int, layout: int):
+def _row_scales(dev, M: int, K: int, G: int, layout: int):
     if layout == SCALES_COMPACT:
-        return _u8((M, K // 32), x.device)
+        return _u8((M, K // 32), dev)
     if layout != SCALES_BLOCKED:
         raise ValueError("scale_layout: SCALES_COMPACT or SCALES_BLOCKED expected")
-    return _u8(_group_bytes(M, K, G), x.device)
+    return _u8(_group_bytes(M, K, G), dev)
 
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+# A small call's time is the host's, and the named checks of __init__ are a third of it.  So what a correct call
+# looks like is asked in one expression first, and the checks, which say what is wrong, follow where the answer is no.
+def _good(t, dtype, ndim):
+    return isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.dim() == ndim and t.is_contiguous()
+
+
+def _scales(s, nbytes):
+    return (isinstance(s, torch.Tensor) and s.dtype is torch.uint8 and s.is_cuda and s.numel() >= nbytes
+            and s.is_contiguous())
+
+
+def _matrix(x, name: str, offs, other=None, other_name: str = ""):
+    """Checks a bf16 matrix x [M, K], one more of its shape and its row groups; returns M, K, groups and their
+    address."""
+    if not (_good(x, torch.bfloat16, 2) and (offs is None or _good(offs, torch.int32, 1))
+            and (other is None or (_good(other, torch.bfloat16, 2) and other.shape == x.shape))):
+        _tensor(x, name, torch.bfloat16, 2)
+        if other is not None:
+            _tensor(other, other_name, torch.bfloat16, shape=x.shape)
+        _width(x.shape[1], name)
+        if offs is not None:
+            _offsets(offs)
+        _cuda(x, other, offs)
+    M, K = x.shape
+    if K < 32 or K % 32:
+        _width(K, name)
+    if offs is None:
+        return M, K, 1, None
+    G = offs.shape[0]
+    if not 1 <= G <= MAX_GROUPS:
+        _offsets(offs)
+    return M, K, G, offs.data_ptr()
+
+
 def mxfp4_quantize_2d(x: torch.Tensor, scale_layout: int = SCALES_BLOCKED, offs: torch.Tensor | None = None):
     """Quantize x[M, K] (bf16) along K.  Returns (q [M, K/2], s): s [M, K/32] compact, or a flat
     blocked buffer whose row groups come from offs (none: one group), padding bytes zero.  offs must
     end at M: rows outside every group are not written."""
-    _tensor(x, "x", torch.bfloat16, 2)
-    M, K = x.shape
-    _width(K, "x")
-    if offs is not None:
-        _offsets(offs)
-    _cuda(x, offs)
-    G = int(offs.numel()) if offs is not None else 1
-    q, s = _u8((M, K // 2), x.device), _row_scales(x, M, K, G, scale_layout)
-    check(load().mxfp4_quantize_2d(_ptr(x), M, K, scale_layout, _ptr(offs), G, _ptr(q), _ptr(s), _raw_stream(x.device.index)),
-          "mxfp4_quantize_2d")
+    M, K, G, off = _matrix(x, "x", offs)
+    dev = x.device
+    q, s = _u8((M, K // 2), dev), _row_scales(dev, M, K, G, scale_layout)
+    check(load().mxfp4_quantize_2d(x.data_ptr(), M, K, scale_layout, off, G, q.data_ptr(), s.data_ptr(),
+                                   _raw_stream(dev.index)), "mxfp4_quantize_2d")
     return q, s
+
+
+def mxfp4_quantize_2d_mxfp8_cols(x: torch.Tensor, offs: torch.Tensor | None = None,
+                                 dev_status: torch.Tensor | None = None):
+    """Both copies of x[M, K] (bf16) that a product with an MXFP4 forward and an MXFP8 weight gradient needs, from
+    one read: (q, s) as mxfp4_quantize_2d returns them and (qT [K, M], sT) as mxfp8_quantize_2d(x, COL) does, with
+    blocked scales.  M and the group sizes multiples of 32."""
+    M, K, G, off = _matrix(x, "x", offs)
+    if M % 32:
+        raise ValueError(f"x: a multiple of 32 rows is needed, got {M}")
+    _status_word(dev_status)
+    _cuda(dev_status)
+    dev = x.device
+    q, s, qT, sT = (_u8((M, K // 2), dev), _u8(_group_bytes(M, K, G), dev), _u8((K, M), dev),
+                    _u8(_col_bytes(K, M, G), dev))
+    check(load().mxfp4_quantize_2d_mxfp8_cols(x.data_ptr(), M, K, off, G, q.data_ptr(), s.data_ptr(), qT.data_ptr(),
+                                              sT.data_ptr(), _ptr(dev_status), _raw_stream(dev.index)),
+          "mxfp4_quantize_2d_mxfp8_cols")
+    return q, s, qT, sT
 
 
 def mxfp4_swiglu_quantize(h1: torch.Tensor, h3: torch.Tensor, scale_layout: int = SCALES_BLOCKED,
                           offs: torch.Tensor | None = None):
     """h = silu(h1) * h3 of two bf16 matrices [M, K], computed in fp32 and quantized as
     mxfp4_quantize_2d does (h is not rounded to bf16 on the way).  Returns (q, s)."""
-    _tensor(h1, "h1", torch.bfloat16, 2)
-    M, K = h1.shape
-    _tensor(h3, "h3", torch.bfloat16, shape=(M, K))
-    _width(K, "h1")
-    if offs is not None:
-        _offsets(offs)
-    _cuda(h1, h3, offs)
-    G = int(offs.numel()) if offs is not None else 1
-    q, s = _u8((M, K // 2), h1.device), _row_scales(h1, M, K, G, scale_layout)
-    check(load().mxfp4_swiglu_quantize(_ptr(h1), _ptr(h3), M, K, scale_layout, _ptr(offs), G, _ptr(q), _ptr(s),
-                                       _raw_stream(h1.device.index)), "mxfp4_swiglu_quantize")
+    if h3 is None:
+        _tensor(h3, "h3", torch.bfloat16)
+    M, K, G, off = _matrix(h1, "h1", offs, h3, "h3")
+    dev = h1.device
+    q, s = _u8((M, K // 2), dev), _row_scales(dev, M, K, G, scale_layout)
+    check(load().mxfp4_swiglu_quantize(h1.data_ptr(), h3.data_ptr(), M, K, scale_layout, off, G, q.data_ptr(),
+                                       s.data_ptr(), _raw_stream(dev.index)), "mxfp4_swiglu_quantize")
     return q, s
 
 
@@ -102,19 +146,27 @@ def mxfp4_dequantize_2d(q: torch.Tensor, s: torch.Tensor, scale_layout: int = SC
                         offs: torch.Tensor | None = None) -> torch.Tensor:
     """The values [M, K] that q [M, K/2] and s (as mxfp4_quantize_2d returns them, with the same
     layout and offs) stand for, in bf16: every E2M1 value times a power of two is a bf16."""
-    _tensor(q, "q", torch.uint8, 2)
-    M, K = q.shape[0], 2 * q.shape[1]
-    _width(K, "q")
-    if offs is not None:
+    good = _good(q, torch.uint8, 2) and (offs is None or _good(offs, torch.int32, 1))
+    if not good:
+        _tensor(q, "q", torch.uint8, 2)
+    M, K = q.shape
+    K *= 2
+    if K < 32 or K % 32:
+        _width(K, "q")
+    if not good and offs is not None:
         _offsets(offs)
-    G = int(offs.numel()) if offs is not None else 1
+    G = offs.numel() if offs is not None else 1
+    if not 1 <= G <= MAX_GROUPS:
+        _offsets(offs)
     need = M * (K // 32) if scale_layout == SCALES_COMPACT else \
         (_group_bytes(M, K, G) if offs is not None else _expert_blocked_bytes(M, K))
-    _bytes_at_least(s, "s", need)
-    _cuda(q, s, offs)
-    out = torch.empty((M, K), dtype=torch.bfloat16, device=q.device)
-    check(load().mxfp4_dequantize(_ptr(q), _ptr(s), 1, M, K, scale_layout, _ptr(offs), G, _ptr(out), _raw_stream(q.device.index)),
-          "mxfp4_dequantize")
+    if not (good and _scales(s, need)):
+        _bytes_at_least(s, "s", need)
+        _cuda(q, s, offs)
+    dev = q.device
+    out = torch.empty((M, K), dtype=torch.bfloat16, device=dev)
+    check(load().mxfp4_dequantize(q.data_ptr(), s.data_ptr(), 1, M, K, scale_layout, _ptr(offs), G, out.data_ptr(),
+                                  _raw_stream(dev.index)), "mxfp4_dequantize")
     return out
 
 
@@ -135,23 +187,32 @@ def mxfp4_dequantize_3d_experts(q: torch.Tensor, s: torch.Tensor,
 def mxfp4_grouped_mm_fwd(a_q, a_s, w_q, w_s, offs, out=None, dev_status=None):
     """out[m, n] = sum_k A[m,k] W[g][n,k] for rows m of group g; a_q [M, K/2] with blocked row-group
     scales, w_q [G, N, K/2] with blocked per-expert scales; bf16 [M, N]."""
-    _tensor(a_q, "a_q", torch.uint8, 2)
-    _tensor(w_q, "w_q", torch.uint8, 3)
-    M, K = a_q.shape[0], 2 * a_q.shape[1]
-    G, N, _ = w_q.shape
-    _tensor(w_q, "w_q", torch.uint8, shape=(G, N, K // 2))
-    _width(K, "a_q")
-    _offsets(offs, G)
-    _bytes_at_least(a_s, "a_s", _group_bytes(M, K, G))
-    _bytes_at_least(w_s, "w_s", G * _expert_blocked_bytes(N, K))
-    if out is not None:
-        _tensor(out, "out", torch.bfloat16, shape=(M, N))
-    _status_word(dev_status)
-    _cuda(a_q, a_s, w_q, w_s, offs, out, dev_status)
+    good = _good(a_q, torch.uint8, 2) and _good(w_q, torch.uint8, 3) and _good(offs, torch.int32, 1)
+    if not good:
+        _tensor(a_q, "a_q", torch.uint8, 2)
+        _tensor(w_q, "w_q", torch.uint8, 3)
+    (M, Kb), (G, N, Wb) = a_q.shape, w_q.shape
+    K = 2 * Kb
+    if Wb != Kb:
+        _tensor(w_q, "w_q", torch.uint8, shape=(G, N, Kb))
+    if K < 32 or K % 32:
+        _width(K, "a_q")
+    if not good or offs.numel() != G or not 1 <= G <= MAX_GROUPS:
+        _offsets(offs, G)
+    a_bytes, w_bytes = _group_bytes(M, K, G), G * _expert_blocked_bytes(N, K)
+    if not (good and _scales(a_s, a_bytes) and _scales(w_s, w_bytes)) or out is not None or dev_status is not None:
+        _bytes_at_least(a_s, "a_s", a_bytes)
+        _bytes_at_least(w_s, "w_s", w_bytes)
+        if out is not None:
+            _tensor(out, "out", torch.bfloat16, shape=(M, N))
+        _status_word(dev_status)
+        _cuda(a_q, a_s, w_q, w_s, offs, out, dev_status)
+    dev = a_q.device
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=a_q.device)
-    check(load().mxfp4_grouped_mm_fwd(_ptr(a_q), _ptr(a_s), _ptr(w_q), _ptr(w_s), _ptr(offs), G, M, N, K, _ptr(out),
-                                      _ptr(dev_status), _raw_stream(a_q.device.index)), "mxfp4_grouped_mm_fwd")
+        out = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+    check(load().mxfp4_grouped_mm_fwd(a_q.data_ptr(), a_s.data_ptr(), w_q.data_ptr(), w_s.data_ptr(), offs.data_ptr(), G,
+                                      M, N, K, out.data_ptr(), _ptr(dev_status), _raw_stream(dev.index)),
+          "mxfp4_grouped_mm_fwd")
     return out
 
 
@@ -207,13 +268,15 @@ class _ToMxfp4ThenScaledGroupedMM(torch.autograd.Function):
             else:
                 _hold, aq, as_ = _carve(A, *a_sizes)
                 wq, ws = w_mxfp4[0].data_ptr(), w_mxfp4[1].data_ptr()
-            check(L.mxfp4_quantize_2d(A.data_ptr(), M, K, SCALES_BLOCKED, off, G, aq, as_, stream), "mxfp4_quantize_2d")
+            if need_dW:  # the token-wise MXFP8 copy for dW, half the bytes of A itself, from the same read
+                aT, aTq, aTs = _carve(A, K * M, _col_bytes(K, M, G))
+                check(L.mxfp4_quantize_2d_mxfp8_cols(A.data_ptr(), M, K, off, G, aq, as_, aTq, aTs, status, stream),
+                      "mxfp4_quantize_2d_mxfp8_cols")
+            else:
+                check(L.mxfp4_quantize_2d(A.data_ptr(), M, K, SCALES_BLOCKED, off, G, aq, as_, stream),
+                      "mxfp4_quantize_2d")
             check(L.mxfp4_grouped_mm_fwd(aq, as_, wq, ws, off, G, M, N, K, out.data_ptr(), status, stream),
                   "mxfp4_grouped_mm_fwd")
-            if need_dW:  # the token-wise MXFP8 copy for dW: half the bytes of A itself
-                aT, q, s = _carve(A, K * M, _col_bytes(K, M, G))
-                check(L.mxfp8_quantize_2d(A.data_ptr(), M, K, COL, SCALES_BLOCKED, off, G, None, None, q, s, status,
-                                          stream), "mxfp8_quantize_2d")
         if st is not None:
             read_status(st, "to_mxfp4_then_scaled_grouped_mm (group offsets)")
         ctx.save_for_backward(aT, W if need_dA else None, offs)

@@ -101,6 +101,30 @@ def test_nonfinite_blocks(mx):
     assert np.array_equal(back[~np.isnan(back)], want[~np.isnan(want)])
 
 
+@pytest.mark.parametrize("sizes,K", [([32], 32), ([96, 0, 160, 32], 288), ([128], 160), ([256, 64, 32], 416), ([544], 1056)])
+def test_quantize_2d_with_mxfp8_columns(mx, sizes, K):
+    """Row-wise MXFP4 and column-wise MXFP8 copies of one read: exact, the blocked layouts' padding included."""
+    M, ends = sum(sizes), sizes_to_ends(sizes)
+    x = hard_rows(M, K, seed=K)
+    x[3, 7], x[M - 1, K - 1], x[M - 9, 0] = float("nan"), float("inf"), -float("inf")
+    q, s, qT, sT = mx.mxfp4_quantize_2d_mxfp8_cols(x.cuda(), offs_of(sizes))
+    check_codes(q, s, f64(x), ends)
+    code, sc = ref.encode(f64(x).T, 8)
+    assert np.array_equal(u8(qT), code)
+    # a group's block columns start on a fresh tile of four
+    pad, start = [], 0
+    for n in sizes:
+        block = np.zeros((K, (n + 127) // 128 * 4), np.uint8)
+        block[:, :n // 32] = sc[:, start // 32:(start + n) // 32]
+        pad.append(block)
+        start += n
+    t = ref.tiles(np.concatenate(pad, 1))
+    assert np.array_equal(u8(sT).reshape(-1)[:t.size], t)
+    if len(sizes) == 1:
+        for a, b in zip(mx.mxfp4_quantize_2d_mxfp8_cols(x.cuda()), (q, s, qT, sT)):
+            assert a.shape == b.shape and torch.equal(a.flatten()[:512], b.flatten()[:512])
+
+
 def test_empty(mx):
     x = torch.empty((0, 64), dtype=torch.bfloat16, device="cuda")
     q, s = mx.mxfp4_quantize_2d(x)

@@ -52,6 +52,9 @@ def test_every_declared_symbol_is_exported():
 
 @pytest.mark.parametrize("call,match", [
     (lambda: mx.mxfp4_quantize_2d(bf(128, 64)), "CUDA"),
+    (lambda: mx.mxfp4_quantize_2d_mxfp8_cols(bf(128, 64)), "CUDA"),
+    (lambda: mx.mxfp4_quantize_2d_mxfp8_cols(bf(128, 48)), "multiple of 32"),
+    (lambda: mx.mxfp4_quantize_2d_mxfp8_cols(bf(128, 64), OFFS.long()), "offs"),
     (lambda: mx.mxfp4_quantize_3d_experts(bf(2, 64, 64)), "CUDA"),
     (lambda: mx.mxfp4_swiglu_quantize(bf(8, 64), bf(8, 64)), "CUDA"),
     (lambda: mx.mxfp4_dequantize_2d(u8(8, 32), u8(512)), "CUDA"),
@@ -131,6 +134,14 @@ def test_refusals_of_the_c_abi():
     assert q3(a, 0, 64, 64, 1, a, a, None) == 2
     assert q3(a, 2, 0, 64, 1, a, a, None) == 2
     assert q3(a, 2, 64, 33, 1, a, a, None) == 3
+    both = L.mxfp4_quantize_2d_mxfp8_cols
+    assert both(a, 33, 64, None, 0, a, a, a, a, None, None) == 3
+    assert both(a, 32, 48, None, 0, a, a, a, a, None, None) == 3
+    assert both(a, -32, 64, None, 0, a, a, a, a, None, None) == 2
+    assert both(a, 32, 64, a, 0, a, a, a, a, None, None) == 2
+    assert both(a, 32, 64, None, 0, a, a, None, a, None, None) == 1
+    assert both(a, 32, 64, None, 0, a, a, a, odd, None, None) == 3
+    assert both(None, 0, 64, None, 0, None, None, None, None, None, None) == 0
     dq = L.mxfp4_dequantize
     assert dq(a, a, 2, 64, 64, 1, a, 2, a, None) == 4   # row groups of several matrices
     assert dq(a, None, 1, 64, 64, 1, None, 0, a, None) == 1
