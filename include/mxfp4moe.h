@@ -40,6 +40,9 @@ extern "C" {
  *   column-wise copy (blocked).  M % 32 == 0; group sizes multiples of 32.
  * mxfp4_quantize_3d_experts -- w[G, N, K] bf16 -> q [G, N, K/2]; scales per expert,
  *   compact [N, K/32] or blocked (ceil(N/128)*128*ceil(K/128)*4 bytes each).
+ * mxfp4_quantize_3d_experts_mxfp8_cols -- the same with blocked scales, and the MXFP8
+ *   copy along N for the input gradient: qT [G, K, N], sT as mxfp8_quantize_3d_experts
+ *   writes its column-wise copy.  N % 32 == 0.
  * mxfp4_dequantize -- the values codes and scales stand for, in bf16 (exact):
  *   out [batch, M, K] from q [batch, M, K/2]; scales compact, or blocked per matrix
  *   (batch > 1 or offs NULL) or blocked with row groups (batch == 1).
@@ -51,6 +54,9 @@ mxfp8_status_t mxfp4_swiglu_quantize(const void* h1_bf16, const void* h3_bf16, i
 mxfp8_status_t mxfp4_quantize_2d_mxfp8_cols(const void* x_bf16, int64_t M, int64_t K, const int32_t* offs, int32_t G,
                                             void* q, void* s, void* qT, void* sT, int32_t* dev_status,
                                             mxfp8_stream_t stream);
+mxfp8_status_t mxfp4_quantize_3d_experts_mxfp8_cols(const void* w_bf16, int32_t G, int64_t N, int64_t K, void* q,
+                                                    void* s, void* qT, void* sT, int32_t* dev_status,
+                                                    mxfp8_stream_t stream);
 mxfp8_status_t mxfp4_quantize_3d_experts(const void* w_bf16, int32_t G, int64_t N, int64_t K, int scale_layout,
                                          void* q, void* s, mxfp8_stream_t stream);
 mxfp8_status_t mxfp4_dequantize(const void* q, const void* s, int32_t batch, int64_t M, int64_t K, int scale_layout,

@@ -31,7 +31,8 @@ __all__ = [
     "mxfp8_debug_wait_timeout", "new_status", "read_status", "to_mxfp8_then_scaled_grouped_mm", "load",
     "quantize_expert_weights", "Mxfp8WeightCache", "mxfp8_grouped_mm_swiglu_fwd", "mxfp8_swiglu_expert",
     "mxfp8_swiglu_bwd_quantize", "mxfp8_grouped_mm_dgrad2",
-    "mxfp4_quantize_2d", "mxfp4_quantize_2d_mxfp8_cols", "mxfp4_swiglu_quantize", "mxfp4_quantize_3d_experts", "mxfp4_dequantize_2d",
+    "mxfp4_quantize_2d", "mxfp4_quantize_2d_mxfp8_cols", "mxfp4_swiglu_quantize", "mxfp4_quantize_3d_experts",
+    "mxfp4_quantize_3d_experts_mxfp8_cols", "mxfp4_dequantize_2d",
     "mxfp4_dequantize_3d_experts", "mxfp4_grouped_mm_fwd", "to_mxfp4_then_scaled_grouped_mm", "MxMoeTokens",
 ]
 
@@ -500,5 +501,5 @@ from .weight_cache import Mxfp8WeightCache  # noqa: E402  (uses quantize_expert_
 from .swiglu import mxfp8_swiglu_expert  # noqa: E402
 from .mxfp4 import (mxfp4_dequantize_2d, mxfp4_dequantize_3d_experts, mxfp4_grouped_mm_fwd,  # noqa: E402
                     mxfp4_quantize_2d, mxfp4_quantize_2d_mxfp8_cols, mxfp4_quantize_3d_experts,
-                    mxfp4_swiglu_quantize, to_mxfp4_then_scaled_grouped_mm)
+                    mxfp4_quantize_3d_experts_mxfp8_cols, mxfp4_swiglu_quantize, to_mxfp4_then_scaled_grouped_mm)
 from .moe_tokens import MxMoeTokens  # noqa: E402

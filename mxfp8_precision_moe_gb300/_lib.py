@@ -73,6 +73,7 @@ def load():
         "mxfp4_quantize_2d": [P, I64, I64, INT, P, I32, P, P, P],
         "mxfp4_swiglu_quantize": [P, P, I64, I64, INT, P, I32, P, P, P],
         "mxfp4_quantize_2d_mxfp8_cols": [P, I64, I64, P, I32, P, P, P, P, P, P],
+        "mxfp4_quantize_3d_experts_mxfp8_cols": [P, I32, I64, I64, P, P, P, P, P, P],
         "mxfp4_quantize_3d_experts": [P, I32, I64, I64, INT, P, P, P],
         "mxfp4_dequantize": [P, P, I32, I64, I64, INT, P, I32, P, P],
         "mxfp4_grouped_mm_fwd": [P, P, P, P, P, I32, I64, I64, I64, P, P, P],

@@ -142,6 +142,25 @@ def mxfp4_quantize_3d_experts(w: torch.Tensor, scale_layout: int = SCALES_BLOCKE
     return q, s
 
 
+def mxfp4_quantize_3d_experts_mxfp8_cols(w: torch.Tensor, dev_status: torch.Tensor | None = None):
+    """Expert weights w[G, N, K] (bf16) for a product with an MXFP4 forward and MXFP8 gradients, from one read:
+    (q [G, N, K/2], s) as mxfp4_quantize_3d_experts returns them and (qT [G, K, N], sT) as mxfp8_quantize_3d_experts(w,
+    COL) does, with blocked scales.  N and K multiples of 32."""
+    _tensor(w, "w", torch.bfloat16, 3)
+    G, N, K = w.shape
+    _width(K, "w")
+    _width(N, "w^T")
+    _status_word(dev_status)
+    _cuda(w, dev_status)
+    dev = w.device
+    q, s, qT, sT = (_u8((G, N, K // 2), dev), _u8((G, _expert_blocked_bytes(N, K)), dev), _u8((G, K, N), dev),
+                    _u8((G, _expert_blocked_bytes(K, N)), dev))
+    check(load().mxfp4_quantize_3d_experts_mxfp8_cols(_ptr(w), G, N, K, _ptr(q), _ptr(s), _ptr(qT), _ptr(sT),
+                                                      _ptr(dev_status), _raw_stream(dev.index)),
+          "mxfp4_quantize_3d_experts_mxfp8_cols")
+    return q, s, qT, sT
+
+
 def mxfp4_dequantize_2d(q: torch.Tensor, s: torch.Tensor, scale_layout: int = SCALES_BLOCKED,
                         offs: torch.Tensor | None = None) -> torch.Tensor:
     """The values [M, K] that q [M, K/2] and s (as mxfp4_quantize_2d returns them, with the same
@@ -257,14 +276,19 @@ class _ToMxfp4ThenScaledGroupedMM(torch.autograd.Function):
         status, off = _ptr(st), offs.data_ptr()
         A = A.contiguous()
         out = torch.empty((M, N), dtype=torch.bfloat16, device=A.device)
-        aT = None
+        aT = wT = None
         if M:
             a_sizes = (M * (K // 2), _group_bytes(M, K, G))
             if w_mxfp4 is None:
                 Wc = W.contiguous()
                 _hold, aq, as_, wq, ws = _carve(A, *a_sizes, G * N * (K // 2), G * _expert_blocked_bytes(N, K))
-                check(L.mxfp4_quantize_3d_experts(Wc.data_ptr(), G, N, K, SCALES_BLOCKED, wq, ws, stream),
-                      "mxfp4_quantize_3d_experts")
+                if need_dA:  # W's copy along N for dA, from the same read
+                    wT, wTq, wTs = _carve(A, G * K * N, G * _expert_blocked_bytes(K, N))
+                    check(L.mxfp4_quantize_3d_experts_mxfp8_cols(Wc.data_ptr(), G, N, K, wq, ws, wTq, wTs, status,
+                                                                 stream), "mxfp4_quantize_3d_experts_mxfp8_cols")
+                else:
+                    check(L.mxfp4_quantize_3d_experts(Wc.data_ptr(), G, N, K, SCALES_BLOCKED, wq, ws, stream),
+                          "mxfp4_quantize_3d_experts")
             else:
                 _hold, aq, as_ = _carve(A, *a_sizes)
                 wq, ws = w_mxfp4[0].data_ptr(), w_mxfp4[1].data_ptr()
@@ -279,13 +303,13 @@ class _ToMxfp4ThenScaledGroupedMM(torch.autograd.Function):
                   "mxfp4_grouped_mm_fwd")
         if st is not None:
             read_status(st, "to_mxfp4_then_scaled_grouped_mm (group offsets)")
-        ctx.save_for_backward(aT, W if need_dA else None, offs)
+        ctx.save_for_backward(aT, wT, W if need_dA and wT is None else None, offs)
         ctx.sizes = (G, M, N, K)
         return out
 
     @staticmethod
     def backward(ctx, dOut):
-        aT, W, offs = ctx.saved_tensors
+        aT, wT, W, offs = ctx.saved_tensors
         need_dA, need_dW = ctx.needs_input_grad[:2]
         G, M, N, K = ctx.sizes
         dOut = dOut.contiguous().to(torch.bfloat16)
@@ -294,17 +318,22 @@ class _ToMxfp4ThenScaledGroupedMM(torch.autograd.Function):
             return dA, dOut.new_zeros((G, N, K)) if need_dW else None, None, None, None
         dW = torch.empty((G, N, K), dtype=torch.bfloat16, device=dOut.device) if need_dW else None
         L, stream, off = load(), _raw_stream(dOut.device.index), offs.data_ptr()
-        row = (M * N, _group_bytes(M, N, G), G * K * N, G * _expert_blocked_bytes(K, N)) if need_dA else (0,) * 4
+        row = (M * N, _group_bytes(M, N, G)) if need_dA else (0, 0)
+        w = (G * K * N, G * _expert_blocked_bytes(K, N)) if need_dA and wT is None else (0, 0)
         col = (N * M, _col_bytes(N, M, G)) if need_dW else (0, 0)
-        _hold, dq, ds, wq, ws, dTq, dTs = _carve(dOut, *row, *col)
+        _hold, dq, ds, wq, ws, dTq, dTs = _carve(dOut, *row, *w, *col)
         dirs = (ROW if need_dA else 0) | (COL if need_dW else 0)
         check(L.mxfp8_quantize_2d(dOut.data_ptr(), M, N, dirs, SCALES_BLOCKED, off, G, dq if need_dA else None,
                                   ds if need_dA else None, dTq if need_dW else None, dTs if need_dW else None, None,
                                   stream), "mxfp8_quantize_2d")
         if need_dA:
-            W = W.contiguous()
-            check(L.mxfp8_quantize_3d_experts(W.data_ptr(), G, N, K, COL, SCALES_BLOCKED, None, None, wq, ws, None,
-                                              stream), "mxfp8_quantize_3d_experts")
+            if wT is not None:
+                wq = wT.data_ptr()
+                ws = wq + (G * K * N + 255) // 256 * 256  # as _carve laid them out in the forward
+            else:
+                W = W.contiguous()
+                check(L.mxfp8_quantize_3d_experts(W.data_ptr(), G, N, K, COL, SCALES_BLOCKED, None, None, wq, ws, None,
+                                                  stream), "mxfp8_quantize_3d_experts")
             check(L.mxfp8_grouped_mm_dgrad(dq, ds, wq, ws, off, G, M, N, K, dA.data_ptr(), None, stream),
                   "mxfp8_grouped_mm_dgrad")
         if need_dW:

@@ -125,6 +125,29 @@ def test_quantize_2d_with_mxfp8_columns(mx, sizes, K):
             assert a.shape == b.shape and torch.equal(a.flatten()[:512], b.flatten()[:512])
 
 
+@pytest.mark.parametrize("G,N,K", [(1, 32, 32), (3, 160, 288), (2, 256, 160)])
+def test_quantize_experts_with_mxfp8_columns(mx, G, N, K):
+    w = hard_rows(G * N, K, seed=N + 1).reshape(G, N, K)
+    w[G - 1, 3, 7], w[0, N - 1, K - 1] = float("nan"), -float("inf")
+    q, s, qT, sT = mx.mxfp4_quantize_3d_experts_mxfp8_cols(w.cuda())
+    for g in range(G):
+        check_codes(q[g], s[g], f64(w[g]), None)
+        code, sc = ref.encode(f64(w[g]).T, 8)
+        assert np.array_equal(u8(qT[g]), code)
+        assert np.array_equal(u8(sT[g]), ref.tiles(sc))
+
+
+def test_gradient_with_weights_kept_quantized(mx):
+    """The same gradients whether W's MXFP4 copy is passed in or made on the way."""
+    A, W = synth.randn_bf16((160, 96), 1.0, seed=3).cuda(), synth.randn_bf16((2, 64, 96), 0.1, seed=4).cuda()
+    got = []
+    for q in (None, mx.mxfp4_quantize_3d_experts(W)):
+        a, w = A.clone().requires_grad_(True), W.clone().requires_grad_(True)
+        mx.to_mxfp4_then_scaled_grouped_mm(a, w, offs_of([32, 128]), w_mxfp4=q).float().square().sum().backward()
+        got.append((a.grad, w.grad))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+
+
 def test_empty(mx):
     x = torch.empty((0, 64), dtype=torch.bfloat16, device="cuda")
     q, s = mx.mxfp4_quantize_2d(x)

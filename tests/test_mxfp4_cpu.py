@@ -56,6 +56,8 @@ def test_every_declared_symbol_is_exported():
     (lambda: mx.mxfp4_quantize_2d_mxfp8_cols(bf(128, 48)), "multiple of 32"),
     (lambda: mx.mxfp4_quantize_2d_mxfp8_cols(bf(128, 64), OFFS.long()), "offs"),
     (lambda: mx.mxfp4_quantize_3d_experts(bf(2, 64, 64)), "CUDA"),
+    (lambda: mx.mxfp4_quantize_3d_experts_mxfp8_cols(bf(2, 64, 64)), "CUDA"),
+    (lambda: mx.mxfp4_quantize_3d_experts_mxfp8_cols(bf(2, 48, 64)), "multiple of 32"),
     (lambda: mx.mxfp4_swiglu_quantize(bf(8, 64), bf(8, 64)), "CUDA"),
     (lambda: mx.mxfp4_dequantize_2d(u8(8, 32), u8(512)), "CUDA"),
     (lambda: mx.mxfp4_dequantize_3d_experts(u8(2, 8, 32), u8(2, 512)), "CUDA"),
@@ -142,6 +144,12 @@ def test_refusals_of_the_c_abi():
     assert both(a, 32, 64, None, 0, a, a, None, a, None, None) == 1
     assert both(a, 32, 64, None, 0, a, a, a, odd, None, None) == 3
     assert both(None, 0, 64, None, 0, None, None, None, None, None, None) == 0
+    both = L.mxfp4_quantize_3d_experts_mxfp8_cols
+    assert both(a, 0, 32, 64, a, a, a, a, None, None) == 2
+    assert both(a, 2, 0, 64, a, a, a, a, None, None) == 2
+    assert both(a, 2, 33, 64, a, a, a, a, None, None) == 3
+    assert both(a, 2, 32, 64, a, None, a, a, None, None) == 1
+    assert both(odd, 2, 32, 64, a, a, a, a, None, None) == 3
     dq = L.mxfp4_dequantize
     assert dq(a, a, 2, 64, 64, 1, a, 2, a, None) == 4   # row groups of several matrices
     assert dq(a, None, 1, 64, 64, 1, None, 0, a, None) == 1
