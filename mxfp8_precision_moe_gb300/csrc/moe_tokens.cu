@@ -83,77 +83,124 @@ struct MtRoute {
 
 __device__ __forceinline__ void route_sync() { asm volatile("bar.sync 2, 128;" ::: "memory"); }
 
-// Top-k of every token and the list of active experts, by threads 0 .. 127 of a CTA (barrier 2); the caller
-// orders what they wrote before anyone reads it.  keys: [T][E] words of scratch memory.  setup() runs while the
-// logits are on their way.
-template <class Setup>
-__device__ __forceinline__ void mt_route(const MtParams& p, uint32_t* keys, MtRoute& r, int tid, Setup setup) {
-    const int T = p.T, E = p.E;
-    for (int i0 = tid; i0 < T * E; i0 += 8 * kMtRouteThreads) {
-        uint32_t b[8];
+// Top-k of every token, the list of active experts and the plan for their number, by threads 0 .. 127 of a CTA
+// (barrier 2); the caller orders what they wrote before anyone reads it, and adds the weights (mt_weights).
+// scratch: room for the [T][E] keys, a mask of tokens for every expert, and a plan for every number of active experts
+// that there can be: a plan takes a dozen divisions, most of a microsecond, which pass here while the logits are on
+// their way.  setup() runs then too.
+template <class Plan, class Setup, class PlanHalf>
+__device__ __forceinline__ void mt_route(const MtParams& p, uint32_t* scratch, MtRoute& r, Plan& plan, int tid, Setup setup,
+                                         PlanHalf plan_half) {
+    constexpr int kBatch = 8;  // logits in flight in a thread
+    const int T = p.T, E = p.E, n = T * E, most = min(E, T * p.top_k);
+    uint32_t* keys = scratch;
+    uint32_t* masks = keys + n;
+    Plan* plans = reinterpret_cast<Plan*>(masks + 2 * E);
+    for (int i0 = tid; i0 < n || i0 == tid; i0 += kBatch * kMtRouteThreads) {
+        uint32_t b[kBatch];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < kBatch; ++j) {
             const int i = i0 + j * kMtRouteThreads;
-            b[j] = i < T * E ? __float_as_uint(p.logits[i]) : 0u;
+            b[j] = 0;
+            if (i < n) asm volatile("ld.global.u32 %0, [%1];" : "=r"(b[j]) : "l"(p.logits + i));
+        }
+        if (i0 == tid) {
+            for (int i = tid; i < T * p.top_k; i += kMtRouteThreads) r.sel_e[i] = 0xFFFFu;
+            for (int i = tid; i < 2 * E; i += kMtRouteThreads) masks[i] = 0;
+            setup();
+            for (int a = tid; a < 2 * most; a += kMtRouteThreads) plans[a >> 1].half[a & 1] = plan_half(a & 1, (uint32_t)(a >> 1) + 1);
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < kBatch; ++j) {
             const int i = i0 + j * kMtRouteThreads;
             // unsigned keys that order as the logits do: NaN above everything, -0 equal to +0
             uint32_t k = (b[j] & 0x80000000u) ? ~b[j] : b[j] | 0x80000000u;
             if ((b[j] & 0x7FFFFFFFu) > 0x7F800000u) k = 0xFFFFFFFFu;
             if (b[j] == 0x80000000u) k = 0x80000000u;
-            if (i < T * E) keys[i] = k;
+            if (i < n) keys[i] = k;
         }
     }
-    for (int i = tid; i < T * p.top_k; i += kMtRouteThreads) r.sel_e[i] = 0xFFFFu;
-    if (tid < kMtMaxExperts / 32) r.active[tid] = 0;
-    for (int i = tid; i < 2 * kMtMaxExperts; i += kMtRouteThreads) r.mask[i >> 1][i & 1] = 0;
-    setup();
     route_sync();
-    for (int i = tid; i < T * E; i += kMtRouteThreads) {
-        const int t = i / E, e = i - t * E;
+    // i / E for i < 2^14, E <= 2^8: the error of the reciprocal times i stays under 1
+    const uint32_t inv_e = 0xFFFFFFFFu / (uint32_t)E + 1;
+    for (int i = tid; i < n; i += kMtRouteThreads) {
+        const int t = E == 1 ? i : (int)__umulhi((uint32_t)i, inv_e), e = i - t * E;
         const uint32_t k = keys[i];
         const uint32_t* row = keys + t * E;
-        int rank = 0;  // logits before this one: larger, or equal at a lower index
-#pragma unroll 8
-        for (int o = 0; o < E; ++o) rank += (row[o] > k) || (row[o] == k && o < e);
+        // logits before this one: larger, or equal at a lower index (no key is 0: -inf has the least, 0x007FFFFF)
+        int rank = 0;
+        auto count = [&](uint32_t key, int o) { rank += key > (o < e ? k - 1 : k); };
+        if (E % 4 == 0) {
+            for (int o = 0; o < E; o += 4) {
+                const uint4 q = *reinterpret_cast<const uint4*>(row + o);
+                count(q.x, o);
+                count(q.y, o + 1);
+                count(q.z, o + 2);
+                count(q.w, o + 3);
+            }
+        } else {
+            for (int o = 0; o < E; ++o) count(row[o], o);
+        }
         if (rank < p.top_k && k != 0x007FFFFFu) {  // -inf is never selected
             r.sel_e[t * p.top_k + rank] = (uint16_t)e;
             r.sel_w[t * p.top_k + rank] = __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k);  // the logit again
-            atomicOr(&r.active[e >> 5], 1u << (e & 31));
+            atomicOr(&masks[2 * e + (t >> 5)], 1u << (t & 31));
         }
     }
     route_sync();
-    if (tid < T) {
-        const uint16_t* se = r.sel_e + tid * p.top_k;
-        float* sw = r.sel_w + tid * p.top_k;
-        if (p.score == MX_SCORE_SIGMOID) {
-            for (int j = 0; j < p.top_k && se[j] != 0xFFFFu; ++j) sw[j] = 1.0f / (1.0f + expf(-sw[j]));
-        } else {
-            const float m = se[0] != 0xFFFFu ? sw[0] : 0.0f;  // the largest logit
-            float sum = 0.0f;
-            if (p.score == MX_SCORE_SOFTMAX) {
-                for (int j = 0; j < p.top_k && se[j] != 0xFFFFu; ++j) sum += expf(sw[j] - m);
-            } else {
-                for (int e = 0; e < E; ++e) sum += expf(p.logits[tid * E + e] - m);
-            }
-            for (int j = 0; j < p.top_k && se[j] != 0xFFFFu; ++j) sw[j] = expf(sw[j] - m) / sum;
+    const int lane = tid & 31, words = (E + 31) / 32;
+    for (int w = tid >> 5; w < words; w += kMtRouteThreads / 32) {
+        const int e = w * 32 + lane;
+        const uint32_t any = __ballot_sync(0xffffffffu, e < E && (masks[2 * e] | masks[2 * e + 1]) != 0);
+        if (lane == 0) r.active[w] = any;
+    }
+    route_sync();
+    int active = 0;
+    for (int w = 0; w < words; ++w) {
+        const uint32_t any = r.active[w];
+        if ((tid >> 5) == (w & (kMtRouteThreads / 32 - 1)) && ((any >> lane) & 1u)) {
+            const int e = w * 32 + lane, a = active + __popc(any & ((1u << lane) - 1u));  // the expert's place
+            r.list[a] = (uint16_t)e;
+            r.mask[a][0] = masks[2 * e];
+            r.mask[a][1] = masks[2 * e + 1];
         }
+        active += __popc(any);
     }
-    for (int i = tid; i < T * p.top_k; i += kMtRouteThreads) {
-        const int e = r.sel_e[i];
-        if (e == 0xFFFF) continue;
-        int a = __popc(r.active[e >> 5] & ((1u << (e & 31)) - 1u));  // the expert's place among the active
-        for (int w = 0; w < (e >> 5); ++w) a += __popc(r.active[w]);
-        const int t = i / p.top_k;
-        r.list[a] = (uint16_t)e;
-        atomicOr(&r.mask[a][t >> 5], 1u << (t & 31));
-    }
-    if (tid == 0) {
+    if (tid == 0) r.active_n = active;
+    constexpr int kWords = sizeof(Plan) / 4;
+    static_assert(kWords <= kMtRouteThreads, "a thread copies a word");
+    if (active && tid < kWords)
+        reinterpret_cast<uint32_t*>(&plan)[tid] = reinterpret_cast<const uint32_t*>(plans + active - 1)[tid];
+}
+
+// The selected experts' logits -> their weights, by one warp.
+__device__ __forceinline__ void mt_weights(const MtParams& p, MtRoute& r, int lane) {
+    for (int t0 = 0; t0 < p.T; t0 += 32) {
+        const int t = t0 + lane;
+        const bool in = t < p.T;
+        const uint16_t* se = r.sel_e + (in ? t : 0) * p.top_k;
+        float* sw = r.sel_w + (in ? t : 0) * p.top_k;
         int n = 0;
-        for (int w = 0; w < kMtMaxExperts / 32; ++w) n += __popc(r.active[w]);
-        r.active_n = n;
+        while (in && n < p.top_k && se[n] != 0xFFFFu) ++n;
+        if (p.score == MX_SCORE_SIGMOID) {
+            for (int j = 0; j < n; ++j) sw[j] = 1.0f / (1.0f + expf(-sw[j]));
+            continue;
+        }
+        const float m = n ? sw[0] : 0.0f;  // the largest logit
+        float sum = 0.0f;
+        if (p.score == MX_SCORE_SOFTMAX) {
+            for (int j = 0; j < n; ++j) sum += expf(sw[j] - m);
+        } else {  // over all experts: a token at a time, its logits spread over the lanes
+            for (int u = 0; u < 32 && t0 + u < p.T; ++u) {
+                const float mu = __shfl_sync(0xffffffffu, m, u);
+                float part = 0.0f;
+                for (int e = lane; e < p.E; e += 32) part += expf(p.logits[(t0 + u) * p.E + e] - mu);
+#pragma unroll
+                for (int d = 16; d; d >>= 1) part += __shfl_xor_sync(0xffffffffu, part, d);
+                if (u == lane) sum = part;
+            }
+        }
+        for (int j = 0; j < n; ++j) sw[j] = expf(sw[j] - m) / sum;
     }
 }
 
@@ -266,12 +313,14 @@ struct MtSplit {
     __device__ __forceinline__ static uint32_t div(uint64_t a, uint32_t b) {
         return a >> 32 ? (uint32_t)(a / b) : (uint32_t)a / b;  // 64-bit division is several times as long
     }
-    __device__ __forceinline__ uint32_t start(uint32_t c) const { return div((uint64_t)c * grains, n) * grain; }
+    __device__ __forceinline__ uint32_t start(uint32_t c) const {  // the first grain of run c
+        return div((uint64_t)c * grains, n);
+    }
     __device__ __forceinline__ uint32_t owner(uint32_t u) const {  // the run that holds unit u
         return div(((uint64_t)u / grain + 1) * n - 1, grains);
     }
     // whether run `c`, which holds some of the tile that begins at unit `begin`, also holds an earlier tile
-    __device__ __forceinline__ bool earlier(uint32_t c, uint32_t begin) const { return start(c) < begin; }
+    __device__ __forceinline__ bool earlier(uint32_t c, uint32_t begin) const { return start(c) * grain < begin; }
     __device__ __forceinline__ bool shared() const { return grain != per; }
 };
 
@@ -280,26 +329,56 @@ struct MtSplit {
 // rest is the wait for the next stage).  Sharing tiles evens the runs out but costs an exchange of partial sums, 7000
 // clocks under load (two trips through L2 and the gathering).  bands: 128-row bands; per: units of one of them.
 // Measured, best cut against shared tiles throughout and whole tiles throughout: one token over MXFP8 experts of
-// 8192 x 5120 35.3 us / 39.1 / 38.5, MXFP4 27.0 / 31.7 / 27.3; four tokens, top-4 of 16 MXFP8 experts of 2048 x 7168 92.8 /
+// 8192 x 5120 35.3 us / 39.1 / 38.5, MXFP4 27.0 / 31.7 / 27.3 (before other steps); four tokens, top-4 of 16 MXFP8 experts of 2048 x 7168 92.8 /
 // 92.1 / 104.9; 64 tokens over the same in MXFP4 80.7 / 89.5 / 90.8; five tokens, six experts of 160 x 352 16.0 / 21.0 / 16.1.
 constexpr float kMtHbm = 3300.0f;  // bytes a clock
 constexpr float kMtExchange = 7000.0f;
 
 __device__ __forceinline__ MtSplit mt_split(uint32_t bands, uint32_t per) {
-    if (bands == 0 || per == 0) return MtSplit{1u, 1u, 1u, 1u, 128};
     const uint32_t g = gridDim.x;
-    const float hbm = (float)per * 32768.0f / kMtHbm;  // a band's bytes at HBM's rate
-    // m rounds of a tile for every CTA, then one for the rest
-    auto rounds = [&](uint32_t tiles, float bytes, float own) -> float {
-        const uint32_t m = tiles / g, r = tiles - m * g;
+    const float hbm = (float)per * (32768.0f * (1.0f / kMtHbm));  // a band's bytes at HBM's rate
+    // m rounds of a tile for every CTA, then one for the other r tiles
+    auto rounds = [&](uint32_t m, uint32_t r, float bytes, float own) -> float {
         return (float)m * fmaxf(own, (float)g * bytes) + (r ? fmaxf(own, (float)r * bytes) : 0.0f);
     };
-    const float whole = rounds(bands, hbm, (float)per * 900.0f), half = rounds(2 * bands, 0.5f * hbm, (float)per * 800.0f);
+    const uint32_t m = bands / g, r = bands - m * g, over = 2 * r >= g ? 1 : 0;
+    const float whole = rounds(m, r, hbm, (float)per * 900.0f),
+                half = rounds(2 * m + over, 2 * r - over * g, 0.5f * hbm, (float)per * 800.0f);
     const uint32_t units = bands * per, runs = min(g, (units + 1) / 2);
-    const float cut = fmaxf((float)bands * hbm, (float)((units + runs - 1) / runs) * 900.0f) + kMtExchange;
+    const float longest = units < 2 * g ? 2.0f : (float)units / (float)g;
+    const float cut = fmaxf((float)bands * hbm, ceilf(longest) * 900.0f) + kMtExchange;
     if (whole <= half && whole <= cut) return MtSplit{bands, min(g, bands), per, per, 128};
     if (half <= cut) return MtSplit{2 * bands, min(g, 2 * bands), per, per, 64};
     return MtSplit{units, runs, 1u, per, 128};
+}
+
+// What a CTA does in one half, for one number of active experts.
+struct MtHalf {
+    MtSplit cut;
+    uint32_t u0, u1;      // its units
+    uint32_t tile, part;  // the tile they begin in, and which part of its band that is
+    uint32_t a, j;        // first half: the tile's active expert and the band of its rows; second: the active expert, and
+                          // how many units of it come before
+};
+struct MtPlan {
+    MtHalf half[2];
+};
+
+__device__ __forceinline__ MtHalf mt_half(int which, uint32_t bands, uint32_t per, uint32_t inner, uint32_t cta) {
+    MtHalf h;
+    h.cut = mt_split(bands, per);
+    const uint32_t g0 = h.cut.start(cta);
+    h.u0 = h.u1 = h.tile = h.part = h.a = h.j = 0;
+    if (cta >= h.cut.n) return h;
+    h.u0 = g0 * h.cut.grain;
+    h.u1 = h.cut.start(cta + 1) * h.cut.grain;
+    h.tile = h.cut.shared() ? h.u0 / per : g0;
+    const uint32_t sh = h.cut.rows == 64 ? 1 : 0, band = h.tile >> sh;
+    h.part = h.tile & sh;
+    const uint32_t from = which ? h.u0 - h.tile * per : band;
+    h.a = from / inner;
+    h.j = from - h.a * inner;
+    return h;
 }
 
 template <int BITS, int N>
@@ -309,6 +388,7 @@ __global__ void __launch_bounds__(kMtThreads, 1)
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t full[kMtStages], empty[kMtStages], tfull[2], tempty[2], drain;
     __shared__ MtRoute route;
+    __shared__ MtPlan plan_s;
     __shared__ float w_s[2][kMtMaxTokens];
     __shared__ uint32_t tmem_base_s, last_s;
     __shared__ int abort_s;
@@ -320,6 +400,27 @@ __global__ void __launch_bounds__(kMtThreads, 1)
     const int64_t D = p.D, H = p.H;
     const uint32_t cta = blockIdx.x;
     const int et = tid - kMtEpiWarp0 * 32;
+    const uint32_t ct_d = (uint32_t)((D + 127) / 128), ct_h = (uint32_t)((H + 127) / 128);
+    const uint32_t K1 = (uint32_t)((D + C::kKE - 1) / C::kKE), K2 = (uint32_t)((H + C::kKE - 1) / C::kKE);
+    // first half: tiles (active expert, band of H, part), units of one step; second: tiles (band of D, part), units of two
+    // steps of one active expert's H
+    const uint32_t K2u = (K2 + 1) / 2;
+    // A stage: two weight tiles, their scale tiles, two token tiles (the first half uses one), theirs.  A 64-row tile is
+    // multiplied as its half of a 128-row one: the other half is whatever lies beside it in shared memory (half a
+    // tile of room is left at both ends) and its results are not looked at.
+    struct Layout {
+        uint32_t sfa, b, sfb, bytes, edge, stages;
+        __device__ constexpr Layout(uint32_t R1, uint32_t R2)
+            : sfa(2 * (R1 > R2 ? R1 : R2) * 128), b(sfa + 2 * C::kSfTiles * 512), sfb(b + 2 * N * 128),
+              bytes(sfb + 2 * C::kSfTiles * 512), edge(R1 < 128 || R2 < 128 ? 64 * 128 : 0),
+              stages((C::kSmem - 1024 - 2 * edge) / bytes) {
+            if (stages > (uint32_t)kMtStages) stages = kMtStages;
+            if (stages > (uint32_t)(512 - C::kSfCol0) / C::kSfCols) stages = (512 - C::kSfCol0) / C::kSfCols;
+        }
+    };
+    auto plan_half = [&](int which, uint32_t A) -> MtHalf {
+        return mt_half(which, which ? ct_d : A * ct_h, which ? A * K2u : K1, which ? K2u : ct_h, cta);
+    };
 
     if (warp >= kMtEpiWarp0) {
         // ------------------------------------------------ quantize a share of x, zero the tile counters
@@ -370,7 +471,7 @@ __global__ void __launch_bounds__(kMtThreads, 1)
         routed_wait();
     } else {
         // ------------------------------------------------ routing (every CTA, the same), barriers
-        mt_route(p, reinterpret_cast<uint32_t*>(smem), route, tid, [&] {  // the keys, before the first stage is filled
+        mt_route(p, reinterpret_cast<uint32_t*>(smem), route, plan_s, tid, [&] {  // in the ring's memory, before it is filled
             if (warp == 2) {
                 if (lane == 0) {
                     for (int s = 0; s < kMtStages; ++s) {
@@ -396,10 +497,12 @@ __global__ void __launch_bounds__(kMtThreads, 1)
                 tmem_alloc(&tmem_base_s, 512);
                 tmem_relinquish();
             }
-        });
-        fence_proxy_async();  // the keys' shared memory is TMA's from here on
+        }, plan_half);
+        fence_proxy_async();  // the scratch memory is TMA's from here on
         tc_fence_before();
         route_sync();
+        if (warp == 3) mt_weights(p, route, lane);
+        __syncwarp();
         routed_arrive();
     }
     tc_fence_after();
@@ -407,24 +510,14 @@ __global__ void __launch_bounds__(kMtThreads, 1)
     const int A = __shfl_sync(0xffffffffu, route.active_n, 0);
     auto mask_of = [&](uint32_t a) -> uint64_t { return route.mask[a][0] | ((uint64_t)route.mask[a][1] << 32); };
 
-    const uint32_t ct_d = (uint32_t)((D + 127) / 128), ct_h = (uint32_t)((H + 127) / 128);
-    const uint32_t K1 = (uint32_t)((D + C::kKE - 1) / C::kKE), K2 = (uint32_t)((H + C::kKE - 1) / C::kKE);
-    // first half: tiles (active expert, band of H, part), units of one step; second: tiles (band of D, part), units of two
-    // steps of one active expert's H
-    const uint32_t K2u = (K2 + 1) / 2, AK2 = (uint32_t)A * K2u;
-    const MtSplit sp1 = mt_split((uint32_t)A * ct_h, K1), sp2 = mt_split(A ? ct_d : 0, AK2);
-    const uint32_t u1_0 = A && cta < sp1.n ? sp1.start(cta) : 0, u1_1 = A && cta < sp1.n ? sp1.start(cta + 1) : 0;
-    const uint32_t u2_0 = A && cta < sp2.n ? sp2.start(cta) : 0, u2_1 = A && cta < sp2.n ? sp2.start(cta + 1) : 0;
-    const uint32_t R1 = sp1.rows, R2 = sp2.rows, parts1 = 128 / R1, parts2 = 128 / R2;
-    // A stage: two weight tiles, their scale tiles, two token tiles (the first half uses one), theirs.  A 64-row tile is
-    // multiplied as its half of a 128-row one: the other half is whatever lies beside it in shared memory (half a
-    // tile of room is left at both ends) and its results are not looked at.
-    const uint32_t off_sfa = 2 * max(R1, R2) * 128, off_b = off_sfa + 2 * C::kSfTiles * 512;
-    const uint32_t off_sfb = off_b + 2 * N * 128, stage_bytes = off_sfb + 2 * C::kSfTiles * 512;
-    const uint32_t edge = min(R1, R2) < 128 ? 64 * 128 : 0;
-    const uint32_t stages = min(min((uint32_t)kMtStages, (uint32_t)(512 - C::kSfCol0) / C::kSfCols),
-                                (C::kSmem - 1024 - 2 * edge) / stage_bytes);
-    uint8_t* ring = smem + edge;
+    const MtHalf h1 = plan_s.half[0], h2 = plan_s.half[1];
+    const MtSplit &sp1 = h1.cut, &sp2 = h2.cut;
+    const uint32_t AK2 = (uint32_t)A * K2u, u1_0 = h1.u0, u1_1 = h1.u1, u2_0 = h2.u0, u2_1 = h2.u1;
+    const uint32_t R1 = sp1.rows, R2 = sp2.rows, parts1 = R1 == 64 ? 2 : 1, parts2 = R2 == 64 ? 2 : 1;
+    constexpr Layout both128(128, 128), both64(64, 64), mixed(128, 64);
+    const Layout lay = R1 != R2 ? mixed : R1 == 64 ? both64 : both128;
+    const uint32_t off_sfa = lay.sfa, off_b = lay.b, off_sfb = lay.sfb, stage_bytes = lay.bytes, stages = lay.stages;
+    uint8_t* ring = smem + lay.edge;
 
     const uint32_t ring_at = __shfl_sync(0xffffffffu, smem_u32(ring), 0);
 
@@ -450,15 +543,7 @@ __global__ void __launch_bounds__(kMtThreads, 1)
             at.phase ^= 1u;
         }
     };
-    // Tiles of the first half in order: (active expert a, band j of its rows, part of the band).
-    struct Tile1 {
-        uint32_t tile, a, j, part;
-    };
-    auto tile1 = [&](uint32_t u) -> Tile1 {
-        const uint32_t tile = u / K1, band = tile / parts1, a = band / ct_h;
-        return Tile1{tile, a, band - a * ct_h, tile - band * parts1};
-    };
-    auto next1 = [&](Tile1& t) {
+    auto next1 = [&](MtHalf& t) {
         ++t.tile;
         if (++t.part < parts1) return;
         t.part = 0;
@@ -466,18 +551,11 @@ __global__ void __launch_bounds__(kMtThreads, 1)
         t.j = 0;
         ++t.a;
     };
-    // The second half: runs of one tile's units that belong to one active expert a.
-    struct Tile2 {
-        uint32_t tile, a;
-    };
-    auto tile2 = [&](uint32_t u) -> Tile2 {
-        const uint32_t tile = u / AK2;
-        return Tile2{tile, (u - tile * AK2) / K2u};
-    };
-    auto next2 = [&](Tile2& t) {
+    auto next2 = [&](MtHalf& t) {
         if (++t.a < (uint32_t)A) return;
         t.a = 0;
         ++t.tile;
+        t.part ^= parts2 - 1;
     };
 
     if (A == 0) {
@@ -496,7 +574,7 @@ __global__ void __launch_bounds__(kMtThreads, 1)
             return true;
         };
         const CUtensorMap *mg = &maps.gate[parts1 - 1], *mu = &maps.up[parts1 - 1], *md = &maps.down[parts2 - 1];
-        Tile1 t1 = tile1(u1_0);
+        MtHalf t1 = h1;
         for (uint32_t u = u1_0; u < u1_1 && ok; next1(t1)) {
             const uint32_t end = min(u1_1, (t1.tile + 1) * K1);
             const uint32_t e = __shfl_sync(0xffffffffu, (uint32_t)route.list[t1.a], 0);
@@ -515,12 +593,12 @@ __global__ void __launch_bounds__(kMtThreads, 1)
                 pass(at);
             }
         }
-        Tile2 t2 = tile2(u2_0);
+        MtHalf t2 = h2;
         for (uint32_t u = u2_0; u < u2_1 && ok; next2(t2)) {
             const uint32_t base = t2.tile * AK2 + t2.a * K2u, end = min(u2_1, base + K2u);
-            const uint32_t band = t2.tile / parts2, part = t2.tile - band * parts2;
+            const uint32_t band = t2.tile >> (parts2 - 1);
             const uint32_t e = __shfl_sync(0xffffffffu, (uint32_t)route.list[t2.a], 0);
-            const int32_t row = (int32_t)((int64_t)e * D + band * 128 + part * R2);
+            const int32_t row = (int32_t)((int64_t)e * D + band * 128 + t2.part * R2);
             uint32_t k = 2 * (u - base);
             const uint8_t* sd = p.s_down + (((int64_t)e * ct_d + band) * ct_h + k * C::kSfTiles) * 512;
             for (; u < end; ++u, k += 2, sd += 2 * C::kSfTiles * 512) {
@@ -551,7 +629,7 @@ __global__ void __launch_bounds__(kMtThreads, 1)
             return true;
         };
         bool ok = __all_sync(0xffffffffu, grid_wait(kMtXDone));
-        uint32_t k = u1_0 % K1;
+        uint32_t k = u1_0 - h1.tile * K1;
         const uint8_t* s = p.xs + k * C::kSfTiles * 512;
         for (uint32_t u = u1_0; u < u1_1 && ok; ++u) {
             ok = load(&maps.x, 0, s, k, 1, ct_d);
@@ -562,8 +640,8 @@ __global__ void __launch_bounds__(kMtThreads, 1)
             }
         }
         if (ok && u2_0 < u2_1) ok = __all_sync(0xffffffffu, grid_wait(kMtHDone));
-        uint32_t a = u2_0 < u2_1 ? u2_0 % AK2 / K2u : 0;
-        k = u2_0 < u2_1 ? 2 * (u2_0 % K2u) : 0;  // AK2 is a multiple of K2u
+        uint32_t a = h2.a;
+        k = 2 * h2.j;
         s = p.hs + ((int64_t)a * ct_h + k * C::kSfTiles) * 512;
         for (uint32_t u = u2_0; u < u2_1 && ok; ++u) {
             ok = load(&maps.h, (int32_t)a, s, k, k + 1 < K2 ? 2 : 1, ct_h);
@@ -625,7 +703,7 @@ __global__ void __launch_bounds__(kMtThreads, 1)
                 pass(at);
             };
             bool ok = true;
-            Tile1 t1 = tile1(u1_0);
+            MtHalf t1 = h1;
             for (uint32_t u = u1_0; u < u1_1 && ok; next1(t1)) {
                 const uint32_t end = min(u1_1, (t1.tile + 1) * K1), back = t1.part * R1 * 8;
                 if (!(ok = open())) break;
@@ -652,10 +730,10 @@ __global__ void __launch_bounds__(kMtThreads, 1)
                 }
                 if (ok) close();
             }
-            Tile2 t2 = tile2(u2_0);
+            MtHalf t2 = h2;
             for (uint32_t u = u2_0; u < u2_1 && ok; next2(t2)) {
                 const uint32_t base = t2.tile * AK2 + t2.a * K2u, end = min(u2_1, base + K2u);
-                const uint32_t back = (t2.tile & (parts2 - 1)) * R2 * 8;
+                const uint32_t back = t2.part * R2 * 8;
                 if (!(ok = open())) break;
                 const uint32_t d0 = tm + buf * 2 * N;
                 for (uint32_t k = 2 * (u - base), acc = 0; u < end; ++u, k += 2) {
@@ -714,9 +792,11 @@ __global__ void __launch_bounds__(kMtThreads, 1)
         // 8-11: tensor memory and the partial sums are both addressed by column, so nothing is done for the others
         // and the code stays a short loop (unrolled over all columns it did not fit the instruction cache).
         constexpr int kCols = 4;
+        MtHalf t1 = h1;
         for (uint32_t u = u1_0; u < u1_1 && ok;) {
-            const uint32_t tile = u / K1, band = tile / parts1, a = band / ct_h, j = band - a * ct_h;
-            const uint32_t end = min(u1_1, (tile + 1) * K1), r0 = (tile & (parts1 - 1)) * R1;
+            const uint32_t tile = t1.tile, a = t1.a, j = t1.j;
+            const uint32_t end = min(u1_1, (tile + 1) * K1), r0 = t1.part * R1;
+            next1(t1);
             const bool whole = u == tile * K1 && end == (tile + 1) * K1;
             u = end;
             ok = epi_all(mbar_wait_bounded<true>(&tfull[buf], buf_phase, p.timeout_ns, abort_flag, p.dev_status));
@@ -854,15 +934,16 @@ __global__ void __launch_bounds__(kMtThreads, 1)
         constexpr int NC = N / 2;  // token columns of this warp
         const int c0 = cg * NC;
         float total[NC];
+        MtHalf t2 = h2;
         for (uint32_t u = u2_0; u < u2_1 && ok;) {
-            const uint32_t tile = u / AK2, t_end = min(u2_1, (tile + 1) * AK2);
+            const uint32_t tile = t2.tile, t_end = min(u2_1, (tile + 1) * AK2);
             const bool whole = u == tile * AK2 && t_end == (tile + 1) * AK2;
-            const uint32_t band = tile / parts2, r0 = (tile & (parts2 - 1)) * R2;
+            const uint32_t band = tile >> (parts2 - 1), r0 = t2.part * R2;
             const bool mine = quarter * 32 >= r0 && quarter * 32 < r0 + R2;
 #pragma unroll
             for (int c = 0; c < NC; ++c) total[c] = 0.0f;
-            uint32_t a = (u - tile * AK2) / K2u;
-            for (; u < t_end; ++a) {
+            for (; u < t_end; next2(t2)) {
+                const uint32_t a = t2.a;
                 u = min(t_end, tile * AK2 + (a + 1) * K2u);
                 if (et < T) {  // token et's weight for this expert
                     const int e = route.list[a];
