@@ -74,7 +74,6 @@ __device__ __forceinline__ uint32_t ld_acquire(const uint32_t* p) {
 // The routing tables, in shared memory.
 struct MtRoute {
     uint32_t mask[kMtMaxExperts][2];            // tokens of each active expert, a bit each
-    uint32_t active[kMtMaxExperts / 32];        // experts that some token selected
     float sel_w[kMtMaxTokens * kMtMaxTopK];     // the selected experts' logits, then their weights
     uint16_t sel_e[kMtMaxTokens * kMtMaxTopK];  // a token's experts [T][top_k], best first (0xFFFF: none)
     uint16_t list[kMtMaxExperts];               // active experts, ascending
@@ -83,19 +82,32 @@ struct MtRoute {
 
 __device__ __forceinline__ void route_sync() { asm volatile("bar.sync 2, 128;" ::: "memory"); }
 
+// The scratch memory of the routing: the [T][E] keys, a mask of tokens for every expert, and a plan for every number of
+// active experts that there can be.  (A plan takes a dozen divisions, most of a microsecond: the epilogue warps make
+// them while the routing warps find out the number.)
+template <class Plan>
+struct MtScratch {
+    uint32_t *keys, *masks;
+    Plan* plans;
+    int most;  // active experts at most
+    __device__ __forceinline__ MtScratch(void* at, const MtParams& p)
+        : keys(static_cast<uint32_t*>(at)), masks(keys + p.T * p.E), plans(reinterpret_cast<Plan*>(masks + 2 * p.E)),
+          most(min(p.E, p.T * p.top_k)) {}
+};
+
+// Barrier 4: the routing warps go on once the epilogue warps have made the plans.
+__device__ __forceinline__ void plans_arrive() { asm volatile("bar.arrive 4, 384;" ::: "memory"); }
+__device__ __forceinline__ void plans_wait() { asm volatile("bar.sync 4, 384;" ::: "memory"); }
+
 // Top-k of every token, the list of active experts and the plan for their number, by threads 0 .. 127 of a CTA
 // (barrier 2); the caller orders what they wrote before anyone reads it, and adds the weights (mt_weights).
-// scratch: room for the [T][E] keys, a mask of tokens for every expert, and a plan for every number of active experts
-// that there can be: a plan takes a dozen divisions, most of a microsecond, which pass here while the logits are on
-// their way.  setup() runs then too.
-template <class Plan, class Setup, class PlanHalf>
-__device__ __forceinline__ void mt_route(const MtParams& p, uint32_t* scratch, MtRoute& r, Plan& plan, int tid, Setup setup,
-                                         PlanHalf plan_half) {
+// setup() runs while the logits are on their way.
+template <class Plan, class Setup>
+__device__ __forceinline__ void mt_route(const MtParams& p, const MtScratch<Plan>& scratch, MtRoute& r, Plan& plan, int tid,
+                                         Setup setup) {
     constexpr int kBatch = 8;  // logits in flight in a thread
-    const int T = p.T, E = p.E, n = T * E, most = min(E, T * p.top_k);
-    uint32_t* keys = scratch;
-    uint32_t* masks = keys + n;
-    Plan* plans = reinterpret_cast<Plan*>(masks + 2 * E);
+    const int T = p.T, E = p.E, n = T * E;
+    uint32_t *keys = scratch.keys, *masks = scratch.masks;
     for (int i0 = tid; i0 < n || i0 == tid; i0 += kBatch * kMtRouteThreads) {
         uint32_t b[kBatch];
 #pragma unroll
@@ -108,7 +120,6 @@ __device__ __forceinline__ void mt_route(const MtParams& p, uint32_t* scratch, M
             for (int i = tid; i < T * p.top_k; i += kMtRouteThreads) r.sel_e[i] = 0xFFFFu;
             for (int i = tid; i < 2 * E; i += kMtRouteThreads) masks[i] = 0;
             setup();
-            for (int a = tid; a < 2 * most; a += kMtRouteThreads) plans[a >> 1].half[a & 1] = plan_half(a & 1, (uint32_t)(a >> 1) + 1);
         }
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
@@ -147,22 +158,18 @@ __device__ __forceinline__ void mt_route(const MtParams& p, uint32_t* scratch, M
             atomicOr(&masks[2 * e + (t >> 5)], 1u << (t & 31));
         }
     }
-    route_sync();
-    const int lane = tid & 31, words = (E + 31) / 32;
-    for (int w = tid >> 5; w < words; w += kMtRouteThreads / 32) {
-        const int e = w * 32 + lane;
-        const uint32_t any = __ballot_sync(0xffffffffu, e < E && (masks[2 * e] | masks[2 * e + 1]) != 0);
-        if (lane == 0) r.active[w] = any;
-    }
-    route_sync();
+    plans_wait();  // of the routing warps too
+    const int lane = tid & 31;
     int active = 0;
-    for (int w = 0; w < words; ++w) {
-        const uint32_t any = r.active[w];
-        if ((tid >> 5) == (w & (kMtRouteThreads / 32 - 1)) && ((any >> lane) & 1u)) {
-            const int e = w * 32 + lane, a = active + __popc(any & ((1u << lane) - 1u));  // the expert's place
+    for (int e0 = 0; e0 < E; e0 += 32) {  // every warp counts them all, and lists its share
+        const int e = e0 + lane;
+        const uint32_t m0 = e < E ? masks[2 * e] : 0u, m1 = e < E ? masks[2 * e + 1] : 0u;
+        const uint32_t any = __ballot_sync(0xffffffffu, (m0 | m1) != 0);
+        if ((m0 | m1) != 0 && (tid >> 5) == ((e0 >> 5) & (kMtRouteThreads / 32 - 1))) {
+            const int a = active + __popc(any & ((1u << lane) - 1u));  // the expert's place
             r.list[a] = (uint16_t)e;
-            r.mask[a][0] = masks[2 * e];
-            r.mask[a][1] = masks[2 * e + 1];
+            r.mask[a][0] = m0;
+            r.mask[a][1] = m1;
         }
         active += __popc(any);
     }
@@ -170,7 +177,7 @@ __device__ __forceinline__ void mt_route(const MtParams& p, uint32_t* scratch, M
     constexpr int kWords = sizeof(Plan) / 4;
     static_assert(kWords <= kMtRouteThreads, "a thread copies a word");
     if (active && tid < kWords)
-        reinterpret_cast<uint32_t*>(&plan)[tid] = reinterpret_cast<const uint32_t*>(plans + active - 1)[tid];
+        reinterpret_cast<uint32_t*>(&plan)[tid] = reinterpret_cast<const uint32_t*>(scratch.plans + active - 1)[tid];
 }
 
 // The selected experts' logits -> their weights, by one warp.
@@ -418,11 +425,17 @@ __global__ void __launch_bounds__(kMtThreads, 1)
             if (stages > (uint32_t)(512 - C::kSfCol0) / C::kSfCols) stages = (512 - C::kSfCol0) / C::kSfCols;
         }
     };
-    auto plan_half = [&](int which, uint32_t A) -> MtHalf {
-        return mt_half(which, which ? ct_d : A * ct_h, which ? A * K2u : K1, which ? K2u : ct_h, cta);
-    };
+    const MtScratch<MtPlan> scratch(smem, p);  // in the ring's memory, before it is filled
 
     if (warp >= kMtEpiWarp0) {
+        // ------------------------------------------------ plans, by the last warps
+        for (int i = kMtEpiThreads - 1 - et; i < 2 * scratch.most; i += kMtEpiThreads) {
+            const uint32_t A = (uint32_t)(i >> 1) + 1;
+            scratch.plans[i >> 1].half[i & 1] =
+                mt_half(i & 1, i & 1 ? ct_d : A * ct_h, i & 1 ? A * K2u : K1, i & 1 ? K2u : ct_h, cta);
+        }
+        __syncwarp();
+        plans_arrive();
         // ------------------------------------------------ quantize a share of x, zero the tile counters
         // (before any weight is asked for: x's loads would wait behind megabytes of them)
         const int64_t per_row = D / 8, items = T * per_row;  // 8 elements each; 4 neighbours make a block
@@ -471,7 +484,7 @@ __global__ void __launch_bounds__(kMtThreads, 1)
         routed_wait();
     } else {
         // ------------------------------------------------ routing (every CTA, the same), barriers
-        mt_route(p, reinterpret_cast<uint32_t*>(smem), route, plan_s, tid, [&] {  // in the ring's memory, before it is filled
+        mt_route(p, scratch, route, plan_s, tid, [&] {
             if (warp == 2) {
                 if (lane == 0) {
                     for (int s = 0; s < kMtStages; ++s) {
@@ -497,7 +510,7 @@ __global__ void __launch_bounds__(kMtThreads, 1)
                 tmem_alloc(&tmem_base_s, 512);
                 tmem_relinquish();
             }
-        }, plan_half);
+        });
         fence_proxy_async();  // the scratch memory is TMA's from here on
         tc_fence_before();
         route_sync();
