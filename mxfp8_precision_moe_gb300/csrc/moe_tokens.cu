@@ -475,10 +475,9 @@ __global__ void __launch_bounds__(kMtThreads, 1)
             }
         }
         for (int i = cta * kMtEpiThreads + et; i < p.ncounters; i += gridDim.x * kMtEpiThreads) p.counters[i] = 0;
-        fence_proxy_async();
         epi_sync();
         if (et == 0) {
-            __threadfence();
+            __threadfence();  // (the proxy fence is the reader's)
             atomicAdd(p.header + kMtXDone, 1u);
         }
         routed_wait();
@@ -801,10 +800,13 @@ __global__ void __launch_bounds__(kMtThreads, 1)
         };
 
         // ------------------------------------------------ first half: gate, up, SwiGLU, quantize h
-        // Token columns are taken kCols at a time from those the expert's mask names, the odd batches by warps
-        // 8-11: tensor memory and the partial sums are both addressed by column, so nothing is done for the others
-        // and the code stays a short loop (unrolled over all columns it did not fit the instruction cache).
-        constexpr int kCols = 4;
+        // Token columns are those that the expert's mask names, one at a time and the odd ones by warps 8-11: tensor
+        // memory and the partial sums are both addressed by column, so nothing is done for the others, and the code
+        // stays short (four columns at a time, it took 1 us longer to get through once: instruction fetches).
+        auto columns = [&](uint64_t left, auto&& f) {
+            for (int turn = 0; left; left &= left - 1, ++turn)
+                if ((turn & 1) == cg) f(__ffsll(left) - 1);
+        };
         MtHalf t1 = h1;
         for (uint32_t u = u1_0; u < u1_1 && ok;) {
             const uint32_t tile = t1.tile, a = t1.a, j = t1.j;
@@ -817,83 +819,37 @@ __global__ void __launch_bounds__(kMtThreads, 1)
             tc_fence_after();
             const uint64_t mask = mask_of(a);
             const uint32_t acc = lane_base + buf * 2 * N;
-            // the next batch of columns: their indexes (the last repeated), and how many
-            auto batch = [&](uint64_t& left, int (&col)[kCols]) -> int {
-                int n = 0;
-#pragma unroll
-                for (int i = 0; i < kCols; ++i) {
-                    if (left) {
-                        col[i] = __ffsll(left) - 1;
-                        left &= left - 1;
-                        n = i + 1;
-                    } else {
-                        col[i] = i ? col[i - 1] : 0;
-                    }
-                }
-                return n;
-            };
-            auto from_tmem = [&](const int (&col)[kCols], float (&g)[kCols], float (&h)[kCols]) {
-                uint32_t x[kCols], y[kCols];
-#pragma unroll
-                for (int i = 0; i < kCols; ++i) {
-                    x[i] = tmem_ld_col(acc + col[i]);
-                    y[i] = tmem_ld_col(acc + N + col[i]);
-                }
-                tmem_ld_wait();
-#pragma unroll
-                for (int i = 0; i < kCols; ++i) {
-                    asm volatile("" : "+r"(x[i]), "+r"(y[i]));  // not before the wait
-                    g[i] = __uint_as_float(x[i]);
-                    h[i] = __uint_as_float(y[i]);
-                }
-            };
-            // SwiGLU and quantization of n columns; the warp's 32 rows are one block of a token's h
+            // SwiGLU and quantization of a column; the warp's 32 rows are one block of the token's h
             const int64_t row = (int64_t)j * 128 + r;
             const bool mine = quarter * 32 >= r0 && quarter * 32 < r0 + R1;  // this warp's rows are in the tile
             const bool in = row < H;
-            auto finish = [&](const int (&col)[kCols], int n, const float (&g)[kCols], const float (&h)[kCols]) {
-                float v[kCols];
-                uint32_t m[kCols];
-#pragma unroll
-                for (int i = 0; i < kCols; ++i) {
-                    v[i] = in ? g[i] / (1.0f + expf(-g[i])) * h[i] : 0.0f;
-                    m[i] = __reduce_max_sync(0xffffffffu, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+            auto finish = [&](int col, float g, float h) {
+                const float v = in ? g / (1.0f + expf(-g)) * h : 0.0f;
+                const uint32_t s = e8m0_of<BITS == 8 ? 8 : 2>(__reduce_max_sync(0xffffffffu, __float_as_uint(v) & 0x7FFFFFFFu));
+                const float f = s == 0xFFu ? __uint_as_float(0x7FC00000u) : __uint_as_float((254u - s) << 23);
+                const int64_t at = (int64_t)a * T + col;
+                if constexpr (BITS == 8) {
+                    if (in) p.hq[at * H + row] = (uint8_t)cvt_e4m3x2(v * f, 0.0f);
+                } else {
+                    const float next = __shfl_down_sync(0xffffffffu, v * f, 1);
+                    if (in && (lane & 1) == 0) p.hq[at * (H / 2) + row / 2] = cvt_e2m1x2(v * f, next);
                 }
-#pragma unroll
-                for (int i = 0; i < kCols; ++i) {
-                    const uint32_t s = e8m0_of<BITS == 8 ? 8 : 2>(m[i]);
-                    const float f = s == 0xFFu ? __uint_as_float(0x7FC00000u) : __uint_as_float((254u - s) << 23);
-                    const int64_t at = (int64_t)a * T + col[i];
-                    if constexpr (BITS == 8) {
-                        if (in && i < n) p.hq[at * H + row] = (uint8_t)cvt_e4m3x2(v[i] * f, 0.0f);
-                    } else {
-                        const float q8[8] = {v[i] * f, __shfl_down_sync(0xffffffffu, v[i] * f, 1), 0, 0, 0, 0, 0, 0};
-                        if (in && i < n && (lane & 1) == 0) p.hq[at * (H / 2) + row / 2] = (uint8_t)cvt_e2m1x8(q8);
-                    }
-                    if (lane == 0 && i < n)
-                        p.hs[((int64_t)a * ct_h + j) * 512 + (col[i] & 31) * 16 + (col[i] >> 5) * 4 + quarter] =
-                            (uint8_t)(in ? s : 0u);
-                }
+                if (lane == 0)
+                    p.hs[((int64_t)a * ct_h + j) * 512 + (col & 31) * 16 + (col >> 5) * 4 + quarter] = (uint8_t)(in ? s : 0u);
             };
             float* own = slot(cta, u1_0 < tile * K1);
-            uint64_t left = mine ? mask : 0;
-            for (int turn = 0; left; ++turn) {
-                int col[kCols];
-                const int n = batch(left, col);
-                if ((turn & 1) != cg) continue;
-                float g[kCols], h[kCols];
-                from_tmem(col, g, h);
+            columns(mine ? mask : 0, [&](int col) {
+                uint32_t x = tmem_ld_col(acc + col), y = tmem_ld_col(acc + N + col);
+                tmem_ld_wait();
+                asm volatile("" : "+r"(x), "+r"(y));  // not before the wait
+                const float g = __uint_as_float(x), h = __uint_as_float(y);
                 if (whole) {
-                    finish(col, n, g, h);
+                    finish(col, g, h);
                 } else {
-#pragma unroll
-                    for (int i = 0; i < kCols; ++i)
-                        if (i < n) {
-                            __stcg(own + col[i] * 128 + r, g[i]);
-                            __stcg(own + (T + col[i]) * 128 + r, h[i]);
-                        }
+                    __stcg(own + col * 128 + r, g);
+                    __stcg(own + (T + col) * 128 + r, h);
                 }
-            }
+            });
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&tempty[buf]);
@@ -902,40 +858,28 @@ __global__ void __launch_bounds__(kMtThreads, 1)
             const uint32_t lo = sp1.owner(tile * K1), hi = sp1.owner((tile + 1) * K1 - 1);
             const bool lo_second = sp1.earlier(lo, tile * K1);  // the others begin in this tile
             if (!arrive_last(p.counters + tile, hi - lo + 1)) continue;
-            left = mask;
-            for (int turn = 0; left; ++turn) {
-                int col[kCols];
-                const int n = batch(left, col);
-                if ((turn & 1) != cg) continue;
-                float g[kCols], h[kCols];
-#pragma unroll
-                for (int i = 0; i < kCols; ++i) g[i] = h[i] = 0.0f;
-                constexpr int kRuns = 4;  // runs whose sums are in flight together
+            columns(mask, [&](int col) {
+                float g = 0.0f, h = 0.0f;
+                constexpr int kRuns = 8;  // runs whose sums are in flight together
                 for (uint32_t o = lo; o <= hi; o += kRuns) {
-                    float v[kRuns][kCols], w[kRuns][kCols];
+                    float v[kRuns], w[kRuns];
 #pragma unroll
                     for (int x = 0; x < kRuns; ++x) {
                         const bool have = o + x <= hi;
                         const float* q = slot(o + x, o + x == lo && lo_second);
-#pragma unroll
-                        for (int i = 0; i < kCols; ++i) {
-                            v[x][i] = w[x][i] = 0.0f;
-                            ld_if(v[x][i], q + col[i] * 128 + r, have && i < n);
-                            ld_if(w[x][i], q + (T + col[i]) * 128 + r, have && i < n);
-                        }
+                        v[x] = w[x] = 0.0f;
+                        ld_if(v[x], q + col * 128 + r, have);
+                        ld_if(w[x], q + (T + col) * 128 + r, have);
                     }
 #pragma unroll
-                    for (int x = 0; x < kRuns; ++x)
-#pragma unroll
-                        for (int i = 0; i < kCols; ++i) {
-                            g[i] += v[x][i];
-                            h[i] += w[x][i];
-                        }
+                    for (int x = 0; x < kRuns; ++x) {
+                        g += v[x];
+                        h += w[x];
+                    }
                 }
-                finish(col, n, g, h);
-            }
+                finish(col, g, h);
+            });
         }
-        fence_proxy_async();
         epi_sync();
         if (et == 0) {
             __threadfence();

@@ -36,6 +36,15 @@ __device__ __forceinline__ uint32_t cvt_e2m1x8(const float (&v)[8]) {
     return r;
 }
 
+// Two of them: one byte.
+__device__ __forceinline__ uint8_t cvt_e2m1x2(float lo, float hi) {
+    uint32_t r;
+    asm("{\n\t.reg .b8 b;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %2, %1;\n\tmov.b32 %0, {b, b, b, b};\n\t}"
+        : "=r"(r)
+        : "f"(lo), "f"(hi));
+    return (uint8_t)r;
+}
+
 // The E2M1 codes of a non-finite block: 7 with each element's sign.
 __device__ __forceinline__ uint32_t nonfinite_e2m1x8(const float (&v)[8]) {
     uint32_t r = 0;
