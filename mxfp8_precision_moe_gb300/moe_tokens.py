@@ -31,8 +31,8 @@ class MxMoeTokens:
 
     score: "softmax" (over the selected experts), "softmax_all" (over all experts) or "sigmoid".
 
-    The layer holds references to the weights and one workspace for each stream it is called on.
-    It computes no gradients."""
+    The layer holds references to the weights and one workspace for each stream it is called on (a call
+    captured into a graph takes one of the graph's memory).  It computes no gradients."""
 
     def __init__(self, gate, up, down, top_k: int, *, score: str = "softmax", max_tokens: int = MAX_TOKENS):
         pairs = []
@@ -77,18 +77,20 @@ class MxMoeTokens:
             raise ValueError("the layer is too large for the kernel's 32-bit tile counts")
         self._fixed = (E, D, H, self.top_k, SCORES[score], bits) + tuple(t.data_ptr() for w in pairs for t in w)
         self._workspaces: dict[int, torch.Tensor] = {}
-        self._captured: list[torch.Tensor] = []
 
-    def _workspace(self, stream: int) -> torch.Tensor:
-        ws = self._workspaces.get(stream)
-        if ws is not None:
-            return ws
+    def _new_workspace(self) -> torch.Tensor:
         ws = torch.empty(self._bytes, dtype=torch.uint8, device=self.device)
         ws[:256].zero_()  # the grid barrier; every launch leaves it at zero
+        return ws
+
+    def _workspace(self, stream: int) -> torch.Tensor:
+        # A captured call gets memory of its graph's pool, zeroed by the graph: the graph may run on any stream, beside
+        # eager calls on the one that it was captured on.
         if torch.cuda.is_current_stream_capturing():
-            self._captured.append(ws)  # a graph's own: its zeroing is part of the graph
-        else:
-            self._workspaces[stream] = ws
+            return self._new_workspace()
+        ws = self._workspaces.get(stream)
+        if ws is None:
+            ws = self._workspaces[stream] = self._new_workspace()
         return ws
 
     def __call__(self, x: torch.Tensor, router_logits: torch.Tensor, out: torch.Tensor | None = None,

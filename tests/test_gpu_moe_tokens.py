@@ -255,6 +255,29 @@ def test_graph(mx):
         assert torch.equal(y, lay.op(nx, nl))
 
 
+def test_graph_beside_eager_calls_of_its_stream(mx):
+    """A graph captured on a stream that has run the layer eagerly shares no workspace with those calls."""
+    lay = Layer(mx, 4, 256, 128, 2, 8)
+    a, b = inputs(5, 256, 4, seed=5), inputs(7, 256, 4, seed=6)
+    want = lay.op(*a), lay.op(*b)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        lay.op(*a)
+    torch.cuda.synchronize()
+    held = {k: v.data_ptr() for k, v in lay.op._workspaces.items()}
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        y = [lay.op(*a) for _ in range(3)]
+    assert {k: v.data_ptr() for k, v in lay.op._workspaces.items()} == held
+    for _ in range(20):
+        graph.replay()
+        with torch.cuda.stream(side):
+            z = lay.op(*b)
+    torch.cuda.synchronize()
+    assert all(torch.equal(v, want[0]) for v in y) and torch.equal(z, want[1])
+
+
 def test_refusals(mx):
     lay = Layer(mx, 4, 128, 64, 2, 8)
     x, logits = inputs(3, 128, 4)
