@@ -79,6 +79,7 @@ struct F4Tile {
     int64_t sfa_chunk, sfb_chunk;     // scale tile (512 bytes) of K element 0; 128-row chunk of B
     __nv_bfloat16* out;               // first element of this CTA's 128 rows
     int valid_rows, valid_cols;
+    int rows;                         // of both CTAs together
 };
 
 // Tile t seen from CTA `half` of the pair.  pt_s: 128-row padded tiles before each group (scale bands);
@@ -105,12 +106,15 @@ __device__ __forceinline__ F4Tile f4_tile(const F4Params& p, int64_t t, int half
     ti.sfa_chunk = (pt_s[g] + min64(2 * m + half, (size + 127) / 128 - 1)) * ct;
     ti.sfb_chunk = (int64_t)g * nchunk + 2 * n;
     ti.out = p.out + ti.a_row * p.N + n * 256;
-    ti.valid_rows = (int)max64(0, min64(128, size - rows0));
+    ti.rows = (int)min64(256, size - m * 256);
+    ti.valid_rows = max(0, min(128, ti.rows - half * 128));
     ti.valid_cols = (int)min64(256, p.N - n * 256);
     return ti;
 }
 
-template <int STAGES>
+// SHORT: groups of few rows.  A is copied in boxes of 32 rows, those that the group reaches: what stays in the rest of
+// a stage meets only rows that are masked at the store.
+template <int STAGES, bool SHORT>
 __global__ void __launch_bounds__(kF4Threads, 1)
     mxfp4_grouped_mm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
                             const __grid_constant__ CUtensorMap tmap_sfa,
@@ -229,14 +233,27 @@ __global__ void __launch_bounds__(kF4Threads, 1)
             const int32_t b_row = __shfl_sync(0xffffffffu, (int32_t)ti.b_row, 0);
             const int32_t sfa = __shfl_sync(0xffffffffu, (int32_t)(2 * ti.sfa_chunk), 0);
             const int32_t sfb = __shfl_sync(0xffffffffu, (int32_t)ti.sfb_chunk, 0);
+            int boxes = 0;  // 32-row boxes of this CTA's A
+            uint32_t tx = C::kTx;
+            if constexpr (SHORT) {
+                const int rows = __shfl_sync(0xffffffffu, ti.rows, 0), even = (min(rows, 128) + 31) / 32,
+                          odd = (max(rows - 128, 0) + 31) / 32;
+                boxes = leader ? even : odd;
+                tx -= (8 - even - odd) * (32 * 128);
+            }
             for (int kt = 0; kt < k_tiles; ++kt) {
                 if (!wait(&empty[stage], phase ^ 1u)) {
                     ok = false;
                     break;
                 }
                 const uint32_t fb = cluster_addr(&full[stage], 0);
-                if (leader) expect_tx(one, &full[stage], C::kTx);
-                load_2d_pair(one, ring + stage * C::kABytes, &tmap_a, kt * 128, a_row, fb);
+                if (leader) expect_tx(one, &full[stage], tx);
+                if constexpr (SHORT) {
+                    for (int i = 0; i < boxes; ++i)
+                        load_2d_pair(one, ring + stage * C::kABytes + i * (32 * 128), &tmap_a, kt * 128, a_row + 32 * i, fb);
+                } else {
+                    load_2d_pair(one, ring + stage * C::kABytes, &tmap_a, kt * 128, a_row, fb);
+                }
                 load_2d_pair(one, ring + C::kOffB + stage * C::kBBytes, &tmap_b, kt * 128, b_row, fb);
                 // two scale tiles a copy (an odd count's last copy reads one tile further, which nothing uses)
                 load_2d_pair(one, ring + C::kOffSfa + stage * C::kSfaBytes, &tmap_sfa, 0, sfa + 4 * kt, fb);
@@ -412,12 +429,12 @@ static bool f4_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int STAGES>
+template <int STAGES, bool SHORT>
 static mxfp8_status_t f4_launch(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& msa,
                                 const CUtensorMap& msb, const F4Params& p, int clusters, cudaStream_t st) {
     using C = CfgF4<STAGES>;
     static std::atomic<int> attr_set[host::kMaxDevices];
-    if (!host::ensure_smem(reinterpret_cast<const void*>(mxfp4_grouped_mm_kernel<STAGES>), C::kMost, attr_set))
+    if (!host::ensure_smem(reinterpret_cast<const void*>(mxfp4_grouped_mm_kernel<STAGES, SHORT>), C::kMost, attr_set))
         return MXFP8_ERR_LAUNCH;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
@@ -431,7 +448,7 @@ static mxfp8_status_t f4_launch(const CUtensorMap& ma, const CUtensorMap& mb, co
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, mxfp4_grouped_mm_kernel<STAGES>, ma, mb, msa, msb, p) != cudaSuccess) {
+    if (cudaLaunchKernelEx(&cfg, mxfp4_grouped_mm_kernel<STAGES, SHORT>, ma, mb, msa, msb, p) != cudaSuccess) {
         cudaGetLastError();
         return MXFP8_ERR_LAUNCH;
     }
@@ -459,8 +476,11 @@ extern "C" mxfp8_status_t mxfp4_grouped_mm_fwd(const void* a_q, const void* a_s,
     const int64_t sfa_rows = ((M + 127) / 128 + G) * ct * 2, sfb_rows = (int64_t)G * ((N + 127) / 128) * ct * 2;
     if (sfa_rows > INT32_MAX - 4 || sfb_rows > INT32_MAX - 4) return MXFP8_ERR_SHAPE;  // TMA coordinates
     if (mxfp8_status_t a = host::check_arch(); a != MXFP8_OK) return a;
+    // Groups of 64 rows and less on average: 16 groups of one row, N = 2048, K = 7168 take 30 us in place of 36, others the
+    // same time; for longer ones the count of boxes costs the issuing warp 2%.
+    const bool few = M <= 64 * (int64_t)G;
     CUtensorMap ma, mb, msa, msb;
-    if (!f4_map(&ma, a_q, M, K / 2, 128, 128, true) || !f4_map(&mb, w_q, (int64_t)G * N, K / 2, 128, 128, true) ||
+    if (!f4_map(&ma, a_q, M, K / 2, few ? 32 : 128, 128, true) || !f4_map(&mb, w_q, (int64_t)G * N, K / 2, 128, 128, true) ||
         !f4_map(&msa, a_s, sfa_rows, 256, 4, 256, false) || !f4_map(&msb, w_s, ct * 2, 256, 4, 256, false, (int64_t)G * ((N + 127) / 128), 2))
         return MXFP8_ERR_DRIVER;
     F4Params p{};
@@ -475,6 +495,9 @@ extern "C" mxfp8_status_t mxfp4_grouped_mm_fwd(const void* a_q, const void* a_s,
     const int64_t bound = ((M + 255) / 256 + G) * ((N + 255) / 256);
     const int clusters = (int)max64(1, min64(bound, host::num_sms() / 2));
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    return G <= CfgF4<6>::kMostGroups ? f4_launch<6>(ma, mb, msa, msb, p, clusters, st)
-                                      : f4_launch<5>(ma, mb, msa, msb, p, clusters, st);
+    if (G > CfgF4<6>::kMostGroups)
+        return few ? f4_launch<5, true>(ma, mb, msa, msb, p, clusters, st)
+                   : f4_launch<5, false>(ma, mb, msa, msb, p, clusters, st);
+    return few ? f4_launch<6, true>(ma, mb, msa, msb, p, clusters, st)
+               : f4_launch<6, false>(ma, mb, msa, msb, p, clusters, st);
 }

@@ -223,6 +223,15 @@ def test_product(mx, sizes, N, K):
         start += n
 
 
+@pytest.mark.parametrize("sizes,N,K", [
+    ([300] + [0] * 7, 96, 288), ([200, 1, 31, 32, 33, 0, 2], 288, 160), ([64, 64], 512, 544), ([97, 2, 3], 256, 1056),
+    ([1, 0] * 150, 32, 64), ([128, 0], 64, 96), ([129] + [1] * 6, 64, 96),
+])
+def test_product_of_short_groups(mx, sizes, N, K):
+    """64 rows a group and less on average, though single groups may be long (and more than 256 groups)."""
+    test_product(mx, sizes, N, K)
+
+
 def test_product_keeps_nonfinite_blocks_to_their_rows(mx):
     """A NaN in one token or one expert reaches that token's rows and that expert's columns only."""
     sizes, N, K = [40, 50, 60], 64, 320
