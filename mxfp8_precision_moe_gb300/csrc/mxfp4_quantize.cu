@@ -11,10 +11,10 @@
 //             two that join a row's four scale bytes into one word.  Against four lanes a block this halves
 //             the instructions per element: [16, 8192, 5120] takes 260 us instead of 303, 6.5 TB/s, which
 //             is HBM's copy rate.  Five CTAs an SM; six spill, four leave loads too few.
-//   SwiGLU    two threads a block, to fit six CTAs an SM.  expf and the correctly rounded division make 25 of
-//             about 32 instructions an element, so it is bound by issue slots, not HBM: 171 us for 16384 x 8192,
-//             3.6 TB/s (a block a thread 174-197 us, four lanes a block 169-190).  A cheaper exponential or
-//             division would move values across E2M1's wide rounding borders; it is not taken.
+//   SwiGLU    two threads a block, to fit six CTAs an SM.  Bound by issue slots more than by HBM: 129 us for
+//             16384 x 8192, 4.7 TB/s, with the quotient as a product with a reciprocal (silu2) in instructions of two
+//             values; with the correctly rounded division 170 us (a block a thread 174-197 us then, four lanes
+//             a block 169-190; five or seven CTAs 135 and 131 now).
 //   inverse   four lanes a block: 16-byte stores of 8 values, whole 32-byte sectors by neighbouring lanes.
 //             274 us for [16, 8192, 5120], 6.2 TB/s (write-heavy traffic).
 
@@ -127,6 +127,33 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
     return d;
 }
 
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float rcp_approx(float x) {  // within 1 ulp
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// a / (1 + e^-a) of two values, as a/4 times the reciprocal of y = (1 + e^-a) / 4: that has no subnormal reciprocal
+// below the largest finite e^-a.  One step of Newton's iteration, r + r (1 - y r), brings the reciprocal from 1 ulp to
+// half of one, so that the whole is off by at most 2^-24 for the sum, the reciprocal and the product each, and
+// expf's 2 ulp.  Where e^-a overflows, r is 0 and stays 0 (y is cut to a finite value in the step, 0 times it being 0):
+// the result is -0, and NaN for a = -inf, as of the division.
+__device__ __forceinline__ float2 silu2(float a, float b) {
+    const float2 quarter = make_float2(0.25f, 0.25f);
+    const float2 y = fma2(make_float2(expf(-a), expf(-b)), quarter, quarter);
+    const float2 r = make_float2(rcp_approx(y.x), rcp_approx(y.y));
+    const float2 e = fma2(make_float2(-fminf(y.x, 3.4e38f), -fminf(y.y, 3.4e38f)), r, make_float2(1.0f, 1.0f));
+    return mul2(mul2(make_float2(a, b), quarter), fma2(r, e, r));
+}
+
 // EPT elements of a block (the other 32 / EPT - 1 shares are the neighbouring lanes') of silu(w) * g in fp32 -> the
 // block's scale byte, this share's codes in c.
 template <int EPT>
@@ -137,8 +164,7 @@ __device__ __forceinline__ uint32_t q4_share_swiglu(const uint32_t (&w)[EPT / 2]
 #pragma unroll
     for (int i = 0; i < EPT / 2; ++i) {
         const float a = bf16lo(w[i]), b = bf16hi(w[i]);
-        const float2 h = mul2(make_float2(a / (1.0f + expf(-a)), b / (1.0f + expf(-b))),
-                              make_float2(bf16lo(g[i]), bf16hi(g[i])));
+        const float2 h = mul2(silu2(a, b), make_float2(bf16lo(g[i]), bf16hi(g[i])));
         v[2 * i] = h.x;
         v[2 * i + 1] = h.y;
         m = max(m, max(__float_as_uint(h.x) & 0x7FFFFFFFu, __float_as_uint(h.y) & 0x7FFFFFFFu));

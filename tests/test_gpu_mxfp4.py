@@ -194,6 +194,37 @@ def test_swiglu_quantize(mx, sizes, K):
     assert agree[firm].all() and firm.mean() > 0.99
 
 
+def test_swiglu_extremes(mx):
+    """Blocks of one pair each: exponentials that overflow or vanish, subnormals, the largest values, infinities, NaN."""
+    one = [0.0, -0.0, 1e-40, 2.0 ** -126, 0.3, 20.0, 87.0, 90.0, 1e30, 3.3e38]
+    gate = torch.tensor([s * v for v in one for s in (1, -1)] + [-86.5, -87.5, -88.5, -100.0, -1000.0]).bfloat16()
+    up = torch.tensor([1.0, -3.0, 1e-30, 7e29, 0.0]).bfloat16()
+    h1 = gate.repeat_interleave(len(up)).repeat_interleave(32).reshape(-1, 32).cuda()
+    h3 = up.repeat(len(gate)).repeat_interleave(32).reshape(-1, 32).cuda()
+    q, s = mx.mxfp4_swiglu_quantize(h1, h3, mx.SCALES_COMPACT)
+    # the formula in 32 bits: e^-a overflows above 88.73, as it is meant to
+    a = f64(h1).astype(np.float32)
+    with np.errstate(over="ignore", invalid="ignore", under="ignore", divide="ignore"):
+        silu = (a / (1 + np.exp(-a).astype(np.float32))).astype(np.float64)
+        v = silu * f64(h3)
+        big = np.abs(v) > 3.4e38
+        v[big] = np.copysign(np.inf, v[big])
+        code, sc = ref.encode(v, 4)
+        firm = np.ones(len(v), bool)
+        for d in (1 - 8 * 2.0 ** -24, 1 + 8 * 2.0 ** -24):
+            c, x = ref.encode(v * d, 4)
+            firm &= (c == code).all(1) & (x == sc).all(1)
+    firm &= (np.abs(v) > 2.0 ** -125).all(1) | (v == 0).all(1)   # below, the 32-bit product is rounded to a subnormal
+    got = ref.unpack(u8(q))
+    same = (got == code) | (((got & 7) == 0) & ((code & 7) == 0))
+    assert firm.sum() > 60 and same[firm].all() and np.array_equal(u8(s)[firm], sc[firm])
+    bad = torch.tensor([float("inf"), -float("inf"), float("nan"), 2.0]).bfloat16().repeat_interleave(32).reshape(-1, 32)
+    other = torch.tensor([2.0, 2.0, 2.0, -float("inf")]).bfloat16().repeat_interleave(32).reshape(-1, 32)
+    q, s = mx.mxfp4_swiglu_quantize(bad.cuda(), other.cuda(), mx.SCALES_COMPACT)
+    assert (u8(s) == 255).all() and ((ref.unpack(u8(q)) & 7) == 7).all()
+    assert (ref.unpack(u8(q))[0] == 7).all() and (ref.unpack(u8(q))[3] == 15).all()
+
+
 def product_bound(a, w, K):
     """bf16 rounding of the result, and a 32-bit sum of K exact products in any order."""
     return lambda o: 2.0 ** -8 * np.abs(o) + K * 2.0 ** -23 * (np.abs(a) @ np.abs(w).T)
