@@ -11,10 +11,10 @@
 //             two that join a row's four scale bytes into one word.  Against four lanes a block this halves
 //             the instructions per element: [16, 8192, 5120] takes 260 us instead of 303, 6.5 TB/s, which
 //             is HBM's copy rate.  Five CTAs an SM; six spill, four leave loads too few.
-//   SwiGLU    two threads a block, to fit six CTAs an SM.  Bound by issue slots more than by HBM: 129 us for
-//             16384 x 8192, 4.7 TB/s, with the quotient as a product with a reciprocal (silu2) in instructions of two
+//   SwiGLU    two threads a block, to fit six CTAs an SM.  Bound by issue slots more than by HBM: 126 us for
+//             16384 x 8192, 4.8 TB/s, with the quotient as a product with a reciprocal (silu2) in instructions of two
 //             values; with the correctly rounded division 170 us (a block a thread 174-197 us then, four lanes
-//             a block 169-190; five or seven CTAs 135 and 131 now).
+//             a block 169-190; five or seven CTAs 135 and 129 now).
 //   inverse   four lanes a block: 16-byte stores of 8 values, whole 32-byte sectors by neighbouring lanes.
 //             274 us for [16, 8192, 5120], 6.2 TB/s (write-heavy traffic).
 
@@ -160,15 +160,16 @@ template <int EPT>
 __device__ __forceinline__ uint32_t q4_share_swiglu(const uint32_t (&w)[EPT / 2], const uint32_t (&g)[EPT / 2],
                                                     uint32_t (&c)[EPT / 8]) {
     float v[EPT];
-    uint32_t m = 0;
+    float top = 0.0f;
 #pragma unroll
     for (int i = 0; i < EPT / 2; ++i) {
         const float a = bf16lo(w[i]), b = bf16hi(w[i]);
         const float2 h = mul2(silu2(a, b), make_float2(bf16lo(g[i]), bf16hi(g[i])));
         v[2 * i] = h.x;
         v[2 * i + 1] = h.y;
-        m = max(m, max(__float_as_uint(h.x) & 0x7FFFFFFFu, __float_as_uint(h.y) & 0x7FFFFFFFu));
+        asm("max.NaN.abs.f32 %0, %0, %1, %2;" : "+f"(top) : "f"(h.x), "f"(h.y));  // NaN wins
     }
+    uint32_t m = __float_as_uint(top);
 #pragma unroll
     for (int d = 1; d < 32 / EPT; d <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
     const uint32_t s = e8m0_of<2>(m);
