@@ -131,6 +131,18 @@ def test_cuts(mx, T, E, D, H, k, bits):
     lay.check(*inputs(T, D, E, seed=T + 1))
 
 
+@pytest.mark.parametrize("T,E,k", [(64, 256, 8), (1, 256, 16), (33, 97, 3), (7, 30, 1), (5, 29, 1), (64, 64, 4), (40, 128, 16)])
+@pytest.mark.parametrize("score", ["softmax", "softmax_all"])
+def test_many_experts(mx, T, E, k, score):
+    """Many experts, with equal logits, -inf and a token that has fewer finite logits than it may select."""
+    lay = Layer(mx, E, 64, 32, k, 8, score=score)
+    x, logits = inputs(T, 64, E, seed=E)
+    logits[:, ::3] = 0.25
+    logits[T // 2, 1:] = -float("inf")
+    logits[:, E - 1] = -float("inf")
+    lay.check(x, logits)
+
+
 @pytest.mark.parametrize("bits", [8, 4])
 def test_wide_layer(mx, bits):
     """Many tiles and steps: runs that begin and end inside tiles, several experts a run."""
