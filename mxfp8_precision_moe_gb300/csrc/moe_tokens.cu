@@ -36,6 +36,7 @@ constexpr int kMtMaxTokens = 64;
 constexpr int kMtMaxExperts = 256;
 constexpr int kMtMaxTopK = 16;
 constexpr int kMtRouteThreads = 128;
+constexpr int kMtThreads = 384;
 constexpr int kMtHeader = 256;  // workspace bytes before the tile counters
 
 // Words of the workspace's header: CTAs that have arrived at each grid-wide point.  One word each: a CTA does not
@@ -97,7 +98,101 @@ struct MtScratch {
 
 // Barrier 4: the routing warps go on once the epilogue warps have made the plans.
 __device__ __forceinline__ void plans_arrive() { asm volatile("bar.arrive 4, 384;" ::: "memory"); }
+// Barrier 5: the keys, where the epilogue warps take a share of the selection.
+__device__ __forceinline__ void keys_sync() { asm volatile("bar.sync 5, 384;" ::: "memory"); }
 __device__ __forceinline__ void plans_wait() { asm volatile("bar.sync 4, 384;" ::: "memory"); }
+
+constexpr int kMtFewLogits = 8 * kMtRouteThreads;  // as many as the routing warps load at once
+// Whether the epilogue warps take a share of the selection: for more logits than that, it is worth waiting for them.
+__device__ __forceinline__ bool mt_shared_selection(const MtParams& p) { return p.T * p.E > kMtFewLogits; }
+
+__device__ __forceinline__ float mt_logit(uint32_t key) {  // the logit that a key was made of
+    return __uint_as_float((key & 0x80000000u) ? key ^ 0x80000000u : ~key);
+}
+
+// Every token's top_k experts out of the keys, by `threads` threads: sel_e, sel_w (the logits) and the experts' masks.
+// Up to 32 experts, every logit's rank among its token's: T E^2 comparisons, of which a thread makes four at a time.  More
+// experts: a warp holds a token's keys, KEYS in a lane, and takes its best top_k times, 100 to 400 clocks a round.
+// 64 tokens over small experts, the layer with ranks and with rounds: top 4 of 16 21.3 and 22.5 us, top 8 of 64 41 and 27, top 8
+// of 256 272 and 48.
+__device__ __forceinline__ void mt_rank(const uint32_t* keys, uint32_t* masks, MtRoute& r, int T, int E, int top_k, int tid,
+                                        int threads) {
+    // i / E for i < 2^14, E <= 2^8: the error of the reciprocal times i stays under 1
+    const uint32_t inv_e = 0xFFFFFFFFu / (uint32_t)E + 1;
+    for (int i = tid; i < T * E; i += threads) {
+        const int t = E == 1 ? i : (int)__umulhi((uint32_t)i, inv_e), e = i - t * E;
+        const uint32_t k = keys[i];
+        const uint32_t* row = keys + t * E;
+        // logits before this one: larger, or equal at a lower index (no key is 0: -inf has the least, 0x007FFFFF)
+        int rank = 0;
+        auto count = [&](uint32_t key, int o) { rank += key > (o < e ? k - 1 : k); };
+        if (E % 4 == 0) {
+            for (int o = 0; o < E; o += 4) {
+                const uint4 q = *reinterpret_cast<const uint4*>(row + o);
+                count(q.x, o);
+                count(q.y, o + 1);
+                count(q.z, o + 2);
+                count(q.w, o + 3);
+            }
+        } else {
+            for (int o = 0; o < E; ++o) count(row[o], o);
+        }
+        if (rank < top_k && k != 0x007FFFFFu) {  // -inf is never selected
+            r.sel_e[t * top_k + rank] = (uint16_t)e;
+            r.sel_w[t * top_k + rank] = mt_logit(k);
+            atomicOr(&masks[2 * e + (t >> 5)], 1u << (t & 31));
+        }
+    }
+}
+template <int KEYS>
+__device__ __forceinline__ void mt_rounds(const uint32_t* keys, uint32_t* masks, MtRoute& r, int T, int E, int top_k, int tid,
+                                          int threads) {
+    const int lane = tid & 31;
+    for (int t = tid >> 5; t < T; t += threads / 32) {
+        uint32_t k[KEYS];
+#pragma unroll
+        for (int j = 0; j < KEYS; ++j) k[j] = lane + 32 * j < E ? keys[t * E + lane + 32 * j] : 0u;
+        uint32_t my_e = 0, my_key = 0;  // lane `place` keeps what round `place` took
+        for (int place = 0; place < top_k; ++place) {
+            uint32_t best = k[0];
+#pragma unroll
+            for (int j = 1; j < KEYS; ++j) best = max(best, k[j]);
+            best = __reduce_max_sync(0xffffffffu, best);
+            if (best <= 0x007FFFFFu) break;  // only -inf is left (padding has 0)
+            uint32_t e = 0;  // of equal ones the first
+#pragma unroll
+            for (int j = KEYS - 1; j >= 0; --j) {
+                const uint32_t have = __ballot_sync(0xffffffffu, k[j] == best);
+                if (have) e = 32 * j + __ffs(have) - 1;
+            }
+#pragma unroll
+            for (int j = 0; j < KEYS; ++j)
+                if (e == (uint32_t)(lane + 32 * j)) k[j] = 0u;
+            if (lane == place) {
+                my_e = e;
+                my_key = best;
+            }
+        }
+        if (my_key) {
+            r.sel_e[t * top_k + lane] = (uint16_t)my_e;
+            r.sel_w[t * top_k + lane] = mt_logit(my_key);
+            atomicOr(&masks[2 * my_e + (t >> 5)], 1u << (t & 31));
+        }
+        __syncwarp();
+    }
+}
+__device__ __forceinline__ void mt_select(const uint32_t* keys, uint32_t* masks, MtRoute& r, int T, int E, int k, int tid,
+                                          int threads) {
+    if (E <= 32) mt_rank(keys, masks, r, T, E, k, tid, threads);
+    else if (E <= 64) mt_rounds<2>(keys, masks, r, T, E, k, tid, threads);
+    else if (E <= 128) mt_rounds<4>(keys, masks, r, T, E, k, tid, threads);
+    else mt_rounds<8>(keys, masks, r, T, E, k, tid, threads);
+}
+// (Not inlined: it would stand in the way of the code around it, in both kinds of warps.)
+__device__ __noinline__ void mt_select_shared(const uint32_t* keys, uint32_t* masks, MtRoute& r, int T, int E, int k,
+                                              int tid) {
+    mt_select(keys, masks, r, T, E, k, tid, kMtThreads);
+}
 
 // Top-k of every token, the list of active experts and the plan for their number, by threads 0 .. 127 of a CTA
 // (barrier 2); the caller orders what they wrote before anyone reads it, and adds the weights (mt_weights).
@@ -105,90 +200,42 @@ __device__ __forceinline__ void plans_wait() { asm volatile("bar.sync 4, 384;" :
 template <class Plan, class Setup>
 __device__ __forceinline__ void mt_route(const MtParams& p, const MtScratch<Plan>& scratch, MtRoute& r, Plan& plan, int tid,
                                          Setup setup) {
-    constexpr int kBatch = 8;  // logits in flight in a thread
-    const int T = p.T, E = p.E, n = T * E;
+    const int E = p.E, n = p.T * E;
     uint32_t *keys = scratch.keys, *masks = scratch.masks;
-    for (int i0 = tid; i0 < n || i0 == tid; i0 += kBatch * kMtRouteThreads) {
-        uint32_t b[kBatch];
+    uint32_t b[8];  // the first kMtFewLogits; the rest straight to shared memory
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-            const int i = i0 + j * kMtRouteThreads;
-            b[j] = 0;
-            if (i < n) asm volatile("ld.global.u32 %0, [%1];" : "=r"(b[j]) : "l"(p.logits + i));
-        }
-        if (i0 == tid) {
-            for (int i = tid; i < T * p.top_k; i += kMtRouteThreads) r.sel_e[i] = 0xFFFFu;
-            for (int i = tid; i < 2 * E; i += kMtRouteThreads) masks[i] = 0;
-            setup();
-        }
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-            const int i = i0 + j * kMtRouteThreads;
-            // unsigned keys that order as the logits do: NaN above everything, -0 equal to +0
-            uint32_t k = (b[j] & 0x80000000u) ? ~b[j] : b[j] | 0x80000000u;
-            if ((b[j] & 0x7FFFFFFFu) > 0x7F800000u) k = 0xFFFFFFFFu;
-            if (b[j] == 0x80000000u) k = 0x80000000u;
-            if (i < n) keys[i] = k;
-        }
+    for (int j = 0; j < 8; ++j) {
+        const int i = tid + j * kMtRouteThreads;
+        b[j] = 0;
+        if (i < n) asm volatile("ld.global.u32 %0, [%1];" : "=r"(b[j]) : "l"(p.logits + i));
     }
-    route_sync();
-    auto select = [&](int t, int place, int e, uint32_t key) {
-        r.sel_e[t * p.top_k + place] = (uint16_t)e;
-        r.sel_w[t * p.top_k + place] = __uint_as_float((key & 0x80000000u) ? key ^ 0x80000000u : ~key);  // the logit again
-        atomicOr(&masks[2 * e + (t >> 5)], 1u << (t & 31));
+    for (int i = tid + kMtFewLogits; i < n; i += kMtRouteThreads)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(keys + i)), "l"(p.logits + i) : "memory");
+    for (int i = tid; i < p.T * p.top_k; i += kMtRouteThreads) r.sel_e[i] = 0xFFFFu;
+    for (int i = tid; i < 2 * E; i += kMtRouteThreads) masks[i] = 0;
+    setup();
+    // unsigned keys that order as the logits do: NaN above everything, -0 equal to +0
+    auto key_of = [](uint32_t v) -> uint32_t {
+        uint32_t k = (v & 0x80000000u) ? ~v : v | 0x80000000u;
+        if ((v & 0x7FFFFFFFu) > 0x7F800000u) k = 0xFFFFFFFFu;
+        if (v == 0x80000000u) k = 0x80000000u;
+        return k;
     };
-    // Few experts: every logit's rank, T E^2 comparisons over the threads.  Many: top_k rounds of a maximum over a warp
-    // that holds a token's keys, about 80 clocks each.  64 tokens, top 8 of 256 small experts: the layer takes 272 us with ranks, 57 with rounds;
-    // of 64 experts 39.3 and 40.0.
-    if (E * E > 850 * p.top_k) {
-        constexpr int kKeys = kMtMaxExperts / 32;
-        const int lane = tid & 31;
-        for (int t = tid >> 5; t < T; t += kMtRouteThreads / 32) {
-            uint32_t k[kKeys];
 #pragma unroll
-            for (int j = 0; j < kKeys; ++j) k[j] = lane + 32 * j < E ? keys[t * E + lane + 32 * j] : 0u;
-            for (int place = 0; place < p.top_k; ++place) {
-                uint32_t best = k[0];
-#pragma unroll
-                for (int j = 1; j < kKeys; ++j) best = max(best, k[j]);
-                best = __reduce_max_sync(0xffffffffu, best);
-                if (best <= 0x007FFFFFu) break;  // only -inf is left
-                uint32_t e = ~0u;  // of equal ones the first
-#pragma unroll
-                for (int j = kKeys - 1; j >= 0; --j) e = k[j] == best ? (uint32_t)(lane + 32 * j) : e;
-                e = __reduce_min_sync(0xffffffffu, e);
-#pragma unroll
-                for (int j = 0; j < kKeys; ++j) k[j] = e == (uint32_t)(lane + 32 * j) ? 0u : k[j];
-                if (lane == 0) select(t, place, (int)e, best);
-            }
-        }
-    } else {
-        // i / E for i < 2^14, E <= 2^8: the error of the reciprocal times i stays under 1
-        const uint32_t inv_e = 0xFFFFFFFFu / (uint32_t)E + 1;
-        for (int i = tid; i < n; i += kMtRouteThreads) {
-            const int t = E == 1 ? i : (int)__umulhi((uint32_t)i, inv_e), e = i - t * E;
-            const uint32_t k = keys[i];
-            const uint32_t* row = keys + t * E;
-            // logits before this one: larger, or equal at a lower index (no key is 0: -inf has the least, 0x007FFFFF)
-            int rank = 0;
-            auto count = [&](uint32_t key, int o) { rank += key > (o < e ? k - 1 : k); };
-            if (E % 4 == 0) {
-                for (int o = 0; o < E; o += 4) {
-                    const uint4 q = *reinterpret_cast<const uint4*>(row + o);
-                    count(q.x, o);
-                    count(q.y, o + 1);
-                    count(q.z, o + 2);
-                    count(q.w, o + 3);
-                }
-            } else {
-                for (int o = 0; o < E; ++o) count(row[o], o);
-            }
-            if (rank < p.top_k && k != 0x007FFFFFu) {  // -inf is never selected
-                select(t, rank, e, k);
-            }
-        }
+    for (int j = 0; j < 8; ++j) {
+        const int i = tid + j * kMtRouteThreads;
+        if (i < n) keys[i] = key_of(b[j]);
     }
-    plans_wait();  // of the routing warps too
+    if (mt_shared_selection(p)) {
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        for (int i = tid + kMtFewLogits; i < n; i += kMtRouteThreads) keys[i] = key_of(keys[i]);
+        keys_sync();
+        mt_select_shared(keys, masks, r, p.T, E, p.top_k, tid);
+    } else {
+        route_sync();
+        mt_select(keys, masks, r, p.T, E, p.top_k, tid, kMtRouteThreads);
+    }
+    plans_wait();  // and the masks, of all that made them
     const int lane = tid & 31;
     int active = 0;
     for (int e0 = 0; e0 < E; e0 += 32) {  // every warp counts them all, and lists its share
@@ -265,7 +312,6 @@ __device__ __forceinline__ void mt_leave(const MtParams& p) {
     }
 }
 
-constexpr int kMtThreads = 384;
 constexpr int kMtEpiWarp0 = 4;
 constexpr int kMtEpiThreads = 256;
 constexpr int kMtStatic = 10 * 1024;  // static shared memory at most
@@ -464,8 +510,9 @@ __global__ void __launch_bounds__(kMtThreads, 1)
             scratch.plans[i >> 1].half[i & 1] =
                 mt_half(i & 1, i & 1 ? ct_d : A * ct_h, i & 1 ? A * K2u : K1, i & 1 ? K2u : ct_h, cta);
         }
+        const bool shared = mt_shared_selection(p);
         __syncwarp();
-        plans_arrive();
+        if (!shared) plans_arrive();
         // ------------------------------------------------ quantize a share of x, zero the tile counters
         // (before any weight is asked for: x's loads would wait behind megabytes of them)
         const int64_t per_row = D / 8, items = T * per_row;  // 8 elements each; 4 neighbours make a block
@@ -509,6 +556,12 @@ __global__ void __launch_bounds__(kMtThreads, 1)
         if (et == 0) {
             __threadfence();  // (the proxy fence is the reader's)
             atomicAdd(p.header + kMtXDone, 1u);
+        }
+        if (shared) {
+            keys_sync();
+            mt_select_shared(scratch.keys, scratch.masks, route, T, p.E, p.top_k, tid);
+            __syncwarp();
+            plans_arrive();
         }
         routed_wait();
     } else {
