@@ -24,7 +24,9 @@
 //   warp 1      token producer (quantized x or h and their scales); waits at the two grid-wide points:
 //               x is quantized, h is complete
 //   warp 2      tensor-core issuer: scale copies into tensor memory, then the block-scaled MMAs
-//   warps 4-11  quantize this CTA's share of x; then the epilogues
+//   warps 4-11  plan the CTA's work for every number of experts that may turn out selected, quantize its share of x
+//               (and, for many logits, select experts with the rest); then the epilogues
+//   warps 0-3   route first, every CTA the same
 // Every wait is bounded by time (MXFP8_ERR_TIMEOUT and an orderly exit).
 
 #include "host_common.h"
