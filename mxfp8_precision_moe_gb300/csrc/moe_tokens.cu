@@ -410,16 +410,17 @@ struct MtSplit {
 };
 
 // The cut that should take least, by clocks.  A half's bytes take their time at HBM's rate; a run takes its own on its
-// SM, 800 clocks a unit of 64-row tiles and 900 of 128-row tiles (the products of a unit are issued in 350 to 500, the
-// rest is the wait for the next stage).  Sharing tiles evens the runs out but costs an exchange of partial sums, 7000
-// clocks under load (two trips through L2 and the gathering).  bands: 128-row bands; per: units of one of them.
-// Measured, best cut against shared tiles throughout and whole tiles throughout: one token over MXFP8 experts of
-// 8192 x 5120 35.3 us / 39.1 / 38.5, MXFP4 27.0 / 31.7 / 27.3 (before other steps); four tokens, top-4 of 16 MXFP8 experts of 2048 x 7168 92.8 /
-// 92.1 / 104.9; 64 tokens over the same in MXFP4 80.7 / 89.5 / 90.8; five tokens, six experts of 160 x 352 16.0 / 21.0 / 16.1.
+// SM, 900 clocks a unit of 128-row tiles and `half_unit` one of 64-row tiles (600 with 16 token columns, 800 with more: the
+// products of a unit are issued in 250 to 500, the rest is the wait for the next stage).  Sharing tiles evens the runs out but
+// costs an exchange of partial sums, 7000 clocks under load (two trips through L2 and the gathering).  bands: 128-row
+// bands; per: units of one of them.  Measured, best cut against shared tiles throughout and whole tiles throughout: one token
+// over MXFP4 experts of 8192 x 5120 23.2 us / 27.4 / 23.4; four tokens, top 4 of 16 MXFP8 experts of 2048 x 7168 89.6 / 88.5 / 89.9;
+// 64 tokens over the same in MXFP4 77 / 89 / 83; five tokens, six experts of 160 x 352 14.0 / 20.1 / 14.7.  With 800 for 16 columns
+// too: eight tokens over eight experts of 1024 x 4096 28.2 in place of 26.2, two tokens over 16 of 1536 x 4096 24.8, not 25.9.
 constexpr float kMtHbm = 3300.0f;  // bytes a clock
 constexpr float kMtExchange = 7000.0f;
 
-__device__ __forceinline__ MtSplit mt_split(uint32_t bands, uint32_t per) {
+__device__ __forceinline__ MtSplit mt_split(uint32_t bands, uint32_t per, float half_unit) {
     const uint32_t g = gridDim.x;
     const float hbm = (float)per * (32768.0f * (1.0f / kMtHbm));  // a band's bytes at HBM's rate
     // m rounds of a tile for every CTA, then one for the other r tiles
@@ -428,7 +429,7 @@ __device__ __forceinline__ MtSplit mt_split(uint32_t bands, uint32_t per) {
     };
     const uint32_t m = bands / g, r = bands - m * g, over = 2 * r >= g ? 1 : 0;
     const float whole = rounds(m, r, hbm, (float)per * 900.0f),
-                half = rounds(2 * m + over, 2 * r - over * g, 0.5f * hbm, (float)per * 800.0f);
+                half = rounds(2 * m + over, 2 * r - over * g, 0.5f * hbm, (float)per * half_unit);
     const uint32_t units = bands * per, runs = min(g, (units + 1) / 2);
     const float longest = units < 2 * g ? 2.0f : (float)units / (float)g;
     const float cut = fmaxf((float)bands * hbm, ceilf(longest) * 900.0f) + kMtExchange;
@@ -449,9 +450,10 @@ struct MtPlan {
     MtHalf half[2];
 };
 
-__device__ __forceinline__ MtHalf mt_half(int which, uint32_t bands, uint32_t per, uint32_t inner, uint32_t cta) {
+__device__ __forceinline__ MtHalf mt_half(int which, uint32_t bands, uint32_t per, uint32_t inner, uint32_t cta,
+                                          float half_unit) {
     MtHalf h;
-    h.cut = mt_split(bands, per);
+    h.cut = mt_split(bands, per, half_unit);
     const uint32_t g0 = h.cut.start(cta);
     h.u0 = h.u1 = h.tile = h.part = h.a = h.j = 0;
     if (cta >= h.cut.n) return h;
@@ -510,7 +512,8 @@ __global__ void __launch_bounds__(kMtThreads, 1)
         for (int i = kMtEpiThreads - 1 - et; i < 2 * scratch.most; i += kMtEpiThreads) {
             const uint32_t A = (uint32_t)(i >> 1) + 1;
             scratch.plans[i >> 1].half[i & 1] =
-                mt_half(i & 1, i & 1 ? ct_d : A * ct_h, i & 1 ? A * K2u : K1, i & 1 ? K2u : ct_h, cta);
+                mt_half(i & 1, i & 1 ? ct_d : A * ct_h, i & 1 ? A * K2u : K1, i & 1 ? K2u : ct_h, cta,
+                        N == 16 ? 600.0f : 800.0f);
         }
         const bool shared = mt_shared_selection(p);
         __syncwarp();
