@@ -349,7 +349,8 @@ def to_mxfp4_then_scaled_grouped_mm(A: torch.Tensor, W: torch.Tensor, offs: torc
     """Differentiable grouped GEMM with an MXFP4 forward: out[m] = A[m] @ W[g]^T for rows m of group
     g (offs = int32 cumulative end rows).  A [M, K] bf16, W [G, N, K] bf16, out [M, N] bf16; K and N
     multiples of 32.  Quantization is the identity for gradients, which are computed from MXFP8
-    operands (group sizes must then be multiples of 32 where W needs a gradient).
+    operands (group sizes must then be multiples of 32 where W needs a gradient).  With gradients
+    disabled (no_grad, inference_mode) nothing is prepared for a backward, and any group sizes go.
 
     w_mxfp4: (q, s) from ``mxfp4_quantize_3d_experts(W)``, when the weights are kept quantized.
     check_offsets: as for ``to_mxfp8_then_scaled_grouped_mm`` (a device check, one stream
@@ -376,4 +377,6 @@ def to_mxfp4_then_scaled_grouped_mm(A: torch.Tensor, W: torch.Tensor, offs: torc
         raise ValueError("offs: must be contiguous")
     if M % 32 and W.requires_grad and torch.is_grad_enabled():
         raise ValueError(f"A: a multiple of 32 rows is needed where W needs a gradient, got {M}")
+    if not torch.is_grad_enabled():  # ctx.needs_input_grad asks requires_grad alone, and is set in evaluation too
+        A, W = A.detach(), W.detach()
     return _ToMxfp4ThenScaledGroupedMM.apply(A, W, offs, w_mxfp4, bool(check_offsets))

@@ -1,0 +1,56 @@
+"""The differentiable calls where no gradient will be asked for."""
+import pytest
+import torch
+
+from mxfp8_precision_moe_gb300 import synth
+from tests._util import require_gpu
+
+pytestmark = pytest.mark.gpu
+
+SIZES = (17, 33)  # no multiples of 32: fine wherever W needs no gradient
+
+
+@pytest.fixture(scope="module")
+def mx():
+    require_gpu()
+    import mxfp8_precision_moe_gb300 as m
+
+    m.load()
+    return m
+
+
+def offs_of(*sizes):
+    return torch.tensor(sizes, device="cuda").cumsum(0).to(torch.int32)
+
+
+def tensors(M, *shapes):
+    return [synth.randn_bf16((M, 64), 1.0, seed=3).cuda()] + \
+        [synth.randn_bf16(s, 0.1, seed=4 + i).cuda() for i, s in enumerate(shapes)]
+
+
+class Recorder:
+    """The library, with the names of the calls made through it."""
+
+    def __init__(self, lib, names):
+        self._lib, self._names = lib, names
+
+    def __getattr__(self, name):
+        self._names.append(name)
+        return getattr(self._lib, name)
+
+
+@pytest.mark.parametrize("mode", [torch.no_grad, torch.inference_mode])
+@pytest.mark.parametrize("a_needs", [False, True])
+def test_mxfp4_evaluation_with_trainable_weights(mx, monkeypatch, mode, a_needs):
+    """Parameters under no_grad: any group sizes, the same result as with detached weights, no copies for a backward."""
+    from mxfp8_precision_moe_gb300 import mxfp4
+
+    A, W = tensors(50, (2, 64, 64))
+    offs = offs_of(*SIZES)
+    want = mx.to_mxfp4_then_scaled_grouped_mm(A, W, offs)
+    names, lib = [], mx.load()
+    monkeypatch.setattr(mxfp4, "load", lambda: Recorder(lib, names))
+    with mode():
+        got = mx.to_mxfp4_then_scaled_grouped_mm(A.clone().requires_grad_(a_needs), torch.nn.Parameter(W.clone()), offs)
+    assert torch.equal(got, want) and not got.requires_grad
+    assert "mxfp4_grouped_mm_fwd" in names and not [n for n in names if n.endswith("_mxfp8_cols")]
