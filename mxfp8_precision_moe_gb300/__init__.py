@@ -454,7 +454,8 @@ def to_mxfp8_then_scaled_grouped_mm(A: torch.Tensor, W: torch.Tensor, offs: torc
     """Differentiable MXFP8 grouped GEMM: out[m] = A[m] @ W[g]^T for rows m of
     group g (offs = int32 cumulative end rows).  A [M, K] bf16, W [G, N, K] bf16,
     out [M, N] bf16.  Group sizes must be multiples of 32 when gradients of W
-    are needed (token-wise quantization for the wgrad).
+    are needed (token-wise quantization for the wgrad); with gradients disabled
+    (no_grad, inference_mode) they are not, whatever W.requires_grad says.
 
     The expert weights are quantized on the fly unless they come prequantized:
     ``w_mxfp8`` = (weight_fp8, weight_scale, weight_t_fp8, weight_t_scale) as
@@ -494,6 +495,8 @@ def to_mxfp8_then_scaled_grouped_mm(A: torch.Tensor, W: torch.Tensor, offs: torc
     if (stochastic_rounding or hadamard_wgrad) and seed is None:
         seed = int(torch.randint(0, 2 ** 62, (1,)).item())
     stability = (bool(stochastic_rounding), bool(hadamard_wgrad), int(seed or 0))
+    if not torch.is_grad_enabled():  # ctx.needs_input_grad asks requires_grad alone, and is set in evaluation too
+        A, W = A.detach(), W.detach()
     return _ToMxfp8ThenScaledGroupedMM.apply(A, W, offs, w_mxfp8, weight_block32x32, stability, bool(check_offsets))
 
 

@@ -77,7 +77,7 @@ def mxfp8_swiglu_expert(x: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, Wd:
     """Differentiable SwiGLU routed expert: y[m] = (silu(x[m] Wg[g]^T) * (x[m] Wu[g]^T)) Wd[g]^T
     for rows m of group g.  x [M, D], Wg and Wu [G, H, D], Wd [G, D, H], all bf16; offs int32
     cumulative end rows; y [M, D] bf16.  Group sizes must be multiples of 32 when weight
-    gradients are needed.  Prequantized weights: ``w_mxfp8 = (gate_quad, up_quad, down_quad)``
+    gradients are needed (never where gradients are disabled).  Prequantized weights: ``w_mxfp8 = (gate_quad, up_quad, down_quad)``
     (each as ``quantize_expert_weights`` returns) or an ``Mxfp8WeightCache``.  check_offsets: as for
     ``to_mxfp8_then_scaled_grouped_mm`` (a device check of offs, one stream synchronization per
     forward; bad offsets raise Mxfp8Error)."""
@@ -95,4 +95,6 @@ def mxfp8_swiglu_expert(x: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, Wd:
     if weight_cache is not None:
         w_mxfp8 = tuple(weight_cache.get(W) for W in (Wg, Wu, Wd))
     qg, qu, qd = w_mxfp8 if w_mxfp8 is not None else (None, None, None)
+    if not torch.is_grad_enabled():  # ctx.needs_input_grad asks requires_grad alone, and is set in evaluation too
+        x, Wg, Wu, Wd = x.detach(), Wg.detach(), Wu.detach(), Wd.detach()
     return _Mxfp8SwiGLUExpert.apply(x, Wg, Wu, Wd, offs, qg, qu, qd, bool(check_offsets))

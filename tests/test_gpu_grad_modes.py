@@ -54,3 +54,37 @@ def test_mxfp4_evaluation_with_trainable_weights(mx, monkeypatch, mode, a_needs)
         got = mx.to_mxfp4_then_scaled_grouped_mm(A.clone().requires_grad_(a_needs), torch.nn.Parameter(W.clone()), offs)
     assert torch.equal(got, want) and not got.requires_grad
     assert "mxfp4_grouped_mm_fwd" in names and not [n for n in names if n.endswith("_mxfp8_cols")]
+
+
+@pytest.mark.parametrize("mode", [torch.no_grad, torch.inference_mode])
+@pytest.mark.parametrize("a_needs", [False, True])
+def test_mxfp8_evaluation_with_trainable_weights(mx, monkeypatch, mode, a_needs):
+    A, W = tensors(50, (2, 64, 64))
+    offs = offs_of(*SIZES)
+    want = mx.to_mxfp8_then_scaled_grouped_mm(A, W, offs)
+    dirs = []
+    for name in ("mxfp8_quantize_2d", "mxfp8_quantize_3d_experts"):
+        f = getattr(mx, name)
+        monkeypatch.setattr(mx, name, lambda x, d, *args, _f=f, **kw: (dirs.append(d), _f(x, d, *args, **kw))[1])
+    with mode():
+        got = mx.to_mxfp8_then_scaled_grouped_mm(A.clone().requires_grad_(a_needs), torch.nn.Parameter(W.clone()), offs)
+    assert torch.equal(got, want) and not got.requires_grad
+    assert dirs == [mx.ROW, mx.ROW]
+
+
+@pytest.mark.parametrize("mode", [torch.no_grad, torch.inference_mode])
+def test_mxfp8_expert_evaluation_with_trainable_weights(mx, monkeypatch, mode):
+    from mxfp8_precision_moe_gb300 import swiglu
+
+    x, *ws = tensors(50, (2, 96, 64), (2, 96, 64), (2, 64, 96))
+    offs = offs_of(*SIZES)
+    want = mx.mxfp8_swiglu_expert(x, *ws, offs)
+    dirs, wise = [], []
+    quantize, gateup = swiglu.mxfp8_quantize_2d, swiglu.mxfp8_grouped_mm_swiglu_fwd
+    monkeypatch.setattr(swiglu, "mxfp8_quantize_2d", lambda x, d, *args: (dirs.append(d), quantize(x, d, *args))[1])
+    monkeypatch.setattr(swiglu, "mxfp8_grouped_mm_swiglu_fwd",
+                        lambda *args, token_wise, **kw: (wise.append(token_wise), gateup(*args, token_wise=token_wise, **kw))[1])
+    with mode():
+        got = mx.mxfp8_swiglu_expert(x, *(torch.nn.Parameter(w.clone()) for w in ws), offs)
+    assert torch.equal(got, want) and not got.requires_grad
+    assert dirs == [mx.ROW] and wise == [False]
