@@ -17,6 +17,7 @@ offsets are int32 cumulative end rows on the device.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -368,6 +369,34 @@ def mxfp8_debug_wait_timeout(dev_status: torch.Tensor, limit_ns: int) -> None:
 
 
 # ---------------------------------------------------------------- composite differentiable op
+class _NoSecondDerivative(torch.autograd.Function):
+    """The identity on a gradient; raises where that gradient is differentiated."""
+
+    @staticmethod
+    def forward(ctx, grad):
+        return grad.view_as(grad)
+
+    @staticmethod
+    def backward(ctx, _):
+        raise RuntimeError("mxfp8: the gradients are kernels' outputs and have no second derivative")
+
+
+def _first_order(backward):
+    """A backward whose results have no graph of their own.  Under create_graph a result without one would count as a
+    constant in whatever is differentiated next, and its term would be lost without a word.  (torch's
+    once_differentiable lets that happen where the incoming gradient is itself a constant.)"""
+
+    @functools.wraps(backward)
+    def first_order(ctx, *grads):
+        with torch.no_grad():
+            out = backward(ctx, *grads)
+        if not torch.is_grad_enabled():
+            return out
+        return tuple(t if t is None else _NoSecondDerivative.apply(t.requires_grad_(True)) for t in out)
+
+    return first_order
+
+
 class _ToMxfp8ThenScaledGroupedMM(torch.autograd.Function):
     """Forward: quantize A along K (and along the tokens for the wgrad), quantize
     W plain (forward) and transposed (dgrad), one grouped GEMM.  Backward:
@@ -402,6 +431,7 @@ class _ToMxfp8ThenScaledGroupedMM(torch.autograd.Function):
         return out
 
     @staticmethod
+    @_first_order
     def backward(ctx, dOut):
         aTq, aTs, wTq, wTs, offs = ctx.saved_tensors
         need_dA, need_dW = ctx.needs_input_grad[0], ctx.needs_input_grad[1]

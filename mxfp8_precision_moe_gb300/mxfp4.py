@@ -11,8 +11,8 @@ from __future__ import annotations
 
 import torch
 
-from . import (COL, MAX_GROUPS, ROW, SCALES_BLOCKED, SCALES_COMPACT, _bytes_at_least, _cuda, _expert_blocked_bytes, _offsets,
-               _status_word, _tensor, _u8, check, load, mxfp8_check_offsets, new_status, read_status)
+from . import (COL, MAX_GROUPS, ROW, SCALES_BLOCKED, SCALES_COMPACT, _bytes_at_least, _cuda, _expert_blocked_bytes,
+               _first_order, _offsets, _status_word, _tensor, _u8, check, load, mxfp8_check_offsets, new_status, read_status)
 
 # torch's handle of a device's current stream as an integer: a few tenths of a microsecond, where
 # torch.cuda.current_stream() builds an object in several
@@ -308,6 +308,7 @@ class _ToMxfp4ThenScaledGroupedMM(torch.autograd.Function):
         return out
 
     @staticmethod
+    @_first_order
     def backward(ctx, dOut):
         aT, wT, W, offs = ctx.saved_tensors
         need_dA, need_dW = ctx.needs_input_grad[:2]

@@ -21,7 +21,7 @@ from __future__ import annotations
 
 import torch
 
-from . import (COL, ROW, SCALES_BLOCKED, _check_quad, _offsets, mxfp8_check_offsets, mxfp8_grouped_mm_dgrad,
+from . import (COL, ROW, SCALES_BLOCKED, _check_quad, _first_order, _offsets, mxfp8_check_offsets, mxfp8_grouped_mm_dgrad,
                mxfp8_grouped_mm_dgrad2, mxfp8_grouped_mm_fwd, mxfp8_grouped_mm_swiglu_fwd, mxfp8_grouped_mm_wgrad,
                mxfp8_quantize_2d, mxfp8_swiglu_bwd_quantize, new_status, quantize_expert_weights, read_status)
 
@@ -51,6 +51,7 @@ class _Mxfp8SwiGLUExpert(torch.autograd.Function):
         return y
 
     @staticmethod
+    @_first_order
     def backward(ctx, dY):
         xTq, xTs, h1, h3, hTq, hTs, gTq, gTs, uTq, uTs, dTq, dTs, offs = ctx.saved_tensors
         need_dx, need_dWg, need_dWu, need_dWd = ctx.needs_input_grad[:4]

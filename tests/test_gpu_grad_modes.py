@@ -1,4 +1,4 @@
-"""The differentiable calls where no gradient will be asked for."""
+"""The differentiable calls where no gradient will be asked for, and where a second derivative is."""
 import pytest
 import torch
 
@@ -88,3 +88,29 @@ def test_mxfp8_expert_evaluation_with_trainable_weights(mx, monkeypatch, mode):
         got = mx.mxfp8_swiglu_expert(x, *(torch.nn.Parameter(w.clone()) for w in ws), offs)
     assert torch.equal(got, want) and not got.requires_grad
     assert dirs == [mx.ROW] and wise == [False]
+
+
+def expert(mx, x, w, offs):
+    return mx.mxfp8_swiglu_expert(x, w, w, w, offs)
+
+
+@pytest.mark.parametrize("call", [
+    lambda mx, a, w, o: mx.to_mxfp4_then_scaled_grouped_mm(a, w, o),
+    lambda mx, a, w, o: mx.to_mxfp8_then_scaled_grouped_mm(a, w, o),
+    expert,
+], ids=["mxfp4", "mxfp8", "expert"])
+def test_a_second_derivative_is_refused(mx, call):
+    """The gradients are kernels' outputs, without a graph: one that is differentiated again raises, and does not count as
+    a constant.  Their values do not depend on create_graph."""
+    A, W = tensors(96, (2, 64, 64))
+    offs = offs_of(32, 64)
+    a, w = A.requires_grad_(True), W.requires_grad_(True)
+    first = torch.autograd.grad(call(mx, a, w, offs).float().sum(), (a, w))
+    assert not any(g.requires_grad for g in first)
+    again = torch.autograd.grad(call(mx, a, w, offs).float().sum(), (a, w), create_graph=True)
+    assert all(torch.equal(g, f) for g, f in zip(again, first))
+    for g in again:
+        with pytest.raises(RuntimeError, match="second derivative"):
+            (g.float().square().sum() + w.float().sum()).backward(retain_graph=True)
+    only, = torch.autograd.grad(call(mx, a, W.detach(), offs).float().sum(), a, create_graph=True)
+    assert torch.equal(only, first[0])
