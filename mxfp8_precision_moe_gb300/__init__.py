@@ -46,13 +46,26 @@ def _stream(device) -> ctypes.c_void_p:
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
 
+def _here(t) -> int:
+    """The index of the device a call with t runs on.  Kernels launch on the calling thread's current device: -2, which
+    no tensor's get_device() returns, where t is not on it."""
+    i = t.get_device() if isinstance(t, torch.Tensor) else -1
+    return i if i >= 0 and i == torch._C._cuda_getDevice() else -2
+
+
 def _cuda(*ts):
+    here = None
     for t in ts:
         if t is not None:
             if not t.is_cuda:
                 raise ValueError("mxfp8: every tensor must live on a CUDA device")
             if not t.is_contiguous():
                 raise ValueError("mxfp8: tensors must be contiguous")
+            if here is None:
+                here = torch._C._cuda_getDevice()
+            if t.get_device() != here:
+                raise ValueError(f"mxfp8: a tensor lives on {t.device}, and the current device, on which the kernels "
+                                 f"launch, is cuda:{here}")
 
 
 def _u8(shape, device):

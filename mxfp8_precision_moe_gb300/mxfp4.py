@@ -12,7 +12,7 @@ from __future__ import annotations
 import torch
 
 from . import (COL, MAX_GROUPS, ROW, SCALES_BLOCKED, SCALES_COMPACT, _bytes_at_least, _cuda, _expert_blocked_bytes,
-               _first_order, _offsets, _status_word, _tensor, _u8, check, load, mxfp8_check_offsets, new_status, read_status)
+               _first_order, _here, _offsets, _status_word, _tensor, _u8, check, load, mxfp8_check_offsets, new_status, read_status)
 
 # torch's handle of a device's current stream as an integer: a few tenths of a microsecond, where
 # torch.cuda.current_stream() builds an object in several
@@ -48,20 +48,23 @@ def _ptr(t):
 
 # A small call's time is the host's, and the named checks of __init__ are a third of it.  So what a correct call
 # looks like is asked in one expression first, and the checks, which say what is wrong, follow where the answer is no.
-def _good(t, dtype, ndim):
-    return isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.dim() == ndim and t.is_contiguous()
+# here: the device of the call, as _here returns it.
+def _good(t, dtype, ndim, here):
+    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == here and t.dim() == ndim
+            and t.is_contiguous())
 
 
-def _scales(s, nbytes):
-    return (isinstance(s, torch.Tensor) and s.dtype is torch.uint8 and s.is_cuda and s.numel() >= nbytes
+def _scales(s, nbytes, here):
+    return (isinstance(s, torch.Tensor) and s.dtype is torch.uint8 and s.get_device() == here and s.numel() >= nbytes
             and s.is_contiguous())
 
 
 def _matrix(x, name: str, offs, other=None, other_name: str = ""):
     """Checks a bf16 matrix x [M, K], one more of its shape and its row groups; returns M, K, groups and their
     address."""
-    if not (_good(x, torch.bfloat16, 2) and (offs is None or _good(offs, torch.int32, 1))
-            and (other is None or (_good(other, torch.bfloat16, 2) and other.shape == x.shape))):
+    here = _here(x)
+    if not (_good(x, torch.bfloat16, 2, here) and (offs is None or _good(offs, torch.int32, 1, here))
+            and (other is None or (_good(other, torch.bfloat16, 2, here) and other.shape == x.shape))):
         _tensor(x, name, torch.bfloat16, 2)
         if other is not None:
             _tensor(other, other_name, torch.bfloat16, shape=x.shape)
@@ -165,7 +168,8 @@ def mxfp4_dequantize_2d(q: torch.Tensor, s: torch.Tensor, scale_layout: int = SC
                         offs: torch.Tensor | None = None) -> torch.Tensor:
     """The values [M, K] that q [M, K/2] and s (as mxfp4_quantize_2d returns them, with the same
     layout and offs) stand for, in bf16: every E2M1 value times a power of two is a bf16."""
-    good = _good(q, torch.uint8, 2) and (offs is None or _good(offs, torch.int32, 1))
+    here = _here(q)
+    good = _good(q, torch.uint8, 2, here) and (offs is None or _good(offs, torch.int32, 1, here))
     if not good:
         _tensor(q, "q", torch.uint8, 2)
     M, K = q.shape
@@ -179,7 +183,7 @@ def mxfp4_dequantize_2d(q: torch.Tensor, s: torch.Tensor, scale_layout: int = SC
         _offsets(offs)
     need = M * (K // 32) if scale_layout == SCALES_COMPACT else \
         (_group_bytes(M, K, G) if offs is not None else _expert_blocked_bytes(M, K))
-    if not (good and _scales(s, need)):
+    if not (good and _scales(s, need, here)):
         _bytes_at_least(s, "s", need)
         _cuda(q, s, offs)
     dev = q.device
@@ -206,7 +210,8 @@ def mxfp4_dequantize_3d_experts(q: torch.Tensor, s: torch.Tensor,
 def mxfp4_grouped_mm_fwd(a_q, a_s, w_q, w_s, offs, out=None, dev_status=None):
     """out[m, n] = sum_k A[m,k] W[g][n,k] for rows m of group g; a_q [M, K/2] with blocked row-group
     scales, w_q [G, N, K/2] with blocked per-expert scales; bf16 [M, N]."""
-    good = _good(a_q, torch.uint8, 2) and _good(w_q, torch.uint8, 3) and _good(offs, torch.int32, 1)
+    here = _here(a_q)
+    good = _good(a_q, torch.uint8, 2, here) and _good(w_q, torch.uint8, 3, here) and _good(offs, torch.int32, 1, here)
     if not good:
         _tensor(a_q, "a_q", torch.uint8, 2)
         _tensor(w_q, "w_q", torch.uint8, 3)
@@ -219,7 +224,7 @@ def mxfp4_grouped_mm_fwd(a_q, a_s, w_q, w_s, offs, out=None, dev_status=None):
     if not good or offs.numel() != G or not 1 <= G <= MAX_GROUPS:
         _offsets(offs, G)
     a_bytes, w_bytes = _group_bytes(M, K, G), G * _expert_blocked_bytes(N, K)
-    if not (good and _scales(a_s, a_bytes) and _scales(w_s, w_bytes)) or out is not None or dev_status is not None:
+    if not (good and _scales(a_s, a_bytes, here) and _scales(w_s, w_bytes, here)) or out is not None or dev_status is not None:
         _bytes_at_least(a_s, "a_s", a_bytes)
         _bytes_at_least(w_s, "w_s", w_bytes)
         if out is not None:
@@ -241,6 +246,9 @@ def _on_one_device(*ts):
             raise ValueError("mxfp4: every tensor must live on a CUDA device")
         if t.device != ts[0].device:
             raise ValueError(f"mxfp4: tensors on {ts[0].device} and {t.device}")
+    if _here(ts[0]) < 0:
+        raise ValueError(f"mxfp4: the tensors live on {ts[0].device}, which is not the current device, on which the "
+                         "kernels launch")
 
 
 def _carve(like: torch.Tensor, *sizes: int):
