@@ -13,7 +13,7 @@ from __future__ import annotations
 
 import torch
 
-from . import _bytes_at_least, _cuda, _expert_blocked_bytes, _status_word, _tensor, check, load
+from . import _bytes_at_least, _cuda, _expert_blocked_bytes, _status_word, _tensor, check, load, new_status
 
 _raw_stream = torch._C._cuda_getCurrentRawStream  # the current stream's handle, without building an object
 
@@ -32,7 +32,10 @@ class MxMoeTokens:
     score: "softmax" (over the selected experts), "softmax_all" (over all experts) or "sigmoid".
 
     The layer holds references to the weights and one workspace for each stream it is called on (a call
-    captured into a graph takes one of the graph's memory).  It computes no gradients."""
+    captured into a graph takes one of the graph's memory).  It computes no gradients.
+
+    A call does not wait for the device.  What the device finds (a wait between CTAs that ran out of time: the output is
+    then incomplete) goes to the layer's own status word, which ``check_status`` reads, or to the caller's dev_status."""
 
     def __init__(self, gate, up, down, top_k: int, *, score: str = "softmax", max_tokens: int = MAX_TOKENS):
         pairs = []
@@ -77,6 +80,7 @@ class MxMoeTokens:
             raise ValueError("the layer is too large for the kernel's 32-bit tile counts")
         self._fixed = (E, D, H, self.top_k, SCORES[score], bits) + tuple(t.data_ptr() for w in pairs for t in w)
         self._workspaces: dict[int, torch.Tensor] = {}
+        self._status = new_status(self.device)
 
     def _new_workspace(self) -> torch.Tensor:
         ws = torch.empty(self._bytes, dtype=torch.uint8, device=self.device)
@@ -93,11 +97,19 @@ class MxMoeTokens:
             ws = self._workspaces[stream] = self._new_workspace()
         return ws
 
+    def check_status(self) -> None:
+        """Synchronize, and raise Mxfp8Error if a call since the last check, eager or captured, has reported an error."""
+        status = int(self._status.item())
+        if status:
+            self._status.zero_()
+            check(status, "MxMoeTokens")
+
     def __call__(self, x: torch.Tensor, router_logits: torch.Tensor, out: torch.Tensor | None = None,
                  dev_status: torch.Tensor | None = None) -> torch.Tensor:
         """x [T, D] bf16, router_logits [T, E] (fp32; fp16 and bf16 are widened), T <= max_tokens -> y
         [T, D] bf16.  A token whose logits are all -inf gets zeros; one with a NaN logit gets NaN.
-        dev_status: an int32 word for errors the device finds (``new_status``, ``read_status``)."""
+        dev_status: an int32 word for errors the device finds (``new_status``, ``read_status``), in place of the
+        layer's own."""
         T = x.shape[0] if x.dim() == 2 else -1
         if x.dtype != torch.bfloat16 or x.dim() != 2 or x.shape[1] != self.D:
             raise ValueError(f"x: expected bf16 [T, {self.D}], got {x.dtype} {tuple(x.shape)}")
@@ -125,6 +137,6 @@ class MxMoeTokens:
         ws = self._workspace(stream)
         E, D, H, k, score, bits, *weights = self._fixed
         check(self._call(x.data_ptr(), router_logits.data_ptr(), T, E, D, H, k, score, bits, *weights, ws.data_ptr(),
-                         self._bytes, out.data_ptr(), None if dev_status is None else dev_status.data_ptr(),
+                         self._bytes, out.data_ptr(), (self._status if dev_status is None else dev_status).data_ptr(),
                          stream), "mx_moe_tokens")
         return out
