@@ -273,13 +273,14 @@ class _ToMxfp4ThenScaledGroupedMM(torch.autograd.Function):
     library directly."""
 
     @staticmethod
-    def forward(ctx, A, W, offs, w_mxfp4, check_offsets):
+    def forward(ctx, A, W, offs, w_mxfp4, check_offsets, dev_status):
         need_dA, need_dW = ctx.needs_input_grad[:2]
         L, stream = load(), _raw_stream(A.device.index)
         (M, K), (G, N, _) = A.shape, W.shape
-        st = None
+        st = ctx.dev_status = dev_status
         if check_offsets:
-            st = new_status(A.device)
+            if st is None:
+                st = new_status(A.device)
             mxfp8_check_offsets(offs, M, 32 if need_dW else 1, st)
         status, off = _ptr(st), offs.data_ptr()
         A = A.contiguous()
@@ -309,7 +310,7 @@ class _ToMxfp4ThenScaledGroupedMM(torch.autograd.Function):
                       "mxfp4_quantize_2d")
             check(L.mxfp4_grouped_mm_fwd(aq, as_, wq, ws, off, G, M, N, K, out.data_ptr(), status, stream),
                   "mxfp4_grouped_mm_fwd")
-        if st is not None:
+        if check_offsets:
             read_status(st, "to_mxfp4_then_scaled_grouped_mm (group offsets)")
         ctx.save_for_backward(aT, wT, W if need_dA and wT is None else None, offs)
         ctx.sizes = (G, M, N, K)
@@ -324,16 +325,16 @@ class _ToMxfp4ThenScaledGroupedMM(torch.autograd.Function):
         dOut = dOut.contiguous().to(torch.bfloat16)
         dA = torch.empty((M, K), dtype=torch.bfloat16, device=dOut.device) if need_dA else None
         if M == 0:
-            return dA, dOut.new_zeros((G, N, K)) if need_dW else None, None, None, None
+            return dA, dOut.new_zeros((G, N, K)) if need_dW else None, None, None, None, None
         dW = torch.empty((G, N, K), dtype=torch.bfloat16, device=dOut.device) if need_dW else None
-        L, stream, off = load(), _raw_stream(dOut.device.index), offs.data_ptr()
+        L, stream, off, status = load(), _raw_stream(dOut.device.index), offs.data_ptr(), _ptr(ctx.dev_status)
         row = (M * N, _group_bytes(M, N, G)) if need_dA else (0, 0)
         w = (G * K * N, G * _expert_blocked_bytes(K, N)) if need_dA and wT is None else (0, 0)
         col = (N * M, _col_bytes(N, M, G)) if need_dW else (0, 0)
         _hold, dq, ds, wq, ws, dTq, dTs = _carve(dOut, *row, *w, *col)
         dirs = (ROW if need_dA else 0) | (COL if need_dW else 0)
         check(L.mxfp8_quantize_2d(dOut.data_ptr(), M, N, dirs, SCALES_BLOCKED, off, G, dq if need_dA else None,
-                                  ds if need_dA else None, dTq if need_dW else None, dTs if need_dW else None, None,
+                                  ds if need_dA else None, dTq if need_dW else None, dTs if need_dW else None, status,
                                   stream), "mxfp8_quantize_2d")
         if need_dA:
             if wT is not None:
@@ -341,20 +342,20 @@ class _ToMxfp4ThenScaledGroupedMM(torch.autograd.Function):
                 ws = wq + (G * K * N + 255) // 256 * 256  # as _carve laid them out in the forward
             else:
                 W = W.contiguous()
-                check(L.mxfp8_quantize_3d_experts(W.data_ptr(), G, N, K, COL, SCALES_BLOCKED, None, None, wq, ws, None,
+                check(L.mxfp8_quantize_3d_experts(W.data_ptr(), G, N, K, COL, SCALES_BLOCKED, None, None, wq, ws, status,
                                                   stream), "mxfp8_quantize_3d_experts")
-            check(L.mxfp8_grouped_mm_dgrad(dq, ds, wq, ws, off, G, M, N, K, dA.data_ptr(), None, stream),
+            check(L.mxfp8_grouped_mm_dgrad(dq, ds, wq, ws, off, G, M, N, K, dA.data_ptr(), status, stream),
                   "mxfp8_grouped_mm_dgrad")
         if need_dW:
             q = aT.data_ptr()
             s = q + (K * M + 255) // 256 * 256  # as _carve laid them out in the forward
-            check(L.mxfp8_grouped_mm_wgrad(dTq, dTs, q, s, off, G, M, N, K, dW.data_ptr(), None, stream),
+            check(L.mxfp8_grouped_mm_wgrad(dTq, dTs, q, s, off, G, M, N, K, dW.data_ptr(), status, stream),
                   "mxfp8_grouped_mm_wgrad")
-        return dA, dW, None, None, None
+        return dA, dW, None, None, None, None
 
 
 def to_mxfp4_then_scaled_grouped_mm(A: torch.Tensor, W: torch.Tensor, offs: torch.Tensor, *, w_mxfp4=None,
-                                    check_offsets: bool = True) -> torch.Tensor:
+                                    check_offsets: bool = True, dev_status: torch.Tensor | None = None) -> torch.Tensor:
     """Differentiable grouped GEMM with an MXFP4 forward: out[m] = A[m] @ W[g]^T for rows m of group
     g (offs = int32 cumulative end rows).  A [M, K] bf16, W [G, N, K] bf16, out [M, N] bf16; K and N
     multiples of 32.  Quantization is the identity for gradients, which are computed from MXFP8
@@ -363,7 +364,9 @@ def to_mxfp4_then_scaled_grouped_mm(A: torch.Tensor, W: torch.Tensor, offs: torc
 
     w_mxfp4: (q, s) from ``mxfp4_quantize_3d_experts(W)``, when the weights are kept quantized.
     check_offsets: as for ``to_mxfp8_then_scaled_grouped_mm`` (a device check, one stream
-    synchronization per forward)."""
+    synchronization per forward).
+    dev_status: an int32 word (``new_status``) that the kernels of the forward and of the backward report errors into,
+    to be read with ``read_status``.  Without one only a forward that checks its offsets reports what its kernels find."""
     if A.dtype != torch.bfloat16 or W.dtype != torch.bfloat16:
         raise ValueError("to_mxfp4_then_scaled_grouped_mm expects bf16 A and W")
     if offs.dtype != torch.int32:
@@ -379,7 +382,8 @@ def to_mxfp4_then_scaled_grouped_mm(A: torch.Tensor, W: torch.Tensor, offs: torc
             raise ValueError("w_mxfp4 must be (codes, scales)")
         _tensor(w_mxfp4[0], "w_mxfp4 codes", torch.uint8, shape=(G, N, K // 2))
         _bytes_at_least(w_mxfp4[1], "w_mxfp4 scales", G * _expert_blocked_bytes(N, K))
-    _on_one_device(A, W, offs, *(w_mxfp4 or ()))
+    _status_word(dev_status)
+    _on_one_device(A, W, offs, *(w_mxfp4 or ()), *(() if dev_status is None else (dev_status,)))
     if w_mxfp4 is not None and not (w_mxfp4[0].is_contiguous() and w_mxfp4[1].is_contiguous()):
         raise ValueError("w_mxfp4: tensors must be contiguous")
     if not offs.is_contiguous():
@@ -388,4 +392,4 @@ def to_mxfp4_then_scaled_grouped_mm(A: torch.Tensor, W: torch.Tensor, offs: torc
         raise ValueError(f"A: a multiple of 32 rows is needed where W needs a gradient, got {M}")
     if not torch.is_grad_enabled():  # ctx.needs_input_grad asks requires_grad alone, and is set in evaluation too
         A, W = A.detach(), W.detach()
-    return _ToMxfp4ThenScaledGroupedMM.apply(A, W, offs, w_mxfp4, bool(check_offsets))
+    return _ToMxfp4ThenScaledGroupedMM.apply(A, W, offs, w_mxfp4, bool(check_offsets), dev_status)

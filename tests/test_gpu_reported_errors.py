@@ -1,4 +1,5 @@
-"""Errors that the device finds reach the caller: the few-token layer's own status word."""
+"""Errors that the device finds reach the caller: the few-token layer's own status word, and the one handed to the
+differentiable 4-bit product, forward and backward."""
 import pytest
 import torch
 
@@ -46,3 +47,49 @@ def test_few_token_layer_keeps_a_status_word(mx):
     torch.cuda.synchronize()
     word = op._status.data_ptr()
     assert passed == [word, word, st.data_ptr(), word]
+
+
+class Recorder:
+    """The library, with every argument of the calls made through it."""
+
+    def __init__(self, lib, seen):
+        self._lib, self._seen = lib, seen
+
+    def __getattr__(self, name):
+        f = getattr(self._lib, name)
+
+        def call(*args):
+            self._seen.append((name, args))
+            return f(*args)
+
+        return call
+
+
+@pytest.mark.parametrize("check", [False, True])
+def test_differentiable_product_reports_into_a_given_word(mx, monkeypatch, check):
+    from mxfp8_precision_moe_gb300 import mxfp4
+
+    A = synth.randn_bf16((96, 64), 1.0, seed=1).cuda().requires_grad_(True)
+    W = synth.randn_bf16((2, 64, 64), 0.1, seed=2).cuda().requires_grad_(True)
+    offs = torch.tensor([32, 96], dtype=torch.int32, device="cuda")
+    seen, lib, st = [], mx.load(), mx.new_status()
+    monkeypatch.setattr(mxfp4, "load", lambda: Recorder(lib, seen))
+    out = mx.to_mxfp4_then_scaled_grouped_mm(A, W, offs, check_offsets=check, dev_status=st)
+    forward = len(seen)
+    out.float().square().sum().backward()
+    mx.read_status(st)
+    reporting = [(n, a) for n, a in seen if n.startswith(("mxfp8_", "mxfp4_grouped", "mxfp4_quantize_2d_", "mxfp4_quantize_3d_experts_"))]
+    assert forward == 3 and len(seen) == 6 and len(reporting) == 6
+    assert all(a[-2] == st.data_ptr() for _, a in reporting)
+    bad = torch.tensor([32, 90], dtype=torch.int32, device="cuda")
+    with pytest.raises(mx.Mxfp8Error):
+        mx.to_mxfp4_then_scaled_grouped_mm(A, W, bad, dev_status=mx.new_status())
+
+
+def test_refusals_of_a_status_word(mx):
+    A, W = synth.randn_bf16((64, 64), 1.0, seed=1).cuda(), synth.randn_bf16((1, 64, 64), 0.1, seed=2).cuda()
+    offs = torch.tensor([64], dtype=torch.int32, device="cuda")
+    for bad in (torch.zeros(1, dtype=torch.int64, device="cuda"), torch.zeros(0, dtype=torch.int32, device="cuda"),
+                torch.zeros(1, dtype=torch.int32)):
+        with pytest.raises(ValueError, match="dev_status|CUDA"):
+            mx.to_mxfp4_then_scaled_grouped_mm(A, W, offs, dev_status=bad)
