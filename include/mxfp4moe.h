@@ -105,6 +105,19 @@ mxfp8_status_t mx_moe_tokens(const void* x_bf16, const float* router_logits, int
                              const void* down_s, void* workspace, size_t workspace_bytes, void* y_bf16,
                              int32_t* dev_status, mxfp8_stream_t stream);
 
+/* ----------------------------------------------------------------------------
+ * mx_debug_moe_tokens -- mx_moe_tokens with the limit of its waits given (0 ns ..
+ *   10 s; mx_moe_tokens: 2 s).  With 0, CTAs that wait for one another give up at
+ *   once: *dev_status becomes MXFP8_ERR_TIMEOUT, y is incomplete, and the
+ *   workspace is ready for the next launch.  It exists so that giving up can be
+ *   exercised without a fault or a hang.
+ * ------------------------------------------------------------------------- */
+mxfp8_status_t mx_debug_moe_tokens(const void* x_bf16, const float* router_logits, int32_t T, int32_t E, int64_t D,
+                                   int64_t H, int32_t top_k, int32_t score, int32_t bits, const void* gate_q,
+                                   const void* gate_s, const void* up_q, const void* up_s, const void* down_q,
+                                   const void* down_s, void* workspace, size_t workspace_bytes, void* y_bf16,
+                                   int32_t* dev_status, uint64_t limit_ns, mxfp8_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -78,6 +78,8 @@ def load():
         "mxfp4_dequantize": [P, P, I32, I64, I64, INT, P, I32, P, P],
         "mxfp4_grouped_mm_fwd": [P, P, P, P, P, I32, I64, I64, I64, P, P, P],
         "mx_moe_tokens": [P, P, I32, I32, I64, I64, I32, I32, I32, P, P, P, P, P, P, P, ctypes.c_size_t, P, P, P],
+        "mx_debug_moe_tokens": [P, P, I32, I32, I64, I64, I32, I32, I32, P, P, P, P, P, P, P, ctypes.c_size_t, P, P,
+                                ctypes.c_uint64, P],
     }.items():
         f = getattr(L, name)
         f.argtypes = args

@@ -319,6 +319,8 @@ constexpr int kMtEpiThreads = 256;
 constexpr int kMtStatic = 10 * 1024;  // static shared memory at most
 
 constexpr int kMtStages = 10;  // at most
+// For what is certain to finish, whatever the limit of the other waits: copies and products that have been issued.
+constexpr uint64_t kMtDrainNs = 2000000000ull;
 
 template <int BITS, int N>
 struct MtCfg {
@@ -478,6 +480,7 @@ __global__ void __launch_bounds__(kMtThreads, 1)
     __shared__ MtPlan plan_s;
     __shared__ float w_s[2][kMtMaxTokens];
     __shared__ uint32_t tmem_base_s, last_s;
+    __shared__ uint32_t issued_s[2];  // stages that the weight and the token producer have asked for
     __shared__ int abort_s;
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
@@ -667,10 +670,12 @@ __global__ void __launch_bounds__(kMtThreads, 1)
         // registers, where these instructions take them from; divisions are paid once a tile.)
         const uint32_t one = elect_one();
         Place at;
+        uint32_t issued = 0;
         bool ok = true;
         auto claim = [&](uint32_t bytes) -> bool {
             if (!take(at, empty, 1u)) return false;
             expect_tx(one, &full[at.stage], bytes);
+            ++issued;
             return true;
         };
         const CUtensorMap *mg = &maps.gate[parts1 - 1], *mu = &maps.up[parts1 - 1], *md = &maps.down[parts2 - 1];
@@ -712,10 +717,12 @@ __global__ void __launch_bounds__(kMtThreads, 1)
                 pass(at);
             }
         }
+        if (lane == 0) issued_s[0] = issued;
     } else if (warp == 1) {
         // ------------------------------------------------ token producer
         const uint32_t one = elect_one();
         Place at;
+        uint32_t issued = 0;
         // steps k .. k + n - 1 of the contraction: tiles of plane z of the map, scale tiles at s
         auto load = [&](const CUtensorMap* m, int32_t z, const uint8_t* s, uint32_t k, uint32_t n, uint32_t ct) -> bool {
             if (!take(at, empty, 1u)) return false;
@@ -725,6 +732,7 @@ __global__ void __launch_bounds__(kMtThreads, 1)
             load_3d(one, st + off_b, m, (int32_t)(k * 128), 0, z, &full[at.stage]);
             if (n == 2) load_3d(one, st + off_b + N * 128, m, (int32_t)(k * 128 + 128), 0, z, &full[at.stage]);
             load_bulk(one, st + off_sfb, s, sfb, &full[at.stage]);
+            ++issued;
             pass(at);
             return true;
         };
@@ -752,6 +760,7 @@ __global__ void __launch_bounds__(kMtThreads, 1)
                 s = p.hs + (int64_t)a * ct_h * 512;
             }
         }
+        if (lane == 0) issued_s[1] = issued;
     } else if (warp == 2) {
         {
             // -------------------------------------------- tensor-core issuer
@@ -861,7 +870,7 @@ __global__ void __launch_bounds__(kMtThreads, 1)
             }
             commit(one, &drain);
             volatile int no_abort = 0;
-            mbar_wait_bounded<true>(&drain, 0, p.timeout_ns, &no_abort, p.dev_status);
+            mbar_wait_bounded<true>(&drain, 0, kMtDrainNs, &no_abort, p.dev_status);
         }
     } else if (warp >= kMtEpiWarp0) {
         const int quarter = warp & 3, cg = (warp - kMtEpiWarp0) >> 2;
@@ -1083,9 +1092,16 @@ __global__ void __launch_bounds__(kMtThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
-    if (abort_s && tid == 0) {  // given up: let the copies in flight land before the CTA's memory goes
-        const uint64_t t0 = globaltimer_ns();
-        while (globaltimer_ns() - t0 < 1000000ull) __nanosleep(1000);
+    if (abort_s && tid == 0) {
+        // Given up: the copies in flight land before the CTA's memory goes.  A stage's barrier wants both producers; where
+        // only one got to it, this thread arrives for the other.  (They are never further apart than the ring is long: a
+        // stage is given out again after its products, which want both.)  Of the stages before the last ring's length of
+        // them, all copies have landed.
+        const uint32_t lo = min(issued_s[0], issued_s[1]), hi = max(issued_s[0], issued_s[1]);
+        for (uint32_t i = lo; i < hi; ++i) mbar_arrive(&full[i % stages]);
+        volatile int no_abort = 0;
+        for (uint32_t i = hi > stages ? hi - stages : 0; i < hi; ++i)
+            mbar_wait_bounded<true>(&full[i % stages], (i / stages) & 1u, kMtDrainNs, &no_abort, p.dev_status);
     }
     __syncthreads();
     if (warp == 2) {
@@ -1172,11 +1188,11 @@ extern "C" size_t mx_moe_tokens_workspace(int32_t max_tokens, int32_t E, int64_t
     return (size_t)mt_layout(max_tokens, E, D, H, top_k, bits).total;
 }
 
-extern "C" mxfp8_status_t mx_moe_tokens(const void* x_bf16, const float* router_logits, int32_t T, int32_t E, int64_t D,
-                                        int64_t H, int32_t top_k, int32_t score, int32_t bits, const void* gate_q,
-                                        const void* gate_s, const void* up_q, const void* up_s, const void* down_q,
-                                        const void* down_s, void* workspace, size_t workspace_bytes, void* y_bf16,
-                                        int32_t* dev_status, mxfp8_stream_t stream) {
+static mxfp8_status_t mt_run(const void* x_bf16, const float* router_logits, int32_t T, int32_t E, int64_t D, int64_t H,
+                             int32_t top_k, int32_t score, int32_t bits, const void* gate_q, const void* gate_s,
+                             const void* up_q, const void* up_s, const void* down_q, const void* down_s, void* workspace,
+                             size_t workspace_bytes, void* y_bf16, int32_t* dev_status, uint64_t limit_ns,
+                             mxfp8_stream_t stream) {
     if (mxfp8_status_t s = mt_shape(T, E, D, H, top_k, bits); s != MXFP8_OK) return s;
     if (score < MX_SCORE_SOFTMAX || score > MX_SCORE_SIGMOID) return MXFP8_ERR_LAYOUT;
     if (T == 0) return MXFP8_OK;
@@ -1208,7 +1224,7 @@ extern "C" mxfp8_status_t mx_moe_tokens(const void* x_bf16, const float* router_
     p.counters = reinterpret_cast<uint32_t*>(ws + l.counters);
     p.y = static_cast<__nv_bfloat16*>(y_bf16);
     p.dev_status = dev_status;
-    p.timeout_ns = 2000000000ull;
+    p.timeout_ns = limit_ns;
     p.D = D;
     p.H = H;
     p.T = T;
@@ -1229,4 +1245,23 @@ extern "C" mxfp8_status_t mx_moe_tokens(const void* x_bf16, const float* router_
     if (bits == 8)
         return N == 16 ? mt_launch<8, 16>(m, p, st) : N == 32 ? mt_launch<8, 32>(m, p, st) : mt_launch<8, 64>(m, p, st);
     return N == 16 ? mt_launch<4, 16>(m, p, st) : N == 32 ? mt_launch<4, 32>(m, p, st) : mt_launch<4, 64>(m, p, st);
+}
+
+extern "C" mxfp8_status_t mx_moe_tokens(const void* x_bf16, const float* router_logits, int32_t T, int32_t E, int64_t D,
+                                        int64_t H, int32_t top_k, int32_t score, int32_t bits, const void* gate_q,
+                                        const void* gate_s, const void* up_q, const void* up_s, const void* down_q,
+                                        const void* down_s, void* workspace, size_t workspace_bytes, void* y_bf16,
+                                        int32_t* dev_status, mxfp8_stream_t stream) {
+    return mt_run(x_bf16, router_logits, T, E, D, H, top_k, score, bits, gate_q, gate_s, up_q, up_s, down_q, down_s, workspace,
+                  workspace_bytes, y_bf16, dev_status, 2000000000ull, stream);
+}
+
+extern "C" mxfp8_status_t mx_debug_moe_tokens(const void* x_bf16, const float* router_logits, int32_t T, int32_t E, int64_t D,
+                                              int64_t H, int32_t top_k, int32_t score, int32_t bits, const void* gate_q,
+                                              const void* gate_s, const void* up_q, const void* up_s, const void* down_q,
+                                              const void* down_s, void* workspace, size_t workspace_bytes, void* y_bf16,
+                                              int32_t* dev_status, uint64_t limit_ns, mxfp8_stream_t stream) {
+    if (limit_ns > 10000000000ull) return MXFP8_ERR_SHAPE;
+    return mt_run(x_bf16, router_logits, T, E, D, H, top_k, score, bits, gate_q, gate_s, up_q, up_s, down_q, down_s, workspace,
+                  workspace_bytes, y_bf16, dev_status, limit_ns, stream);
 }
