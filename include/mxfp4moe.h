@@ -118,6 +118,16 @@ mxfp8_status_t mx_debug_moe_tokens(const void* x_bf16, const float* router_logit
                                    const void* down_s, void* workspace, size_t workspace_bytes, void* y_bf16,
                                    int32_t* dev_status, uint64_t limit_ns, mxfp8_stream_t stream);
 
+/* ----------------------------------------------------------------------------
+ * mx_debug_moe_tokens_cut -- how mx_moe_tokens divides one half of the layer (0:
+ *   gate and up, 1: down) among `ctas` CTAs, one a multiprocessor, when T tokens
+ *   have selected `active` experts: 128 or 64 where every CTA has whole tiles of so
+ *   many weight rows, 1 where CTAs share tiles, 0 for arguments out of range.  Host
+ *   only; it tells tests which way a size goes.
+ * ------------------------------------------------------------------------- */
+int32_t mx_debug_moe_tokens_cut(int32_t half, int32_t T, int32_t active, int64_t D, int64_t H, int32_t bits,
+                                int32_t ctas);
+
 #ifdef __cplusplus
 }
 #endif

@@ -86,6 +86,8 @@ def load():
         f.restype = S
     L.mx_moe_tokens_workspace.argtypes = [I32, I32, I64, I64, I32, I32]
     L.mx_moe_tokens_workspace.restype = ctypes.c_size_t
+    L.mx_debug_moe_tokens_cut.argtypes = [I32, I32, I32, I64, I64, I32, I32]
+    L.mx_debug_moe_tokens_cut.restype = I32
     _lib = L
     return L
 

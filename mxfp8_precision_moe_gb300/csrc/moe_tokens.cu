@@ -415,15 +415,15 @@ struct MtSplit {
 // SM, 900 clocks a unit of 128-row tiles and `half_unit` one of 64-row tiles (600 with 16 token columns, 800 with more: the
 // products of a unit are issued in 250 to 500, the rest is the wait for the next stage).  Sharing tiles evens the runs out but
 // costs an exchange of partial sums, 7000 clocks under load (two trips through L2 and the gathering).  bands: 128-row
-// bands; per: units of one of them.  Measured, best cut against shared tiles throughout and whole tiles throughout: one token
+// bands; per: units of one of them; g: CTAs.  Measured, best cut against shared tiles throughout and whole tiles throughout: one token
 // over MXFP4 experts of 8192 x 5120 23.2 us / 27.4 / 23.4; four tokens, top 4 of 16 MXFP8 experts of 2048 x 7168 89.6 / 88.5 / 89.9;
 // 64 tokens over the same in MXFP4 77 / 89 / 83; five tokens, six experts of 160 x 352 14.0 / 20.1 / 14.7.  With 800 for 16 columns
 // too: eight tokens over eight experts of 1024 x 4096 28.2 in place of 26.2, two tokens over 16 of 1536 x 4096 24.8, not 25.9.
 constexpr float kMtHbm = 3300.0f;  // bytes a clock
 constexpr float kMtExchange = 7000.0f;
+__host__ __device__ constexpr float mt_half_unit(int columns) { return columns == 16 ? 600.0f : 800.0f; }
 
-__device__ __forceinline__ MtSplit mt_split(uint32_t bands, uint32_t per, float half_unit) {
-    const uint32_t g = gridDim.x;
+__host__ __device__ __forceinline__ MtSplit mt_split(uint32_t bands, uint32_t per, float half_unit, uint32_t g) {
     const float hbm = (float)per * (32768.0f * (1.0f / kMtHbm));  // a band's bytes at HBM's rate
     // m rounds of a tile for every CTA, then one for the other r tiles
     auto rounds = [&](uint32_t m, uint32_t r, float bytes, float own) -> float {
@@ -455,7 +455,7 @@ struct MtPlan {
 __device__ __forceinline__ MtHalf mt_half(int which, uint32_t bands, uint32_t per, uint32_t inner, uint32_t cta,
                                           float half_unit) {
     MtHalf h;
-    h.cut = mt_split(bands, per, half_unit);
+    h.cut = mt_split(bands, per, half_unit, gridDim.x);
     const uint32_t g0 = h.cut.start(cta);
     h.u0 = h.u1 = h.tile = h.part = h.a = h.j = 0;
     if (cta >= h.cut.n) return h;
@@ -516,7 +516,7 @@ __global__ void __launch_bounds__(kMtThreads, 1)
             const uint32_t A = (uint32_t)(i >> 1) + 1;
             scratch.plans[i >> 1].half[i & 1] =
                 mt_half(i & 1, i & 1 ? ct_d : A * ct_h, i & 1 ? A * K2u : K1, i & 1 ? K2u : ct_h, cta,
-                        N == 16 ? 600.0f : 800.0f);
+                        mt_half_unit(N));
         }
         const bool shared = mt_shared_selection(p);
         __syncwarp();
@@ -1114,6 +1114,8 @@ __global__ void __launch_bounds__(kMtThreads, 1)
 // ---------------------------------------------------------------- host side
 static int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
 
+static int mt_columns(int T) { return T <= 16 ? 16 : T <= 32 ? 32 : 64; }  // token columns of the products
+
 struct MtLayout {
     int64_t counters, ncounters, xq, xs, hq, hs, part, total;
 };
@@ -1207,7 +1209,7 @@ static mxfp8_status_t mt_run(const void* x_bf16, const float* router_logits, int
     const MtLayout l = mt_layout(T, E, D, H, top_k, bits);
     if (workspace_bytes < (size_t)l.total) return MXFP8_ERR_SHAPE;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    const int N = T <= 16 ? 16 : T <= 32 ? 32 : 64;
+    const int N = mt_columns(T);
     const int64_t Db = D * bits / 8, Hb = H * bits / 8;
     MtParams p{};
     p.x = static_cast<const uint8_t*>(x_bf16);
@@ -1264,4 +1266,14 @@ extern "C" mxfp8_status_t mx_debug_moe_tokens(const void* x_bf16, const float* r
     if (limit_ns > 10000000000ull) return MXFP8_ERR_SHAPE;
     return mt_run(x_bf16, router_logits, T, E, D, H, top_k, score, bits, gate_q, gate_s, up_q, up_s, down_q, down_s, workspace,
                   workspace_bytes, y_bf16, dev_status, limit_ns, stream);
+}
+
+extern "C" int32_t mx_debug_moe_tokens_cut(int32_t half, int32_t T, int32_t active, int64_t D, int64_t H, int32_t bits,
+                                           int32_t ctas) {
+    if (half < 0 || half > 1 || T < 1 || ctas < 1 || mt_shape(T, active, D, H, 1, bits) != MXFP8_OK) return 0;
+    const uint32_t ct_d = (uint32_t)((D + 127) / 128), ct_h = (uint32_t)((H + 127) / 128);
+    const uint32_t step = bits == 8 ? 128 : 256, K1 = (uint32_t)((D + step - 1) / step), K2 = (uint32_t)((H + step - 1) / step);
+    const MtSplit c = half ? mt_split(ct_d, active * ((K2 + 1) / 2), mt_half_unit(mt_columns(T)), ctas)
+                           : mt_split(active * ct_h, K1, mt_half_unit(mt_columns(T)), ctas);
+    return c.grain != c.per ? 1 : c.rows;
 }
