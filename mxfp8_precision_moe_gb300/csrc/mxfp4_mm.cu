@@ -15,13 +15,14 @@
 // multiple of 256 multiplies only the 64-wide steps that hold any of it (a row's tail past K is TMA's zero
 // fill and the scale layout's zero padding).  Every wait is bounded.
 //
-// At 4 bits a stage's four MMAs take about 0.25 us, so what the issuing threads do per stage decides.  8 experts,
-// 16384 tokens, N = 8192, K = 5120: 249 us (5.5 PFLOP/s) with one thread issuing from a lane == 0 branch,
-// 210 us with whole warps and an elected lane (mx4.cuh) and one copy for both of B's scale tiles, 204 us
-// (6.7 PFLOP/s) with six stages instead of five.  What is left: with a quarter of the MMAs the same kernel takes 166 us,
-// with half the operand loads 186, without its stores 195, so L2's feed (18 TB/s at 166 us) and the tensor cores
-// bound it together, and the single accumulator's drain adds the rest (a second one does not fit beside the
-// scales' columns).  Rastering bands of 8 or 32 tiles instead of 16: 218 and 223 us.
+// At 4 bits a stage's four MMAs take 0.28 us at the nominal rate of their K = 64 form (four times bf16's; the form with
+// K = 96, which is not used, has six times), so what the issuing threads do per stage decides.  8 experts, 16384 tokens,
+// N = 8192, K = 5120: 249 us (5.5 PFLOP/s) with one thread issuing from a lane == 0 branch, 210 us with whole warps and an
+// elected lane (mx4.cuh) and one copy for both of B's scale tiles, 204 us (6.7 PFLOP/s) with six stages instead of five.
+// Four times the measured bf16 rate would be 181 us.  What is left has no single cause: with a quarter of the MMAs the same
+// kernel takes 166 us, with half the operand loads 186, without its stores 195.  A serial part of every tile is the drain of
+// the only accumulator, which the next tile's MMAs wait for; a second one of 256 columns does not fit beside the scale
+// columns as they are, a slot for each of the six stages.  Rastering bands of 8 or 32 tiles instead of 16: 218 and 223 us.
 
 #include "host_common.h"
 #include "mx4.cuh"

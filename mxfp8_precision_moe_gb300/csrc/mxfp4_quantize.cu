@@ -11,8 +11,9 @@
 //             two that join a row's four scale bytes into one word.  Against four lanes a block this halves
 //             the instructions per element: [16, 8192, 5120] takes 260 us instead of 303, 6.5 TB/s, which
 //             is HBM's copy rate.  Five CTAs an SM; six spill, four leave loads too few.
-//   SwiGLU    two threads a block, to fit six CTAs an SM.  Bound by issue slots more than by HBM: 126 us for
-//             16384 x 8192, 4.8 TB/s, with the quotient as a product with a reciprocal (silu2) in instructions of two
+//   SwiGLU    two threads a block, to fit six CTAs an SM.  126 us for 16384 x 8192, 4.8 TB/s, with neither the
+//             issue slots nor DRAM full (68% each under ncu): a thread's next loads wait for its arithmetic, and only
+//             the other warps fill the gap.  The quotient is a product with a reciprocal (silu2) in instructions of two
 //             values; with the correctly rounded division 170 us (a block a thread 174-197 us then, four lanes
 //             a block 169-190; five or seven CTAs 135 and 129 now).
 //   inverse   four lanes a block: 16-byte stores of 8 values, whole 32-byte sectors by neighbouring lanes.

@@ -29,7 +29,9 @@ class MxMoeTokens:
     ``mxfp4_quantize_3d_experts`` (codes two to a byte) returns them.  The codes' width tells the
     format.  D and H multiples of 32, E <= 256, top_k <= min(E, 16), max_tokens <= 64.
 
-    score: "softmax" (over the selected experts), "softmax_all" (over all experts) or "sigmoid".
+    score: "softmax" (over the selected experts), "softmax_all" (over all experts) or "sigmoid".  The weight multiplies
+    an expert's output.  (Where the input is to be scaled instead, which SwiGLU tells apart, and top_k is 1: scale x and
+    leave the score at "softmax", whose only weight is 1.)
 
     The layer holds references to the weights and one workspace for each stream it is called on (a call
     captured into a graph takes one of the graph's memory).  It computes no gradients.

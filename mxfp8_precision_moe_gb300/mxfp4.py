@@ -209,7 +209,8 @@ def mxfp4_dequantize_3d_experts(q: torch.Tensor, s: torch.Tensor,
 
 def mxfp4_grouped_mm_fwd(a_q, a_s, w_q, w_s, offs, out=None, dev_status=None):
     """out[m, n] = sum_k A[m,k] W[g][n,k] for rows m of group g; a_q [M, K/2] with blocked row-group
-    scales, w_q [G, N, K/2] with blocked per-expert scales; bf16 [M, N]."""
+    scales, w_q [G, N, K/2] with blocked per-expert scales; bf16 [M, N].  dev_status: an int32 word (``new_status``) for
+    errors the device finds; without one they are not reported."""
     here = _here(a_q)
     good = _good(a_q, torch.uint8, 2, here) and _good(w_q, torch.uint8, 3, here) and _good(offs, torch.int32, 1, here)
     if not good:
