@@ -82,7 +82,8 @@ class MxMoeTokens:
             raise ValueError("the layer is too large for the kernel's 32-bit tile counts")
         self._fixed = (E, D, H, self.top_k, SCORES[score], bits) + tuple(t.data_ptr() for w in pairs for t in w)
         self._workspaces: dict[int, torch.Tensor] = {}
-        self._status = new_status(self.device)
+        with torch.inference_mode(False):  # a tensor made in inference mode could not be zeroed outside of it
+            self._status = new_status(self.device)
 
     def _new_workspace(self) -> torch.Tensor:
         ws = torch.empty(self._bytes, dtype=torch.uint8, device=self.device)

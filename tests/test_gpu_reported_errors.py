@@ -49,6 +49,16 @@ def test_few_token_layer_keeps_a_status_word(mx):
     assert passed == [word, word, st.data_ptr(), word]
 
 
+def test_few_token_layer_made_in_inference_mode(mx):
+    with torch.inference_mode():
+        op = layer(mx)
+    op._status.copy_(torch.full((1,), TIMEOUT, dtype=torch.int32, device="cuda"))
+    with pytest.raises(mx.Mxfp8Error, match="TIMEOUT"):
+        op.check_status()
+    with torch.inference_mode():
+        op.check_status()
+
+
 class Recorder:
     """The library, with every argument of the calls made through it."""
 
