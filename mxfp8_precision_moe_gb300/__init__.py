@@ -35,6 +35,8 @@ __all__ = [
     "mxfp4_quantize_2d", "mxfp4_quantize_2d_mxfp8_cols", "mxfp4_swiglu_quantize", "mxfp4_quantize_3d_experts",
     "mxfp4_quantize_3d_experts_mxfp8_cols", "mxfp4_dequantize_2d",
     "mxfp4_dequantize_3d_experts", "mxfp4_grouped_mm_fwd", "to_mxfp4_then_scaled_grouped_mm", "MxMoeTokens",
+    "moe_route", "moe_plan", "MoePlan", "moe_gather", "moe_combine", "mxfp8_gather_quantize", "mxfp4_gather_quantize",
+    "mxfp8_dequantize_2d", "mxfp8_moe_swiglu",
 ]
 
 
@@ -549,3 +551,5 @@ from .mxfp4 import (mxfp4_dequantize_2d, mxfp4_dequantize_3d_experts, mxfp4_grou
                     mxfp4_quantize_2d, mxfp4_quantize_2d_mxfp8_cols, mxfp4_quantize_3d_experts,
                     mxfp4_quantize_3d_experts_mxfp8_cols, mxfp4_swiglu_quantize, to_mxfp4_then_scaled_grouped_mm)
 from .moe_tokens import MxMoeTokens  # noqa: E402
+from .routing import (MoePlan, moe_combine, moe_gather, moe_plan, moe_route, mxfp4_gather_quantize,  # noqa: E402
+                      mxfp8_dequantize_2d, mxfp8_gather_quantize, mxfp8_moe_swiglu)

@@ -1,4 +1,4 @@
-"""ctypes loader for libmxfp8moe.so (the sm_103a C ABI in include/mxfp8moe.h and include/mxfp4moe.h).
+"""ctypes loader for libmxfp8moe.so (the sm_103a C ABI in include/mxfp8moe.h, mxfp4moe.h and mxrouting.h).
 
 There is no fallback: if the library is missing or the device is not sm_103,
 every call raises.
@@ -80,10 +80,23 @@ def load():
         "mx_moe_tokens": [P, P, I32, I32, I64, I64, I32, I32, I32, P, P, P, P, P, P, P, ctypes.c_size_t, P, P, P],
         "mx_debug_moe_tokens": [P, P, I32, I32, I64, I64, I32, I32, I32, P, P, P, P, P, P, P, ctypes.c_size_t, P, P,
                                 ctypes.c_uint64, P],
+        "mx_moe_route": [P, I32, I64, I32, I32, I32, P, I32, I32, I32, I32, ctypes.c_float, P, P, P],
+        "mx_moe_route_bwd": [P, I32, I64, I32, I32, I32, I32, ctypes.c_float, P, P, P, P],
+        "mx_moe_plan": [P, I32, I64, I32, I32, I32, I64, P, P, P, P, P, ctypes.c_size_t, P],
+        "mx_moe_gather": [P, P, P, I64, I64, I32, I64, P, P],
+        "mx_moe_combine": [P, P, P, I64, I64, I32, I64, P, P],
+        "mx_moe_combine_bwd": [P, P, P, P, P, I64, I64, I32, I64, P, P, P],
+        "mxfp8_gather_quantize": [P, P, P, I64, I64, I32, I64, U32, P, I32, P, P, P, P, P, P],
+        "mxfp4_gather_quantize": [P, P, I64, I64, I32, I64, P, I32, P, P, P],
+        "mxfp8_dequantize": [P, P, I64, I64, U32, INT, P, I32, P, P],
     }.items():
         f = getattr(L, name)
         f.argtypes = args
         f.restype = S
+    L.mx_moe_plan_rows.argtypes = [I64, I32, I32, I32]
+    L.mx_moe_plan_rows.restype = I64
+    L.mx_moe_plan_workspace.argtypes = [I64, I32, I32]
+    L.mx_moe_plan_workspace.restype = ctypes.c_size_t
     L.mx_moe_tokens_workspace.argtypes = [I32, I32, I64, I64, I32, I32]
     L.mx_moe_tokens_workspace.restype = ctypes.c_size_t
     L.mx_debug_moe_tokens_cut.argtypes = [I32, I32, I32, I64, I64, I32, I32]

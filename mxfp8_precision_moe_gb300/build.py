@@ -21,7 +21,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libmxfp8moe.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
-SOURCES = ["api.cu", "quantize.cu", "grouped_mm.cu", "mxfp4_quantize.cu", "mxfp4_mm.cu", "moe_tokens.cu"]
+SOURCES = ["api.cu", "quantize.cu", "grouped_mm.cu", "mxfp4_quantize.cu", "mxfp4_mm.cu", "moe_tokens.cu", "routing.cu",
+           "token_rows.cu"]
 
 
 def nvcc() -> str:
@@ -36,7 +37,7 @@ def nvcc() -> str:
 
 def _deps() -> list[str]:
     out = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    out += [os.path.join(ROOT, "include", h) for h in ("mxfp8moe.h", "mxfp4moe.h")]
+    out += [os.path.join(ROOT, "include", h) for h in ("mxfp8moe.h", "mxfp4moe.h", "mxrouting.h")]
     return out
 
 

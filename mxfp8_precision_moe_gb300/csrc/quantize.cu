@@ -29,6 +29,7 @@
 #include "common.cuh"
 #include "host_common.h"
 #include "mx4.cuh"
+#include "../../include/mxrouting.h"
 
 namespace mx {
 
@@ -59,13 +60,19 @@ struct QParams {
     uint8_t* s_row2;
     uint8_t* q_col2;
     uint8_t* s_col2;
+    // the gather only: row r is x's row slot[r] / top_k (times row_w[slot[r]], where given), zeros where slot[r] is not in
+    // [0, slots)
+    const int32_t* slot;
+    const float* row_w;
+    int32_t top_k, slots;
 };
 
 // Kernel modes: plain MX quantization; the Hadamard variants (fp32 values), without and with
 // stochastic rounding; the fused SwiGLU backward (three inputs dh, h1, h3; two quantized outputs);
 // stochastic rounding alone (the plain kernel's bf16 data path with stochastic codes); MXFP4 codes for the
-// row-wise copy beside MXFP8 ones for the column-wise copy.
-enum QuantMode : int { kModePlain = 0, kModeExt = 1, kModeSwiBwd = 2, kModeSR = 3, kModeExtSR = 4, kModeRow4 = 5 };
+// row-wise copy beside MXFP8 ones for the column-wise copy; rows gathered through a plan.
+enum QuantMode : int { kModePlain = 0, kModeExt = 1, kModeSwiBwd = 2, kModeSR = 3, kModeExtSR = 4, kModeRow4 = 5,
+                       kModeGather = 6 };
 
 // Warp 0 builds, for G groups over R rows, the clamped monotone end rows and
 // the padded start rows P[g] = sum_{h<g} ceil(size_h/128)*128 (also the scale
@@ -302,6 +309,8 @@ constexpr int kQConsumerThreads = 256;         // 8 consumer warps, no producer 
 // kModeSwiBwd (ROW|COL only): 256 threads, no TMA ring: each warp loads its patches of dh, h1 and h3
 // straight from global memory (three inputs a stage would leave room for too few warps to hide the
 // arithmetic's latency), computes dh1 and dh3 and quantizes each both ways.
+// kModeGather (ROW, COL, ROW|COL): loads as in kModeSwiBwd, each row through its slot.  Tiles go down a column strip
+// before the next strip, so that the strip of x (256 bytes a token) stays in L2 for all rows that a token has.
 // The stochastic-rounding kernels have no producer warp: warp 0's lane 0 issues the ring's loads (the
 // first kQStages tiles up front, then each stage again once all 8 warps are done with it), so that 2
 // CTAs of 8 warps leave each thread 128 registers instead of 96 (their random words spilled at 96).
@@ -309,8 +318,11 @@ constexpr int kQConsumerThreads = 256;         // 8 consumer warps, no producer 
 // refill waits for the slowest warp's whole tile, which costs more than the registers give.
 template <int kMode>
 constexpr bool kFoldedProducer = kMode == kModeSR || kMode == kModeExtSR;
+// No TMA ring: each warp loads its own patches.
 template <int kMode>
-constexpr int kQThreadsOf = (kMode == kModeSwiBwd || kFoldedProducer<kMode>) ? kQConsumerThreads : kQThreads;
+constexpr bool kDirectLoads = kMode == kModeSwiBwd || kMode == kModeGather;
+template <int kMode>
+constexpr int kQThreadsOf = (kDirectLoads<kMode> || kFoldedProducer<kMode>) ? kQConsumerThreads : kQThreads;
 
 // kHad (the Hadamard kernels only): bit 0 = transform the row-wise copy, bit 1 = the column-wise copy,
 // fixed per instance so that each holds only the paths its options take.
@@ -319,6 +331,7 @@ __global__ void __launch_bounds__(kQThreadsOf<kMode>, 2)
     quant_tile_kernel(const __grid_constant__ CUtensorMap xmap, QParams p) {
     constexpr bool kExt = kMode == kModeExt || kMode == kModeExtSR;
     constexpr bool kSwiBwd = kMode == kModeSwiBwd;
+    constexpr bool kGather = kMode == kModeGather;
     constexpr int kStages = kQStages;
     constexpr uint32_t kStageBytes = kQTileBytes;
     constexpr bool kRow = (DIRS & MXFP8_ROW) != 0;
@@ -470,7 +483,8 @@ __global__ void __launch_bounds__(kQThreadsOf<kMode>, 2)
 
     for (int64_t t = blockIdx.x; t < p.ntiles; t += gridDim.x) {
         const uint32_t tt = (uint32_t)t, b32 = tt / per_b, rem = tt - b32 * per_b;
-        const uint32_t tr = rem / tiles_c, tc = rem - tr * tiles_c;
+        const uint32_t tiles_r = (uint32_t)p.tiles_r;
+        const uint32_t tr = kGather ? rem % tiles_r : rem / tiles_c, tc = kGather ? rem / tiles_r : rem - tr * tiles_c;
         const int64_t b = b32;
         const int64_t row0 = (int64_t)tr * 128 + wi * 32, col0 = (int64_t)tc * 128 + wj * 64;
         // this warp's 32 x 64 sub-tile: lane rows 8li..8li+7, columns 8lj..8lj+7 (16 bytes each)
@@ -478,7 +492,7 @@ __global__ void __launch_bounds__(kQThreadsOf<kMode>, 2)
         uint32_t v[8][4];
         int cur_stage = 0;
         uint32_t cur_phase = 0;
-        if constexpr (!kSwiBwd) {
+        if constexpr (!kDirectLoads<kMode>) {
             if (!mbar_wait_bounded(&full[stage], phase, kQTimeoutNs, abort_flag, p.dev_status)) break;
             src = tiles + stage * kStageBytes + (32 * wi + 8 * li) * 256 + (64 * wj + 8 * lj) * 2;
             if constexpr (!kExt) {
@@ -1032,6 +1046,31 @@ __global__ void __launch_bounds__(kQThreadsOf<kMode>, 2)
                 }
             quant_rowcol(a, p.q_row, p.s_row, p.q_col, p.s_col);
             quant_rowcol(u3, p.q_row2, p.s_row2, p.q_col2, p.s_col2);
+        } else if constexpr (kGather) {
+            // each lane looks one row up; its patch's eight come from the lanes that hold them
+            const int32_t slot = row0 + lane < R ? __ldg(p.slot + row0 + lane) : -1;
+            const bool has = slot >= 0 && slot < p.slots;
+            const int32_t token = has ? (int32_t)((uint32_t)slot / (uint32_t)p.top_k) : -1;
+#pragma unroll
+            for (int rr = 0; rr < 8; ++rr) {
+                const int32_t from = __shfl_sync(0xffffffffu, token, 8 * li + rr);
+                uint4 u = make_uint4(0, 0, 0, 0);
+                if (from >= 0 && cval) u = __ldg(reinterpret_cast<const uint4*>(p.x + (int64_t)from * C + c8));
+                v[rr][0] = u.x; v[rr][1] = u.y; v[rr][2] = u.z; v[rr][3] = u.w;
+            }
+            if (p.row_w != nullptr) {  // bf16(w x), as the combination's backward gives
+                const float w = has ? __ldg(p.row_w + slot) : 0.0f;
+#pragma unroll
+                for (int rr = 0; rr < 8; ++rr) {
+                    const float f = __shfl_sync(0xffffffffu, w, 8 * li + rr);
+                    // a row without a token stays zeros, not zeros with f's sign
+                    const bool some = __shfl_sync(0xffffffffu, token, 8 * li + rr) >= 0;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (some) v[rr][k] = pack_bf16x2(bf16lo(v[rr][k]) * f, bf16hi(v[rr][k]) * f);
+                }
+            }
+            quant_rowcol(v, p.q_row, p.s_row, p.q_col, p.s_col);
         } else {
             quant_rowcol(v, p.q_row, p.s_row, p.q_col, p.s_col);
         }
@@ -1078,8 +1117,7 @@ static bool make_x_map(CUtensorMap* m, const QParams& p, const uint16_t* base) {
 
 template <unsigned DIRS, int kMode = kModePlain, unsigned kHad = 0>
 static mxfp8_status_t launch_dirs(const CUtensorMap& m, const QParams& p, int64_t grid, cudaStream_t st) {
-    constexpr bool direct = kMode == kModeSwiBwd;  // no TMA ring: no dynamic shared memory, no producer warp
-    constexpr int smem = direct ? 0 : kQSmem;
+    constexpr int smem = kDirectLoads<kMode> ? 0 : kQSmem;
     static std::atomic<int> attr_set[host::kMaxDevices];
     if (!host::ensure_smem(reinterpret_cast<const void*>(quant_tile_kernel<DIRS, kMode, kHad>), smem, attr_set))
         return MXFP8_ERR_LAUNCH;
@@ -1176,6 +1214,96 @@ static mxfp8_status_t launch_swiglu_bwd(const QParams& p, cudaStream_t st) {
     if (!make_x_map(&m, p, p.x)) return MXFP8_ERR_DRIVER;
     const int64_t grid = std::min<int64_t>(p.ntiles, (int64_t)host::num_sms() * 2);
     return launch_dirs<MXFP8_ROW | MXFP8_COL, kModeSwiBwd>(m, p, grid, st);
+}
+
+// Rows through a plan.  The tensor map is unused.
+static mxfp8_status_t gather_quantize(QParams& p, unsigned dirs, cudaStream_t st) {
+    const CUtensorMap m{};
+    const int64_t grid = std::min<int64_t>(p.ntiles, (int64_t)host::num_sms() * 2);
+    switch (dirs) {
+        case MXFP8_ROW: return launch_dirs<MXFP8_ROW, kModeGather>(m, p, grid, st);
+        case MXFP8_COL: return launch_dirs<MXFP8_COL, kModeGather>(m, p, grid, st);
+        default: return launch_dirs<MXFP8_ROW | MXFP8_COL, kModeGather>(m, p, grid, st);
+    }
+}
+
+// ---------------------------------------------------------------- the inverse
+struct DqParams {
+    const uint8_t* q;   // [R][C]
+    const uint8_t* s;
+    uint16_t* out;      // [R][C]
+    int64_t R, C;       // as q lies: C runs along the scales' blocks
+    int blocked;
+    const int32_t* offs;  // groups of M, nullptr: one
+    int32_t G;
+    uint32_t tiles_r, tiles_c;
+};
+
+// A warp takes 16 rows of a 128 x 128 tile, four at a time, a lane 16 neighbouring values (half a block): one 16-byte
+// load, one scale byte, two 16-byte stores.  In the column-wise copy the groups run along C, so that a lane's place in the
+// scales is found once a tile.
+template <bool kCol>
+__global__ void __launch_bounds__(256) mxfp8_dequantize_kernel(const DqParams p) {
+    __shared__ int32_t ends_s[kMaxGroups];
+    __shared__ int32_t pstart_s[kMaxGroups];
+    __shared__ int32_t ptotal_s;
+    const int64_t R = p.R, C = p.C, M = kCol ? C : R;
+    const bool grouped = p.blocked && p.offs != nullptr && p.G > 1;
+    if (grouped && threadIdx.x < 32) build_group_table(p.offs, p.G, M, ends_s, pstart_s, &ptotal_s);
+    __syncthreads();
+    const int64_t ct = kCol ? (grouped ? (int64_t)ptotal_s / 128 : (M + 127) / 128) : (C + 127) / 128;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // the place of index m of the grouped axis in the padded layout, -1: in no group
+    auto padded = [&](int64_t m) -> int64_t {
+        if (!grouped) return m;
+        const int g = find_group(ends_s, p.G, m);
+        return g < p.G ? pstart_s[g] + (m - (g ? ends_s[g - 1] : 0)) : -1;
+    };
+    for (uint32_t t = blockIdx.x; t < p.tiles_r * p.tiles_c; t += gridDim.x) {
+        const uint32_t tr = t / p.tiles_c, tc = t - tr * p.tiles_c;
+        const int64_t c = (int64_t)tc * 128 + (lane & 7) * 16;
+        if (c >= C) continue;
+        int64_t cb = c / kBlk;  // block-column in the scales
+        bool none = false;
+        if (kCol && p.blocked) {
+            const int64_t m = padded(c);
+            none = m < 0;
+            cb = m / kBlk;
+        }
+        uint4 codes[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t r = (int64_t)tr * 128 + warp * 16 + 4 * i + (lane >> 3);
+            codes[i] = make_uint4(0, 0, 0, 0);
+            if (r < R) codes[i] = __ldg(reinterpret_cast<const uint4*>(p.q + r * C + c));
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t r = (int64_t)tr * 128 + warp * 16 + 4 * i + (lane >> 3);
+            if (r >= R) continue;
+            const int64_t pr = !kCol && p.blocked ? padded(r) : r;
+            uint4 o[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+            if (!none && pr >= 0) {
+                const float f = e8m0_value(p.s[p.blocked ? blocked_off(pr, cb, ct) : r * (C / kBlk) + cb]);
+                const uint32_t w[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
+                uint32_t h[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    float lo, hi;  // every E4M3 value is a half
+                    asm("{\n\t.reg .b32 v;\n\t.reg .f16 a, b;\n\tcvt.rn.f16x2.e4m3x2 v, %2;\n\tmov.b32 {a, b}, v;\n\t"
+                        "cvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
+                        : "=f"(lo), "=f"(hi)
+                        : "h"((uint16_t)(w[k >> 1] >> (16 * (k & 1)))));
+                    h[k] = pack_bf16x2(lo * f, hi * f);
+                }
+                o[0] = make_uint4(h[0], h[1], h[2], h[3]);
+                o[1] = make_uint4(h[4], h[5], h[6], h[7]);
+            }
+            uint4* out = reinterpret_cast<uint4*>(p.out + r * C + c);
+            out[0] = o[0];
+            out[1] = o[1];
+        }
+    }
 }
 
 static mxfp8_status_t quantize_2d(const void* x_bf16, int64_t M, int64_t K, unsigned dirs, int scale_layout,
@@ -1325,4 +1453,69 @@ extern "C" mxfp8_status_t mxfp4_quantize_3d_experts_mxfp8_cols(const void* w_bf1
     if (G < 1 || G > MXFP8_MAX_GROUPS || N <= 0) return MXFP8_ERR_SHAPE;
     QParams p{};
     return mx::quantize_row4(p, w_bf16, N, K, G, q, s, qT, sT, dev_status, reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" mxfp8_status_t mxfp8_gather_quantize(const void* x_bf16, const int32_t* slot, const float* w, int64_t rows,
+                                                int64_t T, int32_t top_k, int64_t D, unsigned dirs, const int32_t* offs,
+                                                int32_t G, void* q_row, void* s_row, void* q_col, void* s_col,
+                                                int32_t* dev_status, mxfp8_stream_t stream) {
+    if (rows < 0 || rows > INT32_MAX || D <= 0 || D > INT32_MAX || T < 0 || top_k < 1 || top_k > MX_MAX_TOP_K ||
+        T * top_k > INT32_MAX || G < 1 || G > MXFP8_MAX_GROUPS)
+        return MXFP8_ERR_SHAPE;
+    const bool row = dirs & MXFP8_ROW, col = dirs & MXFP8_COL;
+    if (dirs == 0 || (dirs & ~(unsigned)(MXFP8_ROW | MXFP8_COL))) return MXFP8_ERR_LAYOUT;
+    if (D % 32 || (col && rows % 32)) return MXFP8_ERR_ALIGN;
+    if (rows == 0) return MXFP8_OK;  // an empty tensor may have no address
+    if ((T && !x_bf16) || !slot || !offs || (row && (!q_row || !s_row)) || (col && (!q_col || !s_col))) return MXFP8_ERR_NULL;
+    for (const void* v : {x_bf16, (const void*)q_row, (const void*)s_row, (const void*)q_col, (const void*)s_col})
+        if (!host::aligned16(v)) return MXFP8_ERR_ALIGN;
+    for (const void* v : {(const void*)slot, (const void*)w, (const void*)offs})
+        if (reinterpret_cast<uintptr_t>(v) & 3u) return MXFP8_ERR_ALIGN;
+    if (mxfp8_status_t a = host::check_arch(); a != MXFP8_OK) return a;
+    QParams p{};
+    p.x = static_cast<const uint16_t*>(x_bf16);
+    p.R = rows; p.C = D; p.batch = 1;
+    p.q_row = static_cast<uint8_t*>(q_row); p.s_row = static_cast<uint8_t*>(s_row);
+    p.q_col = static_cast<uint8_t*>(q_col); p.s_col = static_cast<uint8_t*>(s_col);
+    p.blocked = 1;
+    p.offs = offs; p.G = G;
+    p.dev_status = dev_status;
+    p.slot = slot; p.row_w = w;
+    p.top_k = top_k; p.slots = (int32_t)(T * top_k);
+    p.tiles_r = (rows + 127) / 128; p.tiles_c = (D + 127) / 128; p.ntiles = p.tiles_r * p.tiles_c;
+    if (p.ntiles >= INT32_MAX) return MXFP8_ERR_SHAPE;
+    return mx::gather_quantize(p, dirs, reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" mxfp8_status_t mxfp8_dequantize(const void* q, const void* s, int64_t M, int64_t K, unsigned dir,
+                                           int scale_layout, const int32_t* offs, int32_t G, void* out_bf16,
+                                           mxfp8_stream_t stream) {
+    if (M < 0 || M > INT32_MAX || K <= 0 || K > INT32_MAX || (offs && (G < 1 || G > MXFP8_MAX_GROUPS))) return MXFP8_ERR_SHAPE;
+    if (dir != MXFP8_ROW && dir != MXFP8_COL) return MXFP8_ERR_LAYOUT;
+    if (scale_layout != MXFP8_SCALES_COMPACT && scale_layout != MXFP8_SCALES_BLOCKED) return MXFP8_ERR_LAYOUT;
+    const bool col = dir == MXFP8_COL;
+    if (K % 32 || (col && M % 32)) return MXFP8_ERR_ALIGN;
+    if (M == 0) return MXFP8_OK;  // an empty tensor may have no address
+    if (!q || !s || !out_bf16) return MXFP8_ERR_NULL;
+    if (!host::aligned16(q) || !host::aligned16(s) || !host::aligned16(out_bf16)) return MXFP8_ERR_ALIGN;
+    if (reinterpret_cast<uintptr_t>(offs) & 3u) return MXFP8_ERR_ALIGN;
+    if (mxfp8_status_t a = host::check_arch(); a != MXFP8_OK) return a;
+    DqParams p{};
+    p.q = static_cast<const uint8_t*>(q);
+    p.s = static_cast<const uint8_t*>(s);
+    p.out = static_cast<uint16_t*>(out_bf16);
+    p.R = col ? K : M;
+    p.C = col ? M : K;
+    p.blocked = scale_layout == MXFP8_SCALES_BLOCKED;
+    p.offs = offs;
+    p.G = offs ? G : 0;
+    const int64_t tr = (p.R + 127) / 128, tc = (p.C + 127) / 128;
+    if (tr * tc >= INT32_MAX) return MXFP8_ERR_SHAPE;
+    p.tiles_r = (uint32_t)tr;
+    p.tiles_c = (uint32_t)tc;
+    const unsigned grid = (unsigned)std::min<int64_t>(tr * tc, (int64_t)host::num_sms() * 6);
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (col) mxfp8_dequantize_kernel<true><<<grid, 256, 0, st>>>(p);
+    else mxfp8_dequantize_kernel<false><<<grid, 256, 0, st>>>(p);
+    return host::last_launch_status();
 }

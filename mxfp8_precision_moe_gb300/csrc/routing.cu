@@ -1,0 +1,670 @@
+// routing.cu -- which experts a token goes to and with what weight, forward and
+// backward, and the plan of the rows that follow from it.
+
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+#include "host_common.h"
+#include "../../include/mxrouting.h"
+
+namespace mx {
+
+// ---------------------------------------------------------------- routing
+struct RouteParams {
+    const void* logits;
+    const float* bias;
+    int32_t* experts;
+    float* weights;
+    const float* dweights;  // the backward only
+    void* dlogits;
+    int64_t T;
+    int32_t E, top_k, score, groups, top_groups, group_max, renormalize;
+    float scale;
+};
+
+constexpr int kRouteWarps = 4;  // tokens of a CTA, a warp each
+constexpr uint32_t kFull = 0xffffffffu;
+
+__device__ __forceinline__ float logit(const float* p) { return *p; }
+__device__ __forceinline__ float logit(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+__device__ __forceinline__ float logit(const __half* p) { return __half2float(*p); }
+__device__ __forceinline__ void put(float* p, float v) { *p = v; }
+__device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+__device__ __forceinline__ void put(__half* p, float v) { *p = __float2half_rn(v); }
+
+// Integers that order as the values do: NaN above everything, -0 as +0.  No value's is 0, which stands for "none".
+__device__ __forceinline__ uint32_t order_of(float v) {
+    if (v != v) return 0xffffffffu;
+    const uint32_t u = __float_as_uint(v + 0.0f);
+    return u >> 31 ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float value_of(uint32_t o) {
+    return o == 0xffffffffu ? __uint_as_float(0x7fc00000u) : __uint_as_float(o >> 31 ? o & 0x7fffffffu : ~o);
+}
+__device__ __forceinline__ unsigned long long order_of(double v) {
+    if (v != v) return ~0ull;
+    const unsigned long long u = (unsigned long long)__double_as_longlong(v + 0.0);
+    return u >> 63 ? ~u : u | (1ull << 63);
+}
+__device__ __forceinline__ double value_of(unsigned long long o) {
+    if (o == ~0ull) return __longlong_as_double(0x7ff8000000000000ll);
+    return __longlong_as_double((long long)(o >> 63 ? o & ~(1ull << 63) : ~o));
+}
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+    for (int d = 16; d; d >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, d));
+    return v;
+}
+template <typename F>
+__device__ __forceinline__ F warp_sum(F v) {
+#pragma unroll
+    for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(kFull, v, d);
+    return v;
+}
+
+// What a group is worth (lane g: group g, from the keys' integers in shared memory), and which groups stay: bit g.
+// The two largest are kept as integers, so that a NaN counts.
+template <typename O>
+__device__ __forceinline__ uint32_t best_groups(const O* keys, const RouteParams& p, int lane, O& worth) {
+    const int size = p.E / p.groups;
+    O top = 0, second = 0;
+    if (lane < p.groups) {
+        int at = lane % size;  // lanes start apart, so that they do not meet in a bank
+        for (int i = 0; i < size; ++i) {
+            const O v = keys[lane * size + at];
+            if (++at == size) at = 0;
+            second = max(second, min(top, v));
+            top = max(top, v);
+        }
+    }
+    worth = top;
+    if (!p.group_max && second) worth = order_of(value_of(top) + value_of(second));
+    int rank = 0;
+    for (int g = 0; g < p.groups; ++g) {
+        const O other = __shfl_sync(kFull, worth, g);
+        rank += other > worth || (other == worth && g < lane);
+    }
+    return __ballot_sync(kFull, lane < p.groups && worth && rank < p.top_groups);
+}
+
+// The selection in 64 bits, for a token whose order 32 bits leave open.  Lane j returns the j-th expert, -1: none.
+template <typename L>
+__device__ __noinline__ int select_64(const RouteParams& p, const L* row, unsigned long long* keys, int lane) {
+    double top = 0.0, sum = 1.0;
+    if (p.score == MX_SCORE_SOFTMAX_ALL) {
+        float m = __uint_as_float(0xff800000u);
+        for (int e = lane; e < p.E; e += 32) m = fmaxf(m, logit(row + e));
+        top = warp_max(m);
+        sum = 0.0;
+        for (int e = lane; e < p.E; e += 32) sum += exp((double)logit(row + e) - top);
+        sum = warp_sum(sum);
+    }
+    for (int e = lane; e < p.E; e += 32) {
+        const float l = logit(row + e), b = p.bias ? p.bias[e] : 0.0f;
+        double s = l;
+        if (p.score == MX_SCORE_SOFTMAX_ALL) s = exp(s - top) / sum;
+        else if (p.score == MX_SCORE_SIGMOID) s = 1.0 / (1.0 + exp(-s));
+        const double key = p.bias ? s + (double)b : s;
+        keys[e] = l == -INFINITY || key == -INFINITY ? 0ull : order_of(key);
+    }
+    __syncwarp();
+    if (p.groups > 1) {
+        unsigned long long worth;
+        const uint32_t stay = best_groups(keys, p, lane, worth);
+        const int size = p.E / p.groups;
+        for (int e = lane; e < p.E; e += 32)
+            if (!(stay >> (e / size) & 1u)) keys[e] = 0ull;
+        __syncwarp();
+    }
+    int mine = -1;
+    for (int j = 0; j < p.top_k; ++j) {
+        unsigned long long best = 0;
+        int at = p.E;
+        for (int e = lane; e < p.E; e += 32)
+            if (keys[e] > best) {
+                best = keys[e];
+                at = e;
+            }
+#pragma unroll
+        for (int d = 16; d; d >>= 1) {
+            const unsigned long long o = __shfl_xor_sync(kFull, best, d);
+            const int i = __shfl_xor_sync(kFull, at, d);
+            if (o > best || (o == best && i < at)) {
+                best = o;
+                at = i;
+            }
+        }
+        if (best == 0) break;
+        if (lane == j) mine = at;
+        __syncwarp();
+        if (lane == 0) keys[at] = 0ull;
+        __syncwarp();
+    }
+    return mine;
+}
+
+// Where a lane holds a selected expert's logit (`in`): its share of the weights, unscaled.  m and sum: the maximum of
+// the token's logits and the sum of their exponentials above it (softmax over all, not renormalised).
+__device__ __forceinline__ float weight_of(const RouteParams& p, bool in, float l, float m, float sum) {
+    if (p.score == MX_SCORE_SIGMOID) {
+        if (!p.renormalize) return in ? 1.0f / (1.0f + expf(-l)) : 0.0f;
+        // s_j / sum s with every s_j times e^-c, c = min(0, max l): where all logits are far below 0 the scores
+        // themselves would underflow, and their quotients are lost
+        const float c = fminf(0.0f, warp_max(in ? l : -INFINITY));
+        const float s = !in ? 0.0f : l >= 0.0f ? 1.0f / (1.0f + expf(-l)) : expf(l - c) / (1.0f + expf(l));
+        const float total = warp_sum(s);
+        return in ? s / total : 0.0f;
+    }
+    if (p.score == MX_SCORE_SOFTMAX_ALL && !p.renormalize) return in ? expf(l - m) / sum : 0.0f;
+    const float top = warp_max(in ? l : -INFINITY);
+    const float s = in ? expf(l - top) : 0.0f;
+    const float total = warp_sum(s);
+    return in ? s / total : 0.0f;
+}
+
+// A warp a token: lane i holds the logits of VPL neighbouring experts.  The k largest keys leave one by one, each by a
+// maximum over the warp (one instruction on 32-bit integers) and a search in the lane that holds it.
+//
+// Keys with a score or a bias are sums of rounded terms, and tokens are told apart by them all the same: each key's
+// error has a bound, and where two neighbours in the order, or the groups on both sides of the cut, are no further
+// apart than their bounds, the token is done again in 64 bits.
+template <typename L, int VPL>
+__global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteParams p) {
+    extern __shared__ unsigned long long route_smem[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t t = (int64_t)blockIdx.x * kRouteWarps + warp;
+    if (t >= p.T) return;
+    unsigned long long* keys = route_smem + (size_t)warp * p.E;  // this warp's, where there are groups or doubts
+    const L* row = static_cast<const L*>(p.logits) + t * p.E;
+    const bool scored = p.bias != nullptr || (p.groups > 1 && !p.group_max);
+    constexpr float kUlp = 0x1p-24f;
+
+    float l[VPL];
+    constexpr int V = VPL * sizeof(L) < 16 ? VPL : 16 / (int)sizeof(L);
+    if (p.E % V == 0 && (reinterpret_cast<uintptr_t>(p.logits) & (V * sizeof(L) - 1)) == 0) {
+#pragma unroll
+        for (int c = 0; c < VPL / V; ++c) {
+            struct alignas(V * sizeof(L)) Vec { L v[V]; } u;
+            const int e = lane * VPL + c * V;
+            if (e < p.E) u = *reinterpret_cast<const Vec*>(row + e);
+#pragma unroll
+            for (int i = 0; i < V; ++i) l[c * V + i] = e < p.E ? logit(u.v + i) : -INFINITY;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) l[i] = lane * VPL + i < p.E ? logit(row + lane * VPL + i) : -INFINITY;
+    }
+
+    float m = 0.0f, sum = 1.0f;
+    if (p.score == MX_SCORE_SOFTMAX_ALL && (scored || !p.renormalize)) {
+        float top = l[0];
+#pragma unroll
+        for (int i = 1; i < VPL; ++i) top = fmaxf(top, l[i]);
+        m = warp_max(top);
+        float part = 0.0f;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) part += expf(l[i] - m);
+        sum = warp_sum(part);
+    }
+
+    uint32_t ord[VPL];
+    float err = 0.0f;  // of a key at most
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+        float key = l[i], own = 0.0f;
+        if (scored) {
+            // in units of 2^-24 of the score: expf 4 (2 ulp), sums and quotients 1 each
+            if (p.score == MX_SCORE_SIGMOID) {
+                key = 1.0f / (1.0f + expf(-key));
+                own = 8 * kUlp * key;
+            } else if (p.score == MX_SCORE_SOFTMAX_ALL) {
+                // the exponent's difference d, which is rounded, here and (7, the entropy, at most) in the sum; two
+                // expf; 5 + VPL sums; the quotient; and what subnormals lose
+                const float d = m - l[i];
+                key = expf(-d) / sum;
+                own = (fminf(d, 200.0f) + 24 + VPL) * kUlp * key + 0x1p-126f;
+            }
+            if (p.bias) {
+                const int e = lane * VPL + i;
+                key += e < p.E ? p.bias[e] : 0.0f;
+                own += kUlp * fabsf(key);
+            }
+        }
+        ord[i] = l[i] == -INFINITY || key == -INFINITY ? 0u : order_of(key);
+        if (ord[i]) err = fmaxf(err, own);
+    }
+    err = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(err)));
+    bool doubt = false;
+
+    if (p.groups > 1) {
+        uint32_t* k32 = reinterpret_cast<uint32_t*>(keys);
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+            if (lane * VPL + i < p.E) k32[lane * VPL + i] = ord[i];
+        __syncwarp();
+        uint32_t worth;
+        const uint32_t stay = best_groups(k32, p, lane, worth);
+        if (!p.group_max || p.bias) {
+            // the least that stays against the best that goes; a sum of two keys, rounded
+            const uint32_t low = __reduce_min_sync(kFull, (stay >> lane & 1u) ? worth : 0xffffffffu);
+            const uint32_t high = __reduce_max_sync(kFull, (stay >> lane & 1u) || lane >= p.groups ? 0u : worth);
+            const float a = value_of(low), b = value_of(high);
+            if (stay && high) doubt = !(a - b > 4 * err + 2 * kUlp * (fabsf(a) + fabsf(b)));
+        }
+        const int size = p.E / p.groups;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+            if (!(stay >> (min(lane * VPL + i, p.E - 1) / size) & 1u)) ord[i] = 0u;
+    }
+
+    int mine = -1;
+    uint32_t my_ord = 0;
+    uint32_t best = ord[0];
+#pragma unroll
+    for (int i = 1; i < VPL; ++i) best = max(best, ord[i]);
+    const int rounds = p.top_k + (err > 0.0f ? 1 : 0);
+    for (int j = 0; j < rounds; ++j) {
+        const uint32_t top = __reduce_max_sync(kFull, best);
+        if (top == 0u) break;
+        const int src = __ffs(__ballot_sync(kFull, best == top)) - 1;
+        int e = 0;
+        if (lane == src) {
+            bool found = false;
+            best = 0u;
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) {
+                if (!found && ord[i] == top) {
+                    found = true;
+                    e = lane * VPL + i;
+                    ord[i] = 0u;
+                }
+                best = max(best, ord[i]);
+            }
+        }
+        e = __shfl_sync(kFull, e, src);
+        if (lane == j) {
+            mine = e;
+            my_ord = top;
+        }
+    }
+    if (err > 0.0f) {
+        const uint32_t next = __shfl_down_sync(kFull, my_ord, 1);
+        // NaN and infinities compare as not further apart
+        const bool close = lane < p.top_k && my_ord && next && !(value_of(my_ord) - value_of(next) > 2 * err);
+        doubt = doubt || __any_sync(kFull, close);
+    }
+    if (doubt) mine = select_64(p, row, keys, lane);
+
+    const bool in = lane < p.top_k && mine >= 0;
+    const float w = weight_of(p, in, in ? logit(row + mine) : 0.0f, m, sum);
+    if (lane < p.top_k) {
+        p.experts[t * p.top_k + lane] = in ? mine : -1;
+        p.weights[t * p.top_k + lane] = in ? w * p.scale : 0.0f;
+    }
+}
+
+// The gradient: with p the unscaled weights and d = scale * dweights,
+//   softmax over the selected (or renormalised):  dl_j = p_j (d_j - <p, d>)
+//   softmax over all:                             dl_e = p_e ([e selected] d_e - <p, d>)
+//   sigmoid:                                      dl_j = d_j s_j (1 - s_j)
+//   sigmoid, renormalised:                        dl_j = p_j (d_j - <p, d>) (1 - s_j)
+// and 0 for every other expert.  A warp a token: the row of zeros (or of the others' softmax), then the selected.
+template <typename L>
+__global__ void __launch_bounds__(kRouteWarps * 32) route_bwd_kernel(const RouteParams p) {
+    const int lane = threadIdx.x & 31;
+    const int64_t t = (int64_t)blockIdx.x * kRouteWarps + (threadIdx.x >> 5);
+    if (t >= p.T) return;
+    const L* row = static_cast<const L*>(p.logits) + t * p.E;
+    L* out = static_cast<L*>(p.dlogits) + t * p.E;
+    int e = -1;
+    float d = 0.0f;
+    if (lane < p.top_k) {
+        e = p.experts[t * p.top_k + lane];
+        d = p.dweights[t * p.top_k + lane] * p.scale;
+    }
+    const bool in = e >= 0 && e < p.E;
+    const float l = in ? logit(row + e) : 0.0f;
+    const bool dense = p.score == MX_SCORE_SOFTMAX_ALL && !p.renormalize;
+    float m = 0.0f, sum = 1.0f;
+    if (dense) {
+        m = -INFINITY;
+        for (int i = lane; i < p.E; i += 32) m = fmaxf(m, logit(row + i));
+        m = warp_max(m);
+        sum = 0.0f;
+        for (int i = lane; i < p.E; i += 32) sum += expf(logit(row + i) - m);
+        sum = warp_sum(sum);
+    }
+    const float w = weight_of(p, in, l, m, sum);
+    float g;
+    if (p.score == MX_SCORE_SIGMOID && !p.renormalize) {
+        g = d * w * (1.0f / (1.0f + expf(l)));
+    } else {
+        const float mean = warp_sum(in ? w * d : 0.0f);
+        g = w * (d - mean);
+        if (p.score == MX_SCORE_SIGMOID) g *= 1.0f / (1.0f + expf(l));
+        if (dense && __any_sync(kFull, in)) {
+            for (int i = lane; i < p.E; i += 32) put(out + i, -(expf(logit(row + i) - m) / sum) * mean);
+            __syncwarp();
+            if (in) put(out + e, g);
+            return;
+        }
+    }
+    for (int i = lane; i < p.E; i += 32) put(out + i, 0.0f);
+    __syncwarp();  // orders the row's zeros before the values that take their places
+    if (in) put(out + e, g);
+}
+
+// ---------------------------------------------------------------- the plan
+// A stable counting sort by expert.  A CTA takes a run of kPlanChunk choices, a warp a run of 32 * kPlanSteps of
+// them in turn: a choice's rank among its warp's is the count so far plus the lanes before it with the same expert (a
+// warp-wide match), so no atomics and no order that could vary.  With several CTAs a first kernel counts each run.
+constexpr int kPlanThreads = 512;
+constexpr int kPlanWarps = kPlanThreads / 32;
+constexpr int kPlanSteps = 8;
+constexpr int kPlanChunk = kPlanThreads * kPlanSteps;
+
+struct PlanParams {
+    const void* experts;
+    int64_t n;  // choices
+    int32_t E, multiple, runs;
+    int64_t rows;
+    int32_t *offs, *counts, *slot, *place;
+    int32_t* hist;  // [runs][E]
+};
+
+template <typename I>
+__device__ __forceinline__ int expert_of(const PlanParams& p, int64_t i) {  // -1: none
+    if (i >= p.n) return -1;
+    const I e = static_cast<const I*>(p.experts)[i];
+    return e >= 0 && e < (I)p.E ? (int)e : -1;
+}
+
+template <typename I>
+__global__ void __launch_bounds__(kPlanThreads) plan_count_kernel(const PlanParams p) {
+    __shared__ int32_t count[kMaxGroups];
+    for (int e = threadIdx.x; e < p.E; e += kPlanThreads) count[e] = 0;
+    __syncthreads();
+    const int64_t base = (int64_t)blockIdx.x * kPlanChunk;
+    int ex[kPlanSteps];
+#pragma unroll
+    for (int s = 0; s < kPlanSteps; ++s) ex[s] = expert_of<I>(p, base + s * kPlanThreads + threadIdx.x);
+#pragma unroll
+    for (int s = 0; s < kPlanSteps; ++s)
+        if (ex[s] >= 0) atomicAdd(&count[ex[s]], 1);
+    __syncthreads();
+    for (int e = threadIdx.x; e < p.E; e += kPlanThreads) p.hist[(int64_t)blockIdx.x * p.E + e] = count[e];
+}
+
+template <typename I>
+__global__ void __launch_bounds__(kPlanThreads) plan_place_kernel(const PlanParams p) {
+    extern __shared__ int32_t plan_smem[];
+    int32_t* table = plan_smem;                  // [kPlanWarps][E]: counts, then first rows
+    int32_t* before = table + kPlanWarps * p.E;  // [E]: choices of earlier runs
+    int32_t* total = before + p.E;               // [E]: choices of all runs
+    int32_t* start = total + p.E;                // [E]: first row of the group
+    __shared__ int32_t warp_part[kPlanWarps];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t base = (int64_t)blockIdx.x * kPlanChunk + warp * 32 * kPlanSteps + lane;
+    int ex[kPlanSteps], rank[kPlanSteps];
+#pragma unroll
+    for (int s = 0; s < kPlanSteps; ++s) ex[s] = expert_of<I>(p, base + s * 32);
+    for (int i = threadIdx.x; i < kPlanWarps * p.E; i += kPlanThreads) table[i] = 0;
+    // counts of the other runs, summed in two halves: those before this one, and the rest
+    for (int e = threadIdx.x; e < p.E; e += kPlanThreads) {
+        int32_t lo = 0, hi = 0;
+        if (p.runs > 1) {
+#pragma unroll 8
+            for (int r = 0; r < p.runs; ++r) {
+                const int32_t c = p.hist[(int64_t)r * p.E + e];
+                if (r < (int)blockIdx.x) lo += c;
+                else hi += c;
+            }
+        }
+        before[e] = lo;
+        total[e] = lo + hi;
+    }
+    __syncthreads();
+    int32_t* mine = table + warp * p.E;
+#pragma unroll
+    for (int s = 0; s < kPlanSteps; ++s) {
+        const uint32_t same = __match_any_sync(kFull, ex[s]);
+        const int ahead = __popc(same & ((1u << lane) - 1u));
+        if (ex[s] >= 0) rank[s] = mine[ex[s]] + ahead;
+        __syncwarp();
+        if (ex[s] >= 0 && ahead == 0) mine[ex[s]] += __popc(same);
+        __syncwarp();
+    }
+    __syncthreads();
+    if (p.runs == 1) {
+        for (int e = threadIdx.x; e < p.E; e += kPlanThreads) {
+            int32_t c = 0;
+#pragma unroll
+            for (int w = 0; w < kPlanWarps; ++w) c += table[w * p.E + e];
+            total[e] = c;
+        }
+        __syncthreads();
+    }
+    // the groups' first rows: a scan of the padded sizes, kMaxGroups / kPlanThreads neighbours a thread
+    constexpr int kPer = kMaxGroups / kPlanThreads;
+    int32_t size[kPer], sum = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int e = threadIdx.x * kPer + i;
+        size[i] = e < p.E ? (total[e] + p.multiple - 1) / p.multiple * p.multiple : 0;
+        sum += size[i];
+    }
+    int32_t incl = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int32_t o = __shfl_up_sync(kFull, incl, d);
+        if (lane >= d) incl += o;
+    }
+    if (lane == 31) warp_part[warp] = incl;
+    __syncthreads();
+    int32_t at = incl - sum, end = 0;
+#pragma unroll
+    for (int w = 0; w < kPlanWarps; ++w) {
+        const int32_t c = warp_part[w];
+        if (w < warp) at += c;
+        end += c;
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int e = threadIdx.x * kPer + i;
+        if (e < p.E) {
+            start[e] = at;
+            if (blockIdx.x == 0) {
+                p.offs[e] = at + size[i];
+                p.counts[e] = total[e];
+            }
+        }
+        at += size[i];
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < p.E; e += kPlanThreads) {
+        int32_t row = start[e] + before[e];
+#pragma unroll
+        for (int w = 0; w < kPlanWarps; ++w) {
+            const int32_t c = table[w * p.E + e];
+            table[w * p.E + e] = row;
+            row += c;
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int s = 0; s < kPlanSteps; ++s) {
+        const int64_t i = base + s * 32;
+        if (i >= p.n) continue;
+        int32_t row = -1;
+        if (ex[s] >= 0) {
+            row = mine[ex[s]] + rank[s];
+            p.slot[row] = (int32_t)i;
+        }
+        p.place[i] = row;
+    }
+    // rows without a token: each group's padding, by the CTAs in turn, a warp a group; and what follows the last group
+    for (int e = blockIdx.x * kPlanWarps + warp; e < p.E; e += gridDim.x * kPlanWarps) {
+        const int32_t from = start[e] + total[e], to = e + 1 < p.E ? start[e + 1] : end;
+        for (int32_t r = from + lane; r < to; r += 32) p.slot[r] = -1;
+    }
+    for (int64_t r = end + (int64_t)blockIdx.x * kPlanThreads + threadIdx.x; r < p.rows; r += (int64_t)gridDim.x * kPlanThreads)
+        p.slot[r] = -1;
+}
+
+// ---------------------------------------------------------------- host side
+static mxfp8_status_t route_check(const RouteParams& p, int32_t type) {
+    if (p.T < 0 || p.E < 1 || p.E > MXFP8_MAX_GROUPS || p.top_k < 1 || p.top_k > MX_MAX_TOP_K || p.top_k > p.E)
+        return MXFP8_ERR_SHAPE;
+    if (p.T * (int64_t)p.top_k > INT32_MAX) return MXFP8_ERR_SHAPE;
+    if (p.score < MX_SCORE_SOFTMAX || p.score > MX_SCORE_SIGMOID || type < MX_LOGITS_FP32 || type > MX_LOGITS_FP16)
+        return MXFP8_ERR_LAYOUT;
+    return MXFP8_OK;
+}
+static bool aligned_to(const void* p, int bytes) { return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(bytes - 1)) == 0; }
+
+template <typename L, int VPL>
+static mxfp8_status_t route_launch(const RouteParams& p, cudaStream_t st) {
+    // 32 KB at most; none where logits are ranked as they are
+    const int smem = p.groups > 1 || p.bias ? kRouteWarps * p.E * (int)sizeof(unsigned long long) : 0;
+    const unsigned grid = (unsigned)((p.T + kRouteWarps - 1) / kRouteWarps);
+    route_kernel<L, VPL><<<grid, kRouteWarps * 32, smem, st>>>(p);
+    return host::last_launch_status();
+}
+template <typename L>
+static mxfp8_status_t route_run(const RouteParams& p, cudaStream_t st) {
+    if (p.E <= 32) return route_launch<L, 1>(p, st);
+    if (p.E <= 64) return route_launch<L, 2>(p, st);
+    if (p.E <= 128) return route_launch<L, 4>(p, st);
+    if (p.E <= 256) return route_launch<L, 8>(p, st);
+    if (p.E <= 512) return route_launch<L, 16>(p, st);
+    return route_launch<L, 32>(p, st);
+}
+
+template <typename I>
+static mxfp8_status_t plan_run(const PlanParams& p, cudaStream_t st) {
+    if (p.runs > 1) {
+        plan_count_kernel<I><<<p.runs, kPlanThreads, 0, st>>>(p);
+        if (mxfp8_status_t s = host::last_launch_status(); s != MXFP8_OK) return s;
+    }
+    static std::atomic<int> attr_set[host::kMaxDevices];
+    constexpr int most = (kPlanWarps + 3) * MXFP8_MAX_GROUPS * 4;
+    if (!host::ensure_smem(reinterpret_cast<const void*>(plan_place_kernel<I>), most, attr_set)) return MXFP8_ERR_LAUNCH;
+    plan_place_kernel<I><<<p.runs, kPlanThreads, (kPlanWarps + 3) * p.E * 4, st>>>(p);
+    return host::last_launch_status();
+}
+
+}  // namespace mx
+
+using namespace mx;
+
+extern "C" mxfp8_status_t mx_moe_route(const void* logits, int32_t logits_type, int64_t T, int32_t E, int32_t top_k,
+                                       int32_t score, const float* bias, int32_t groups, int32_t top_groups,
+                                       int32_t group_score, int32_t renormalize, float scale, int32_t* experts,
+                                       float* weights, mxfp8_stream_t stream) {
+    RouteParams p{};
+    p.logits = logits;
+    p.bias = bias;
+    p.experts = experts;
+    p.weights = weights;
+    p.T = T;
+    p.E = E;
+    p.top_k = top_k;
+    p.score = score;
+    p.groups = groups;
+    p.top_groups = top_groups;
+    p.group_max = group_score == MX_GROUP_MAX;
+    p.renormalize = renormalize != 0;
+    p.scale = scale;
+    if (mxfp8_status_t s = route_check(p, logits_type); s != MXFP8_OK) return s;
+    if (groups < 1 || groups > 32 || E % groups || top_groups < 1 || top_groups > groups || top_k > top_groups * (E / groups))
+        return MXFP8_ERR_SHAPE;
+    if (group_score != MX_GROUP_TOP2 && group_score != MX_GROUP_MAX) return MXFP8_ERR_LAYOUT;
+    if (T == 0) return MXFP8_OK;  // an empty tensor may have no address
+    if (!logits || !experts || !weights) return MXFP8_ERR_NULL;
+    if (!aligned_to(logits, logits_type == MX_LOGITS_FP32 ? 4 : 2) || !aligned_to(bias, 4) || !aligned_to(experts, 4) ||
+        !aligned_to(weights, 4))
+        return MXFP8_ERR_ALIGN;
+    if (mxfp8_status_t a = host::check_arch(); a != MXFP8_OK) return a;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (logits_type == MX_LOGITS_FP32) return route_run<float>(p, st);
+    if (logits_type == MX_LOGITS_BF16) return route_run<__nv_bfloat16>(p, st);
+    return route_run<__half>(p, st);
+}
+
+extern "C" mxfp8_status_t mx_moe_route_bwd(const void* logits, int32_t logits_type, int64_t T, int32_t E, int32_t top_k,
+                                           int32_t score, int32_t renormalize, float scale, const int32_t* experts,
+                                           const float* dweights, void* dlogits, mxfp8_stream_t stream) {
+    RouteParams p{};
+    p.logits = logits;
+    p.experts = const_cast<int32_t*>(experts);
+    p.dweights = dweights;
+    p.dlogits = dlogits;
+    p.T = T;
+    p.E = E;
+    p.top_k = top_k;
+    p.score = score;
+    p.renormalize = renormalize != 0;
+    p.scale = scale;
+    if (mxfp8_status_t s = route_check(p, logits_type); s != MXFP8_OK) return s;
+    if (T == 0) return MXFP8_OK;
+    if (!logits || !experts || !dweights || !dlogits) return MXFP8_ERR_NULL;
+    const int size = logits_type == MX_LOGITS_FP32 ? 4 : 2;
+    if (!aligned_to(logits, size) || !aligned_to(dlogits, size) || !aligned_to(experts, 4) || !aligned_to(dweights, 4))
+        return MXFP8_ERR_ALIGN;
+    if (mxfp8_status_t a = host::check_arch(); a != MXFP8_OK) return a;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const unsigned grid = (unsigned)((T + kRouteWarps - 1) / kRouteWarps);
+    if (logits_type == MX_LOGITS_FP32) route_bwd_kernel<float><<<grid, kRouteWarps * 32, 0, st>>>(p);
+    else if (logits_type == MX_LOGITS_BF16) route_bwd_kernel<__nv_bfloat16><<<grid, kRouteWarps * 32, 0, st>>>(p);
+    else route_bwd_kernel<__half><<<grid, kRouteWarps * 32, 0, st>>>(p);
+    return host::last_launch_status();
+}
+
+static bool plan_sizes(int64_t T, int32_t top_k, int32_t E, int32_t multiple) {
+    if (T < 0 || T > INT32_MAX || top_k < 1 || top_k > MX_MAX_TOP_K || E < 1 || E > MXFP8_MAX_GROUPS || multiple < 1 ||
+        multiple > 1024)
+        return false;
+    return T * top_k + (int64_t)E * multiple <= INT32_MAX;
+}
+
+extern "C" int64_t mx_moe_plan_rows(int64_t T, int32_t top_k, int32_t E, int32_t multiple) {
+    if (!plan_sizes(T, top_k, E, multiple)) return -1;
+    const int64_t n = T * top_k;
+    return (n + min64(E, n) * (multiple - 1)) / multiple * multiple;
+}
+
+extern "C" size_t mx_moe_plan_workspace(int64_t T, int32_t top_k, int32_t E) {
+    if (!plan_sizes(T, top_k, E, 1)) return 0;
+    const int64_t runs = (T * top_k + kPlanChunk - 1) / kPlanChunk;
+    return runs > 1 ? (size_t)(runs * E * 4) : 0;
+}
+
+extern "C" mxfp8_status_t mx_moe_plan(const void* experts, int32_t index_bytes, int64_t T, int32_t top_k, int32_t E,
+                                      int32_t multiple, int64_t rows, int32_t* offs, int32_t* counts, int32_t* slot,
+                                      int32_t* place, void* workspace, size_t workspace_bytes, mxfp8_stream_t stream) {
+    if (!plan_sizes(T, top_k, E, multiple) || rows < mx_moe_plan_rows(T, top_k, E, multiple) || rows > INT32_MAX)
+        return MXFP8_ERR_SHAPE;
+    if (index_bytes != 4 && index_bytes != 8) return MXFP8_ERR_LAYOUT;
+    const size_t need = mx_moe_plan_workspace(T, top_k, E);
+    if (!offs || !counts || (rows && !slot) || (T && (!experts || !place)) || (need && !workspace)) return MXFP8_ERR_NULL;
+    if (workspace_bytes < need) return MXFP8_ERR_SHAPE;
+    if (!aligned_to(experts, index_bytes) || !aligned_to(offs, 4) || !aligned_to(counts, 4) || !aligned_to(slot, 4) ||
+        !aligned_to(place, 4) || !aligned_to(workspace, 16))
+        return MXFP8_ERR_ALIGN;
+    if (mxfp8_status_t a = host::check_arch(); a != MXFP8_OK) return a;
+    PlanParams p{};
+    p.experts = experts;
+    p.n = T * top_k;
+    p.E = E;
+    p.multiple = multiple;
+    p.runs = (int32_t)max64(1, (p.n + kPlanChunk - 1) / kPlanChunk);
+    p.rows = rows;
+    p.offs = offs;
+    p.counts = counts;
+    p.slot = slot;
+    p.place = place;
+    p.hist = static_cast<int32_t*>(workspace);
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    return index_bytes == 4 ? plan_run<int32_t>(p, st) : plan_run<int64_t>(p, st);
+}
