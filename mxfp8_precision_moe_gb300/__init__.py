@@ -403,10 +403,10 @@ def _first_order(backward):
 
     @functools.wraps(backward)
     def first_order(ctx, *grads):
+        if not torch.is_grad_enabled():
+            return backward(ctx, *grads)
         with torch.no_grad():
             out = backward(ctx, *grads)
-        if not torch.is_grad_enabled():
-            return out
         return tuple(t if t is None else _NoSecondDerivative.apply(t.requires_grad_(True)) for t in out)
 
     return first_order

@@ -18,7 +18,8 @@ struct RouteParams {
     const float* dweights;  // the backward only
     void* dlogits;
     int64_t T;
-    int32_t E, top_k, score, groups, top_groups, group_max, renormalize;
+    int32_t type, E, top_k, score, groups, top_groups, group_max, renormalize;
+    int32_t group_size, group_lanes;  // group_lanes: of the route kernel, where a group is a power of two of them; else 0
     float scale;
 };
 
@@ -31,6 +32,24 @@ __device__ __forceinline__ float logit(const __half* p) { return __half2float(*p
 __device__ __forceinline__ void put(float* p, float v) { *p = v; }
 __device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 __device__ __forceinline__ void put(__half* p, float v) { *p = __float2half_rn(v); }
+
+__device__ __forceinline__ float logit_at(const RouteParams& p, int64_t t, int e) {
+    const int64_t i = t * p.E + e;
+    if (p.type == MX_LOGITS_FP32) return logit(static_cast<const float*>(p.logits) + i);
+    if (p.type == MX_LOGITS_BF16) return logit(static_cast<const __nv_bfloat16*>(p.logits) + i);
+    return logit(static_cast<const __half*>(p.logits) + i);
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {  // within 2 ulp
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float rcp_approx(float x) {  // within 1 ulp
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
 
 // Integers that order as the values do: NaN above everything, -0 as +0.  No value's is 0, which stands for "none".
 __device__ __forceinline__ uint32_t order_of(float v) {
@@ -67,7 +86,7 @@ __device__ __forceinline__ F warp_sum(F v) {
 // The two largest are kept as integers, so that a NaN counts.
 template <typename O>
 __device__ __forceinline__ uint32_t best_groups(const O* keys, const RouteParams& p, int lane, O& worth) {
-    const int size = p.E / p.groups;
+    const int size = p.group_size;
     O top = 0, second = 0;
     if (lane < p.groups) {
         int at = lane % size;  // lanes start apart, so that they do not meet in a bank
@@ -88,33 +107,36 @@ __device__ __forceinline__ uint32_t best_groups(const O* keys, const RouteParams
     return __ballot_sync(kFull, lane < p.groups && worth && rank < p.top_groups);
 }
 
+// The maximum of a token's logits and the sum of their exponentials above it, in 64 bits (softmax over all experts).
+__device__ __forceinline__ void softmax_64(const RouteParams& p, int64_t t, int lane, double& top, double& sum) {
+    float m = -INFINITY;
+    for (int e = lane; e < p.E; e += 32) m = fmaxf(m, logit_at(p, t, e));
+    top = warp_max(m);
+    sum = 0.0;
+    for (int e = lane; e < p.E; e += 32) sum += exp((double)logit_at(p, t, e) - top);
+    sum = warp_sum(sum);
+}
+// The integer that orders as expert e's key does, from 64 bits; 0: not to be selected.
+__device__ __forceinline__ unsigned long long key_64(const RouteParams& p, int64_t t, int e, double top, double sum) {
+    const float l = logit_at(p, t, e), b = p.bias ? p.bias[e] : 0.0f;
+    double s = l;
+    if (p.score == MX_SCORE_SOFTMAX_ALL) s = exp(s - top) / sum;
+    else if (p.score == MX_SCORE_SIGMOID) s = 1.0 / (1.0 + exp(-s));
+    const double key = p.bias ? s + (double)b : s;
+    return l == -INFINITY || key == -INFINITY ? 0ull : order_of(key);
+}
+
 // The selection in 64 bits, for a token whose order 32 bits leave open.  Lane j returns the j-th expert, -1: none.
-template <typename L>
-__device__ __noinline__ int select_64(const RouteParams& p, const L* row, unsigned long long* keys, int lane) {
+__device__ __noinline__ int select_64(const RouteParams& p, int64_t t, unsigned long long* keys, int lane) {
     double top = 0.0, sum = 1.0;
-    if (p.score == MX_SCORE_SOFTMAX_ALL) {
-        float m = __uint_as_float(0xff800000u);
-        for (int e = lane; e < p.E; e += 32) m = fmaxf(m, logit(row + e));
-        top = warp_max(m);
-        sum = 0.0;
-        for (int e = lane; e < p.E; e += 32) sum += exp((double)logit(row + e) - top);
-        sum = warp_sum(sum);
-    }
-    for (int e = lane; e < p.E; e += 32) {
-        const float l = logit(row + e), b = p.bias ? p.bias[e] : 0.0f;
-        double s = l;
-        if (p.score == MX_SCORE_SOFTMAX_ALL) s = exp(s - top) / sum;
-        else if (p.score == MX_SCORE_SIGMOID) s = 1.0 / (1.0 + exp(-s));
-        const double key = p.bias ? s + (double)b : s;
-        keys[e] = l == -INFINITY || key == -INFINITY ? 0ull : order_of(key);
-    }
+    if (p.score == MX_SCORE_SOFTMAX_ALL) softmax_64(p, t, lane, top, sum);
+    for (int e = lane; e < p.E; e += 32) keys[e] = key_64(p, t, e, top, sum);
     __syncwarp();
     if (p.groups > 1) {
         unsigned long long worth;
         const uint32_t stay = best_groups(keys, p, lane, worth);
-        const int size = p.E / p.groups;
         for (int e = lane; e < p.E; e += 32)
-            if (!(stay >> (e / size) & 1u)) keys[e] = 0ull;
+            if (!(stay >> (e / p.group_size) & 1u)) keys[e] = 0ull;
         __syncwarp();
     }
     int mine = -1;
@@ -148,11 +170,16 @@ __device__ __noinline__ int select_64(const RouteParams& p, const L* row, unsign
 // the token's logits and the sum of their exponentials above it (softmax over all, not renormalised).
 __device__ __forceinline__ float weight_of(const RouteParams& p, bool in, float l, float m, float sum) {
     if (p.score == MX_SCORE_SIGMOID) {
-        if (!p.renormalize) return in ? 1.0f / (1.0f + expf(-l)) : 0.0f;
-        // s_j / sum s with every s_j times e^-c, c = min(0, max l): where all logits are far below 0 the scores
-        // themselves would underflow, and their quotients are lost
-        const float c = fminf(0.0f, warp_max(in ? l : -INFINITY));
-        const float s = !in ? 0.0f : l >= 0.0f ? 1.0f / (1.0f + expf(-l)) : expf(l - c) / (1.0f + expf(l));
+        const float a = expf(-fabsf(l));
+        float s = l >= 0.0f ? 1.0f : a;
+        if (p.renormalize) {
+            // s_j / sum s with every s_j times e^-c, c the largest logit where that is negative: where all logits are far
+            // below 0 the scores themselves would underflow, and their quotients be lost
+            const float c = warp_max(in ? l : -INFINITY);
+            if (c < 0.0f) s = expf(l - c);
+        }
+        s = in ? (l == l ? s / (1.0f + a) : l) : 0.0f;
+        if (!p.renormalize) return s;
         const float total = warp_sum(s);
         return in ? s / total : 0.0f;
     }
@@ -163,41 +190,81 @@ __device__ __forceinline__ float weight_of(const RouteParams& p, bool in, float 
     return in ? s / total : 0.0f;
 }
 
-// A warp a token: lane i holds the logits of VPL neighbouring experts.  The k largest keys leave one by one, each by a
-// maximum over the warp (one instruction on 32-bit integers) and a search in the lane that holds it.
-//
-// Keys with a score or a bias are sums of rounded terms, and tokens are told apart by them all the same: each key's
-// error has a bound, and where two neighbours in the order, or the groups on both sides of the cut, are no further
-// apart than their bounds, the token is done again in 64 bits.
+// VPL neighbouring values of a row of n from lane * VPL on, `fill` past its end; by vectors where the row's start allows.
 template <typename L, int VPL>
-__global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteParams p) {
-    extern __shared__ unsigned long long route_smem[];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t t = (int64_t)blockIdx.x * kRouteWarps + warp;
-    if (t >= p.T) return;
-    unsigned long long* keys = route_smem + (size_t)warp * p.E;  // this warp's, where there are groups or doubts
-    const L* row = static_cast<const L*>(p.logits) + t * p.E;
-    const bool scored = p.bias != nullptr || (p.groups > 1 && !p.group_max);
-    constexpr float kUlp = 0x1p-24f;
-
-    float l[VPL];
+__device__ __forceinline__ void load_row(const L* row, const void* base, int n, int lane, float fill, float (&out)[VPL]) {
     constexpr int V = VPL * sizeof(L) < 16 ? VPL : 16 / (int)sizeof(L);
-    if (p.E % V == 0 && (reinterpret_cast<uintptr_t>(p.logits) & (V * sizeof(L) - 1)) == 0) {
+    if (n % V == 0 && (reinterpret_cast<uintptr_t>(base) & (V * sizeof(L) - 1)) == 0) {
 #pragma unroll
         for (int c = 0; c < VPL / V; ++c) {
             struct alignas(V * sizeof(L)) Vec { L v[V]; } u;
             const int e = lane * VPL + c * V;
-            if (e < p.E) u = *reinterpret_cast<const Vec*>(row + e);
+            if (e < n) u = *reinterpret_cast<const Vec*>(row + e);
 #pragma unroll
-            for (int i = 0; i < V; ++i) l[c * V + i] = e < p.E ? logit(u.v + i) : -INFINITY;
+            for (int i = 0; i < V; ++i) out[c * V + i] = e < n ? logit(u.v + i) : fill;
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) l[i] = lane * VPL + i < p.E ? logit(row + lane * VPL + i) : -INFINITY;
+        for (int i = 0; i < VPL; ++i) out[i] = lane * VPL + i < n ? logit(row + lane * VPL + i) : fill;
     }
+}
+template <int VPL>
+__device__ __forceinline__ void load_logits(const RouteParams& p, int64_t t, int lane, float (&l)[VPL]) {
+    if (p.type == MX_LOGITS_FP32) {
+        load_row<float, VPL>(static_cast<const float*>(p.logits) + t * p.E, p.logits, p.E, lane, -INFINITY, l);
+    } else if (p.type == MX_LOGITS_BF16) {
+        load_row<__nv_bfloat16, VPL>(static_cast<const __nv_bfloat16*>(p.logits) + t * p.E, p.logits, p.E, lane, -INFINITY, l);
+    } else {
+        load_row<__half, VPL>(static_cast<const __half*>(p.logits) + t * p.E, p.logits, p.E, lane, -INFINITY, l);
+    }
+}
 
+// Keys: the logits themselves (exact), logit + bias, or a score (+ bias).
+enum RouteKeys : int { kKeysLogits = 0, kKeysBias = 1, kKeysSigmoid = 2, kKeysSoftmax = 3 };
+
+// The same where the groups are settled and the experts that come into question are few: lane i's is e, -1: none; they
+// lie in the order of their indices.
+__device__ __noinline__ int select_64_among(const RouteParams& p, int64_t t, int e, int total, uint2* shared, int lane) {
+    double top = 0.0, sum = 1.0;
+    if (p.score == MX_SCORE_SOFTMAX_ALL) softmax_64(p, t, lane, top, sum);
+    const unsigned long long key = e >= 0 ? key_64(p, t, e, top, sum) : 0ull;
+    int rank = 0;
+    for (int j = 0; j < total; ++j) {
+        const unsigned long long other = __shfl_sync(kFull, key, j);
+        rank += other > key || (other == key && j < lane);
+    }
+    if (lane < total) shared[rank].y = (uint32_t)e;
+    __syncwarp();
+    return lane < min(total, p.top_k) ? (int)shared[lane].y : -1;
+}
+
+// A warp a token: lane i holds VPL neighbouring experts.
+//
+// The largest top_k (and one more, for the doubts below): with few experts a lane they leave one by one, each by a maximum
+// over the warp (one instruction on 32-bit integers).  With more, the (top_k + 1)-th largest of the lanes' own
+// maxima bounds them from below; what reaches it, rarely more than a dozen, is gathered in shared memory, one a lane, and
+// ranked by counting.  (More than 32 such candidates: one by one.)
+//
+// Keys with a score or a bias are sums of rounded terms, and experts are told apart by them all the same: a key's
+// error has a bound, and where two neighbours in the order, or the groups on both sides of the cut, are no further
+// apart than their bounds, the token is done again in 64 bits: among the candidates (that come within four bounds of the
+// least, so that the exact largest are there), one a lane, or, where the groups are in doubt, from the start.  The keys can
+// then be made of the approximate exponential and reciprocal; weights are not.
+template <int VPL, int KEYS>
+__global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteParams p) {
+    extern __shared__ unsigned long long route_smem[];
+    constexpr bool kCandidates = VPL > 2;
+    __shared__ uint2 candidates[kCandidates ? kRouteWarps : 1][32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t t = (int64_t)blockIdx.x * kRouteWarps + warp;
+    if (t >= p.T) return;
+    unsigned long long* keys = route_smem + (size_t)warp * p.E;  // this warp's, where there are groups or doubts
+    constexpr float kUlp = 0x1p-24f;
+
+    float l[VPL];
+    load_logits(p, t, lane, l);
     float m = 0.0f, sum = 1.0f;
-    if (p.score == MX_SCORE_SOFTMAX_ALL && (scored || !p.renormalize)) {
+    if (KEYS == kKeysSoftmax || (KEYS <= kKeysBias && p.score == MX_SCORE_SOFTMAX_ALL && !p.renormalize)) {
         float top = l[0];
 #pragma unroll
         for (int i = 1; i < VPL; ++i) top = fmaxf(top, l[i]);
@@ -210,94 +277,196 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RoutePara
 
     uint32_t ord[VPL];
     float err = 0.0f;  // of a key at most
+    if constexpr (KEYS == kKeysLogits) {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-        float key = l[i], own = 0.0f;
-        if (scored) {
-            // in units of 2^-24 of the score: expf 4 (2 ulp), sums and quotients 1 each
-            if (p.score == MX_SCORE_SIGMOID) {
-                key = 1.0f / (1.0f + expf(-key));
-                own = 8 * kUlp * key;
-            } else if (p.score == MX_SCORE_SOFTMAX_ALL) {
-                // the exponent's difference d, which is rounded, here and (7, the entropy, at most) in the sum; two
-                // expf; 5 + VPL sums; the quotient; and what subnormals lose
-                const float d = m - l[i];
-                key = expf(-d) / sum;
-                own = (fminf(d, 200.0f) + 24 + VPL) * kUlp * key + 0x1p-126f;
+        for (int i = 0; i < VPL; ++i) ord[i] = l[i] == -INFINITY ? 0u : order_of(l[i]);
+    } else {
+        float b[VPL], top = -INFINITY, largest = 0.0f;  // the largest logit, the largest |key|
+        if (p.bias != nullptr) load_row<float, VPL>(p.bias, p.bias, p.E, lane, 0.0f, b);
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+            float key = l[i];
+            if constexpr (KEYS == kKeysSigmoid) {
+                top = fmaxf(top, key);
+                key = rcp_approx(1.0f + exp2_approx(key * -1.4426950408889634f));
+            } else if constexpr (KEYS == kKeysSoftmax) {
+                key = expf(l[i] - m) / sum;
             }
-            if (p.bias) {
-                const int e = lane * VPL + i;
-                key += e < p.E ? p.bias[e] : 0.0f;
-                own += kUlp * fabsf(key);
+            if (p.bias != nullptr) {
+                key += b[i];
+                if (key != -INFINITY) largest = fmaxf(largest, fabsf(key));
             }
+            ord[i] = l[i] == -INFINITY || key == -INFINITY ? 0u : order_of(key);
         }
-        ord[i] = l[i] == -INFINITY || key == -INFINITY ? 0u : order_of(key);
-        if (ord[i]) err = fmaxf(err, own);
+        // Bounds in units of 2^-24.
+        if constexpr (KEYS == kKeysSigmoid) {
+            // Of a score s: e^-l's exponent is a product with a rounded constant (1.5 |l|, times e^-l / (1 + e^-l)), its
+            // value good to 2 ulp (4); the sum 1; the reciprocal 2 (1 ulp): at most s (7 + 1.5 ln(1/s)), which grows with
+            // s, so that the largest score's holds for all.  (ln(1/s) <= |l| + ln 2.)
+            top = value_of(__reduce_max_sync(kFull, order_of(top)));
+            const float s = rcp_approx(1.0f + exp2_approx(top * -1.4426950408889634f)) * 1.001f;
+            err = s * (9 + 1.5f * (top < 0.0f ? fminf(-top, 128.0f) : 0.0f)) * kUlp + 0x1p-125f;
+        } else if constexpr (KEYS == kKeysSoftmax) {
+            // Of a score p: the exponent's difference d, which is rounded, here and (7, the entropy, at most) in the sum;
+            // two expf of 4; 5 + VPL sums; the quotient: p (d + 21 + VPL), where p <= e^-d and d e^-d < 1
+            err = (26 + VPL) * kUlp * fminf(1.001f / sum, 1.0f) + kUlp + 0x1p-125f;
+        }
+        if (p.bias != nullptr) err += kUlp * __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(largest)));
     }
-    err = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(err)));
     bool doubt = false;
 
     if (p.groups > 1) {
-        uint32_t* k32 = reinterpret_cast<uint32_t*>(keys);
+        const int size = p.group_size, lanes = p.group_lanes;
+        uint32_t low, high;  // the least worth that stays, the best that goes
+        if (lanes) {
+            // a group is a power of two of neighbouring lanes: its two largest by exchanges between them
+            uint32_t top = ord[0], second = 0u;
 #pragma unroll
-        for (int i = 0; i < VPL; ++i)
-            if (lane * VPL + i < p.E) k32[lane * VPL + i] = ord[i];
-        __syncwarp();
-        uint32_t worth;
-        const uint32_t stay = best_groups(k32, p, lane, worth);
-        if (!p.group_max || p.bias) {
-            // the least that stays against the best that goes; a sum of two keys, rounded
-            const uint32_t low = __reduce_min_sync(kFull, (stay >> lane & 1u) ? worth : 0xffffffffu);
-            const uint32_t high = __reduce_max_sync(kFull, (stay >> lane & 1u) || lane >= p.groups ? 0u : worth);
-            const float a = value_of(low), b = value_of(high);
-            if (stay && high) doubt = !(a - b > 4 * err + 2 * kUlp * (fabsf(a) + fabsf(b)));
+            for (int i = 1; i < VPL; ++i) {
+                second = max(second, min(top, ord[i]));
+                top = max(top, ord[i]);
+            }
+            for (int d = 1; d < lanes; d <<= 1) {
+                const uint32_t t2 = __shfl_xor_sync(kFull, top, d), s2 = __shfl_xor_sync(kFull, second, d);
+                second = max(min(top, t2), max(second, s2));
+                top = max(top, t2);
+            }
+            const uint32_t worth = p.group_max || !second ? top : order_of(value_of(top) + value_of(second));
+            int rank = 0;
+#pragma unroll 4
+            for (int first = 0; first < 32; first += lanes) {  // (past the last group: 0, which counts nowhere)
+                const uint32_t other = __shfl_sync(kFull, worth, first);
+                rank += other > worth || (other == worth && first + lanes <= lane);
+            }
+            const bool stay = worth && rank < p.top_groups;  // lanes past the last group hold nothing: worth is 0
+            low = __reduce_min_sync(kFull, stay ? worth : 0xffffffffu);
+            high = __reduce_max_sync(kFull, stay ? 0u : worth);
+            if (!stay) {
+#pragma unroll
+                for (int i = 0; i < VPL; ++i) ord[i] = 0u;
+            }
+        } else {
+            uint32_t* k32 = reinterpret_cast<uint32_t*>(keys);
+#pragma unroll
+            for (int i = 0; i < VPL; ++i)
+                if (lane * VPL + i < p.E) k32[lane * VPL + i] = ord[i];
+            __syncwarp();
+            uint32_t worth;
+            const uint32_t stay = best_groups(k32, p, lane, worth);
+            low = __reduce_min_sync(kFull, (stay >> lane & 1u) ? worth : 0xffffffffu);
+            high = __reduce_max_sync(kFull, (stay >> lane & 1u) || lane >= p.groups ? 0u : worth);
+#pragma unroll
+            for (int i = 0; i < VPL; ++i)
+                if (!(stay >> (min(lane * VPL + i, p.E - 1) / size) & 1u)) ord[i] = 0u;
+            __syncwarp();
         }
-        const int size = p.E / p.groups;
-#pragma unroll
-        for (int i = 0; i < VPL; ++i)
-            if (!(stay >> (min(lane * VPL + i, p.E - 1) / size) & 1u)) ord[i] = 0u;
+        if (high && (KEYS != kKeysLogits || !p.group_max)) {
+            // each sum of two keys off by twice a key's error, and rounded
+            const float a = value_of(low), b = value_of(high);
+            doubt = !(a - b > 4 * err + 2 * kUlp * (fabsf(a) + fabsf(b)));
+        }
     }
 
-    int mine = -1;
+    int mine = -1, candidate = -1, total = 0;
     uint32_t my_ord = 0;
     uint32_t best = ord[0];
 #pragma unroll
     for (int i = 1; i < VPL; ++i) best = max(best, ord[i]);
-    const int rounds = p.top_k + (err > 0.0f ? 1 : 0);
-    for (int j = 0; j < rounds; ++j) {
-        const uint32_t top = __reduce_max_sync(kFull, best);
-        if (top == 0u) break;
-        const int src = __ffs(__ballot_sync(kFull, best == top)) - 1;
-        int e = 0;
-        if (lane == src) {
-            bool found = false;
-            best = 0u;
+    const int wanted = p.top_k + (err > 0.0f ? 1 : 0);
+    bool one_by_one = true;
+    if constexpr (kCandidates) {
+        uint32_t left = best, least = 1u;
+        for (int j = 0; j < wanted; ++j) {  // equal ones leave together: there are then more candidates
+            least = __reduce_max_sync(kFull, left);
+            if (least == 0u) break;
+            if (left == least) left = 0u;
+        }
+        if (least == 0u) least = 1u;
+        else if (KEYS != kKeysLogits && err > 0.0f) least = order_of(value_of(least) - 4 * err);
+        int n = 0;
 #pragma unroll
-            for (int i = 0; i < VPL; ++i) {
-                if (!found && ord[i] == top) {
-                    found = true;
-                    e = lane * VPL + i;
-                    ord[i] = 0u;
-                }
-                best = max(best, ord[i]);
+        for (int i = 0; i < VPL; ++i) n += ord[i] >= least;
+        int at = n;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(kFull, at, d);
+            if (lane >= d) at += o;
+        }
+        total = __shfl_sync(kFull, at, 31);
+        at -= n;
+        if (total <= 32) {
+            one_by_one = false;
+            if (n) {
+#pragma unroll
+                for (int i = 0; i < VPL; ++i)
+                    if (ord[i] >= least) candidates[warp][at++] = make_uint2(ord[i], lane * VPL + i);
+            }
+            __syncwarp();
+            uint2 c = make_uint2(0u, 0u);
+            if (lane < total) {
+                c = candidates[warp][lane];
+                candidate = (int)c.y;
+            }
+            int rank = 0;  // they lie in the order of the experts
+#pragma unroll 4
+            for (int j = 0; j < total; ++j) {
+                const uint32_t other = __shfl_sync(kFull, c.x, j);
+                rank += other > c.x || (other == c.x && j < lane);
+            }
+            __syncwarp();
+            if (lane < total) candidates[warp][rank] = c;
+            __syncwarp();
+            if (lane < min(total, wanted)) {
+                c = candidates[warp][lane];
+                my_ord = c.x;
+                mine = (int)c.y;
             }
         }
-        e = __shfl_sync(kFull, e, src);
-        if (lane == j) {
-            mine = e;
-            my_ord = top;
+    }
+    if (one_by_one) {
+        for (int j = 0; j < wanted; ++j) {
+            const uint32_t top = __reduce_max_sync(kFull, best);
+            if (top == 0u) break;
+            const int src = __ffs(__ballot_sync(kFull, best == top)) - 1;
+            int e = 0;
+            if (lane == src) {
+                bool found = false;
+                best = 0u;
+#pragma unroll
+                for (int i = 0; i < VPL; ++i) {
+                    if (!found && ord[i] == top) {
+                        found = true;
+                        e = lane * VPL + i;
+                        ord[i] = 0u;
+                    }
+                    best = max(best, ord[i]);
+                }
+            }
+            e = __shfl_sync(kFull, e, src);
+            if (lane == j) {
+                mine = e;
+                my_ord = top;
+            }
         }
     }
-    if (err > 0.0f) {
-        const uint32_t next = __shfl_down_sync(kFull, my_ord, 1);
-        // NaN and infinities compare as not further apart
-        const bool close = lane < p.top_k && my_ord && next && !(value_of(my_ord) - value_of(next) > 2 * err);
-        doubt = doubt || __any_sync(kFull, close);
+    if constexpr (KEYS != kKeysLogits) {
+        if (err > 0.0f) {
+            const uint32_t next = __shfl_down_sync(kFull, my_ord, 1);
+            // NaN and infinities compare as not further apart
+            const bool close = lane < p.top_k && my_ord && next && !(value_of(my_ord) - value_of(next) > 2 * err);
+            const bool order = __any_sync(kFull, close);
+            if (kCandidates && order && !doubt && !one_by_one) {
+                __syncwarp();
+                mine = select_64_among(p, t, candidate, total, candidates[warp], lane);
+            } else {
+                doubt = doubt || order;
+            }
+        }
     }
-    if (doubt) mine = select_64(p, row, keys, lane);
+    if (doubt) mine = select_64(p, t, keys, lane);
 
     const bool in = lane < p.top_k && mine >= 0;
-    const float w = weight_of(p, in, in ? logit(row + mine) : 0.0f, m, sum);
+    const float w = weight_of(p, in, in ? logit_at(p, t, mine) : 0.0f, m, sum);
     if (lane < p.top_k) {
         p.experts[t * p.top_k + lane] = in ? mine : -1;
         p.weights[t * p.top_k + lane] = in ? w * p.scale : 0.0f;
@@ -523,22 +692,28 @@ static mxfp8_status_t route_check(const RouteParams& p, int32_t type) {
 }
 static bool aligned_to(const void* p, int bytes) { return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(bytes - 1)) == 0; }
 
-template <typename L, int VPL>
-static mxfp8_status_t route_launch(const RouteParams& p, cudaStream_t st) {
+template <int VPL>
+static mxfp8_status_t route_launch(RouteParams& p, cudaStream_t st) {
+    p.group_size = p.E / p.groups;
+    const int lanes = p.group_size / VPL;
+    p.group_lanes = p.group_size % VPL == 0 && (lanes & (lanes - 1)) == 0 ? lanes : 0;
     // 32 KB at most; none where logits are ranked as they are
     const int smem = p.groups > 1 || p.bias ? kRouteWarps * p.E * (int)sizeof(unsigned long long) : 0;
     const unsigned grid = (unsigned)((p.T + kRouteWarps - 1) / kRouteWarps);
-    route_kernel<L, VPL><<<grid, kRouteWarps * 32, smem, st>>>(p);
+    const bool scored = p.bias != nullptr || (p.groups > 1 && !p.group_max);
+    if (scored && p.score == MX_SCORE_SIGMOID) route_kernel<VPL, kKeysSigmoid><<<grid, kRouteWarps * 32, smem, st>>>(p);
+    else if (scored && p.score == MX_SCORE_SOFTMAX_ALL) route_kernel<VPL, kKeysSoftmax><<<grid, kRouteWarps * 32, smem, st>>>(p);
+    else if (p.bias) route_kernel<VPL, kKeysBias><<<grid, kRouteWarps * 32, smem, st>>>(p);
+    else route_kernel<VPL, kKeysLogits><<<grid, kRouteWarps * 32, smem, st>>>(p);
     return host::last_launch_status();
 }
-template <typename L>
-static mxfp8_status_t route_run(const RouteParams& p, cudaStream_t st) {
-    if (p.E <= 32) return route_launch<L, 1>(p, st);
-    if (p.E <= 64) return route_launch<L, 2>(p, st);
-    if (p.E <= 128) return route_launch<L, 4>(p, st);
-    if (p.E <= 256) return route_launch<L, 8>(p, st);
-    if (p.E <= 512) return route_launch<L, 16>(p, st);
-    return route_launch<L, 32>(p, st);
+static mxfp8_status_t route_run(RouteParams& p, cudaStream_t st) {
+    if (p.E <= 32) return route_launch<1>(p, st);
+    if (p.E <= 64) return route_launch<2>(p, st);
+    if (p.E <= 128) return route_launch<4>(p, st);
+    if (p.E <= 256) return route_launch<8>(p, st);
+    if (p.E <= 512) return route_launch<16>(p, st);
+    return route_launch<32>(p, st);
 }
 
 template <typename I>
@@ -564,6 +739,7 @@ extern "C" mxfp8_status_t mx_moe_route(const void* logits, int32_t logits_type, 
                                        float* weights, mxfp8_stream_t stream) {
     RouteParams p{};
     p.logits = logits;
+    p.type = logits_type;
     p.bias = bias;
     p.experts = experts;
     p.weights = weights;
@@ -586,10 +762,7 @@ extern "C" mxfp8_status_t mx_moe_route(const void* logits, int32_t logits_type, 
         !aligned_to(weights, 4))
         return MXFP8_ERR_ALIGN;
     if (mxfp8_status_t a = host::check_arch(); a != MXFP8_OK) return a;
-    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (logits_type == MX_LOGITS_FP32) return route_run<float>(p, st);
-    if (logits_type == MX_LOGITS_BF16) return route_run<__nv_bfloat16>(p, st);
-    return route_run<__half>(p, st);
+    return route_run(p, reinterpret_cast<cudaStream_t>(stream));
 }
 
 extern "C" mxfp8_status_t mx_moe_route_bwd(const void* logits, int32_t logits_type, int64_t T, int32_t E, int32_t top_k,

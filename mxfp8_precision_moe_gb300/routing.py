@@ -99,6 +99,7 @@ class _MoeRoute(torch.autograd.Function):
     def forward(ctx, logits, bias, args):
         experts, weights = _route(logits, bias, args)
         ctx.mark_non_differentiable(experts)
+        ctx.set_materialize_grads(False)  # no zeros for the experts' place
         ctx.save_for_backward(logits, experts)
         ctx.args = args
         return experts, weights
@@ -106,6 +107,8 @@ class _MoeRoute(torch.autograd.Function):
     @staticmethod
     @_first_order
     def backward(ctx, _, dweights):
+        if dweights is None:
+            return None, None, None
         logits, experts = ctx.saved_tensors
         return _route_bwd(logits, experts, dweights.contiguous(), ctx.args), None, None
 
@@ -137,7 +140,7 @@ def moe_route(logits: torch.Tensor, top_k: int, *, score: str = "softmax", bias:
         bias = bias.detach().contiguous()
     if _needs_grad(logits):
         return _MoeRoute.apply(logits, bias, args)
-    return _route(logits.detach(), bias, args)
+    return _route(logits, bias, args)
 
 
 # ---------------------------------------------------------------- the plan
@@ -166,6 +169,12 @@ class MoePlan:
             if not t.is_contiguous() or t.device != offs.device:
                 raise ValueError("MoePlan: contiguous tensors of one device expected")
         self.offs, self.counts, self.slot, self.place, self.multiple = offs, counts, slot, place, int(multiple)
+
+    @classmethod
+    def _of(cls, offs, counts, slot, place, multiple):  # arrays that need no checks
+        plan = cls.__new__(cls)
+        plan.offs, plan.counts, plan.slot, plan.place, plan.multiple = offs, counts, slot, place, multiple
+        return plan
 
     @property
     def rows(self) -> int:
@@ -200,27 +209,28 @@ def moe_plan(experts: torch.Tensor, num_experts: int, multiple: int = 1, *, exac
     if not 1 <= multiple <= MAX_MULTIPLE:
         raise ValueError(f"multiple: 1 .. {MAX_MULTIPLE}, got {multiple}")
     _on_device(experts)
-    L = load()
-    rows = L.mx_moe_plan_rows(T, k, E, multiple)
-    if rows < 0:
+    n = T * k
+    if n + E * multiple >= 2 ** 31:
         raise ValueError(f"experts: too many rows for 32-bit row numbers ({T} tokens of {k})")
+    rows = (n + min(E, n) * (multiple - 1)) // multiple * multiple  # mx_moe_plan_rows
     experts = experts.contiguous()
     dev = experts.device
+    L = load()
     nbytes = L.mx_moe_plan_workspace(T, k, E)
-    # one allocation for the plan's four arrays and the workspace, each on a 16-byte boundary
-    sizes = (E, E, rows, T * k, (nbytes + 3) // 4)
-    ends, at = [], 0
-    for n in sizes:
-        ends.append((at, at + n))
-        at += (n + 3) // 4 * 4
-    buf = torch.empty(at, dtype=torch.int32, device=dev)
-    offs, counts, slot, place, ws = (buf[a:b] for a, b in ends)
-    check(L.mx_moe_plan(experts.data_ptr(), experts.element_size(), T, k, E, multiple, rows, offs.data_ptr(),
-                        counts.data_ptr(), slot.data_ptr(), place.data_ptr(), ws.data_ptr(), nbytes,
-                        _raw_stream(dev.index)), "mx_moe_plan")
+    # one allocation for the plan's arrays and the workspace, each on a 16-byte boundary
+    counts_at = (E + 3) // 4 * 4
+    slot_at = 2 * counts_at
+    place_at = slot_at + (rows + 3) // 4 * 4
+    ws_at = place_at + (n + 3) // 4 * 4
+    buf = torch.empty(ws_at + nbytes // 4, dtype=torch.int32, device=dev)
+    at = buf.data_ptr()
+    check(L.mx_moe_plan(experts.data_ptr(), experts.element_size(), T, k, E, multiple, rows, at, at + 4 * counts_at,
+                        at + 4 * slot_at, at + 4 * place_at, at + 4 * ws_at, nbytes, _raw_stream(dev.index)), "mx_moe_plan")
+    offs, counts = buf.as_strided((E,), (1,), 0), buf.as_strided((E,), (1,), counts_at)
+    slot, place = buf.as_strided((rows,), (1,), slot_at), buf.as_strided((T, k), (k, 1), place_at)
     if exact:
         slot = slot[:int(offs[-1])]
-    return MoePlan(offs, counts, slot, place.view(T, k), multiple)
+    return MoePlan._of(offs, counts, slot, place, multiple)
 
 
 # ---------------------------------------------------------------- rows
