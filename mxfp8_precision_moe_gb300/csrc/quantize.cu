@@ -65,6 +65,9 @@ struct QParams {
     const int32_t* slot;
     const float* row_w;
     int32_t top_k, slots;
+    uint32_t seg;        // column tiles of a unit: what a CTA takes in a row, of one row of tiles
+    uint32_t strip;      // units of a strip of columns
+    int64_t units;
 };
 
 // Kernel modes: plain MX quantization; the Hadamard variants (fp32 values), without and with
@@ -309,8 +312,15 @@ constexpr int kQConsumerThreads = 256;         // 8 consumer warps, no producer 
 // kModeSwiBwd (ROW|COL only): 256 threads, no TMA ring: each warp loads its patches of dh, h1 and h3
 // straight from global memory (three inputs a stage would leave room for too few warps to hide the
 // arithmetic's latency), computes dh1 and dh3 and quantizes each both ways.
-// kModeGather (ROW, COL, ROW|COL): loads as in kModeSwiBwd, each row through its slot.  Tiles go down a column strip
-// before the next strip, so that the strip of x (256 bytes a token) stays in L2 for all rows that a token has.
+// kModeGather (ROW, COL, ROW|COL): a warp fills a ring of its own patches (32 rows x 64 columns) by 16-byte asynchronous
+// copies, each row through its slot; warps do not wait for one another.  A CTA takes units of up to 8 column tiles, whose
+// rows' slots, weights and places in the scales are looked up once.  16384 x 5120 both ways, 69 us (the plain kernel with
+// its TMA ring 61): bulk copies by a producer warp, 256 bytes a row, 107 (one takes about 50 clocks); a producer warp's
+// 16-byte copies 84 (its instructions bind); each warp's own loads without a ring 95; this ring with a division and a
+// look-up a tile 80.  Eight rows a token of 7168, 70 thousand rows, 340 us, where moe_gather and the plain kernel take 560.
+// Units go down a strip of columns before the next strip, row of tiles by row of tiles within it: a strip as wide as x's
+// share of it stays in L2 for all rows that a token has, and no narrower, since short pieces of rows far apart are slow to
+// read and write.
 // The stochastic-rounding kernels have no producer warp: warp 0's lane 0 issues the ring's loads (the
 // first kQStages tiles up front, then each stage again once all 8 warps are done with it), so that 2
 // CTAs of 8 warps leave each thread 128 registers instead of 96 (their random words spilled at 96).
@@ -318,11 +328,47 @@ constexpr int kQConsumerThreads = 256;         // 8 consumer warps, no producer 
 // refill waits for the slowest warp's whole tile, which costs more than the registers give.
 template <int kMode>
 constexpr bool kFoldedProducer = kMode == kModeSR || kMode == kModeExtSR;
-// No TMA ring: each warp loads its own patches.
 template <int kMode>
-constexpr bool kDirectLoads = kMode == kModeSwiBwd || kMode == kModeGather;
+constexpr int kQThreadsOf = (kMode == kModeSwiBwd || kMode == kModeGather || kFoldedProducer<kMode>) ? kQConsumerThreads
+                                                                                                     : kQThreads;
+constexpr int kGatherStages = 3;                          // patches of a warp in flight
+constexpr int kPatchBytes = 32 * 64 * 2;
+constexpr int kGatherSmem = 8 * kGatherStages * kPatchBytes;
 template <int kMode>
-constexpr int kQThreadsOf = (kDirectLoads<kMode> || kFoldedProducer<kMode>) ? kQConsumerThreads : kQThreads;
+constexpr int kQSmemOf = kMode == kModeSwiBwd ? 0 : kMode == kModeGather ? kGatherSmem + 128 : kQSmem;
+
+// Asynchronous copy of 16 bytes to shared memory; zeros where there is no source.
+__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src, bool some) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(some ? 16 : 0) : "memory");
+}
+
+// A CTA's way through its gather tiles: units blockIdx.x, + gridDim.x, ..., strip by strip, row of tiles by row of tiles
+// within a strip; of a unit its column tiles.
+struct GatherCursor {
+    int64_t unit;
+    uint32_t tr, tc, last;  // the unit's row of tiles, the column tile, the unit's last one
+    __device__ __forceinline__ void enter(const QParams& p) {
+        if (unit >= p.units) return;
+        const uint32_t u = (uint32_t)unit, tiles_r = (uint32_t)p.tiles_r, tiles_c = (uint32_t)p.tiles_c;
+        const uint32_t segs = (tiles_c + p.seg - 1) / p.seg;
+        const uint32_t first = u / (tiles_r * p.strip) * p.strip;  // the strip's first segment
+        const uint32_t rem = u - first * tiles_r, width = min(p.strip, segs - first);
+        tr = rem / width;
+        tc = (first + (rem - tr * width)) * p.seg;
+        last = min(tc + p.seg, tiles_c) - 1;
+    }
+    __device__ __forceinline__ bool done(const QParams& p) const { return unit >= p.units; }
+    // to the next tile; true where a unit begins
+    __device__ __forceinline__ bool step(const QParams& p) {
+        if (tc < last) {
+            ++tc;
+            return false;
+        }
+        unit += gridDim.x;
+        enter(p);
+        return true;
+    }
+};
 
 // kHad (the Hadamard kernels only): bit 0 = transform the row-wise copy, bit 1 = the column-wise copy,
 // fixed per instance so that each holds only the paths its options take.
@@ -354,7 +400,7 @@ __global__ void __launch_bounds__(kQThreadsOf<kMode>, 2)
     const bool grouped = p.offs != nullptr && p.G > 1;
     if (grouped && p.blocked && threadIdx.x < 32) build_group_table(p.offs, p.G, p.R, ends_s, pstart_s, &ptotal_s);
     constexpr bool kFolded = kFoldedProducer<kMode>;
-    if (threadIdx.x == (kFolded ? 0 : 256)) {
+    if (!kGather && threadIdx.x == (kFolded ? 0 : 256)) {
         for (int s = 0; s < kQStages; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 8);
@@ -418,6 +464,77 @@ __global__ void __launch_bounds__(kQThreadsOf<kMode>, 2)
         return;
     }
 
+    // ---- the gather's ring.  `ahead` walks before the tiles that are worked on; a unit's tokens (of this warp's row
+    // `lane`) are looked up while the unit before it is copied.
+    uint8_t* patches = tiles + warp * (kGatherStages * kPatchBytes);
+    auto row_slot = [&](const GatherCursor& at) -> int32_t {
+        const int64_t r = (int64_t)at.tr * 128 + (warp >> 1) * 32 + lane;
+        const int32_t slot = !at.done(p) && r < p.R ? __ldg(p.slot + r) : -1;
+        return slot < p.slots ? slot : -1;
+    };
+    auto token_of = [&](int32_t slot) -> int32_t {
+        return slot >= 0 ? (int32_t)((uint32_t)slot / (uint32_t)p.top_k) : -1;
+    };
+    GatherCursor ahead{}, here{};
+    int32_t token = -1, next_slot = -1;
+    float row_w = 1.0f, next_w = 1.0f;
+    int64_t row_at = -1, col_at = -1;  // of the unit: row `lane`'s place in the row scales, the warp's in the column scales
+    auto copy_patch = [&](int stage) {
+        if (!ahead.done(p)) {
+            const int64_t c = (int64_t)ahead.tc * 128 + (warp & 1) * 64 + 8 * (lane & 7);  // of one row in four
+            const uint16_t* base = p.x + (c < p.C ? c : 0);
+            const uint32_t dst = smem_u32(patches + stage * kPatchBytes) + lane * 16;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int32_t from = __shfl_sync(0xffffffffu, token, 4 * i + (lane >> 3));
+                copy16_async(dst + 512 * i, base + (int64_t)max(from, 0) * p.C, from >= 0 && c < p.C);
+            }
+            if (ahead.step(p)) {
+                token = token_of(next_slot);
+                GatherCursor then = ahead;
+                then.unit += gridDim.x;
+                then.enter(p);
+                next_slot = row_slot(then);
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    auto weight_of = [&](const GatherCursor& at) -> float {
+        const int32_t slot = p.row_w != nullptr ? row_slot(at) : -1;
+        return slot >= 0 ? __ldg(p.row_w + slot) : 1.0f;
+    };
+    // what the tiles of a unit have in common
+    auto enter_unit = [&]() {
+        const int64_t r0 = (int64_t)here.tr * 128 + (warp >> 1) * 32;
+        row_w = next_w;
+        GatherCursor then = here;
+        then.unit += gridDim.x;
+        then.enter(p);
+        next_w = weight_of(then);
+        row_at = r0 + lane;
+        col_at = r0 / kBlk;
+        if (grouped && !here.done(p)) {
+            const int g = find_group(ends_s, p.G, r0 + lane);
+            row_at = g < p.G ? pstart_s[g] + (r0 + lane - (g ? ends_s[g - 1] : 0)) : -1;
+            col_at = __shfl_sync(0xffffffffu, row_at, 0);
+            if (col_at >= 0) col_at /= kBlk;
+        }
+    };
+    if constexpr (kGather) {
+        ahead.unit = here.unit = blockIdx.x;
+        ahead.enter(p);
+        here.enter(p);
+        token = token_of(row_slot(ahead));
+        GatherCursor then = ahead;
+        then.unit += gridDim.x;
+        then.enter(p);
+        next_slot = row_slot(then);
+#pragma unroll
+        for (int s = 0; s < kGatherStages; ++s) copy_patch(s);
+        next_w = weight_of(here);
+        enter_unit();
+    }
+
     // ---- zero padding of the blocked layouts (bytes no tile writes).  Done before the tile loop, so it
     // overlaps the producer filling the ring, in small units spread over all CTAs:
     //   row layout:    (batch, group, 32-row chunk) of the group's padding rows, every column tile;
@@ -439,11 +556,10 @@ __global__ void __launch_bounds__(kQThreadsOf<kMode>, 2)
                 const int64_t P = grouped ? pstart_s[g] : 0;
                 const int64_t r0 = size + chunk * 32, r1 = min64(r0 + 32, ((size + 127) / 128) * 128);
                 uint8_t* sb = s_row + bb * p.s_row_bstride;
-                for (int64_t i = tid; i < (r1 - r0) * ct_row; i += 256) {
-                    const int64_t pr = P + r0 + i / ct_row, t = i % ct_row;
-                    *reinterpret_cast<uint32_t*>(sb + ((pr >> 7) * ct_row + t) * 512 + (pr & 31) * 16 +
-                                                 ((pr >> 5) & 3) * 4) = 0u;
-                }
+                for (int64_t pr = P + r0 + (tid >> 5); pr < P + r1; pr += 8)
+                    for (int64_t t = tid & 31; t < ct_row; t += 32)
+                        *reinterpret_cast<uint32_t*>(sb + ((pr >> 7) * ct_row + t) * 512 + (pr & 31) * 16 +
+                                                     ((pr >> 5) & 3) * 4) = 0u;
             } else if (u < units_row + units_colg) {
                 const int64_t u2 = u - units_row;
                 const int64_t bb = u2 / (G_eff * rslices);
@@ -455,19 +571,16 @@ __global__ void __launch_bounds__(kQThreadsOf<kMode>, 2)
                 const int64_t c0 = Q + size / kBlk, c1 = Q + ((size + 127) / 128) * 4;
                 const int64_t rlo = rs * 128, rn = min64(128, C - rlo);
                 uint8_t* sb = s_col + bb * p.s_col_bstride;
-                for (int64_t i = tid; i < rn * (c1 - c0); i += 256) {
-                    const int64_t r = rlo + i / (c1 - c0), c = c0 + i % (c1 - c0);
-                    sb[blocked_off(r, c, ct_col)] = 0;
-                }
+                if ((tid & 127) < rn)
+                    for (int64_t c = c0 + (tid >> 7); c < c1; c += 2) sb[blocked_off(rlo + (tid & 127), c, ct_col)] = 0;
             } else {
                 const int64_t bb = u - units_row - units_colg;
                 const int64_t rows_p = ((C + 127) / 128) * 128;
                 uint8_t* sb = s_col + bb * p.s_col_bstride;
-                for (int64_t i = tid; i < (rows_p - C) * ct_col; i += 256) {
-                    const int64_t r = C + i / ct_col, t = i % ct_col;
-                    *reinterpret_cast<uint32_t*>(sb + ((r >> 7) * ct_col + t) * 512 + (r & 31) * 16 +
-                                                 ((r >> 5) & 3) * 4) = 0u;
-                }
+                for (int64_t r = C + (tid >> 5); r < rows_p; r += 8)
+                    for (int64_t t = tid & 31; t < ct_col; t += 32)
+                        *reinterpret_cast<uint32_t*>(sb + ((r >> 7) * ct_col + t) * 512 + (r & 31) * 16 +
+                                                     ((r >> 5) & 3) * 4) = 0u;
             }
         }
     };
@@ -481,10 +594,18 @@ __global__ void __launch_bounds__(kQThreadsOf<kMode>, 2)
     int stage = 0;
     uint32_t phase = 0;
 
-    for (int64_t t = blockIdx.x; t < p.ntiles; t += gridDim.x) {
-        const uint32_t tt = (uint32_t)t, b32 = tt / per_b, rem = tt - b32 * per_b;
-        const uint32_t tiles_r = (uint32_t)p.tiles_r;
-        const uint32_t tr = kGather ? rem % tiles_r : rem / tiles_c, tc = kGather ? rem / tiles_r : rem - tr * tiles_c;
+    for (int64_t t = blockIdx.x; kGather ? !here.done(p) : t < p.ntiles; t += gridDim.x) {
+        uint32_t b32 = 0, tr, tc;
+        if constexpr (kGather) {
+            tr = here.tr;
+            tc = here.tc;
+        } else {
+            const uint32_t tt = (uint32_t)t;
+            b32 = tt / per_b;
+            const uint32_t rem = tt - b32 * per_b;
+            tr = rem / tiles_c;
+            tc = rem - tr * tiles_c;
+        }
         const int64_t b = b32;
         const int64_t row0 = (int64_t)tr * 128 + wi * 32, col0 = (int64_t)tc * 128 + wj * 64;
         // this warp's 32 x 64 sub-tile: lane rows 8li..8li+7, columns 8lj..8lj+7 (16 bytes each)
@@ -492,7 +613,19 @@ __global__ void __launch_bounds__(kQThreadsOf<kMode>, 2)
         uint32_t v[8][4];
         int cur_stage = 0;
         uint32_t cur_phase = 0;
-        if constexpr (!kDirectLoads<kMode>) {
+        if constexpr (kGather) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(kGatherStages - 1) : "memory");
+            __syncwarp();
+            src = patches + stage * kPatchBytes + (8 * li) * 128 + 8 * lj * 2;
+#pragma unroll
+            for (int rr = 0; rr < 8; ++rr) {
+                const uint4 u = *reinterpret_cast<const uint4*>(src + rr * 128);
+                v[rr][0] = u.x; v[rr][1] = u.y; v[rr][2] = u.z; v[rr][3] = u.w;
+            }
+            __syncwarp();
+            copy_patch(stage);
+            if (++stage == kGatherStages) stage = 0;
+        } else if constexpr (!kSwiBwd) {
             if (!mbar_wait_bounded(&full[stage], phase, kQTimeoutNs, abort_flag, p.dev_status)) break;
             src = tiles + stage * kStageBytes + (32 * wi + 8 * li) * 256 + (64 * wj + 8 * lj) * 2;
             if constexpr (!kExt) {
@@ -527,6 +660,11 @@ __global__ void __launch_bounds__(kQThreadsOf<kMode>, 2)
                     issue_tile(tn, cur_stage, cur_phase ^ 1u);
             }
         };
+        const int64_t row_place = row_at, col_place = col_at;
+        const float row_weight = row_w;
+        if constexpr (kGather) {
+            if (here.step(p)) enter_unit();
+        }
         if (row0 >= R || col0 >= C) {  // warp-uniform
             if constexpr (kExt) release_stage();
             continue;
@@ -535,7 +673,7 @@ __global__ void __launch_bounds__(kQThreadsOf<kMode>, 2)
         const int64_t c8 = col0 + 8 * lj;  // first column of this lane
         const bool cval = c8 < C;          // C % 32 == 0: 8-column chunks are all-in or all-out
         int wg0 = 0, wg1 = 0;              // groups of the warp's first and last row (warp-uniform)
-        if (grouped && p.blocked) {
+        if (!kGather && grouped && p.blocked) {
             wg0 = find_group(ends_s, p.G, row0);
             const int64_t rl = min64(row0 + 31, R - 1);
             wg1 = (wg0 < p.G && rl < ends_s[wg0]) ? wg0 : find_group(ends_s, p.G, rl);
@@ -562,7 +700,10 @@ __global__ void __launch_bounds__(kQThreadsOf<kMode>, 2)
                 return;
             }
             int64_t pr = row;
-            if (grouped) {
+            if constexpr (kGather) {
+                pr = row_place;
+                if (pr < 0) return;
+            } else if (grouped) {
                 int g = wg0;
                 if (wg0 != wg1) g = find_group(ends_s, p.G, row);
                 if (g >= p.G) return;
@@ -587,7 +728,10 @@ __global__ void __launch_bounds__(kQThreadsOf<kMode>, 2)
                 return;
             }
             int64_t pc = rb;
-            if (grouped) {
+            if constexpr (kGather) {
+                pc = col_place;
+                if (pc < 0) return;
+            } else if (grouped) {
                 if (wg0 >= p.G) return;
                 pc = pstart_s[wg0] / kBlk + (row0 - (wg0 ? ends_s[wg0 - 1] : 0)) / kBlk;
             }
@@ -1047,27 +1191,12 @@ __global__ void __launch_bounds__(kQThreadsOf<kMode>, 2)
             quant_rowcol(a, p.q_row, p.s_row, p.q_col, p.s_col);
             quant_rowcol(u3, p.q_row2, p.s_row2, p.q_col2, p.s_col2);
         } else if constexpr (kGather) {
-            // each lane looks one row up; its patch's eight come from the lanes that hold them
-            const int32_t slot = row0 + lane < R ? __ldg(p.slot + row0 + lane) : -1;
-            const bool has = slot >= 0 && slot < p.slots;
-            const int32_t token = has ? (int32_t)((uint32_t)slot / (uint32_t)p.top_k) : -1;
-#pragma unroll
-            for (int rr = 0; rr < 8; ++rr) {
-                const int32_t from = __shfl_sync(0xffffffffu, token, 8 * li + rr);
-                uint4 u = make_uint4(0, 0, 0, 0);
-                if (from >= 0 && cval) u = __ldg(reinterpret_cast<const uint4*>(p.x + (int64_t)from * C + c8));
-                v[rr][0] = u.x; v[rr][1] = u.y; v[rr][2] = u.z; v[rr][3] = u.w;
-            }
-            if (p.row_w != nullptr) {  // bf16(w x), as the combination's backward gives
-                const float w = has ? __ldg(p.row_w + slot) : 0.0f;
+            if (p.row_w != nullptr) {  // bf16(w x), as the combination's backward gives; a row without a token stays zeros
 #pragma unroll
                 for (int rr = 0; rr < 8; ++rr) {
-                    const float f = __shfl_sync(0xffffffffu, w, 8 * li + rr);
-                    // a row without a token stays zeros, not zeros with f's sign
-                    const bool some = __shfl_sync(0xffffffffu, token, 8 * li + rr) >= 0;
+                    const float f = __shfl_sync(0xffffffffu, row_weight, 8 * li + rr);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if (some) v[rr][k] = pack_bf16x2(bf16lo(v[rr][k]) * f, bf16hi(v[rr][k]) * f);
+                    for (int k = 0; k < 4; ++k) v[rr][k] = pack_bf16x2(bf16lo(v[rr][k]) * f, bf16hi(v[rr][k]) * f);
                 }
             }
             quant_rowcol(v, p.q_row, p.s_row, p.q_col, p.s_col);
@@ -1117,7 +1246,7 @@ static bool make_x_map(CUtensorMap* m, const QParams& p, const uint16_t* base) {
 
 template <unsigned DIRS, int kMode = kModePlain, unsigned kHad = 0>
 static mxfp8_status_t launch_dirs(const CUtensorMap& m, const QParams& p, int64_t grid, cudaStream_t st) {
-    constexpr int smem = kDirectLoads<kMode> ? 0 : kQSmem;
+    constexpr int smem = kQSmemOf<kMode>;
     static std::atomic<int> attr_set[host::kMaxDevices];
     if (!host::ensure_smem(reinterpret_cast<const void*>(quant_tile_kernel<DIRS, kMode, kHad>), smem, attr_set))
         return MXFP8_ERR_LAUNCH;
@@ -1219,7 +1348,7 @@ static mxfp8_status_t launch_swiglu_bwd(const QParams& p, cudaStream_t st) {
 // Rows through a plan.  The tensor map is unused.
 static mxfp8_status_t gather_quantize(QParams& p, unsigned dirs, cudaStream_t st) {
     const CUtensorMap m{};
-    const int64_t grid = std::min<int64_t>(p.ntiles, (int64_t)host::num_sms() * 2);
+    const int64_t grid = std::min<int64_t>(p.units, (int64_t)host::num_sms() * 2);
     switch (dirs) {
         case MXFP8_ROW: return launch_dirs<MXFP8_ROW, kModeGather>(m, p, grid, st);
         case MXFP8_COL: return launch_dirs<MXFP8_COL, kModeGather>(m, p, grid, st);
@@ -1473,7 +1602,7 @@ extern "C" mxfp8_status_t mxfp8_gather_quantize(const void* x_bf16, const int32_
         if (reinterpret_cast<uintptr_t>(v) & 3u) return MXFP8_ERR_ALIGN;
     if (mxfp8_status_t a = host::check_arch(); a != MXFP8_OK) return a;
     QParams p{};
-    p.x = static_cast<const uint16_t*>(x_bf16);
+    p.x = static_cast<const uint16_t*>(T ? x_bf16 : row ? q_row : q_col);  // of no tokens: an address, never read
     p.R = rows; p.C = D; p.batch = 1;
     p.q_row = static_cast<uint8_t*>(q_row); p.s_row = static_cast<uint8_t*>(s_row);
     p.q_col = static_cast<uint8_t*>(q_col); p.s_col = static_cast<uint8_t*>(s_col);
@@ -1484,6 +1613,14 @@ extern "C" mxfp8_status_t mxfp8_gather_quantize(const void* x_bf16, const int32_
     p.top_k = top_k; p.slots = (int32_t)(T * top_k);
     p.tiles_r = (rows + 127) / 128; p.tiles_c = (D + 127) / 128; p.ntiles = p.tiles_r * p.tiles_c;
     if (p.ntiles >= INT32_MAX) return MXFP8_ERR_SHAPE;
+    // Units of several column tiles share what their rows need (slots, weights, places in the scales), as long as every CTA
+    // has enough of them to come out even.
+    p.seg = 1;
+    while (p.seg < 8 && p.ntiles >= (int64_t)16 * p.seg * 2 * host::num_sms()) p.seg *= 2;
+    const int64_t segs = (p.tiles_c + p.seg - 1) / p.seg;
+    p.units = p.tiles_r * segs;
+    // x's share of a strip: 32 MB, a quarter of L2, where a token has several rows
+    p.strip = (uint32_t)(top_k == 1 ? segs : std::max<int64_t>(1, std::min(segs, (int64_t)(32 << 20) / (max64(T, 1) * 256 * p.seg))));
     return mx::gather_quantize(p, dirs, reinterpret_cast<cudaStream_t>(stream));
 }
 
