@@ -94,11 +94,13 @@ mxfp8_status_t mx_moe_combine_bwd(const void* dout_bf16, const void* y_bf16, con
  *   are multiples of 32.  Buffers as for mxfp8_quantize_2d with M = rows.
  * mxfp4_gather_quantize -- mxfp4_quantize_2d(rows, blocked, offs) of the same rows.
  * ------------------------------------------------------------------------- */
-mxfp8_status_t mxfp8_gather_quantize(const void* x_bf16, const int32_t* slot, const float* w, int64_t rows, int64_t T,
-                                     int32_t top_k, int64_t D, unsigned dirs, const int32_t* offs, int32_t G, void* q_row,
-                                     void* s_row, void* q_col, void* s_col, int32_t* dev_status, mxfp8_stream_t stream);
-mxfp8_status_t mxfp4_gather_quantize(const void* x_bf16, const int32_t* slot, int64_t rows, int64_t T, int32_t top_k,
-                                     int64_t D, const int32_t* offs, int32_t G, void* q, void* s, mxfp8_stream_t stream);
+mxfp8_status_t mxfp8_gather_quantize(const void* x_bf16, const int32_t* slot, const int32_t* place, const float* w,
+                                     int64_t rows, int64_t T, int32_t top_k, int64_t D, unsigned dirs, const int32_t* offs,
+                                     int32_t G, void* q_row, void* s_row, void* q_col, void* s_col, int32_t* dev_status,
+                                     mxfp8_stream_t stream);
+mxfp8_status_t mxfp4_gather_quantize(const void* x_bf16, const int32_t* slot, const int32_t* place, int64_t rows, int64_t T,
+                                     int32_t top_k, int64_t D, const int32_t* offs, int32_t G, void* q, void* s,
+                                     mxfp8_stream_t stream);
 
 /* ----------------------------------------------------------------------------
  * mxfp8_dequantize -- the values that one copy of mxfp8_quantize_2d stands for, in bf16:

@@ -22,7 +22,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libmxfp8moe.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["api.cu", "quantize.cu", "grouped_mm.cu", "mxfp4_quantize.cu", "mxfp4_mm.cu", "moe_tokens.cu", "routing.cu",
-           "token_rows.cu"]
+           "token_rows.cu", "gather_quantize.cu"]
 
 
 def nvcc() -> str:

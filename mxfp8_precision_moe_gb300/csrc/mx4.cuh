@@ -66,6 +66,52 @@ __device__ __forceinline__ float2 e2m1x2_value(uint32_t byte) {
     return make_float2(lo, hi);
 }
 
+// Largest magnitude of each half of two bf16 pairs, NaN winning (the sign bits left are not used).
+__device__ __forceinline__ uint32_t amax_pair(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+// A bf16 pair times the bf16 power of two f, exact in fp32 (a -0 addend keeps the sign of a zero).
+__device__ __forceinline__ float2 scale_pair(uint32_t w, uint32_t f) {
+    float2 r;
+    asm("{\n\t.reg .b16 a0, a1, b0, b1;\n\tmov.b32 {a0, a1}, %2;\n\tmov.b32 {b0, b1}, %3;\n\t"
+        "fma.rn.f32.bf16 %0, a0, b0, 0f80000000;\n\tfma.rn.f32.bf16 %1, a1, b0, 0f80000000;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "r"(w), "r"(f));
+    return r;
+}
+
+// A block of 32 bf16 (16 pairs) -> its scale byte, codes in c.
+__device__ __forceinline__ uint32_t q4_block_bf16(const uint32_t (&w)[16], uint32_t (&c)[4]) {
+    uint32_t m = w[0];
+#pragma unroll
+    for (int i = 1; i < 16; ++i) m = amax_pair(m, w[i]);
+    const uint32_t s = e8m0_of<2>(max(m & 0x7FFFu, (m >> 16) & 0x7FFFu) << 16);
+    const uint32_t f = (254u - s) << 7;  // 2^(127 - s) as a bf16: s <= 252 for a finite amax
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 r = scale_pair(w[4 * i + j], f);
+            v[2 * j] = r.x;
+            v[2 * j + 1] = r.y;
+        }
+        c[i] = cvt_e2m1x8(v);
+    }
+    if (s == 0xFFu) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float v[8] = {bf16lo(w[4 * i]), bf16hi(w[4 * i]), bf16lo(w[4 * i + 1]), bf16hi(w[4 * i + 1]),
+                                bf16lo(w[4 * i + 2]), bf16hi(w[4 * i + 2]), bf16lo(w[4 * i + 3]), bf16hi(w[4 * i + 3])};
+            c[i] = nonfinite_e2m1x8(v);
+        }
+    }
+    return s;
+}
+
 // Where padded 128-row tile `t` of G row groups over M rows comes from.  Groups start on fresh
 // 128-row tiles, so the tile's number is also its band in the blocked scale layout.
 struct RowTile {

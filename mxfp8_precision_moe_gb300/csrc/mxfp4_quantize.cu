@@ -21,7 +21,6 @@
 
 #include "host_common.h"
 #include "mx4.cuh"
-#include "../../include/mxrouting.h"
 
 namespace mx {
 
@@ -41,11 +40,9 @@ struct Q4Params {
     int blocked;
     int cols_per_cta;      // column tiles a CTA walks
     int row_steps;         // of a tile's row steps, how many a CTA takes (blockIdx.z: which)
-    const int32_t* slot;   // gather: row r is x's row slot[r] / top_k, zeros where slot[r] is not in [0, slots)
-    int32_t top_k, slots;
 };
 
-enum Q4Kind : int { kQ4Plain = 0, kQ4Swiglu = 1, kQ4Dequant = 2, kQ4Gather = 3 };
+enum Q4Kind : int { kQ4Plain = 0, kQ4Swiglu = 1, kQ4Dequant = 2 };
 
 // The CTA's rows: matrix b, first row, rows inside, band of the scale layout.
 struct Q4Rows {
@@ -73,52 +70,6 @@ __device__ __forceinline__ Q4Rows q4_rows(const Q4Params& p) {
         r.rows = (int)min64(128, p.R - r.row0);
     }
     return r;
-}
-
-// Largest magnitude of each half of two bf16 pairs, NaN winning (the sign bits left are not used).
-__device__ __forceinline__ uint32_t amax_pair(uint32_t a, uint32_t b) {
-    uint32_t d;
-    asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    return d;
-}
-
-// A bf16 pair times the bf16 power of two f, exact in fp32 (a -0 addend keeps the sign of a zero).
-__device__ __forceinline__ float2 scale_pair(uint32_t w, uint32_t f) {
-    float2 r;
-    asm("{\n\t.reg .b16 a0, a1, b0, b1;\n\tmov.b32 {a0, a1}, %2;\n\tmov.b32 {b0, b1}, %3;\n\t"
-        "fma.rn.f32.bf16 %0, a0, b0, 0f80000000;\n\tfma.rn.f32.bf16 %1, a1, b0, 0f80000000;\n\t}"
-        : "=f"(r.x), "=f"(r.y)
-        : "r"(w), "r"(f));
-    return r;
-}
-
-// A block of 32 bf16 (16 pairs) -> its scale byte, codes in c.
-__device__ __forceinline__ uint32_t q4_block_bf16(const uint32_t (&w)[16], uint32_t (&c)[4]) {
-    uint32_t m = w[0];
-#pragma unroll
-    for (int i = 1; i < 16; ++i) m = amax_pair(m, w[i]);
-    const uint32_t s = e8m0_of<2>(max(m & 0x7FFFu, (m >> 16) & 0x7FFFu) << 16);
-    const uint32_t f = (254u - s) << 7;  // 2^(127 - s) as a bf16: s <= 252 for a finite amax
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        float v[8];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float2 r = scale_pair(w[4 * i + j], f);
-            v[2 * j] = r.x;
-            v[2 * j + 1] = r.y;
-        }
-        c[i] = cvt_e2m1x8(v);
-    }
-    if (s == 0xFFu) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float v[8] = {bf16lo(w[4 * i]), bf16hi(w[4 * i]), bf16lo(w[4 * i + 1]), bf16hi(w[4 * i + 1]),
-                                bf16lo(w[4 * i + 2]), bf16hi(w[4 * i + 2]), bf16lo(w[4 * i + 3]), bf16hi(w[4 * i + 3])};
-            c[i] = nonfinite_e2m1x8(v);
-        }
-    }
-    return s;
 }
 
 // fp32 pairs, two lanes of one instruction.
@@ -228,17 +179,10 @@ __global__ void __launch_bounds__(kQ4Threads, KIND == kQ4Swiglu ? 6 : 5) mxfp4_q
             const int r = r0 + i;
             const bool in = cin && r < t.rows;
             uint32_t w[EPT / 2], g[KIND == kQ4Swiglu ? EPT / 2 : 1], codes[EPT / 8], s;
-            int64_t from = at;
-            bool has = in;
-            if constexpr (KIND == kQ4Gather) {
-                const int32_t slot = in ? __ldg(p.slot + t.row0 + r) : -1;
-                has = slot >= 0 && slot < p.slots;
-                from = (int64_t)((uint32_t)slot / (uint32_t)p.top_k) * C + c;
-            }
 #pragma unroll
             for (int j = 0; j < EPT / 8; ++j) {
                 uint4 u = make_uint4(0, 0, 0, 0);
-                if (has) u = *reinterpret_cast<const uint4*>(p.x + from * 2 + 16 * j);
+                if (in) u = *reinterpret_cast<const uint4*>(p.x + at * 2 + 16 * j);
                 w[4 * j] = u.x; w[4 * j + 1] = u.y; w[4 * j + 2] = u.z; w[4 * j + 3] = u.w;
                 if constexpr (KIND == kQ4Swiglu) {
                     if (in) u = *reinterpret_cast<const uint4*>(p.x2 + at * 2 + 16 * j);
@@ -337,14 +281,13 @@ static mxfp8_status_t q4_run(int kind, Q4Params& p, int32_t batch, int scale_lay
     const int64_t gy = (tc + p.cols_per_cta - 1) / p.cols_per_cta;
     if (gx > INT32_MAX || gy > 65535) return MXFP8_ERR_SHAPE;
     // few tiles: their row steps (a load's latency each) go to CTAs of their own
-    const int steps = kind == kQ4Plain || kind == kQ4Gather ? 4 : kind == kQ4Swiglu ? 8 : 2;
+    const int steps = kind == kQ4Plain ? 4 : kind == kQ4Swiglu ? 8 : 2;
     int split = 1;
     while (split < steps && gx * gy * split * 2 <= 4 * (int64_t)host::num_sms()) split *= 2;
     p.row_steps = steps / split;
     const dim3 grid((unsigned)gx, (unsigned)gy, (unsigned)split);
     if (kind == kQ4Plain) mxfp4_quantize_kernel<kQ4Plain><<<grid, kQ4Threads, 0, st>>>(p);
     else if (kind == kQ4Swiglu) mxfp4_quantize_kernel<kQ4Swiglu><<<grid, kQ4Threads, 0, st>>>(p);
-    else if (kind == kQ4Gather) mxfp4_quantize_kernel<kQ4Gather><<<grid, kQ4Threads, 0, st>>>(p);
     else mxfp4_dequantize_kernel<<<grid, kQ4Threads, 0, st>>>(p);
     return host::last_launch_status();
 }
@@ -379,26 +322,6 @@ extern "C" mxfp8_status_t mxfp4_swiglu_quantize(const void* h1_bf16, const void*
     p.offs = offs;
     p.G = G;
     return q4_run(kQ4Swiglu, p, 1, scale_layout, reinterpret_cast<cudaStream_t>(stream));
-}
-
-extern "C" mxfp8_status_t mxfp4_gather_quantize(const void* x_bf16, const int32_t* slot, int64_t rows, int64_t T,
-                                                int32_t top_k, int64_t D, const int32_t* offs, int32_t G, void* q, void* s,
-                                                mxfp8_stream_t stream) {
-    if (T < 0 || top_k < 1 || top_k > MX_MAX_TOP_K || T * top_k > INT32_MAX) return MXFP8_ERR_SHAPE;
-    if (rows > 0 && (!slot || !offs)) return MXFP8_ERR_NULL;
-    if (reinterpret_cast<uintptr_t>(slot) & 3u) return MXFP8_ERR_ALIGN;
-    Q4Params p{};
-    p.x = static_cast<const uint8_t*>(x_bf16);
-    p.q = static_cast<uint8_t*>(q);
-    p.s = static_cast<uint8_t*>(s);
-    p.R = rows;
-    p.C = D;
-    p.offs = offs;
-    p.G = G;
-    p.slot = slot;
-    p.top_k = top_k;
-    p.slots = (int32_t)(T * top_k);
-    return q4_run(kQ4Gather, p, 1, MXFP8_SCALES_BLOCKED, reinterpret_cast<cudaStream_t>(stream));
 }
 
 extern "C" mxfp8_status_t mxfp4_quantize_3d_experts(const void* w_bf16, int32_t G, int64_t N, int64_t K,

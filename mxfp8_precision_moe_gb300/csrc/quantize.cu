@@ -27,6 +27,7 @@
 #include <type_traits>
 
 #include "common.cuh"
+#include "groups.cuh"
 #include "host_common.h"
 #include "mx4.cuh"
 #include "../../include/mxrouting.h"
@@ -76,61 +77,6 @@ struct QParams {
 // row-wise copy beside MXFP8 ones for the column-wise copy; rows gathered through a plan.
 enum QuantMode : int { kModePlain = 0, kModeExt = 1, kModeSwiBwd = 2, kModeSR = 3, kModeExtSR = 4, kModeRow4 = 5,
                        kModeGather = 6 };
-
-// Warp 0 builds, for G groups over R rows, the clamped monotone end rows and
-// the padded start rows P[g] = sum_{h<g} ceil(size_h/128)*128 (also the scale
-// column base of a column-grouped layout, in units of 32 rows: P[g]/32).
-// Returns the padded total through *total.
-__device__ void build_group_table(const int32_t* offs, int G, int64_t R, int32_t* ends_s, int32_t* pstart_s,
-                                  int32_t* total) {
-    const int lane = threadIdx.x & 31;
-    const int per = (G + 31) / 32;
-    const int g0 = lane * per, g1 = min(G, g0 + per);
-    const int32_t Rc = (int32_t)R;
-    // pass 1: running max of clamped offsets (makes them monotone)
-    int32_t mx = 0;
-    for (int g = g0; g < g1; ++g) mx = max(mx, min(max(offs[g], 0), Rc));
-    int32_t incl = mx;
-    for (int d = 1; d < 32; d <<= 1) {
-        int32_t o = __shfl_up_sync(0xffffffffu, incl, d);
-        if (lane >= d) incl = max(incl, o);
-    }
-    int32_t run = __shfl_up_sync(0xffffffffu, incl, 1);
-    if (lane == 0) run = 0;
-    // pass 2: ends, padded sizes, exclusive scan of padded sizes
-    int32_t prev = run, psum = 0;
-    for (int g = g0; g < g1; ++g) {
-        int32_t e = max(prev, min(max(offs[g], 0), Rc));
-        ends_s[g] = e;
-        psum += ((e - prev + 127) / 128) * 128;
-        prev = e;
-    }
-    int32_t sincl = psum;
-    for (int d = 1; d < 32; d <<= 1) {
-        int32_t o = __shfl_up_sync(0xffffffffu, sincl, d);
-        if (lane >= d) sincl += o;
-    }
-    int32_t sexcl = sincl - psum;
-    prev = run;
-    for (int g = g0; g < g1; ++g) {
-        pstart_s[g] = sexcl;
-        int32_t e = ends_s[g];
-        sexcl += ((e - prev + 127) / 128) * 128;
-        prev = e;
-    }
-    if (lane == 31) *total = sincl;
-}
-
-// Group of row r (ends_s monotone): first g with r < ends_s[g]; G if none.
-__device__ __forceinline__ int find_group(const int32_t* ends_s, int G, int64_t r) {
-    int lo = 0, hi = G;
-    while (lo < hi) {
-        int mid = (lo + hi) >> 1;
-        if (r < ends_s[mid]) hi = mid;
-        else lo = mid + 1;
-    }
-    return lo;
-}
 
 // ---- stability variants ("MXFP8 (Micro-scaling FP8)", "Numerical stability": random Hadamard
 // transforms before quantization, stochastic rounding)
@@ -1346,6 +1292,11 @@ static mxfp8_status_t launch_swiglu_bwd(const QParams& p, cudaStream_t st) {
 }
 
 // Rows through a plan.  The tensor map is unused.
+// The row-wise copy alone, without weights, goes by token (gather_quantize.cu).
+mxfp8_status_t gather_quantize_rows(int bits, const void* x, const int32_t* slot, const int32_t* place, int64_t rows,
+                                    int64_t T, int32_t top_k, int64_t D, const int32_t* offs, int32_t G, void* q, void* s,
+                                    cudaStream_t st);
+
 static mxfp8_status_t gather_quantize(QParams& p, unsigned dirs, cudaStream_t st) {
     const CUtensorMap m{};
     const int64_t grid = std::min<int64_t>(p.units, (int64_t)host::num_sms() * 2);
@@ -1368,9 +1319,9 @@ struct DqParams {
     uint32_t tiles_r, tiles_c;
 };
 
-// A warp takes 16 rows of a 128 x 128 tile, four at a time, a lane 16 neighbouring values (half a block): one 16-byte
-// load, one scale byte, two 16-byte stores.  In the column-wise copy the groups run along C, so that a lane's place in the
-// scales is found once a tile.
+// A warp takes 16 rows of a 128 x 128 tile, two at a time, a lane 8 neighbouring values (a quarter of a block): stores of
+// whole sectors by neighbouring lanes (with 16 values a lane, two 16-byte stores 32 bytes apart, 57 us for 16384 x 5120
+// instead of 47).  Bound by memory: 1.03 bytes read and 2 written an element.
 template <bool kCol>
 __global__ void __launch_bounds__(256) mxfp8_dequantize_kernel(const DqParams p) {
     __shared__ int32_t ends_s[kMaxGroups];
@@ -1384,53 +1335,68 @@ __global__ void __launch_bounds__(256) mxfp8_dequantize_kernel(const DqParams p)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // the place of index m of the grouped axis in the padded layout, -1: in no group
     auto padded = [&](int64_t m) -> int64_t {
-        if (!grouped) return m;
+        if (!grouped) return m < M ? m : -1;
         const int g = find_group(ends_s, p.G, m);
         return g < p.G ? pstart_s[g] + (m - (g ? ends_s[g - 1] : 0)) : -1;
     };
     for (uint32_t t = blockIdx.x; t < p.tiles_r * p.tiles_c; t += gridDim.x) {
         const uint32_t tr = t / p.tiles_c, tc = t - tr * p.tiles_c;
-        const int64_t c = (int64_t)tc * 128 + (lane & 7) * 16;
-        if (c >= C) continue;
-        int64_t cb = c / kBlk;  // block-column in the scales
+        const int64_t c = (int64_t)tc * 128 + (lane & 15) * 8;
+        const int64_t r0 = (int64_t)tr * 128 + warp * 16;
+        uint2 codes[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int64_t r = r0 + 2 * i + (lane >> 4);
+            codes[i] = make_uint2(0, 0);
+            if (r < R && c < C) codes[i] = __ldg(reinterpret_cast<const uint2*>(p.q + r * C + c));
+        }
+        // the scales of this lane's values, a byte a row; of a place in no group 0, with its values
+        uint32_t scale[8];
         bool none = false;
-        if (kCol && p.blocked) {
-            const int64_t m = padded(c);
-            none = m < 0;
-            cb = m / kBlk;
-        }
-        uint4 codes[4];
+        if (!p.blocked) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t r = (int64_t)tr * 128 + warp * 16 + 4 * i + (lane >> 3);
-            codes[i] = make_uint4(0, 0, 0, 0);
-            if (r < R) codes[i] = __ldg(reinterpret_cast<const uint4*>(p.q + r * C + c));
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t r = (int64_t)tr * 128 + warp * 16 + 4 * i + (lane >> 3);
-            if (r >= R) continue;
-            const int64_t pr = !kCol && p.blocked ? padded(r) : r;
-            uint4 o[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-            if (!none && pr >= 0) {
-                const float f = e8m0_value(p.s[p.blocked ? blocked_off(pr, cb, ct) : r * (C / kBlk) + cb]);
-                const uint32_t w[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
-                uint32_t h[8];
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    float lo, hi;  // every E4M3 value is a half
-                    asm("{\n\t.reg .b32 v;\n\t.reg .f16 a, b;\n\tcvt.rn.f16x2.e4m3x2 v, %2;\n\tmov.b32 {a, b}, v;\n\t"
-                        "cvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
-                        : "=f"(lo), "=f"(hi)
-                        : "h"((uint16_t)(w[k >> 1] >> (16 * (k & 1)))));
-                    h[k] = pack_bf16x2(lo * f, hi * f);
-                }
-                o[0] = make_uint4(h[0], h[1], h[2], h[3]);
-                o[1] = make_uint4(h[4], h[5], h[6], h[7]);
+            for (int i = 0; i < 8; ++i) {
+                const int64_t r = r0 + 2 * i + (lane >> 4);
+                scale[i] = r < R && c < C ? __ldg(p.s + r * (C / kBlk) + c / kBlk) : 0u;
             }
-            uint4* out = reinterpret_cast<uint4*>(p.out + r * C + c);
-            out[0] = o[0];
-            out[1] = o[1];
+        } else if constexpr (kCol) {
+            const int64_t m = c < C ? padded(c) : -1;
+            none = m < 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int64_t r = r0 + 2 * i + (lane >> 4);
+                scale[i] = r < R && !none ? __ldg(p.s + blocked_off(r, m / kBlk, ct)) : 0u;
+            }
+        } else {
+            // lane i < 16 fetches the four scales of row i in this tile, one word
+            const int64_t pr = lane < 16 && r0 + lane < R ? padded(r0 + lane) : -1;
+            const uint32_t word = pr >= 0 ? __ldg(reinterpret_cast<const uint32_t*>(p.s + blocked_off(pr, (int64_t)tc * 4, ct))) : 0u;
+            const uint32_t dead = __ballot_sync(0xffffffffu, pr < 0);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int from = 2 * i + (lane >> 4);
+                scale[i] = (__shfl_sync(0xffffffffu, word, from) >> (8 * ((lane >> 2) & 3))) & 0xFFu;
+                if (dead >> from & 1u) codes[i] = make_uint2(0, 0);
+            }
+        }
+        if (c >= C) continue;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int64_t r = r0 + 2 * i + (lane >> 4);
+            if (r >= R) continue;
+            const float f = e8m0_value(scale[i]);
+            uint32_t h[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                float lo, hi;  // every E4M3 value is a half
+                asm("{\n\t.reg .b32 v;\n\t.reg .f16 a, b;\n\tcvt.rn.f16x2.e4m3x2 v, %2;\n\tmov.b32 {a, b}, v;\n\t"
+                    "cvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
+                    : "=f"(lo), "=f"(hi)
+                    : "h"((uint16_t)((k < 2 ? codes[i].x : codes[i].y) >> (16 * (k & 1)))));
+                h[k] = pack_bf16x2(lo * f, hi * f);
+            }
+            *reinterpret_cast<uint4*>(p.out + r * C + c) =
+                none ? make_uint4(0, 0, 0, 0) : make_uint4(h[0], h[1], h[2], h[3]);
         }
     }
 }
@@ -1584,8 +1550,8 @@ extern "C" mxfp8_status_t mxfp4_quantize_3d_experts_mxfp8_cols(const void* w_bf1
     return mx::quantize_row4(p, w_bf16, N, K, G, q, s, qT, sT, dev_status, reinterpret_cast<cudaStream_t>(stream));
 }
 
-extern "C" mxfp8_status_t mxfp8_gather_quantize(const void* x_bf16, const int32_t* slot, const float* w, int64_t rows,
-                                                int64_t T, int32_t top_k, int64_t D, unsigned dirs, const int32_t* offs,
+extern "C" mxfp8_status_t mxfp8_gather_quantize(const void* x_bf16, const int32_t* slot, const int32_t* place,
+                                                const float* w, int64_t rows, int64_t T, int32_t top_k, int64_t D, unsigned dirs, const int32_t* offs,
                                                 int32_t G, void* q_row, void* s_row, void* q_col, void* s_col,
                                                 int32_t* dev_status, mxfp8_stream_t stream) {
     if (rows < 0 || rows > INT32_MAX || D <= 0 || D > INT32_MAX || T < 0 || top_k < 1 || top_k > MX_MAX_TOP_K ||
@@ -1595,12 +1561,14 @@ extern "C" mxfp8_status_t mxfp8_gather_quantize(const void* x_bf16, const int32_
     if (dirs == 0 || (dirs & ~(unsigned)(MXFP8_ROW | MXFP8_COL))) return MXFP8_ERR_LAYOUT;
     if (D % 32 || (col && rows % 32)) return MXFP8_ERR_ALIGN;
     if (rows == 0) return MXFP8_OK;  // an empty tensor may have no address
-    if ((T && !x_bf16) || !slot || !offs || (row && (!q_row || !s_row)) || (col && (!q_col || !s_col))) return MXFP8_ERR_NULL;
+    if ((T && (!x_bf16 || !place)) || !slot || !offs || (row && (!q_row || !s_row)) || (col && (!q_col || !s_col))) return MXFP8_ERR_NULL;
     for (const void* v : {x_bf16, (const void*)q_row, (const void*)s_row, (const void*)q_col, (const void*)s_col})
         if (!host::aligned16(v)) return MXFP8_ERR_ALIGN;
-    for (const void* v : {(const void*)slot, (const void*)w, (const void*)offs})
+    for (const void* v : {(const void*)slot, (const void*)place, (const void*)w, (const void*)offs})
         if (reinterpret_cast<uintptr_t>(v) & 3u) return MXFP8_ERR_ALIGN;
     if (mxfp8_status_t a = host::check_arch(); a != MXFP8_OK) return a;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (!col && !w) return gather_quantize_rows(8, x_bf16, slot, place, rows, T, top_k, D, offs, G, q_row, s_row, st);
     QParams p{};
     p.x = static_cast<const uint16_t*>(T ? x_bf16 : row ? q_row : q_col);  // of no tokens: an address, never read
     p.R = rows; p.C = D; p.batch = 1;
@@ -1621,7 +1589,7 @@ extern "C" mxfp8_status_t mxfp8_gather_quantize(const void* x_bf16, const int32_
     p.units = p.tiles_r * segs;
     // x's share of a strip: 32 MB, a quarter of L2, where a token has several rows
     p.strip = (uint32_t)(top_k == 1 ? segs : std::max<int64_t>(1, std::min(segs, (int64_t)(32 << 20) / (max64(T, 1) * 256 * p.seg))));
-    return mx::gather_quantize(p, dirs, reinterpret_cast<cudaStream_t>(stream));
+    return mx::gather_quantize(p, dirs, st);
 }
 
 extern "C" mxfp8_status_t mxfp8_dequantize(const void* q, const void* s, int64_t M, int64_t K, unsigned dir,

@@ -358,8 +358,8 @@ def mxfp8_gather_quantize(x: torch.Tensor, plan: MoePlan, dirs: int = ROW, weigh
     if dirs & COL:
         q_col, s_col = _u8((D, M), dev), _u8(mxfp8_scale_bytes_colgroups(D, M, G), dev)
     at = [None if t is None else t.data_ptr() for t in (weights, q_row, s_row, q_col, s_col, dev_status)]
-    check(load().mxfp8_gather_quantize(x.data_ptr(), plan.slot.data_ptr(), at[0], M, T, plan.top_k, D, dirs,
-                                       plan.offs.data_ptr(), G, *at[1:], _raw_stream(dev.index)), "mxfp8_gather_quantize")
+    check(load().mxfp8_gather_quantize(x.data_ptr(), plan.slot.data_ptr(), plan.place.data_ptr(), at[0], M, T, plan.top_k, D,
+                                       dirs, plan.offs.data_ptr(), G, *at[1:], _raw_stream(dev.index)), "mxfp8_gather_quantize")
     return q_row, s_row, q_col, s_col
 
 
@@ -370,8 +370,8 @@ def mxfp4_gather_quantize(x: torch.Tensor, plan: MoePlan):
     _cuda(x, plan.offs)
     (T, D), M, G, dev = x.shape, plan.rows, plan.offs.shape[0], x.device
     q, s = _u8((M, D // 2), dev), _u8(_group_bytes(M, D, G), dev)
-    check(load().mxfp4_gather_quantize(x.data_ptr(), plan.slot.data_ptr(), M, T, plan.top_k, D, plan.offs.data_ptr(), G,
-                                       q.data_ptr(), s.data_ptr(), _raw_stream(dev.index)), "mxfp4_gather_quantize")
+    check(load().mxfp4_gather_quantize(x.data_ptr(), plan.slot.data_ptr(), plan.place.data_ptr(), M, T, plan.top_k, D,
+                                       plan.offs.data_ptr(), G, q.data_ptr(), s.data_ptr(), _raw_stream(dev.index)), "mxfp4_gather_quantize")
     return q, s
 
 

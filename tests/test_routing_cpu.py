@@ -256,15 +256,15 @@ def test_refusals_of_the_c_abi():
         L.mx_moe_combine_bwd(dout, y, slot, place, w, rows, T, k, D, dy, dw, None))
     assert b(D=4) == 3 and b(k=17) == 2 and b(dout=None) == 1 and b(y=None) == 1 and b(slot=None) == 1 and b(dy=odd) == 3
     assert b(dw=half) == 3 and b(dy=None, dw=None) == 0 and b(T=0, rows=0) == 0
-    q = lambda x=a, slot=a, w=None, rows=64, T=4, k=2, D=64, dirs=3, offs=a, G=2, qr=a, sr=a, qc=a, sc=a: (  # noqa: E731
-        L.mxfp8_gather_quantize(x, slot, w, rows, T, k, D, dirs, offs, G, qr, sr, qc, sc, None, None))
+    q = lambda x=a, slot=a, place=a, w=None, rows=64, T=4, k=2, D=64, dirs=3, offs=a, G=2, qr=a, sr=a, qc=a, sc=a: (  # noqa: E731
+        L.mxfp8_gather_quantize(x, slot, place, w, rows, T, k, D, dirs, offs, G, qr, sr, qc, sc, None, None))
     assert q(rows=-1) == 2 and q(D=0) == 2 and q(G=0) == 2 and q(G=1025) == 2 and q(T=1 << 31) == 2 and q(dirs=0) == 4
     assert q(dirs=4) == 4 and q(dirs=5) == 4 and q(D=48) == 3 and q(rows=40) == 3 and q(x=None) == 1 and q(offs=None) == 1
-    assert q(qc=None) == 1 and q(sr=odd) == 3 and q(w=half) == 3 and q(rows=0, qr=None) == 0
-    f = lambda x=a, slot=a, rows=64, T=4, k=2, D=64, offs=a, G=2, q=a, s=a: (  # noqa: E731
-        L.mxfp4_gather_quantize(x, slot, rows, T, k, D, offs, G, q, s, None))
+    assert q(place=None) == 1 and q(place=half) == 3 and q(qc=None) == 1 and q(sr=odd) == 3 and q(w=half) == 3 and q(rows=0, qr=None) == 0
+    f = lambda x=a, slot=a, place=a, rows=64, T=4, k=2, D=64, offs=a, G=2, q=a, s=a: (  # noqa: E731
+        L.mxfp4_gather_quantize(x, slot, place, rows, T, k, D, offs, G, q, s, None))
     assert f(T=-1) == 2 and f(k=17) == 2 and f(slot=None) == 1 and f(offs=None) == 1 and f(D=48) == 3 and f(G=0) == 2
-    assert f(q=None) == 1 and f(x=odd) == 3 and f(slot=half) == 3 and f(rows=0, q=None) == 0
+    assert f(place=None) == 1 and f(q=None) == 1 and f(x=odd) == 3 and f(slot=half) == 3 and f(rows=0, q=None) == 0
     d = lambda q=a, s=a, M=64, K=64, dir=1, layout=1, offs=None, G=0, out=a: (  # noqa: E731
         L.mxfp8_dequantize(q, s, M, K, dir, layout, offs, G, out, None))
     assert d(M=-1) == 2 and d(K=0) == 2 and d(offs=a) == 2 and d(dir=3) == 4 and d(layout=2) == 4 and d(K=48) == 3
