@@ -525,13 +525,22 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_bwd_kernel(const Route
 }
 
 // ---------------------------------------------------------------- the plan
-// A stable counting sort by expert.  A CTA takes a run of kPlanChunk choices, a warp a run of 32 * kPlanSteps of
-// them in turn: a choice's rank among its warp's is the count so far plus the lanes before it with the same expert (a
+// A stable counting sort by expert.  A CTA takes a run of choices, a warp a part of it, 32 choices a step,
+// in turn: a choice's rank among its warp's is the count so far plus the lanes before it with the same expert (a
 // warp-wide match), so no atomics and no order that could vary.  With several CTAs a first kernel counts each run.
+// Bound by latency: 262144 choices of 256 experts take 12.3 us, of which the counts of 128 runs, which every CTA sums, 4.7,
+// and the scattered slots 2 (CTAs of 1024 threads 13.4, longer runs 18, the second kernel launched while the first runs 13.1).
 constexpr int kPlanThreads = 512;
 constexpr int kPlanWarps = kPlanThreads / 32;
-constexpr int kPlanSteps = 8;
-constexpr int kPlanChunk = kPlanThreads * kPlanSteps;
+// Steps of a run: few, so that many CTAs share the work; many where the counts of very many runs, which every CTA reads,
+// would cost more.
+constexpr int kPlanShort = 4, kPlanLong = 16;
+constexpr int64_t kPlanLongFrom = 1 << 20;
+static int plan_steps(int64_t choices) { return choices < kPlanLongFrom ? kPlanShort : kPlanLong; }
+static int64_t plan_runs(int64_t choices) {
+    const int64_t run = (int64_t)kPlanThreads * plan_steps(choices);
+    return max64(1, (choices + run - 1) / run);
+}
 
 struct PlanParams {
     const void* experts;
@@ -549,23 +558,23 @@ __device__ __forceinline__ int expert_of(const PlanParams& p, int64_t i) {  // -
     return e >= 0 && e < (I)p.E ? (int)e : -1;
 }
 
-template <typename I>
+template <typename I, int STEPS>
 __global__ void __launch_bounds__(kPlanThreads) plan_count_kernel(const PlanParams p) {
     __shared__ int32_t count[kMaxGroups];
     for (int e = threadIdx.x; e < p.E; e += kPlanThreads) count[e] = 0;
     __syncthreads();
-    const int64_t base = (int64_t)blockIdx.x * kPlanChunk;
-    int ex[kPlanSteps];
+    const int64_t base = (int64_t)blockIdx.x * (kPlanThreads * STEPS);
+    int ex[STEPS];
 #pragma unroll
-    for (int s = 0; s < kPlanSteps; ++s) ex[s] = expert_of<I>(p, base + s * kPlanThreads + threadIdx.x);
+    for (int s = 0; s < STEPS; ++s) ex[s] = expert_of<I>(p, base + s * kPlanThreads + threadIdx.x);
 #pragma unroll
-    for (int s = 0; s < kPlanSteps; ++s)
+    for (int s = 0; s < STEPS; ++s)
         if (ex[s] >= 0) atomicAdd(&count[ex[s]], 1);
     __syncthreads();
     for (int e = threadIdx.x; e < p.E; e += kPlanThreads) p.hist[(int64_t)blockIdx.x * p.E + e] = count[e];
 }
 
-template <typename I>
+template <typename I, int STEPS>
 __global__ void __launch_bounds__(kPlanThreads) plan_place_kernel(const PlanParams p) {
     extern __shared__ int32_t plan_smem[];
     int32_t* table = plan_smem;                  // [kPlanWarps][E]: counts, then first rows
@@ -574,29 +583,16 @@ __global__ void __launch_bounds__(kPlanThreads) plan_place_kernel(const PlanPara
     int32_t* start = total + p.E;                // [E]: first row of the group
     __shared__ int32_t warp_part[kPlanWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t base = (int64_t)blockIdx.x * kPlanChunk + warp * 32 * kPlanSteps + lane;
-    int ex[kPlanSteps], rank[kPlanSteps];
+    const int64_t base = (int64_t)blockIdx.x * (kPlanThreads * STEPS) + warp * 32 * STEPS + lane;
+    int ex[STEPS], rank[STEPS];
 #pragma unroll
-    for (int s = 0; s < kPlanSteps; ++s) ex[s] = expert_of<I>(p, base + s * 32);
+    for (int s = 0; s < STEPS; ++s) ex[s] = expert_of<I>(p, base + s * 32);
     for (int i = threadIdx.x; i < kPlanWarps * p.E; i += kPlanThreads) table[i] = 0;
-    // counts of the other runs, summed in two halves: those before this one, and the rest
-    for (int e = threadIdx.x; e < p.E; e += kPlanThreads) {
-        int32_t lo = 0, hi = 0;
-        if (p.runs > 1) {
-#pragma unroll 8
-            for (int r = 0; r < p.runs; ++r) {
-                const int32_t c = p.hist[(int64_t)r * p.E + e];
-                if (r < (int)blockIdx.x) lo += c;
-                else hi += c;
-            }
-        }
-        before[e] = lo;
-        total[e] = lo + hi;
-    }
+    for (int e = threadIdx.x; e < p.E; e += kPlanThreads) before[e] = total[e] = 0;
     __syncthreads();
     int32_t* mine = table + warp * p.E;
 #pragma unroll
-    for (int s = 0; s < kPlanSteps; ++s) {
+    for (int s = 0; s < STEPS; ++s) {
         const uint32_t same = __match_any_sync(kFull, ex[s]);
         const int ahead = __popc(same & ((1u << lane) - 1u));
         if (ex[s] >= 0) rank[s] = mine[ex[s]] + ahead;
@@ -612,8 +608,22 @@ __global__ void __launch_bounds__(kPlanThreads) plan_place_kernel(const PlanPara
             for (int w = 0; w < kPlanWarps; ++w) c += table[w * p.E + e];
             total[e] = c;
         }
-        __syncthreads();
+    } else {
+        // the counts of all runs, and of those before this one: several threads an expert where there are enough
+        const int parts = max(1, kPlanThreads / p.E), part = threadIdx.x / p.E;
+        for (int e = parts > 1 ? threadIdx.x - part * p.E : threadIdx.x; e < p.E && part < parts; e += kPlanThreads) {
+            int32_t lo = 0, all = 0;
+#pragma unroll 16
+            for (int r = parts > 1 ? part : 0; r < p.runs; r += parts) {
+                const int32_t c = __ldcg(p.hist + (int64_t)r * p.E + e);
+                all += c;
+                if (r < (int)blockIdx.x) lo += c;
+            }
+            atomicAdd(before + e, lo);  // integers: any order
+            atomicAdd(total + e, all);
+        }
     }
+    __syncthreads();
     // the groups' first rows: a scan of the padded sizes, kMaxGroups / kPlanThreads neighbours a thread
     constexpr int kPer = kMaxGroups / kPlanThreads;
     int32_t size[kPer], sum = 0;
@@ -662,7 +672,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_place_kernel(const PlanPara
     }
     __syncthreads();
 #pragma unroll
-    for (int s = 0; s < kPlanSteps; ++s) {
+    for (int s = 0; s < STEPS; ++s) {
         const int64_t i = base + s * 32;
         if (i >= p.n) continue;
         int32_t row = -1;
@@ -716,16 +726,16 @@ static mxfp8_status_t route_run(RouteParams& p, cudaStream_t st) {
     return route_launch<32>(p, st);
 }
 
-template <typename I>
+template <typename I, int STEPS>
 static mxfp8_status_t plan_run(const PlanParams& p, cudaStream_t st) {
     if (p.runs > 1) {
-        plan_count_kernel<I><<<p.runs, kPlanThreads, 0, st>>>(p);
+        plan_count_kernel<I, STEPS><<<p.runs, kPlanThreads, 0, st>>>(p);
         if (mxfp8_status_t s = host::last_launch_status(); s != MXFP8_OK) return s;
     }
     static std::atomic<int> attr_set[host::kMaxDevices];
     constexpr int most = (kPlanWarps + 3) * MXFP8_MAX_GROUPS * 4;
-    if (!host::ensure_smem(reinterpret_cast<const void*>(plan_place_kernel<I>), most, attr_set)) return MXFP8_ERR_LAUNCH;
-    plan_place_kernel<I><<<p.runs, kPlanThreads, (kPlanWarps + 3) * p.E * 4, st>>>(p);
+    if (!host::ensure_smem(reinterpret_cast<const void*>(plan_place_kernel<I, STEPS>), most, attr_set)) return MXFP8_ERR_LAUNCH;
+    plan_place_kernel<I, STEPS><<<p.runs, kPlanThreads, (kPlanWarps + 3) * p.E * 4, st>>>(p);
     return host::last_launch_status();
 }
 
@@ -809,7 +819,7 @@ extern "C" int64_t mx_moe_plan_rows(int64_t T, int32_t top_k, int32_t E, int32_t
 
 extern "C" size_t mx_moe_plan_workspace(int64_t T, int32_t top_k, int32_t E) {
     if (!plan_sizes(T, top_k, E, 1)) return 0;
-    const int64_t runs = (T * top_k + kPlanChunk - 1) / kPlanChunk;
+    const int64_t runs = plan_runs(T * top_k);
     return runs > 1 ? (size_t)(runs * E * 4) : 0;
 }
 
@@ -831,7 +841,7 @@ extern "C" mxfp8_status_t mx_moe_plan(const void* experts, int32_t index_bytes, 
     p.n = T * top_k;
     p.E = E;
     p.multiple = multiple;
-    p.runs = (int32_t)max64(1, (p.n + kPlanChunk - 1) / kPlanChunk);
+    p.runs = (int32_t)plan_runs(p.n);
     p.rows = rows;
     p.offs = offs;
     p.counts = counts;
@@ -839,5 +849,7 @@ extern "C" mxfp8_status_t mx_moe_plan(const void* experts, int32_t index_bytes, 
     p.place = place;
     p.hist = static_cast<int32_t*>(workspace);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    return index_bytes == 4 ? plan_run<int32_t>(p, st) : plan_run<int64_t>(p, st);
+    if (plan_steps(p.n) == kPlanShort)
+        return index_bytes == 4 ? plan_run<int32_t, kPlanShort>(p, st) : plan_run<int64_t, kPlanShort>(p, st);
+    return index_bytes == 4 ? plan_run<int32_t, kPlanLong>(p, st) : plan_run<int64_t, kPlanLong>(p, st);
 }

@@ -217,17 +217,13 @@ def moe_plan(experts: torch.Tensor, num_experts: int, multiple: int = 1, *, exac
     dev = experts.device
     L = load()
     nbytes = L.mx_moe_plan_workspace(T, k, E)
-    # one allocation for the plan's arrays and the workspace, each on a 16-byte boundary
-    counts_at = (E + 3) // 4 * 4
-    slot_at = 2 * counts_at
-    place_at = slot_at + (rows + 3) // 4 * 4
-    ws_at = place_at + (n + 3) // 4 * 4
-    buf = torch.empty(ws_at + nbytes // 4, dtype=torch.int32, device=dev)
-    at = buf.data_ptr()
-    check(L.mx_moe_plan(experts.data_ptr(), experts.element_size(), T, k, E, multiple, rows, at, at + 4 * counts_at,
-                        at + 4 * slot_at, at + 4 * place_at, at + 4 * ws_at, nbytes, _raw_stream(dev.index)), "mx_moe_plan")
-    offs, counts = buf.as_strided((E,), (1,), 0), buf.as_strided((E,), (1,), counts_at)
-    slot, place = buf.as_strided((rows,), (1,), slot_at), buf.as_strided((T, k), (k, 1), place_at)
+    # (tensors of their own: views of one allocation take the host longer than allocations do)
+    offs, counts = (torch.empty(E, dtype=torch.int32, device=dev) for _ in range(2))
+    slot, place = torch.empty(rows, dtype=torch.int32, device=dev), torch.empty((T, k), dtype=torch.int32, device=dev)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+    check(L.mx_moe_plan(experts.data_ptr(), experts.element_size(), T, k, E, multiple, rows, offs.data_ptr(),
+                        counts.data_ptr(), slot.data_ptr(), place.data_ptr(), None if ws is None else ws.data_ptr(), nbytes,
+                        _raw_stream(dev.index)), "mx_moe_plan")
     if exact:
         slot = slot[:int(offs[-1])]
     return MoePlan._of(offs, counts, slot, place, multiple)

@@ -265,6 +265,23 @@ def test_plan_of_one_group_or_none(fill, T):
     check_plan(torch.full((T, 2), fill, device="cuda", dtype=torch.int32), 6, 32)
 
 
+def test_plan_of_many_tokens():
+    """More choices than a short run's kernels take, against torch's stable sort."""
+    T, k, E, multiple = 70000, 16, 300, 32
+    e = torch.randint(-1, E, (T, k), device="cuda", generator=torch.Generator(device="cuda").manual_seed(1))
+    p = mx.moe_plan(e, E, multiple)
+    flat = e.flatten()
+    counts = torch.bincount(flat[flat >= 0], minlength=E)
+    padded = (counts + multiple - 1) // multiple * multiple
+    ends = padded.cumsum(0)
+    assert torch.equal(p.counts.long(), counts) and torch.equal(p.offs.long(), ends)
+    order = torch.where(flat >= 0, flat, E).sort(stable=True)[1][:int(counts.sum())]
+    row = (ends - padded)[flat[order]] + torch.arange(order.numel(), device="cuda") - (counts.cumsum(0) - counts)[flat[order]]
+    slot = torch.full((p.rows,), -1, device="cuda").scatter(0, row, order)
+    assert torch.equal(p.slot.long(), slot)
+    assert torch.equal(p.place.flatten().long(), torch.full_like(flat, -1).scatter(0, order, row))
+
+
 def test_plan_of_values_past_32_bits():
     e = torch.tensor([[2 ** 32, 1], [-2 ** 33 + 1, 2 ** 40 + 2]], device="cuda")
     check_plan(e, 4, 1)
