@@ -2,10 +2,11 @@
 
     python examples/mxfp4_layer.py
 
-1. One fine-tuning step: the three products of the layer are differentiable MXFP4 products (forward in 4 bits,
-   gradients in 8), over tokens grouped by expert.
+1. One fine-tuning step: tokens are routed, planned and gathered by expert, and the three products of the layer are
+   differentiable MXFP4 products (forward in 4 bits, gradients in 8).
 2. The weights are quantized once for serving.
-3. A prompt's tokens go through the grouped products, with SwiGLU and the quantization of h in one kernel.
+3. A prompt's tokens are routed the same way, quantized on their way into the plan's order, go through the grouped products,
+   with SwiGLU and the quantization of h in one kernel, and are added up by their weights.
 4. The tokens that follow go through ``MxMoeTokens``, a few at a time, over the same weights.
 
 Random weights and tokens; prints how far the two serving paths are apart and what each takes."""
@@ -22,42 +23,25 @@ import mxfp8_precision_moe_gb300 as mx  # noqa: E402
 
 
 def dispatch(logits: torch.Tensor, top_k: int, multiple: int = 1):
-    """Tokens grouped by expert: for each of M rows the token it takes (-1: padding, to make every group a
-    multiple of ``multiple`` rows) and its weight, and the groups' end rows."""
-    T, E = logits.shape
-    top, experts = logits.topk(top_k, dim=1)
-    weights = top.softmax(1).flatten()
-    experts = experts.flatten()
-    order = experts.argsort(stable=True)
-    counts = torch.bincount(experts, minlength=E)
-    padded = (counts + multiple - 1) // multiple * multiple
-    ends, starts = padded.cumsum(0), counts.cumsum(0) - counts
-    place = torch.arange(T * top_k, device=logits.device) - starts[experts[order]] + (ends - padded)[experts[order]]
-    token = torch.full((int(ends[-1]),), -1, dtype=torch.long, device=logits.device)
-    weight = torch.zeros(token.shape, device=logits.device)
-    token[place] = order // top_k
-    weight[place] = weights[order]
-    return token, weight, ends.to(torch.int32)
-
-
-def gather(x: torch.Tensor, token: torch.Tensor) -> torch.Tensor:
-    return torch.where((token >= 0)[:, None], x[token.clamp_min(0)], 0)
-
-
-def combine(y: torch.Tensor, token: torch.Tensor, weight: torch.Tensor, T: int) -> torch.Tensor:
-    out = torch.zeros((T, y.shape[1]), device=y.device)
-    return out.index_add(0, token.clamp_min(0), y.float() * weight[:, None])
+    """Who goes where, row by row: for each row of the plan its token (-1: padding, to make every group a multiple of
+    ``multiple`` rows) and its weight, and the groups' end rows."""
+    experts, weights = mx.moe_route(logits, top_k)
+    plan = mx.moe_plan(experts, logits.shape[1], multiple, exact=True)
+    some = plan.slot >= 0
+    token = torch.where(some, plan.slot // top_k, -1).long()
+    return token, torch.where(some, weights.flatten()[plan.slot.clamp_min(0).long()], 0.0), plan.offs
 
 
 def train_layer(x, logits, gate, up, down, top_k: int) -> torch.Tensor:
-    """The layer for training: y [T, D], differentiable in x and the weights."""
-    token, weight, offs = dispatch(logits, top_k, multiple=32)
-    rows = gather(x, token)
-    h1 = mx.to_mxfp4_then_scaled_grouped_mm(rows, gate, offs)
-    h3 = mx.to_mxfp4_then_scaled_grouped_mm(rows, up, offs, check_offsets=False)
+    """The layer for training: y [T, D], differentiable in x, the logits and the weights."""
+    experts, weights = mx.moe_route(logits, top_k)
+    plan = mx.moe_plan(experts, gate.shape[0], multiple=32)
+    rows = mx.moe_gather(x, plan)
+    h1 = mx.to_mxfp4_then_scaled_grouped_mm(rows, gate, plan.offs, check_offsets=False)
+    h3 = mx.to_mxfp4_then_scaled_grouped_mm(rows, up, plan.offs, check_offsets=False)
     h = torch.nn.functional.silu(h1.float()) * h3.float()
-    y = mx.to_mxfp4_then_scaled_grouped_mm(h.bfloat16(), down, offs, check_offsets=False)
-    return combine(y, token, weight, x.shape[0])
+    y = mx.to_mxfp4_then_scaled_grouped_mm(h.bfloat16(), down, plan.offs, check_offsets=False)
+    return mx.moe_combine(y, plan, weights)
 
 
 class ServingLayer:
@@ -70,12 +54,13 @@ class ServingLayer:
 
     @torch.no_grad()
     def prompt(self, x: torch.Tensor, logits: torch.Tensor) -> torch.Tensor:
-        token, weight, offs = dispatch(logits, self.top_k)
-        q = mx.mxfp4_quantize_2d(x[token], offs=offs)
-        h1 = mx.mxfp4_grouped_mm_fwd(*q, *self.gate, offs)
-        h3 = mx.mxfp4_grouped_mm_fwd(*q, *self.up, offs)
-        y = mx.mxfp4_grouped_mm_fwd(*mx.mxfp4_swiglu_quantize(h1, h3, offs=offs), *self.down, offs)
-        return combine(y, token, weight, x.shape[0]).bfloat16()
+        experts, weights = mx.moe_route(logits, self.top_k)
+        plan = mx.moe_plan(experts, logits.shape[1])
+        q = mx.mxfp4_gather_quantize(x, plan)
+        h1 = mx.mxfp4_grouped_mm_fwd(*q, *self.gate, plan.offs)
+        h3 = mx.mxfp4_grouped_mm_fwd(*q, *self.up, plan.offs)
+        h = mx.mxfp4_swiglu_quantize(h1, h3, offs=plan.offs)
+        return mx.moe_combine(mx.mxfp4_grouped_mm_fwd(*h, *self.down, plan.offs), plan, weights)
 
     @torch.no_grad()
     def tokens(self, x: torch.Tensor, logits: torch.Tensor) -> torch.Tensor:
@@ -92,7 +77,7 @@ def run(E: int = 8, D: int = 1024, H: int = 2048, top_k: int = 2, prompt: int = 
     gate, up, down = rand(E, H, D, scale=D ** -0.5), rand(E, H, D, scale=D ** -0.5), rand(E, D, H, scale=H ** -0.5)
     x, logits = rand(prompt, D), rand(prompt, E).float()
     leaves = [w.requires_grad_(True) for w in (gate, up, down)]
-    loss = (train_layer(x, logits, *leaves, top_k) - x.float()).square().mean()
+    loss = (train_layer(x, logits, *leaves, top_k).float() - x.float()).square().mean()
     grads = torch.autograd.grad(loss, leaves)
     with torch.no_grad():
         for w, d in zip(leaves, grads):
@@ -113,6 +98,8 @@ def main() -> None:
         return a.elapsed_time(b) * 1e3 / n
 
     grads, many, few, layer, (x, logits) = run()
+    ends = dispatch(logits, layer.top_k)[2].tolist()
+    print("tokens of each expert", [b - a for a, b in zip([0] + ends, ends)])
     print("gradient norms", [round(float(d.float().norm()), 4) for d in grads])
     apart = (many.float() - few.float()).norm() / few.float().norm()
     print(f"the same tokens in the prompt and by themselves: {float(apart):.4f} apart (relative)")
