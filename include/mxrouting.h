@@ -55,7 +55,8 @@ mxfp8_status_t mx_moe_route_bwd(const void* logits, int32_t logits_type, int64_t
  *   (int32, or int64 where index_bytes is 8; a value outside 0 .. E - 1 takes no row).
  *   Row order: by expert, within an expert by t * top_k + j.  Group sizes are padded to
  *   multiples of `multiple`.
- *   offs [E]: cumulative end rows;  counts [E]: rows that hold a token;
+ *   offs [E]: cumulative end rows (of one expert: all rows);  counts [E]: rows that hold a
+ *   token;
  *   slot [rows]: t * top_k + j of the row, -1 for padding and for rows past offs[E - 1];
  *   place [T, top_k]: the row, -1 where there is none.
  *   rows >= mx_moe_plan_rows(...), which always suffices: the largest multiple of

@@ -631,6 +631,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_place_kernel(const PlanPara
     for (int i = 0; i < kPer; ++i) {
         const int e = threadIdx.x * kPer + i;
         size[i] = e < p.E ? (total[e] + p.multiple - 1) / p.multiple * p.multiple : 0;
+        // one group is all rows: that is how the quantizations lay its scales out, whatever its end
+        if (p.E == 1 && e == 0) size[i] = (int32_t)p.rows;
         sum += size[i];
     }
     int32_t incl = sum;

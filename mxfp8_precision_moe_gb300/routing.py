@@ -147,7 +147,7 @@ def moe_route(logits: torch.Tensor, top_k: int, *, score: str = "softmax", bias:
 class MoePlan:
     """Rows of tokens grouped by expert (``moe_plan``); int32 tensors of one device:
 
-    offs [E]      end row of each expert's group, for the grouped products
+    offs [E]      end row of each expert's group, for the grouped products (of one expert: all rows)
     counts [E]    rows of the group that hold a token
     slot [rows]   t * top_k + j, the choice that the row holds; -1: none (padding, and rows past offs[E - 1])
     place [T, top_k]  the row that holds the choice; -1: none
@@ -196,8 +196,8 @@ def moe_plan(experts: torch.Tensor, num_experts: int, multiple: int = 1, *, exac
 
     The rows' number depends on the experts, which are on the device.  By default the plan has as many as can be
     needed, T * top_k + E * (multiple - 1) at most, and those past offs[E - 1] are in no group (the grouped products do
-    not touch them; ``check_offsets`` would refuse them); ``exact`` reads the number back, which waits for the device, and has
-    only those."""
+    not touch them; ``check_offsets`` would refuse them); ``exact`` reads the number back, which waits for the device (and so
+    cannot be captured into a graph), and has only those."""
     if not isinstance(experts, torch.Tensor) or experts.dtype not in (torch.int32, torch.int64) or experts.dim() != 2:
         raise ValueError("experts: expected [T, top_k] in int32 or int64")
     T, k = experts.shape
@@ -209,6 +209,8 @@ def moe_plan(experts: torch.Tensor, num_experts: int, multiple: int = 1, *, exac
     if not 1 <= multiple <= MAX_MULTIPLE:
         raise ValueError(f"multiple: 1 .. {MAX_MULTIPLE}, got {multiple}")
     _on_device(experts)
+    if exact and torch.cuda.is_current_stream_capturing():
+        raise ValueError("exact: the rows' number cannot be read back in a captured call")
     n = T * k
     if n + E * multiple >= 2 ** 31:
         raise ValueError(f"experts: too many rows for 32-bit row numbers ({T} tokens of {k})")

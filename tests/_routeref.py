@@ -116,4 +116,8 @@ def plan(experts, E, multiple):
         slot += rows + [-1] * (padded - len(rows))
         at += padded
         ends.append(at)
+    if E == 1:  # one group is all rows there can be
+        n = len(flat)
+        ends = [(n + min(1, n) * (multiple - 1)) // multiple * multiple]
+        slot += [-1] * (ends[0] - len(slot))
     return ends, [len(r) for r in groups], slot, np.array(place).reshape(np.asarray(experts).shape)

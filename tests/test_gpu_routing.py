@@ -244,7 +244,7 @@ def check_plan(experts, E, multiple, exact=False):
 
 
 @pytest.mark.parametrize("T,k,E,multiple", [
-    (1, 1, 1, 1), (1, 1, 7, 32), (5, 2, 6, 1), (64, 4, 16, 32), (77, 3, 13, 5), (300, 8, 256, 32), (100, 16, 1024, 1),
+    (1, 1, 1, 1), (70, 1, 1, 32), (1, 1, 7, 32), (5, 2, 6, 1), (64, 4, 16, 32), (77, 3, 13, 5), (300, 8, 256, 32), (100, 16, 1024, 1),
     (1024, 4, 16, 128), (1025, 4, 16, 32), (4096, 1, 8, 1), (5000, 3, 100, 32), (9000, 8, 256, 1), (3000, 16, 1024, 3)])
 @pytest.mark.parametrize("dtype", [torch.int32, torch.int64])
 def test_plan(T, k, E, multiple, dtype):
@@ -285,6 +285,17 @@ def test_plan_of_many_tokens():
 def test_plan_of_values_past_32_bits():
     e = torch.tensor([[2 ** 32, 1], [-2 ** 33 + 1, 2 ** 40 + 2]], device="cuda")
     check_plan(e, 4, 1)
+
+
+def test_exact_plan_is_refused_in_a_capture():
+    e = torch.zeros((4, 2), device="cuda", dtype=torch.int32)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        with pytest.raises(ValueError, match="captured"):
+            mx.moe_plan(e, 4, exact=True)
+        p = mx.moe_plan(e, 4)
+    graph.replay()
+    assert p.counts.tolist() == [8, 0, 0, 0]
 
 
 def test_plan_of_no_tokens():

@@ -158,6 +158,12 @@ def test_of_no_tokens():
     rows = mx.moe_gather(x, plan)
     assert rows.shape == (128, 64) and not rows.any() and not torch.autograd.grad(rows.sum(), x)[0].any()
     assert not mx.moe_combine(rows.detach(), plan).any()
+    plan = mx.moe_plan(torch.full((3, 2), -1, dtype=torch.int32, device="cuda"), 4, 32, exact=True)
+    rows = mx.moe_gather(x, plan)
+    assert rows.shape == (0, 64) and not torch.autograd.grad(rows.sum(), x)[0].any()
+    w = torch.ones((3, 2), device="cuda", requires_grad=True)
+    out = mx.moe_combine(rows.detach(), plan, w)
+    assert out.shape == (3, 64) and not out.any() and not torch.autograd.grad(out.sum(), w)[0].any()
 
 
 def test_any_layout_is_taken_and_modes():
@@ -297,14 +303,14 @@ def weights_of(E, D, H, seed):
     return [randn((E, H, D), seed, D ** -0.5), randn((E, H, D), seed + 1, D ** -0.5), randn((E, D, H), seed + 2, H ** -0.5)]
 
 
-def by_steps(x, logits, ws, k, route, w_mxfp8=None):
+def by_steps(x, logits, ws, k, route, exact=False):
     e, w = mx.moe_route(logits, k, **route)
-    plan = mx.moe_plan(e, ws[0].shape[0], 32)
-    y = mx.mxfp8_swiglu_expert(mx.moe_gather(x, plan), *ws, plan.offs, check_offsets=False, w_mxfp8=w_mxfp8)
+    plan = mx.moe_plan(e, ws[0].shape[0], 32, exact=exact)
+    y = mx.mxfp8_swiglu_expert(mx.moe_gather(x, plan), *ws, plan.offs, check_offsets=exact)
     return mx.moe_combine(y, plan, w)
 
 
-LAYERS = [(1, 4, 32, 32, 2, {}), (70, 5, 352, 160, 3, dict(score="sigmoid", renormalize=True, scale=2.5)),
+LAYERS = [(1, 4, 32, 32, 2, {}), (50, 1, 64, 96, 1, dict(score="sigmoid")), (70, 5, 352, 160, 3, dict(score="sigmoid", renormalize=True, scale=2.5)),
           (600, 8, 256, 512, 2, dict(score="softmax_all")),
           (257, 64, 128, 64, 8, dict(score="sigmoid", groups=8, top_groups=3, renormalize=True))]
 
@@ -312,29 +318,31 @@ LAYERS = [(1, 4, 32, 32, 2, {}), (70, 5, 352, 160, 3, dict(score="sigmoid", reno
 @pytest.mark.parametrize("T,E,D,H,k,route", LAYERS)
 @pytest.mark.parametrize("masked", [False, True])
 def test_layer_is_its_steps(T, E, D, H, k, route, masked):
-    """Outputs and all five gradients of mxfp8_moe_swiglu, bit for bit those of its steps."""
+    """Outputs and all five gradients of mxfp8_moe_swiglu, bit for bit those of its steps, also over a plan without rows past
+    the last group, whose offsets are checked."""
     x, logits, ws = randn((T, D), 1), torch.randn((T, E), generator=gen(2), device="cuda"), weights_of(E, D, H, 3)
     bias = None
     if masked:
         logits[T // 2:] = float("-inf")      # the end of a padded batch
         bias = torch.randn(E, generator=gen(9), device="cuda") * 0.1
-        bias[0] = float("-inf")              # an expert that takes nothing
+        bias[0] = float("-inf") if E > 1 else 0.0   # an expert that takes nothing
         route = dict(route, bias=bias)
     d = randn((T, D), 8, 1e-2)
     results = []
-    for f in (lambda a, b, c: mx.mxfp8_moe_swiglu(a, b, *c, k, **route), lambda a, b, c: by_steps(a, b, c, k, route)):
+    for f in (lambda a, b, c: mx.mxfp8_moe_swiglu(a, b, *c, k, **route), lambda a, b, c: by_steps(a, b, c, k, route),
+              lambda a, b, c: by_steps(a, b, c, k, route, exact=T > 1 or not masked)):  # (no rows at all: not for the expert)
         leaves = [t.clone().requires_grad_(True) for t in (x, logits, *ws)]
         out = f(leaves[0], leaves[1], leaves[2:])
         results.append((out.detach(),) + torch.autograd.grad(out, leaves, d))
-    for a, b in zip(*results):
-        assert torch.isfinite(a.float()).all() and torch.equal(a, b)
+    for a, b, c in zip(*results):
+        assert torch.isfinite(a.float()).all() and torch.equal(a, b) and torch.equal(a, c)
     if T // 2 and not masked:
         assert all(r.any() for r in results[0][:2])
 
 
 def test_layer_gradients_by_themselves():
     """Each gradient alone is the one that all of them together give; none where gradients are disabled."""
-    T, E, D, H, k, route = LAYERS[1]
+    T, E, D, H, k, route = LAYERS[2]
     x, logits, ws = randn((T, D), 1), torch.randn((T, E), generator=gen(2), device="cuda"), weights_of(E, D, H, 3)
     d = randn((T, D), 8, 1e-2)
 
@@ -385,7 +393,7 @@ def test_layer_of_no_tokens():
 
 def test_layer_captured_forward_and_backward():
     """Two captured training steps replayed on streams of their own, beside an eager one."""
-    T, E, D, H, k, route = LAYERS[1]
+    T, E, D, H, k, route = LAYERS[2]
     ws = weights_of(E, D, H, 3)
     steps = []
     for seed in (1, 2):
@@ -424,7 +432,7 @@ def test_layer_captured_forward_and_backward():
 
 def test_on_another_stream():
     s = torch.cuda.Stream()
-    T, E, D, H, k, route = LAYERS[2]
+    T, E, D, H, k, route = LAYERS[3]
     x, logits, ws = randn((T, D), 1), torch.randn((T, E), generator=gen(2), device="cuda"), weights_of(E, D, H, 3)
     want = mx.mxfp8_moe_swiglu(x, logits, *ws, k, **route)
     torch.cuda.synchronize()
