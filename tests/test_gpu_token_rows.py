@@ -184,6 +184,42 @@ def test_any_layout_is_taken_and_modes():
         mx.mxfp8_gather_quantize(x.T.contiguous().T, plan)
 
 
+def test_offsets_past_32_bits():
+    """2.2 thousand million elements a matrix, its last rows among what is checked."""
+    T, D = 270016, 8192
+    x = torch.empty((T, D), dtype=torch.bfloat16, device="cuda")
+    for i in range(0, T, 4096):
+        x[i:i + 4096] = randn((min(4096, T - i), D), i)
+    e = torch.randint(0, 4, (T, 1), generator=gen(5), device="cuda")
+    plan = mx.moe_plan(e, 4, 32, exact=True)
+    rows = mx.moe_gather(x, plan)
+    token = plan.slot.long()
+    for at in (slice(0, 500), slice(plan.rows // 2, plan.rows // 2 + 500), slice(plan.rows - 500, plan.rows)):
+        t = token[at]
+        assert torch.equal(rows[at], torch.where((t >= 0)[:, None], x[t.clamp_min(0)], 0.0))
+    assert torch.equal(mx.moe_combine(rows, plan), x)
+    both = mx.ROW | mx.COL
+    got = mx.mxfp8_gather_quantize(x, plan, both)
+    same_copies(got, mx.mxfp8_quantize_2d(rows, both, mx.SCALES_BLOCKED, plan.offs), plan, D)
+    q, s, *_ = mx.mxfp8_gather_quantize(x, plan)
+    same_copies((q, s, None, None), (got[0], got[1], None, None), plan, D)
+    values = mx.mxfp8_dequantize_2d(q, s, offs=plan.offs)
+    # half a step is 2^-4 of a value, saturation of a block's largest (512 to 448) 2^-3
+    assert ((values[-500:].float() - rows[-500:].float()).abs() <= 2.0 ** -3 * rows[-500:].float().abs() + 2.0 ** -9).all()
+    del got, q, s, values
+    q, s = mx.mxfp4_gather_quantize(x, plan)
+    want = mx.mxfp4_quantize_2d(rows, offs=plan.offs)
+    assert torch.equal(q, want[0])
+    del q, s, want
+    w = torch.rand((T, 1), generator=gen(6), device="cuda").requires_grad_(True)
+    y = rows.detach().requires_grad_(True)
+    dy, dw = torch.autograd.grad(mx.moe_combine(y, plan, w), (y, w), x)
+    t = token[-500:]
+    assert ((dy[-500:].float() - rows[-500:].float() * torch.where(t >= 0, w.detach().flatten()[t.clamp_min(0)], 0.0)[:, None]).abs()
+            <= 2 * BF16 * dy[-500:].float().abs()).all()
+    assert ((dw[-500:, 0] - x[-500:].float().square().sum(1)).abs() <= 1e-3 * dw[-500:, 0]).all()
+
+
 # ---------------------------------------------------------------- quantized on the way
 Q_SHAPES = [(1, 1, 1, 32, 32), (5, 2, 6, 32, 352), (77, 3, 13, 32, 160), (300, 8, 256, 32, 96), (1000, 4, 16, 128, 2080),
             (129, 6, 8, 32, 7168), (2000, 1, 3, 32, 128), (64, 16, 40, 64, 1024)]
