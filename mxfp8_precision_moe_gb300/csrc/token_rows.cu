@@ -21,6 +21,7 @@ struct RowsParams {
     int32_t k;
     uint32_t C;
     uint32_t token_ctas;   // of the gather: CTAs that take tokens; the others take padding rows
+    uint32_t parts;        // warps that share a token
 };
 
 constexpr int kRowsThreads = 256;
@@ -35,17 +36,6 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
 __device__ __forceinline__ int64_t row_or_none(const RowsParams& p, int64_t i) {
     const int32_t r = __ldg(p.place + i);
     return r >= 0 && r < p.rows ? r : -1;
-}
-
-// This thread's piece of a [T][C] matrix: one long division a CTA, a short one a thread.
-struct Piece {
-    int64_t i, t;  // its index, its row
-    uint32_t c;    // its place in the row
-};
-__device__ __forceinline__ Piece piece_of(uint32_t C) {
-    const int64_t first = (int64_t)blockIdx.x * kRowsThreads, t0 = first / C;
-    const uint32_t c0 = (uint32_t)(first - t0 * C) + threadIdx.x, more = c0 / C;
-    return Piece{first + threadIdx.x, t0 + more, c0 - more * C};
 }
 
 // Rows without a token are zeros: a warp takes 32 rows' slots at a time.
@@ -63,64 +53,100 @@ __device__ __forceinline__ void zero_padding_rows(const RowsParams& p, int64_t c
     }
 }
 
-// A thread a piece of a token's row: read once, written to the token's rows (times their weights).
+// A warp a token, or a share of one where tokens are few: two pieces a lane at a time, read once, written to the token's
+// rows (times their weights), which are looked up once, a lane each.
+constexpr int kGatherPieces = 2;
 template <bool kWeighted>
 __global__ void __launch_bounds__(kRowsThreads) gather_rows_kernel(const RowsParams p) {
     if (blockIdx.x >= p.token_ctas) {
         zero_padding_rows(p, blockIdx.x - p.token_ctas);
         return;
     }
-    const auto [i, t, c] = piece_of(p.C);
+    constexpr int U = kGatherPieces;
+    const int lane = threadIdx.x & 31;
+    const int64_t item = (int64_t)blockIdx.x * (kRowsThreads / 32) + (threadIdx.x >> 5), t = item / p.parts;
     if (t >= p.T) return;
-    const uint4 u = __ldg(p.x + i);
-    for (int j = 0; j < p.k; ++j) {
-        const int64_t r = row_or_none(p, t * p.k + j);
-        if (r < 0) continue;
-        uint4 o = u;
-        if constexpr (kWeighted) {
-            const float w = __ldg(p.w + t * p.k + j);
-            float v[8];
-            unpack8(u, v);
+    int32_t mine = -1;
+    float mine_w = 1.0f;
+    if (lane < p.k) {
+        mine = (int32_t)row_or_none(p, t * p.k + lane);
+        if constexpr (kWeighted) mine_w = __ldg(p.w + t * p.k + lane);
+    }
+    for (uint32_t first = (uint32_t)(item - t * p.parts) * (32 * U); first < p.C; first += p.parts * (32 * U)) {
+        const uint32_t c0 = first + lane;
+        uint4 u[U];
 #pragma unroll
-            for (int q = 0; q < 8; ++q) v[q] *= w;
-            o = pack8(v);
+        for (int q = 0; q < U; ++q)
+            if (c0 + 32 * q < p.C) u[q] = __ldg(p.x + t * p.C + c0 + 32 * q);
+        for (int j = 0; j < p.k; ++j) {
+            const int32_t row = __shfl_sync(0xffffffffu, mine, j);
+            const float w = kWeighted ? __shfl_sync(0xffffffffu, mine_w, j) : 1.0f;
+            if (row < 0) continue;  // the same for the whole warp
+#pragma unroll
+            for (int q = 0; q < U; ++q) {
+                uint4 o = u[q];
+                if constexpr (kWeighted) {
+                    float v[8];
+                    unpack8(u[q], v);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[e] *= w;
+                    o = pack8(v);
+                }
+                if (c0 + 32 * q < p.C) p.out[(int64_t)row * p.C + c0 + 32 * q] = o;
+            }
         }
-        p.out[r * p.C + c] = o;
     }
 }
 
-// A thread a piece of a token's output; KB rows' loads in flight at a time.
-template <int KB>
+// A warp a token, or a share of one where tokens are few: it looks the token's rows up once, a lane each, and then takes U
+// pieces a lane of up to KB rows at a time, U * KB loads in flight.
+template <int KB, int U>
 __global__ void __launch_bounds__(kRowsThreads) combine_kernel(const RowsParams p) {
-    const auto [i, t, c] = piece_of(p.C);
+    const int lane = threadIdx.x & 31;
+    const int64_t item = (int64_t)blockIdx.x * (kRowsThreads / 32) + (threadIdx.x >> 5), t = item / p.parts;
     if (t >= p.T) return;
-    float acc[8];
+    int32_t mine = -1;
+    float mine_w = 1.0f;
+    if (lane < p.k) {
+        mine = (int32_t)row_or_none(p, t * p.k + lane);
+        if (p.w) mine_w = __ldg(p.w + t * p.k + lane);
+    }
+    for (uint32_t first = (uint32_t)(item - t * p.parts) * (32 * U); first < p.C; first += p.parts * (32 * U)) {
+        const uint32_t c0 = first + lane;
+        float acc[U][8];
 #pragma unroll
-    for (int q = 0; q < 8; ++q) acc[q] = 0.0f;
-    for (int j0 = 0; j0 < p.k; j0 += KB) {
-        uint4 u[KB];
-        float w[KB];
-        bool has[KB];
+        for (int q = 0; q < U; ++q)
 #pragma unroll
-        for (int b = 0; b < KB; ++b) {
-            const int64_t r = j0 + b < p.k ? row_or_none(p, t * p.k + j0 + b) : -1;
-            has[b] = r >= 0;
-            w[b] = 1.0f;
-            if (has[b]) {
-                u[b] = __ldg(p.y + r * p.C + c);
-                if (p.w) w[b] = __ldg(p.w + t * p.k + j0 + b);
+            for (int e = 0; e < 8; ++e) acc[q][e] = 0.0f;
+        for (int j0 = 0; j0 < p.k; j0 += KB) {
+            uint4 u[KB][U];
+            int32_t row[KB];
+#pragma unroll
+            for (int b = 0; b < KB; ++b) {
+                row[b] = __shfl_sync(0xffffffffu, mine, (j0 + b) & 31);
+                if (j0 + b >= p.k) row[b] = -1;
+                if (row[b] < 0) continue;  // the same for the whole warp
+#pragma unroll
+                for (int q = 0; q < U; ++q)
+                    if (c0 + 32 * q < p.C) u[b][q] = __ldg(p.y + (int64_t)row[b] * p.C + c0 + 32 * q);
+            }
+#pragma unroll
+            for (int b = 0; b < KB; ++b) {
+                const float w = __shfl_sync(0xffffffffu, mine_w, (j0 + b) & 31);
+                if (row[b] < 0) continue;
+#pragma unroll
+                for (int q = 0; q < U; ++q) {
+                    float v[8];
+                    unpack8(u[b][q], v);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) acc[q][e] = fmaf(w, v[e], acc[q][e]);
+                }
             }
         }
 #pragma unroll
-        for (int b = 0; b < KB; ++b)
-            if (has[b]) {
-                float v[8];
-                unpack8(u[b], v);
-#pragma unroll
-                for (int q = 0; q < 8; ++q) acc[q] = fmaf(w[b], v[q], acc[q]);
-            }
+        for (int q = 0; q < U; ++q)
+            if (c0 + 32 * q < p.C) p.out[t * p.C + c0 + 32 * q] = pack8(acc[q]);
     }
-    p.out[i] = pack8(acc);
 }
 
 // A CTA a token: each piece of dout is read once, with the pieces of the token's rows of y; dy's are written, and the
@@ -189,20 +215,35 @@ static mxfp8_status_t rows_check(RowsParams& p, int64_t rows, int64_t T, int32_t
     p.T = T;
     p.k = top_k;
     p.C = (uint32_t)(D / 8);
-    if (T * p.C > (int64_t)INT32_MAX * kRowsThreads / 2) return MXFP8_ERR_SHAPE;
     return MXFP8_OK;
 }
 static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 static int64_t padding_ctas(const RowsParams& p) { return (p.rows + kRowsThreads - 1) / kRowsThreads; }
 
+// Warps for each token, of which one takes `width` pieces at a time: as many as fill the GPU twice, or one for each width.
+static uint32_t parts_of(const RowsParams& p, int width) {
+    const int64_t widths = (p.C + width - 1) / width, want = (int64_t)host::num_sms() * 128;
+    return (uint32_t)max64(1, min64(widths, (want + p.T - 1) / max64(p.T, 1)));
+}
+static int64_t token_ctas(const RowsParams& p) {
+    constexpr int kWarps = kRowsThreads / 32;
+    return (p.T * p.parts + kWarps - 1) / kWarps;
+}
+
 static mxfp8_status_t run_gather(RowsParams& p, cudaStream_t st) {
     if (p.rows == 0) return MXFP8_OK;
-    const int64_t tokens = (p.T * p.C + kRowsThreads - 1) / kRowsThreads;
-    p.token_ctas = (uint32_t)tokens;
-    const unsigned grid = (unsigned)(tokens + padding_ctas(p));
+    p.parts = parts_of(p, 32 * kGatherPieces);
+    p.token_ctas = (uint32_t)token_ctas(p);
+    const unsigned grid = (unsigned)(p.token_ctas + padding_ctas(p));
     if (p.w) gather_rows_kernel<true><<<grid, kRowsThreads, 0, st>>>(p);
     else gather_rows_kernel<false><<<grid, kRowsThreads, 0, st>>>(p);
     return host::last_launch_status();
+}
+
+template <int KB, int U>
+static void run_combine(RowsParams& p, cudaStream_t st) {
+    p.parts = parts_of(p, 32 * U);
+    combine_kernel<KB, U><<<(unsigned)token_ctas(p), kRowsThreads, 0, st>>>(p);
 }
 
 template <bool kDy>
@@ -246,11 +287,11 @@ extern "C" mxfp8_status_t mx_moe_combine(const void* y_bf16, const int32_t* plac
     p.w = w;
     p.out = static_cast<uint4*>(out_bf16);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    const unsigned grid = (unsigned)((T * p.C + kRowsThreads - 1) / kRowsThreads);
-    if (p.k == 1) combine_kernel<1><<<grid, kRowsThreads, 0, st>>>(p);
-    else if (p.k == 2) combine_kernel<2><<<grid, kRowsThreads, 0, st>>>(p);
-    else if (p.k <= 4) combine_kernel<4><<<grid, kRowsThreads, 0, st>>>(p);
-    else combine_kernel<8><<<grid, kRowsThreads, 0, st>>>(p);
+    // rows at a time x pieces: 8 rows a token of 7168, four by two 154 us (one by eight 202, two by four 184, eight by two
+    // 162); 4 of 5120, four by two 121 (four by one 160, two by four 139); 2, two by two 76 (two by four 86); 1, 55 and 56
+    if (p.k > 2) run_combine<4, 2>(p, st);
+    else if (p.k == 2) run_combine<2, 2>(p, st);
+    else run_combine<1, 2>(p, st);
     return host::last_launch_status();
 }
 
