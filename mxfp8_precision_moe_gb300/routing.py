@@ -21,7 +21,7 @@ from . import (COL, MAX_GROUPS, ROW, SCALES_BLOCKED, SCALES_COMPACT, _bytes_at_l
                mxfp8_grouped_mm_wgrad, mxfp8_scale_bytes, mxfp8_scale_bytes_colgroups, mxfp8_swiglu_bwd_quantize,
                quantize_expert_weights)
 from .moe_tokens import MAX_TOP_K, SCORES
-from .mxfp4 import _group_bytes
+from .mxfp4 import _good, _group_bytes
 
 _raw_stream = torch._C._cuda_getCurrentRawStream  # the current stream's handle, without building an object
 
@@ -41,10 +41,6 @@ def _on_device(*ts):
         if t.get_device() != here:
             raise ValueError(f"mxfp8: a tensor lives on {t.device}, and the current device, on which the kernels "
                              f"launch, is cuda:{here}")
-
-
-def _needs_grad(*ts) -> bool:
-    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in ts)
 
 
 # ---------------------------------------------------------------- routing
@@ -138,7 +134,7 @@ def moe_route(logits: torch.Tensor, top_k: int, *, score: str = "softmax", bias:
     logits = logits.contiguous()
     if bias is not None:
         bias = bias.detach().contiguous()
-    if _needs_grad(logits):
+    if logits.requires_grad and torch.is_grad_enabled():
         return _MoeRoute.apply(logits, bias, args)
     return _route(logits, bias, args)
 
@@ -152,9 +148,9 @@ class MoePlan:
     slot [rows]   t * top_k + j, the choice that the row holds; -1: none (padding, and rows past offs[E - 1])
     place [T, top_k]  the row that holds the choice; -1: none
 
-    Group sizes are multiples of ``multiple``."""
+    rows, tokens (T), top_k and ``multiple`` are numbers.  Group sizes are multiples of ``multiple``."""
 
-    __slots__ = ("offs", "counts", "slot", "place", "multiple")
+    __slots__ = ("offs", "counts", "slot", "place", "multiple", "rows", "tokens", "top_k")
 
     def __init__(self, offs, counts, slot, place, multiple: int = 1):
         _offsets(offs)
@@ -168,25 +164,13 @@ class MoePlan:
         for t in (offs, counts, slot, place):
             if not t.is_contiguous() or t.device != offs.device:
                 raise ValueError("MoePlan: contiguous tensors of one device expected")
-        self.offs, self.counts, self.slot, self.place, self.multiple = offs, counts, slot, place, int(multiple)
+        self._fill(offs, counts, slot, place, int(multiple))
 
-    @classmethod
-    def _of(cls, offs, counts, slot, place, multiple):  # arrays that need no checks
-        plan = cls.__new__(cls)
-        plan.offs, plan.counts, plan.slot, plan.place, plan.multiple = offs, counts, slot, place, multiple
-        return plan
-
-    @property
-    def rows(self) -> int:
-        return self.slot.shape[0]
-
-    @property
-    def tokens(self) -> int:
-        return self.place.shape[0]
-
-    @property
-    def top_k(self) -> int:
-        return self.place.shape[1]
+    def _fill(self, offs, counts, slot, place, multiple):
+        self.offs, self.counts, self.slot, self.place, self.multiple = offs, counts, slot, place, multiple
+        self.rows = slot.shape[0]
+        self.tokens, self.top_k = place.shape
+        return self
 
 
 def moe_plan(experts: torch.Tensor, num_experts: int, multiple: int = 1, *, exact: bool = False) -> MoePlan:
@@ -228,10 +212,19 @@ def moe_plan(experts: torch.Tensor, num_experts: int, multiple: int = 1, *, exac
                         _raw_stream(dev.index)), "mx_moe_plan")
     if exact:
         slot = slot[:int(offs[-1])]
-    return MoePlan._of(offs, counts, slot, place, multiple)
+    return MoePlan.__new__(MoePlan)._fill(offs, counts, slot, place, multiple)
 
 
 # ---------------------------------------------------------------- rows
+# A small call's time is the host's: what a correct call looks like is asked first, in a few expressions, and the named
+# checks, which say what is wrong, follow where the answer is no.
+def _good_rows(x, n: int, multiple: int, plan, weights=None) -> bool:
+    here = torch._C._cuda_getDevice() if isinstance(x, torch.Tensor) and x.is_cuda else -2
+    return (_good(x, torch.bfloat16, 2, here) and x.shape[0] == n and x.shape[1] % multiple == 0 and x.shape[1] >= multiple
+            and plan.offs.get_device() == here
+            and (weights is None or (_good(weights, torch.float32, 2, here) and weights.shape == plan.place.shape)))
+
+
 def _rows_matrix(x, name: str, n: int, what: str, multiple: int = 8):
     _tensor(x, name, torch.bfloat16, 2)
     if x.shape[0] != n:
@@ -294,10 +287,11 @@ class _MoeGather(torch.autograd.Function):
 def moe_gather(x: torch.Tensor, plan: MoePlan) -> torch.Tensor:
     """Token rows in the plan's order: x [T, D] bf16 -> [plan.rows, D], zeros in rows without a token.  D a multiple of 8.
     Differentiable: a token's gradient is the sum of its rows' in fp32, rounded once."""
-    _rows_matrix(x, "x", _plan_of(plan).tokens, "tokens")
-    _on_device(x, plan.offs)
-    x = x.contiguous()
-    if _needs_grad(x):
+    if not _good_rows(x, _plan_of(plan).tokens, 8, plan):
+        _rows_matrix(x, "x", plan.tokens, "tokens")
+        _on_device(x, plan.offs)
+        x = x.contiguous()
+    if x.requires_grad and torch.is_grad_enabled():
         return _MoeGather.apply(x, plan)
     return _gather(x, plan, torch.empty((plan.rows, x.shape[1]), dtype=torch.bfloat16, device=x.device))
 
@@ -323,13 +317,14 @@ def moe_combine(y: torch.Tensor, plan: MoePlan, weights: torch.Tensor | None = N
     weights [T, top_k] fp32 (none: ones) -> [T, D] bf16.  fp32 sums in the order of j, rounded once; a choice without a row
     counts nothing, a token without any gets zeros.  D a multiple of 8.  Differentiable in y (rows without a token get
     zeros) and in the weights."""
-    _rows_matrix(y, "y", _plan_of(plan).rows, "rows")
-    _choice_weights(weights, plan)
-    _on_device(y, plan.offs, weights)
-    y = y.contiguous()
-    if weights is not None:
-        weights = weights.contiguous()
-    if _needs_grad(y, weights):
+    if not _good_rows(y, _plan_of(plan).rows, 8, plan, weights):
+        _rows_matrix(y, "y", plan.rows, "rows")
+        _choice_weights(weights, plan)
+        _on_device(y, plan.offs, weights)
+        y = y.contiguous()
+        if weights is not None:
+            weights = weights.contiguous()
+    if (y.requires_grad or (weights is not None and weights.requires_grad)) and torch.is_grad_enabled():
         return _MoeCombine.apply(y, weights, plan)
     return _combine(y, plan, weights)
 
@@ -341,14 +336,16 @@ def mxfp8_gather_quantize(x: torch.Tensor, plan: MoePlan, dirs: int = ROW, weigh
     (q_row [rows, D], s_row, q_col [D, rows], s_col), None for a direction not asked for (ROW, COL or both).  With
     weights [T, top_k] the rows are bf16(weight * row), which is what ``moe_combine`` hands back to its rows' gradient.
     D a multiple of 32; the plan's multiple one of 32 for COL."""
-    _rows_matrix(x, "x", _plan_of(plan).tokens, "tokens", 32)
     if dirs not in (ROW, COL, ROW | COL):
         raise ValueError("dirs: ROW, COL or both expected")
-    if dirs & COL and (plan.multiple % 32 or plan.rows % 32):
-        raise ValueError(f"plan: COL needs groups of multiples of 32 rows, got multiples of {plan.multiple}")
-    _choice_weights(weights, plan)
-    _status_word(dev_status)
-    _cuda(x, plan.offs, weights, dev_status)
+    if not _good_rows(x, _plan_of(plan).tokens, 32, plan, weights) or dev_status is not None \
+            or (dirs & COL and (plan.multiple % 32 or plan.rows % 32)):
+        _rows_matrix(x, "x", plan.tokens, "tokens", 32)
+        if dirs & COL and (plan.multiple % 32 or plan.rows % 32):
+            raise ValueError(f"plan: COL needs groups of multiples of 32 rows, got multiples of {plan.multiple}")
+        _choice_weights(weights, plan)
+        _status_word(dev_status)
+        _cuda(x, plan.offs, weights, dev_status)
     (T, D), M, G, dev = x.shape, plan.rows, plan.offs.shape[0], x.device
     q_row = s_row = q_col = s_col = None
     if dirs & ROW:
@@ -364,8 +361,9 @@ def mxfp8_gather_quantize(x: torch.Tensor, plan: MoePlan, dirs: int = ROW, weigh
 def mxfp4_gather_quantize(x: torch.Tensor, plan: MoePlan):
     """``mxfp4_quantize_2d(moe_gather(x, plan), offs=plan.offs)`` without the rows in between: (q [rows, D/2], s).  D a
     multiple of 32.  Rows past the last group are not written."""
-    _rows_matrix(x, "x", _plan_of(plan).tokens, "tokens", 32)
-    _cuda(x, plan.offs)
+    if not _good_rows(x, _plan_of(plan).tokens, 32, plan):
+        _rows_matrix(x, "x", plan.tokens, "tokens", 32)
+        _cuda(x, plan.offs)
     (T, D), M, G, dev = x.shape, plan.rows, plan.offs.shape[0], x.device
     q, s = _u8((M, D // 2), dev), _u8(_group_bytes(M, D, G), dev)
     check(load().mxfp4_gather_quantize(x.data_ptr(), plan.slot.data_ptr(), plan.place.data_ptr(), M, T, plan.top_k, D,
