@@ -381,7 +381,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RoutePara
             if (least == 0u) break;
             if (left == least) left = 0u;
         }
-        if (least == 0u) least = 1u;
+        if (least == 0u || err == INFINITY) least = 1u;  // few are left, or nothing is known: all
         else if (KEYS != kKeysLogits && err > 0.0f) least = order_of(value_of(least) - 4 * err);
         int n = 0;
 #pragma unroll

@@ -151,6 +151,23 @@ def test_a_bias_of_minus_infinity_masks_an_expert():
         assert (e[:, 9] == -1).all() and (w[:, 9] == 0).all() and (e[:, :9] >= 0).all()
 
 
+@pytest.mark.parametrize("E", [12, 60, 100, 256, 1024])
+@pytest.mark.parametrize("score", ["softmax", "softmax_all", "sigmoid"])
+@pytest.mark.parametrize("groups", [1, 4])
+def test_many_infinite_keys(E, score, groups):
+    """Infinite biases, of few experts and of nearly all, and sums past fp32's largest: they tie or rank as exact sums do."""
+    l = logits_of(6, E, torch.float32, E)
+    for n in (1, 3, E // 2, E - 1, E):
+        bias = torch.zeros(E, device="cuda")
+        bias[torch.randperm(E, generator=torch.Generator().manual_seed(n))[:n].cuda()] = math.inf
+        check(l, 3, bias=bias, score=score, groups=groups, top_groups=groups)
+        check(l, 2, bias=bias, score=score, groups=groups, top_groups=1)
+    huge = torch.full((E,), 3e38, device="cuda") + torch.arange(E, device="cuda") * 1e33
+    e, _ = mx.moe_route(huge[None] * torch.ones(2, 1, device="cuda"), 3, score=score, bias=huge)
+    if score == "softmax":
+        assert e.tolist() == [[E - 1, E - 2, E - 3]] * 2
+
+
 @pytest.mark.parametrize("score", ["softmax", "softmax_all", "sigmoid"])
 def test_order_that_32_bits_leave_open(score):
     """Pairs of experts whose keys are made equal to 32 bits: their order is that of the exact sums."""
