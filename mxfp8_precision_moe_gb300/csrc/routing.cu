@@ -175,8 +175,7 @@ __device__ __forceinline__ float weight_of(const RouteParams& p, bool in, float 
         if (p.renormalize) {
             // s_j / sum s with every s_j times e^-c, c the largest logit where that is negative: where all logits are far
             // below 0 the scores themselves would underflow, and their quotients be lost
-            const float c = warp_max(in ? l : -INFINITY);
-            if (c < 0.0f) s = expf(l - c);
+            if (!__any_sync(kFull, in && !(l < 0.0f))) s = expf(l - warp_max(in ? l : -INFINITY));
         }
         s = in ? (l == l ? s / (1.0f + a) : l) : 0.0f;
         if (!p.renormalize) return s;
@@ -222,8 +221,7 @@ __device__ __forceinline__ void load_logits(const RouteParams& p, int64_t t, int
 // Keys: the logits themselves (exact), logit + bias, or a score (+ bias).
 enum RouteKeys : int { kKeysLogits = 0, kKeysBias = 1, kKeysSigmoid = 2, kKeysSoftmax = 3 };
 
-// The same where the groups are settled and the experts that come into question are few: lane i's is e, -1: none; they
-// lie in the order of their indices.
+// The same where the groups are settled and the experts that come into question are few: lane i's is e, -1: none.
 __device__ __noinline__ int select_64_among(const RouteParams& p, int64_t t, int e, int total, uint2* shared, int lane) {
     double top = 0.0, sum = 1.0;
     if (p.score == MX_SCORE_SOFTMAX_ALL) softmax_64(p, t, lane, top, sum);
@@ -231,7 +229,8 @@ __device__ __noinline__ int select_64_among(const RouteParams& p, int64_t t, int
     int rank = 0;
     for (int j = 0; j < total; ++j) {
         const unsigned long long other = __shfl_sync(kFull, key, j);
-        rank += other > key || (other == key && j < lane);
+        const int expert = __shfl_sync(kFull, e, j);
+        rank += other > key || (other == key && expert < e);
     }
     if (lane < total) shared[rank].y = (uint32_t)e;
     __syncwarp();
@@ -254,10 +253,12 @@ template <int VPL, int KEYS>
 __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteParams p) {
     extern __shared__ unsigned long long route_smem[];
     constexpr bool kCandidates = VPL > 2;
-    __shared__ uint2 candidates[kCandidates ? kRouteWarps : 1][32];
+    __shared__ __align__(8) uint2 candidates[kCandidates ? kRouteWarps : 1][32];  // ~expert, key: as 64 bits the order
+    __shared__ int filled[kRouteWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t t = (int64_t)blockIdx.x * kRouteWarps + warp;
     if (t >= p.T) return;
+    if (kCandidates && lane == 0) filled[warp] = 0;  // (before any of the exchanges below)
     unsigned long long* keys = route_smem + (size_t)warp * p.E;  // this warp's, where there are groups or doubts
     constexpr float kUlp = 0x1p-24f;
 
@@ -332,15 +333,18 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RoutePara
                 top = max(top, t2);
             }
             const uint32_t worth = p.group_max || !second ? top : order_of(value_of(top) + value_of(second));
-            int rank = 0;
-#pragma unroll 4
-            for (int first = 0; first < 32; first += lanes) {  // (past the last group: 0, which counts nowhere)
-                const uint32_t other = __shfl_sync(kFull, worth, first);
-                rank += other > worth || (other == worth && first + lanes <= lane);
+            // the best groups leave one by one, of equal ones the first (lanes past the last group hold nothing: 0)
+            uint32_t left = worth;
+            low = 0xffffffffu;
+            for (int g = 0; g < p.top_groups; ++g) {
+                const uint32_t most = __reduce_max_sync(kFull, left);
+                if (most == 0u) break;
+                low = most;
+                const int src = __ffs(__ballot_sync(kFull, left == most)) - 1;
+                if (((lane ^ src) & -lanes) == 0) left = 0u;  // of the same group
             }
-            const bool stay = worth && rank < p.top_groups;  // lanes past the last group hold nothing: worth is 0
-            low = __reduce_min_sync(kFull, stay ? worth : 0xffffffffu);
-            high = __reduce_max_sync(kFull, stay ? 0u : worth);
+            high = __reduce_max_sync(kFull, left);
+            const bool stay = left == 0u;
             if (!stay) {
 #pragma unroll
                 for (int i = 0; i < VPL; ++i) ord[i] = 0u;
@@ -386,40 +390,34 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RoutePara
         int n = 0;
 #pragma unroll
         for (int i = 0; i < VPL; ++i) n += ord[i] >= least;
-        int at = n;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int o = __shfl_up_sync(kFull, at, d);
-            if (lane >= d) at += o;
-        }
-        total = __shfl_sync(kFull, at, 31);
-        at -= n;
+        total = __reduce_add_sync(kFull, n);
         if (total <= 32) {
             one_by_one = false;
+            // in any order: they are told apart by their experts
+            __syncwarp();
+            int at = n ? atomicAdd(&filled[warp], n) : 0;
             if (n) {
 #pragma unroll
                 for (int i = 0; i < VPL; ++i)
-                    if (ord[i] >= least) candidates[warp][at++] = make_uint2(ord[i], lane * VPL + i);
+                    if (ord[i] >= least) candidates[warp][at++] = make_uint2(~(uint32_t)(lane * VPL + i), ord[i]);
             }
             __syncwarp();
             uint2 c = make_uint2(0u, 0u);
             if (lane < total) {
                 c = candidates[warp][lane];
-                candidate = (int)c.y;
+                candidate = (int)~c.x;
             }
-            int rank = 0;  // they lie in the order of the experts
+            const unsigned long long own = (unsigned long long)c.y << 32 | c.x;
+            int rank = 0;
 #pragma unroll 4
-            for (int j = 0; j < total; ++j) {
-                const uint32_t other = __shfl_sync(kFull, c.x, j);
-                rank += other > c.x || (other == c.x && j < lane);
-            }
+            for (int j = 0; j < total; ++j) rank += reinterpret_cast<const unsigned long long*>(candidates[warp])[j] > own;
             __syncwarp();
             if (lane < total) candidates[warp][rank] = c;
             __syncwarp();
             if (lane < min(total, wanted)) {
                 c = candidates[warp][lane];
-                my_ord = c.x;
-                mine = (int)c.y;
+                my_ord = c.y;
+                mine = (int)~c.x;
             }
         }
     }
