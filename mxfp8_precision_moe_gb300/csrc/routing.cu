@@ -249,6 +249,9 @@ __device__ __noinline__ int select_64_among(const RouteParams& p, int64_t t, int
 // apart than their bounds, the token is done again in 64 bits: among the candidates (that come within four bounds of the
 // least, so that the exact largest are there), one a lane, or, where the groups are in doubt, from the start.  The keys can
 // then be made of the approximate exponential and reciprocal; weights are not.
+//
+// Bound by its instructions: 32768 tokens, 8 of 256 experts in 8 groups, 34.1 us (10 for the bytes of this and the
+// backward, which takes 9.6); about a dozen of those tokens are done again.
 template <int VPL, int KEYS>
 __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteParams p) {
     extern __shared__ unsigned long long route_smem[];
