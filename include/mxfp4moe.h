@@ -79,7 +79,8 @@ mxfp8_status_t mxfp4_grouped_mm_fwd(const void* a_q, const void* a_s, const void
  *   S_t  = the top_k largest of router_logits[t] (NaN ranks above everything, ties go to
  *          the lowest expert, -inf is never selected);
  *   w_te = MX_SCORE_SOFTMAX: softmax over S_t; MX_SCORE_SOFTMAX_ALL: softmax over all
- *          experts; MX_SCORE_SIGMOID: 1 / (1 + e^-logit);
+ *          experts; MX_SCORE_SIGMOID: 1 / (1 + e^-logit); MX_SCORE_GIVEN: the entry itself
+ *          (a matrix of weights with -inf for what is not selected, as mx_moe_route writes it);
  *   h_te = silu(xq_t Wg_e^T) * (xq_t Wu_e^T) in fp32;
  *   y_t  = bf16( sum over e in S_t of w_te MX(h_te) Wd_e^T ), fp32 sums, one rounding.
  * xq = MX(x_t) and MX(h) are quantized along D and H to the weights' format: bits = 8
@@ -96,7 +97,7 @@ mxfp8_status_t mxfp4_grouped_mm_fwd(const void* a_q, const void* a_s, const void
  *   MXFP8_ERR_TIMEOUT in dev_status); it can be captured into a graph.
  * mx_moe_tokens_workspace returns 0 for arguments mx_moe_tokens would refuse.
  * ------------------------------------------------------------------------- */
-enum { MX_SCORE_SOFTMAX = 0, MX_SCORE_SOFTMAX_ALL = 1, MX_SCORE_SIGMOID = 2 };
+enum { MX_SCORE_SOFTMAX = 0, MX_SCORE_SOFTMAX_ALL = 1, MX_SCORE_SIGMOID = 2, MX_SCORE_GIVEN = 16 };
 
 size_t mx_moe_tokens_workspace(int32_t max_tokens, int32_t E, int64_t D, int64_t H, int32_t top_k, int32_t bits);
 mxfp8_status_t mx_moe_tokens(const void* x_bf16, const float* router_logits, int32_t T, int32_t E, int64_t D,

@@ -35,6 +35,8 @@ extern "C" {
  *   experts [T, top_k] int32 and weights [T, top_k] fp32 in the order of the keys,
  *   largest first.  A token with fewer than top_k experts to select has -1 and 0 in
  *   the places left.
+ *   dense [T, E] fp32 or NULL: the weights by expert, -inf for what is not selected (what
+ *   mx_moe_tokens takes with MX_SCORE_GIVEN); with it experts and weights may be NULL.
  *   1 <= E <= MXFP8_MAX_GROUPS, 1 <= top_k <= MX_MAX_TOP_K, groups divides E and is at most
  *   32, top_k <= top_groups * E / groups.  Pointers aligned to their elements.
  * mx_moe_route_bwd -- dlogits [T, E] (of logits_type) from dweights [T, top_k] fp32 for
@@ -45,7 +47,8 @@ enum { MX_GROUP_TOP2 = 0, MX_GROUP_MAX = 1 };
 
 mxfp8_status_t mx_moe_route(const void* logits, int32_t logits_type, int64_t T, int32_t E, int32_t top_k, int32_t score,
                             const float* bias, int32_t groups, int32_t top_groups, int32_t group_score,
-                            int32_t renormalize, float scale, int32_t* experts, float* weights, mxfp8_stream_t stream);
+                            int32_t renormalize, float scale, int32_t* experts, float* weights, float* dense,
+                            mxfp8_stream_t stream);
 mxfp8_status_t mx_moe_route_bwd(const void* logits, int32_t logits_type, int64_t T, int32_t E, int32_t top_k,
                                 int32_t score, int32_t renormalize, float scale, const int32_t* experts,
                                 const float* dweights, void* dlogits, mxfp8_stream_t stream);

@@ -80,7 +80,7 @@ def load():
         "mx_moe_tokens": [P, P, I32, I32, I64, I64, I32, I32, I32, P, P, P, P, P, P, P, ctypes.c_size_t, P, P, P],
         "mx_debug_moe_tokens": [P, P, I32, I32, I64, I64, I32, I32, I32, P, P, P, P, P, P, P, ctypes.c_size_t, P, P,
                                 ctypes.c_uint64, P],
-        "mx_moe_route": [P, I32, I64, I32, I32, I32, P, I32, I32, I32, I32, ctypes.c_float, P, P, P],
+        "mx_moe_route": [P, I32, I64, I32, I32, I32, P, I32, I32, I32, I32, ctypes.c_float, P, P, P, P],
         "mx_moe_route_bwd": [P, I32, I64, I32, I32, I32, I32, ctypes.c_float, P, P, P, P],
         "mx_moe_plan": [P, I32, I64, I32, I32, I32, I64, P, P, P, P, P, ctypes.c_size_t, P],
         "mx_moe_gather": [P, P, P, I64, I64, I32, I64, P, P],

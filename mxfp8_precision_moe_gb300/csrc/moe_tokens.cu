@@ -261,6 +261,7 @@ __device__ __forceinline__ void mt_route(const MtParams& p, const MtScratch<Plan
 
 // The selected experts' logits -> their weights, by one warp.
 __device__ __forceinline__ void mt_weights(const MtParams& p, MtRoute& r, int lane) {
+    if (p.score == MX_SCORE_GIVEN) return;
     for (int t0 = 0; t0 < p.T; t0 += 32) {
         const int t = t0 + lane;
         const bool in = t < p.T;
@@ -1196,7 +1197,7 @@ static mxfp8_status_t mt_run(const void* x_bf16, const float* router_logits, int
                              size_t workspace_bytes, void* y_bf16, int32_t* dev_status, uint64_t limit_ns,
                              mxfp8_stream_t stream) {
     if (mxfp8_status_t s = mt_shape(T, E, D, H, top_k, bits); s != MXFP8_OK) return s;
-    if (score < MX_SCORE_SOFTMAX || score > MX_SCORE_SIGMOID) return MXFP8_ERR_LAYOUT;
+    if ((score < MX_SCORE_SOFTMAX || score > MX_SCORE_SIGMOID) && score != MX_SCORE_GIVEN) return MXFP8_ERR_LAYOUT;
     if (T == 0) return MXFP8_OK;
     const void* ptrs[] = {x_bf16, gate_q, gate_s, up_q, up_s, down_q, down_s, workspace, y_bf16};
     if (!router_logits) return MXFP8_ERR_NULL;

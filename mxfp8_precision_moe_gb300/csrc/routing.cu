@@ -15,6 +15,7 @@ struct RouteParams {
     const float* bias;
     int32_t* experts;
     float* weights;
+    float* dense;
     const float* dweights;  // the backward only
     void* dlogits;
     int64_t T;
@@ -468,9 +469,14 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RoutePara
 
     const bool in = lane < p.top_k && mine >= 0;
     const float w = weight_of(p, in, in ? logit_at(p, t, mine) : 0.0f, m, sum);
-    if (lane < p.top_k) {
+    if (p.experts != nullptr && lane < p.top_k) {
         p.experts[t * p.top_k + lane] = in ? mine : -1;
         p.weights[t * p.top_k + lane] = in ? w * p.scale : 0.0f;
+    }
+    if (p.dense != nullptr) {
+        for (int e = lane; e < p.E; e += 32) p.dense[t * p.E + e] = -INFINITY;
+        __syncwarp();  // orders the row before the values that take their places
+        if (in) p.dense[t * p.E + mine] = w * p.scale;
     }
 }
 
@@ -749,13 +755,14 @@ using namespace mx;
 extern "C" mxfp8_status_t mx_moe_route(const void* logits, int32_t logits_type, int64_t T, int32_t E, int32_t top_k,
                                        int32_t score, const float* bias, int32_t groups, int32_t top_groups,
                                        int32_t group_score, int32_t renormalize, float scale, int32_t* experts,
-                                       float* weights, mxfp8_stream_t stream) {
+                                       float* weights, float* dense, mxfp8_stream_t stream) {
     RouteParams p{};
     p.logits = logits;
     p.type = logits_type;
     p.bias = bias;
     p.experts = experts;
     p.weights = weights;
+    p.dense = dense;
     p.T = T;
     p.E = E;
     p.top_k = top_k;
@@ -770,9 +777,9 @@ extern "C" mxfp8_status_t mx_moe_route(const void* logits, int32_t logits_type, 
         return MXFP8_ERR_SHAPE;
     if (group_score != MX_GROUP_TOP2 && group_score != MX_GROUP_MAX) return MXFP8_ERR_LAYOUT;
     if (T == 0) return MXFP8_OK;  // an empty tensor may have no address
-    if (!logits || !experts || !weights) return MXFP8_ERR_NULL;
+    if (!logits || !experts != !weights || (!experts && !dense)) return MXFP8_ERR_NULL;
     if (!aligned_to(logits, logits_type == MX_LOGITS_FP32 ? 4 : 2) || !aligned_to(bias, 4) || !aligned_to(experts, 4) ||
-        !aligned_to(weights, 4))
+        !aligned_to(weights, 4) || !aligned_to(dense, 4))
         return MXFP8_ERR_ALIGN;
     if (mxfp8_status_t a = host::check_arch(); a != MXFP8_OK) return a;
     return route_run(p, reinterpret_cast<cudaStream_t>(stream));

@@ -18,6 +18,7 @@ from . import _bytes_at_least, _cuda, _expert_blocked_bytes, _status_word, _tens
 _raw_stream = torch._C._cuda_getCurrentRawStream  # the current stream's handle, without building an object
 
 SCORES = {"softmax": 0, "softmax_all": 1, "sigmoid": 2}
+SCORE_GIVEN = 16
 MAX_TOKENS, MAX_EXPERTS, MAX_TOP_K = 64, 256, 16
 
 
@@ -33,13 +34,21 @@ class MxMoeTokens:
     an expert's output.  (Where the input is to be scaled instead, which SwiGLU tells apart, and top_k is 1: scale x and
     leave the score at "softmax", whose only weight is 1.)
 
+    bias, groups, top_groups, group_score, renormalize, scale: as for ``moe_route``, which then runs before the layer (one
+    launch more); without any of them the layer routes by itself.  The layer reads the bias at each call, so that updates in
+    place count.
+
     The layer holds references to the weights and one workspace for each stream it is called on (a call
     captured into a graph takes one of the graph's memory).  It computes no gradients.
 
     A call does not wait for the device.  What the device finds (a wait between CTAs that ran out of time: the output is
     then incomplete) goes to the layer's own status word, which ``check_status`` reads, or to the caller's dev_status."""
 
-    def __init__(self, gate, up, down, top_k: int, *, score: str = "softmax", max_tokens: int = MAX_TOKENS):
+    _routing = _bias = None  # what moe_route is asked, where it runs first
+
+    def __init__(self, gate, up, down, top_k: int, *, score: str = "softmax", max_tokens: int = MAX_TOKENS,
+                 bias: torch.Tensor | None = None, groups: int = 1, top_groups: int | None = None,
+                 group_score: str = "top2", renormalize: bool = False, scale: float = 1.0):
         pairs = []
         for name, w in (("gate", gate), ("up", up), ("down", down)):
             if not isinstance(w, (tuple, list)) or len(w) < 2:
@@ -68,9 +77,15 @@ class MxMoeTokens:
             raise ValueError(f"score: one of {sorted(SCORES)}, got {score!r}")
         if not 1 <= max_tokens <= MAX_TOKENS:
             raise ValueError(f"max_tokens: 1 .. {MAX_TOKENS}, got {max_tokens}")
+        if bias is not None or groups != 1 or top_groups is not None or renormalize or scale != 1.0:
+            from .routing import _route_args
+
+            self._routing = _route_args(max_tokens, E, top_k, score, bias, groups, top_groups, group_score, renormalize, scale)
+        if bias is not None:
+            self._bias = bias.detach()
         for name, s, rows, cols in (("gate", gs, H, D), ("up", us, H, D), ("down", ds, D, H)):
             _bytes_at_least(s, f"{name} scales", E * _expert_blocked_bytes(rows, cols))
-        _cuda(gq, gs, uq, us, dq, ds)
+        _cuda(gq, gs, uq, us, dq, ds, self._bias)
         if len({t.device for t in (gq, gs, uq, us, dq, ds)}) != 1:
             raise ValueError("the weights must live on one device")
         self.E, self.H, self.D, self.bits, self.top_k = E, H, D, bits, int(top_k)
@@ -80,7 +95,7 @@ class MxMoeTokens:
         self._bytes = int(load().mx_moe_tokens_workspace(self.max_tokens, E, D, H, self.top_k, bits))
         if self._bytes == 0:
             raise ValueError("the layer is too large for the kernel's 32-bit tile counts")
-        self._fixed = (E, D, H, self.top_k, SCORES[score], bits) + tuple(t.data_ptr() for w in pairs for t in w)
+        self._fixed = (E, D, H, self.top_k, SCORES[score] if self._routing is None else SCORE_GIVEN, bits) + tuple(t.data_ptr() for w in pairs for t in w)
         self._workspaces: dict[int, torch.Tensor] = {}
         with torch.inference_mode(False):  # a tensor made in inference mode could not be zeroed outside of it
             self._status = new_status(self.device)
@@ -123,7 +138,8 @@ class MxMoeTokens:
         if router_logits.dtype != torch.float32:
             if router_logits.dtype not in (torch.bfloat16, torch.float16):
                 raise ValueError(f"router_logits: expected a floating type, got {router_logits.dtype}")
-            router_logits = router_logits.float()
+            if self._routing is None:
+                router_logits = router_logits.float()
         if torch.is_grad_enabled() and (x.requires_grad or router_logits.requires_grad):
             raise ValueError("MxMoeTokens computes no gradients: call it under torch.no_grad()")
         if out is not None:
@@ -136,6 +152,10 @@ class MxMoeTokens:
             out = torch.empty((T, self.D), dtype=torch.bfloat16, device=self.device)
         if T == 0:
             return out
+        if self._routing is not None:
+            from .routing import _route_dense
+
+            router_logits = _route_dense(router_logits, self._bias, self._routing)
         stream = _raw_stream(self.device.index)
         ws = self._workspace(stream)
         E, D, H, k, score, bits, *weights = self._fixed

@@ -67,16 +67,27 @@ def _route_args(T, E, top_k, score, bias, groups, top_groups, group_score, renor
     return int(top_k), SCORES[score], int(groups), int(top_groups), GROUP_SCORES[group_score], bool(renormalize), float(scale)
 
 
-def _route(logits, bias, args):
+def _route_into(logits, bias, args, experts, weights, dense):
     T, E = logits.shape
     top_k, score, groups, top_groups, group_score, renormalize, scale = args
-    dev = logits.device
-    experts = torch.empty((T, top_k), dtype=torch.int32, device=dev)
-    weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
     check(load().mx_moe_route(logits.data_ptr(), LOGITS_TYPES[logits.dtype], T, E, top_k, score,
                               None if bias is None else bias.data_ptr(), groups, top_groups, group_score, renormalize,
-                              scale, experts.data_ptr(), weights.data_ptr(), _raw_stream(dev.index)), "mx_moe_route")
+                              scale, experts, weights, dense, _raw_stream(logits.device.index)), "mx_moe_route")
+
+
+def _route(logits, bias, args):
+    T, top_k, dev = logits.shape[0], args[0], logits.device
+    experts = torch.empty((T, top_k), dtype=torch.int32, device=dev)
+    weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
+    _route_into(logits, bias, args, experts.data_ptr(), weights.data_ptr(), None)
     return experts, weights
+
+
+def _route_dense(logits, bias, args):
+    """The weights [T, E] fp32, -inf for what is not selected: what the layer for a few tokens takes."""
+    dense = torch.empty(logits.shape, dtype=torch.float32, device=logits.device)
+    _route_into(logits, bias, args, None, None, dense.data_ptr())
+    return dense
 
 
 def _route_bwd(logits, experts, dweights, args):

@@ -417,6 +417,53 @@ def test_layer_agrees_with_the_few_token_layer():
     assert (few - many).norm() <= 2 * (2.0 ** -8 / 12) ** 0.5 * few.norm()
 
 
+def few_layers(E, D, H, bits, seed, top_k, **route):
+    ws = weights_of(E, D, H, seed)
+    quads = [mx.quantize_expert_weights(w) if bits == 8 else mx.mxfp4_quantize_3d_experts(w) for w in ws]
+    return ws, quads, mx.MxMoeTokens(*quads, top_k, **route)
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("T,E", [(1, 4), (5, 40), (64, 8)])
+def test_few_token_layer_routed_by_moe_route(bits, T, E):
+    """A bias of zeros changes nothing: the same experts, and with two of them the same sums in the same order, so the
+    same bits, whichever kernel routes."""
+    _, quads, routed = few_layers(E, 128, 64, bits, 3, 2, bias=torch.zeros(E, device="cuda"))
+    x, logits = randn((T, 128), 1), torch.randn((T, E), generator=gen(2), device="cuda")
+    want = mx.MxMoeTokens(*quads, 2)(x, logits)
+    got = routed(x, logits)
+    routed.check_status()
+    assert torch.equal(got, want)
+    assert torch.equal(routed(x, logits.bfloat16()), mx.MxMoeTokens(*quads, 2)(x, logits.bfloat16()))
+    logits[0] = float("-inf")
+    assert not routed(x, logits)[0].any()
+
+
+@pytest.mark.parametrize("E,k,route", [
+    (64, 8, dict(score="sigmoid", groups=8, top_groups=3, renormalize=True, scale=2.5)),
+    (6, 2, dict(score="softmax_all", renormalize=True)), (12, 3, dict(score="softmax", groups=4, top_groups=2, group_score="max")),
+    (8, 1, dict(score="sigmoid", scale=0.5))])
+@pytest.mark.parametrize("with_bias", [True, False])
+def test_few_token_layer_with_options_agrees_with_the_layer(E, k, route, with_bias):
+    """Both serving paths with the same routing; they differ as in test_layer_agrees_with_the_few_token_layer."""
+    D, H, T = 256, 512, 20
+    bias = torch.randn(E, generator=gen(9), device="cuda") * 0.2 if with_bias else None
+    ws, quads, few = few_layers(E, D, H, 8, 3, k, bias=bias, **route)
+    x, logits = randn((T, D), 1), torch.randn((T, E), generator=gen(2), device="cuda")
+    logits[3] = float("-inf")
+    a = few(x, logits).double()
+    b = mx.mxfp8_moe_swiglu(x, logits, *ws, k, bias=bias, **route).double()
+    assert (a - b).norm() <= 2 * (2.0 ** -8 / 12) ** 0.5 * b.norm() and not a[3].any()
+    if with_bias:  # the layer reads the bias at each call, captured ones too
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            held = few(x, logits)
+        bias.copy_(-bias)
+        graph.replay()
+        assert torch.equal(held, few(x, logits)) and not torch.equal(held.double(), a)
+        few.check_status()
+
+
 def test_layer_of_no_tokens():
     ws = [w.requires_grad_(True) for w in weights_of(4, 64, 32, 3)]
     x = torch.zeros((0, 64), dtype=torch.bfloat16, device="cuda", requires_grad=True)

@@ -168,6 +168,16 @@ def test_refusals_of_the_binding(call, match):
         call()
 
 
+@pytest.mark.parametrize("kw,match", [
+    (dict(groups=3), "groups"), (dict(groups=2, top_groups=3), "top_groups"), (dict(groups=2, group_score="sum"), "group_score"),
+    (dict(bias=torch.zeros(3)), "bias"), (dict(bias=torch.zeros(2).double()), "bias"), (dict(bias=torch.zeros(2)), "CUDA"),
+    (dict(renormalize=True, score="tanh"), "score"), (dict(top_groups=0), "top_groups"), (dict(scale=2.0), "CUDA")])
+def test_refusals_of_the_few_token_layers_routing(kw, match):
+    w = (u8(2, 64, 128), u8(2, 512)), (u8(2, 64, 128), u8(2, 512)), (u8(2, 128, 64), u8(2, 512))
+    with pytest.raises(ValueError, match=match):
+        mx.MxMoeTokens(*w, 1, **kw)
+
+
 def fake(shape, dtype, index):
     with FakeTensorMode():
         return torch.empty(shape, dtype=dtype, device=f"cuda:{index}")
@@ -224,14 +234,16 @@ def test_refusals_of_the_c_abi():
     P = ctypes.c_void_p
     a = P(1 << 20)          # never dereferenced: validation fails first
     odd, half = P((1 << 20) + 8), P((1 << 20) + 2)
-    ok = dict(l=a, type=0, T=4, E=8, k=2, score=0, bias=None, groups=1, top=1, gs=0, renorm=0, scale=1.0, e=a, w=a, st=None)
+    ok = dict(l=a, type=0, T=4, E=8, k=2, score=0, bias=None, groups=1, top=1, gs=0, renorm=0, scale=1.0, e=a, w=a, dense=None,
+              st=None)
     call = lambda **kw: L.mx_moe_route(*{**ok, **kw}.values())  # noqa: E731
     assert call(T=-1) == 2 and call(E=0) == 2 and call(E=1025) == 2 and call(k=0) == 2 and call(k=9) == 2
     assert call(E=64, k=17) == 2 and call(T=1 << 31) == 2 and call(groups=3) == 2 and call(groups=0) == 2
     assert call(E=64, groups=64, top=64) == 2 and call(groups=2, top=3) == 2 and call(groups=2, top=0) == 2
     assert call(k=5, groups=2, top=1) == 2
     assert call(type=3) == 4 and call(score=3) == 4 and call(score=-1) == 4 and call(gs=2) == 4
-    assert call(l=None) == 1 and call(e=None) == 1 and call(w=None) == 1
+    assert call(l=None) == 1 and call(e=None) == 1 and call(w=None) == 1 and call(e=None, w=None) == 1
+    assert call(e=None, dense=a) == 1 and call(dense=half) == 3
     assert call(l=half) == 3 and call(w=half) == 3 and call(bias=half) == 3
     assert call(T=0, l=None, e=None, w=None) == 0
     ok = dict(l=a, type=0, T=4, E=8, k=2, score=0, renorm=0, scale=1.0, e=a, dw=a, dl=a, st=None)
