@@ -117,6 +117,18 @@ mxfp8_status_t mxfp4_gather_quantize(const void* x_bf16, const int32_t* slot, co
 mxfp8_status_t mxfp8_dequantize(const void* q, const void* s, int64_t M, int64_t K, unsigned dir, int scale_layout,
                                 const int32_t* offs, int32_t G, void* out_bf16, mxfp8_stream_t stream);
 
+/* ----------------------------------------------------------------------------
+ * mxfp8_swiglu_bwd_quantize_mxfp8 -- mxfp8_swiglu_bwd_quantize with h1 and h3 kept in 8
+ *   bits: h1_q, h3_q [M, H] codes and h1_s, h3_s [M, H/32] compact scales, as
+ *   mxfp8_quantize_2d(MXFP8_ROW, MXFP8_SCALES_COMPACT) writes them.  The outputs are those
+ *   of mxfp8_swiglu_bwd_quantize for the bf16 values that mxfp8_dequantize gives.
+ * ------------------------------------------------------------------------- */
+mxfp8_status_t mxfp8_swiglu_bwd_quantize_mxfp8(const void* dh_bf16, const void* h1_q, const void* h1_s, const void* h3_q,
+                                               const void* h3_s, int64_t M, int64_t H, const int32_t* offs, int32_t G,
+                                               void* dh1_q, void* dh1_s, void* dh1T_q, void* dh1T_s, void* dh3_q,
+                                               void* dh3_s, void* dh3T_q, void* dh3T_s, int32_t* dev_status,
+                                               mxfp8_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

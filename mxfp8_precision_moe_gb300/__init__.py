@@ -36,7 +36,7 @@ __all__ = [
     "mxfp4_quantize_3d_experts_mxfp8_cols", "mxfp4_dequantize_2d",
     "mxfp4_dequantize_3d_experts", "mxfp4_grouped_mm_fwd", "to_mxfp4_then_scaled_grouped_mm", "MxMoeTokens",
     "moe_route", "moe_plan", "MoePlan", "moe_gather", "moe_combine", "mxfp8_gather_quantize", "mxfp4_gather_quantize",
-    "mxfp8_dequantize_2d", "mxfp8_moe_swiglu",
+    "mxfp8_dequantize_2d", "mxfp8_swiglu_bwd_quantize_mxfp8", "mxfp8_moe_swiglu",
 ]
 
 
@@ -552,4 +552,4 @@ from .mxfp4 import (mxfp4_dequantize_2d, mxfp4_dequantize_3d_experts, mxfp4_grou
                     mxfp4_quantize_3d_experts_mxfp8_cols, mxfp4_swiglu_quantize, to_mxfp4_then_scaled_grouped_mm)
 from .moe_tokens import MxMoeTokens  # noqa: E402
 from .routing import (MoePlan, moe_combine, moe_gather, moe_plan, moe_route, mxfp4_gather_quantize,  # noqa: E402
-                      mxfp8_dequantize_2d, mxfp8_gather_quantize, mxfp8_moe_swiglu)
+                      mxfp8_dequantize_2d, mxfp8_gather_quantize, mxfp8_moe_swiglu, mxfp8_swiglu_bwd_quantize_mxfp8)

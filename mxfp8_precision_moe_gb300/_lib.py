@@ -88,6 +88,7 @@ def load():
         "mx_moe_combine_bwd": [P, P, P, P, P, I64, I64, I32, I64, P, P, P],
         "mxfp8_gather_quantize": [P, P, P, P, I64, I64, I32, I64, U32, P, I32, P, P, P, P, P, P],
         "mxfp4_gather_quantize": [P, P, P, I64, I64, I32, I64, P, I32, P, P, P],
+        "mxfp8_swiglu_bwd_quantize_mxfp8": [P, P, P, P, P, I64, I64, P, I32, P, P, P, P, P, P, P, P, P, P],
         "mxfp8_dequantize": [P, P, I64, I64, U32, INT, P, I32, P, P],
     }.items():
         f = getattr(L, name)

@@ -57,6 +57,8 @@ struct QParams {
     // second output set
     const uint16_t* x2;
     const uint16_t* x3;
+    const uint8_t* s2;   // of MXFP8 h1 and h3 (x2 and x3 are their codes): compact scales
+    const uint8_t* s3;
     uint8_t* q_row2;
     uint8_t* s_row2;
     uint8_t* q_col2;
@@ -74,9 +76,10 @@ struct QParams {
 // Kernel modes: plain MX quantization; the Hadamard variants (fp32 values), without and with
 // stochastic rounding; the fused SwiGLU backward (three inputs dh, h1, h3; two quantized outputs);
 // stochastic rounding alone (the plain kernel's bf16 data path with stochastic codes); MXFP4 codes for the
-// row-wise copy beside MXFP8 ones for the column-wise copy; rows gathered through a plan.
+// row-wise copy beside MXFP8 ones for the column-wise copy; rows gathered through a plan; the fused SwiGLU backward with h1
+// and h3 in MXFP8.
 enum QuantMode : int { kModePlain = 0, kModeExt = 1, kModeSwiBwd = 2, kModeSR = 3, kModeExtSR = 4, kModeRow4 = 5,
-                       kModeGather = 6 };
+                       kModeGather = 6, kModeSwiBwd8 = 7 };
 
 // ---- stability variants ("MXFP8 (Micro-scaling FP8)", "Numerical stability": random Hadamard
 // transforms before quantization, stochastic rounding)
@@ -246,6 +249,21 @@ __device__ __forceinline__ uint2 signs8(const uint32_t (&w)[4]) {
     return r;
 }
 
+// Eight E4M3 codes times a scale -> eight bf16 (exact but below bf16's smallest subnormal).
+__device__ __forceinline__ uint4 e4m3x8_values(uint2 codes, float f) {
+    uint32_t h[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        float lo, hi;  // every E4M3 value is a half
+        asm("{\n\t.reg .b32 v;\n\t.reg .f16 a, b;\n\tcvt.rn.f16x2.e4m3x2 v, %2;\n\tmov.b32 {a, b}, v;\n\t"
+            "cvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
+            : "=f"(lo), "=f"(hi)
+            : "h"((uint16_t)((k < 2 ? codes.x : codes.y) >> (16 * (k & 1)))));
+        h[k] = pack_bf16x2(lo * f, hi * f);
+    }
+    return make_uint4(h[0], h[1], h[2], h[3]);
+}
+
 constexpr int kQStages = 3;                    // SMEM ring depth (tiles in flight per CTA)
 constexpr int kQTileBytes = 128 * 128 * 2;     // one 128 x 128 bf16 tile
 constexpr int kQThreads = 288;                 // 8 consumer warps + 1 TMA producer warp
@@ -257,7 +275,9 @@ constexpr int kQConsumerThreads = 256;         // 8 consumer warps, no producer 
 // kModeSR: stochastic rounding alone, on the bf16 data path.
 // kModeSwiBwd (ROW|COL only): 256 threads, no TMA ring: each warp loads its patches of dh, h1 and h3
 // straight from global memory (three inputs a stage would leave room for too few warps to hide the
-// arithmetic's latency), computes dh1 and dh3 and quantizes each both ways.
+// arithmetic's latency), computes dh1 and dh3 and quantizes each both ways.  kModeSwiBwd8: h1 and h3 come as MXFP8 codes
+// with compact row-wise scales, 2.06 bytes a pair instead of 4.  Both are bound by their arithmetic, so that the fewer bytes
+// do not pay for the decoding: 16384 x 8192 406 and 476 us (548 where h1 and h3 are dequantized first).
 // kModeGather (ROW, COL, ROW|COL): a warp fills a ring of its own patches (32 rows x 64 columns) by 16-byte asynchronous
 // copies, each row through its slot; warps do not wait for one another.  A CTA takes units of up to 8 column tiles, whose
 // rows' slots, weights and places in the scales are looked up once.  16384 x 5120 both ways, 69 us (the plain kernel with
@@ -275,13 +295,15 @@ constexpr int kQConsumerThreads = 256;         // 8 consumer warps, no producer 
 template <int kMode>
 constexpr bool kFoldedProducer = kMode == kModeSR || kMode == kModeExtSR;
 template <int kMode>
-constexpr int kQThreadsOf = (kMode == kModeSwiBwd || kMode == kModeGather || kFoldedProducer<kMode>) ? kQConsumerThreads
-                                                                                                     : kQThreads;
+constexpr bool kSwiBwdOf = kMode == kModeSwiBwd || kMode == kModeSwiBwd8;
+template <int kMode>
+constexpr int kQThreadsOf = (kSwiBwdOf<kMode> || kMode == kModeGather || kFoldedProducer<kMode>) ? kQConsumerThreads
+                                                                                                 : kQThreads;
 constexpr int kGatherStages = 2;                          // patches of a warp in flight (3: 1-2% slower, 4: 40%)
 constexpr int kPatchBytes = 32 * 64 * 2;
 constexpr int kGatherSmem = 8 * kGatherStages * kPatchBytes;
 template <int kMode>
-constexpr int kQSmemOf = kMode == kModeSwiBwd ? 0 : kMode == kModeGather ? kGatherSmem + 128 : kQSmem;
+constexpr int kQSmemOf = kSwiBwdOf<kMode> ? 0 : kMode == kModeGather ? kGatherSmem + 128 : kQSmem;
 
 // Asynchronous copy of 16 bytes to shared memory; zeros where there is no source.
 __device__ __forceinline__ void copy16_async(uint32_t dst, const void* src, bool some) {
@@ -322,7 +344,7 @@ template <unsigned DIRS, int kMode = kModePlain, unsigned kHad = 0>
 __global__ void __launch_bounds__(kQThreadsOf<kMode>, 2)
     quant_tile_kernel(const __grid_constant__ CUtensorMap xmap, QParams p) {
     constexpr bool kExt = kMode == kModeExt || kMode == kModeExtSR;
-    constexpr bool kSwiBwd = kMode == kModeSwiBwd;
+    constexpr bool kSwiBwd = kSwiBwdOf<kMode>;
     constexpr bool kGather = kMode == kModeGather;
     constexpr int kStages = kQStages;
     constexpr uint32_t kStageBytes = kQTileBytes;
@@ -383,7 +405,7 @@ __global__ void __launch_bounds__(kQThreadsOf<kMode>, 2)
                 if (t < p.ntiles) issue_tile(t, s, 0u);
             }
     }
-    if (warp == 8) {
+    if (!kGather && warp == 8) {
         // ------------------------------------------------ TMA producer: whole 128x128 tiles, OOB zero-filled
         if (lane == 0) {
             int stage = 0;
@@ -1111,29 +1133,59 @@ __global__ void __launch_bounds__(kQThreadsOf<kMode>, 2)
             // bf16 autograd ops (silu(h1), dh*h3, their products each rounded to bf16), fp32 inside.
             // Rows past the matrix read as zeros (what the TMA path's fill gives).
             uint32_t a[8][4], u3[8][4];
+            if constexpr (kMode == kModeSwiBwd8) {
+                uint2 c1[8], c3[8];
+                uint32_t s13[8];  // h1's scale byte, h3's above it
+                const uint8_t* q1 = reinterpret_cast<const uint8_t*>(p.x2);
+                const uint8_t* q3 = reinterpret_cast<const uint8_t*>(p.x3);
 #pragma unroll
-            for (int rr = 0; rr < 8; ++rr) {
-                const int64_t row = row0 + 8 * li + rr;
-                uint4 g = make_uint4(0, 0, 0, 0), x1 = g, x3 = g;
-                if (row < R && cval) {
-                    const int64_t off = row * C + c8;
-                    g = __ldg(reinterpret_cast<const uint4*>(p.x + off));
-                    x1 = __ldg(reinterpret_cast<const uint4*>(p.x2 + off));
-                    x3 = __ldg(reinterpret_cast<const uint4*>(p.x3 + off));
+                for (int rr = 0; rr < 8; ++rr) {
+                    const int64_t row = row0 + 8 * li + rr, off = row * C + c8;
+                    uint4 g = make_uint4(0, 0, 0, 0);
+                    c1[rr] = c3[rr] = make_uint2(0, 0);
+                    s13[rr] = 0;
+                    if (row < R && cval) {
+                        g = __ldg(reinterpret_cast<const uint4*>(p.x + off));
+                        c1[rr] = __ldg(reinterpret_cast<const uint2*>(q1 + off));
+                        c3[rr] = __ldg(reinterpret_cast<const uint2*>(q3 + off));
+                        s13[rr] = __ldg(p.s2 + row * Cb + c8 / kBlk) | (uint32_t)__ldg(p.s3 + row * Cb + c8 / kBlk) << 8;
+                    }
+                    v[rr][0] = g.x; v[rr][1] = g.y; v[rr][2] = g.z; v[rr][3] = g.w;
                 }
-                v[rr][0] = g.x; v[rr][1] = g.y; v[rr][2] = g.z; v[rr][3] = g.w;
-                a[rr][0] = x1.x; a[rr][1] = x1.y; a[rr][2] = x1.z; a[rr][3] = x1.w;
-                u3[rr][0] = x3.x; u3[rr][1] = x3.y; u3[rr][2] = x3.z; u3[rr][3] = x3.w;
+#pragma unroll
+                for (int rr = 0; rr < 8; ++rr) {
+                    const uint4 x1 = e4m3x8_values(c1[rr], e8m0_value(s13[rr] & 0xFFu)),
+                                x3 = e4m3x8_values(c3[rr], e8m0_value(s13[rr] >> 8));
+                    swiglu_bwd_pair(v[rr][0], x1.x, x3.x, a[rr][0], u3[rr][0]);
+                    swiglu_bwd_pair(v[rr][1], x1.y, x3.y, a[rr][1], u3[rr][1]);
+                    swiglu_bwd_pair(v[rr][2], x1.z, x3.z, a[rr][2], u3[rr][2]);
+                    swiglu_bwd_pair(v[rr][3], x1.w, x3.w, a[rr][3], u3[rr][3]);
+                }
+            } else {
+#pragma unroll
+                for (int rr = 0; rr < 8; ++rr) {
+                    const int64_t row = row0 + 8 * li + rr;
+                    uint4 g = make_uint4(0, 0, 0, 0), x1 = g, x3 = g;
+                    if (row < R && cval) {
+                        const int64_t off = row * C + c8;
+                        g = __ldg(reinterpret_cast<const uint4*>(p.x + off));
+                        x1 = __ldg(reinterpret_cast<const uint4*>(p.x2 + off));
+                        x3 = __ldg(reinterpret_cast<const uint4*>(p.x3 + off));
+                    }
+                    v[rr][0] = g.x; v[rr][1] = g.y; v[rr][2] = g.z; v[rr][3] = g.w;
+                    a[rr][0] = x1.x; a[rr][1] = x1.y; a[rr][2] = x1.z; a[rr][3] = x1.w;
+                    u3[rr][0] = x3.x; u3[rr][1] = x3.y; u3[rr][2] = x3.z; u3[rr][3] = x3.w;
+                }
+#pragma unroll
+                for (int rr = 0; rr < 8; ++rr)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t d1, d3;
+                        swiglu_bwd_pair(v[rr][k], a[rr][k], u3[rr][k], d1, d3);
+                        a[rr][k] = d1;
+                        u3[rr][k] = d3;
+                    }
             }
-#pragma unroll
-            for (int rr = 0; rr < 8; ++rr)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    uint32_t d1, d3;
-                    swiglu_bwd_pair(v[rr][k], a[rr][k], u3[rr][k], d1, d3);
-                    a[rr][k] = d1;
-                    u3[rr][k] = d3;
-                }
             quant_rowcol(a, p.q_row, p.s_row, p.q_col, p.s_col);
             quant_rowcol(u3, p.q_row2, p.s_row2, p.q_col2, p.s_col2);
         } else if constexpr (kGather) {
@@ -1283,12 +1335,13 @@ static mxfp8_status_t quantize_row4(QParams& p, const void* x, int64_t R, int64_
 }
 
 // The fused SwiGLU backward: p.x = dh, p.x2 = h1, p.x3 = h3 (direct loads; the tensor map is unused).
+template <int kMode>
 static mxfp8_status_t launch_swiglu_bwd(const QParams& p, cudaStream_t st) {
     if (p.ntiles == 0) return MXFP8_OK;
     CUtensorMap m;
     if (!make_x_map(&m, p, p.x)) return MXFP8_ERR_DRIVER;
     const int64_t grid = std::min<int64_t>(p.ntiles, (int64_t)host::num_sms() * 2);
-    return launch_dirs<MXFP8_ROW | MXFP8_COL, kModeSwiBwd>(m, p, grid, st);
+    return launch_dirs<MXFP8_ROW | MXFP8_COL, kMode>(m, p, grid, st);
 }
 
 // Rows through a plan.  The tensor map is unused.
@@ -1385,20 +1438,43 @@ __global__ void __launch_bounds__(256) mxfp8_dequantize_kernel(const DqParams p)
             const int64_t r = r0 + 2 * i + (lane >> 4);
             if (r >= R) continue;
             const float f = e8m0_value(scale[i]);
-            uint32_t h[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                float lo, hi;  // every E4M3 value is a half
-                asm("{\n\t.reg .b32 v;\n\t.reg .f16 a, b;\n\tcvt.rn.f16x2.e4m3x2 v, %2;\n\tmov.b32 {a, b}, v;\n\t"
-                    "cvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
-                    : "=f"(lo), "=f"(hi)
-                    : "h"((uint16_t)((k < 2 ? codes[i].x : codes[i].y) >> (16 * (k & 1)))));
-                h[k] = pack_bf16x2(lo * f, hi * f);
-            }
-            *reinterpret_cast<uint4*>(p.out + r * C + c) =
-                none ? make_uint4(0, 0, 0, 0) : make_uint4(h[0], h[1], h[2], h[3]);
+            *reinterpret_cast<uint4*>(p.out + r * C + c) = none ? make_uint4(0, 0, 0, 0) : e4m3x8_values(codes[i], f);
         }
     }
+}
+
+// s1, s3: NULL where h1 and h3 are bf16, else the scales of their MXFP8 codes.
+static mxfp8_status_t swiglu_bwd_quantize(const void* dh_bf16, const void* h1, const void* h1_s, const void* h3,
+                                          const void* h3_s, bool mxfp8, int64_t M, int64_t H, const int32_t* offs, int32_t G,
+                                          void* dh1_q, void* dh1_s, void* dh1T_q, void* dh1T_s, void* dh3_q, void* dh3_s,
+                                          void* dh3T_q, void* dh3T_s, int32_t* dev_status, cudaStream_t st) {
+    if (!dh_bf16 || !h1 || !h3 || (mxfp8 && (!h1_s || !h3_s)) || !offs || !dh1_q || !dh1_s || !dh1T_q || !dh1T_s || !dh3_q ||
+        !dh3_s || !dh3T_q || !dh3T_s)
+        return MXFP8_ERR_NULL;
+    if (M < 0 || H <= 0 || G < 1 || G > MXFP8_MAX_GROUPS || M > INT32_MAX) return MXFP8_ERR_SHAPE;
+    if (H % 32 || M % 32) return MXFP8_ERR_ALIGN;
+    const void* ptrs[] = {dh_bf16, h1, h3, h1_s, h3_s, dh1_q, dh1_s, dh1T_q, dh1T_s, dh3_q, dh3_s, dh3T_q, dh3T_s};
+    for (const void* q : ptrs)
+        if (!host::aligned16(q)) return MXFP8_ERR_ALIGN;
+    if (mxfp8_status_t a = host::check_arch(); a != MXFP8_OK) return a;
+    if (M == 0) return MXFP8_OK;
+    QParams p{};
+    p.x = static_cast<const uint16_t*>(dh_bf16);
+    p.R = M; p.C = H; p.batch = 1;
+    p.q_row = static_cast<uint8_t*>(dh1_q); p.s_row = static_cast<uint8_t*>(dh1_s);
+    p.q_col = static_cast<uint8_t*>(dh1T_q); p.s_col = static_cast<uint8_t*>(dh1T_s);
+    p.q_row2 = static_cast<uint8_t*>(dh3_q); p.s_row2 = static_cast<uint8_t*>(dh3_s);
+    p.q_col2 = static_cast<uint8_t*>(dh3T_q); p.s_col2 = static_cast<uint8_t*>(dh3T_s);
+    p.blocked = 1;
+    p.offs = offs; p.G = G;
+    p.dev_status = dev_status;
+    p.tiles_r = (M + 127) / 128; p.tiles_c = (H + 127) / 128; p.ntiles = p.tiles_r * p.tiles_c;
+    if (p.ntiles >= INT32_MAX) return MXFP8_ERR_SHAPE;
+    p.x2 = static_cast<const uint16_t*>(h1);
+    p.x3 = static_cast<const uint16_t*>(h3);
+    p.s2 = static_cast<const uint8_t*>(h1_s);
+    p.s3 = static_cast<const uint8_t*>(h3_s);
+    return mxfp8 ? launch_swiglu_bwd<kModeSwiBwd8>(p, st) : launch_swiglu_bwd<kModeSwiBwd>(p, st);
 }
 
 static mxfp8_status_t quantize_2d(const void* x_bf16, int64_t M, int64_t K, unsigned dirs, int scale_layout,
@@ -1505,31 +1581,18 @@ extern "C" mxfp8_status_t mxfp8_swiglu_bwd_quantize(const void* dh_bf16, const v
                                                     void* dh1_q, void* dh1_s, void* dh1T_q, void* dh1T_s, void* dh3_q,
                                                     void* dh3_s, void* dh3T_q, void* dh3T_s, int32_t* dev_status,
                                                     mxfp8_stream_t stream) {
-    if (!dh_bf16 || !h1_bf16 || !h3_bf16 || !offs || !dh1_q || !dh1_s || !dh1T_q || !dh1T_s || !dh3_q || !dh3_s ||
-        !dh3T_q || !dh3T_s)
-        return MXFP8_ERR_NULL;
-    if (M < 0 || H <= 0 || G < 1 || G > MXFP8_MAX_GROUPS || M > INT32_MAX) return MXFP8_ERR_SHAPE;
-    if (H % 32 || M % 32) return MXFP8_ERR_ALIGN;
-    const void* ptrs[] = {dh_bf16, h1_bf16, h3_bf16, dh1_q, dh1_s, dh1T_q, dh1T_s, dh3_q, dh3_s, dh3T_q, dh3T_s};
-    for (const void* q : ptrs)
-        if (!host::aligned16(q)) return MXFP8_ERR_ALIGN;
-    if (mxfp8_status_t a = host::check_arch(); a != MXFP8_OK) return a;
-    if (M == 0) return MXFP8_OK;
-    QParams p{};
-    p.x = static_cast<const uint16_t*>(dh_bf16);
-    p.R = M; p.C = H; p.batch = 1;
-    p.q_row = static_cast<uint8_t*>(dh1_q); p.s_row = static_cast<uint8_t*>(dh1_s);
-    p.q_col = static_cast<uint8_t*>(dh1T_q); p.s_col = static_cast<uint8_t*>(dh1T_s);
-    p.q_row2 = static_cast<uint8_t*>(dh3_q); p.s_row2 = static_cast<uint8_t*>(dh3_s);
-    p.q_col2 = static_cast<uint8_t*>(dh3T_q); p.s_col2 = static_cast<uint8_t*>(dh3T_s);
-    p.blocked = 1;
-    p.offs = offs; p.G = G;
-    p.dev_status = dev_status;
-    p.tiles_r = (M + 127) / 128; p.tiles_c = (H + 127) / 128; p.ntiles = p.tiles_r * p.tiles_c;
-    if (p.ntiles >= INT32_MAX) return MXFP8_ERR_SHAPE;
-    p.x2 = static_cast<const uint16_t*>(h1_bf16);
-    p.x3 = static_cast<const uint16_t*>(h3_bf16);
-    return launch_swiglu_bwd(p, reinterpret_cast<cudaStream_t>(stream));
+    return mx::swiglu_bwd_quantize(dh_bf16, h1_bf16, nullptr, h3_bf16, nullptr, false, M, H, offs, G, dh1_q, dh1_s, dh1T_q,
+                                   dh1T_s, dh3_q, dh3_s, dh3T_q, dh3T_s, dev_status, reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" mxfp8_status_t mxfp8_swiglu_bwd_quantize_mxfp8(const void* dh_bf16, const void* h1_q, const void* h1_s,
+                                                          const void* h3_q, const void* h3_s, int64_t M, int64_t H,
+                                                          const int32_t* offs, int32_t G, void* dh1_q, void* dh1_s,
+                                                          void* dh1T_q, void* dh1T_s, void* dh3_q, void* dh3_s,
+                                                          void* dh3T_q, void* dh3T_s, int32_t* dev_status,
+                                                          mxfp8_stream_t stream) {
+    return mx::swiglu_bwd_quantize(dh_bf16, h1_q, h1_s, h3_q, h3_s, true, M, H, offs, G, dh1_q, dh1_s, dh1T_q, dh1T_s, dh3_q,
+                                   dh3_s, dh3T_q, dh3T_s, dev_status, reinterpret_cast<cudaStream_t>(stream));
 }
 
 extern "C" mxfp8_status_t mxfp4_quantize_2d_mxfp8_cols(const void* x_bf16, int64_t M, int64_t K, const int32_t* offs,

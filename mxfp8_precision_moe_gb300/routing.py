@@ -18,7 +18,7 @@ import torch
 from . import (COL, MAX_GROUPS, ROW, SCALES_BLOCKED, SCALES_COMPACT, _bytes_at_least, _check_quad, _cuda,
                _expert_blocked_bytes, _first_order, _offsets, _status_word, _tensor, _u8, check, load,
                mxfp8_grouped_mm_dgrad, mxfp8_grouped_mm_dgrad2, mxfp8_grouped_mm_fwd, mxfp8_grouped_mm_swiglu_fwd,
-               mxfp8_grouped_mm_wgrad, mxfp8_scale_bytes, mxfp8_scale_bytes_colgroups, mxfp8_swiglu_bwd_quantize,
+               mxfp8_grouped_mm_wgrad, mxfp8_quantize_2d, mxfp8_scale_bytes, mxfp8_scale_bytes_colgroups, mxfp8_swiglu_bwd_quantize,
                quantize_expert_weights)
 from .moe_tokens import MAX_TOP_K, SCORES
 from .mxfp4 import _good, _group_bytes
@@ -414,13 +414,48 @@ def mxfp8_dequantize_2d(q: torch.Tensor, s: torch.Tensor, direction: int = ROW, 
     return out
 
 
+# ---------------------------------------------------------------- activations kept in 8 bits
+def mxfp8_swiglu_bwd_quantize_mxfp8(dh: torch.Tensor, h1, h3, offs: torch.Tensor, dev_status: torch.Tensor | None = None):
+    """``mxfp8_swiglu_bwd_quantize`` with h1 and h3 kept in 8 bits: each (q [M, H], s [M, H/32]) as
+    ``mxfp8_quantize_2d(h, ROW, SCALES_COMPACT)`` gives them.  Returns what that call does for the values they stand for."""
+    _tensor(dh, "dh", torch.bfloat16, 2)
+    M, H = dh.shape
+    if H < 32 or H % 32 or M % 32:
+        raise ValueError(f"dh: multiples of 32 expected, got {tuple(dh.shape)}")
+    for name, h in (("h1", h1), ("h3", h3)):
+        if not isinstance(h, (tuple, list)) or len(h) != 2:
+            raise ValueError(f"{name}: expected (codes, scales)")
+        _tensor(h[0], f"{name} codes", torch.uint8, shape=(M, H))
+        _bytes_at_least(h[1], f"{name} scales", M * (H // 32))
+    _offsets(offs)
+    _status_word(dev_status)
+    _cuda(dh, *h1, *h3, offs, dev_status)
+    G, dev = offs.shape[0], dh.device
+
+    def outs():
+        return (_u8((M, H), dev), _u8(mxfp8_scale_bytes(M, H, G, SCALES_BLOCKED), dev), _u8((H, M), dev),
+                _u8(mxfp8_scale_bytes_colgroups(H, M, G), dev))
+
+    o1, o3 = outs(), outs()
+    check(load().mxfp8_swiglu_bwd_quantize_mxfp8(dh.data_ptr(), *(t.data_ptr() for t in (*h1, *h3)), M, H, offs.data_ptr(), G,
+                                                 *(t.data_ptr() for t in (*o1, *o3)),
+                                                 None if dev_status is None else dev_status.data_ptr(),
+                                                 _raw_stream(dev.index)), "mxfp8_swiglu_bwd_quantize_mxfp8")
+    return o1, o3
+
+
+def _keep_mxfp8(x):
+    """An activation for the backward, in 8 bits: (codes, compact scales)."""
+    return mxfp8_quantize_2d(x, ROW, SCALES_COMPACT)[:2]
+
+
 # ---------------------------------------------------------------- the layer
 class _Mxfp8MoeSwiGLU(torch.autograd.Function):
     """Route, plan, gather + quantize, gate and up with SwiGLU, down, combine.  The backward's rows are quantized the
     same way, straight from dout, and the tokens' gradients are added up from the experts'."""
 
     @staticmethod
-    def forward(ctx, x, logits, Wg, Wu, Wd, bias, route, quads, dev_status):
+    def forward(ctx, x, logits, Wg, Wu, Wd, bias, route, quads, keep8, dev_status):
         need_dx, need_dl, need_dWg, need_dWu, need_dWd = ctx.needs_input_grad[:5]
         front = need_dx or need_dWg or need_dWu
         st = ctx.dev_status = dev_status
@@ -441,9 +476,12 @@ class _Mxfp8MoeSwiGLU(torch.autograd.Function):
                                                                dev_status=st)
         y = mxfp8_grouped_mm_fwd(hq, hs, *qd[:2], plan.offs, dev_status=st)
         ctx.plan, ctx.route = plan, route
-        ctx.save_for_backward(logits if need_dl else None, experts, weights, y if need_dl else None, xTq, xTs,
-                              h1 if front else None, h3 if front else None, hTq, hTs, qg[2], qg[3], qu[2], qu[3], qd[2],
-                              qd[3])
+        # what the backward reads of h1, h3 and y: themselves, or 8 bits of each
+        kept = []
+        for t, needed in ((h1, front), (h3, front), (y, need_dl)):
+            kept += (None, None) if not needed else _keep_mxfp8(t) if keep8 else (t, None)
+        ctx.save_for_backward(logits if need_dl else None, experts, weights, *kept, xTq, xTs, hTq, hTs, qg[2], qg[3], qu[2],
+                              qu[3], qd[2], qd[3])
         return _combine(y, plan, weights)
 
     @staticmethod
@@ -451,8 +489,9 @@ class _Mxfp8MoeSwiGLU(torch.autograd.Function):
     def backward(ctx, dout):
         if ctx.empty is not None:  # no tokens: no gradients
             return tuple(dout.new_zeros(s, dtype=d) if n else None
-                         for (s, d), n in zip(ctx.empty, ctx.needs_input_grad)) + (None,) * 4
-        logits, experts, weights, y, xTq, xTs, h1, h3, hTq, hTs, gTq, gTs, uTq, uTs, dTq, dTs = ctx.saved_tensors
+                         for (s, d), n in zip(ctx.empty, ctx.needs_input_grad)) + (None,) * 5
+        (logits, experts, weights, h1, h1_s, h3, h3_s, y, y_s, xTq, xTs, hTq, hTs, gTq, gTs, uTq, uTs, dTq,
+         dTs) = ctx.saved_tensors
         need_dx, need_dl, need_dWg, need_dWu, need_dWd = ctx.needs_input_grad[:5]
         plan, st = ctx.plan, ctx.dev_status
         offs = plan.offs
@@ -460,6 +499,8 @@ class _Mxfp8MoeSwiGLU(torch.autograd.Function):
         front = need_dx or need_dWg or need_dWu
         dlogits = dx = dWg = dWu = dWd = None
         if need_dl:
+            if y_s is not None:
+                y = mxfp8_dequantize_2d(y, y_s, ROW, SCALES_COMPACT)
             _, dw = _combine_bwd(dout, y, plan, weights, False, True)
             dlogits = _route_bwd(logits, experts, dw, ctx.route)
         if front or need_dWd:
@@ -469,7 +510,10 @@ class _Mxfp8MoeSwiGLU(torch.autograd.Function):
                 dWd = mxfp8_grouped_mm_wgrad(dqT, dsT, hTq, hTs, offs, dev_status=st)
         if front:
             dh = mxfp8_grouped_mm_dgrad(dq, ds, dTq, dTs, offs, dev_status=st)
-            a1, a3 = mxfp8_swiglu_bwd_quantize(dh, h1, h3, offs, dev_status=st)
+            if h1_s is not None:
+                a1, a3 = mxfp8_swiglu_bwd_quantize_mxfp8(dh, (h1, h1_s), (h3, h3_s), offs, dev_status=st)
+            else:
+                a1, a3 = mxfp8_swiglu_bwd_quantize(dh, h1, h3, offs, dev_status=st)
             if need_dx:
                 rows = mxfp8_grouped_mm_dgrad2(a1[0], a1[1], gTq, gTs, a3[0], a3[1], uTq, uTs, offs, dev_status=st)
                 dx = _combine(rows, plan, None)
@@ -477,13 +521,13 @@ class _Mxfp8MoeSwiGLU(torch.autograd.Function):
                 dWg = mxfp8_grouped_mm_wgrad(a1[2], a1[3], xTq, xTs, offs, dev_status=st)
             if need_dWu:
                 dWu = mxfp8_grouped_mm_wgrad(a3[2], a3[3], xTq, xTs, offs, dev_status=st)
-        return dx, dlogits, dWg, dWu, dWd, None, None, None, None
+        return dx, dlogits, dWg, dWu, dWd, None, None, None, None, None
 
 
 def mxfp8_moe_swiglu(x: torch.Tensor, router_logits: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, Wd: torch.Tensor,
                      top_k: int, *, score: str = "softmax", bias: torch.Tensor | None = None, groups: int = 1,
                      top_groups: int | None = None, group_score: str = "top2", renormalize: bool = False,
-                     scale: float = 1.0, w_mxfp8=None, weight_cache=None,
+                     scale: float = 1.0, w_mxfp8=None, weight_cache=None, checkpoint_mxfp8: bool = False,
                      dev_status: torch.Tensor | None = None) -> torch.Tensor:
     """A routed SwiGLU layer for any number of tokens, differentiable in x, the logits and the weights:
 
@@ -494,7 +538,9 @@ def mxfp8_moe_swiglu(x: torch.Tensor, router_logits: torch.Tensor, Wg: torch.Ten
     ``moe_route``, ``moe_plan``, ``moe_gather``, ``mxfp8_swiglu_expert`` and ``moe_combine`` in turn); token rows are
     gathered inside the quantizations, forward and backward.  It does not wait for the device.
 
-    w_mxfp8, weight_cache: as for ``mxfp8_swiglu_expert``.  dev_status: an int32 word (``new_status``) that the kernels
+    w_mxfp8, weight_cache: as for ``mxfp8_swiglu_expert``.  checkpoint_mxfp8: what the backward reads of h1, h3 and the
+    experts' rows is kept in MXFP8 (1.03 bytes a value instead of 2; x and h are in 8 bits either way); outputs stay as they
+    are, gradients are those at the rounded values.  dev_status: an int32 word (``new_status``) that the kernels
     report errors into, to be read with ``read_status``."""
     for name, t, dim in (("x", x, 2), ("Wg", Wg, 3), ("Wu", Wu, 3), ("Wd", Wd, 3)):
         _tensor(t, name, torch.bfloat16, dim)
@@ -522,4 +568,5 @@ def mxfp8_moe_swiglu(x: torch.Tensor, router_logits: torch.Tensor, Wg: torch.Ten
         bias = bias.detach().contiguous()
     if not torch.is_grad_enabled():  # ctx.needs_input_grad asks requires_grad alone, and is set in evaluation too
         x, router_logits, Wg, Wu, Wd = (t.detach() for t in (x, router_logits, Wg, Wu, Wd))
-    return _Mxfp8MoeSwiGLU.apply(x, router_logits, Wg, Wu, Wd, bias, route, quads, dev_status)
+    return _Mxfp8MoeSwiGLU.apply(x, router_logits, Wg, Wu, Wd, bias, route, quads, bool(checkpoint_mxfp8),
+                                 dev_status)

@@ -71,7 +71,7 @@ def test_every_declared_symbol_is_exported():
     mx.load()
     src = re.sub(r"/\*.*?\*/", "", open(os.path.join(ROOT, "include", "mxrouting.h")).read(), flags=re.S)
     names = re.findall(r"^\w[\w\s\*]*?\b(mx\w+)\s*\(", src, flags=re.M)
-    assert len(names) == 11
+    assert len(names) == 12
     raw = ctypes.CDLL(os.path.join(ROOT, "mxfp8_precision_moe_gb300", "libmxfp8moe.so"))
     assert not [n for n in names if not hasattr(raw, n)]
 
@@ -89,6 +89,8 @@ def test_plan_rows():
 
 
 ROUTE = lambda l=None, k=2, **kw: mx.moe_route(torch.zeros(4, 8) if l is None else l, k, **kw)  # noqa: E731
+BACK = lambda dh=bf(64, 64), h1=(u8(64, 64), u8(64, 2)), h3=(u8(64, 64), u8(64, 2)), offs=i32(2): (  # noqa: E731
+    mx.mxfp8_swiglu_bwd_quantize_mxfp8(dh, h1, h3, offs))
 LAYER = lambda x=bf(4, 64), l=torch.zeros(4, 2), g=bf(2, 32, 64), u=bf(2, 32, 64), d=bf(2, 64, 32), k=1, **kw: (  # noqa: E731
     mx.mxfp8_moe_swiglu(x, l, g, u, d, k, **kw))
 
@@ -153,6 +155,14 @@ LAYER = lambda x=bf(4, 64), l=torch.zeros(4, 2), g=bf(2, 32, 64), u=bf(2, 32, 64
     (lambda: mx.mxfp8_dequantize_2d(u8(64, 48), u8(512), mx.COL), "multiples of 32"),
     (lambda: mx.mxfp8_dequantize_2d(u8(64, 64), u8(512), mx.ROW | mx.COL), "direction"),
     (lambda: mx.mxfp8_dequantize_2d(bf(64, 64), u8(512)), "q:"),
+    (lambda: BACK(), "CUDA"),
+    (lambda: BACK(dh=bf(64, 48)), "multiples of 32"),
+    (lambda: BACK(dh=bf(48, 64)), "multiples of 32"),
+    (lambda: BACK(dh=bf(64, 64).float()), "dh"),
+    (lambda: BACK(h1=u8(64, 64)), "h1"),
+    (lambda: BACK(h1=(u8(64, 32), u8(64, 2))), "h1 codes"),
+    (lambda: BACK(h3=(u8(64, 64), u8(127))), "h3 scales"),
+    (lambda: BACK(offs=i32(2).long()), "offs"),
     (lambda: LAYER(), "CUDA"),
     (lambda: LAYER(l=torch.zeros(4, 3)), "router_logits"),
     (lambda: LAYER(x=bf(4, 32)), "shapes"),
@@ -199,6 +209,9 @@ DEVICE_CALLS = {
         fake((4, 64), torch.bfloat16, i), fplan(i), weights=fake((4, 2), torch.float32, j)),
     "mxfp4_gather_quantize": lambda i, j: mx.mxfp4_gather_quantize(fake((4, 64), torch.bfloat16, i), fplan(j)),
     "mxfp8_dequantize_2d": lambda i, j: mx.mxfp8_dequantize_2d(fake((64, 64), torch.uint8, i), fake((512,), torch.uint8, j)),
+    "mxfp8_swiglu_bwd_quantize_mxfp8": lambda i, j: mx.mxfp8_swiglu_bwd_quantize_mxfp8(
+        fake((64, 64), torch.bfloat16, i), (fake((64, 64), torch.uint8, i), fake((64, 2), torch.uint8, i)),
+        (fake((64, 64), torch.uint8, i), fake((64, 2), torch.uint8, j)), fake((2,), torch.int32, i)),
     "mxfp8_moe_swiglu": lambda i, j: mx.mxfp8_moe_swiglu(
         fake((4, 64), torch.bfloat16, i), fake((4, 2), torch.float32, i), fake((2, 32, 64), torch.bfloat16, i),
         fake((2, 32, 64), torch.bfloat16, j), fake((2, 64, 32), torch.bfloat16, i), 1),
@@ -277,6 +290,12 @@ def test_refusals_of_the_c_abi():
         L.mxfp4_gather_quantize(x, slot, place, rows, T, k, D, offs, G, q, s, None))
     assert f(T=-1) == 2 and f(k=17) == 2 and f(slot=None) == 1 and f(offs=None) == 1 and f(D=48) == 3 and f(G=0) == 2
     assert f(place=None) == 1 and f(q=None) == 1 and f(x=odd) == 3 and f(slot=half) == 3 and f(rows=0, q=None) == 0
+    o = [a] * 8
+    w = lambda dh=a, h1=a, s1=a, h3=a, s3=a, M=64, H=64, offs=a, G=2, outs=o: (  # noqa: E731
+        L.mxfp8_swiglu_bwd_quantize_mxfp8(dh, h1, s1, h3, s3, M, H, offs, G, *outs, None, None))
+    assert w(dh=None) == 1 and w(s1=None) == 1 and w(s3=None) == 1 and w(offs=None) == 1 and w(outs=o[:7] + [None]) == 1
+    assert w(M=-1) == 2 and w(H=0) == 2 and w(G=0) == 2 and w(M=40) == 3 and w(H=48) == 3 and w(h1=odd) == 3 and w(s3=odd) == 3
+    assert w(outs=o[:7] + [odd]) == 3
     d = lambda q=a, s=a, M=64, K=64, dir=1, layout=1, offs=None, G=0, out=a: (  # noqa: E731
         L.mxfp8_dequantize(q, s, M, K, dir, layout, offs, G, out, None))
     assert d(M=-1) == 2 and d(K=0) == 2 and d(offs=a) == 2 and d(dir=3) == 4 and d(layout=2) == 4 and d(K=48) == 3
