@@ -3,7 +3,7 @@
 //
 // By token: a token's row is read and quantized once, and its codes and scales go to each of its top_k rows.  Going by the
 // plan's rows, x is read and quantized top_k times: 8 rows a token of 8192 x 7168, MXFP4 153 us, MXFP8 206 us; by token
-// 85 and 140, against 55 and 94 us for the bytes at the copy rate.  Codes go out by whole rows; the scales, whose layout
+// 79 and 127, against 55 and 94 us for the bytes at the copy rate.  Codes go out by whole rows; the scales, whose layout
 // keeps a row's 512 bytes apart, by 4-byte words of 128 columns, which L2 joins (14 and 17 us of the time).  Five CTAs an SM;
 // four are up to 10% slower where a token has one row, six 3% where it has eight.
 
@@ -146,7 +146,9 @@ __global__ void __launch_bounds__(kGatherWarps * 32, 5) gather_quantize_kernel(c
 template <int BITS>
 static mxfp8_status_t run_gather_quantize(GatherParams& p, cudaStream_t st) {
     constexpr int EPT = BITS == 4 ? 32 : 16;
-    const int64_t chunks = (p.C + 32 * EPT - 1) / (32 * EPT), ctas = (int64_t)host::num_sms() * 5;
+    // Where a token has several rows, more CTAs than the five that fit on an SM, and more warps on a token, even the ends out:
+    // 8 rows a token of 8192 x 7168 MXFP4 84 -> 79 us, MXFP8 141 -> 127; with one row a token of 16384 x 5120 48 -> 50.
+    const int64_t chunks = (p.C + 32 * EPT - 1) / (32 * EPT), ctas = (int64_t)host::num_sms() * 5 * (p.k < 4 ? p.k : 4);
     // a warp takes a whole token, for which it looks its rows up once; of few tokens, several share one
     p.parts = (int32_t)max64(1, min64(chunks, (ctas * kGatherWarps + p.T - 1) / max64(p.T, 1)));
     p.token_items = p.T * p.parts;

@@ -1374,7 +1374,7 @@ struct DqParams {
 
 // A warp takes 16 rows of a 128 x 128 tile, two at a time, a lane 8 neighbouring values (a quarter of a block): stores of
 // whole sectors by neighbouring lanes (with 16 values a lane, two 16-byte stores 32 bytes apart, 57 us for 16384 x 5120
-// instead of 47).  Bound by memory: 1.03 bytes read and 2 written an element.
+// instead of 47, now 43).  Bound by memory: 1.03 bytes read and 2 written an element.
 template <bool kCol>
 __global__ void __launch_bounds__(256) mxfp8_dequantize_kernel(const DqParams p) {
     __shared__ int32_t ends_s[kMaxGroups];
@@ -1681,7 +1681,9 @@ extern "C" mxfp8_status_t mxfp8_dequantize(const void* q, const void* s, int64_t
     if (tr * tc >= INT32_MAX) return MXFP8_ERR_SHAPE;
     p.tiles_r = (uint32_t)tr;
     p.tiles_c = (uint32_t)tc;
-    const unsigned grid = (unsigned)std::min<int64_t>(tr * tc, (int64_t)host::num_sms() * 6);
+    // more CTAs than fit at a time (four an SM) even their ends out: 16384 x 5120 43 us, 70 thousand x 7168 236 us; 47 and
+    // 259 with four or six, 46 and 276 with a CTA a tile, as each works the groups out
+    const unsigned grid = (unsigned)std::min<int64_t>(tr * tc, (int64_t)host::num_sms() * 32);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (col) mxfp8_dequantize_kernel<true><<<grid, 256, 0, st>>>(p);
     else mxfp8_dequantize_kernel<false><<<grid, 256, 0, st>>>(p);

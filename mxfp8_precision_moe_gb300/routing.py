@@ -18,8 +18,8 @@ import torch
 from . import (COL, MAX_GROUPS, ROW, SCALES_BLOCKED, SCALES_COMPACT, _bytes_at_least, _check_quad, _cuda,
                _expert_blocked_bytes, _first_order, _offsets, _status_word, _tensor, _u8, check, load,
                mxfp8_grouped_mm_dgrad, mxfp8_grouped_mm_dgrad2, mxfp8_grouped_mm_fwd, mxfp8_grouped_mm_swiglu_fwd,
-               mxfp8_grouped_mm_wgrad, mxfp8_quantize_2d, mxfp8_scale_bytes, mxfp8_scale_bytes_colgroups, mxfp8_swiglu_bwd_quantize,
-               quantize_expert_weights)
+               mxfp8_grouped_mm_wgrad, mxfp8_quantize_2d, mxfp8_scale_bytes, mxfp8_scale_bytes_colgroups,
+               mxfp8_swiglu_bwd_quantize, quantize_expert_weights)
 from .moe_tokens import MAX_TOP_K, SCORES
 from .mxfp4 import _good, _group_bytes
 
@@ -378,7 +378,8 @@ def mxfp4_gather_quantize(x: torch.Tensor, plan: MoePlan):
     (T, D), M, G, dev = x.shape, plan.rows, plan.offs.shape[0], x.device
     q, s = _u8((M, D // 2), dev), _u8(_group_bytes(M, D, G), dev)
     check(load().mxfp4_gather_quantize(x.data_ptr(), plan.slot.data_ptr(), plan.place.data_ptr(), M, T, plan.top_k, D,
-                                       plan.offs.data_ptr(), G, q.data_ptr(), s.data_ptr(), _raw_stream(dev.index)), "mxfp4_gather_quantize")
+                                       plan.offs.data_ptr(), G, q.data_ptr(), s.data_ptr(), _raw_stream(dev.index)),
+          "mxfp4_gather_quantize")
     return q, s
 
 
