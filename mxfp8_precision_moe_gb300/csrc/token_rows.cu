@@ -220,9 +220,10 @@ static mxfp8_status_t rows_check(RowsParams& p, int64_t rows, int64_t T, int32_t
 static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 static int64_t padding_ctas(const RowsParams& p) { return (p.rows + kRowsThreads - 1) / kRowsThreads; }
 
-// Warps for each token, of which one takes `width` pieces at a time: as many as fill the GPU twice, or one for each width.
-static uint32_t parts_of(const RowsParams& p, int width) {
-    const int64_t widths = (p.C + width - 1) / width, want = (int64_t)host::num_sms() * 128;
+// Warps for each token, of which one takes `width` pieces at a time: as many as fill the GPU twice (`times` over), or one
+// for each width.
+static uint32_t parts_of(const RowsParams& p, int width, int times) {
+    const int64_t widths = (p.C + width - 1) / width, want = (int64_t)host::num_sms() * 128 * times;
     return (uint32_t)max64(1, min64(widths, (want + p.T - 1) / max64(p.T, 1)));
 }
 static int64_t token_ctas(const RowsParams& p) {
@@ -232,7 +233,9 @@ static int64_t token_ctas(const RowsParams& p) {
 
 static mxfp8_status_t run_gather(RowsParams& p, cudaStream_t st) {
     if (p.rows == 0) return MXFP8_OK;
-    p.parts = parts_of(p, 32 * kGatherPieces);
+    // a token with several rows is many writes: 4 rows of 5120 each, 16384 tokens, 127 us by short warps, 131 by long ones;
+    // one row 55 and 53
+    p.parts = parts_of(p, 32 * kGatherPieces, p.k < 4 ? p.k * p.k : 16);
     p.token_ctas = (uint32_t)token_ctas(p);
     const unsigned grid = (unsigned)(p.token_ctas + padding_ctas(p));
     if (p.w) gather_rows_kernel<true><<<grid, kRowsThreads, 0, st>>>(p);
@@ -242,7 +245,7 @@ static mxfp8_status_t run_gather(RowsParams& p, cudaStream_t st) {
 
 template <int KB, int U>
 static void run_combine(RowsParams& p, cudaStream_t st) {
-    p.parts = parts_of(p, 32 * U);
+    p.parts = parts_of(p, 32 * U, 1);
     combine_kernel<KB, U><<<(unsigned)token_ctas(p), kRowsThreads, 0, st>>>(p);
 }
 
