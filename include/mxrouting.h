@@ -21,8 +21,8 @@ extern "C" {
  * mx_moe_route -- the experts of each token and their weights.
  *   logits [T, E] of `logits_type`; bias [E] fp32 or NULL.
  *   key_te = score(l_te) + bias_e, score as MX_SCORE_*: the logit itself
- *   (MX_SCORE_SOFTMAX), softmax over all experts or 1 / (1 + e^-l).  Without a bias,
- *   and where groups are not ranked by a sum, the logits are ranked themselves, which
+ *   (MX_SCORE_SOFTMAX), softmax over all experts or 1 / (1 + e^-l).  Without a bias, and
+ *   with one that is the same finite value for all, experts rank by their logits, which
  *   order as their scores do.
  *   groups > 1: expert e is of group e / (E / groups); a group is worth the sum of its
  *   two largest keys (MX_GROUP_TOP2) or its largest (MX_GROUP_MAX), and only the

@@ -83,23 +83,23 @@ __device__ __forceinline__ F warp_sum(F v) {
     return v;
 }
 
-// What a group is worth (lane g: group g, from the keys' integers in shared memory), and which groups stay: bit g.
-// The two largest are kept as integers, so that a NaN counts.
+// The two largest of group `lane` among the integers in shared memory (kept as integers, so that a NaN counts).
 template <typename O>
-__device__ __forceinline__ uint32_t best_groups(const O* keys, const RouteParams& p, int lane, O& worth) {
+__device__ __forceinline__ void group_top2(const O* keys, const RouteParams& p, int lane, O& top, O& second) {
     const int size = p.group_size;
-    O top = 0, second = 0;
-    if (lane < p.groups) {
-        int at = lane % size;  // lanes start apart, so that they do not meet in a bank
-        for (int i = 0; i < size; ++i) {
-            const O v = keys[lane * size + at];
-            if (++at == size) at = 0;
-            second = max(second, min(top, v));
-            top = max(top, v);
-        }
+    top = second = 0;
+    if (lane >= p.groups) return;
+    int at = lane % size;  // lanes start apart, so that they do not meet in a bank
+    for (int i = 0; i < size; ++i) {
+        const O v = keys[lane * size + at];
+        if (++at == size) at = 0;
+        second = max(second, min(top, v));
+        top = max(top, v);
     }
-    worth = top;
-    if (!p.group_max && second) worth = order_of(value_of(top) + value_of(second));
+}
+// Which groups stay, where lane g holds what group g is worth: bit g.
+template <typename O>
+__device__ __forceinline__ uint32_t best_groups(O worth, const RouteParams& p, int lane) {
     int rank = 0;
     for (int g = 0; g < p.groups; ++g) {
         const O other = __shfl_sync(kFull, worth, g);
@@ -117,25 +117,38 @@ __device__ __forceinline__ void softmax_64(const RouteParams& p, int64_t t, int 
     for (int e = lane; e < p.E; e += 32) sum += exp((double)logit_at(p, t, e) - top);
     sum = warp_sum(sum);
 }
+__device__ __forceinline__ double score_64(const RouteParams& p, double l, double top, double sum) {
+    if (p.score == MX_SCORE_SOFTMAX_ALL) return exp(l - top) / sum;
+    if (p.score == MX_SCORE_SIGMOID) return 1.0 / (1.0 + exp(-l));
+    return l;
+}
 // The integer that orders as expert e's key does, from 64 bits; 0: not to be selected.
 __device__ __forceinline__ unsigned long long key_64(const RouteParams& p, int64_t t, int e, double top, double sum) {
-    const float l = logit_at(p, t, e), b = p.bias ? p.bias[e] : 0.0f;
-    double s = l;
-    if (p.score == MX_SCORE_SOFTMAX_ALL) s = exp(s - top) / sum;
-    else if (p.score == MX_SCORE_SIGMOID) s = 1.0 / (1.0 + exp(-s));
-    const double key = p.bias ? s + (double)b : s;
+    const float l = logit_at(p, t, e);
+    const double key = score_64(p, l, top, sum) + (double)p.bias[e];
     return l == -INFINITY || key == -INFINITY ? 0ull : order_of(key);
 }
 
-// The selection in 64 bits, for a token whose order 32 bits leave open.  Lane j returns the j-th expert, -1: none.
-__device__ __noinline__ int select_64(const RouteParams& p, int64_t t, unsigned long long* keys, int lane) {
+// The selection in 64 bits, for a token whose order 32 bits leave open.  by_logits: the experts rank by their logits.  Lane
+// j returns the j-th expert, -1: none.
+__device__ __noinline__ int select_64(const RouteParams& p, int64_t t, bool by_logits, unsigned long long* keys, int lane) {
     double top = 0.0, sum = 1.0;
     if (p.score == MX_SCORE_SOFTMAX_ALL) softmax_64(p, t, lane, top, sum);
-    for (int e = lane; e < p.E; e += 32) keys[e] = key_64(p, t, e, top, sum);
+    for (int e = lane; e < p.E; e += 32) {
+        const float l = logit_at(p, t, e);
+        keys[e] = !by_logits ? key_64(p, t, e, top, sum) : l == -INFINITY ? 0ull : order_of((double)l);
+    }
     __syncwarp();
     if (p.groups > 1) {
-        unsigned long long worth;
-        const uint32_t stay = best_groups(keys, p, lane, worth);
+        unsigned long long first, second, worth;
+        group_top2(keys, p, lane, first, second);
+        worth = first;
+        if (!p.group_max && first) {
+            double v = by_logits ? score_64(p, value_of(first), top, sum) : value_of(first);
+            if (second) v += by_logits ? score_64(p, value_of(second), top, sum) : value_of(second);
+            worth = order_of(v);
+        }
+        const uint32_t stay = best_groups(worth, p, lane);
         for (int e = lane; e < p.E; e += 32)
             if (!(stay >> (e / p.group_size) & 1u)) keys[e] = 0ull;
         __syncwarp();
@@ -219,8 +232,24 @@ __device__ __forceinline__ void load_logits(const RouteParams& p, int64_t t, int
     }
 }
 
-// Keys: the logits themselves (exact), logit + bias, or a score (+ bias).
+// Keys: the logits themselves (exact), logit + bias, or a score + bias.  Without a bias, and with one that is the same for
+// all, experts rank by their logits, which order as their scores do; then a score is only needed of a group's two best.
 enum RouteKeys : int { kKeysLogits = 0, kKeysBias = 1, kKeysSigmoid = 2, kKeysSoftmax = 3 };
+
+__device__ __forceinline__ float sigmoid_approx(float l) { return rcp_approx(1.0f + exp2_approx(l * -1.4426950408889634f)); }
+
+// How far a score s computed in 32 bits may be off, in units of 2^-24:
+//   sigmoid_approx  e^-l: its exponent is a product with a rounded constant (1.5 |l|, times e^-l / (1 + e^-l), so that it only
+//                   counts below 0), its value good to 2 ulp (4); the sum 1; the reciprocal 2 (1 ulp): s (7 + 1.5 max(0, -l)),
+//                   at most s (7 + 1.5 ln(1/s)), which grows with s
+//   softmax         the exponent's difference d, which is rounded, here and (7, the entropy, at most) in the sum; two expf of
+//                   4; 5 + VPL sums; the quotient: s (d + 21 + VPL), where s <= e^-d
+// and what subnormals lose.  `at` is l or d.
+template <int KEYS, int VPL>
+__device__ __forceinline__ float score_error(float s, float at) {
+    const float units = KEYS == kKeysSigmoid ? 9.0f + 1.5f * fminf(fmaxf(-at, 0.0f), 128.0f) : 24.0f + VPL + fminf(at, 200.0f);
+    return s * units * 0x1p-24f + 0x1p-125f;
+}
 
 // The same where the groups are settled and the experts that come into question are few: lane i's is e, -1: none.
 __device__ __noinline__ int select_64_among(const RouteParams& p, int64_t t, int e, int total, uint2* shared, int lane) {
@@ -251,10 +280,11 @@ __device__ __noinline__ int select_64_among(const RouteParams& p, int64_t t, int
 // least, so that the exact largest are there), one a lane, or, where the groups are in doubt, from the start.  The keys can
 // then be made of the approximate exponential and reciprocal; weights are not.
 //
-// Bound by its instructions: 32768 tokens, 8 of 256 experts in 8 groups, 34.1 us (10 for the bytes of this and the
-// backward, which takes 9.6); about a dozen of those tokens are done again.
+// Bound by its instructions: 32768 tokens, 8 of 256 experts in 8 groups, 34.7 us (10 for the bytes of this and the
+// backward, which takes 9.6); about a dozen of those tokens are done again.  Registers for 11 CTAs an SM (10 where a lane has
+// two experts at most, which is bound by latency): 36.4 us with as many as the compiler likes.
 template <int VPL, int KEYS>
-__global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteParams p) {
+__global__ void __launch_bounds__(kRouteWarps * 32, VPL <= 2 ? 10 : VPL <= 8 ? 11 : 1) route_kernel(const RouteParams p) {
     extern __shared__ unsigned long long route_smem[];
     constexpr bool kCandidates = VPL > 2;
     __shared__ __align__(8) uint2 candidates[kCandidates ? kRouteWarps : 1][32];  // ~expert, key: as 64 bits the order
@@ -282,50 +312,54 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RoutePara
 
     uint32_t ord[VPL];
     float err = 0.0f;  // of a key at most
-    if constexpr (KEYS == kKeysLogits) {
+    bool by_logits = KEYS == kKeysLogits || p.bias == nullptr;
+    float b[KEYS == kKeysLogits ? 1 : VPL];
+    if constexpr (KEYS != kKeysLogits) {
+        if (p.bias != nullptr) {
+            load_row<float, VPL>(p.bias, p.bias, p.E, lane, 0.0f, b);
+            const float first = __shfl_sync(kFull, b[0], 0);
+            bool same = fabsf(first) < INFINITY;
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) same = same && (b[i] == first || lane * VPL + i >= p.E);
+            by_logits = __all_sync(kFull, same);
+        }
+    }
+    if (by_logits) {
 #pragma unroll
         for (int i = 0; i < VPL; ++i) ord[i] = l[i] == -INFINITY ? 0u : order_of(l[i]);
-    } else {
-        float b[VPL], top = -INFINITY, largest = 0.0f;  // the largest logit, the largest |key|
-        if (p.bias != nullptr) load_row<float, VPL>(p.bias, p.bias, p.E, lane, 0.0f, b);
+    } else if constexpr (KEYS != kKeysLogits) {
+        float top = -INFINITY, largest = 0.0f;  // the largest logit, the largest |key|
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
             float key = l[i];
             if constexpr (KEYS == kKeysSigmoid) {
                 top = fmaxf(top, key);
-                key = rcp_approx(1.0f + exp2_approx(key * -1.4426950408889634f));
+                key = sigmoid_approx(key);
             } else if constexpr (KEYS == kKeysSoftmax) {
                 key = expf(l[i] - m) / sum;
             }
-            if (p.bias != nullptr) {
-                key += b[i];
-                if (key != -INFINITY) largest = fmaxf(largest, fabsf(key));
-            }
+            key += b[i];
+            if (key != -INFINITY) largest = fmaxf(largest, fabsf(key));
             ord[i] = l[i] == -INFINITY || key == -INFINITY ? 0u : order_of(key);
         }
-        // Bounds in units of 2^-24.
+        // (bounds: score_error, at the largest score, as they grow with it)
         if constexpr (KEYS == kKeysSigmoid) {
-            // Of a score s: e^-l's exponent is a product with a rounded constant (1.5 |l|, times e^-l / (1 + e^-l)), its
-            // value good to 2 ulp (4); the sum 1; the reciprocal 2 (1 ulp): at most s (7 + 1.5 ln(1/s)), which grows with
-            // s, so that the largest score's holds for all.  (ln(1/s) <= |l| + ln 2.)
             top = value_of(__reduce_max_sync(kFull, order_of(top)));
-            const float s = rcp_approx(1.0f + exp2_approx(top * -1.4426950408889634f)) * 1.001f;
-            err = s * (9 + 1.5f * (top < 0.0f ? fminf(-top, 128.0f) : 0.0f)) * kUlp + 0x1p-125f;
+            err = score_error<KEYS, VPL>(sigmoid_approx(top) * 1.001f, fminf(top, 0.0f));
         } else if constexpr (KEYS == kKeysSoftmax) {
-            // Of a score p: the exponent's difference d, which is rounded, here and (7, the entropy, at most) in the sum;
-            // two expf of 4; 5 + VPL sums; the quotient: p (d + 21 + VPL), where p <= e^-d and d e^-d < 1
-            err = (26 + VPL) * kUlp * fminf(1.001f / sum, 1.0f) + kUlp + 0x1p-125f;
+            err = score_error<KEYS, VPL>(fminf(1.001f / sum, 1.0f), 1.0f);  // d e^-d < 1
         }
-        if (p.bias != nullptr) err += kUlp * __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(largest)));
+        err += kUlp * __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(largest)));
     }
     bool doubt = false;
 
     if (p.groups > 1) {
         const int size = p.group_size, lanes = p.group_lanes;
-        uint32_t low, high;  // the least worth that stays, the best that goes
+        uint32_t top, second;  // of a group: every of its lanes, or lane g
         if (lanes) {
             // a group is a power of two of neighbouring lanes: its two largest by exchanges between them
-            uint32_t top = ord[0], second = 0u;
+            top = ord[0];
+            second = 0u;
 #pragma unroll
             for (int i = 1; i < VPL; ++i) {
                 second = max(second, min(top, ord[i]));
@@ -336,7 +370,34 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RoutePara
                 second = max(min(top, t2), max(second, s2));
                 top = max(top, t2);
             }
-            const uint32_t worth = p.group_max || !second ? top : order_of(value_of(top) + value_of(second));
+        } else {
+            uint32_t* k32 = reinterpret_cast<uint32_t*>(keys);
+#pragma unroll
+            for (int i = 0; i < VPL; ++i)
+                if (lane * VPL + i < p.E) k32[lane * VPL + i] = ord[i];
+            __syncwarp();
+            group_top2(k32, p, lane, top, second);
+            __syncwarp();
+        }
+        // what the group is worth, and how far that may be off
+        uint32_t worth = top;
+        float off = 2 * err;
+        if (!p.group_max && top) {
+            float v = value_of(top), w = second ? value_of(second) : 0.0f;
+            if (KEYS >= kKeysSigmoid && by_logits) {
+                const float lv = v, lw = w;
+                v = KEYS == kKeysSigmoid ? sigmoid_approx(lv) : expf(lv - m) / sum;
+                w = !second ? 0.0f : KEYS == kKeysSigmoid ? sigmoid_approx(lw) : expf(lw - m) / sum;
+                off = score_error<KEYS, VPL>(v, KEYS == kKeysSigmoid ? lv : m - lv) +
+                      score_error<KEYS, VPL>(w, KEYS == kKeysSigmoid ? lw : m - lw);
+            }
+            if (second) v += w;
+            off += kUlp * fabsf(v);
+            worth = order_of(v);
+        }
+        uint32_t low, high;  // the least worth that stays, the best that goes
+        bool stay;
+        if (lanes) {
             // the best groups leave one by one, of equal ones the first (lanes past the last group hold nothing: 0)
             uint32_t left = worth;
             low = 0xffffffffu;
@@ -348,30 +409,32 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RoutePara
                 if (((lane ^ src) & -lanes) == 0) left = 0u;  // of the same group
             }
             high = __reduce_max_sync(kFull, left);
-            const bool stay = left == 0u;
+            stay = left == 0u;
             if (!stay) {
 #pragma unroll
                 for (int i = 0; i < VPL; ++i) ord[i] = 0u;
             }
         } else {
-            uint32_t* k32 = reinterpret_cast<uint32_t*>(keys);
+            const uint32_t mask = best_groups(worth, p, lane);
+            stay = mask >> lane & 1u;
+            low = __reduce_min_sync(kFull, stay ? worth : 0xffffffffu);
+            high = __reduce_max_sync(kFull, stay ? 0u : worth);
 #pragma unroll
             for (int i = 0; i < VPL; ++i)
-                if (lane * VPL + i < p.E) k32[lane * VPL + i] = ord[i];
-            __syncwarp();
-            uint32_t worth;
-            const uint32_t stay = best_groups(k32, p, lane, worth);
-            low = __reduce_min_sync(kFull, (stay >> lane & 1u) ? worth : 0xffffffffu);
-            high = __reduce_max_sync(kFull, (stay >> lane & 1u) || lane >= p.groups ? 0u : worth);
-#pragma unroll
-            for (int i = 0; i < VPL; ++i)
-                if (!(stay >> (min(lane * VPL + i, p.E - 1) / size) & 1u)) ord[i] = 0u;
-            __syncwarp();
+                if (!(mask >> (min(lane * VPL + i, p.E - 1) / size) & 1u)) ord[i] = 0u;
         }
-        if (high && (KEYS != kKeysLogits || !p.group_max)) {
-            // each sum of two keys off by twice a key's error, and rounded
-            const float a = value_of(low), b = value_of(high);
-            doubt = !(a - b > 4 * err + 2 * kUlp * (fabsf(a) + fabsf(b)));
+        if (high && !(by_logits && p.group_max)) {
+            // groups on both sides of the cut that are no further apart than their bounds are told apart in 64 bits, but
+            // where all of them have the same two logits: they tie, and lie in order
+            const float a = value_of(low), c = value_of(high), v = value_of(worth);
+            off = 2 * __uint_as_float(__reduce_max_sync(kFull, worth ? __float_as_uint(off) : 0u));
+            if (!(a - c > off)) {
+                const bool near = worth && !(stay ? v - c > off : a - v > off);
+                const bool ties = by_logits &&
+                                  __reduce_max_sync(kFull, near ? top : 0u) == __reduce_min_sync(kFull, near ? top : ~0u) &&
+                                  __reduce_max_sync(kFull, near ? second : 0u) == __reduce_min_sync(kFull, near ? second : ~0u);
+                doubt = !ties;
+            }
         }
     }
 
@@ -465,7 +528,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RoutePara
             }
         }
     }
-    if (doubt) mine = select_64(p, t, keys, lane);
+    if (doubt) mine = select_64(p, t, by_logits, keys, lane);
 
     const bool in = lane < p.top_k && mine >= 0;
     const float w = weight_of(p, in, in ? logit_at(p, t, mine) : 0.0f, m, sum);

@@ -126,8 +126,9 @@ def moe_route(logits: torch.Tensor, top_k: int, *, score: str = "softmax", bias:
     """The experts of each token and their weights: logits [T, E] (fp32, bf16 or fp16) -> (experts [T, top_k] int32,
     weights [T, top_k] fp32), the weights differentiable in the logits.  E <= 1024, top_k <= 16.
 
-    Experts are ranked by score(logit) + bias, largest first; equal ones by their index, NaN above everything; an
-    expert whose logit or bias is -inf is never selected.  A token that has fewer than top_k experts to select gets
+    Experts are ranked by score(logit) + bias (without a bias, or with the same one for all, by the logits, which order as
+    their scores do), largest first; equal ones by their index, NaN above everything; an expert whose logit or bias is -inf is
+    never selected.  A token that has fewer than top_k experts to select gets
     -1 with weight 0 in the places left.
 
     score: "softmax" (the ranking takes the logits, the weights are a softmax over the selected), "softmax_all" (over all

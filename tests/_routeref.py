@@ -28,24 +28,28 @@ def softmax(v):
 def select(l, k, score, bias=None, groups=1, top_groups=None, group_score="top2"):
     """The experts of one token with logits l (floats)."""
     E = len(l)
-    key = [float(x) for x in l]
-    if bias is not None or (groups > 1 and group_score == "top2"):
-        if score == "sigmoid":
-            key = [sigmoid(x) for x in key]
-        elif score == "softmax_all":
-            live = [x for x in key if x != -math.inf]
-            p = softmax(live) if live else []
-            it = iter(p)
-            key = [next(it) if x != -math.inf else 0.0 for x in key]
-        if bias is not None:
-            key = [x + float(b) for x, b in zip(key, bias)]
+    scores = [float(x) for x in l]
+    if score == "sigmoid":
+        scores = [sigmoid(x) for x in scores]
+    elif score == "softmax_all":
+        live = [x for x in scores if x != -math.inf]
+        p = softmax(live) if live else []
+        it = iter(p)
+        scores = [next(it) if x != -math.inf else 0.0 for x in scores]
+    # without a bias, and with one that is the same for all, the order is the logits'
+    same = bias is None or (len(set(float(b) for b in bias)) == 1 and math.isfinite(float(bias[0])))
+    key = [float(x) for x in l] if same else [x + float(b) for x, b in zip(scores, bias)]
     key = [-math.inf if x == -math.inf else v for x, v in zip(l, key)]
+    value = [float(x) for x in (scores if same else key)]  # what a group's sum is of
     if groups > 1:
         n = E // groups
         worth = []
         for g in range(groups):
             part = key[g * n:(g + 1) * n]
-            best = [part[i] for i in rank(part, 1 if group_score == "max" else 2)]
+            if group_score == "max":
+                best = [part[i] for i in rank(part, 1)]
+            else:
+                best = [value[g * n + i] for i in rank(part, 2)]
             worth.append(sum(best) if best else -math.inf)
         stay = rank(worth, top_groups)
         key = [v if i // n in stay else -math.inf for i, v in enumerate(key)]

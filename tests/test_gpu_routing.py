@@ -131,11 +131,10 @@ def test_masked_and_special_logits(kw, groups):
     dw = torch.linspace(-1, 1, 30, device="cuda").view(10, 3)
     check(l[finite], 3, dw[finite], **kw, **top)
     check(l[~finite & ~(l == inf).any(1)], 3, **kw, **top)
-    # an infinite logit: first (of softmax over all every score is NaN then, and where scores are ranked, the lowest
-    # indices are), and no finite weight can be told for it but of a sigmoid
+    # an infinite logit (of softmax over all every score is NaN then, and so is every group's sum): no finite weight can be
+    # told for it but of a sigmoid
     e, w = mx.moe_route(l[7:8], 3, **kw, **top)
     assert e[0].tolist() == ref.select(l[7].tolist(), 3, kw["score"], groups=groups, top_groups=3)
-    assert e[0, 0] == (0 if kw["score"] == "softmax_all" and groups > 1 else 1)
     assert kw["score"] == "sigmoid" or w[0].isnan().any()
 
 
@@ -149,6 +148,20 @@ def test_a_bias_of_minus_infinity_masks_an_expert():
         assert (e[:, 0] == 5).all() and not torch.isin(e, torch.tensor([0, 3, 11], device="cuda")).any()
         e, w = mx.moe_route(l, 10, score=score, bias=bias)
         assert (e[:, 9] == -1).all() and (w[:, 9] == 0).all() and (e[:, :9] >= 0).all()
+
+
+@pytest.mark.parametrize("E,groups,top_groups,k", [(64, 8, 3, 8), (100, 5, 2, 7), (256, 8, 4, 8), (48, 16, 5, 4)])
+@pytest.mark.parametrize("score", ["softmax", "softmax_all", "sigmoid"])
+@pytest.mark.parametrize("bias", [None, 0.0, 0.375])
+def test_coarse_logits_tie(E, groups, top_groups, k, score, bias):
+    """Logits of few values, as bf16 gives them: experts tie, and groups with the same two best; scores too, which only the
+    logits tell apart (a sigmoid of 40 and more is 1 in any precision)."""
+    b = None if bias is None else torch.full((E,), bias, device="cuda")
+    for seed, l in enumerate((logits_of(40, E, torch.bfloat16, 5, 2.0), logits_of(40, E, torch.float32, 6, 1.0).mul(2).round(),
+                              logits_of(40, E, torch.float32, 7, 1.0).round() + 40.0,
+                              logits_of(40, E, torch.float32, 8, 1.0).mul(4).round().div(4) - 30.0)):
+        check(l, k, bias=b, score=score, groups=groups, top_groups=top_groups)
+        check(l, k, bias=b, score=score)
 
 
 @pytest.mark.parametrize("E", [12, 60, 100, 256, 1024])
