@@ -74,8 +74,9 @@ mxfp8_status_t mx_moe_plan(const void* experts, int32_t index_bytes, int64_t T, 
                            void* workspace, size_t workspace_bytes, mxfp8_stream_t stream);
 
 /* ----------------------------------------------------------------------------
- * Rows.  slot [rows] and place [T, top_k] as mx_moe_plan writes them; entries out of
- * range are taken as -1.  D % 8 == 0; matrices 16-byte aligned.
+ * Rows.  slot [rows] and place [T, top_k] as mx_moe_plan writes them: place[t, j] = r where
+ * slot[r] = t * top_k + j, and only there (kernels read the one or the other); entries out
+ * of range are taken as -1.  D % 8 == 0; matrices 16-byte aligned.
  * mx_moe_gather -- out[r] = x[slot[r] / top_k], 0 where slot[r] is -1; bf16.
  * mx_moe_combine -- out[t] = sum over j of w[t, j] y[place[t, j]] (w NULL: of ones), fp32
  *   sums in the order of j, one rounding to bf16; y [rows, D], out [T, D] bf16.

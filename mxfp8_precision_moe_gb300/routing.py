@@ -160,7 +160,10 @@ class MoePlan:
     slot [rows]   t * top_k + j, the choice that the row holds; -1: none (padding, and rows past offs[E - 1])
     place [T, top_k]  the row that holds the choice; -1: none
 
-    rows, tokens (T), top_k and ``multiple`` are numbers.  Group sizes are multiples of ``multiple``."""
+    rows, tokens (T), top_k and ``multiple`` are numbers.  Group sizes are multiples of ``multiple``.
+
+    slot and place say the same: place[t, j] = r where slot[r] = t * top_k + j, and a choice that is dropped is -1 in both
+    (some kernels read the one, some the other).  To drop choices, set their experts to -1 before ``moe_plan``."""
 
     __slots__ = ("offs", "counts", "slot", "place", "multiple", "rows", "tokens", "top_k")
 
@@ -256,30 +259,37 @@ def _plan_of(plan):
     return plan
 
 
-def _gather(x, plan, out):
-    T, D = x.shape
-    check(load().mx_moe_gather(x.data_ptr(), plan.slot.data_ptr(), plan.place.data_ptr(), plan.rows, T, plan.top_k, D,
-                               out.data_ptr(), _raw_stream(x.device.index)), "mx_moe_gather")
+def _incoming(grad):
+    """A gradient as the kernels read it: autograd may hand over a view of any strides and at any offset."""
+    grad = grad.contiguous()
+    return grad if grad.data_ptr() % 16 == 0 else grad.clone()
+
+
+def _gather(x, slot, place):
+    (T, D), rows = x.shape, slot.shape[0]
+    out = torch.empty((rows, D), dtype=torch.bfloat16, device=x.device)
+    check(load().mx_moe_gather(x.data_ptr(), slot.data_ptr(), place.data_ptr(), rows, T, place.shape[1], D, out.data_ptr(),
+                               _raw_stream(x.device.index)), "mx_moe_gather")
     return out
 
 
-def _combine(y, plan, weights):
-    out = torch.empty((plan.tokens, y.shape[1]), dtype=torch.bfloat16, device=y.device)
-    check(load().mx_moe_combine(y.data_ptr(), plan.place.data_ptr(), None if weights is None else weights.data_ptr(),
-                                plan.rows, plan.tokens, plan.top_k, y.shape[1], out.data_ptr(),
-                                _raw_stream(y.device.index)), "mx_moe_combine")
+def _combine(y, place, weights):
+    (rows, D), (T, k) = y.shape, place.shape
+    out = torch.empty((T, D), dtype=torch.bfloat16, device=y.device)
+    check(load().mx_moe_combine(y.data_ptr(), place.data_ptr(), None if weights is None else weights.data_ptr(), rows, T, k,
+                                D, out.data_ptr(), _raw_stream(y.device.index)), "mx_moe_combine")
     return out
 
 
-def _combine_bwd(dout, y, plan, weights, need_dy: bool, need_dw: bool):
-    T, D = dout.shape
+def _combine_bwd(dout, y, slot, place, weights, need_dy: bool, need_dw: bool):
+    (T, D), rows, k = dout.shape, slot.shape[0], place.shape[1]
     dev = dout.device
-    dy = torch.empty((plan.rows, D), dtype=torch.bfloat16, device=dev) if need_dy else None
-    dw = torch.empty((T, plan.top_k), dtype=torch.float32, device=dev) if need_dw else None
-    check(load().mx_moe_combine_bwd(dout.data_ptr(), y.data_ptr() if need_dw else None, plan.slot.data_ptr(),
-                                    plan.place.data_ptr(), None if weights is None else weights.data_ptr(), plan.rows, T,
-                                    plan.top_k, D, None if dy is None else dy.data_ptr(),
-                                    None if dw is None else dw.data_ptr(), _raw_stream(dev.index)), "mx_moe_combine_bwd")
+    dy = torch.empty((rows, D), dtype=torch.bfloat16, device=dev) if need_dy else None
+    dw = torch.empty((T, k), dtype=torch.float32, device=dev) if need_dw else None
+    check(load().mx_moe_combine_bwd(dout.data_ptr(), y.data_ptr() if need_dw else None, slot.data_ptr(), place.data_ptr(),
+                                    None if weights is None else weights.data_ptr(), rows, T, k, D,
+                                    None if dy is None else dy.data_ptr(), None if dw is None else dw.data_ptr(),
+                                    _raw_stream(dev.index)), "mx_moe_combine_bwd")
     return dy, dw
 
 
@@ -287,13 +297,13 @@ class _MoeGather(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x, plan):
-        ctx.plan = plan
-        return _gather(x, plan, torch.empty((plan.rows, x.shape[1]), dtype=torch.bfloat16, device=x.device))
+        ctx.save_for_backward(plan.place)  # (so that a plan overwritten in between is noticed)
+        return _gather(x, plan.slot, plan.place)
 
     @staticmethod
     @_first_order
     def backward(ctx, drows):
-        return _combine(drows.contiguous(), ctx.plan, None), None
+        return _combine(_incoming(drows), ctx.saved_tensors[0], None), None
 
 
 def moe_gather(x: torch.Tensor, plan: MoePlan) -> torch.Tensor:
@@ -305,23 +315,22 @@ def moe_gather(x: torch.Tensor, plan: MoePlan) -> torch.Tensor:
         x = x.contiguous()
     if x.requires_grad and torch.is_grad_enabled():
         return _MoeGather.apply(x, plan)
-    return _gather(x, plan, torch.empty((plan.rows, x.shape[1]), dtype=torch.bfloat16, device=x.device))
+    return _gather(x, plan.slot, plan.place)
 
 
 class _MoeCombine(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, y, weights, plan):
-        ctx.plan = plan
-        ctx.save_for_backward(y if ctx.needs_input_grad[1] else None, weights)
-        return _combine(y, plan, weights)
+        ctx.save_for_backward(y if ctx.needs_input_grad[1] else None, weights, plan.slot, plan.place)
+        return _combine(y, plan.place, weights)
 
     @staticmethod
     @_first_order
     def backward(ctx, dout):
-        y, weights = ctx.saved_tensors
+        y, weights, slot, place = ctx.saved_tensors
         need_dy, need_dw = ctx.needs_input_grad[:2]
-        return _combine_bwd(dout.contiguous(), y, ctx.plan, weights, need_dy, need_dw) + (None,)
+        return _combine_bwd(_incoming(dout), y, slot, place, weights, need_dy, need_dw) + (None,)
 
 
 def moe_combine(y: torch.Tensor, plan: MoePlan, weights: torch.Tensor | None = None) -> torch.Tensor:
@@ -338,7 +347,7 @@ def moe_combine(y: torch.Tensor, plan: MoePlan, weights: torch.Tensor | None = N
             weights = weights.contiguous()
     if (y.requires_grad or (weights is not None and weights.requires_grad)) and torch.is_grad_enabled():
         return _MoeCombine.apply(y, weights, plan)
-    return _combine(y, plan, weights)
+    return _combine(y, plan.place, weights)
 
 
 # ---------------------------------------------------------------- rows, quantized on the way
@@ -484,7 +493,7 @@ class _Mxfp8MoeSwiGLU(torch.autograd.Function):
             kept += (None, None) if not needed else _keep_mxfp8(t) if keep8 else (t, None)
         ctx.save_for_backward(logits if need_dl else None, experts, weights, *kept, xTq, xTs, hTq, hTs, qg[2], qg[3], qu[2],
                               qu[3], qd[2], qd[3])
-        return _combine(y, plan, weights)
+        return _combine(y, plan.place, weights)
 
     @staticmethod
     @_first_order
@@ -497,13 +506,13 @@ class _Mxfp8MoeSwiGLU(torch.autograd.Function):
         need_dx, need_dl, need_dWg, need_dWu, need_dWd = ctx.needs_input_grad[:5]
         plan, st = ctx.plan, ctx.dev_status
         offs = plan.offs
-        dout = dout.contiguous()
+        dout = _incoming(dout)
         front = need_dx or need_dWg or need_dWu
         dlogits = dx = dWg = dWu = dWd = None
         if need_dl:
             if y_s is not None:
                 y = mxfp8_dequantize_2d(y, y_s, ROW, SCALES_COMPACT)
-            _, dw = _combine_bwd(dout, y, plan, weights, False, True)
+            _, dw = _combine_bwd(dout, y, plan.slot, plan.place, weights, False, True)
             dlogits = _route_bwd(logits, experts, dw, ctx.route)
         if front or need_dWd:
             dirs = (ROW if front else 0) | (COL if need_dWd else 0)
@@ -518,7 +527,7 @@ class _Mxfp8MoeSwiGLU(torch.autograd.Function):
                 a1, a3 = mxfp8_swiglu_bwd_quantize(dh, h1, h3, offs, dev_status=st)
             if need_dx:
                 rows = mxfp8_grouped_mm_dgrad2(a1[0], a1[1], gTq, gTs, a3[0], a3[1], uTq, uTs, offs, dev_status=st)
-                dx = _combine(rows, plan, None)
+                dx = _combine(rows, plan.place, None)
             if need_dWg:
                 dWg = mxfp8_grouped_mm_wgrad(a1[2], a1[3], xTq, xTs, offs, dev_status=st)
             if need_dWu:

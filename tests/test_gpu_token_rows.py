@@ -142,6 +142,36 @@ def test_entries_out_of_range_are_none():
     assert torch.equal(q[0], mx.mxfp4_quantize_2d(rows, offs=plan.offs)[0])
 
 
+def test_gradients_at_any_offset():
+    """Autograd hands over views: those of a concatenation start at whatever lies before."""
+    T, k, E, D = 40, 2, 4, 32
+    plan = make_plan(T, k, E, 1, 1)
+    x, w, head = randn((T, D), 1), torch.rand((T, k), device="cuda", generator=gen(2)), randn((3,), 3)
+    ws = weights_of(E, D, 32, 4)
+    logits = torch.randn((T, E), device="cuda", generator=gen(5))
+    for leaves, f in (([x], lambda x: mx.moe_gather(x, plan)),
+                      ([randn((plan.rows, D), 6), w], lambda y, w: mx.moe_combine(y, plan, w)),
+                      ([x, logits, *ws], lambda x, l, *ws: mx.mxfp8_moe_swiglu(x, l, *ws, k))):
+        leaves = [t.detach().requires_grad_(True) for t in leaves]
+        out = f(*leaves)
+        d = randn(out.shape, 7)
+        want = torch.autograd.grad(out, leaves, d)
+        whole = torch.cat([head, f(*leaves).flatten()])
+        got = torch.autograd.grad(whole, leaves, torch.cat([head, d.flatten()]))
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+
+
+def test_a_plan_overwritten_before_the_backward_is_noticed():
+    x = randn((20, 32), 1).requires_grad_(True)
+    for f in (lambda plan: mx.moe_gather(x, plan), lambda plan: mx.moe_combine(mx.moe_gather(x.detach(), plan).requires_grad_(True), plan)):
+        plan = make_plan(20, 2, 4, 1, 1)
+        out = f(plan)
+        plan.place.copy_(make_plan(20, 2, 4, 1, 2).place)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            out.sum().backward()
+
+
 def test_of_no_tokens():
     plan = mx.moe_plan(torch.zeros((0, 2), dtype=torch.int32, device="cuda"), 4, 32)
     x = torch.zeros((0, 64), dtype=torch.bfloat16, device="cuda", requires_grad=True)
