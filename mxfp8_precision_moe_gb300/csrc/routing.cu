@@ -602,15 +602,22 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_bwd_kernel(const Route
 // and the scattered slots 2 (CTAs of 1024 threads 13.4, longer runs 18, the second kernel launched while the first runs 13.1).
 constexpr int kPlanThreads = 512;
 constexpr int kPlanWarps = kPlanThreads / 32;
-// Steps of a run: few, so that many CTAs share the work; many where the counts of very many runs, which every CTA reads,
-// would cost more.
-constexpr int kPlanShort = 4, kPlanLong = 16;
+// Steps of a run: few, so that many CTAs share the work; more where there are enough of them (1.6 million choices of 64 experts
+// 27.6 us, 35.5 with 16 steps; 4 million of 256, 59, 65 with 4 steps).
+constexpr int kPlanShort = 4, kPlanLong = 8;
 constexpr int64_t kPlanLongFrom = 1 << 20;
 static int plan_steps(int64_t choices) { return choices < kPlanLongFrom ? kPlanShort : kPlanLong; }
 static int64_t plan_runs(int64_t choices) {
     const int64_t run = (int64_t)kPlanThreads * plan_steps(choices);
     return max64(1, (choices + run - 1) / run);
 }
+// More counts, or more runs, than these are summed up by a kernel of their own, as what every CTA reads grows with them.
+// Choices, experts, us with every CTA for itself / with the kernel: 262144, 256 12.1 / 12.9;  524288, 256 20.4 / 17.2;  800000, 64
+// 18.0 / 21.7;  800000, 128 23.6 / 22.1;  2 million, 64 35.8 / 32.4;  2 million, 16 22.3 / 24.0;  8 million, 16 90 / 73;
+// 34 million, 256 2630 / 427.
+constexpr int64_t kPlanScanCounts = 32768, kPlanScanRuns = 500;
+static bool plan_scanned(int64_t runs, int32_t E) { return runs * E > kPlanScanCounts ? runs > 1 : runs > kPlanScanRuns; }
+static int64_t plan_hist_rows(int64_t runs, int32_t E) { return runs == 1 ? 0 : runs + plan_scanned(runs, E); }
 
 struct PlanParams {
     const void* experts;
@@ -618,7 +625,8 @@ struct PlanParams {
     int32_t E, multiple, runs;
     int64_t rows;
     int32_t *offs, *counts, *slot, *place;
-    int32_t* hist;  // [runs][E]
+    int32_t* hist;  // [runs][E]: a run's counts; scanned: those of the runs before it, and [E] behind, of all
+    bool scanned;
 };
 
 template <typename I>
@@ -642,6 +650,35 @@ __global__ void __launch_bounds__(kPlanThreads) plan_count_kernel(const PlanPara
         if (ex[s] >= 0) atomicAdd(&count[ex[s]], 1);
     __syncthreads();
     for (int e = threadIdx.x; e < p.E; e += kPlanThreads) p.hist[(int64_t)blockIdx.x * p.E + e] = count[e];
+}
+
+// hist: the runs' counts -> those of the runs before each, and of all.  A CTA takes 32 experts, a warp a 32nd of the runs.
+constexpr int kScanWarps = 32;
+__global__ void __launch_bounds__(kScanWarps * 32) plan_scan_kernel(const PlanParams p) {
+    __shared__ int32_t part[kScanWarps][32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, e = blockIdx.x * 32 + lane;
+    const int per = (p.runs + kScanWarps - 1) / kScanWarps, from = min(p.runs, warp * per), to = min(p.runs, from + per);
+    int32_t sum = 0;
+    if (e < p.E) {
+#pragma unroll 16
+        for (int r = from; r < to; ++r) sum += __ldcg(p.hist + (int64_t)r * p.E + e);
+    }
+    part[warp][lane] = sum;
+    __syncthreads();
+    if (e >= p.E) return;
+    int32_t before = 0;
+    for (int w = 0; w < warp; ++w) before += part[w][lane];
+    if (warp == kScanWarps - 1) p.hist[(int64_t)p.runs * p.E + e] = before + sum;
+    for (int r0 = from; r0 < to; r0 += 16) {
+        int32_t c[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) c[i] = r0 + i < to ? __ldcg(p.hist + (int64_t)(r0 + i) * p.E + e) : 0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            if (r0 + i < to) p.hist[(int64_t)(r0 + i) * p.E + e] = before;
+            before += c[i];
+        }
+    }
 }
 
 template <typename I, int STEPS>
@@ -677,6 +714,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_place_kernel(const PlanPara
 #pragma unroll
             for (int w = 0; w < kPlanWarps; ++w) c += table[w * p.E + e];
             total[e] = c;
+        }
+    } else if (p.scanned) {
+        for (int e = threadIdx.x; e < p.E; e += kPlanThreads) {
+            before[e] = __ldcg(p.hist + (int64_t)blockIdx.x * p.E + e);
+            total[e] = __ldcg(p.hist + (int64_t)p.runs * p.E + e);
         }
     } else {
         // the counts of all runs, and of those before this one: several threads an expert where there are enough
@@ -757,7 +799,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_place_kernel(const PlanPara
     // rows without a token: each group's padding, by the CTAs in turn, a warp a group; and what follows the last group
     for (int e = blockIdx.x * kPlanWarps + warp; e < p.E; e += gridDim.x * kPlanWarps) {
         const int32_t from = start[e] + total[e], to = e + 1 < p.E ? start[e + 1] : end;
-        for (int32_t r = from + lane; r < to; r += 32) p.slot[r] = -1;
+        for (int64_t r = (int64_t)from + lane; r < to; r += 32) p.slot[r] = -1;  // (rows may come near 2^31)
     }
     for (int64_t r = end + (int64_t)blockIdx.x * kPlanThreads + threadIdx.x; r < p.rows; r += (int64_t)gridDim.x * kPlanThreads)
         p.slot[r] = -1;
@@ -802,6 +844,10 @@ template <typename I, int STEPS>
 static mxfp8_status_t plan_run(const PlanParams& p, cudaStream_t st) {
     if (p.runs > 1) {
         plan_count_kernel<I, STEPS><<<p.runs, kPlanThreads, 0, st>>>(p);
+        if (mxfp8_status_t s = host::last_launch_status(); s != MXFP8_OK) return s;
+    }
+    if (p.scanned) {
+        plan_scan_kernel<<<(p.E + 31) / 32, kScanWarps * 32, 0, st>>>(p);
         if (mxfp8_status_t s = host::last_launch_status(); s != MXFP8_OK) return s;
     }
     static std::atomic<int> attr_set[host::kMaxDevices];
@@ -892,8 +938,7 @@ extern "C" int64_t mx_moe_plan_rows(int64_t T, int32_t top_k, int32_t E, int32_t
 
 extern "C" size_t mx_moe_plan_workspace(int64_t T, int32_t top_k, int32_t E) {
     if (!plan_sizes(T, top_k, E, 1)) return 0;
-    const int64_t runs = plan_runs(T * top_k);
-    return runs > 1 ? (size_t)(runs * E * 4) : 0;
+    return (size_t)(plan_hist_rows(plan_runs(T * top_k), E) * E * 4);
 }
 
 extern "C" mxfp8_status_t mx_moe_plan(const void* experts, int32_t index_bytes, int64_t T, int32_t top_k, int32_t E,
@@ -915,6 +960,7 @@ extern "C" mxfp8_status_t mx_moe_plan(const void* experts, int32_t index_bytes, 
     p.E = E;
     p.multiple = multiple;
     p.runs = (int32_t)plan_runs(p.n);
+    p.scanned = plan_scanned(p.runs, E);
     p.rows = rows;
     p.offs = offs;
     p.counts = counts;

@@ -312,6 +312,38 @@ def test_plan_of_many_tokens():
     assert torch.equal(p.place.flatten().long(), torch.full_like(flat, -1).scatter(0, order, row))
 
 
+@pytest.mark.parametrize("T,k,E,multiple", [
+    (524288, 1, 37, 1), (524289, 1, 37, 32), (700000, 1, 1024, 3), (262144, 8, 256, 32), (262145, 8, 300, 1), (900001, 5, 33, 32)])
+def test_plan_of_very_many_tokens(T, k, E, multiple):
+    """Of so many runs that their counts are summed up first, and just below; against torch's stable sort."""
+    g = torch.Generator(device="cuda").manual_seed(T)
+    e = torch.randint(-1, E, (T, k), device="cuda", generator=g, dtype=torch.int32)
+    e[T // 3:T // 2] = E // 2
+    p = mx.moe_plan(e, E, multiple)
+    flat = e.flatten().long()
+    counts = torch.bincount(flat[flat >= 0], minlength=E)
+    padded = (counts + multiple - 1) // multiple * multiple
+    ends = padded.cumsum(0)
+    assert torch.equal(p.counts.long(), counts) and torch.equal(p.offs.long(), ends)
+    order = torch.where(flat >= 0, flat, E).sort(stable=True)[1][:int(counts.sum())]
+    row = (ends - padded)[flat[order]] + torch.arange(order.numel(), device="cuda") - (counts.cumsum(0) - counts)[flat[order]]
+    assert torch.equal(p.slot.long(), torch.full((p.rows,), -1, device="cuda").scatter(0, row, order))
+    assert torch.equal(p.place.flatten().long(), torch.full_like(flat, -1).scatter(0, order, row))
+
+
+def test_plan_of_nearly_2_31_rows():
+    """Row numbers up to the last that 32 bits hold: even tokens go to the first expert, odd ones to the second."""
+    T = 2 ** 31 - 3
+    e = torch.arange(T, dtype=torch.int32, device="cuda").bitwise_and_(1).view(T, 1)
+    p = mx.moe_plan(e, 2)
+    first = T // 2 + 1
+    assert p.rows == T and p.offs.tolist() == [first, T] and p.counts.tolist() == [first, T - first]
+    for at in (0, T // 2 - 1000, T - 2 ** 20):
+        t = torch.arange(at, min(at + 2 ** 20, T), device="cuda")
+        row = t // 2 + (t & 1) * first
+        assert torch.equal(p.place[t, 0].long(), row) and torch.equal(p.slot[row].long(), t)
+
+
 def test_plan_of_values_past_32_bits():
     e = torch.tensor([[2 ** 32, 1], [-2 ** 33 + 1, 2 ** 40 + 2]], device="cuda")
     check_plan(e, 4, 1)
