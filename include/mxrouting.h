@@ -98,6 +98,7 @@ mxfp8_status_t mx_moe_combine_bwd(const void* dout_bf16, const void* y_bf16, con
  *   dirs: MXFP8_ROW and / or MXFP8_COL; D % 32 == 0; for MXFP8_COL rows and group sizes
  *   are multiples of 32.  Buffers as for mxfp8_quantize_2d with M = rows.
  * mxfp4_gather_quantize -- mxfp4_quantize_2d(rows, blocked, offs) of the same rows.
+ * Groups padded to 128 rows are counted in 32 bits: rows + 127 G < 2^31.
  * ------------------------------------------------------------------------- */
 mxfp8_status_t mxfp8_gather_quantize(const void* x_bf16, const int32_t* slot, const int32_t* place, const float* w,
                                      int64_t rows, int64_t T, int32_t top_k, int64_t D, unsigned dirs, const int32_t* offs,
@@ -113,7 +114,7 @@ mxfp8_status_t mxfp4_gather_quantize(const void* x_bf16, const int32_t* slot, co
  *   or blocked with the row groups of offs (NULL: one group of M rows).  out has q's
  *   shape.  Values are exact but for those below bf16's smallest subnormal, which round;
  *   a block whose scale is 0xFF is NaN; rows (columns) outside every group are 0.
- *   K % 32 == 0, for MXFP8_COL M % 32 == 0; pointers 16-byte aligned.
+ *   K % 32 == 0, for MXFP8_COL M % 32 == 0; pointers 16-byte aligned; with offs M + 127 G < 2^31.
  * ------------------------------------------------------------------------- */
 mxfp8_status_t mxfp8_dequantize(const void* q, const void* s, int64_t M, int64_t K, unsigned dir, int scale_layout,
                                 const int32_t* offs, int32_t G, void* out_bf16, mxfp8_stream_t stream);

@@ -185,7 +185,7 @@ extern "C" mxfp8_status_t mxfp4_gather_quantize(const void* x_bf16, const int32_
                                                 int64_t T, int32_t top_k, int64_t D, const int32_t* offs, int32_t G, void* q,
                                                 void* s, mxfp8_stream_t stream) {
     if (rows < 0 || rows > INT32_MAX || D <= 0 || D > INT32_MAX || T < 0 || top_k < 1 || top_k > MX_MAX_TOP_K ||
-        T * top_k > INT32_MAX || G < 1 || G > MXFP8_MAX_GROUPS)
+        T * top_k > INT32_MAX || G < 1 || G > MXFP8_MAX_GROUPS || !padded_rows_fit(rows, G))
         return MXFP8_ERR_SHAPE;
     if (D % 32) return MXFP8_ERR_ALIGN;
     if (rows == 0) return MXFP8_OK;  // an empty tensor may have no address

@@ -50,6 +50,9 @@ static __device__ __forceinline__ void build_group_table(const int32_t* offs, in
     if (lane == 31) *total = sincl;
 }
 
+// The table's padded rows are 32-bit numbers.
+static inline bool padded_rows_fit(int64_t R, int32_t G) { return R + (int64_t)127 * G <= INT32_MAX; }
+
 // Group of row r (ends_s monotone): first g with r < ends_s[g]; G if none.
 __device__ __forceinline__ int find_group(const int32_t* ends_s, int G, int64_t r) {
     int lo = 0, hi = G;

@@ -1618,7 +1618,7 @@ extern "C" mxfp8_status_t mxfp8_gather_quantize(const void* x_bf16, const int32_
                                                 int32_t G, void* q_row, void* s_row, void* q_col, void* s_col,
                                                 int32_t* dev_status, mxfp8_stream_t stream) {
     if (rows < 0 || rows > INT32_MAX || D <= 0 || D > INT32_MAX || T < 0 || top_k < 1 || top_k > MX_MAX_TOP_K ||
-        T * top_k > INT32_MAX || G < 1 || G > MXFP8_MAX_GROUPS)
+        T * top_k > INT32_MAX || G < 1 || G > MXFP8_MAX_GROUPS || !padded_rows_fit(rows, G))
         return MXFP8_ERR_SHAPE;
     const bool row = dirs & MXFP8_ROW, col = dirs & MXFP8_COL;
     if (dirs == 0 || (dirs & ~(unsigned)(MXFP8_ROW | MXFP8_COL))) return MXFP8_ERR_LAYOUT;
@@ -1658,7 +1658,8 @@ extern "C" mxfp8_status_t mxfp8_gather_quantize(const void* x_bf16, const int32_
 extern "C" mxfp8_status_t mxfp8_dequantize(const void* q, const void* s, int64_t M, int64_t K, unsigned dir,
                                            int scale_layout, const int32_t* offs, int32_t G, void* out_bf16,
                                            mxfp8_stream_t stream) {
-    if (M < 0 || M > INT32_MAX || K <= 0 || K > INT32_MAX || (offs && (G < 1 || G > MXFP8_MAX_GROUPS))) return MXFP8_ERR_SHAPE;
+    if (M < 0 || M > INT32_MAX || K <= 0 || K > INT32_MAX || (offs && (G < 1 || G > MXFP8_MAX_GROUPS || !padded_rows_fit(M, G))))
+        return MXFP8_ERR_SHAPE;
     if (dir != MXFP8_ROW && dir != MXFP8_COL) return MXFP8_ERR_LAYOUT;
     if (scale_layout != MXFP8_SCALES_COMPACT && scale_layout != MXFP8_SCALES_BLOCKED) return MXFP8_ERR_LAYOUT;
     const bool col = dir == MXFP8_COL;

@@ -290,6 +290,7 @@ def test_refusals_of_the_c_abi():
         L.mxfp4_gather_quantize(x, slot, place, rows, T, k, D, offs, G, q, s, None))
     assert f(T=-1) == 2 and f(k=17) == 2 and f(slot=None) == 1 and f(offs=None) == 1 and f(D=48) == 3 and f(G=0) == 2
     assert f(place=None) == 1 and f(q=None) == 1 and f(x=odd) == 3 and f(slot=half) == 3 and f(rows=0, q=None) == 0
+    assert q(rows=2 ** 31 - 128) == f(rows=2 ** 31 - 128) == 2  # whose padded rows pass 32 bits
     o = [a] * 8
     w = lambda dh=a, h1=a, s1=a, h3=a, s3=a, M=64, H=64, offs=a, G=2, outs=o: (  # noqa: E731
         L.mxfp8_swiglu_bwd_quantize_mxfp8(dh, h1, s1, h3, s3, M, H, offs, G, *outs, None, None))
@@ -299,4 +300,5 @@ def test_refusals_of_the_c_abi():
     d = lambda q=a, s=a, M=64, K=64, dir=1, layout=1, offs=None, G=0, out=a: (  # noqa: E731
         L.mxfp8_dequantize(q, s, M, K, dir, layout, offs, G, out, None))
     assert d(M=-1) == 2 and d(K=0) == 2 and d(offs=a) == 2 and d(dir=3) == 4 and d(layout=2) == 4 and d(K=48) == 3
+    assert d(M=2 ** 31 - 128, offs=a, G=2) == 2
     assert d(M=40, dir=2) == 3 and d(out=None) == 1 and d(q=odd) == 3 and d(M=0, q=None) == 0
