@@ -10,6 +10,9 @@ on the way to MXFP8 or MXFP4) and their combination, and the routed SwiGLU layer
 
 or all of it, with the gather inside the quantizations, as ``mxfp8_moe_swiglu``.  Nothing here waits for the device
 (but ``moe_plan(..., exact=True)``), and a sum's order is fixed: equal inputs give equal bits.
+
+Every call can be captured into a CUDA graph, backward passes too: with the usual warm-up on a side stream, and while no
+graph of an eager forward of the same leaves is alive (torch ties a leaf's accumulation to the stream it first saw).
 """
 from __future__ import annotations
 
