@@ -25,8 +25,10 @@ extern "C" {
  *   with one that is the same finite value for all, experts rank by their logits, which
  *   order as their scores do.
  *   groups > 1: expert e is of group e / (E / groups); a group is worth the sum of its
- *   two largest keys (MX_GROUP_TOP2) or its largest (MX_GROUP_MAX), and only the
- *   experts of the top_groups best groups can be selected.
+ *   two largest keys (MX_GROUP_TOP2; of the one, where only one of its experts can be
+ *   selected) or its largest (MX_GROUP_MAX), and only the experts of the top_groups best
+ *   groups can be selected.  A bias is part of the keys here even where it is the same
+ *   for all: a group with one expert left has it once, others twice.
  *   S_t = the top_k largest keys.  Keys, and sums of keys, rank as exact values do: those
  *   whose order 32 bits leave open are computed in 64.  Ties go to the lowest index; NaN
  *   ranks above everything; an expert whose logit or bias is -inf is never selected.

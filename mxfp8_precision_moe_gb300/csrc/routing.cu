@@ -97,6 +97,12 @@ __device__ __forceinline__ void group_top2(const O* keys, const RouteParams& p, 
         top = max(top, v);
     }
 }
+// Whether a bias that is the same for all tells groups apart: it counts once for each of a group's two largest keys, so not
+// where all groups have two experts to select, or one.  The whole warp asks, every lane for its group (0, 0: none).
+template <typename O>
+__device__ __forceinline__ bool uneven_groups(const RouteParams& p, O top, O second) {
+    return p.bias != nullptr && __any_sync(kFull, second != 0) && __any_sync(kFull, top != 0 && second == 0);
+}
 // Which groups stay, where lane g holds what group g is worth: bit g.
 template <typename O>
 __device__ __forceinline__ uint32_t best_groups(O worth, const RouteParams& p, int lane) {
@@ -143,9 +149,10 @@ __device__ __noinline__ int select_64(const RouteParams& p, int64_t t, bool by_l
         unsigned long long first, second, worth;
         group_top2(keys, p, lane, first, second);
         worth = first;
+        const double common = by_logits && !p.group_max && uneven_groups(p, first, second) ? (double)*p.bias : 0.0;
         if (!p.group_max && first) {
-            double v = by_logits ? score_64(p, value_of(first), top, sum) : value_of(first);
-            if (second) v += by_logits ? score_64(p, value_of(second), top, sum) : value_of(second);
+            double v = by_logits ? score_64(p, value_of(first), top, sum) + common : value_of(first);
+            if (second) v += by_logits ? score_64(p, value_of(second), top, sum) + common : value_of(second);
             worth = order_of(v);
         }
         const uint32_t stay = best_groups(worth, p, lane);
@@ -381,7 +388,10 @@ __global__ void __launch_bounds__(kRouteWarps * 32, VPL <= 2 ? 10 : VPL <= 8 ? 1
         }
         // what the group is worth, and how far that may be off
         uint32_t worth = top;
-        float off = 2 * err;
+        float off = 2 * err, common = 0.0f;
+        if constexpr (KEYS != kKeysLogits) {
+            if (by_logits && !p.group_max && uneven_groups(p, top, second)) common = __ldg(p.bias);
+        }
         if (!p.group_max && top) {
             float v = value_of(top), w = second ? value_of(second) : 0.0f;
             if (KEYS >= kKeysSigmoid && by_logits) {
@@ -390,6 +400,11 @@ __global__ void __launch_bounds__(kRouteWarps * 32, VPL <= 2 ? 10 : VPL <= 8 ? 1
                 w = !second ? 0.0f : KEYS == kKeysSigmoid ? sigmoid_approx(lw) : expf(lw - m) / sum;
                 off = score_error<KEYS, VPL>(v, KEYS == kKeysSigmoid ? lv : m - lv) +
                       score_error<KEYS, VPL>(w, KEYS == kKeysSigmoid ? lw : m - lw);
+            }
+            if (common != 0.0f) {
+                v += common;
+                w += common;
+                off += kUlp * (fabsf(v) + fabsf(w));
             }
             if (second) v += w;
             off += kUlp * fabsf(v);

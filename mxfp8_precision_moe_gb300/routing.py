@@ -138,7 +138,8 @@ def moe_route(logits: torch.Tensor, top_k: int, *, score: str = "softmax", bias:
     experts) or "sigmoid".  bias [E] fp32: for balance; it moves the ranking, not the weights, and has no gradient.
     renormalize: the selected scores divided by their sum.  scale: a factor of all weights.
     groups: the experts lie in so many groups of neighbours (a divisor of E, 32 at most), each worth the sum of its two
-    largest keys (group_score "top2") or its largest ("max"); only the top_groups best groups are selected from.
+    largest keys (group_score "top2"; of the one, where one of its experts can be selected), bias included, or its largest
+    ("max"); only the top_groups best groups are selected from.
 
     Where 32 bits leave the order of two sums open, they are compared in 64."""
     if not isinstance(logits, torch.Tensor) or logits.dim() != 2 or logits.dtype not in LOGITS_TYPES:
