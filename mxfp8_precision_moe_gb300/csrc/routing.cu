@@ -130,9 +130,8 @@ __device__ __forceinline__ double score_64(const RouteParams& p, double l, doubl
 }
 // The integer that orders as expert e's key does, from 64 bits; 0: not to be selected.
 __device__ __forceinline__ unsigned long long key_64(const RouteParams& p, int64_t t, int e, double top, double sum) {
-    const float l = logit_at(p, t, e);
-    const double key = score_64(p, l, top, sum) + (double)p.bias[e];
-    return l == -INFINITY || key == -INFINITY ? 0ull : order_of(key);
+    const float l = logit_at(p, t, e), bias = p.bias[e];  // asked by themselves: a NaN score's key would not tell
+    return l == -INFINITY || bias == -INFINITY ? 0ull : order_of(score_64(p, l, top, sum) + (double)bias);
 }
 
 // The selection in 64 bits, for a token whose order 32 bits leave open.  by_logits: the experts rank by their logits.  Lane
@@ -347,7 +346,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32, VPL <= 2 ? 10 : VPL <= 8 ? 1
             }
             key += b[i];
             if (key != -INFINITY) largest = fmaxf(largest, fabsf(key));
-            ord[i] = l[i] == -INFINITY || key == -INFINITY ? 0u : order_of(key);
+            ord[i] = l[i] == -INFINITY || b[i] == -INFINITY || key == -INFINITY ? 0u : order_of(key);
         }
         // (bounds: score_error, at the largest score, as they grow with it)
         if constexpr (KEYS == kKeysSigmoid) {

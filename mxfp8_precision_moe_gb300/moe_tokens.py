@@ -125,7 +125,8 @@ class MxMoeTokens:
     def __call__(self, x: torch.Tensor, router_logits: torch.Tensor, out: torch.Tensor | None = None,
                  dev_status: torch.Tensor | None = None) -> torch.Tensor:
         """x [T, D] bf16, router_logits [T, E] (fp32; fp16 and bf16 are widened), T <= max_tokens -> y
-        [T, D] bf16.  A token whose logits are all -inf gets zeros; one with a NaN logit gets NaN.
+        [T, D] bf16.  A token whose logits are all -inf gets zeros; one with a NaN logit gets NaN
+        (where a bias of -inf takes that expert out, only of the score "softmax_all").
         dev_status: an int32 word for errors the device finds (``new_status``, ``read_status``), in place of the
         layer's own."""
         T = x.shape[0] if x.dim() == 2 else -1

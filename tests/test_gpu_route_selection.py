@@ -74,3 +74,41 @@ def test_a_common_bias_that_32_bits_leave_open(score, E, groups):
             row[((t + 2) % groups) * size] = -3.0
         s = ref.scores(row.tolist(), score)
         check(row[None], 1, torch.full((E,), s[a] - s[c] - s[c + 1]), score=score, groups=groups, top_groups=1)
+
+
+# ---------------------------------------------------------------- a bias of -inf, whatever the logit
+def test_a_masked_expert_is_out_whatever_its_logit():
+    bias = [-inf, 0, 0, 0.1]
+    for junk in (nan, inf, 5.0):
+        for score in ("softmax", "sigmoid"):
+            e, w = mx.moe_route(torch.tensor([[junk, 1, 2, 0]], device="cuda"), 4, score=score,
+                                bias=torch.tensor(bias, device="cuda"))
+            assert e.tolist() == [[2, 1, 3, -1]] and torch.isfinite(w).all() and w[0, 3] == 0
+    # every score of a softmax over all is NaN then: who is left ties
+    for l in ([nan, 1, 2, 0], [inf, 1, 2, 0], [0, 1, nan, 2], [0, 1, inf, 2]):
+        assert select([l], 4, bias, score="softmax_all") == [[1, 2, 3, -1]]
+    # a group of which only masked experts are NaN is worth what is left in it: 2 keys of -1 against -3 and -4
+    l, bias = [nan, -1, -1, 0, -3, -4, -9, -9], [-inf, 0, 0, -inf, 0, 0, 0, 0.1]
+    assert select([l], 3, bias, groups=2, top_groups=1) == [[1, 2, -1]]
+    l = l[4:] + l[:4]
+    assert select([l], 3, bias[4:] + bias[:4], groups=2, top_groups=1) == [[5, 6, -1]]
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups,top_groups,k", [(12, 1, 1, 9), (64, 8, 3, 8), (100, 5, 2, 7), (256, 8, 4, 8), (256, 1, 1, 8),
+                                                   (1024, 32, 5, 16)])
+@pytest.mark.parametrize("most", [0.0, inf])
+def test_what_masked_experts_have_for_logits_changes_nothing(score, E, groups, top_groups, k, most):
+    """A quarter of the experts is masked.  most: one bias of +inf has every order told in 64 bits."""
+    l, bias = randn((20, E), E), 0.1 * randn(E, 1)
+    out = torch.randperm(E, generator=torch.Generator().manual_seed(2))[:E // 4]
+    bias[out] = -inf
+    bias[[e for e in range(E) if e not in out.tolist()][0]] += most
+    kw = dict(score=score, groups=groups, top_groups=top_groups)
+    l[:, out] = 0.0
+    plain, bias = l.clone().cuda(), bias.cuda()
+    want = mx.moe_route(plain, k, bias=bias, **kw)
+    assert not torch.isin(want[0], out.cuda()).any()
+    l[:, out] = torch.tensor([nan, inf, -inf, 3e38])[torch.arange(E // 4) % 4]
+    for got, w in zip(mx.moe_route(l.cuda(), k, bias=bias, **kw), want):
+        assert torch.equal(got, w)
