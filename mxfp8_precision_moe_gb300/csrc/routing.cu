@@ -345,8 +345,10 @@ __global__ void __launch_bounds__(kRouteWarps * 32, VPL <= 2 ? 10 : VPL <= 8 ? 1
                 key = expf(l[i] - m) / sum;
             }
             key += b[i];
-            if (key != -INFINITY) largest = fmaxf(largest, fabsf(key));
-            ord[i] = l[i] == -INFINITY || b[i] == -INFINITY || key == -INFINITY ? 0u : order_of(key);
+            // (a finite logit and a finite bias may add up to an infinite key: its bound is infinite, and 64 bits tell)
+            const bool out = l[i] == -INFINITY || b[i] == -INFINITY;
+            if (!out) largest = fmaxf(largest, fabsf(key));
+            ord[i] = out ? 0u : order_of(key);
         }
         // (bounds: score_error, at the largest score, as they grow with it)
         if constexpr (KEYS == kKeysSigmoid) {

@@ -112,3 +112,22 @@ def test_what_masked_experts_have_for_logits_changes_nothing(score, E, groups, t
     l[:, out] = torch.tensor([nan, inf, -inf, 3e38])[torch.arange(E // 4) % 4]
     for got, w in zip(mx.moe_route(l.cuda(), k, bias=bias, **kw), want):
         assert torch.equal(got, w)
+
+
+# ---------------------------------------------------------------- sums below fp32's range
+@pytest.mark.parametrize("E,groups", [(12, 1), (12, 4), (60, 1), (100, 5), (256, 1), (256, 8)])
+def test_keys_below_fp32s_lowest_rank_as_exact_sums(E, groups):
+    """Finite logits and biases, whose sums have no fp32: their experts are there to be selected."""
+    low = -3e38 - torch.arange(E) * 1e33
+    check(torch.stack((low, low.flip(0))), 3, low, score="softmax", groups=groups, top_groups=max(1, groups // 2))
+    # two experts in fp32's range: they come first, and the places left go to the others
+    l = low.clone()
+    l[[E // 2, E - 1]] = torch.tensor([1.0, 2.0])
+    bias = low.clone()
+    bias[[E // 2, E - 1]] = torch.tensor([0.5, 0.25])
+    check(l[None], 4, bias, score="softmax", groups=groups, top_groups=groups)
+    check(l[None], 3, bias, score="softmax", groups=groups, top_groups=groups, group_score="max")
+    # masked ones stay out
+    bias[0] = -inf
+    l[1] = -inf
+    check(l[None], E if E <= 16 else 16, bias, score="softmax", groups=groups, top_groups=groups)
