@@ -132,7 +132,7 @@ def moe_route(logits: torch.Tensor, top_k: int, *, score: str = "softmax", bias:
     Experts are ranked by score(logit) + bias (without a bias, or with the same one for all, by the logits, which order as
     their scores do), largest first; equal ones by their index, NaN above everything; an expert whose logit or bias is -inf is
     never selected.  A token that has fewer than top_k experts to select gets
-    -1 with weight 0 in the places left.
+    -1 with weight 0 in the places left.  (The gradient reads the experts: change a copy, not this tensor.)
 
     score: "softmax" (the ranking takes the logits, the weights are a softmax over the selected), "softmax_all" (over all
     experts) or "sigmoid".  bias [E] fp32: for balance; it moves the ranking, not the weights, and has no gradient.
@@ -167,7 +167,9 @@ class MoePlan:
     rows, tokens (T), top_k and ``multiple`` are numbers.  Group sizes are multiples of ``multiple``.
 
     slot and place say the same: place[t, j] = r where slot[r] = t * top_k + j, and a choice that is dropped is -1 in both
-    (some kernels read the one, some the other).  To drop choices, set their experts to -1 before ``moe_plan``."""
+    (some kernels read the one, some the other).  To drop choices, give ``moe_plan`` a copy of the experts with -1 in their
+    places, as ``torch.where(keep, experts, -1)`` does: ``moe_route``'s own tensor is what its gradient reads, and changed in
+    place it is refused there."""
 
     __slots__ = ("offs", "counts", "slot", "place", "multiple", "rows", "tokens", "top_k")
 
