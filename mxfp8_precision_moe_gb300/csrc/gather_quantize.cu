@@ -146,8 +146,11 @@ __global__ void __launch_bounds__(kGatherWarps * 32, 5) gather_quantize_kernel(c
 template <int BITS>
 static mxfp8_status_t run_gather_quantize(GatherParams& p, cudaStream_t st) {
     constexpr int EPT = BITS == 4 ? 32 : 16;
-    // Where a token has several rows, more CTAs than the five that fit on an SM, and more warps on a token, even the ends out:
-    // 8 rows a token of 8192 x 7168 MXFP4 84 -> 79 us, MXFP8 141 -> 127; with one row a token of 16384 x 5120 48 -> 50.
+    // Where a token has several rows, more CTAs than the five that fit on an SM, and more warps on a token, even the ends out.
+    // Once (twice, 3, 4, 8 times) as many, us: 16384 tokens of 5120, MXFP8, one row 48.1 (49.0 50.1 50.9 58.4), two 61.1 (61.2
+    // 63.4 62.0 68.3), three 79.2 (75.7 77.2 75.7 79.9), four 97.0 (91.4 93.7 89.9 92.9); MXFP4, one 37.1 (37.5 40.9 40.8 45.5),
+    // two 44.4 (44.0 49.4 47.3 51.5), three 56.4 (52.1 56.2 54.0 57.7), four 67.4 (61.4 65.8 62.0 64.2); 8192 of 7168, eight rows
+    // MXFP8 136.6 (134.8 134.4 127.3 123.1), MXFP4 87.9 (86.9 85.9 83.6 83.8).
     const int64_t chunks = (p.C + 32 * EPT - 1) / (32 * EPT), ctas = (int64_t)host::num_sms() * 5 * (p.k < 4 ? p.k : 4);
     // a warp takes a whole token, for which it looks its rows up once; of few tokens, several share one
     p.parts = (int32_t)max64(1, min64(chunks, (ctas * kGatherWarps + p.T - 1) / max64(p.T, 1)));

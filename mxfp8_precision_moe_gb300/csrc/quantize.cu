@@ -276,14 +276,18 @@ constexpr int kQConsumerThreads = 256;         // 8 consumer warps, no producer 
 // kModeSwiBwd (ROW|COL only): 256 threads, no TMA ring: each warp loads its patches of dh, h1 and h3
 // straight from global memory (three inputs a stage would leave room for too few warps to hide the
 // arithmetic's latency), computes dh1 and dh3 and quantizes each both ways.  kModeSwiBwd8: h1 and h3 come as MXFP8 codes
-// with compact row-wise scales, 2.06 bytes a pair instead of 4.  Both are bound by their arithmetic, so that the fewer bytes
-// do not pay for the decoding: 16384 x 8192 406 and 476 us (548 where h1 and h3 are dequantized first).
+// with compact row-wise scales, 2.06 bytes a pair instead of 4: 16384 x 8192 406 and 476 us (548 where h1 and h3 are
+// dequantized first; 203 and 164 for the bytes).  Neither memory (38 and 24% of its rate) nor a pipe (ALU 37 and 35%) is
+// full; both are bound by their instructions at the 16 warps an SM that 128 registers allow, which fill half of the issue
+// slots: the decoding adds 16% of instructions, and the codes' and scales' loads are waited for longer (2.0 cycles an
+// instruction, 0.8).
 // kModeGather (ROW, COL, ROW|COL): a warp fills a ring of its own patches (32 rows x 64 columns) by 16-byte asynchronous
 // copies, each row through its slot; warps do not wait for one another.  A CTA takes units of up to 8 column tiles, whose
 // rows' slots, weights and places in the scales are looked up once.  16384 x 5120 both ways, 69 us (the plain kernel with
 // its TMA ring 61): bulk copies by a producer warp, 256 bytes a row, 107 (one takes about 50 clocks); a producer warp's
 // 16-byte copies 84 (its instructions bind); each warp's own loads without a ring 95; this ring with a division and a
-// look-up a tile 80.  Eight rows a token of 7168, 70 thousand rows, 340 us, where moe_gather and the plain kernel take 560.
+// look-up a tile 80.  Eight rows a token of 7168, 70 thousand rows, 334 us, where moe_gather and the plain kernel take 549; the
+// column-wise copy alone 229.  With weights 77 and 374 us (about a third more instructions).
 // Units go down a strip of columns before the next strip, row of tiles by row of tiles within it: a strip as wide as x's
 // share of it stays in L2 for all rows that a token has, and no narrower, since short pieces of rows far apart are slow to
 // read and write.

@@ -565,6 +565,8 @@ __global__ void __launch_bounds__(kRouteWarps * 32, VPL <= 2 ? 10 : VPL <= 8 ? 1
 //   sigmoid:                                      dl_j = d_j s_j (1 - s_j)
 //   sigmoid, renormalised:                        dl_j = p_j (d_j - <p, d>) (1 - s_j)
 // and 0 for every other expert.  A warp a token: the row of zeros (or of the others' softmax), then the selected.
+// 32768 tokens, 8 of 256, fp32: the selected alone 9.5 us for 5.5 of bytes (its 4-byte stores: DRAM 65%, issue slots 63% of
+// their rate); softmax over all 18.4 for 10.3 (issue slots 80%: the row is read three times, with two exponentials a logit).
 template <typename L>
 __global__ void __launch_bounds__(kRouteWarps * 32) route_bwd_kernel(const RouteParams p) {
     const int lane = threadIdx.x & 31;

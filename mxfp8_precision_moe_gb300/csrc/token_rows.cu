@@ -150,7 +150,9 @@ __global__ void __launch_bounds__(kRowsThreads) combine_kernel(const RowsParams 
 }
 
 // A CTA a token: each piece of dout is read once, with the pieces of the token's rows of y; dy's are written, and the
-// threads' partial products <dout, y> are added up in a fixed order.
+// threads' partial products <dout, y> are added up in a fixed order.  At the copy rate where a row fills the CTA: 16384 tokens,
+// 4 rows of 5120 each, 224 us for 226 of bytes.  Shorter rows leave threads without a piece, and the adding up costs as much
+// as ever: 65536 tokens, 4 rows of 1024, 301 us for 181; of 512 266 for 90; of 352 257 for 62.
 template <int KB, bool kDy>
 __global__ void __launch_bounds__(kRowsThreads) combine_bwd_kernel(const RowsParams p) {
     __shared__ float part[kRowsThreads / 32][MX_MAX_TOP_K];
@@ -233,8 +235,9 @@ static int64_t token_ctas(const RowsParams& p) {
 
 static mxfp8_status_t run_gather(RowsParams& p, cudaStream_t st) {
     if (p.rows == 0) return MXFP8_OK;
-    // a token with several rows is many writes: 4 rows of 5120 each, 16384 tokens, 127 us by short warps, 131 by long ones;
-    // one row 55 and 53
+    // the more writes a token is, the more warps share it: once (twice, 4, 8, 16 times) over, 16384 tokens of 5120, us, one row
+    // 52.8 (52.1 51.3 52.8 53.1), two 78.5 (78.6 77.8 78.0 77.4), three 106.1 (104.6 103.6 103.9 103.9), four 133.2 (131.0 129.7
+    // 128.6 127.8); 8192 tokens of 7168, eight 179.5 (177.5 176.0 173.1 173.6)
     p.parts = parts_of(p, 32 * kGatherPieces, p.k < 4 ? p.k * p.k : 16);
     p.token_ctas = (uint32_t)token_ctas(p);
     const unsigned grid = (unsigned)(p.token_ctas + padding_ctas(p));
